@@ -11,6 +11,7 @@ Functions (same names as the C entry points):
   decode(...)   one query row per sequence            -> atlas_attn_decode
   suffix(...)   the last q_len positions as queries   -> atlas_attn_suffix
   prefill(...)  causal self-attention of a prompt     -> atlas_attn_prefill
+  cross(...)    decoder rows over an encoder's states -> atlas_attn_cross
   kv_append(...)  new tokens' K/V into their pages    -> atlas_kv_append
   workspace_size(kind, ...)                            -> atlas_attn_workspace_size
   run_host(kind, ...)  host tensors in, host tensor out (copies on the stream)
@@ -25,12 +26,14 @@ import torch
 
 from . import _build
 
-__all__ = ["AtlasError", "decode", "suffix", "prefill", "kv_append", "workspace_size", "run_host",
+__all__ = ["AtlasError", "decode", "suffix", "prefill", "cross", "kv_append", "workspace_size", "run_host",
            "library_path", "DEV_BAD_PAGE", "DEV_BAD_SEQLEN", "DEV_TIMEOUT",
-           "DEBUG_WITHHOLD_STAGE", "KIND_DECODE", "KIND_SUFFIX", "KIND_PREFILL"]
+           "DEBUG_WITHHOLD_STAGE", "KIND_DECODE", "KIND_SUFFIX", "KIND_PREFILL",
+           "KIND_CROSS"]
 
-KIND_DECODE, KIND_SUFFIX, KIND_PREFILL = 0, 1, 2
-_KINDS = {"decode": KIND_DECODE, "suffix": KIND_SUFFIX, "prefill": KIND_PREFILL}
+KIND_DECODE, KIND_SUFFIX, KIND_PREFILL, KIND_CROSS = 0, 1, 2, 3
+_KINDS = {"decode": KIND_DECODE, "suffix": KIND_SUFFIX, "prefill": KIND_PREFILL,
+          "cross": KIND_CROSS}
 DEV_BAD_PAGE, DEV_BAD_SEQLEN, DEV_TIMEOUT = 1, 2, 4
 DEBUG_WITHHOLD_STAGE = 1
 DEBUG_TC_DIRECT = 2
@@ -114,7 +117,8 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
     lib = ctypes.CDLL(_build.LIB)
     args = [ctypes.c_void_p] * 5 + [ctypes.c_int32] * 4 + [ctypes.c_float,
                                                            ctypes.POINTER(_Launch)]
-    for name in ("atlas_attn_decode", "atlas_attn_suffix", "atlas_attn_prefill"):
+    for name in ("atlas_attn_decode", "atlas_attn_suffix", "atlas_attn_prefill",
+                 "atlas_attn_cross"):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
@@ -300,6 +304,14 @@ def prefill(q, k_pages, v_pages, page_table, seq_lens, n_q_heads, n_kv_heads, he
             page_tokens, scale, **kw):
     """Causal self-attention of whole prompts (seq_lens[b] == q_len for every b)."""
     return _call("prefill", q, k_pages, v_pages, page_table, seq_lens, n_q_heads, n_kv_heads,
+                 head_dim, page_tokens, scale, **kw)
+
+
+def cross(q, k_pages, v_pages, page_table, enc_lens, n_q_heads, n_kv_heads, head_dim,
+          page_tokens, scale, **kw):
+    """Attention of q_len decoder rows to all enc_lens[b] encoder states of their
+    sequence (no causal mask; enc_lens[b] == 0 gives rows of 0 and lse -inf)."""
+    return _call("cross", q, k_pages, v_pages, page_table, enc_lens, n_q_heads, n_kv_heads,
                  head_dim, page_tokens, scale, **kw)
 
 

@@ -103,7 +103,9 @@ atlas_status make_plan(atlas_kind kind, int32_t Hq, int32_t Hkv, int32_t D, int3
     if (!L) return ATLAS_ERR_INVALID_ARG;
     if (L->sm_count < 0) return ATLAS_ERR_INVALID_ARG;
     const int sms = L->sm_count > 0 ? L->sm_count : device_sm_count();
-    if (kind != ATLAS_KIND_DECODE && kind != ATLAS_KIND_SUFFIX && kind != ATLAS_KIND_PREFILL)
+    const bool cross = kind == ATLAS_KIND_CROSS;
+    if (kind != ATLAS_KIND_DECODE && kind != ATLAS_KIND_SUFFIX && kind != ATLAS_KIND_PREFILL &&
+        !cross)
         return ATLAS_ERR_INVALID_ARG;
     if (L->batch < 1 || L->max_pages_per_seq < 1 || L->num_pages < 1 || L->q_len < 1 || Hq < 1 ||
         Hkv < 1 || Hq % Hkv != 0)
@@ -127,7 +129,10 @@ atlas_status make_plan(atlas_kind kind, int32_t Hq, int32_t Hkv, int32_t D, int3
     const int64_t work_ctx =
         L->window > 0 ? std::min(max_ctx, (int64_t)L->window + L->q_len + 127) : max_ctx;
     if ((int64_t)L->num_pages * Hkv * P >= INT32_MAX) return ATLAS_ERR_INVALID_ARG;
-    if (L->q_len > max_ctx) return ATLAS_ERR_INVALID_ARG;
+    if (L->q_len > (cross ? INT32_MAX / 2 : max_ctx)) return ATLAS_ERR_INVALID_ARG;
+    // Cross attention has no positions to window, and runs as one whole call.
+    if (cross && L->window != 0) return ATLAS_ERR_INVALID_ARG;
+    if (cross && (L->phase != ATLAS_PHASE_ALL || L->chunk_range)) return ATLAS_ERR_UNSUPPORTED;
     // Output rows are indexed in 32 bits (the merge, the tensor-core tiles).
     if ((int64_t)L->batch * Hq * L->q_len >= INT32_MAX) return ATLAS_ERR_INVALID_ARG;
     if (L->split_tokens < 0 || L->split_tokens % kSplitBlockTokens != 0)
@@ -177,7 +182,7 @@ atlas_status make_plan(atlas_kind kind, int32_t Hq, int32_t Hkv, int32_t D, int3
         } else {
             if (tiles > INT32_MAX || L->phase != ATLAS_PHASE_ALL) return ATLAS_ERR_UNSUPPORTED;
             plan->chunk = plan->n_chunks = 0;
-            plan->tiles_per_head = (L->q_len % 128 == 0) ? L->q_len / 128 : 0;
+            plan->tiles_per_head = (L->q_len % 128 == 0 && !cross) ? L->q_len / 128 : 0;
             plan->acc_bytes = plan->ml_offset = plan->ws_bytes = 0;
         }
         return ATLAS_OK;
@@ -318,6 +323,7 @@ atlas_status run(atlas_kind kind, const void *q, const void *k_pages, const void
     sp.n_chunks = plan.n_chunks;
     sp.col_tiles = plan.col_tiles;
     sp.require_full = kind == ATLAS_KIND_PREFILL;
+    sp.row_step = kind == ATLAS_KIND_CROSS ? 0 : 1;
     sp.scale_log2 = scale * kLog2e;
     sp.window = L->window;
     sp.q_lens = L->q_lens;
@@ -372,6 +378,7 @@ atlas_status run(atlas_kind kind, const void *q, const void *k_pages, const void
         tp.n_chunks = plan.n_chunks;
         tp.balanced = plan.balanced;
         tp.require_full = kind == ATLAS_KIND_PREFILL;
+        tp.row_step = sp.row_step;
         tp.hilo_below = fabsf(scale) * sqrtf((float)D) > kHiLoScale ? INT32_MAX : kHiLoBelow;
         tp.negate_scores = scale < 0.f;
         tp.scale_log2 = fabsf(scale) * kLog2e;
@@ -428,6 +435,7 @@ atlas_status run(atlas_kind kind, const void *q, const void *k_pages, const void
     mp.n_chunks = plan.n_chunks;
     mp.balanced = plan.balanced;
     mp.require_full = sp.require_full;
+    mp.row_step = sp.row_step;
     mp.window = L->window;
     mp.sinks = L->sinks;
     mp.q_lens = L->q_lens;
@@ -469,6 +477,14 @@ atlas_status atlas_attn_prefill(const void *q, const void *k_pages, const void *
                                 int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                                 int32_t page_tokens, float scale, const atlas_launch *L) {
     return atlas::run(ATLAS_KIND_PREFILL, q, k_pages, v_pages, page_table, seq_lens, n_q_heads,
+                      n_kv_heads, head_dim, page_tokens, scale, L);
+}
+
+atlas_status atlas_attn_cross(const void *q, const void *k_pages, const void *v_pages,
+                              const int32_t *page_table, const int32_t *enc_lens,
+                              int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                              int32_t page_tokens, float scale, const atlas_launch *L) {
+    return atlas::run(ATLAS_KIND_CROSS, q, k_pages, v_pages, page_table, enc_lens, n_q_heads,
                       n_kv_heads, head_dim, page_tokens, scale, L);
 }
 

@@ -72,7 +72,8 @@ struct TcWork {
     int kv_begin, kv_end, nb;  // key range and its 128-key blocks
     bool hilo, tail_fix;       // hi + lo P on every block; last block partly past kv_end
     int tail_first;            // first key row of the last block past kv_end
-    int state;                 // 0: compute; 1: nothing to compute; 2: bad seq_len
+    int state;                 // 0: compute; 1: nothing to compute; 2: bad seq_len;
+                               // 3: no encoder states (direct mode writes the empty rows)
 };
 
 template <int NT, int D>
@@ -166,6 +167,22 @@ __device__ void nan_row(const TcParams &p, int b, int hkv, int f) {
     if (p.lse) p.lse[row] = nan;
 }
 
+// Row f of (b, hkv) of cross attention over no encoder states, direct mode: 0, with
+// lse -inf (or the sink, whose weight has no value row).
+template <int D>
+__device__ void empty_row(const TcParams &p, int b, int hkv, int f) {
+    const int64_t row = tile_row(p, b, hkv, f);
+    const float sink = p.sinks ? p.sinks[(row / p.q_len) % p.Hq] : -INFINITY;
+    if (isnan(sink)) {
+        nan_row<D>(p, b, hkv, f);
+        return;
+    }
+    const int bytes = D * (p.out_bf16 ? 2 : 4);
+    uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + row * bytes);
+    for (int k = 0; k < bytes / 16; ++k) o[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse) p.lse[row] = sink;
+}
+
 template <int NT>
 __device__ TcWork tc_work(const TcParams &p, int u, int c, int t0, int tstep, int split_keys) {
     TcWork w{};
@@ -178,11 +195,13 @@ __device__ TcWork tc_work(const TcParams &p, int u, int c, int t0, int tstep, in
     w.qn = p.q_lens ? p.q_lens[w.b] : p.q_len;  // query rows of this sequence
     w.rows_unit = p.G * p.q_len;
     // Both tiles cover the same prompt rows, so their key ranges agree.
+    // (cross attention: every row sees every key, and the tiles are neighbours)
     const int f0 = t0 * BM;
-    const int f_last = min(f0 + BM, w.rows_unit) - 1;
+    const int f_last = min(f0 + (p.row_step ? BM : NT * BM), w.rows_unit) - 1;
     const bool spans = (f_last / p.q_len) != (f0 / p.q_len);
     const int i_min = spans ? 0 : f0 % p.q_len;
-    if (w.qn < 0 || w.qn > p.q_len || seq_len < w.qn || seq_len > p.max_pages * p.P ||
+    if (w.qn < 0 || w.qn > p.q_len || seq_len < p.row_step * w.qn ||
+        seq_len > p.max_pages * p.P ||
         (p.require_full && seq_len != w.qn)) {
         w.state = 2;
         return w;
@@ -194,11 +213,16 @@ __device__ TcWork tc_work(const TcParams &p, int u, int c, int t0, int tstep, in
     // Last real row of the tiles; with L shifted by q_len - qn, row i sits at
     // position L - q_len + i = seq_len - qn + i as in a full batch.
     const int i_max = min(spans ? p.q_len - 1 : f_last % p.q_len, w.qn - 1);
-    w.L = seq_len - w.qn + p.q_len;
-    const int kv_hi = w.L - p.q_len + i_max + 1;  // keys the tiles' last row sees
+    // (cross attention: a shift of q_len - 1 and no step make it seq_len for every row)
+    w.L = seq_len + p.q_len - (p.row_step ? w.qn : 1);
+    const int kv_hi = w.L - p.q_len + p.row_step * i_max + 1;  // keys the tiles' last row sees
+    if (kv_hi == 0) {  // no encoder states
+        w.state = 3;
+        return w;
+    }
     // Keys the tiles' first row sees (its window may cut that short).
-    const int kv_min = p.window > 0 ? min(w.L - p.q_len + i_min + 1, p.window)
-                                    : w.L - p.q_len + i_min + 1;
+    const int kv_first = w.L - p.q_len + p.row_step * i_min + 1;
+    const int kv_min = p.window > 0 ? min(kv_first, p.window) : kv_first;
     // Blocks below every row's window are skipped whole.
     const int kv_lo = p.window > 0 ? max(0, w.L - p.q_len + i_min + 1 - p.window) / BN * BN : 0;
     w.kv_begin = kv_lo;
@@ -233,8 +257,8 @@ __device__ void tc_direct_item(const TcParams &p, int r, int &u, int &t0, int &t
         tstep = p.tiles_per_head;
     } else {
         u = r % units;
-        t0 = r / units;
-        tstep = 0;
+        t0 = r / units * NT;  // NT = 2: cross attention's neighbouring tiles of one unit
+        tstep = NT - 1;
     }
 }
 
@@ -347,6 +371,11 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                 if (f < w.rows_unit && f % p.q_len < rows_valid) nan_row<D>(p, w.b, w.hkv, f);
             }
             // split mode: the merge writes NaN rows for this sequence
+        } else if (w.state == 3) {
+            if (!p.split && threadIdx.x < NT * BM) {
+                const int f = (w.t0 + (int)(threadIdx.x / BM) * w.tstep) * BM + threadIdx.x % BM;
+                if (f < w.rows_unit && f % p.q_len < w.qn) empty_row<D>(p, w.b, w.hkv, f);
+            }
         } else if ((bad_page >> it) & 1) {
             if (threadIdx.x == 0 && p.status) atomicOr(p.status, ATLAS_DEV_BAD_PAGE);
             if (threadIdx.x < NT * BM) {
@@ -658,7 +687,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         const int f = (w.t0 + x * w.tstep) * BM + r;
         const bool valid = f < w.rows_unit && f % p.q_len < w.qn;  // padding rows: no queries
         const int i = valid ? f % p.q_len : 0;
-        const int lim_row = valid ? min(w.L - p.q_len + i + 1, w.kv_end) : 0;
+        const int lim_row = valid ? min(w.L - p.q_len + p.row_step * i + 1, w.kv_end) : 0;
         const int lo_row =
             (valid && p.window > 0) ? max(0, w.L - p.q_len + i + 1 - p.window) : 0;
         float m_used = -INFINITY, l = 0.f;
@@ -1084,7 +1113,10 @@ cudaError_t launch_instance(const TcParams &p, const CUtensorMap &tmQ, const CUt
         configured[dev] = 1;
     }
     const int tiles = p.B * p.Hkv * p.tiles_per_unit;
-    dim3 grid = p.split ? dim3(p.n_chunks, tiles, 1) : dim3(tiles / NT, 1, 1);
+    // (cross attention pairs the tiles of one unit; an odd count leaves half a pair idle)
+    const int pairs = p.B * p.Hkv * ((p.tiles_per_unit + NT - 1) / NT);
+    dim3 grid = p.split ? dim3(p.n_chunks, tiles, 1)
+                        : dim3(p.tiles_per_head > 0 ? tiles / NT : pairs, 1, 1);
     // Direct prefill with more tile pairs than SMs: one CTA per SM walks several
     // (at most kMaxItems), so that CTA start-up, the first loads and the epilogue
     // overlap the neighbouring items' work.
@@ -1112,8 +1144,10 @@ cudaError_t launch_instance(const TcParams &p, const CUtensorMap &tmQ, const CUt
 cudaError_t launch_fmha_tc(const TcParams &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,
                            const CUtensorMap &tmV, cudaStream_t stream) {
     // Two tiles per CTA when two q heads of a group can share every K/V block:
-    // direct output, an even group, prompt rows in whole tiles.
-    const bool pair = !p.split && p.tiles_per_head > 0 && p.G % 2 == 0;
+    // direct output, an even group, prompt rows in whole tiles.  Cross attention's rows
+    // all see the same keys, so there any two tiles of one (sequence, kv head) do.
+    const bool pair = !p.split && (p.row_step ? p.tiles_per_head > 0 && p.G % 2 == 0
+                                              : p.tiles_per_unit > 1);
     if (p.D == 64)
         return pair ? launch_instance<2, 64>(p, tmQ, tmK, tmV, stream)
                     : launch_instance<1, 64>(p, tmQ, tmK, tmV, stream);

@@ -165,6 +165,18 @@ __device__ void nan_row(const TcParams &p, int b, int hkv, int f) {
     if (p.lse) p.lse[row] = nan;
 }
 
+// Row f of (b, hkv) of cross attention over no encoder states, direct mode: 0, with
+// lse -inf (or the sink, whose weight has no value row).
+template <int D>
+__device__ void empty_row(const TcParams &p, int b, int hkv, int f) {
+    const int64_t row = tile_row(p, b, hkv, f);
+    const float sink = p.sinks ? p.sinks[(row / p.q_len) % p.Hq] : -INFINITY;
+    const float v = isnan(sink) ? sink : 0.f;
+    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * D);
+    for (int k = 0; k < D / 4; ++k) o[k] = make_float4(v, v, v, v);
+    if (p.lse) p.lse[row] = sink;
+}
+
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     fmha_tf32x3_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -223,7 +235,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const bool spans = (f_last / p.q_len) != (f0 / p.q_len);
     const int i_min = spans ? 0 : f0 % p.q_len;
 
-    if (qn < 0 || qn > p.q_len || seq_len < qn || seq_len > p.max_pages * p.P ||
+    if (qn < 0 || qn > p.q_len || seq_len < p.row_step * qn || seq_len > p.max_pages * p.P ||
         (p.require_full && seq_len != qn)) {
         if (threadIdx.x == 0 && c == 0 && p.status) atomicOr(p.status, ATLAS_DEV_BAD_SEQLEN);
         const int rows_valid = (qn >= 0 && qn <= p.q_len) ? qn : p.q_len;
@@ -235,8 +247,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     }
     if (i_min >= qn) return;  // only padding rows of a ragged sequence
     const int i_max = min(spans ? p.q_len - 1 : f_last % p.q_len, qn - 1);
-    const int L = seq_len - qn + p.q_len;
-    const int kv_hi = L - p.q_len + i_max + 1;
+    // Row i sees L - q_len + row_step * i + 1 keys: the suffix rule, or (cross attention)
+    // all seq_len encoder states.
+    const int L = seq_len + p.q_len - (p.row_step ? qn : 1);
+    const int kv_hi = L - p.q_len + p.row_step * i_max + 1;
+    if (kv_hi == 0) {  // no encoder states (split mode: the merge writes these rows)
+        if (!p.split && threadIdx.x < BM) {
+            const int f = f0 + threadIdx.x;
+            if (f < rows_unit && f % p.q_len < qn) empty_row<D>(p, b, hkv, f);
+        }
+        return;
+    }
     const int kv_lo = p.window > 0 ? max(0, L - p.q_len + i_min + 1 - p.window) / BN * BN : 0;
     int kv_begin = kv_lo, kv_end = kv_hi;
     if (p.split) {
@@ -594,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const int f = f0 + r;
         const bool valid = f < rows_unit && f % p.q_len < qn;
         const int i = valid ? f % p.q_len : 0;
-        const int lim_row = valid ? min(L - p.q_len + i + 1, kv_end) : 0;
+        const int lim_row = valid ? min(L - p.q_len + p.row_step * i + 1, kv_end) : 0;
         const int lo_row = (valid && p.window > 0) ? max(0, L - p.q_len + i + 1 - p.window) : 0;
         const bool capped = p.softcap_log2 > 0.f;
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);

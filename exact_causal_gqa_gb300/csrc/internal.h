@@ -46,6 +46,9 @@ struct SplitParams {
     int32_t n_chunks;           // splits per (sequence, kv head): ceil(max_pages*P / chunk)
     int32_t col_tiles;          // ceil(G*q_len / columns per CTA)
     int32_t require_full;       // prefill: seq_len must equal q_len
+    // Keys one query row sees more than the row before it: 1 (causal), or 0 for cross
+    // attention, whose rows all see the seq_len encoder states (possibly none).
+    int32_t row_step;
     float scale_log2;           // scale * log2(e)
     int32_t window;             // > 0: keys pos - window < t <= pos only
     float softcap_log2;         // > 0: s2 = softcap_log2 * tanh(raw * softcap_inv)
@@ -73,6 +76,7 @@ struct MergeParams {
     const int32_t *seq_lens;
     int32_t B, Hq, D, q_len, max_pages, P, chunk, n_chunks, require_full;
     int32_t balanced;           // splits of balanced_split(seq_len, chunk) keys
+    int32_t row_step;           // 1 causal, 0 cross attention (as in SplitParams)
     int32_t window;             // splits below a row's window hold nothing for it
     const float *sinks;         // [Hq] natural-log logits or null: one more state (m, 1, 0)
     const int32_t *q_lens;      // [B] ragged query rows or null; padding rows untouched
@@ -101,6 +105,7 @@ struct TcParams {
     int32_t balanced;         // split mode: balanced splits in longest-first order
                               // (tc_order.cuh); the grid's CTAs are work items
     int32_t require_full;
+    int32_t row_step;         // 1 causal, 0 cross attention (as in SplitParams)
     int32_t hilo_below;       // tiles whose rows see fewer keys use a hi+lo split of P
     int32_t negate_scores;    // scale < 0: S = -Q K^T with |scale| (keeps the max exact)
     float scale_log2;         // |scale| * log2(e)

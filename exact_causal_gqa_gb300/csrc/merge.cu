@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const MergeParams p)
     const int b = bh / p.Hq;
     const int L = active ? p.seq_lens[b] : 0;
     const int qn = !active ? 0 : p.q_lens ? p.q_lens[b] : p.q_len;  // ragged: rows of b
-    const bool bad_len = qn < 0 || qn > p.q_len || L < qn || L > p.max_pages * p.P ||
+    const bool bad_len = qn < 0 || qn > p.q_len || L < p.row_step * qn || L > p.max_pages * p.P ||
                          (p.require_full && L != qn);
     if (!bad_len && i >= qn) active = false;  // padding row: not a query, not written
     if (W == 1 && !active) return;            // (W > 1: every warp reaches the exchange)
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const MergeParams p)
     for (int j = 0; j < DPL; ++j) acc[j] = 0.f;
     bool has_nan = false;
     if (active && !bad_len) {
-        const int visible = L - qn + i + 1;
+        const int visible = p.row_step ? L - qn + i + 1 : L;
         // splits holding this row's keys: [first, nsplit)
         const int chunk =
             p.balanced ? balanced_split(min(L, p.max_pages * p.P), p.chunk) : p.chunk;
@@ -158,7 +158,12 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const MergeParams p)
 
     float o[DPL];
     float lse = __int_as_float(0x7fc00000);
-    if (bad_len || has_nan || M == -INFINITY) {
+    if (!bad_len && !has_nan && M == -INFINITY && p.row_step == 0 && L == 0) {
+        // cross attention over no encoder states: nothing to weigh
+#pragma unroll
+        for (int j = 0; j < DPL; ++j) o[j] = 0.f;
+        lse = -INFINITY;
+    } else if (bad_len || has_nan || M == -INFINITY) {
 #pragma unroll
         for (int j = 0; j < DPL; ++j) o[j] = __int_as_float(0x7fc00000);
     } else {

@@ -36,7 +36,7 @@ __device__ __forceinline__ void record(uint32_t *status, uint32_t bit) {
 
 // qn: the sequence's query rows (q_lens[b] when ragged, else q_len).
 __device__ __forceinline__ bool seq_len_bad(const SplitParams &p, int L, int qn) {
-    return qn < 0 || qn > p.q_len || L < qn || L > p.max_pages * p.P ||
+    return qn < 0 || qn > p.q_len || L < p.row_step * qn || L > p.max_pages * p.P ||
            (p.require_full && L != qn);
 }
 
@@ -46,11 +46,16 @@ __device__ __forceinline__ int64_t column_row(const SplitParams &p, int b, int h
     return ((int64_t)b * p.Hq + (int64_t)hkv * p.G) * p.q_len + n;
 }
 
-// Keys visible to column n (absolute count), as defined by the suffix rule.  L
-// here is the sequence length shifted by q_len - qn (see split_prologue), so the
-// same formula serves ragged batches.
+// The sequence length shifted so that row i sees shifted - q_len + row_step * i + 1
+// keys: by q_len - qn for causal rows (the suffix rule, ragged batches included), and
+// by q_len - 1 for cross attention, where that is seq_len for every row.
+__device__ __forceinline__ int shifted_len(const SplitParams &p, int seq_len, int qn) {
+    return seq_len + p.q_len - (p.row_step ? qn : 1);
+}
+
+// Keys visible to column n (absolute count); L is the shifted length.
 __device__ __forceinline__ int column_visible(const SplitParams &p, int L, int n) {
-    return L - p.q_len + (n % p.q_len) + 1;
+    return L - p.q_len + p.row_step * (n % p.q_len) + 1;
 }
 
 // First key column n may see: the lower end of its window, or 0.
@@ -81,9 +86,27 @@ __device__ void direct_nan_rows(const SplitParams &p, int b, int hkv, int col0, 
     }
 }
 
+// Direct mode, cross attention over no encoder states: the softmax over nothing (or
+// over the sink alone) has no value rows, so the rows are 0 and lse is -inf (or the sink).
+__device__ void direct_empty_rows(const SplitParams &p, int b, int hkv, int col0, int ncols,
+                                  int qn) {
+    for (int idx = threadIdx.x; idx < ncols * p.D; idx += blockDim.x) {
+        const int c = idx / p.D, d = idx % p.D;
+        if ((col0 + c) % p.q_len >= qn) continue;
+        const int64_t row = column_row(p, b, hkv, col0 + c);
+        const float sink = p.sinks ? p.sinks[(row / p.q_len) % p.Hq] : -INFINITY;
+        const float o = isnan(sink) ? sink : 0.f;
+        if (p.out_bf16)
+            static_cast<__nv_bfloat16 *>(p.out)[row * p.D + d] = __float2bfloat16_rn(o);
+        else
+            static_cast<float *>(p.out)[row * p.D + d] = o;
+        if (d == 0 && p.lse) p.lse[row] = sink;
+    }
+}
+
 // Shared prologue: decides whether this CTA has work.  Returns false when the
 // CTA must exit (nothing visible, or an error that has been recorded).
-// Returns L shifted to L - qn + q_len: with it, row i (< qn) of a ragged sequence
+// Returns L as shifted_len: with it, row i (< qn) of a ragged causal sequence
 // sits at position L_shifted - q_len + i = seq_len - qn + i, as in a full batch.
 // Columns with row index >= qn are padding (qn out).
 // Why split_prologue found no work for the CTA.
@@ -113,7 +136,8 @@ __device__ bool split_prologue(const SplitParams &p, int ct, int &L, int &kv_beg
         why = kBadLen;
         return false;
     }
-    L = L - qn + p.q_len;
+    const int seq_len = L;
+    L = shifted_len(p, seq_len, qn);
     int i_max = -1, i_min = p.q_len;
     for (int c = 0; c < ncols; ++c) {
         const int i = (col0 + c) % p.q_len;
@@ -122,7 +146,11 @@ __device__ bool split_prologue(const SplitParams &p, int ct, int &L, int &kv_beg
         i_min = min(i_min, i);
     }
     if (i_max < 0) return false;  // only padding rows
-    const int kv_hi = L - p.q_len + i_max + 1;
+    if (!p.row_step && seq_len == 0) {  // no encoder states (the merges know this case too)
+        if (p.direct) direct_empty_rows(p, b, hkv, col0, ncols, qn);
+        return false;
+    }
+    const int kv_hi = L - p.q_len + p.row_step * i_max + 1;
     // Keys below every column's window are skipped whole (64-key blocks).
     const int kv_lo = p.window > 0 ? max(0, L - p.q_len + i_min + 1 - p.window) : 0;
     kv_begin = max((int)blockIdx.x * p.chunk, kv_lo / kSplitBlockTokens * kSplitBlockTokens);
@@ -645,7 +673,7 @@ __device__ void cluster_merge(const SplitParams &p, float *slots, int col0, int 
         const int64_t row = column_row(p, b, hkv, col0 + c);
         float o = __int_as_float(0x7fc00000), lse = o;
         if (!bad_len) {
-            const int visible = L - qn + i + 1;
+            const int visible = p.row_step ? L - qn + i + 1 : L;
             // splits holding this row's keys: [first, nsplit)
             const int first = p.window > 0 ? max(0, visible - p.window) / p.chunk : 0;
             const int nsplit = min((visible + p.chunk - 1) / p.chunk, p.n_chunks);
@@ -669,7 +697,10 @@ __device__ void cluster_merge(const SplitParams &p, float *slots, int col0, int 
                 if (isnan(l[u]) || isnan(m[u])) has_nan = true;
                 else if (l[u] > 0.f) M = fmaxf(M, m[u]);
             }
-            if (!has_nan && M != -INFINITY) {
+            if (!has_nan && visible == 0 && M == -INFINITY) {
+                o = 0.f;  // cross attention over no encoder states
+                lse = -INFINITY;
+            } else if (!has_nan && M != -INFINITY) {
                 float lsum = p.sinks ? ex2(sink2 - M) : 0.f, acc = 0.f;
 #pragma unroll
                 for (int u = 0; u < kClusterSlots; ++u) {

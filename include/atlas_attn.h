@@ -77,7 +77,12 @@ typedef enum {
 
 typedef enum { ATLAS_F32 = 0, ATLAS_BF16 = 1 } atlas_dtype;
 
-typedef enum { ATLAS_KIND_DECODE = 0, ATLAS_KIND_SUFFIX = 1, ATLAS_KIND_PREFILL = 2 } atlas_kind;
+typedef enum {
+    ATLAS_KIND_DECODE = 0,
+    ATLAS_KIND_SUFFIX = 1,
+    ATLAS_KIND_PREFILL = 2,
+    ATLAS_KIND_CROSS = 3
+} atlas_kind;
 
 /* Bits the kernels OR into *status_word. */
 #define ATLAS_DEV_BAD_PAGE 1u    /* a page id outside [0, num_pages) */
@@ -188,6 +193,28 @@ atlas_status atlas_attn_prefill(const void *q, const void *k_pages, const void *
                                 const int32_t *page_table, const int32_t *seq_lens,
                                 int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                                 int32_t page_tokens, float scale, const atlas_launch *L);
+
+/*
+ * atlas_attn_cross: attention of decoder rows to an encoder's states, whose K/V lie
+ * in pages like any cache (one pool for both is fine: the page table says which
+ * pages are whose).  There are no positions: every one of sequence b's query rows
+ * sees all keys t < enc_lens[b], so
+ *   out[b][h][i] = sum_{t < enc_lens[b]} exp(s_t - M) v_t / sum_{t < enc_lens[b]} exp(s_t - M)
+ * and q_len has nothing to do with enc_lens: one row (a decode step), or a prompt's
+ * rows (ragged with L->q_lens: rows i >= q_lens[b] are not written).  enc_lens[b] may
+ * be 0, a sequence without encoder states: its rows are 0 with lse -inf, or, with
+ * sinks, 0 with lse = sink (a sink has no value row).  Softcap, sinks and the fixed
+ * split size work as in the causal calls.  A window is ATLAS_ERR_INVALID_ARG (nothing
+ * has a position); a phase other than ATLAS_PHASE_ALL or a chunk_range is
+ * ATLAS_ERR_UNSUPPORTED.  enc_lens[b] < 0 or > max_pages_per_seq * page_tokens sets
+ * ATLAS_DEV_BAD_SEQLEN and leaves that sequence's rows NaN.  The CFR-Atlas README,
+ * "Core contract", gives the same result for any set of exact pages; the pages have
+ * no entry point for it.
+ */
+atlas_status atlas_attn_cross(const void *q, const void *k_pages, const void *v_pages,
+                              const int32_t *page_table, const int32_t *enc_lens,
+                              int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                              int32_t page_tokens, float scale, const atlas_launch *L);
 
 /*
  * Bytes of device workspace the call of `kind` with these arguments needs (0 if
