@@ -13,12 +13,16 @@ Functions (same names as the C entry points):
   prefill(...)  causal self-attention of a prompt     -> atlas_attn_prefill
   cross(...)    decoder rows over an encoder's states -> atlas_attn_cross
   kv_append(...)  new tokens' K/V into their pages    -> atlas_kv_append
+  kv_append_rope(...)  the same, with rotary positions of several axes applied to the
+                new keys and the step's queries       -> atlas_kv_append_rope
   workspace_size(kind, ...)                            -> atlas_attn_workspace_size
   run_host(kind, ...)  host tensors in, host tensor out (copies on the stream)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -26,10 +30,11 @@ import torch
 
 from . import _build
 
-__all__ = ["AtlasError", "decode", "suffix", "prefill", "cross", "kv_append", "workspace_size", "run_host",
+__all__ = ["AtlasError", "decode", "suffix", "prefill", "cross", "kv_append",
+           "kv_append_rope", "workspace_size", "run_host",
            "library_path", "DEV_BAD_PAGE", "DEV_BAD_SEQLEN", "DEV_TIMEOUT",
            "DEBUG_WITHHOLD_STAGE", "KIND_DECODE", "KIND_SUFFIX", "KIND_PREFILL",
-           "KIND_CROSS"]
+           "KIND_CROSS", "rope_sections"]
 
 KIND_DECODE, KIND_SUFFIX, KIND_PREFILL, KIND_CROSS = 0, 1, 2, 3
 _KINDS = {"decode": KIND_DECODE, "suffix": KIND_SUFFIX, "prefill": KIND_PREFILL,
@@ -97,6 +102,19 @@ class _Append(ctypes.Structure):
                 ("stream", ctypes.c_void_p)]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("kv_dtype", ctypes.c_int), ("n_q_heads", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("q_strides", ctypes.c_int64 * 3), ("k_strides", ctypes.c_int64 * 3),
+                ("v_strides", ctypes.c_int64 * 3), ("positions", ctypes.c_void_p),
+                ("n_axes", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("pair_axis", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("theta", ctypes.c_double),
+                ("status_word", ctypes.c_void_p), ("stream", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -128,6 +146,9 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.atlas_kv_append.argtypes = [ctypes.c_void_p] * 7 + [ctypes.c_int32] * 3 + [
         ctypes.POINTER(_Append)]
     lib.atlas_kv_append.restype = ctypes.c_int
+    lib.atlas_kv_append_rope.argtypes = [ctypes.c_void_p] * 7 + [ctypes.c_int32] * 3 + [
+        ctypes.POINTER(_Rope)]
+    lib.atlas_kv_append_rope.restype = ctypes.c_int
     lib.atlas_attn_status_string.argtypes = [ctypes.c_int]
     lib.atlas_attn_status_string.restype = ctypes.c_char_p
     lib.atlas_attn_split_tokens.argtypes = [ctypes.c_int] + [ctypes.c_int32] * 4 + [
@@ -311,8 +332,9 @@ def cross(q, k_pages, v_pages, page_table, enc_lens, n_q_heads, n_kv_heads, head
           page_tokens, scale, **kw):
     """Attention of q_len decoder rows to all enc_lens[b] encoder states of their
     sequence (no causal mask; enc_lens[b] == 0 gives rows of 0 and lse -inf)."""
-    return _call("cross", q, k_pages, v_pages, page_table, enc_lens, n_q_heads, n_kv_heads,
-                 head_dim, page_tokens, scale, **kw)
+    with _on(q.device):
+        return _call("cross", q, k_pages, v_pages, page_table, enc_lens, n_q_heads, n_kv_heads,
+                     head_dim, page_tokens, scale, **kw)
 
 
 def run(problem, **kw):
@@ -349,6 +371,124 @@ def kv_append(k_new, v_new, k_pages, v_pages, page_table, seq_lens, n_new=None,
                              ctypes.byref(A))
     if rc != 0:
         raise AtlasError(rc, status_string(rc))
+
+
+def _on(device):
+    """The device guard of a call: work goes to the tensors' device, whichever is current."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _check(like, **tensors):
+    """Every given tensor is a CUDA tensor of `like`'s device, contiguous, of the dtype given."""
+    for name, (t, dtype) in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda or t.device != like.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor on {like.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}")
+
+
+@functools.lru_cache(maxsize=64)
+def _host_array(ctype, values):
+    return (ctype * len(values))(*values)
+
+
+def _row_strides(name, t):
+    """Element strides (batch, head, token) of a [B][H][n][D] view with contiguous rows."""
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name} must have contiguous rows of head_dim elements")
+    return (ctypes.c_int64 * 3)(*([0, 0, 0] if t.is_contiguous() else t.stride()[:3]))
+
+
+def kv_append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, positions, *,
+                   theta=10000.0, inv_freq=None, rot_dim=None, pair_axis=None,
+                   interleaved=False, n_new=None, q_out=None, status=None):
+    """Rotate the step's queries and new keys by their positions, and write the keys and
+    values into the cache (atlas_kv_append_rope).
+
+    q [B][Hq][n][D] (or None), k_new and v_new [B][Hkv][n][D]: views with contiguous rows,
+    e.g. slices of a fused projection [B][n][heads][D] transposed to [B][heads][n][D].
+    positions int32 [n_axes][B][n] (or [B][n] for one axis).  rot_dim: rotated leading
+    elements of a row (default all); pair_axis: rot_dim // 2 axis numbers, one per pair
+    (default 0), see ``rope_sections``; inv_freq: rot_dim // 2 host floats, radians per
+    position (default theta ** (-2 p / rot_dim)); interleaved: pairs (2p, 2p + 1) rather
+    than (p, p + rot_dim / 2).  Returns the rotated queries [B][Hq][n][D] (q_out, which
+    may be q itself when q is contiguous); None without q."""
+    lib = load_library()
+    if k_new.dim() != 4 or v_new.shape != k_new.shape or k_pages.dim() != 4 or \
+            v_pages.shape != k_pages.shape or k_pages.shape[1] != k_new.shape[1] or \
+            k_pages.shape[3] != k_new.shape[3]:
+        raise ValueError("k_new/v_new must be [B][Hkv][n][D], pools [pages][Hkv][P][D]")
+    B, Hkv, n, D = k_new.shape
+    dtype = k_pages.dtype
+    if q is not None and (q.dim() != 4 or q.shape[0] != B or q.shape[2:] != k_new.shape[2:]):
+        raise ValueError("q must be [B][Hq][n][D] like k_new")
+    for name, t in (("q", q), ("k_new", k_new), ("v_new", v_new)):
+        if t is not None and (not t.is_cuda or t.device != k_pages.device or t.dtype != dtype):
+            raise ValueError(f"{name} must be a {dtype} tensor on {k_pages.device}")
+    if positions.dim() == 2:
+        positions = positions[None]
+    if positions.dim() != 3 or positions.shape[1:] != (B, n):
+        raise ValueError("positions must be [n_axes][B][n]")
+    _check(k_pages, k_pages=(k_pages, dtype), v_pages=(v_pages, dtype),
+           page_table=(page_table, torch.int32), seq_lens=(seq_lens, torch.int32),
+           positions=(positions, torch.int32), n_new=(n_new, torch.int32),
+           q_out=(q_out, dtype), status=(status, torch.int32))
+    if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.numel() != B or \
+            (n_new is not None and n_new.numel() != B):
+        raise ValueError("page_table must be [B][max_pages]; seq_lens and n_new [B]")
+    rot_dim = D if rot_dim is None else rot_dim
+    for name, x in (("pair_axis", pair_axis), ("inv_freq", inv_freq)):
+        if x is not None and len(x) != rot_dim // 2:
+            raise ValueError(f"{name} must have rot_dim / 2 entries")
+    if q_out is not None and (q is None or q_out.shape != q.shape):
+        raise ValueError("q_out must have q's shape")
+    if q_out is not None and q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+        raise ValueError("q_out may be q itself only when q is contiguous")
+    R = _Rope()
+    R.batch, R.max_pages_per_seq, R.num_pages, R.max_new = B, page_table.shape[1], k_pages.shape[0], n
+    R.kv_dtype = _DTYPES.get(dtype, -1)
+    R.k_strides, R.v_strides = _row_strides("k_new", k_new), _row_strides("v_new", v_new)
+    R.n_q_heads = 0
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        R.n_q_heads, R.q, R.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        R.q_strides = _row_strides("q", q)
+    R.positions, R.n_axes = positions.data_ptr(), positions.shape[0]
+    R.rot_dim, R.interleaved, R.theta = rot_dim, int(bool(interleaved)), theta
+    if pair_axis is not None:
+        R.pair_axis = ctypes.addressof(_host_array(ctypes.c_int32, tuple(pair_axis)))
+    if inv_freq is not None:
+        freq = (ctypes.c_double * len(inv_freq))(*inv_freq)
+        R.inv_freq = ctypes.addressof(freq)
+    R.status_word = _ptr(status)
+    R.stream = torch.cuda.current_stream(k_pages.device).cuda_stream
+    with _on(k_pages.device):
+        rc = lib.atlas_kv_append_rope(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(),
+                                      v_pages.data_ptr(), page_table.data_ptr(),
+                                      seq_lens.data_ptr(), _ptr(n_new), Hkv, D,
+                                      k_pages.shape[2], ctypes.byref(R))
+    if rc != 0:
+        raise AtlasError(rc, status_string(rc))
+    return q_out
+
+
+def rope_sections(sizes, cycle=False):
+    """The pair_axis of kv_append_rope for axes that turn sizes[a] pairs each: axis 0's
+    pairs, then axis 1's, ... or (cycle) pair after pair to the next axis that has any left."""
+    if not cycle:
+        return tuple(a for a, size in enumerate(sizes) for _ in range(size))
+    left, out = list(sizes), []
+    while any(left):
+        for a, size in enumerate(left):
+            if size > 0:
+                out.append(a)
+                left[a] -= 1
+    return tuple(out)
 
 
 class EventTimer:

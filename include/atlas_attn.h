@@ -271,6 +271,63 @@ atlas_status atlas_kv_append(const void *k_new, const void *v_new, void *k_pages
                              const int32_t *n_new, int32_t n_kv_heads, int32_t head_dim,
                              int32_t page_tokens, const atlas_append *A);
 
+/* Arguments of atlas_kv_append_rope beyond its pointer / size list. */
+#define ATLAS_ROPE_MAX_AXES 4
+typedef struct {
+    int32_t batch;
+    int32_t max_pages_per_seq;
+    int32_t num_pages;
+    int32_t max_new;           /* rows per sequence in q, k_new and v_new;
+                                  batch * max_new < 2^31 - 1 */
+    atlas_dtype kv_dtype;      /* element type of q, q_out, k_new, v_new and the pools */
+    int32_t n_q_heads;         /* heads of q; 0: no queries (q and q_out are ignored) */
+    const void *q;             /* device, read: [batch][n_q_heads][max_new][head_dim] by q_strides */
+    void *q_out;               /* device, written: the rotated queries, dense
+                                  [batch][n_q_heads][max_new][head_dim] as the attention calls
+                                  take them; may be q itself when q is dense, and overlaps no
+                                  other input */
+    int64_t q_strides[3];      /* element strides (batch, head, token) of q, k_new and v_new, */
+    int64_t k_strides[3];      /* whose rows of head_dim elements are contiguous; all three 0: */
+    int64_t v_strides[3];      /* dense.  Multiples of 16 bytes (a fused projection's output
+                                  [batch][token][heads][head_dim] is read where it lies) */
+    const int32_t *positions;  /* device [n_axes][batch][max_new]: the position of each new
+                                  token along each axis (any int32) */
+    int32_t n_axes;            /* 1 .. ATLAS_ROPE_MAX_AXES: e.g. time, height, width */
+    int32_t rot_dim;           /* even, 2 .. head_dim: the first rot_dim elements of a row of q
+                                  or k are rotated, the others copied */
+    int32_t interleaved;       /* 0: pair p is elements p and p + rot_dim / 2; 1: 2p and 2p + 1 */
+    const int32_t *pair_axis;  /* HOST [rot_dim / 2]: the axis whose position turns pair p;
+                                  NULL: axis 0 for every pair */
+    const double *inv_freq;    /* HOST [rot_dim / 2]: radians per position of pair p (finite);
+                                  NULL: theta^(-2 p / rot_dim) */
+    double theta;              /* base of the frequencies when inv_freq is NULL; > 0 */
+    uint32_t *status_word;     /* optional device word (ATLAS_DEV_* bits) */
+    void *stream;              /* cudaStream_t; NULL = the legacy default stream */
+} atlas_rope;
+
+/*
+ * atlas_kv_append_rope: atlas_kv_append with rotary positions applied on the way, and
+ * the step's queries rotated by the same angles.  For b < batch, j < n_new[b] (n_new
+ * NULL: all max_new rows), pair p of a row of q or k (x, y its two elements) becomes
+ *   (x cos z - y sin z, y cos z + x sin z),   z = positions[pair_axis[p]][b][j] * inv_freq[p],
+ * computed in float32 from an angle that is exact to 2^-24 turns at any position (for
+ * |inv_freq| <= 1), and rounded once; v is copied.  Rotated keys and values go to position seq_lens[b] + j of
+ * the cache (the slot, which eviction may have made smaller than the token's position),
+ * rotated queries to q_out.  The pair_axis and inv_freq arrays are read before the call
+ * returns (a captured call keeps the angles it was captured with; positions are read on
+ * the device).  Conditions and errors as for atlas_kv_append: the pages of the new
+ * positions must be in page_table, no two new tokens may share a slot, seq_lens is not
+ * advanced; a bad page id or position sets ATLAS_DEV_BAD_PAGE / ATLAS_DEV_BAD_SEQLEN and
+ * that token's k and v are skipped (its q_out row is written all the same); an n_new[b]
+ * outside [0, max_new] sets ATLAS_DEV_BAD_SEQLEN and skips the sequence.  Rows
+ * j >= n_new[b] of q_out are not written.
+ */
+atlas_status atlas_kv_append_rope(const void *k_new, const void *v_new, void *k_pages,
+                                  void *v_pages, const int32_t *page_table,
+                                  const int32_t *seq_lens, const int32_t *n_new,
+                                  int32_t n_kv_heads, int32_t head_dim, int32_t page_tokens,
+                                  const atlas_rope *R);
+
 /* Static, human-readable text for a status code. */
 const char *atlas_attn_status_string(atlas_status status);
 

@@ -1,6 +1,7 @@
 """Plain fp64 forms of the cache operators, for the tests: numpy on logical (unpaged)
 arrays, one row at a time, with nothing of the library's.  Paging is tests/paging.py's."""
 import math
+from fractions import Fraction
 
 import numpy as np
 
@@ -8,6 +9,14 @@ import numpy as np
 def widen(t):
     """The exact values of a torch tensor (any float type) as fp64 numpy."""
     return t.detach().cpu().double().numpy()
+
+
+TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582")
+
+
+def angle(position, freq):
+    """position * freq (an int and a double) modulo a turn, exact to the last bit of a double."""
+    return float(Fraction(int(position)) * Fraction(freq) % TWO_PI)
 
 
 def cross_rows(q, k, v, lens, scale, q_lens=None, sinks=None, softcap=0.0):
@@ -32,3 +41,17 @@ def cross_rows(q, k, v, lens, scale, q_lens=None, sinks=None, softcap=0.0):
                 out[b, h, i] = p @ v[b, h // G, : lens[b]] / total
                 lse[b, h, i] = m + math.log(total)
     return out, lse
+
+
+def pair_elements(pairs, interleaved):
+    a = np.arange(pairs) * 2 if interleaved else np.arange(pairs)
+    return a, a + 1 if interleaved else a + pairs
+
+
+def turned(x, angles, interleaved):
+    """Rows x [..., D] with their first 2 * len(angles) elements turned by angles."""
+    a, b = pair_elements(len(angles), interleaved)
+    y = x.copy()
+    y[..., a] = x[..., a] * np.cos(angles) - x[..., b] * np.sin(angles)
+    y[..., b] = x[..., b] * np.cos(angles) + x[..., a] * np.sin(angles)
+    return y
