@@ -1,6 +1,6 @@
 """Exact causal grouped-query attention over paged K/V on GB300 (sm_103a).
 
-Python binding of ``libatlas_attn.so`` (C ABI in ``include/atlas_attn.h``).
+Python binding of ``libatlas_attn.so`` (C ABI in ``include/*.h``).
 This module only marshals arguments: it checks tensor shapes and dtypes,
 allocates outputs and workspace with torch, and passes raw device pointers and
 the current torch stream to the library.  Every step of the computation runs in
@@ -15,6 +15,9 @@ Functions (same names as the C entry points):
   kv_append(...)  new tokens' K/V into their pages    -> atlas_kv_append
   kv_append_rope(...)  the same, with rotary positions of several axes applied to the
                 new keys and the step's queries       -> atlas_kv_append_rope
+  kv_weights(...)  attention weight each cached key received -> atlas_kv_weights
+  kv_select(...)   the keys that stay under a budget  -> atlas_kv_select
+  kv_compact(...)  pages with only those keys left    -> atlas_kv_compact
   workspace_size(kind, ...)                            -> atlas_attn_workspace_size
   run_host(kind, ...)  host tensors in, host tensor out (copies on the stream)
 """
@@ -31,7 +34,7 @@ import torch
 from . import _build
 
 __all__ = ["AtlasError", "decode", "suffix", "prefill", "cross", "kv_append",
-           "kv_append_rope", "workspace_size", "run_host",
+           "kv_append_rope", "kv_weights", "kv_select", "kv_compact", "workspace_size", "run_host",
            "library_path", "DEV_BAD_PAGE", "DEV_BAD_SEQLEN", "DEV_TIMEOUT",
            "DEBUG_WITHHOLD_STAGE", "KIND_DECODE", "KIND_SUFFIX", "KIND_PREFILL",
            "KIND_CROSS", "rope_sections"]
@@ -115,6 +118,33 @@ class _Rope(ctypes.Structure):
                 ("status_word", ctypes.c_void_p), ("stream", ctypes.c_void_p)]
 
 
+class _Weights(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("q_len", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("weights", ctypes.c_void_p),
+                ("row_tokens", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+                ("q_lens", ctypes.c_void_p), ("window", ctypes.c_int32),
+                ("softcap", ctypes.c_float), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("status_word", ctypes.c_void_p),
+                ("stream", ctypes.c_void_p), ("sm_count", ctypes.c_int32)]
+
+
+class _Select(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("row_tokens", ctypes.c_int32),
+                ("budget", ctypes.c_int32), ("keep_first", ctypes.c_int32),
+                ("keep_recent", ctypes.c_int32), ("kept", ctypes.c_void_p),
+                ("new_lens", ctypes.c_void_p), ("kept_weights", ctypes.c_void_p),
+                ("status_word", ctypes.c_void_p), ("stream", ctypes.c_void_p)]
+
+
+class _Compact(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_kept", ctypes.c_int32),
+                ("kv_dtype", ctypes.c_int), ("new_page_table", ctypes.c_void_p),
+                ("new_max_pages", ctypes.c_int32), ("status_word", ctypes.c_void_p),
+                ("stream", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -149,6 +179,18 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.atlas_kv_append_rope.argtypes = [ctypes.c_void_p] * 7 + [ctypes.c_int32] * 3 + [
         ctypes.POINTER(_Rope)]
     lib.atlas_kv_append_rope.restype = ctypes.c_int
+    lib.atlas_kv_weights.argtypes = [ctypes.c_void_p] * 5 + [ctypes.c_int32] * 4 + [
+        ctypes.c_float, ctypes.POINTER(_Weights)]
+    lib.atlas_kv_weights.restype = ctypes.c_int
+    lib.atlas_kv_weights_workspace_size.argtypes = [ctypes.c_int32] * 4 + [
+        ctypes.POINTER(_Weights)]
+    lib.atlas_kv_weights_workspace_size.restype = ctypes.c_size_t
+    lib.atlas_kv_select.argtypes = [ctypes.c_void_p] * 2 + [ctypes.c_int32,
+                                                            ctypes.POINTER(_Select)]
+    lib.atlas_kv_select.restype = ctypes.c_int
+    lib.atlas_kv_compact.argtypes = [ctypes.c_void_p] * 5 + [ctypes.c_int32] * 3 + [
+        ctypes.POINTER(_Compact)]
+    lib.atlas_kv_compact.restype = ctypes.c_int
     lib.atlas_attn_status_string.argtypes = [ctypes.c_int]
     lib.atlas_attn_status_string.restype = ctypes.c_char_p
     lib.atlas_attn_split_tokens.argtypes = [ctypes.c_int] + [ctypes.c_int32] * 4 + [
@@ -489,6 +531,123 @@ def rope_sections(sizes, cycle=False):
                 out.append(a)
                 left[a] -= 1
     return tuple(out)
+
+
+def kv_weights(q, k_pages, page_table, seq_lens, lse, n_q_heads, n_kv_heads, head_dim,
+               page_tokens, scale, *, weights=None, accumulate=True, q_lens=None, window=0,
+               softcap=0.0, workspace=None, status=None, sm_count=0):
+    """Add the attention weight that each cached key received from the rows q
+    [B][Hq][q_len][D] to weights [B][Hkv][row_tokens] (float32; new zeros of
+    max_pages * P tokens when None), or overwrite with it (atlas_kv_weights).  lse
+    [B][Hq][q_len]: what the attention call with the same rows and options returned.
+    Returns weights."""
+    lib = load_library()
+    if q.dim() != 4 or k_pages.dim() != 4:
+        raise ValueError("q must be [B][Hq][q_len][D] and the pool [num_pages][Hkv][P][D]")
+    B = q.shape[0]
+    if q.shape[1] != n_q_heads or q.shape[3] != head_dim or \
+            k_pages.shape[1:] != (n_kv_heads, page_tokens, head_dim):
+        raise ValueError("q and the pool must have the shapes the sizes given say")
+    if weights is None:
+        weights = torch.zeros((B, n_kv_heads, page_table.shape[1] * page_tokens), device=q.device)
+    _check(q, q=(q, q.dtype), k_pages=(k_pages, q.dtype), page_table=(page_table, torch.int32),
+           seq_lens=(seq_lens, torch.int32), lse=(lse, torch.float32),
+           weights=(weights, torch.float32), q_lens=(q_lens, torch.int32),
+           status=(status, torch.int32))
+    if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.numel() != B or \
+            lse.numel() != q.shape[0] * q.shape[1] * q.shape[2] or weights.dim() != 3 or \
+            weights.shape[:2] != (B, n_kv_heads) or (q_lens is not None and q_lens.numel() != B):
+        raise ValueError("page_table must be [B][max_pages], seq_lens and q_lens [B], lse "
+                         "[B][Hq][q_len], weights [B][Hkv][row_tokens]")
+    W = _Weights()
+    W.batch, W.q_len, W.dtype = B, q.shape[2], _DTYPES.get(q.dtype, -1)
+    W.max_pages_per_seq, W.num_pages = page_table.shape[1], k_pages.shape[0]
+    W.weights, W.row_tokens, W.accumulate = weights.data_ptr(), weights.shape[2], int(bool(accumulate))
+    W.q_lens, W.window, W.softcap, W.sm_count = _ptr(q_lens), window, softcap, sm_count
+    W.status_word = _ptr(status)
+    W.stream = torch.cuda.current_stream(q.device).cuda_stream
+    with _on(q.device):
+        need = lib.atlas_kv_weights_workspace_size(n_q_heads, n_kv_heads, head_dim, page_tokens,
+                                                   ctypes.byref(W))
+        if workspace is None and 0 < need < ctypes.c_size_t(-1).value:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if workspace is not None:
+            W.workspace = workspace.data_ptr()
+            W.workspace_bytes = workspace.numel() * workspace.element_size()
+        rc = lib.atlas_kv_weights(q.data_ptr(), k_pages.data_ptr(), page_table.data_ptr(),
+                                  seq_lens.data_ptr(), lse.data_ptr(), n_q_heads, n_kv_heads,
+                                  head_dim, page_tokens, float(scale), ctypes.byref(W))
+    if rc != 0:
+        raise AtlasError(rc, status_string(rc))
+    return weights
+
+
+def kv_select(weights, seq_lens, budget, *, keep_first=0, keep_recent=0, kept=None, new_lens=None,
+              kept_weights=None, status=None):
+    """The keys of each (sequence, kv head) that stay under the budget: the first and the
+    most recent ones, the others by weights [B][Hkv][row_tokens] (atlas_kv_select).
+    Returns kept int32 [B][Hkv][budget] (ascending, then -1), new_lens int32 [B] and
+    kept_weights [B][Hkv][budget], the totals to go on with after kv_compact."""
+    lib = load_library()
+    if weights.dim() != 3 or seq_lens.numel() != weights.shape[0]:
+        raise ValueError("weights must be [B][Hkv][row_tokens] and seq_lens [B]")
+    B, Hkv, T = weights.shape
+    budget = int(budget)
+    shape = (B, Hkv, max(budget, 0))
+    dev = weights.device
+    if kept is None:
+        kept = torch.empty(shape, dtype=torch.int32, device=dev)
+    if kept_weights is None:
+        kept_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    _check(weights, weights=(weights, torch.float32), seq_lens=(seq_lens, torch.int32),
+           kept=(kept, torch.int32), kept_weights=(kept_weights, torch.float32),
+           new_lens=(new_lens, torch.int32), status=(status, torch.int32))
+    if kept.shape != shape or kept_weights.shape != shape or new_lens.numel() != B:
+        raise ValueError("kept and kept_weights must be [B][Hkv][budget] and new_lens [B]")
+    S = _Select()
+    S.batch, S.row_tokens, S.budget = B, T, budget
+    S.keep_first, S.keep_recent = keep_first, keep_recent
+    S.kept, S.new_lens, S.kept_weights = kept.data_ptr(), new_lens.data_ptr(), kept_weights.data_ptr()
+    S.status_word = _ptr(status)
+    S.stream = torch.cuda.current_stream(dev).cuda_stream
+    with _on(dev):
+        rc = lib.atlas_kv_select(weights.data_ptr(), seq_lens.data_ptr(), Hkv, ctypes.byref(S))
+    if rc != 0:
+        raise AtlasError(rc, status_string(rc))
+    return kept, new_lens, kept_weights
+
+
+def kv_compact(k_pages, v_pages, page_table, kept, new_lens, *, new_page_table=None, status=None):
+    """Move the kept rows of both pools together (atlas_kv_compact): into the sequences'
+    own pages (new_page_table None; kept ascending, pages not shared), or into the fresh
+    pages of new_page_table [B][new_max_pages].  The pools are updated in place."""
+    lib = load_library()
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("pools must be [num_pages][Hkv][P][D]")
+    num_pages, Hkv, P, D = k_pages.shape
+    _check(k_pages, k_pages=(k_pages, k_pages.dtype), v_pages=(v_pages, k_pages.dtype),
+           page_table=(page_table, torch.int32), kept=(kept, torch.int32),
+           new_lens=(new_lens, torch.int32), new_page_table=(new_page_table, torch.int32),
+           status=(status, torch.int32))
+    if page_table.dim() != 2 or kept.dim() != 3 or \
+            kept.shape[:2] != (page_table.shape[0], Hkv) or \
+            new_lens.numel() != page_table.shape[0] or (new_page_table is not None and (
+                new_page_table.dim() != 2 or new_page_table.shape[0] != page_table.shape[0])):
+        raise ValueError("page tables must be [B][max_pages], kept [B][Hkv][max_kept], new_lens [B]")
+    C = _Compact()
+    C.batch, C.max_pages_per_seq = page_table.shape
+    C.num_pages, C.max_kept, C.kv_dtype = num_pages, kept.shape[2], _DTYPES.get(k_pages.dtype, -1)
+    if new_page_table is not None:
+        C.new_page_table, C.new_max_pages = new_page_table.data_ptr(), new_page_table.shape[1]
+    C.status_word = _ptr(status)
+    C.stream = torch.cuda.current_stream(k_pages.device).cuda_stream
+    with _on(k_pages.device):
+        rc = lib.atlas_kv_compact(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                                  kept.data_ptr(), new_lens.data_ptr(), Hkv, D, P, ctypes.byref(C))
+    if rc != 0:
+        raise AtlasError(rc, status_string(rc))
 
 
 class EventTimer:

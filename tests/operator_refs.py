@@ -55,3 +55,52 @@ def turned(x, angles, interleaved):
     y[..., a] = x[..., a] * np.cos(angles) - x[..., b] * np.sin(angles)
     y[..., b] = x[..., b] * np.cos(angles) + x[..., a] * np.sin(angles)
     return y
+
+
+def key_weights(q, k, lens, lse, scale, q_lens=None, window=0, softcap=0.0):
+    """What atlas_kv_weights adds: [B][Hkv][T] in fp64, 0 for keys nobody sees."""
+    B, Hq, n, D = q.shape
+    Hkv, T = k.shape[1:3]
+    w = np.zeros((B, Hkv, T))
+    for b in range(B):
+        rows = n if q_lens is None else q_lens[b]
+        for h in range(Hq):
+            for i in range(rows):
+                if lse[b, h, i] == -math.inf:
+                    continue
+                end = lens[b] - rows + i + 1
+                start = max(0, end - window) if window else 0
+                g = h // (Hq // Hkv)
+                s = scale * (k[b, g, start:end] @ q[b, h, i])
+                if softcap:
+                    s = softcap * np.tanh(s / softcap)
+                w[b, g, start:end] += np.exp(s - lse[b, h, i])
+    return w
+
+
+def row_lse(q, k, lens, scale, q_lens=None, window=0, softcap=0.0):
+    """The log-sum-exp of each causal row, fp64; rows >= q_lens[b] NaN."""
+    B, Hq, n, D = q.shape
+    lse = np.full((B, Hq, n), np.nan)
+    for b in range(B):
+        rows = n if q_lens is None else q_lens[b]
+        for h in range(Hq):
+            for i in range(rows):
+                end = lens[b] - rows + i + 1
+                start = max(0, end - window) if window else 0
+                s = scale * (k[b, h * k.shape[1] // Hq, start:end] @ q[b, h, i])
+                if softcap:
+                    s = softcap * np.tanh(s / softcap)
+                lse[b, h, i] = s.max() + math.log(np.exp(s - s.max()).sum())
+    return lse
+
+
+def keys_to_keep(w, L, budget, first, recent):
+    """Indices that stay of one row of totals, by the rule of atlas_kv_select."""
+    if L <= budget:
+        return list(range(L))
+    must = [t for t in range(L) if t < first or t >= L - recent]
+    rest = [t for t in range(first, L - recent)]
+    value = [-math.inf if math.isnan(w[t]) else w[t] for t in range(L)]
+    rest.sort(key=lambda t: (-value[t], t))
+    return sorted(must + rest[: budget - len(must)])
