@@ -229,13 +229,8 @@ atlas_status make_plan(atlas_kind kind, int32_t Hq, int32_t Hkv, int32_t D, int3
     return ATLAS_OK;
 }
 
-namespace {
-
-// 2-D view of a bf16 (or fp32) tensor with D elements per row: `rows` rows; boxes
-// of one 128-byte row slab (64 bf16 or 32 fp32 elements) x box_rows rows with
-// 128-byte swizzling.
 atlas_status encode_rows_map(CUtensorMap *map, const void *base, int64_t rows, int32_t D,
-                             int32_t box_rows, bool f32 = false) {
+                             int32_t box_rows, bool f32) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return ATLAS_ERR_CUDA;
     const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
@@ -248,6 +243,8 @@ atlas_status encode_rows_map(CUtensorMap *map, const void *base, int64_t rows, i
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
+
+namespace {
 
 // View of a page pool (rows = num_pages*Hkv*P, D bf16 per row, 128-byte swizzle)
 // for the split kernel.  Pages of fewer than 64 tokens: a 3-D view [D/64 slabs]

@@ -139,6 +139,12 @@ cudaError_t launch_fmha_tc(const TcParams &p, const CUtensorMap &tmQ, const CUte
 cudaError_t launch_fmha_tc_f32(const TcParams &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,
                                const CUtensorMap &tmV, cudaStream_t stream);
 
+// TMA view of a bf16 (or fp32) tensor with D elements per row: `rows` rows; boxes of
+// one 128-byte row slab (64 bf16 or 32 fp32 elements) x box_rows rows with 128-byte
+// swizzling.
+atlas_status encode_rows_map(CUtensorMap *map, const void *base, int64_t rows, int32_t D,
+                             int32_t box_rows, bool f32 = false);
+
 // Columns handled by one CTA of the bf16 split kernel.
 int split_bf16_cols_per_cta(int G, int q_len);
 

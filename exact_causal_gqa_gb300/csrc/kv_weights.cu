@@ -5,53 +5,27 @@
 // lse2 the row's log-sum-exp that the attention call returned, both in log2 units.  No
 // softmax state is needed -- lse normalises every row -- and K is read once.
 //
-// weights_ffma_kernel: a CTA owns 128 keys of one (sequence, kv head), held in shared
-// memory as fp32, and walks the columns in tiles of NC.  A thread forms 4 keys x NC / 8
+// bf16 runs on the tensor cores (kv_weights_tc.cu); this file has the entry point and
+// fp32.  weights_ffma_kernel: a CTA owns 128 keys of one (sequence, kv head), held in shared
+// memory, and walks the columns in tiles of NC.  A thread forms 4 keys x NC / 8
 // columns of scores as whole dot products, exponentiates them and keeps one sum per key;
 // the 8 lanes that share a key add up at the end.
-#include "internal.h"
-#include "ptx.cuh"
-
-#include "atlas_evict.h"
-
-#include <math.h>
+#include "kv_weights.cuh"
 
 namespace atlas {
 namespace {
 
-struct WeightsParams {
-    const void *q, *k_pages;
-    const int32_t *page_table, *seq_lens, *q_lens;
-    const float *lse;
-    float *weights;
-    int32_t B, Hq, Hkv, G, P, q_len, max_pages, num_pages, row_tokens;
-    int32_t accumulate, window;
-    float scale_log2, softcap_log2, softcap_inv;
-    uint32_t *status;
-};
-
-__device__ __forceinline__ void record(uint32_t *status, uint32_t bit) {
-    if (status) atomicOr(status, bit);
-}
-
-__device__ __forceinline__ bool bad_lens(const WeightsParams &p, int L, int qn) {
-    return qn < 0 || qn > p.q_len || L < qn || L > p.max_pages * p.P || L > p.row_tokens;
-}
-
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
-
 constexpr int kKeys = 128;  // keys of a CTA
 
-template <typename T, int D, int NC>
+template <int D, int NC>
 struct FfmaLayout {
     static constexpr int KS = D + 4;  // padded row stride (floats): conflict-free 16-byte reads
     static constexpr int kBytes = (kKeys + NC) * KS * 4;
 };
 
-template <typename T, int D, int NC>
+template <int D, int NC>
 __global__ void __launch_bounds__(256) weights_ffma_kernel(const WeightsParams p) {
-    using Lay = FfmaLayout<T, D, NC>;
+    using Lay = FfmaLayout<D, NC>;
     constexpr int KS = Lay::KS, CPT = NC / 8;  // columns per thread
     extern __shared__ __align__(16) float smem_f[];
     __shared__ float col_lse[NC];
@@ -67,29 +41,21 @@ __global__ void __launch_bounds__(256) weights_ffma_kernel(const WeightsParams p
     if (kb >= L) return;
     const int lp = 31 - __clz(p.P);
     const int nkeys = min(kKeys, L - kb);
-    bool bad = false;
-    for (int pg = (kb >> lp) + (int)threadIdx.x; pg <= (kb + nkeys - 1) >> lp; pg += 256) {
-        const int id = p.page_table[(int64_t)b * p.max_pages + pg];
-        bad |= id < 0 || id >= p.num_pages;
-    }
-    if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) record(p.status, ATLAS_DEV_BAD_PAGE);
-        return;
-    }
-    // K block: V elements of 16 bytes each per load, keys past the end zero
-    constexpr int V = 16 / sizeof(T);
-    for (int i = threadIdx.x; i < kKeys * (D / V); i += 256) {
-        const int r = i / (D / V), d = i % (D / V) * V;
-        T x[V];
+    // the K block; keys past the end or on a bad page stay zero
+    for (int i = threadIdx.x; i < kKeys * (D / 4); i += 256) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < nkeys) {
             const int t = kb + r;
-            const int64_t page = p.page_table[(int64_t)b * p.max_pages + (t >> lp)];
-            const int64_t row = (page * p.Hkv + hkv) * p.P + (t & (p.P - 1));
-            *reinterpret_cast<uint4 *>(x) =
-                *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k_pages) + row * D + d);
+            const int page = p.page_table[(int64_t)b * p.max_pages + (t >> lp)];
+            if (page >= 0 && page < p.num_pages) {
+                const int64_t row = ((int64_t)page * p.Hkv + hkv) * p.P + (t & (p.P - 1));
+                x = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.k_pages) + row * D + d);
+            } else if (d == 0) {
+                record(p.status, ATLAS_DEV_BAD_PAGE);
+            }
         }
-#pragma unroll
-        for (int e = 0; e < V; ++e) sK[r * KS + d + e] = r < nkeys ? widen(x[e]) : 0.f;
+        *reinterpret_cast<float4 *>(sK + r * KS + d) = x;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int cg = lane & 7, kg = warp * 4 + (lane >> 3);  // keys kg + 32 r, columns cg + 8 c
@@ -101,24 +67,19 @@ __global__ void __launch_bounds__(256) weights_ffma_kernel(const WeightsParams p
         if (threadIdx.x < NC) {
             const int f = c0 + (int)threadIdx.x;
             const int i = f % p.q_len;
-            float lse = -INFINITY;
-            if (f < ncols && i < qn) lse = p.lse[row0 + f];
-            const bool real = lse != -INFINITY;  // a row that saw nothing adds nothing
+            const bool real = f < ncols && i < qn;
             const int visible = L - qn + i + 1;
-            col_lse[threadIdx.x] = lse * kLog2e;
+            col_lse[threadIdx.x] = real ? lse_log2(p.lse[row0 + f]) : INFINITY;
             col_lim[threadIdx.x] = real ? visible : 0;
             col_lo[threadIdx.x] = p.window > 0 ? max(0, visible - p.window) : 0;
         }
-        for (int i = threadIdx.x; i < NC * (D / V); i += 256) {
-            const int r = i / (D / V), d = i % (D / V) * V;
+        for (int i = threadIdx.x; i < NC * (D / 4); i += 256) {
+            const int r = i / (D / 4), d = i % (D / 4) * 4;
             const int f = c0 + r;
-            const bool in = f < ncols && f % p.q_len < qn;
-            T x[V];
-            if (in)
-                *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>(
-                    static_cast<const T *>(p.q) + (row0 + f) * D + d);
-#pragma unroll
-            for (int e = 0; e < V; ++e) sQ[r * KS + d + e] = in ? widen(x[e]) : 0.f;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (f < ncols && f % p.q_len < qn)
+                x = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + (row0 + f) * D + d);
+            *reinterpret_cast<float4 *>(sQ + r * KS + d) = x;
         }
         __syncthreads();
         float s[4][CPT];
@@ -151,10 +112,7 @@ __global__ void __launch_bounds__(256) weights_ffma_kernel(const WeightsParams p
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int t = kb + kg + 32 * r;
-                const float s2 = p.softcap_log2 > 0.f
-                                     ? p.softcap_log2 * tanh_acc(s[r][c] * p.softcap_inv)
-                                     : s[r][c] * p.scale_log2;
-                sum[r] += t < lim && t >= lo ? ex2(s2 - lse2) : 0.f;
+                sum[r] += t < lim && t >= lo ? ex2(score_log2(p, s[r][c]) - lse2) : 0.f;
             }
         }
     }
@@ -164,17 +122,17 @@ __global__ void __launch_bounds__(256) weights_ffma_kernel(const WeightsParams p
         sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
         sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 4);
         const int t = kb + kg + 32 * r;
-        if (cg == 0 && t < L) {
+        if (cg == 0 && t < L && page_ok(p, b, t, lp)) {
             float *w = p.weights + ((int64_t)b * p.Hkv + hkv) * p.row_tokens + t;
             *w = (p.accumulate ? *w : 0.f) + sum[r];
         }
     }
 }
 
-template <typename T, int D, int NC>
+template <int D, int NC>
 cudaError_t launch_ffma(const WeightsParams &p, cudaStream_t stream) {
-    using Lay = FfmaLayout<T, D, NC>;
-    auto kern = weights_ffma_kernel<T, D, NC>;
+    using Lay = FfmaLayout<D, NC>;
+    auto kern = weights_ffma_kernel<D, NC>;
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -207,6 +165,13 @@ atlas_status check(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const atlas_we
     return ATLAS_OK;
 }
 
+// fp32 has no plan to make: one CTA per 128 keys, no workspace.
+WeightsPlan plan_of(int32_t Hq, int32_t Hkv, int32_t P, const atlas_weights *W) {
+    if (W->dtype == ATLAS_F32) return WeightsPlan{};
+    return weights_tc_plan(W->batch, Hkv, Hq / Hkv, W->q_len, (int64_t)W->max_pages_per_seq * P,
+                           W->sm_count > 0 ? W->sm_count : device_sm_count());
+}
+
 }  // namespace
 }  // namespace atlas
 
@@ -215,7 +180,7 @@ extern "C" {
 size_t atlas_kv_weights_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                                        int32_t page_tokens, const atlas_weights *W) {
     if (atlas::check(n_q_heads, n_kv_heads, head_dim, page_tokens, W) != ATLAS_OK) return SIZE_MAX;
-    return 0;
+    return atlas::plan_of(n_q_heads, n_kv_heads, page_tokens, W).ws_bytes;
 }
 
 atlas_status atlas_kv_weights(const void *q, const void *k_pages, const int32_t *page_table,
@@ -232,6 +197,9 @@ atlas_status atlas_kv_weights(const void *q, const void *k_pages, const int32_t 
     if (!(fabsf(scale) < INFINITY)) return ATLAS_ERR_INVALID_ARG;
     const atlas_status st = check(n_q_heads, n_kv_heads, head_dim, page_tokens, W);
     if (st != ATLAS_OK) return st;
+    const WeightsPlan plan = plan_of(n_q_heads, n_kv_heads, page_tokens, W);
+    if (plan.ws_bytes > 0 && (!W->workspace || W->workspace_bytes < plan.ws_bytes))
+        return ATLAS_ERR_WORKSPACE;
     WeightsParams p{};
     p.q = q;
     p.k_pages = k_pages;
@@ -250,22 +218,27 @@ atlas_status atlas_kv_weights(const void *q, const void *k_pages, const int32_t 
     p.num_pages = W->num_pages;
     p.row_tokens = W->row_tokens;
     p.accumulate = W->accumulate;
-    p.window = W->window;
+    p.window = W->window < (1 << 30) ? W->window : 1 << 30;  // key + window fits 32 bits
     p.scale_log2 = scale * kLog2e;
     p.softcap_log2 = W->softcap > 0.f ? W->softcap * kLog2e : 0.f;
     p.softcap_inv = W->softcap > 0.f ? scale / W->softcap : 0.f;
     p.status = W->status_word;
     const cudaStream_t stream = static_cast<cudaStream_t>(W->stream);
     (void)cudaGetLastError();
-    const bool few = (int64_t)p.G * p.q_len <= 8;
     cudaError_t err;
     if (W->dtype == ATLAS_BF16) {
-        using T = __nv_bfloat16;
-        err = head_dim == 128 ? (few ? launch_ffma<T, 128, 8>(p, stream) : launch_ffma<T, 128, 32>(p, stream))
-                              : (few ? launch_ffma<T, 64, 8>(p, stream) : launch_ffma<T, 64, 32>(p, stream));
+        p.parts = static_cast<float *>(W->workspace);
+        p.n_parts = plan.parts;
+        p.tiles_per_part = plan.tiles_per_part;
+        CUtensorMap tmQ, tmK;
+        if (encode_rows_map(&tmQ, q, (int64_t)p.B * p.Hq * p.q_len, head_dim, 128) != ATLAS_OK ||
+            encode_rows_map(&tmK, k_pages, (int64_t)p.num_pages * p.Hkv * p.P, head_dim, p.P) != ATLAS_OK)
+            return ATLAS_ERR_CUDA;
+        err = launch_weights_tc(p, plan, head_dim, tmQ, tmK, stream);
     } else {
-        err = head_dim == 128 ? (few ? launch_ffma<float, 128, 8>(p, stream) : launch_ffma<float, 128, 32>(p, stream))
-                              : (few ? launch_ffma<float, 64, 8>(p, stream) : launch_ffma<float, 64, 32>(p, stream));
+        const bool few = (int64_t)p.G * p.q_len <= 8;
+        err = head_dim == 128 ? (few ? launch_ffma<128, 8>(p, stream) : launch_ffma<128, 32>(p, stream))
+                              : (few ? launch_ffma<64, 8>(p, stream) : launch_ffma<64, 32>(p, stream));
     }
     return err == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }

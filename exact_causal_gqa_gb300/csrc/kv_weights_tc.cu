@@ -1,0 +1,711 @@
+// kv_weights_tc.cu -- attention weights per cached key (kv_weights.cuh) for bf16 q and K
+// on the 5th-generation tensor cores.
+//
+// The keys go on M: S^T[128 keys x N columns] = K . Q^T lands in tensor memory with one
+// key per lane, so the sum over columns that the operator wants runs along the lane's
+// TMEM columns: each epilogue thread owns one key, reads its scores, exponentiates
+// (2^(s scale log2 e - lse log2 e): one packed FMA and one MUFU exponential per score) and
+// adds in a register.  No shuffles, no atomics, no second pass; the order of a key's sum
+// depends only on the call's sizes.
+//
+// weights_stream_kernel, at most 256 columns (decode, observer rows): the columns stay in
+//   shared memory, packed so that only real rows take part, and a CTA streams the 128-key
+//   tiles of its share of the context past them.  Bound by K's bytes.
+// weights_tile_kernel, more columns (a prompt's rows): a CTA keeps 512 keys (four tiles)
+//   and streams 128-row query tiles past them, each loaded once for four products; query
+//   tiles no key of the CTA is visible to are not loaded.  Bound by the exponentials and
+//   the tensor core.  When (sequence, kv head) x 512-key groups alone would not fill the
+//   GPU, the query tiles are split between CTAs; their sums per key go to the workspace
+//   and weights_join_kernel adds them in order.
+//
+// Keys on a bad page, or behind the end, only fill lanes of their own, whose results are
+// dropped.  Every mbarrier wait is bounded; a CTA that gives up records
+// ATLAS_DEV_TIMEOUT, lets its copies and MMAs finish, frees TMEM and writes NaN.
+#include "kv_weights.cuh"
+
+namespace atlas {
+namespace {
+
+constexpr int BT = 128;           // keys per tile
+constexpr int kSlab = 128 * 128;  // one 64-element slab of a 128-row bf16 tile
+
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, kWaitLimitNs));
+}
+
+// One tile of 128 keys from kb (keys below `end`) into shared memory, page by page; the
+// whole warp calls it.  Boxes of bad pages are left out (`bar` counts the others' bytes).
+template <int D>
+__device__ __forceinline__ void load_keys(const WeightsParams &p, const CUtensorMap &tmK,
+                                          PageIdCache &pages, int hkv, int kb, int end, int lp,
+                                          uint32_t dst, uint32_t bar, uint64_t policy) {
+    const int lane = threadIdx.x & 31;
+    const int nbox = (min(BT, end - kb) + p.P - 1) >> lp;  // <= 16
+    const int id = pages.get_line(kb >> lp, lane < nbox ? lane : 0);
+    const bool good = lane < nbox && id >= 0 && id < p.num_pages;
+    const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, good));
+    if (lane == 0) mbar_arrive_expect_tx(bar, (boxes << lp) * 128u * (D / 64));
+    __syncwarp();
+    if (good) {
+        const int y = (id * p.Hkv + hkv) << lp;
+#pragma unroll
+        for (int sl = 0; sl < D / 64; ++sl)
+            tma_load_2d_hint(dst + sl * kSlab + (lane << lp) * 128, &tmK, 64 * sl, y, bar, policy);
+    }
+    __syncwarp();
+}
+
+// S^T[128 x n] of one key tile and a query tile of n rows (K-major, 128-byte swizzle;
+// its 64-element slabs q_slab bytes apart).
+template <int D>
+__device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t k_smem, uint32_t q_smem,
+                                             uint32_t q_slab, uint32_t idesc) {
+    const uint64_t kd = sdesc_sw128(k_smem, 16, 1024), qd = sdesc_sw128(q_smem, 16, 1024);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+        umma_bf16(d_tmem, kd + (((kk >> 2) * kSlab + (kk & 3) * 32) >> 4),
+                  qd + (((kk >> 2) * q_slab + (kk & 3) * 32) >> 4), idesc, kk > 0);
+}
+
+// Adds 2^(s2 - lse2[c]) of NC columns of scores; with `masked`, of those columns c that
+// key t is visible to (t < lim[c], and t >= lim[c] - window with a window).
+template <int NC>
+__device__ __forceinline__ void add_weights(const WeightsParams &p, const uint32_t (&s)[NC],
+                                            const float *lse2, const int *lim, int t, bool masked,
+                                            float2 (&sum)[2]) {
+    const float2 sc = make_float2(p.scale_log2, p.scale_log2);
+    const bool capped = p.softcap_log2 > 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; c += 4) {
+        const float4 l4 = *reinterpret_cast<const float4 *>(lse2 + c);
+        float2 a = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        float2 b = make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+        if (capped) {
+            a = make_float2(score_log2(p, a.x) - l4.x, score_log2(p, a.y) - l4.y);
+            b = make_float2(score_log2(p, b.x) - l4.z, score_log2(p, b.y) - l4.w);
+        } else {
+            a = ffma2(a, sc, make_float2(-l4.x, -l4.y));
+            b = ffma2(b, sc, make_float2(-l4.z, -l4.w));
+        }
+        if (masked) {
+            const int4 m = *reinterpret_cast<const int4 *>(lim + c);
+            const int far = p.window > 0 ? t + p.window : INT32_MAX;
+            a.x = t < m.x && m.x <= far ? a.x : -INFINITY;
+            a.y = t < m.y && m.y <= far ? a.y : -INFINITY;
+            b.x = t < m.z && m.z <= far ? b.x : -INFINITY;
+            b.y = t < m.w && m.w <= far ? b.y : -INFINITY;
+        }
+        sum[0] = fadd2(sum[0], make_float2(ex2(a.x), ex2(a.y)));
+        sum[1] = fadd2(sum[1], make_float2(ex2(b.x), ex2(b.y)));
+    }
+}
+
+// ---------------------------------------------------------------- few columns
+template <int D, int N>
+struct StreamCfg {
+    static constexpr int kTile = BT * D * 2;
+    static constexpr int kQ = N * D * 2;
+    // Up to 32 columns two CTAs share an SM (one's start-up hides behind the other);
+    // beyond, the accumulators and queries leave room for one with a deeper ring.
+    static constexpr int kCtas = N <= 32 ? 2 : 1;
+    static constexpr int kStages = (N <= 32 ? 3 : N <= 128 ? 5 : 4) * (128 / D);
+    static constexpr int kGroups = N >= 128 ? 2 : 1;  // epilogue warpgroups (alternate tiles)
+    static constexpr int kThreads = 128 + 128 * kGroups;
+    static constexpr uint32_t kCols = 2 * N < 32 ? 32 : 2 * N;  // TMEM: two score buffers
+    static constexpr int OFF_Q = kStages * kTile;
+    static constexpr int OFF_LSE = OFF_Q + kQ;
+    static constexpr int OFF_LIM = OFF_LSE + N * 4;
+    static constexpr int OFF_BAR = OFF_LIM + N * 4;
+    static constexpr int B_FULL = 0, B_EMPTY = kStages, B_SFULL = 2 * kStages,
+                         B_SEMPTY = B_SFULL + 2, B_FINAL = B_SEMPTY + 2, kBars = B_FINAL + 1;
+    static constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
+    static constexpr int kSmem = OFF_TMEM + 16 + 1024;
+    static_assert(kCtas * (kSmem + 1024) <= 233472, "shared memory of an SM");
+};
+
+// grid (chunks of the context, Hkv, B)
+template <int D, int N>
+__global__ void __launch_bounds__(StreamCfg<D, N>::kThreads, StreamCfg<D, N>::kCtas)
+    weights_stream_kernel(const __grid_constant__ CUtensorMap tmK, const WeightsParams p,
+                          const int chunk) {
+    using C = StreamCfg<D, N>;
+    constexpr int S = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    float *lse2 = reinterpret_cast<float *>(smem + C::OFF_LSE);
+    int *lim = reinterpret_cast<int *>(smem + C::OFF_LIM);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_TMEM + 8);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.z, hkv = blockIdx.y;
+#define BAR(i) (sb + C::OFF_BAR + 8u * (uint32_t)(i))
+    const int L = p.seq_lens[b];
+    const int qn = p.q_lens ? p.q_lens[b] : p.q_len;
+    if (bad_lens(p, L, qn)) {
+        if (threadIdx.x == 0 && blockIdx.x == 0) record(p.status, ATLAS_DEV_BAD_SEQLEN);
+        return;
+    }
+    const int lp = 31 - __clz(p.P);
+    const int first = (int)blockIdx.x * chunk, end = min(L, first + chunk);
+    if (first >= end) return;
+    float *w = p.weights + ((int64_t)b * p.Hkv + hkv) * p.row_tokens;
+    // Keys below every row's window (or all of them, without rows) get nothing.
+    const int seen = qn == 0 ? end : p.window > 0 ? min(end, max(first, L - qn + 1 - p.window)) : first;
+    const int begin = qn == 0 ? end : seen / BT * BT < first ? first : seen / BT * BT;
+    for (int pg = (first >> lp) + (int)threadIdx.x; pg <= (end - 1) >> lp; pg += blockDim.x) {
+        const int id = p.page_table[(int64_t)b * p.max_pages + pg];
+        if (id < 0 || id >= p.num_pages) record(p.status, ATLAS_DEV_BAD_PAGE);
+    }
+    if (!p.accumulate)
+        for (int t = first + (int)threadIdx.x; t < begin; t += blockDim.x)
+            if (page_ok(p, b, t, lp)) w[t] = 0.f;
+    if (begin >= end) return;
+    const int tiles = (end - begin + BT - 1) / BT;
+    const int ncols = p.G * qn;                  // packed: column c is row c % qn of head c / qn
+    constexpr int kStep = N == 16 ? 16 : 32;     // columns of one TMEM load
+    const int nmma = (ncols + kStep - 1) / kStep * kStep;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(BAR(C::B_FULL + s), 1);
+            mbar_init(BAR(C::B_EMPTY + s), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(BAR(C::B_SFULL + s), 1);
+            mbar_init(BAR(C::B_SEMPTY + s), 128);
+        }
+        mbar_init(BAR(C::B_FINAL), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::kCols);
+    // The columns: rows packed and zero-filled to the product's N, their lse and limits.
+    const int64_t row0 = ((int64_t)b * p.Hq + (int64_t)hkv * p.G) * p.q_len;
+    for (int i = threadIdx.x; i < nmma * (D / 8); i += C::kThreads) {
+        const int c = i / (D / 8), ch = i % (D / 8);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (c < ncols)
+            v = *reinterpret_cast<const uint4 *>(
+                static_cast<const __nv_bfloat16 *>(p.q) +
+                (row0 + (int64_t)(c / qn) * p.q_len + c % qn) * D + ch * 8);
+        st_shared_v4(sb + C::OFF_Q + (ch / 8) * (N * 128) + sw128(c, ch % 8), v.x, v.y, v.z, v.w);
+    }
+    for (int c = threadIdx.x; c < N; c += C::kThreads) {
+        const bool real = c < ncols;
+        const int i = real ? c % qn : 0;
+        lse2[c] = real ? lse_log2(p.lse[row0 + (int64_t)(c / qn) * p.q_len + i]) : INFINITY;
+        lim[c] = real ? L - qn + i + 1 : 0;
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool failed = false;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) prefetch_tmap(&tmK);
+        const uint64_t policy = policy_evict_first();
+        PageIdCache pages{p.page_table + (int64_t)b * p.max_pages, (end - 1) >> lp};
+        int issued = 0;
+        for (int j = 0; j < tiles; ++j) {
+            const int s = j % S;
+            if (j >= S && !wait_warp(BAR(C::B_EMPTY + s), ((j / S) - 1) & 1, abort_flag)) {
+                failed = true;
+                break;
+            }
+            load_keys<D>(p, tmK, pages, hkv, begin + j * BT, end, lp, sb + s * C::kTile,
+                         BAR(C::B_FULL + s), policy);
+            issued = j + 1;
+        }
+        if (failed && lane == 0) {
+            *abort_flag = 1;
+            int no_abort = 0;  // the copies in flight land before the CTA leaves
+            for (int j = max(0, issued - S); j < issued; ++j)
+                mbar_wait_bounded(BAR(C::B_FULL + j % S), (j / S) & 1, &no_abort, kWaitLimitNs);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16_f32(128, nmma, false);
+            bool ok = true;
+            for (int j = 0; ok && j < tiles; ++j) {
+                const int s = j % S, buf = j & 1;
+                ok = mbar_wait_bounded(BAR(C::B_FULL + s), (j / S) & 1, abort_flag, kWaitLimitNs) &&
+                     (j < 2 || mbar_wait_bounded(BAR(C::B_SEMPTY + buf), ((j >> 1) - 1) & 1,
+                                                 abort_flag, kWaitLimitNs));
+                if (!ok) break;
+                tc_fence_after();
+                issue_scores<D>(tmem + buf * N, sb + s * C::kTile, sb + C::OFF_Q, N * 128, idesc);
+                umma_commit(BAR(C::B_EMPTY + s));
+                umma_commit(BAR(C::B_SFULL + buf));
+            }
+            if (!ok) {
+                failed = true;
+                *abort_flag = 1;
+            }
+            umma_commit(BAR(C::B_FINAL));  // every MMA is done before TMEM is released
+            int no_abort = 0;
+            mbar_wait_bounded(BAR(C::B_FINAL), 0, &no_abort, kWaitLimitNs);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ epilogue
+        const int group = (warp - 4) / 4, q4 = warp % 4;
+        const int r = q4 * 32 + lane;
+        for (int j = group; j < tiles; j += C::kGroups) {
+            const int buf = j & 1;
+            const int kb = begin + j * BT, t = kb + r;
+            const bool mine = t < end && page_ok(p, b, t, lp);
+            const float old = mine && p.accumulate ? w[t] : 0.f;
+            // a tile that every row sees whole needs no limits
+            const bool masked = kb + BT > L - qn + 1 || (p.window > 0 && kb < L - p.window);
+            if (!wait_warp(BAR(C::B_SFULL + buf), (j >> 1) & 1, abort_flag)) {
+                failed = true;
+                *abort_flag = 1;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t ts = tmem + buf * N + ((uint32_t)(q4 * 32) << 16);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            if (N == 16) {
+                uint32_t s[16];
+                tmem_ld16(ts, s);
+                tmem_wait_ld();
+                tc_fence_before();
+                mbar_arrive(BAR(C::B_SEMPTY + buf));
+                // (padding columns are zero rows: 0 times a non-finite key is not 0)
+                add_weights<16>(p, s, lse2, lim, t, masked || ncols < 16, sum);
+            } else {
+#pragma unroll 1
+                for (int c0 = 0; c0 < nmma; c0 += 32) {
+                    uint32_t s[32];
+                    tmem_ld32(ts + c0, s);
+                    tmem_wait_ld32(s);
+                    add_weights<32>(p, s, lse2 + c0, lim + c0, t, masked || c0 + 32 > ncols, sum);
+                }
+                tc_fence_before();
+                mbar_arrive(BAR(C::B_SEMPTY + buf));
+            }
+            if (mine) w[t] = old + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+        }
+    }
+    tc_fence_before();
+    const bool any_failed = __syncthreads_or(failed) != 0;
+    if (any_failed) {
+        if (threadIdx.x == 0) record(p.status, ATLAS_DEV_TIMEOUT);
+        for (int t = begin + (int)threadIdx.x; t < end; t += C::kThreads)
+            if (page_ok(p, b, t, lp)) w[t] = __int_as_float(0x7fc00000);
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kCols);
+    }
+#undef BAR
+}
+
+// ---------------------------------------------------------------- many columns
+constexpr int kTiles = 4;                // key tiles of a CTA
+constexpr int kGroupKeys = kTiles * BT;  // 512
+
+template <int D>
+struct TileCfg {
+    static constexpr int kTile = BT * D * 2;  // 128 rows of K or Q
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kThreads = 128 + 128 * kTiles;
+    static constexpr int OFF_Q = kTiles * kTile;
+    static constexpr int OFF_LSE = OFF_Q + kStages * kTile;    // [kStages][128]
+    static constexpr int OFF_LIM = OFF_LSE + kStages * BT * 4;  // [kStages][128]
+    static constexpr int OFF_BAR = OFF_LIM + kStages * BT * 4;
+    static constexpr int B_K = 0;
+    static constexpr int B_QFULL = B_K + kTiles;
+    static constexpr int B_QEMPTY = B_QFULL + kStages;
+    static constexpr int B_CFULL = B_QEMPTY + kStages;   // the tile's lse and limits
+    static constexpr int B_CEMPTY = B_CFULL + kStages;   // one arrival per epilogue warp
+    static constexpr int B_SFULL = B_CEMPTY + kStages;
+    static constexpr int B_SEMPTY = B_SFULL + kTiles;
+    static constexpr int B_FINAL = B_SEMPTY + kTiles;
+    static constexpr int kBars = B_FINAL + 1;
+    static constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
+    static constexpr int kSmem = OFF_TMEM + 16 + 1024;
+    static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+// The query tiles first .. end - 1 of a (sequence, kv head) that have a row which sees a
+// key of [kb, kb + kGroupKeys), in order: rows 128 j .. 128 j + 127 of its G * q_len
+// (q head, row) pairs, and the keys their real rows see.  Every role of the kernel walks
+// the same list.
+struct QueryTiles {
+    const WeightsParams &p;
+    const int L, qn, kb, end;
+    int j, i;              // tile, and its first row's place in its head
+    int n = -1;            // tiles taken before this one: ring position and phase
+    bool started = false;
+    bool whole = false;    // every row is real
+    int lim_min = 0, lim_max = 0;  // keys below: seen by the earliest / latest row
+
+    __device__ __forceinline__ QueryTiles(const WeightsParams &p_, int L_, int qn_, int kb_,
+                                          int first, int end_)
+        : p(p_), L(L_), qn(qn_), kb(kb_), end(end_), j(first - 1),
+          i((int)((int64_t)first * BT % p_.q_len)) {}
+
+    // Moves on to the next tile of the list; false at its end.
+    __device__ __forceinline__ bool next() {
+        for (;;) {
+            if (++j >= end) return false;
+            if (started) {
+                i += BT;
+                if (i >= p.q_len) i = p.q_len >= BT ? i - p.q_len : i % p.q_len;
+            }
+            started = true;
+            const int count = min(BT, p.G * p.q_len - j * BT);
+            const bool spans = i + count > p.q_len;
+            const int i0 = spans ? 0 : i;
+            const int i1 = min(spans ? p.q_len : i + count, qn) - 1;
+            if (i0 >= qn) continue;  // padding rows only
+            whole = count == BT && (qn == p.q_len || (!spans && i + count <= qn));
+            lim_min = L - qn + i0 + 1;
+            lim_max = L - qn + i1 + 1;
+            if (!seen(kb, kGroupKeys)) continue;
+            ++n;
+            return true;
+        }
+    }
+    // Whether a row of the tile sees a key of [k0, k0 + keys).
+    __device__ __forceinline__ bool seen(int k0, int keys) const {
+        return k0 < lim_max && (p.window == 0 || k0 + keys > lim_min - p.window);
+    }
+};
+
+// grid: items, the key groups of every (sequence, kv head) in ascending order (under a
+// causal mask the first groups have the most rows), the parts of one group together.
+template <int D>
+__global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
+    weights_tile_kernel(const __grid_constant__ CUtensorMap tmQ,
+                        const __grid_constant__ CUtensorMap tmK, const WeightsParams p) {
+    using C = TileCfg<D>;
+    constexpr int S = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_TMEM + 8);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#define BAR(i) (sb + C::OFF_BAR + 8u * (uint32_t)(i))
+    const int units = p.B * p.Hkv;
+    const int part = (int)(blockIdx.x % (unsigned)p.n_parts);
+    const int u = (int)(blockIdx.x / (unsigned)p.n_parts % (unsigned)units);
+    const int kb0 = (int)(blockIdx.x / (unsigned)p.n_parts / (unsigned)units) * kGroupKeys;
+    const int b = u / p.Hkv, hkv = u % p.Hkv;
+    const int L = p.seq_lens[b];
+    const int qn = p.q_lens ? p.q_lens[b] : p.q_len;
+    if (bad_lens(p, L, qn)) {
+        if (threadIdx.x == 0 && kb0 == 0 && part == 0) record(p.status, ATLAS_DEV_BAD_SEQLEN);
+        return;
+    }
+    if (kb0 >= L) return;
+    const int lp = 31 - __clz(p.P);
+    const int end = min(L, kb0 + kGroupKeys);
+    for (int pg = (kb0 >> lp) + (int)threadIdx.x; pg <= (end - 1) >> lp; pg += blockDim.x) {
+        const int id = p.page_table[(int64_t)b * p.max_pages + pg];
+        if (id < 0 || id >= p.num_pages) record(p.status, ATLAS_DEV_BAD_PAGE);
+    }
+    const int nq = (p.G * p.q_len + BT - 1) / BT;
+    const int q_begin = part * p.tiles_per_part, q_end = min(nq, q_begin + p.tiles_per_part);
+    const int64_t row0 = ((int64_t)b * p.Hq + (int64_t)hkv * p.G) * p.q_len;
+    const int ktiles = (end - kb0 + BT - 1) / BT;
+
+    if (threadIdx.x == 0) {
+        for (int x = 0; x < kTiles; ++x) {
+            mbar_init(BAR(C::B_K + x), 1);
+            mbar_init(BAR(C::B_SFULL + x), 1);
+            mbar_init(BAR(C::B_SEMPTY + x), 128);
+        }
+        for (int s = 0; s < S; ++s) {
+            mbar_init(BAR(C::B_QFULL + s), 1);
+            mbar_init(BAR(C::B_QEMPTY + s), 1);
+            mbar_init(BAR(C::B_CFULL + s), 1);
+            mbar_init(BAR(C::B_CEMPTY + s), 4 * kTiles);
+        }
+        mbar_init(BAR(C::B_FINAL), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool failed = false;
+    QueryTiles q(p, L, qn, kb0, q_begin, q_end);
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            prefetch_tmap(&tmQ);
+            prefetch_tmap(&tmK);
+        }
+        const uint64_t keep = policy_evict_last();  // other CTAs read the same K and Q
+        PageIdCache pages{p.page_table + (int64_t)b * p.max_pages, (end - 1) >> lp};
+        int issued = 0;
+        for (int x = 0; x < ktiles; ++x)
+            load_keys<D>(p, tmK, pages, hkv, kb0 + x * BT, end, lp, sb + x * C::kTile,
+                         BAR(C::B_K + x), keep);
+        while (q.next()) {
+            const int s = q.n % S;
+            if (q.n >= S && !wait_warp(BAR(C::B_QEMPTY + s), ((q.n / S) - 1) & 1, abort_flag)) {
+                failed = true;
+                break;
+            }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(BAR(C::B_QFULL + s), C::kTile);
+#pragma unroll
+                for (int sl = 0; sl < D / 64; ++sl)
+                    tma_load_2d_hint(sb + C::OFF_Q + s * C::kTile + sl * kSlab, &tmQ, 64 * sl,
+                                     (int)(row0 + q.j * BT), BAR(C::B_QFULL + s), keep);
+            }
+            issued = q.n + 1;
+        }
+        if (lane == 0) {
+            // Nothing is in flight when the CTA leaves: K tiles that no product waited for
+            // (a part without rows for them), and after an abort the queries too.
+            int no_abort = 0;
+            for (int x = 0; x < ktiles; ++x)
+                mbar_wait_bounded(BAR(C::B_K + x), 0, &no_abort, kWaitLimitNs);
+            if (failed) {
+                *abort_flag = 1;
+                for (int k = max(0, issued - S); k < issued; ++k)
+                    mbar_wait_bounded(BAR(C::B_QFULL + k % S), (k / S) & 1, &no_abort, kWaitLimitNs);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false);
+            bool ok = true;
+            int used[kTiles] = {0, 0, 0, 0};  // products so far of each key tile
+            while (ok && q.next()) {
+                const int s = q.n % S;
+                ok = mbar_wait_bounded(BAR(C::B_QFULL + s), (q.n / S) & 1, abort_flag, kWaitLimitNs);
+                if (!ok) break;
+#pragma unroll
+                for (int x = 0; x < kTiles; ++x) {
+                    if (!ok || x >= ktiles || !q.seen(kb0 + x * BT, BT)) continue;
+                    if (used[x] == 0)
+                        ok = mbar_wait_bounded(BAR(C::B_K + x), 0, abort_flag, kWaitLimitNs);
+                    else
+                        ok = mbar_wait_bounded(BAR(C::B_SEMPTY + x), (used[x] - 1) & 1, abort_flag,
+                                               kWaitLimitNs);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    issue_scores<D>(tmem + x * BT, sb + x * C::kTile, sb + C::OFF_Q + s * C::kTile,
+                                    kSlab, idesc);
+                    umma_commit(BAR(C::B_SFULL + x));
+                    ++used[x];
+                }
+                umma_commit(BAR(C::B_QEMPTY + s));
+            }
+            if (!ok) {
+                failed = true;
+                *abort_flag = 1;
+            }
+            umma_commit(BAR(C::B_FINAL));
+            int no_abort = 0;
+            mbar_wait_bounded(BAR(C::B_FINAL), 0, &no_abort, kWaitLimitNs);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ lse and limits
+        while (q.next()) {
+            const int s = q.n % S;
+            float v[4];
+            int m[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int f = q.j * BT + e * 32 + lane;
+                const int i = f % p.q_len;
+                const bool real = f < p.G * p.q_len && i < qn;
+                v[e] = real ? lse_log2(p.lse[row0 + f]) : INFINITY;
+                m[e] = real ? L - qn + i + 1 : 0;
+            }
+            if (q.n >= S && !wait_warp(BAR(C::B_CEMPTY + s), ((q.n / S) - 1) & 1, abort_flag)) {
+                failed = true;
+                break;
+            }
+            float *lse2 = reinterpret_cast<float *>(smem + C::OFF_LSE) + s * BT;
+            int *lim = reinterpret_cast<int *>(smem + C::OFF_LIM) + s * BT;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                lse2[e * 32 + lane] = v[e];
+                lim[e * 32 + lane] = m[e];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::B_CFULL + s));
+        }
+        if (failed && lane == 0) *abort_flag = 1;
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ epilogue
+        const int x = (warp - 4) / 4, q4 = warp % 4;
+        const int kb = kb0 + x * BT, t = kb + q4 * 32 + lane;
+        const uint32_t ts = tmem + x * BT + ((uint32_t)(q4 * 32) << 16);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        int used = 0;
+        while (q.next()) {
+            const int s = q.n % S;
+            // (also for a tile this warpgroup skips: it frees the slot like the others)
+            if (!wait_warp(BAR(C::B_CFULL + s), (q.n / S) & 1, abort_flag)) {
+                failed = true;
+                break;
+            }
+            if (x < ktiles && q.seen(kb, BT)) {
+                if (!wait_warp(BAR(C::B_SFULL + x), used & 1, abort_flag)) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after();
+                const bool masked = !q.whole || kb + BT > q.lim_min ||
+                                    (p.window > 0 && kb < q.lim_max - p.window);
+                const float *lse2 = reinterpret_cast<const float *>(smem + C::OFF_LSE) + s * BT;
+                const int *lim = reinterpret_cast<const int *>(smem + C::OFF_LIM) + s * BT;
+#pragma unroll 1
+                for (int c0 = 0; c0 < BT; c0 += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(ts + c0, v);
+                    tmem_wait_ld32(v);
+                    if (c0 == BT - 32) {  // all read: the next product may overwrite them
+                        tc_fence_before();
+                        mbar_arrive(BAR(C::B_SEMPTY + x));
+                    }
+                    add_weights<32>(p, v, lse2 + c0, lim + c0, t, masked, sum);
+                }
+                ++used;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::B_CEMPTY + s));
+        }
+        if (failed && lane == 0) *abort_flag = 1;
+        if (t < end && page_ok(p, b, t, lp)) {
+            const float total = failed ? __int_as_float(0x7fc00000)
+                                       : (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            if (p.n_parts > 1) {
+                p.parts[((int64_t)part * units + u) * ((int64_t)p.max_pages * p.P) + t] = total;
+            } else {
+                float *w = p.weights + (int64_t)u * p.row_tokens + t;
+                *w = (p.accumulate ? *w : 0.f) + total;
+            }
+        }
+    }
+    tc_fence_before();
+    const bool any_failed = __syncthreads_or(failed) != 0;
+    if (any_failed && threadIdx.x == 0) record(p.status, ATLAS_DEV_TIMEOUT);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+#undef BAR
+}
+
+// The parts' sums of each key, in order.  grid (keys / 256, Hkv, B)
+__global__ void __launch_bounds__(256) weights_join_kernel(const WeightsParams p) {
+    const int b = blockIdx.z, u = b * p.Hkv + (int)blockIdx.y;
+    const int t = (int)blockIdx.x * 256 + (int)threadIdx.x;
+    const int L = p.seq_lens[b];
+    const int qn = p.q_lens ? p.q_lens[b] : p.q_len;
+    if (bad_lens(p, L, qn) || t >= L || !page_ok(p, b, t, 31 - __clz(p.P))) return;
+    const int64_t ctx = (int64_t)p.max_pages * p.P, units = (int64_t)p.B * p.Hkv;
+    float sum = 0.f;
+    for (int k = 0; k < p.n_parts; ++k) sum += p.parts[(k * units + u) * ctx + t];
+    float *w = p.weights + (int64_t)u * p.row_tokens + t;
+    *w = (p.accumulate ? *w : 0.f) + sum;
+}
+
+cudaError_t configure(const void *kern, int bytes, int (&done)[64]) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 64 && done[dev]) return cudaSuccess;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess && dev < 64) done[dev] = 1;
+    return err;
+}
+
+template <int D, int N>
+cudaError_t launch_stream(const WeightsParams &p, int chunk_tiles, const CUtensorMap &tmK,
+                          cudaStream_t stream) {
+    using C = StreamCfg<D, N>;
+    static int done[64] = {0};
+    auto kern = weights_stream_kernel<D, N>;
+    const cudaError_t err = configure(reinterpret_cast<const void *>(kern), C::kSmem, done);
+    if (err != cudaSuccess) return err;
+    const int64_t ctx = (int64_t)p.max_pages * p.P, chunk = (int64_t)chunk_tiles * BT;
+    const dim3 grid((unsigned)((ctx + chunk - 1) / chunk), (unsigned)p.Hkv, (unsigned)p.B);
+    kern<<<grid, C::kThreads, C::kSmem, stream>>>(tmK, p, (int)chunk);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const WeightsParams &p, const WeightsPlan &plan, const CUtensorMap &tmQ,
+                     const CUtensorMap &tmK, cudaStream_t stream) {
+    if (plan.stream) {
+        const int cols = p.G * p.q_len;
+        return cols <= 16    ? launch_stream<D, 16>(p, plan.chunk_tiles, tmK, stream)
+               : cols <= 32  ? launch_stream<D, 32>(p, plan.chunk_tiles, tmK, stream)
+               : cols <= 64  ? launch_stream<D, 64>(p, plan.chunk_tiles, tmK, stream)
+               : cols <= 128 ? launch_stream<D, 128>(p, plan.chunk_tiles, tmK, stream)
+                             : launch_stream<D, 256>(p, plan.chunk_tiles, tmK, stream);
+    }
+    using C = TileCfg<D>;
+    static int done[64] = {0};
+    auto kern = weights_tile_kernel<D>;
+    cudaError_t err = configure(reinterpret_cast<const void *>(kern), C::kSmem, done);
+    if (err != cudaSuccess) return err;
+    const int64_t ctx = (int64_t)p.max_pages * p.P, units = (int64_t)p.B * p.Hkv;
+    const int64_t items = (ctx + kGroupKeys - 1) / kGroupKeys * units * p.n_parts;
+    if (items > INT32_MAX) return cudaErrorInvalidValue;
+    kern<<<(unsigned)items, C::kThreads, C::kSmem, stream>>>(tmQ, tmK, p);
+    err = cudaGetLastError();
+    if (err == cudaSuccess && p.n_parts > 1) {
+        weights_join_kernel<<<dim3((unsigned)((ctx + 255) / 256), (unsigned)p.Hkv, (unsigned)p.B), 256,
+                              0, stream>>>(p);
+        err = cudaGetLastError();
+    }
+    return err;
+}
+
+}  // namespace
+
+// A pure function of the call's sizes.
+WeightsPlan weights_tc_plan(int B, int Hkv, int G, int q_len, int64_t ctx, int sms) {
+    WeightsPlan plan{};
+    const int64_t units = (int64_t)B * Hkv, cols = (int64_t)G * q_len;
+    const int64_t tiles = (ctx + BT - 1) / BT;
+    if (cols <= 256) {
+        // Shares of 1 to 32 tiles (4096 keys) that give each SM about 8 CTAs at the
+        // largest context.
+        plan.stream = 1;
+        int64_t chunk = tiles * units / ((int64_t)sms * 8);
+        plan.chunk_tiles = (int)(chunk < 1 ? 1 : chunk > 32 ? 32 : chunk);
+        return plan;
+    }
+    // Query tiles split until there are about 6 items per SM, none below 8 tiles.
+    const int64_t nq = (cols + BT - 1) / BT;
+    const int64_t items = (ctx + kGroupKeys - 1) / kGroupKeys * units;
+    int64_t parts = ((int64_t)sms * 6 + items - 1) / items;
+    if (parts > (nq + 7) / 8) parts = (nq + 7) / 8;
+    plan.tiles_per_part = (int)((nq + parts - 1) / parts);
+    plan.parts = (int)((nq + plan.tiles_per_part - 1) / plan.tiles_per_part);
+    plan.ws_bytes = plan.parts > 1 ? (size_t)plan.parts * units * ctx * sizeof(float) : 0;
+    return plan;
+}
+
+cudaError_t launch_weights_tc(const WeightsParams &p, const WeightsPlan &plan, int D,
+                              const CUtensorMap &tmQ, const CUtensorMap &tmK, cudaStream_t stream) {
+    return D == 128 ? launch_d<128>(p, plan, tmQ, tmK, stream) : launch_d<64>(p, plan, tmQ, tmK, stream);
+}
+
+}  // namespace atlas

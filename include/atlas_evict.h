@@ -68,7 +68,8 @@ typedef struct {
  * and adds nothing.  Keys t >= seq_lens[b] are not touched.  A bad seq_len or q_len
  * (seq_len < rows, > max_pages_per_seq * page_tokens or > row_tokens) sets
  * ATLAS_DEV_BAD_SEQLEN and a page id outside [0, num_pages) ATLAS_DEV_BAD_PAGE; the
- * weights of that sequence (of up to 512 keys around the bad page) are left as they were.
+ * weights of that sequence (of the keys on that page) are left as they were.
+ * ATLAS_DEV_TIMEOUT leaves the keys concerned NaN.
  * Supported sizes and types are those of the attention calls.
  */
 atlas_status atlas_kv_weights(const void *q, const void *k_pages, const int32_t *page_table,

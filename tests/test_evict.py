@@ -141,7 +141,11 @@ WEIGHTS = [
     ("bf16", 8, 2, 64, 16, 128, [128, 777], dict(window=100)),
     ("bf16", 2, 1, 128, 32, 600, [600, 601], dict(ragged=[600, 333])),
     ("bf16", 2, 2, 64, 8, 300, [1100], dict(scale=-0.2)),
+    ("bf16", 8, 1, 128, 16, 25, [3000, 25, 150], dict(window=2 ** 31 - 1)),
+    ("bf16", 4, 1, 64, 32, 129, [129, 2500], dict(window=2 ** 31 - 1, ragged=[0, 128])),
+    ("bf16", 8, 2, 128, 128, 16, [1029, 17], dict(window=1)),
     ("f32", 6, 2, 64, 32, 100, [100, 333], dict(ragged=[100, 50])),
+    ("f32", 2, 2, 64, 32, 3, [100, 333], dict(window=2 ** 31 - 1, ragged=[0, 2])),
     ("f32", 4, 2, 128, 16, 65, [400], dict(window=33, softcap=4.0)),
 ]
 
