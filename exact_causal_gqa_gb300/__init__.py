@@ -311,7 +311,7 @@ def _call(kind: str, q, k_pages, v_pages, page_table, seq_lens, n_q_heads, n_kv_
     if q_lens is not None and (not q_lens.is_cuda or q_lens.dtype != torch.int32 or
                                q_lens.numel() != q.shape[0]):
         raise ValueError("q_lens must be an int32 CUDA tensor [batch]")
-    stream = torch.cuda.current_stream(q.device).cuda_stream
+    stream = _stream(q.device)
     L = _launch(q, k_pages, page_table, out_dtype, out, lse, None, status, stream,
                 split_tokens, debug_flags,
                 None if events is None else ctypes.cast(events, ctypes.c_void_p).value,
@@ -374,7 +374,7 @@ def cross(q, k_pages, v_pages, page_table, enc_lens, n_q_heads, n_kv_heads, head
           page_tokens, scale, **kw):
     """Attention of q_len decoder rows to all enc_lens[b] encoder states of their
     sequence (no causal mask; enc_lens[b] == 0 gives rows of 0 and lse -inf)."""
-    with _on(q.device):
+    with _on(_cuda_device("q", q)):
         return _call("cross", q, k_pages, v_pages, page_table, enc_lens, n_q_heads, n_kv_heads,
                      head_dim, page_tokens, scale, **kw)
 
@@ -415,27 +415,51 @@ def kv_append(k_new, v_new, k_pages, v_pages, page_table, seq_lens, n_new=None,
         raise AtlasError(rc, status_string(rc))
 
 
+_SAME_DEVICE = contextlib.nullcontext()
+
+
 def _on(device):
     """The device guard of a call: work goes to the tensors' device, whichever is current."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+    if device.index == torch._C._cuda_getDevice():
+        return _SAME_DEVICE
     return torch.cuda.device(device)
 
 
-def _check(like, **tensors):
-    """Every given tensor is a CUDA tensor of `like`'s device, contiguous, of the dtype given."""
+def _stream(device):
+    """Handle of the current torch stream of a CUDA device (torch.cuda.current_stream
+    builds a Stream object around it, several microseconds a call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _check(device, **tensors):
+    """Every given tensor is a contiguous tensor of `device` and of the dtype given."""
     for name, (t, dtype) in tensors.items():
         if t is None:
             continue
-        if not t.is_cuda or t.device != like.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor on {like.device}")
+        if t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}")
+
+
+def _cuda_device(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
 
 
 @functools.lru_cache(maxsize=64)
 def _host_array(ctype, values):
     return (ctype * len(values))(*values)
+
+
+@functools.lru_cache(maxsize=64)
+def _frequencies(theta, rot_dim):
+    """theta^(-2 p / rot_dim) of every pair: a table of its arguments alone."""
+    if not 0.0 < theta < float("inf") or not 2 <= rot_dim <= 4096:
+        return None  # the library refuses these
+    return _host_array(ctypes.c_double, tuple(theta ** (-2.0 * p / rot_dim)
+                                              for p in range(rot_dim // 2)))
 
 
 def _row_strides(name, t):
@@ -468,14 +492,15 @@ def kv_append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, posi
     dtype = k_pages.dtype
     if q is not None and (q.dim() != 4 or q.shape[0] != B or q.shape[2:] != k_new.shape[2:]):
         raise ValueError("q must be [B][Hq][n][D] like k_new")
+    device = _cuda_device("k_pages", k_pages)
     for name, t in (("q", q), ("k_new", k_new), ("v_new", v_new)):
-        if t is not None and (not t.is_cuda or t.device != k_pages.device or t.dtype != dtype):
-            raise ValueError(f"{name} must be a {dtype} tensor on {k_pages.device}")
+        if t is not None and (t.device != device or t.dtype != dtype):
+            raise ValueError(f"{name} must be a {dtype} tensor on {device}")
     if positions.dim() == 2:
         positions = positions[None]
     if positions.dim() != 3 or positions.shape[1:] != (B, n):
         raise ValueError("positions must be [n_axes][B][n]")
-    _check(k_pages, k_pages=(k_pages, dtype), v_pages=(v_pages, dtype),
+    _check(device, k_pages=(k_pages, dtype), v_pages=(v_pages, dtype),
            page_table=(page_table, torch.int32), seq_lens=(seq_lens, torch.int32),
            positions=(positions, torch.int32), n_new=(n_new, torch.int32),
            q_out=(q_out, dtype), status=(status, torch.int32))
@@ -504,12 +529,13 @@ def kv_append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, posi
     R.rot_dim, R.interleaved, R.theta = rot_dim, int(bool(interleaved)), theta
     if pair_axis is not None:
         R.pair_axis = ctypes.addressof(_host_array(ctypes.c_int32, tuple(pair_axis)))
-    if inv_freq is not None:
-        freq = (ctypes.c_double * len(inv_freq))(*inv_freq)
+    freq = _frequencies(theta, rot_dim) if inv_freq is None else \
+        (ctypes.c_double * len(inv_freq))(*inv_freq)
+    if freq is not None:
         R.inv_freq = ctypes.addressof(freq)
     R.status_word = _ptr(status)
-    R.stream = torch.cuda.current_stream(k_pages.device).cuda_stream
-    with _on(k_pages.device):
+    R.stream = _stream(device)
+    with _on(device):
         rc = lib.atlas_kv_append_rope(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(),
                                       v_pages.data_ptr(), page_table.data_ptr(),
                                       seq_lens.data_ptr(), _ptr(n_new), Hkv, D,
@@ -550,7 +576,8 @@ def kv_weights(q, k_pages, page_table, seq_lens, lse, n_q_heads, n_kv_heads, hea
         raise ValueError("q and the pool must have the shapes the sizes given say")
     if weights is None:
         weights = torch.zeros((B, n_kv_heads, page_table.shape[1] * page_tokens), device=q.device)
-    _check(q, q=(q, q.dtype), k_pages=(k_pages, q.dtype), page_table=(page_table, torch.int32),
+    device = _cuda_device("q", q)
+    _check(device, q=(q, q.dtype), k_pages=(k_pages, q.dtype), page_table=(page_table, torch.int32),
            seq_lens=(seq_lens, torch.int32), lse=(lse, torch.float32),
            weights=(weights, torch.float32), q_lens=(q_lens, torch.int32),
            status=(status, torch.int32))
@@ -565,8 +592,8 @@ def kv_weights(q, k_pages, page_table, seq_lens, lse, n_q_heads, n_kv_heads, hea
     W.weights, W.row_tokens, W.accumulate = weights.data_ptr(), weights.shape[2], int(bool(accumulate))
     W.q_lens, W.window, W.softcap, W.sm_count = _ptr(q_lens), window, softcap, sm_count
     W.status_word = _ptr(status)
-    W.stream = torch.cuda.current_stream(q.device).cuda_stream
-    with _on(q.device):
+    W.stream = _stream(device)
+    with _on(device):
         need = lib.atlas_kv_weights_workspace_size(n_q_heads, n_kv_heads, head_dim, page_tokens,
                                                    ctypes.byref(W))
         if workspace is None and 0 < need < ctypes.c_size_t(-1).value:
@@ -594,14 +621,14 @@ def kv_select(weights, seq_lens, budget, *, keep_first=0, keep_recent=0, kept=No
     B, Hkv, T = weights.shape
     budget = int(budget)
     shape = (B, Hkv, max(budget, 0))
-    dev = weights.device
+    dev = _cuda_device("weights", weights)
     if kept is None:
         kept = torch.empty(shape, dtype=torch.int32, device=dev)
     if kept_weights is None:
         kept_weights = torch.empty(shape, dtype=torch.float32, device=dev)
     if new_lens is None:
         new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-    _check(weights, weights=(weights, torch.float32), seq_lens=(seq_lens, torch.int32),
+    _check(dev, weights=(weights, torch.float32), seq_lens=(seq_lens, torch.int32),
            kept=(kept, torch.int32), kept_weights=(kept_weights, torch.float32),
            new_lens=(new_lens, torch.int32), status=(status, torch.int32))
     if kept.shape != shape or kept_weights.shape != shape or new_lens.numel() != B:
@@ -611,7 +638,7 @@ def kv_select(weights, seq_lens, budget, *, keep_first=0, keep_recent=0, kept=No
     S.keep_first, S.keep_recent = keep_first, keep_recent
     S.kept, S.new_lens, S.kept_weights = kept.data_ptr(), new_lens.data_ptr(), kept_weights.data_ptr()
     S.status_word = _ptr(status)
-    S.stream = torch.cuda.current_stream(dev).cuda_stream
+    S.stream = _stream(dev)
     with _on(dev):
         rc = lib.atlas_kv_select(weights.data_ptr(), seq_lens.data_ptr(), Hkv, ctypes.byref(S))
     if rc != 0:
@@ -627,7 +654,8 @@ def kv_compact(k_pages, v_pages, page_table, kept, new_lens, *, new_page_table=N
     if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
         raise ValueError("pools must be [num_pages][Hkv][P][D]")
     num_pages, Hkv, P, D = k_pages.shape
-    _check(k_pages, k_pages=(k_pages, k_pages.dtype), v_pages=(v_pages, k_pages.dtype),
+    device = _cuda_device("k_pages", k_pages)
+    _check(device, k_pages=(k_pages, k_pages.dtype), v_pages=(v_pages, k_pages.dtype),
            page_table=(page_table, torch.int32), kept=(kept, torch.int32),
            new_lens=(new_lens, torch.int32), new_page_table=(new_page_table, torch.int32),
            status=(status, torch.int32))
@@ -642,8 +670,8 @@ def kv_compact(k_pages, v_pages, page_table, kept, new_lens, *, new_page_table=N
     if new_page_table is not None:
         C.new_page_table, C.new_max_pages = new_page_table.data_ptr(), new_page_table.shape[1]
     C.status_word = _ptr(status)
-    C.stream = torch.cuda.current_stream(k_pages.device).cuda_stream
-    with _on(k_pages.device):
+    C.stream = _stream(device)
+    with _on(device):
         rc = lib.atlas_kv_compact(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
                                   kept.data_ptr(), new_lens.data_ptr(), Hkv, D, P, ctypes.byref(C))
     if rc != 0:

@@ -3,13 +3,14 @@
 //
 // Selection.  One thread-block cluster per (sequence, kv head), its CTAs sharing the row:
 // each maps its part of the weights to order-preserving 32-bit keys in shared memory (read
-// from memory once), and four 8-bit digits, from the top, narrow the k-th largest key down
-// exactly: a histogram of the digit over the keys that match the digits found so far,
-// summed over the cluster through distributed shared memory, tells which bin the k-th
-// largest lies in and how many are still wanted there.  What equals the last key is taken
-// by lowest index, so the set never depends on timing, and positions in the ascending
-// output are counts of kept keys before (ballots in a warp, sums over warps and CTAs).
-// Memory: 4 bytes per key in, 8 per kept key out; bound by latency, five cluster barriers.
+// from memory once), and three digits of 11, 11 and 10 bits, from the top, narrow the k-th
+// largest key down exactly: a histogram of the digit over the keys that match the digits
+// found so far, summed over the cluster through distributed shared memory, tells which bin
+// the k-th largest lies in and how many are still wanted there.  What equals the last key
+// is taken by lowest index, so the set never depends on timing, and positions in the
+// ascending output are counts of kept keys before (ballots in a warp, sums over warps and
+// CTAs).  Memory: 4 bytes per key in, 8 per kept key out; bound by latency: a load, four
+// cluster barriers, and per digit a pass over the keys in shared memory and a scan.
 //
 // Compaction.  Rows of head_dim elements move between page slots, 16 bytes per thread and
 // step.  Into fresh pages every row is independent.  In place, row j takes row kept[j] >= j:
@@ -17,9 +18,9 @@
 // in chunks, and since a chunk's sources lie at or behind its own destinations, it is
 // enough that a chunk is read completely (a CTA barrier) before it is written: later
 // chunks' sources lie behind it, earlier ones have been read.  No CTA waits on another:
-// each owns a 64-byte wide strip of one (sequence, kv head, K or V) from end to end, reads
-// one chunk ahead (and page ids and indices two and three ahead), so a step costs one
-// memory latency.
+// each owns a 64-byte wide strip of one (sequence, kv head, K or V) from end to end, with
+// seven chunks in flight (cp.async) ahead of the one it writes, and their page ids and
+// indices read one and two chunks before that.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -35,9 +36,12 @@ __device__ __forceinline__ void record(uint32_t *status, uint32_t bit) {
 }
 
 // ---------------------------------------------------------------- selection
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelMaxCtas = 8;  // the portable cluster size
+constexpr int kSelMaxCtas = 8;    // the portable cluster size
+constexpr int kSelKeys = 8192;    // keys of a CTA, while there are fewer than 8 of them
+constexpr int kBins = 2 * kSelThreads;
+constexpr int kSelCache = 200 * 1024;
 
 struct SelectParams {
     const float *weights;
@@ -62,21 +66,29 @@ __device__ __forceinline__ void cluster_barrier() {
         "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The 32-bit word that CTA `rank` of the cluster holds where this CTA holds *local.
+// The 32-bit words that CTA `rank` of the cluster holds where this CTA holds *local.
 __device__ __forceinline__ uint32_t ld_cluster(const uint32_t *local, int rank) {
     uint32_t addr, v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ uint2 ld_cluster2(const uint32_t *local, int rank) {
+    uint32_t addr;
+    uint2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
 
 // grid (CTAs of a row's cluster, Hkv, B).  CACHED: the row's keys stay in shared memory;
 // else (rows too long for that) each pass reads the weights again.
 template <bool CACHED>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectParams p) {
     extern __shared__ uint32_t cached[];
-    __shared__ uint32_t hist[2][256];
+    __shared__ __align__(8) uint32_t hist[2][kBins];
     __shared__ uint32_t found[2];                 // digit, keys above it
+    __shared__ uint32_t warp_sum[kSelWarps];
     __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
     __shared__ uint32_t cta_gt, cta_eq;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -93,116 +105,118 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     const float *w = p.weights + row * p.row_tokens;
     int32_t *kept = p.kept + row * p.budget;
     float *kept_w = p.kept_weights ? p.kept_weights + row * p.budget : nullptr;
+    // Keys that stay whatever their weight: all of them, or the first and the recent ones.
+    const bool whole = L <= p.budget;
+    const int lo = whole ? L : p.first, hi = whole ? L : L - p.recent;
+    uint32_t want = (uint32_t)(n - lo - (L - hi));  // of the keys in [lo, hi)
+    const int seg = (hi - lo + ctas - 1) / ctas;
+    const int s0 = min(hi, lo + rank * seg), len = want == 0 ? 0 : min(hi, s0 + seg) - s0;
+    if (CACHED) {
+#pragma unroll 8
+        for (int i = tid; i < len; i += kSelThreads) cached[i] = order_key(w[s0 + i]);
+    }
     for (int j = n + me; j < p.budget; j += all) {
         kept[j] = -1;
         if (kept_w) kept_w[j] = 0.f;
     }
-    // Keys that stay whatever their weight: all of them, or the first and the recent ones.
-    const bool whole = L <= p.budget;
-    const int lo = whole ? L : p.first, hi = whole ? L : L - p.recent;
     for (int j = me; j < lo + (L - hi); j += all) {
         const int t = j < lo ? j : hi + (j - lo);
         const int at = j < lo ? j : n - (L - hi) + (j - lo);
         kept[at] = t;
         if (kept_w) kept_w[at] = w[t];
     }
-    uint32_t want = (uint32_t)(n - lo - (L - hi));  // of the keys in [lo, hi)
-    if (want == 0) return;                          // the whole cluster alike
-
-    const int seg = (hi - lo + ctas - 1) / ctas;
-    const int s0 = min(hi, lo + rank * seg), len = min(hi, s0 + seg) - s0;
-    if (CACHED)
-        for (int i = tid; i < len; i += kSelThreads) cached[i] = order_key(w[s0 + i]);
+    if (want == 0) return;  // the whole cluster alike
     auto key_of = [&](int i) { return CACHED ? cached[i] : order_key(w[s0 + i]); };
 
     uint32_t prefix = 0;
 #pragma unroll 1
-    for (int d = 0; d < 4; ++d) {
-        const int shift = 24 - 8 * d;
+    for (int d = 0; d < 3; ++d) {
+        const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+        const uint32_t mask = d == 2 ? 1023u : 2047u;
+        const uint32_t known = d == 0 ? 0u : ~0u << (d == 1 ? 21 : 10);  // the digits found
         uint32_t *h = hist[d & 1];
-        for (int i = tid; i < 256; i += kSelThreads) h[i] = 0u;
+        h[tid] = h[tid + kSelThreads] = 0u;
         __syncthreads();
         for (int i0 = 0; i0 < len; i0 += kSelThreads) {
             const int i = i0 + tid;
-            uint32_t bin = 256;  // no vote
+            uint32_t bin = kBins;  // no vote
             if (i < len) {
                 const uint32_t k = key_of(i);
-                if (d == 0 || ((k ^ prefix) >> (shift + 8)) == 0u) bin = (k >> shift) & 255u;
+                if (((k ^ prefix) & known) == 0u) bin = (k >> shift) & mask;
             }
-            // one addition per distinct digit of the warp: the top digits are nearly all
-            // alike, and 32 additions to one word would go one after another
-            const uint32_t peers = __match_any_sync(0xffffffffu, bin);
-            if (bin < 256 && lane == __ffs(peers) - 1) atomicAdd(&h[bin], (uint32_t)__popc(peers));
+            // Equal keys all fall into one bin: a warp that agrees adds once.
+            const uint32_t votes = __ballot_sync(0xffffffffu, bin < kBins);
+            if (votes == 0u) continue;
+            const uint32_t one = __shfl_sync(0xffffffffu, bin, __ffs(votes) - 1);
+            if (__ballot_sync(0xffffffffu, bin == one) == votes) {
+                if (lane == 0) atomicAdd(&h[one], (uint32_t)__popc(votes));
+            } else if (bin < kBins) {
+                atomicAdd(&h[bin], 1u);
+            }
         }
         cluster_barrier();
-        if (warp == 0) {
-            // lane l: bins 255 - 8l .. 248 - 8l, from the top
-            uint32_t cnt[8], sum = 0;
+        // Thread l owns bins 2047 - 2l and 2046 - 2l: a scan over threads goes from the top.
+        uint32_t first = 0, second = 0;
+#pragma unroll 8
+        for (int r = 0; r < ctas; ++r) {
+            const uint2 v = ld_cluster2(&h[kBins - 2 - 2 * tid], r);
+            first += v.y;
+            second += v.x;
+        }
+        uint32_t above = first + second;  // inclusive over the warp's lanes
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                cnt[e] = 0;
-                for (int r = 0; r < ctas; ++r) cnt[e] += ld_cluster(&h[255 - 8 * lane - e], r);
-                sum += cnt[e];
-            }
-            uint32_t above = sum;  // inclusive scan over lanes, then exclusive
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, above, o);
-                if (lane >= o) above += v;
-            }
-            above -= sum;
-            if (above < want && above + sum >= want) {  // exactly one lane
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (above < want && above + cnt[e] >= want) {
-                        found[0] = 255u - 8u * lane - e;
-                        found[1] = above;
-                    }
-                    above += cnt[e];
-                }
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, above, o);
+            if (lane >= o) above += v;
+        }
+        if (lane == 31) warp_sum[warp] = above;
+        __syncthreads();
+        above += __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u) - (first + second);
+        if (above < want && above + first + second >= want) {  // exactly one thread
+            const bool top = above + first >= want;
+            found[0] = (uint32_t)(kBins - 1 - 2 * tid - (top ? 0 : 1));
+            found[1] = above + (top ? 0u : first);
         }
         __syncthreads();
         prefix |= found[0] << shift;
         want -= found[1];
-        // (found is written again only after the next cluster barrier; this digit's
-        // histogram only after the one after that, when every CTA has read it)
+        // (found and warp_sum are written again only after the next cluster barrier; this
+        // digit's histogram only after the one after that, when every CTA has read it)
     }
     // Keys above `prefix` stay, and the first `want` equal to it.  A warp takes a
     // contiguous part, 32 keys at a time in order.
     const int part = ((len + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
     const int w0 = min(len, warp * part), w1 = min(len, w0 + part);
     uint32_t gt = 0, eq = 0;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < w1 ? key_of(i) : 0u;
-        gt += __popc(__ballot_sync(0xffffffffu, i < w1 && k > prefix));
-        eq += __popc(__ballot_sync(0xffffffffu, i < w1 && k == prefix));
+    for (int i = w0 + lane; i < w1; i += 32) {
+        const uint32_t k = key_of(i);
+        gt += k > prefix;
+        eq += k == prefix;
     }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
     if (lane == 0) {
         warp_gt[warp] = gt;
         warp_eq[warp] = eq;
     }
     __syncthreads();
-    if (tid == 0) {
-        uint32_t a = 0, c = 0;
-        for (int k = 0; k < kSelWarps; ++k) {
-            a += warp_gt[k];
-            c += warp_eq[k];
+    if (warp == 0) {
+        const uint32_t a = __reduce_add_sync(0xffffffffu, warp_gt[lane]);
+        const uint32_t c = __reduce_add_sync(0xffffffffu, warp_eq[lane]);
+        if (lane == 0) {
+            cta_gt = a;
+            cta_eq = c;
         }
-        cta_gt = a;
-        cta_eq = c;
     }
     cluster_barrier();
-    uint32_t gt_before = 0, eq_before = 0;
-    for (int r = 0; r < rank; ++r) {
-        gt_before += ld_cluster(&cta_gt, r);
-        eq_before += ld_cluster(&cta_eq, r);
+    // kept keys before this warp's: earlier CTAs (lanes 0..7 read one each), earlier warps
+    uint32_t gt_before = lane < warp ? warp_gt[lane] : 0u, eq_before = lane < warp ? warp_eq[lane] : 0u;
+    if (lane < rank) {
+        gt_before += ld_cluster(&cta_gt, lane);
+        eq_before += ld_cluster(&cta_eq, lane);
     }
-    for (int k = 0; k < warp; ++k) {
-        gt_before += warp_gt[k];
-        eq_before += warp_eq[k];
-    }
+    gt_before = __reduce_add_sync(0xffffffffu, gt_before);
+    eq_before = __reduce_add_sync(0xffffffffu, eq_before);
     uint32_t at = (uint32_t)lo + gt_before + min(want, eq_before);
     const uint32_t below = (1u << lane) - 1u;
     for (int i0 = w0; i0 < w1; i0 += 32) {
@@ -306,81 +320,98 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const Compac
         if (dst[u] >= 0) s.pool[dst[u]] = x[u];
 }
 
-constexpr int kShiftThreads = 512, kShiftRows = 4;
+// In place: one CTA per strip walks the rows in order, kShiftRows rows per thread and
+// chunk, each thread copying its own pieces through its own slots of a ring.
+constexpr int kShiftThreads = 512, kShiftRows = 2, kShiftStages = 8;
+constexpr int kShiftSmem = kShiftStages * kShiftRows * kShiftThreads * 16;
 
-// In place: one CTA per strip walks the rows in order, a chunk at a time.
-__global__ void __launch_bounds__(kShiftThreads) compact_shift_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kShiftThreads, 1) compact_shift_kernel(const CompactParams p) {
+    extern __shared__ __align__(16) uint4 ring[];  // [stage][row][thread]
     Strip s;
     if (!strip_of(p, s)) return;
+    constexpr int R = kShiftRows, S = kShiftStages;
     const int lp = 31 - __clz(p.P);
     const int per = kShiftThreads >> p.lg_piece;
-    const int chunk = per * kShiftRows;
     const int r = (int)threadIdx.x >> p.lg_piece;
     const int64_t ctx = (int64_t)p.max_pages * p.P;
-    // Index of row u of chunk c (-1: no such row), and the page ids of an index and of
-    // its destination; both are only used a step later.
-    auto index = [&](int64_t c, int (&t)[kShiftRows]) {
+    const int64_t chunks = (s.n + (int64_t)per * R - 1) / (per * R);
+    auto row = [&](int64_t c, int u) { return c * (per * R) + u * per + r; };
+    // The index of a row (unchecked; -1: no such row), and the page ids of an index and of
+    // a row: each only used a chunk later.
+    auto index = [&](int64_t c, int (&t)[R]) {
 #pragma unroll
-        for (int u = 0; u < kShiftRows; ++u) {
-            const int64_t j = c * chunk + u * per + r;
-            t[u] = j < s.n ? s.kept[j] : -1;
-            if (j < s.n && (t[u] < j || t[u] >= ctx)) {
+        for (int u = 0; u < R; ++u) t[u] = row(c, u) < s.n ? s.kept[row(c, u)] : -1;
+    };
+    auto source = [&](int64_t c, int (&t)[R], int (&a)[R]) {
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            if (row(c, u) < s.n && (t[u] < row(c, u) || t[u] >= ctx)) {
                 if (s.tells) record(p.status, ATLAS_DEV_BAD_SEQLEN);
                 t[u] = -1;
             }
-        }
-    };
-    auto pages = [&](int64_t c, const int (&t)[kShiftRows], int (&a)[kShiftRows], int (&z)[kShiftRows]) {
-#pragma unroll
-        for (int u = 0; u < kShiftRows; ++u) {
-            const int64_t j = c * chunk + u * per + r;
             a[u] = t[u] >= 0 ? s.src_table[t[u] >> lp] : 0;
-            z[u] = t[u] >= 0 ? s.dst_table[j >> lp] : 0;
         }
     };
-    // Loads chunk c; dst -1 where nothing moves (no row, a bad page, a row already there).
-    auto load = [&](int64_t c, const int (&t)[kShiftRows], const int (&a)[kShiftRows],
-                    const int (&z)[kShiftRows], uint4 (&x)[kShiftRows], int64_t (&dst)[kShiftRows]) {
+    auto target = [&](int64_t c, int (&z)[R]) {
 #pragma unroll
-        for (int u = 0; u < kShiftRows; ++u) {
-            const int64_t j = c * chunk + u * per + r;
-            dst[u] = -1;
+        for (int u = 0; u < R; ++u) z[u] = row(c, u) < s.n ? s.dst_table[row(c, u) >> lp] : -1;
+    };
+    uint32_t moving = 0;  // bit (chunk % S) * R + u: that row is in the ring
+    auto load = [&](int64_t c, const int (&t)[R], const int (&a)[R]) {
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            const uint32_t bit = 1u << ((int)(c % S) * R + u);
+            moving &= ~bit;
             if (t[u] < 0) continue;
-            if (a[u] < 0 || a[u] >= p.num_pages || z[u] < 0 || z[u] >= p.num_pages) {
+            if (a[u] < 0 || a[u] >= p.num_pages) {
                 if (s.tells) record(p.status, ATLAS_DEV_BAD_PAGE);
                 continue;
             }
-            if (t[u] == j) continue;
-            x[u] = s.pool[slot_of(p, a[u], t[u]) + s.piece];
-            dst[u] = slot_of(p, z[u], (int)j) + s.piece;
+            if (t[u] == row(c, u)) continue;  // it is where it belongs
+            moving |= bit;
+            cp_async16(smem_u32(ring + ((int)(c % S) * R + u) * kShiftThreads + threadIdx.x),
+                       s.pool + slot_of(p, a[u], t[u]) + s.piece, 16);
         }
+        cp_async_commit();
     };
-    const int64_t chunks = (s.n + chunk - 1) / chunk;
-    int t1[kShiftRows], t2[kShiftRows], a1[kShiftRows], z1[kShiftRows];
-    uint4 cur[kShiftRows], nxt[kShiftRows];
-    int64_t dst[kShiftRows], dst_nxt[kShiftRows];
-    index(0, t1);
-    index(1, t2);
-    pages(0, t1, a1, z1);
-    load(0, t1, a1, z1, cur, dst);
-    pages(1, t2, a1, z1);
+    // Chunks 0 .. S - 2 are on their way before the first is written.
+    int t0[R], t1[R], a0[R], z0[R];
+    index(0, t0);
+    index(1, t1);
+    source(0, t0, a0);
+#pragma unroll 1
+    for (int64_t c = 0; c < S - 1; ++c) {
+        load(c, t0, a0);
 #pragma unroll
-    for (int u = 0; u < kShiftRows; ++u) t1[u] = t2[u];
-    index(2, t2);
+        for (int u = 0; u < R; ++u) t0[u] = t1[u];
+        source(c + 1, t0, a0);
+        index(c + 2, t1);
+    }
+    target(0, z0);
+#pragma unroll 1
     for (int64_t c = 0; c < chunks; ++c) {
-        load(c + 1, t1, a1, z1, nxt, dst_nxt);
-        pages(c + 2, t2, a1, z1);
+        load(c + S - 1, t0, a0);
+        int z1[R];
+        target(c + 1, z1);
 #pragma unroll
-        for (int u = 0; u < kShiftRows; ++u) t1[u] = t2[u];
-        index(c + 3, t2);
-        __syncthreads();  // every thread has read chunk c
+        for (int u = 0; u < R; ++u) t0[u] = t1[u];
+        source(c + S, t0, a0);
+        index(c + S + 1, t1);
+        cp_async_wait<S - 1>();
+        __syncthreads();  // every thread has chunk c (and all before it) in the ring
 #pragma unroll
-        for (int u = 0; u < kShiftRows; ++u) {
-            if (dst[u] >= 0) s.pool[dst[u]] = cur[u];
-            cur[u] = nxt[u];
-            dst[u] = dst_nxt[u];
+        for (int u = 0; u < R; ++u) {
+            const int at = (int)(c % S) * R + u;
+            if ((moving >> at) & 1u) {
+                if (z0[u] >= 0 && z0[u] < p.num_pages)
+                    s.pool[slot_of(p, z0[u], (int)row(c, u)) + s.piece] = ring[at * kShiftThreads + threadIdx.x];
+                else if (s.tells)
+                    record(p.status, ATLAS_DEV_BAD_PAGE);
+            }
+            z0[u] = z1[u];
         }
     }
+    cp_async_wait<0>();
 }
 
 }  // namespace
@@ -412,18 +443,17 @@ atlas_status atlas_kv_select(const float *weights, const int32_t *seq_lens, int3
     p.new_lens = S->new_lens;
     p.kept_weights = S->kept_weights;
     p.status = S->status_word;
-    // CTAs per row: up to 8 of about 4096 keys each.
     int ctas = 1;
-    while (ctas < kSelMaxCtas && (int64_t)ctas * 4096 < p.row_tokens) ctas *= 2;
+    while (ctas < kSelMaxCtas && (int64_t)ctas * kSelKeys < p.row_tokens) ctas *= 2;
     const int64_t bytes = ((int64_t)p.row_tokens + ctas - 1) / ctas * 4;
-    const bool cached = bytes <= 200 * 1024;
+    const bool cached = bytes <= kSelCache;
     auto kern = cached ? select_kernel<true> : select_kernel<false>;
     static int configured[64] = {0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return ATLAS_ERR_CUDA;
     if (dev >= 64 || !configured[dev]) {
         if (cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 200 * 1024) != cudaSuccess)
+                                 kSelCache) != cudaSuccess)
             return ATLAS_ERR_CUDA;
         if (dev < 64) configured[dev] = 1;
     }
@@ -482,9 +512,18 @@ atlas_status atlas_kv_compact(void *k_pages, void *v_pages, const int32_t *page_
                         (unsigned)C->batch);
         compact_move_kernel<<<grid, kMoveThreads, 0, stream>>>(p);
     } else {
+        static int configured[64] = {0};
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return ATLAS_ERR_CUDA;
+        if (dev >= 64 || !configured[dev]) {
+            if (cudaFuncSetAttribute(compact_shift_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kShiftSmem) != cudaSuccess)
+                return ATLAS_ERR_CUDA;
+            if (dev < 64) configured[dev] = 1;
+        }
         p.lg_piece = 2;  // 64-byte strips
         const dim3 grid(1, (unsigned)(2 * n_kv_heads * (p.vec >> 2)), (unsigned)C->batch);
-        compact_shift_kernel<<<grid, kShiftThreads, 0, stream>>>(p);
+        compact_shift_kernel<<<grid, kShiftThreads, kShiftSmem, stream>>>(p);
     }
     return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }

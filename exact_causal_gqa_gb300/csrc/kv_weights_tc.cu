@@ -67,29 +67,28 @@ __device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t k_smem, u
                   qd + (((kk >> 2) * q_slab + (kk & 3) * 32) >> 4), idesc, kk > 0);
 }
 
-// Adds 2^(s2 - lse2[c]) of NC columns of scores; with `masked`, of those columns c that
+// Adds 2^(s2 + neg_lse2[c]) of NC columns of scores; with kMasked, of those columns c that
 // key t is visible to (t < lim[c], and t >= lim[c] - window with a window).
-template <int NC>
-__device__ __forceinline__ void add_weights(const WeightsParams &p, const uint32_t (&s)[NC],
-                                            const float *lse2, const int *lim, int t, bool masked,
+template <int NC, bool kMasked, bool kCapped>
+__device__ __forceinline__ void add_columns(const WeightsParams &p, const uint32_t (&s)[NC],
+                                            const float *neg_lse2, const int *lim, int t,
                                             float2 (&sum)[2]) {
     const float2 sc = make_float2(p.scale_log2, p.scale_log2);
-    const bool capped = p.softcap_log2 > 0.f;
+    const int far = p.window > 0 ? t + p.window : INT32_MAX;
 #pragma unroll
     for (int c = 0; c < NC; c += 4) {
-        const float4 l4 = *reinterpret_cast<const float4 *>(lse2 + c);
+        const float4 l4 = *reinterpret_cast<const float4 *>(neg_lse2 + c);
         float2 a = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
         float2 b = make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-        if (capped) {
-            a = make_float2(score_log2(p, a.x) - l4.x, score_log2(p, a.y) - l4.y);
-            b = make_float2(score_log2(p, b.x) - l4.z, score_log2(p, b.y) - l4.w);
+        if (kCapped) {
+            a = make_float2(score_log2(p, a.x) + l4.x, score_log2(p, a.y) + l4.y);
+            b = make_float2(score_log2(p, b.x) + l4.z, score_log2(p, b.y) + l4.w);
         } else {
-            a = ffma2(a, sc, make_float2(-l4.x, -l4.y));
-            b = ffma2(b, sc, make_float2(-l4.z, -l4.w));
+            a = ffma2(a, sc, make_float2(l4.x, l4.y));
+            b = ffma2(b, sc, make_float2(l4.z, l4.w));
         }
-        if (masked) {
+        if (kMasked) {
             const int4 m = *reinterpret_cast<const int4 *>(lim + c);
-            const int far = p.window > 0 ? t + p.window : INT32_MAX;
             a.x = t < m.x && m.x <= far ? a.x : -INFINITY;
             a.y = t < m.y && m.y <= far ? a.y : -INFINITY;
             b.x = t < m.z && m.z <= far ? b.x : -INFINITY;
@@ -98,6 +97,18 @@ __device__ __forceinline__ void add_weights(const WeightsParams &p, const uint32
         sum[0] = fadd2(sum[0], make_float2(ex2(a.x), ex2(a.y)));
         sum[1] = fadd2(sum[1], make_float2(ex2(b.x), ex2(b.y)));
     }
+}
+
+// The common case (no cap, every column visible) on a path of its own: compares and
+// selects computed and not used doubled the time of the prompt's kernel.
+template <int NC>
+__device__ __forceinline__ void add_weights(const WeightsParams &p, const uint32_t (&s)[NC],
+                                            const float *neg_lse2, const int *lim, int t, bool masked,
+                                            float2 (&sum)[2]) {
+    const bool capped = p.softcap_log2 > 0.f;
+    if (!masked && !capped) add_columns<NC, false, false>(p, s, neg_lse2, lim, t, sum);
+    else if (!capped) add_columns<NC, true, false>(p, s, neg_lse2, lim, t, sum);
+    else add_columns<NC, true, true>(p, s, neg_lse2, lim, t, sum);
 }
 
 // ---------------------------------------------------------------- few columns
@@ -134,7 +145,7 @@ __global__ void __launch_bounds__(StreamCfg<D, N>::kThreads, StreamCfg<D, N>::kC
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
-    float *lse2 = reinterpret_cast<float *>(smem + C::OFF_LSE);
+    float *nlse = reinterpret_cast<float *>(smem + C::OFF_LSE);
     int *lim = reinterpret_cast<int *>(smem + C::OFF_LIM);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_TMEM + 8);
@@ -195,7 +206,7 @@ __global__ void __launch_bounds__(StreamCfg<D, N>::kThreads, StreamCfg<D, N>::kC
     for (int c = threadIdx.x; c < N; c += C::kThreads) {
         const bool real = c < ncols;
         const int i = real ? c % qn : 0;
-        lse2[c] = real ? lse_log2(p.lse[row0 + (int64_t)(c / qn) * p.q_len + i]) : INFINITY;
+        nlse[c] = real ? -lse_log2(p.lse[row0 + (int64_t)(c / qn) * p.q_len + i]) : -INFINITY;
         lim[c] = real ? L - qn + i + 1 : 0;
     }
     fence_proxy_async_smem();
@@ -279,14 +290,14 @@ __global__ void __launch_bounds__(StreamCfg<D, N>::kThreads, StreamCfg<D, N>::kC
                 tc_fence_before();
                 mbar_arrive(BAR(C::B_SEMPTY + buf));
                 // (padding columns are zero rows: 0 times a non-finite key is not 0)
-                add_weights<16>(p, s, lse2, lim, t, masked || ncols < 16, sum);
+                add_weights<16>(p, s, nlse, lim, t, masked || ncols < 16, sum);
             } else {
 #pragma unroll 1
                 for (int c0 = 0; c0 < nmma; c0 += 32) {
                     uint32_t s[32];
                     tmem_ld32(ts + c0, s);
                     tmem_wait_ld32(s);
-                    add_weights<32>(p, s, lse2 + c0, lim + c0, t, masked || c0 + 32 > ncols, sum);
+                    add_weights<32>(p, s, nlse + c0, lim + c0, t, masked || c0 + 32 > ncols, sum);
                 }
                 tc_fence_before();
                 mbar_arrive(BAR(C::B_SEMPTY + buf));
@@ -530,18 +541,18 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
                 const int f = q.j * BT + e * 32 + lane;
                 const int i = f % p.q_len;
                 const bool real = f < p.G * p.q_len && i < qn;
-                v[e] = real ? lse_log2(p.lse[row0 + f]) : INFINITY;
+                v[e] = real ? -lse_log2(p.lse[row0 + f]) : -INFINITY;
                 m[e] = real ? L - qn + i + 1 : 0;
             }
             if (q.n >= S && !wait_warp(BAR(C::B_CEMPTY + s), ((q.n / S) - 1) & 1, abort_flag)) {
                 failed = true;
                 break;
             }
-            float *lse2 = reinterpret_cast<float *>(smem + C::OFF_LSE) + s * BT;
+            float *nlse = reinterpret_cast<float *>(smem + C::OFF_LSE) + s * BT;
             int *lim = reinterpret_cast<int *>(smem + C::OFF_LIM) + s * BT;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                lse2[e * 32 + lane] = v[e];
+                nlse[e * 32 + lane] = v[e];
                 lim[e * 32 + lane] = m[e];
             }
             __syncwarp();
@@ -570,7 +581,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
                 tc_fence_after();
                 const bool masked = !q.whole || kb + BT > q.lim_min ||
                                     (p.window > 0 && kb < q.lim_max - p.window);
-                const float *lse2 = reinterpret_cast<const float *>(smem + C::OFF_LSE) + s * BT;
+                const float *nlse = reinterpret_cast<const float *>(smem + C::OFF_LSE) + s * BT;
                 const int *lim = reinterpret_cast<const int *>(smem + C::OFF_LIM) + s * BT;
 #pragma unroll 1
                 for (int c0 = 0; c0 < BT; c0 += 32) {
@@ -581,7 +592,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
                         tc_fence_before();
                         mbar_arrive(BAR(C::B_SEMPTY + x));
                     }
-                    add_weights<32>(p, v, lse2 + c0, lim + c0, t, masked, sum);
+                    add_weights<32>(p, v, nlse + c0, lim + c0, t, masked, sum);
                 }
                 ++used;
             }
