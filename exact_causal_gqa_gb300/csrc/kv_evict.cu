@@ -17,10 +17,11 @@
 // a row may only be overwritten once it has been read.  Rows are taken in ascending order
 // in chunks, and since a chunk's sources lie at or behind its own destinations, it is
 // enough that a chunk is read completely (a CTA barrier) before it is written: later
-// chunks' sources lie behind it, earlier ones have been read.  No CTA waits on another:
-// each owns a 64-byte wide strip of one (sequence, kv head, K or V) from end to end, with
-// seven chunks in flight (cp.async) ahead of the one it writes, and their page ids and
-// indices read one and two chunks before that.
+// chunks' sources lie behind it, earlier ones have been read.  A thread-block cluster
+// shares the rows of one (sequence, kv head, K or V): its barrier stands between reading a
+// chunk and writing it, arrived at one chunk ahead, with four chunks in flight (cp.async);
+// indices and page tables come through shared memory, so that nothing but the data's own
+// latency is in the loop.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -39,9 +40,10 @@ __device__ __forceinline__ void record(uint32_t *status, uint32_t bit) {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelMaxCtas = 8;    // the portable cluster size
-constexpr int kSelKeys = 8192;    // keys of a CTA, while there are fewer than 8 of them
+constexpr int kSelKeys = 8192;    // keys of a CTA, while fewer than 8 CTAs share a row
 constexpr int kBins = 2 * kSelThreads;
 constexpr int kSelCache = 200 * 1024;
+constexpr int kSelAhead = 8;
 
 struct SelectParams {
     const float *weights;
@@ -60,10 +62,19 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+// Orders nothing, so it does not wait for earlier writes to be performed.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_barrier() {
-    asm volatile(
-        "barrier.cluster.arrive.release.aligned;\n\t"
-        "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 // The 32-bit words that CTA `rank` of the cluster holds where this CTA holds *local.
@@ -111,47 +122,66 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
     uint32_t want = (uint32_t)(n - lo - (L - hi));  // of the keys in [lo, hi)
     const int seg = (hi - lo + ctas - 1) / ctas;
     const int s0 = min(hi, lo + rank * seg), len = want == 0 ? 0 : min(hi, s0 + seg) - s0;
-    if (CACHED) {
-#pragma unroll 8
-        for (int i = tid; i < len; i += kSelThreads) cached[i] = order_key(w[s0 + i]);
+    // The entries that no weight decides.  Written last: the cluster barrier before would
+    // wait for them to reach L2.
+    auto fixed = [&] {
+        for (int j = n + me; j < p.budget; j += all) {
+            kept[j] = -1;
+            if (kept_w) kept_w[j] = 0.f;
+        }
+        for (int j = me; j < lo + (L - hi); j += all) {
+            const int t = j < lo ? j : hi + (j - lo);
+            const int at = j < lo ? j : n - (L - hi) + (j - lo);
+            kept[at] = t;
+            if (kept_w) kept_w[at] = w[t];
+        }
+    };
+    if (want == 0) {  // the whole cluster alike
+        fixed();
+        return;
     }
-    for (int j = n + me; j < p.budget; j += all) {
-        kept[j] = -1;
-        if (kept_w) kept_w[j] = 0.f;
-    }
-    for (int j = me; j < lo + (L - hi); j += all) {
-        const int t = j < lo ? j : hi + (j - lo);
-        const int at = j < lo ? j : n - (L - hi) + (j - lo);
-        kept[at] = t;
-        if (kept_w) kept_w[at] = w[t];
-    }
-    if (want == 0) return;  // the whole cluster alike
     auto key_of = [&](int i) { return CACHED ? cached[i] : order_key(w[s0 + i]); };
 
     uint32_t prefix = 0;
 #pragma unroll 1
     for (int d = 0; d < 3; ++d) {
         const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
-        const uint32_t mask = d == 2 ? 1023u : 2047u;
-        const uint32_t known = d == 0 ? 0u : ~0u << (d == 1 ? 21 : 10);  // the digits found
         uint32_t *h = hist[d & 1];
         h[tid] = h[tid + kSelThreads] = 0u;
         __syncthreads();
-        for (int i0 = 0; i0 < len; i0 += kSelThreads) {
-            const int i = i0 + tid;
-            uint32_t bin = kBins;  // no vote
-            if (i < len) {
-                const uint32_t k = key_of(i);
-                if (((k ^ prefix) & known) == 0u) bin = (k >> shift) & mask;
+        if (d == 0) {
+            // Every key votes, on its way into shared memory, kSelAhead loads of a thread at
+            // a time.  Equal weights all fall into one bin: a warp that agrees adds once.
+            for (int i0 = 0; i0 < len; i0 += kSelAhead * kSelThreads) {
+                float v[kSelAhead];
+#pragma unroll
+                for (int e = 0; e < kSelAhead; ++e) {
+                    const int i = i0 + e * kSelThreads + tid;
+                    v[e] = i < len ? w[s0 + i] : 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < kSelAhead; ++e) {
+                    const int i = i0 + e * kSelThreads + tid;
+                    if (i0 + e * kSelThreads >= len) break;
+                    const uint32_t k = order_key(v[e]);
+                    if (CACHED && i < len) cached[i] = k;
+                    int same;
+                    __match_all_sync(0xffffffffu, i < len ? k >> shift : (uint32_t)kBins, &same);
+                    if (i < len && (!same || lane == 0)) atomicAdd(&h[k >> shift], same ? 32u : 1u);
+                }
             }
-            // Equal keys all fall into one bin: a warp that agrees adds once.
-            const uint32_t votes = __ballot_sync(0xffffffffu, bin < kBins);
-            if (votes == 0u) continue;
-            const uint32_t one = __shfl_sync(0xffffffffu, bin, __ffs(votes) - 1);
-            if (__ballot_sync(0xffffffffu, bin == one) == votes) {
-                if (lane == 0) atomicAdd(&h[one], (uint32_t)__popc(votes));
-            } else if (bin < kBins) {
-                atomicAdd(&h[bin], 1u);
+        } else {
+            // Few keys match the digits found, or (many equal weights) whole warps do.
+            const uint32_t known = ~0u << (d == 1 ? 21 : 10), mask = d == 1 ? 2047u : 1023u;
+            for (int i0 = 0; i0 < len; i0 += kSelThreads) {
+                const int i = i0 + tid;
+                const uint32_t k = i < len ? key_of(i) : ~prefix;
+                const bool votes = ((k ^ prefix) & known) == 0u;
+                if (!__any_sync(0xffffffffu, votes)) continue;
+                const uint32_t bin = (k >> shift) & mask;
+                int same;
+                __match_all_sync(0xffffffffu, votes ? bin : (uint32_t)kBins, &same);
+                if (votes && (!same || lane == 0)) atomicAdd(&h[bin], same ? 32u : 1u);
             }
         }
         cluster_barrier();
@@ -217,6 +247,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
     }
     gt_before = __reduce_add_sync(0xffffffffu, gt_before);
     eq_before = __reduce_add_sync(0xffffffffu, eq_before);
+    cluster_arrive_relaxed();  // this thread has read what it needs of the others
     uint32_t at = (uint32_t)lo + gt_before + min(want, eq_before);
     const uint32_t below = (1u << lane) - 1u;
     for (int i0 = w0; i0 < w1; i0 += 32) {
@@ -234,7 +265,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
         at += __popc(keeps);
         eq_before += __popc(eqs);
     }
-    cluster_barrier();  // no CTA leaves while another may still read its counts
+    fixed();
+    cluster_wait();  // no CTA leaves while another may still read its counts
 }
 
 // ---------------------------------------------------------------- compaction
@@ -243,11 +275,11 @@ struct CompactParams {
     const int32_t *page_table, *new_table, *kept, *new_lens;
     int32_t Hkv, P, max_pages, new_max_pages, num_pages, max_kept;
     int32_t vec;       // 16-byte pieces per row: 8, 16 or 32
-    int32_t lg_piece;  // log2 of the pieces of a row that one CTA moves
+    int32_t lg_piece;  // log2 of it
     uint32_t *status;
 };
 
-// Which strip of which pool this CTA moves, and the rows of its sequence.
+// The rows that this CTA moves: those of one kv head in one pool of one sequence.
 struct Strip {
     uint4 *pool;
     const int32_t *src_table, *dst_table, *kept;
@@ -255,15 +287,10 @@ struct Strip {
     bool tells;    // this thread reports what is wrong with its rows
 };
 
+// grid (.., 2 Hkv, B); false: nothing to move.
 __device__ __forceinline__ bool strip_of(const CompactParams &p, Strip &s) {
-    const int strips = p.vec >> p.lg_piece;
-    const int b = blockIdx.z;
-    int y = blockIdx.y;
-    const int strip = y % strips;
-    y /= strips;
-    const int g = y % p.Hkv, kv = y / p.Hkv;
-    const int in_strip = (int)threadIdx.x & ((1 << p.lg_piece) - 1);
-    s.piece = (strip << p.lg_piece) + in_strip;
+    const int b = blockIdx.z, g = (int)blockIdx.y % p.Hkv, kv = (int)blockIdx.y / p.Hkv;
+    s.piece = (int)threadIdx.x & (p.vec - 1);
     s.tells = kv == 0 && s.piece == 0;
     s.pool = static_cast<uint4 *>(kv ? p.v_pages : p.k_pages) + (int64_t)g * p.P * p.vec;
     s.kept = p.kept + ((int64_t)b * p.Hkv + g) * p.max_kept;
@@ -284,7 +311,10 @@ __device__ __forceinline__ int64_t slot_of(const CompactParams &p, int page, int
     return ((int64_t)page * p.Hkv * p.P + (t & (p.P - 1))) * p.vec;
 }
 
-constexpr int kMoveThreads = 256, kMoveRows = 4;
+#ifndef MOVE_ROWS
+#define MOVE_ROWS 4
+#endif
+constexpr int kMoveThreads = 256, kMoveRows = MOVE_ROWS;
 
 // Fresh pages: a CTA moves kMoveRows rows per thread, all loads before the first store.
 __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const CompactParams p) {
@@ -320,97 +350,110 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const Compac
         if (dst[u] >= 0) s.pool[dst[u]] = x[u];
 }
 
-// In place: one CTA per strip walks the rows in order, kShiftRows rows per thread and
-// chunk, each thread copying its own pieces through its own slots of a ring.
-constexpr int kShiftThreads = 512, kShiftRows = 2, kShiftStages = 8;
-constexpr int kShiftSmem = kShiftStages * kShiftRows * kShiftThreads * 16;
+// In place.  grid (CTAs of a cluster, 2 Hkv, B): the cluster takes kShiftRows rows per
+// thread and CTA at a time, in order; each thread copies its own pieces through its own
+// slots of a ring.
+constexpr int kShiftThreads = 256, kShiftRows = 4, kShiftStages = 5;
+constexpr int kShiftPer = 16;                                   // chunks whose indices come together
+constexpr int kShiftBatch = kShiftPer * kShiftRows * kShiftThreads / 8;  // rows of 8 pieces or more
+constexpr int kShiftPages = 4096;                               // page ids kept in shared memory
+constexpr int kShiftRing = kShiftStages * kShiftRows * kShiftThreads * 16;
+constexpr int kShiftSmem = kShiftRing + 2 * kShiftBatch * 4 + kShiftPages * 4;
+static_assert(2 * (kShiftSmem + 1024) <= 233472, "two CTAs share an SM");
 
-__global__ void __launch_bounds__(kShiftThreads, 1) compact_shift_kernel(const CompactParams p) {
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__global__ void __launch_bounds__(kShiftThreads, 2) compact_shift_kernel(const CompactParams p) {
     extern __shared__ __align__(16) uint4 ring[];  // [stage][row][thread]
+    int32_t *kept = reinterpret_cast<int32_t *>(ring + kShiftRing / 16);  // [2][kShiftBatch]
+    int32_t *ids = kept + 2 * kShiftBatch;
     Strip s;
-    if (!strip_of(p, s)) return;
+    if (!strip_of(p, s)) return;  // the whole cluster alike
     constexpr int R = kShiftRows, S = kShiftStages;
+    const int tid = threadIdx.x;
     const int lp = 31 - __clz(p.P);
-    const int per = kShiftThreads >> p.lg_piece;
-    const int r = (int)threadIdx.x >> p.lg_piece;
+    const int per = kShiftThreads >> p.lg_piece;      // rows of a CTA at once
+    const int mine = per * R, step = mine * (int)gridDim.x;  // rows of a chunk: this CTA's, all
+    const int first = (int)blockIdx.x * mine;
     const int64_t ctx = (int64_t)p.max_pages * p.P;
-    const int64_t chunks = (s.n + (int64_t)per * R - 1) / (per * R);
-    auto row = [&](int64_t c, int u) { return c * (per * R) + u * per + r; };
-    // The index of a row (unchecked; -1: no such row), and the page ids of an index and of
-    // a row: each only used a chunk later.
-    auto index = [&](int64_t c, int (&t)[R]) {
-#pragma unroll
-        for (int u = 0; u < R; ++u) t[u] = row(c, u) < s.n ? s.kept[row(c, u)] : -1;
-    };
-    auto source = [&](int64_t c, int (&t)[R], int (&a)[R]) {
-#pragma unroll
-        for (int u = 0; u < R; ++u) {
-            if (row(c, u) < s.n && (t[u] < row(c, u) || t[u] >= ctx)) {
-                if (s.tells) record(p.status, ATLAS_DEV_BAD_SEQLEN);
-                t[u] = -1;
-            }
-            a[u] = t[u] >= 0 ? s.src_table[t[u] >> lp] : 0;
+    const int chunks = (s.n + step - 1) / step;
+    // Page ids from shared memory, or (tables too long for that) from memory.
+    const int32_t *table = s.src_table;
+    if (p.max_pages <= kShiftPages) {
+        for (int i = tid; i < p.max_pages; i += kShiftThreads) cp_async4(smem_u32(ids + i), table + i);
+        table = ids;
+    }
+    auto fetch = [&](int batch) {  // this CTA's indices of chunks [batch * kShiftPer, + kShiftPer)
+        for (int i = tid; i < kShiftPer * mine; i += kShiftThreads) {
+            const int64_t j = (int64_t)(batch * kShiftPer + i / mine) * step + first + i % mine;
+            if (j < s.n) cp_async4(smem_u32(kept + (batch & 1) * kShiftBatch + i), s.kept + j);
         }
     };
-    auto target = [&](int64_t c, int (&z)[R]) {
-#pragma unroll
-        for (int u = 0; u < R; ++u) z[u] = row(c, u) < s.n ? s.dst_table[row(c, u) >> lp] : -1;
-    };
     uint32_t moving = 0;  // bit (chunk % S) * R + u: that row is in the ring
-    auto load = [&](int64_t c, const int (&t)[R], const int (&a)[R]) {
+    auto load = [&](int c) {
+        const int slot = c % S;
+        const int32_t *index = kept + (c / kShiftPer & 1) * kShiftBatch + c % kShiftPer * mine;
+        moving &= ~(((1u << R) - 1u) << (slot * R));
 #pragma unroll
         for (int u = 0; u < R; ++u) {
-            const uint32_t bit = 1u << ((int)(c % S) * R + u);
-            moving &= ~bit;
-            if (t[u] < 0) continue;
-            if (a[u] < 0 || a[u] >= p.num_pages) {
+            const int in = u * per + (tid >> p.lg_piece);
+            const int64_t j = (int64_t)c * step + first + in;
+            if (j >= s.n) continue;
+            const int t = index[in];
+            if (t < j || t >= ctx) {
+                if (s.tells) record(p.status, ATLAS_DEV_BAD_SEQLEN);
+                continue;
+            }
+            if (t == j) continue;  // it is where it belongs
+            const int a = table[t >> lp], z = table[j >> lp];
+            if (a < 0 || a >= p.num_pages || z < 0 || z >= p.num_pages) {
                 if (s.tells) record(p.status, ATLAS_DEV_BAD_PAGE);
                 continue;
             }
-            if (t[u] == row(c, u)) continue;  // it is where it belongs
-            moving |= bit;
-            cp_async16(smem_u32(ring + ((int)(c % S) * R + u) * kShiftThreads + threadIdx.x),
-                       s.pool + slot_of(p, a[u], t[u]) + s.piece, 16);
+            moving |= 1u << (slot * R + u);
+            cp_async16(smem_u32(ring + (slot * R + u) * kShiftThreads + tid),
+                       s.pool + slot_of(p, a, t) + s.piece, 16);
         }
         cp_async_commit();
     };
+    fetch(0);
+    fetch(1);
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
     // Chunks 0 .. S - 2 are on their way before the first is written.
-    int t0[R], t1[R], a0[R], z0[R];
-    index(0, t0);
-    index(1, t1);
-    source(0, t0, a0);
 #pragma unroll 1
-    for (int64_t c = 0; c < S - 1; ++c) {
-        load(c, t0, a0);
-#pragma unroll
-        for (int u = 0; u < R; ++u) t0[u] = t1[u];
-        source(c + 1, t0, a0);
-        index(c + 2, t1);
-    }
-    target(0, z0);
+    for (int c = 0; c < S - 1; ++c) load(c);
+    cp_async_wait<S - 2>();
+    // The barrier only has to keep writes behind reads that have already delivered their
+    // data (cp.async has landed): relaxed arrivals, which do not wait for the writes of
+    // the chunk before (a release did, for most of the kernel's time).
+    cluster_arrive_relaxed();  // this thread has read chunk 0
 #pragma unroll 1
-    for (int64_t c = 0; c < chunks; ++c) {
-        load(c + S - 1, t0, a0);
-        int z1[R];
-        target(c + 1, z1);
-#pragma unroll
-        for (int u = 0; u < R; ++u) t0[u] = t1[u];
-        source(c + S, t0, a0);
-        index(c + S + 1, t1);
-        cp_async_wait<S - 1>();
-        __syncthreads();  // every thread has chunk c (and all before it) in the ring
+    for (int c = 0; c < chunks; ++c) {
+        // Where batch k of the indices begins, its fetch (kShiftPer chunks ago, long waited
+        // for by each thread) becomes visible to the CTA, every thread is done with batch
+        // k - 1, and batch k + 1 can be fetched over it.
+        const int next = c + S - 1;
+        if (next % kShiftPer == 0) {
+            __syncthreads();
+            fetch(next / kShiftPer + 1);
+        }
+        load(next);
+        cp_async_wait<S - 2>();  // chunk c + 1 is in the ring
+        cluster_wait();          // the whole cluster has read chunk c
+        cluster_arrive_relaxed();
+        const int slot = c % S;
 #pragma unroll
         for (int u = 0; u < R; ++u) {
-            const int at = (int)(c % S) * R + u;
-            if ((moving >> at) & 1u) {
-                if (z0[u] >= 0 && z0[u] < p.num_pages)
-                    s.pool[slot_of(p, z0[u], (int)row(c, u)) + s.piece] = ring[at * kShiftThreads + threadIdx.x];
-                else if (s.tells)
-                    record(p.status, ATLAS_DEV_BAD_PAGE);
-            }
-            z0[u] = z1[u];
+            if (!((moving >> (slot * R + u)) & 1u)) continue;
+            const int j = c * step + first + u * per + (tid >> p.lg_piece);
+            s.pool[slot_of(p, table[j >> lp], j) + s.piece] = ring[(slot * R + u) * kShiftThreads + tid];
         }
     }
+    cluster_wait();
     cp_async_wait<0>();
 }
 
@@ -443,8 +486,12 @@ atlas_status atlas_kv_select(const float *weights, const int32_t *seq_lens, int3
     p.new_lens = S->new_lens;
     p.kept_weights = S->kept_weights;
     p.status = S->status_word;
+    // More CTAs per row as long as one wave holds them all.
+    const int64_t rows = (int64_t)S->batch * n_kv_heads;
     int ctas = 1;
-    while (ctas < kSelMaxCtas && (int64_t)ctas * kSelKeys < p.row_tokens) ctas *= 2;
+    while (ctas < kSelMaxCtas && (int64_t)ctas * kSelKeys < p.row_tokens &&
+           (rows * ctas * 2 <= device_sm_count() || (int64_t)ctas * kSelCache / 4 < p.row_tokens))
+        ctas *= 2;
     const int64_t bytes = ((int64_t)p.row_tokens + ctas - 1) / ctas * 4;
     const bool cached = bytes <= kSelCache;
     auto kern = cached ? select_kernel<true> : select_kernel<false>;
@@ -505,8 +552,8 @@ atlas_status atlas_kv_compact(void *k_pages, void *v_pages, const int32_t *page_
     p.status = C->status_word;
     const cudaStream_t stream = static_cast<cudaStream_t>(C->stream);
     (void)cudaGetLastError();
+    p.lg_piece = p.vec == 8 ? 3 : p.vec == 16 ? 4 : 5;
     if (p.new_table) {
-        p.lg_piece = p.vec == 8 ? 3 : p.vec == 16 ? 4 : 5;  // whole rows
         const int rows = (kMoveThreads >> p.lg_piece) * kMoveRows;
         const dim3 grid((unsigned)((p.max_kept + rows - 1) / rows), (unsigned)(2 * n_kv_heads),
                         (unsigned)C->batch);
@@ -521,9 +568,26 @@ atlas_status atlas_kv_compact(void *k_pages, void *v_pages, const int32_t *page_
                 return ATLAS_ERR_CUDA;
             if (dev < 64) configured[dev] = 1;
         }
-        p.lg_piece = 2;  // 64-byte strips
-        const dim3 grid(1, (unsigned)(2 * n_kv_heads * (p.vec >> 2)), (unsigned)C->batch);
-        compact_shift_kernel<<<grid, kShiftThreads, kShiftSmem, stream>>>(p);
+        // As many CTAs per (sequence, kv head, pool) as fit at once (two to an SM, a few SMs
+        // lost to whole clusters), up to a cluster's 8 and to the rows there are.
+        const int64_t units = 2 * (int64_t)n_kv_heads * C->batch;
+        const int rows = (kShiftThreads >> p.lg_piece) * kShiftRows;
+        int ctas = 1;
+        while (ctas < 8 && units * ctas * 2 <= (int64_t)device_sm_count() * 15 / 8 &&
+               (int64_t)ctas * rows < p.max_kept)
+            ctas *= 2;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)ctas, (unsigned)(2 * n_kv_heads), (unsigned)C->batch);
+        cfg.blockDim = dim3(kShiftThreads, 1, 1);
+        cfg.dynamicSmemBytes = kShiftSmem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)ctas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, compact_shift_kernel, p) != cudaSuccess) return ATLAS_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }

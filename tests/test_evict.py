@@ -316,9 +316,9 @@ def moved(pool, table, to, kept, lens):
     table, to, kept = table.cpu(), to.cpu(), kept.cpu()
     for b, n in enumerate(lens):
         for g in range(pool.shape[1]):
-            for j in range(n):
-                t = int(kept[b, g, j])
-                out[int(to[b, j // P]), g, j % P] = pool[int(table[b, t // P]), g, t % P]
+            j, t = torch.arange(n), kept[b, g, :n].long()
+            src, dst = table[b, t // P].long(), to[b, j // P].long()
+            out[dst.cuda(), g, (j % P).cuda()] = pool[src.cuda(), g, (t % P).cuda()]
     return out
 
 
@@ -326,7 +326,9 @@ def moved(pool, table, to, kept, lens):
 @pytest.mark.parametrize("dtype,Hkv,D,P,lens,L", [
     ("bf16", 2, 128, 16, [100, 33, 0], 240), ("bf16", 1, 64, 64, [129, 1, 64], 192),
     ("f32", 2, 64, 8, [77, 80, 5], 80), ("f32", 1, 128, 128, [300, 2, 301], 640),
-    ("bf16", 1, 128, 8, [1500, 1499, 700], 2048)])
+    ("bf16", 1, 128, 8, [1500, 1499, 700], 2048),
+    ("bf16", 1, 64, 8, [900, 40, 0], 65600),                # a table of 8200 pages
+    ("bf16", 2, 64, 32, [20000, 8193, 4096], 24000)])       # several batches of indices
 @pytest.mark.parametrize("in_place", [False, True])
 def test_compact_moves_the_kept_rows(dtype, Hkv, D, P, lens, L, in_place):
     n = max(lens)
