@@ -62,6 +62,10 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+__device__ __forceinline__ float key_weight(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -96,7 +100,7 @@ __device__ __forceinline__ uint2 ld_cluster2(const uint32_t *local, int rank) {
 // else (rows too long for that) each pass reads the weights again.
 template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectParams p) {
-    extern __shared__ uint32_t cached[];
+    extern __shared__ __align__(16) uint32_t cached[];
     __shared__ __align__(8) uint32_t hist[2][kBins];
     __shared__ uint32_t found[2];                 // digit, keys above it
     __shared__ uint32_t warp_sum[kSelWarps];
@@ -140,7 +144,21 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
         fixed();
         return;
     }
-    auto key_of = [&](int i) { return CACHED ? cached[i] : order_key(w[s0 + i]); };
+    // Keys i .. i + 3 (i a multiple of 4); past the end 0, which `in` tells apart.
+    auto keys_of = [&](int i, bool (&in)[4]) {
+        uint4 k = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) in[e] = i + e < len;
+        if (CACHED) {
+            if (in[0]) k = *reinterpret_cast<const uint4 *>(cached + i);
+        } else {
+            if (in[0]) k.x = order_key(w[s0 + i]);
+            if (in[1]) k.y = order_key(w[s0 + i + 1]);
+            if (in[2]) k.z = order_key(w[s0 + i + 2]);
+            if (in[3]) k.w = order_key(w[s0 + i + 3]);
+        }
+        return k;
+    };
 
     uint32_t prefix = 0;
 #pragma unroll 1
@@ -173,15 +191,24 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
         } else {
             // Few keys match the digits found, or (many equal weights) whole warps do.
             const uint32_t known = ~0u << (d == 1 ? 21 : 10), mask = d == 1 ? 2047u : 1023u;
-            for (int i0 = 0; i0 < len; i0 += kSelThreads) {
-                const int i = i0 + tid;
-                const uint32_t k = i < len ? key_of(i) : ~prefix;
-                const bool votes = ((k ^ prefix) & known) == 0u;
-                if (!__any_sync(0xffffffffu, votes)) continue;
-                const uint32_t bin = (k >> shift) & mask;
-                int same;
-                __match_all_sync(0xffffffffu, votes ? bin : (uint32_t)kBins, &same);
-                if (votes && (!same || lane == 0)) atomicAdd(&h[bin], same ? 32u : 1u);
+            for (int i0 = 0; i0 < len; i0 += 4 * kSelThreads) {
+                bool in[4];
+                const uint4 k4 = keys_of(i0 + 4 * tid, in);
+                const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+                bool any = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    in[e] = in[e] && ((k[e] ^ prefix) & known) == 0u;
+                    any |= in[e];
+                }
+                if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t bin = (k[e] >> shift) & mask;
+                    int same;
+                    __match_all_sync(0xffffffffu, in[e] ? bin : (uint32_t)kBins, &same);
+                    if (in[e] && (!same || lane == 0)) atomicAdd(&h[bin], same ? 32u : 1u);
+                }
             }
         }
         cluster_barrier();
@@ -214,14 +241,17 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
         // digit's histogram only after the one after that, when every CTA has read it)
     }
     // Keys above `prefix` stay, and the first `want` equal to it.  A warp takes a
-    // contiguous part, 32 keys at a time in order.
-    const int part = ((len + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+    // contiguous part, 128 keys at a time, four consecutive ones to a lane.
+    const int part = ((len + kSelWarps - 1) / kSelWarps + 127) / 128 * 128;
     const int w0 = min(len, warp * part), w1 = min(len, w0 + part);
     uint32_t gt = 0, eq = 0;
-    for (int i = w0 + lane; i < w1; i += 32) {
-        const uint32_t k = key_of(i);
-        gt += k > prefix;
-        eq += k == prefix;
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+        bool in[4];
+        const uint4 k = keys_of(i0 + 4 * lane, in);
+        gt += (in[0] && k.x > prefix) + (in[1] && k.y > prefix) + (in[2] && k.z > prefix) +
+              (in[3] && k.w > prefix);
+        eq += (in[0] && k.x == prefix) + (in[1] && k.y == prefix) + (in[2] && k.z == prefix) +
+              (in[3] && k.w == prefix);
     }
     gt = __reduce_add_sync(0xffffffffu, gt);
     eq = __reduce_add_sync(0xffffffffu, eq);
@@ -249,21 +279,55 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
     eq_before = __reduce_add_sync(0xffffffffu, eq_before);
     cluster_arrive_relaxed();  // this thread has read what it needs of the others
     uint32_t at = (uint32_t)lo + gt_before + min(want, eq_before);
-    const uint32_t below = (1u << lane) - 1u;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < w1 ? key_of(i) : 0u;
-        const uint32_t eqs = __ballot_sync(0xffffffffu, i < w1 && k == prefix);
-        const bool keep = i < w1 && (k > prefix || (k == prefix &&
-                                                    eq_before + __popc(eqs & below) < want));
-        const uint32_t keeps = __ballot_sync(0xffffffffu, keep);
-        if (keep) {
-            const uint32_t j = at + __popc(keeps & below);
-            kept[j] = s0 + i;
-            if (kept_w) kept_w[j] = w[s0 + i];
+    // Exclusive sum over the lanes before this one, and the warp's total.
+    auto lanes_before = [&](uint32_t v, uint32_t &total) {
+        uint32_t sum = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += x;
         }
-        at += __popc(keeps);
-        eq_before += __popc(eqs);
+        total = __shfl_sync(0xffffffffu, sum, 31);
+        return sum - v;
+    };
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+        const int i = i0 + 4 * lane;
+        bool in[4];
+        const uint4 k4 = keys_of(i, in);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        bool same[4], keep[4];
+        uint32_t equals = 0, count = 0, total;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            same[e] = in[e] && k[e] == prefix;
+            equals += same[e];
+        }
+        if (__any_sync(0xffffffffu, equals != 0)) {  // ties, by index
+            uint32_t rank_eq = eq_before + lanes_before(equals, total);
+            eq_before += total;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (same[e]) same[e] = rank_eq++ < want;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            keep[e] = same[e] || (in[e] && k[e] > prefix);
+            count += keep[e];
+        }
+        uint32_t j = at + lanes_before(count, total);
+        at += total;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (!keep[e]) continue;
+            kept[j] = s0 + i + e;
+            if (kept_w) {
+                // the weight from its key, without another trip to memory, but for the
+                // keys that two weights share (0 and -0; NaN and -inf)
+                const float v = key_weight(k[e]);
+                kept_w[j] = v == 0.f || v == -INFINITY ? w[s0 + i + e] : v;
+            }
+            ++j;
+        }
     }
     fixed();
     cluster_wait();  // no CTA leaves while another may still read its counts
@@ -283,15 +347,12 @@ struct CompactParams {
 struct Strip {
     uint4 *pool;
     const int32_t *src_table, *dst_table, *kept;
-    int n, piece;  // rows of the compacted sequence; this thread's piece of each
-    bool tells;    // this thread reports what is wrong with its rows
+    int n;  // rows of the compacted sequence
 };
 
 // grid (.., 2 Hkv, B); false: nothing to move.
 __device__ __forceinline__ bool strip_of(const CompactParams &p, Strip &s) {
     const int b = blockIdx.z, g = (int)blockIdx.y % p.Hkv, kv = (int)blockIdx.y / p.Hkv;
-    s.piece = (int)threadIdx.x & (p.vec - 1);
-    s.tells = kv == 0 && s.piece == 0;
     s.pool = static_cast<uint4 *>(kv ? p.v_pages : p.k_pages) + (int64_t)g * p.P * p.vec;
     s.kept = p.kept + ((int64_t)b * p.Hkv + g) * p.max_kept;
     s.src_table = p.page_table + (int64_t)b * p.max_pages;
@@ -311,19 +372,18 @@ __device__ __forceinline__ int64_t slot_of(const CompactParams &p, int page, int
     return ((int64_t)page * p.Hkv * p.P + (t & (p.P - 1))) * p.vec;
 }
 
-#ifndef MOVE_ROWS
-#define MOVE_ROWS 4
-#endif
-constexpr int kMoveThreads = 256, kMoveRows = MOVE_ROWS;
+constexpr int kMoveThreads = 256, kMovePieces = 4, kMoveRows = 2;
 
-// Fresh pages: a CTA moves kMoveRows rows per thread, all loads before the first store.
+// Fresh pages: a thread moves kMovePieces pieces of kMoveRows rows, all loads before the
+// first store.
 __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const CompactParams p) {
     Strip s;
     if (!strip_of(p, s)) return;
-    const int lp = 31 - __clz(p.P);
-    const int per = kMoveThreads >> p.lg_piece;
-    const int j0 = (int)blockIdx.x * per * kMoveRows + ((int)threadIdx.x >> p.lg_piece);
-    uint4 x[kMoveRows];
+    const int lp = 31 - __clz(p.P), lg = p.lg_piece - 2;  // threads per row: vec / 4
+    const int per = kMoveThreads >> lg;
+    const int in_row = (int)threadIdx.x & ((1 << lg) - 1);
+    const int j0 = (int)blockIdx.x * per * kMoveRows + ((int)threadIdx.x >> lg);
+    uint4 x[kMoveRows][kMovePieces];
     int64_t dst[kMoveRows];
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u) {
@@ -339,25 +399,31 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const Compac
             if (a < 0 || a >= p.num_pages || z < 0 || z >= p.num_pages) {
                 bad = ATLAS_DEV_BAD_PAGE;
             } else {
-                x[u] = s.pool[slot_of(p, a, t) + s.piece];
-                dst[u] = slot_of(p, z, j) + s.piece;
+                const uint4 *src = s.pool + slot_of(p, a, t) + in_row;
+#pragma unroll
+                for (int k = 0; k < kMovePieces; ++k) x[u][k] = src[k << lg];
+                dst[u] = slot_of(p, z, j) + in_row;
             }
         }
-        if (bad && s.tells) record(p.status, bad);
+        if (bad && in_row == 0 && blockIdx.y < (unsigned)p.Hkv) record(p.status, bad);
     }
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u)
-        if (dst[u] >= 0) s.pool[dst[u]] = x[u];
+        if (dst[u] >= 0) {
+#pragma unroll
+            for (int k = 0; k < kMovePieces; ++k) s.pool[dst[u] + (k << lg)] = x[u][k];
+        }
 }
 
-// In place.  grid (CTAs of a cluster, 2 Hkv, B): the cluster takes kShiftRows rows per
-// thread and CTA at a time, in order; each thread copies its own pieces through its own
-// slots of a ring.
-constexpr int kShiftThreads = 256, kShiftRows = 4, kShiftStages = 5;
+// In place.  grid (CTAs of a cluster, 2 Hkv, B): the cluster takes one row per group of
+// vec / 4 threads and CTA at a time, in order; each thread copies its own four pieces of a
+// row through its own slots of a ring (with a row's index, page and address worked out for
+// every piece, the instructions took longer than the copies).
+constexpr int kShiftThreads = 256, kShiftPieces = 4, kShiftStages = 4;
 constexpr int kShiftPer = 16;                                   // chunks whose indices come together
-constexpr int kShiftBatch = kShiftPer * kShiftRows * kShiftThreads / 8;  // rows of 8 pieces or more
+constexpr int kShiftBatch = kShiftPer * kShiftThreads / 2;      // groups of 2 threads or more
 constexpr int kShiftPages = 4096;                               // page ids kept in shared memory
-constexpr int kShiftRing = kShiftStages * kShiftRows * kShiftThreads * 16;
+constexpr int kShiftRing = kShiftStages * kShiftPieces * kShiftThreads * 16;
 constexpr int kShiftSmem = kShiftRing + 2 * kShiftBatch * 4 + kShiftPages * 4;
 static_assert(2 * (kShiftSmem + 1024) <= 233472, "two CTAs share an SM");
 
@@ -366,19 +432,21 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
 }
 
 __global__ void __launch_bounds__(kShiftThreads, 2) compact_shift_kernel(const CompactParams p) {
-    extern __shared__ __align__(16) uint4 ring[];  // [stage][row][thread]
+    extern __shared__ __align__(16) uint4 ring[];  // [stage][piece][thread]
     int32_t *kept = reinterpret_cast<int32_t *>(ring + kShiftRing / 16);  // [2][kShiftBatch]
     int32_t *ids = kept + 2 * kShiftBatch;
     Strip s;
     if (!strip_of(p, s)) return;  // the whole cluster alike
-    constexpr int R = kShiftRows, S = kShiftStages;
+    constexpr int N = kShiftPieces, S = kShiftStages;
     const int tid = threadIdx.x;
     const int lp = 31 - __clz(p.P);
-    const int per = kShiftThreads >> p.lg_piece;      // rows of a CTA at once
-    const int mine = per * R, step = mine * (int)gridDim.x;  // rows of a chunk: this CTA's, all
+    const int lg = p.lg_piece - 2;                       // threads per row: vec / 4
+    const int mine = kShiftThreads >> lg, step = mine * (int)gridDim.x;  // rows of a chunk
+    const int group = tid >> lg, in_row = tid & ((1 << lg) - 1);
     const int first = (int)blockIdx.x * mine;
-    const int64_t ctx = (int64_t)p.max_pages * p.P;
+    const int ctx = p.max_pages * p.P;                   // below 2^30 (host)
     const int chunks = (s.n + step - 1) / step;
+    const bool tells = blockIdx.y < (unsigned)p.Hkv && in_row == 0;
     // Page ids from shared memory, or (tables too long for that) from memory.
     const int32_t *table = s.src_table;
     if (p.max_pages <= kShiftPages) {
@@ -391,30 +459,28 @@ __global__ void __launch_bounds__(kShiftThreads, 2) compact_shift_kernel(const C
             if (j < s.n) cp_async4(smem_u32(kept + (batch & 1) * kShiftBatch + i), s.kept + j);
         }
     };
-    uint32_t moving = 0;  // bit (chunk % S) * R + u: that row is in the ring
-    auto load = [&](int c) {
-        const int slot = c % S;
-        const int32_t *index = kept + (c / kShiftPer & 1) * kShiftBatch + c % kShiftPer * mine;
-        moving &= ~(((1u << R) - 1u) << (slot * R));
-#pragma unroll
-        for (int u = 0; u < R; ++u) {
-            const int in = u * per + (tid >> p.lg_piece);
-            const int64_t j = (int64_t)c * step + first + in;
-            if (j >= s.n) continue;
-            const int t = index[in];
+    uint32_t moving = 0;  // bit `slot`: that row is in the ring
+    // Sends for chunk c, into slot c % S of the ring.
+    auto load = [&](int c, int slot) {
+        moving &= ~(1u << slot);
+        const int64_t j = (int64_t)c * step + first + group;
+        const int t = j < s.n ? kept[(c / kShiftPer & 1) * kShiftBatch + c % kShiftPer * mine + group] : 0;
+        if (j < s.n && t != j) {  // (t == j: it is where it belongs)
             if (t < j || t >= ctx) {
-                if (s.tells) record(p.status, ATLAS_DEV_BAD_SEQLEN);
-                continue;
+                if (tells) record(p.status, ATLAS_DEV_BAD_SEQLEN);
+            } else {
+                const int a = table[t >> lp], z = table[(int)j >> lp];
+                if (a < 0 || a >= p.num_pages || z < 0 || z >= p.num_pages) {
+                    if (tells) record(p.status, ATLAS_DEV_BAD_PAGE);
+                } else {
+                    moving |= 1u << slot;
+                    const uint4 *src = s.pool + slot_of(p, a, t) + in_row;
+                    const uint32_t dst = smem_u32(ring + slot * N * kShiftThreads + tid);
+#pragma unroll
+                    for (int k = 0; k < N; ++k)
+                        cp_async16(dst + k * kShiftThreads * 16, src + (k << lg), 16);
+                }
             }
-            if (t == j) continue;  // it is where it belongs
-            const int a = table[t >> lp], z = table[j >> lp];
-            if (a < 0 || a >= p.num_pages || z < 0 || z >= p.num_pages) {
-                if (s.tells) record(p.status, ATLAS_DEV_BAD_PAGE);
-                continue;
-            }
-            moving |= 1u << (slot * R + u);
-            cp_async16(smem_u32(ring + (slot * R + u) * kShiftThreads + tid),
-                       s.pool + slot_of(p, a, t) + s.piece, 16);
         }
         cp_async_commit();
     };
@@ -425,12 +491,13 @@ __global__ void __launch_bounds__(kShiftThreads, 2) compact_shift_kernel(const C
     __syncthreads();
     // Chunks 0 .. S - 2 are on their way before the first is written.
 #pragma unroll 1
-    for (int c = 0; c < S - 1; ++c) load(c);
+    for (int c = 0; c < S - 1; ++c) load(c, c);
     cp_async_wait<S - 2>();
     // The barrier only has to keep writes behind reads that have already delivered their
     // data (cp.async has landed): relaxed arrivals, which do not wait for the writes of
     // the chunk before (a release did, for most of the kernel's time).
     cluster_arrive_relaxed();  // this thread has read chunk 0
+    int slot = 0, ahead = S - 1;  // the slots of chunks c and c + S - 1
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
         // Where batch k of the indices begins, its fetch (kShiftPer chunks ago, long waited
@@ -441,17 +508,19 @@ __global__ void __launch_bounds__(kShiftThreads, 2) compact_shift_kernel(const C
             __syncthreads();
             fetch(next / kShiftPer + 1);
         }
-        load(next);
+        load(next, ahead);
         cp_async_wait<S - 2>();  // chunk c + 1 is in the ring
         cluster_wait();          // the whole cluster has read chunk c
         cluster_arrive_relaxed();
-        const int slot = c % S;
+        if ((moving >> slot) & 1u) {
+            const int j = c * step + first + group;
+            uint4 *dst = s.pool + slot_of(p, table[j >> lp], j) + in_row;
+            const uint4 *src = ring + slot * N * kShiftThreads + tid;
 #pragma unroll
-        for (int u = 0; u < R; ++u) {
-            if (!((moving >> (slot * R + u)) & 1u)) continue;
-            const int j = c * step + first + u * per + (tid >> p.lg_piece);
-            s.pool[slot_of(p, table[j >> lp], j) + s.piece] = ring[(slot * R + u) * kShiftThreads + tid];
+            for (int k = 0; k < N; ++k) dst[k << lg] = src[k * kShiftThreads];
         }
+        slot = slot + 1 == S ? 0 : slot + 1;
+        ahead = ahead + 1 == S ? 0 : ahead + 1;
     }
     cluster_wait();
     cp_async_wait<0>();
@@ -492,7 +561,7 @@ atlas_status atlas_kv_select(const float *weights, const int32_t *seq_lens, int3
     while (ctas < kSelMaxCtas && (int64_t)ctas * kSelKeys < p.row_tokens &&
            (rows * ctas * 2 <= device_sm_count() || (int64_t)ctas * kSelCache / 4 < p.row_tokens))
         ctas *= 2;
-    const int64_t bytes = ((int64_t)p.row_tokens + ctas - 1) / ctas * 4;
+    const int64_t bytes = (((int64_t)p.row_tokens + ctas - 1) / ctas + 3) / 4 * 16;
     const bool cached = bytes <= kSelCache;
     auto kern = cached ? select_kernel<true> : select_kernel<false>;
     static int configured[64] = {0};
@@ -554,7 +623,7 @@ atlas_status atlas_kv_compact(void *k_pages, void *v_pages, const int32_t *page_
     (void)cudaGetLastError();
     p.lg_piece = p.vec == 8 ? 3 : p.vec == 16 ? 4 : 5;
     if (p.new_table) {
-        const int rows = (kMoveThreads >> p.lg_piece) * kMoveRows;
+        const int rows = (kMoveThreads >> (p.lg_piece - 2)) * kMoveRows;
         const dim3 grid((unsigned)((p.max_kept + rows - 1) / rows), (unsigned)(2 * n_kv_heads),
                         (unsigned)C->batch);
         compact_move_kernel<<<grid, kMoveThreads, 0, stream>>>(p);
@@ -571,7 +640,7 @@ atlas_status atlas_kv_compact(void *k_pages, void *v_pages, const int32_t *page_
         // As many CTAs per (sequence, kv head, pool) as fit at once (two to an SM, a few SMs
         // lost to whole clusters), up to a cluster's 8 and to the rows there are.
         const int64_t units = 2 * (int64_t)n_kv_heads * C->batch;
-        const int rows = (kShiftThreads >> p.lg_piece) * kShiftRows;
+        const int rows = kShiftThreads >> (p.lg_piece - 2);
         int ctas = 1;
         while (ctas < 8 && units * ctas * 2 <= (int64_t)device_sm_count() * 15 / 8 &&
                (int64_t)ctas * rows < p.max_kept)

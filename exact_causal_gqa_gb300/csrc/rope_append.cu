@@ -15,12 +15,18 @@
 // int32 position and |f_p| <= 1.  The top two bits (rounded) give the quadrant and the
 // rest an angle within an eighth of a turn, for sincospif.
 //
-// What bounds it: memory, (read + write) of every row of q, k and v once.  A thread owns
-// one token and one slot of its rows -- V pairs, i.e. two vectors of V elements (16 bytes
-// each at V = 8 bf16) -- computes those V sines and cosines once and walks heads with
-// them, kUnroll rows in flight.  Consecutive threads take consecutive slots of a row, so
-// a warp reads and writes whole rows.  Few tokens (a decode step) leave too few threads
-// for that: the heads are then shared between CTAs (grid.y), each redoing the angles.
+// What bounds it: memory, (read + write) of every row of q, k and v once.  A CTA takes
+// kMaxTokens neighbouring tokens: it puts their cosines and sines (shared by all heads)
+// and row offsets into shared memory once, then its threads walk the tokens' rows, one
+// slot -- V pairs, i.e. two vectors of V elements, 16 bytes each at V = 8 bf16 -- of one
+// head at a time.  Consecutive threads take consecutive slots, then heads, so a fused
+// projection is read front to back.  With 32 registers a thread, all 2048 threads of an
+// SM have their two loads in flight; more slots in flight per thread cost that occupancy
+// and were slower, as were angles held in registers.  4 x 8192 tokens of 32 + 8 + 8 heads
+// of 128 bf16 (806 MB): 125 us, 6.4 TB/s (95 % of the measured copy); 2 slots a thread
+// 149 us, a slot of one token for all heads per thread 197 us; 1, 4, 8, 16, 32 tokens
+// per CTA 139, 128, 133, 143, 169 us.  Few tokens (a decode step) leave too few CTAs: the
+// heads are then shared between CTAs (grid.y).
 #include "internal.h"
 
 #include <cuda_bf16.h>
@@ -30,7 +36,7 @@ namespace atlas {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
+constexpr int kMaxTokens = 2;
 constexpr int kMaxPairs = 64;  // head_dim 128 / 2
 
 struct RopeParams {
@@ -41,7 +47,7 @@ struct RopeParams {
     int32_t B, Hq, Hkv, D, P, n, max_pages, num_pages;
     int32_t pairs;                // rotated pairs of a row; the D - 2 pairs others are copied
     int32_t interleaved;
-    int32_t heads_per_cta;
+    int32_t tokens_per_cta, heads_per_cta;
     uint32_t *status;
     uint64_t turn[kMaxPairs];     // f_p / 2 pi mod 1, times 2^64
     uint8_t axis[kMaxPairs];
@@ -51,6 +57,24 @@ template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
     T e[V];
 };
+
+// One access of the whole vector (16 bytes as uint4: a struct copy became narrower ones).
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load_vec(const T *p) {
+    Vec<T, V> x;
+    if constexpr (sizeof(x) == 16)
+        *reinterpret_cast<uint4 *>(&x) = *reinterpret_cast<const uint4 *>(p);
+    else
+        x = *reinterpret_cast<const Vec<T, V> *>(p);
+    return x;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T *p, const Vec<T, V> &x) {
+    if constexpr (sizeof(x) == 16)
+        *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(&x);
+    else
+        *reinterpret_cast<Vec<T, V> *>(p) = x;
+}
 
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -74,127 +98,129 @@ __device__ __forceinline__ void cos_sin_turns(uint64_t turn, float &c, float &s)
     s = (quarter & 2) ? -b : b;
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
-    const int lg_slots = 30 - __clz(p.D) - (V == 8 ? 3 : V == 4 ? 2 : V == 2 ? 1 : 0);
-    const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;  // slots: D / (2 V)
-    const int64_t token = at >> lg_slots;
-    if (token >= (int64_t)p.B * p.n) return;
-    const int slot = (int)at & ((1 << lg_slots) - 1);
-    const int b = (int32_t)token / p.n, j = (int32_t)token % p.n;  // B * n < 2^31
-    const int count = p.n_new ? p.n_new[b] : p.n;
-    if (count < 0 || count > p.n) {
-        if (j == 0 && slot == 0 && blockIdx.y == 0 && p.status)
-            atomicOr(p.status, ATLAS_DEV_BAD_SEQLEN);
-        return;
-    }
-    if (j >= count) return;
-    const int h0 = (int)blockIdx.y * p.heads_per_cta;
-    const int heads = p.Hq + 2 * p.Hkv;
-    const int h1 = min(heads, h0 + p.heads_per_cta);
+// Element offsets of a token's rows of head 0; cache < 0: no slot (reported).
+struct TokenRows {
+    int64_t q, k, v, q_out, cache;
+    bool any;  // a real token
+};
 
-    // The two vectors of this slot: pairs V slot .. V slot + V - 1, or (past the rotated
-    // part, which V divides too) two vectors of the elements that are only copied.
-    const int pair0 = slot * V;
-    const bool turns = pair0 < p.pairs;
-    int e0, e1;
-    if (turns && !p.interleaved) {
-        e0 = pair0;
-        e1 = pair0 + p.pairs;
-    } else {
-        e0 = 2 * pair0;
-        e1 = e0 + V;
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const __grid_constant__ RopeParams p) {
+    __shared__ __align__(16) float cs[kMaxTokens][2][kMaxPairs];  // cosines, sines
+    __shared__ TokenRows rows[kMaxTokens];
+    const int token0 = (int)blockIdx.x * p.tokens_per_cta;
+    const int tokens = min(p.tokens_per_cta, p.B * p.n - token0);  // B * n < 2^31
+    const int h0 = (int)blockIdx.y * p.heads_per_cta;
+    const int h1 = min(p.Hq + 2 * p.Hkv, h0 + p.heads_per_cta);
+
+    for (int i = threadIdx.x; i < tokens * p.pairs && h0 < p.Hq + p.Hkv; i += kThreads) {
+        const int k = i / p.pairs, pair = i - k * p.pairs;
+        const int32_t pos = p.positions[(int64_t)p.axis[pair] * p.B * p.n + token0 + k];
+        cos_sin_turns((uint64_t)(int64_t)pos * p.turn[pair], cs[k][0][pair], cs[k][1][pair]);
     }
-    float c[V], s[V];
-    if (turns && h0 < p.Hq + p.Hkv) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int32_t pos = p.positions[((int64_t)p.axis[pair0 + i] * p.B + b) * p.n + j];
-            cos_sin_turns((uint64_t)(int64_t)pos * p.turn[pair0 + i], c[i], s[i]);
-        }
-    }
-    // The cache slot of this token; -1: nowhere (reported).
-    int64_t cache = -1;
-    if (h1 > p.Hq) {
-        const int64_t t = (int64_t)p.seq_lens[b] + j;
-        uint32_t bad = ATLAS_DEV_BAD_SEQLEN;
-        if (t >= 0 && t < (int64_t)p.max_pages * p.P) {
-            const int lp = 31 - __clz(p.P);  // page_tokens is a power of two
-            const int page = p.page_table[(int64_t)b * p.max_pages + (t >> lp)];
-            bad = page < 0 || page >= p.num_pages ? ATLAS_DEV_BAD_PAGE : 0u;
-            if (!bad) cache = ((int64_t)page * p.Hkv * p.P + (t & (p.P - 1))) * p.D;
-        }
-        if (bad && slot == 0 && p.status) atomicOr(p.status, bad);
-    }
-    using X = Vec<T, V>;
-    for (int h = h0; h < h1; h += kUnroll) {
-        X x0[kUnroll], x1[kUnroll];
-        T *dst[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            dst[u] = nullptr;
-            const int hh = h + u;
-            if (hh >= h1) continue;
-            const T *src;
-            if (hh < p.Hq) {
-                src = static_cast<const T *>(p.q) + b * p.qs[0] + hh * p.qs[1] + j * p.qs[2];
-                dst[u] = static_cast<T *>(p.q_out) + (((int64_t)b * p.Hq + hh) * p.n + j) * p.D;
+    if ((int)threadIdx.x < tokens) {
+        const int b = (token0 + (int)threadIdx.x) / p.n, j = (token0 + (int)threadIdx.x) % p.n;
+        const int count = p.n_new ? p.n_new[b] : p.n;
+        uint32_t bad = 0;
+        TokenRows r;
+        r.any = count >= 0 && count <= p.n && j < count;
+        if (count < 0 || count > p.n) bad = ATLAS_DEV_BAD_SEQLEN;
+        r.q = b * p.qs[0] + j * p.qs[2];
+        r.k = b * p.ks[0] + j * p.ks[2];
+        r.v = b * p.vs[0] + j * p.vs[2];
+        r.q_out = ((int64_t)b * p.Hq * p.n + j) * p.D;
+        r.cache = -1;
+        if (r.any && h1 > p.Hq) {
+            const int64_t t = (int64_t)p.seq_lens[b] + j;
+            if (t < 0 || t >= (int64_t)p.max_pages * p.P) {
+                bad = ATLAS_DEV_BAD_SEQLEN;
             } else {
-                const bool is_k = hh < p.Hq + p.Hkv;
-                const int g = hh - p.Hq - (is_k ? 0 : p.Hkv);
-                if (cache < 0) continue;
-                src = is_k ? static_cast<const T *>(p.k_new) + b * p.ks[0] + g * p.ks[1] + j * p.ks[2]
-                           : static_cast<const T *>(p.v_new) + b * p.vs[0] + g * p.vs[1] + j * p.vs[2];
-                dst[u] = static_cast<T *>(is_k ? p.k_pages : p.v_pages) + cache +
-                         (int64_t)g * p.P * p.D;
+                const int lp = 31 - __clz(p.P);  // page_tokens is a power of two
+                const int page = p.page_table[(int64_t)b * p.max_pages + (t >> lp)];
+                if (page < 0 || page >= p.num_pages) bad = ATLAS_DEV_BAD_PAGE;
+                else r.cache = ((int64_t)page * p.Hkv * p.P + (t & (p.P - 1))) * p.D;
             }
-            x0[u] = *reinterpret_cast<const X *>(src + e0);
-            x1[u] = *reinterpret_cast<const X *>(src + e1);
         }
+        if (bad && p.status) atomicOr(p.status, bad);
+        rows[threadIdx.x] = r;
+    }
+    __syncthreads();
+
+    // Item: slot `slot` of head h0 + item / slots of token `k`; D / (2 V) slots a row.
+    using X = Vec<T, V>;
+    const int lg_slots = 30 - __clz(p.D) - (V == 8 ? 3 : V == 4 ? 2 : V == 2 ? 1 : 0);
+    const int per_token = (h1 - h0) << lg_slots;
+    for (int k = 0, item = threadIdx.x;; item += kThreads) {
+        while (k < tokens && item >= per_token) {
+            item -= per_token;
+            ++k;
+        }
+        if (k >= tokens) break;
+        const TokenRows &r = rows[k];
+        const int h = h0 + (item >> lg_slots), slot = item & ((1 << lg_slots) - 1);
+        if (!r.any || (h >= p.Hq && r.cache < 0)) continue;
+        const T *src;
+        T *dst;
+        if (h < p.Hq) {
+            src = static_cast<const T *>(p.q) + r.q + h * p.qs[1];
+            dst = static_cast<T *>(p.q_out) + r.q_out + (int64_t)h * p.n * p.D;
+        } else if (h < p.Hq + p.Hkv) {
+            src = static_cast<const T *>(p.k_new) + r.k + (h - p.Hq) * p.ks[1];
+            dst = static_cast<T *>(p.k_pages) + r.cache + (int64_t)(h - p.Hq) * p.P * p.D;
+        } else {
+            src = static_cast<const T *>(p.v_new) + r.v + (h - p.Hq - p.Hkv) * p.vs[1];
+            dst = static_cast<T *>(p.v_pages) + r.cache + (int64_t)(h - p.Hq - p.Hkv) * p.P * p.D;
+        }
+        // The slot's two vectors: of its pairs, or (past the rotated part, which V divides
+        // too) of the elements that are only copied.
+        const int pair0 = slot * V;
+        const bool turned = pair0 < p.pairs;
+        const int e0 = turned && !p.interleaved ? pair0 : 2 * pair0;
+        const int e1 = turned && !p.interleaved ? pair0 + p.pairs : e0 + V;
+        X x0 = load_vec<T, V>(src + e0), x1 = load_vec<T, V>(src + e1);
+        if (turned && h < p.Hq + p.Hkv) {
+            const float *c = cs[k][0] + pair0, *s = cs[k][1] + pair0;
+            X y0, y1;
+            if (!p.interleaved) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (!dst[u]) continue;
-            if (turns && h + u < p.Hq + p.Hkv) {
-                X y0, y1;
-                if (!p.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float x = widen(x0[u].e[i]), y = widen(x1[u].e[i]);
-                        y0.e[i] = narrow<T>(x * c[i] - y * s[i]);
-                        y1.e[i] = narrow<T>(y * c[i] + x * s[i]);
-                    }
-                } else {
-                    // x0 and x1 hold 2 V consecutive elements: pair i at 2i, 2i + 1
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const T &ex = 2 * i < V ? x0[u].e[2 * i % V] : x1[u].e[2 * i % V];
-                        const T &ey = 2 * i + 1 < V ? x0[u].e[(2 * i + 1) % V]
-                                                    : x1[u].e[(2 * i + 1) % V];
-                        const float x = widen(ex), y = widen(ey);
-                        (2 * i < V ? y0 : y1).e[2 * i % V] = narrow<T>(x * c[i] - y * s[i]);
-                        (2 * i + 1 < V ? y0 : y1).e[(2 * i + 1) % V] = narrow<T>(y * c[i] + x * s[i]);
-                    }
+                for (int i = 0; i < V; ++i) {
+                    const float x = widen(x0.e[i]), y = widen(x1.e[i]);
+                    y0.e[i] = narrow<T>(x * c[i] - y * s[i]);
+                    y1.e[i] = narrow<T>(y * c[i] + x * s[i]);
                 }
-                x0[u] = y0;
-                x1[u] = y1;
+            } else {
+                // x0 and x1 hold 2 V consecutive elements: pair i at 2i, 2i + 1
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float x = widen(2 * i < V ? x0.e[2 * i % V] : x1.e[2 * i % V]);
+                    const float y = widen(2 * i + 1 < V ? x0.e[(2 * i + 1) % V] : x1.e[(2 * i + 1) % V]);
+                    (2 * i < V ? y0 : y1).e[2 * i % V] = narrow<T>(x * c[i] - y * s[i]);
+                    (2 * i + 1 < V ? y0 : y1).e[(2 * i + 1) % V] = narrow<T>(y * c[i] + x * s[i]);
+                }
             }
-            *reinterpret_cast<X *>(dst[u] + e0) = x0[u];
-            *reinterpret_cast<X *>(dst[u] + e1) = x1[u];
+            x0 = y0;
+            x1 = y1;
         }
+        store_vec<T, V>(dst + e0, x0);
+        store_vec<T, V>(dst + e1, x1);
     }
 }
 
 template <typename T, int V>
 cudaError_t launch(RopeParams &p, cudaStream_t stream) {
-    const int64_t threads = (int64_t)p.B * p.n * (p.D / (2 * V));
+    const int64_t tokens = (int64_t)p.B * p.n;
     const int heads = p.Hq + 2 * p.Hkv;
-    // As many head groups as it takes to give every SM its 2048 threads.
-    const int64_t want = (int64_t)device_sm_count() * 2048;
-    int64_t groups = (want + threads - 1) / threads;
-    if (groups > heads) groups = heads;
+    // kMaxTokens tokens per CTA while that leaves eight CTAs for each SM; with fewer
+    // than that of single tokens, the heads in as many groups as it takes.
+    const int64_t want = (int64_t)device_sm_count() * 8;
+    p.tokens_per_cta = tokens >= want * kMaxTokens ? kMaxTokens : 1;
+    const int64_t ctas = (tokens + p.tokens_per_cta - 1) / p.tokens_per_cta;
+    int64_t groups = (want + ctas - 1) / ctas;
+    // (a group has at least one item for each thread)
+    const int64_t most = ((int64_t)heads * (p.D / (2 * V)) + kThreads - 1) / kThreads;
+    if (groups > most) groups = most;
     p.heads_per_cta = (int)((heads + groups - 1) / groups);
-    const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads),
-                    (unsigned)((heads + p.heads_per_cta - 1) / p.heads_per_cta));
+    const dim3 grid((unsigned)ctas, (unsigned)((heads + p.heads_per_cta - 1) / p.heads_per_cta));
     rope_append_kernel<T, V><<<grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
@@ -241,10 +267,9 @@ extern "C" atlas_status atlas_kv_append_rope(const void *k_new, const void *v_ne
     if (R->n_axes < 1 || R->n_axes > ATLAS_ROPE_MAX_AXES || R->rot_dim < 2 || R->rot_dim % 2 ||
         R->rot_dim > head_dim || (R->interleaved != 0 && R->interleaved != 1))
         return ATLAS_ERR_INVALID_ARG;
-    // the kernel's index limits: tokens in 32 bits, (token, head) rows of q_out below 2^31
+    // the kernel's index limits: tokens and a token's slots in 32 bits
     const int64_t heads = (int64_t)R->n_q_heads + 2 * (int64_t)n_kv_heads;
-    if ((int64_t)R->batch * R->max_new * (head_dim / 2) >= (int64_t)INT32_MAX * 256 ||
-        (int64_t)R->batch * R->max_new >= INT32_MAX || heads > 65535)
+    if ((int64_t)R->batch * R->max_new >= INT32_MAX - kMaxTokens || heads > 65535)
         return ATLAS_ERR_INVALID_ARG;
 
     RopeParams p{};
