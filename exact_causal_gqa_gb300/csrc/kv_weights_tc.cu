@@ -142,14 +142,14 @@ __global__ void __launch_bounds__(StreamCfg<D, N>::kThreads, StreamCfg<D, N>::kC
     using C = StreamCfg<D, N>;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // aligned by an offset: the compiler still sees shared memory, not a generic address
+    uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     const uint32_t sb = smem_u32(smem);
     float *nlse = reinterpret_cast<float *>(smem + C::OFF_LSE);
     int *lim = reinterpret_cast<int *>(smem + C::OFF_LIM);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_TMEM + 8);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int b = blockIdx.z, hkv = blockIdx.y;
 #define BAR(i) (sb + C::OFF_BAR + 8u * (uint32_t)(i))
     const int L = p.seq_lens[b];
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(StreamCfg<D, N>::kThreads, StreamCfg<D, N>::kC
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     bool failed = false;
 
     if (warp == 0) {
@@ -241,28 +241,29 @@ __global__ void __launch_bounds__(StreamCfg<D, N>::kThreads, StreamCfg<D, N>::kC
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            const uint32_t idesc = idesc_bf16_f32(128, nmma, false);
-            bool ok = true;
-            for (int j = 0; ok && j < tiles; ++j) {
-                const int s = j % S, buf = j & 1;
-                ok = mbar_wait_bounded(BAR(C::B_FULL + s), (j / S) & 1, abort_flag, kWaitLimitNs) &&
-                     (j < 2 || mbar_wait_bounded(BAR(C::B_SEMPTY + buf), ((j >> 1) - 1) & 1,
-                                                 abort_flag, kWaitLimitNs));
-                if (!ok) break;
-                tc_fence_after();
+        const uint32_t idesc = idesc_bf16_f32(128, nmma, false);
+        bool ok = true;
+        for (int j = 0; ok && j < tiles; ++j) {
+            const int s = j % S, buf = j & 1;
+            ok = wait_warp(BAR(C::B_FULL + s), (j / S) & 1, abort_flag) &&
+                 (j < 2 || wait_warp(BAR(C::B_SEMPTY + buf), ((j >> 1) - 1) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
                 issue_scores<D>(tmem + buf * N, sb + s * C::kTile, sb + C::OFF_Q, N * 128, idesc);
                 umma_commit(BAR(C::B_EMPTY + s));
                 umma_commit(BAR(C::B_SFULL + buf));
             }
-            if (!ok) {
-                failed = true;
-                *abort_flag = 1;
-            }
-            umma_commit(BAR(C::B_FINAL));  // every MMA is done before TMEM is released
-            int no_abort = 0;
-            mbar_wait_bounded(BAR(C::B_FINAL), 0, &no_abort, kWaitLimitNs);
+            __syncwarp();
         }
+        if (!ok) {
+            failed = true;
+            *abort_flag = 1;
+        }
+        // every MMA is done before TMEM is released
+        if (elect_one()) umma_commit(BAR(C::B_FINAL));
+        int no_abort = 0;
+        mbar_wait_bounded(BAR(C::B_FINAL), 0, &no_abort, kWaitLimitNs);
         __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ epilogue
@@ -331,7 +332,8 @@ struct TileCfg {
     static constexpr int OFF_Q = kTiles * kTile;
     static constexpr int OFF_LSE = OFF_Q + kStages * kTile;    // [kStages][128]
     static constexpr int OFF_LIM = OFF_LSE + kStages * BT * 4;  // [kStages][128]
-    static constexpr int OFF_BAR = OFF_LIM + kStages * BT * 4;
+    static constexpr int OFF_INFO = OFF_LIM + kStages * BT * 4;  // [kStages] TileInfo
+    static constexpr int OFF_BAR = OFF_INFO + kStages * 16;
     static constexpr int B_K = 0;
     static constexpr int B_QFULL = B_K + kTiles;
     static constexpr int B_QEMPTY = B_QFULL + kStages;
@@ -346,10 +348,16 @@ struct TileCfg {
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
+// Whether rows of which the earliest sees keys below lim_min and the latest keys below
+// lim_max see one of [k0, k0 + keys).
+__device__ __forceinline__ bool sees(const WeightsParams &p, int lim_min, int lim_max, int k0, int keys) {
+    return k0 < lim_max && (p.window == 0 || k0 + keys > lim_min - p.window);
+}
+
 // The query tiles first .. end - 1 of a (sequence, kv head) that have a row which sees a
 // key of [kb, kb + kGroupKeys), in order: rows 128 j .. 128 j + 127 of its G * q_len
-// (q head, row) pairs, and the keys their real rows see.  Every role of the kernel walks
-// the same list.
+// (q head, row) pairs, and the keys their real rows see.  The producer, the MMA warp and
+// the warp that brings the columns each walk this list.
 struct QueryTiles {
     const WeightsParams &p;
     const int L, qn, kb, end;
@@ -386,10 +394,16 @@ struct QueryTiles {
             return true;
         }
     }
-    // Whether a row of the tile sees a key of [k0, k0 + keys).
     __device__ __forceinline__ bool seen(int k0, int keys) const {
-        return k0 < lim_max && (p.window == 0 || k0 + keys > lim_min - p.window);
+        return sees(p, lim_min, lim_max, k0, keys);
     }
+};
+
+// What the epilogue needs to know of a query tile, worked out once by the warp that
+// brings its columns.
+struct __align__(16) TileInfo {
+    int lim_min, lim_max;  // as in QueryTiles
+    int whole, stop;       // stop: no tile, the list has ended
 };
 
 // grid: items, the key groups of every (sequence, kv head) in ascending order (under a
@@ -401,12 +415,12 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
     using C = TileCfg<D>;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // aligned by an offset: the compiler still sees shared memory, not a generic address
+    uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     const uint32_t sb = smem_u32(smem);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_TMEM + 8);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
 #define BAR(i) (sb + C::OFF_BAR + 8u * (uint32_t)(i))
     const int units = p.B * p.Hkv;
     const int part = (int)(blockIdx.x % (unsigned)p.n_parts);
@@ -451,7 +465,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     bool failed = false;
     QueryTiles q(p, L, qn, kb0, q_begin, q_end);
     if (warp == 0) {
@@ -496,65 +510,73 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false);
-            bool ok = true;
-            int used[kTiles] = {0, 0, 0, 0};  // products so far of each key tile
-            while (ok && q.next()) {
-                const int s = q.n % S;
-                ok = mbar_wait_bounded(BAR(C::B_QFULL + s), (q.n / S) & 1, abort_flag, kWaitLimitNs);
-                if (!ok) break;
+        constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false);
+        bool ok = true;
+        int used[kTiles] = {0, 0, 0, 0};  // products so far of each key tile
+        while (ok && q.next()) {
+            const int s = q.n % S;
+            ok = wait_warp(BAR(C::B_QFULL + s), (q.n / S) & 1, abort_flag);
+            if (!ok) break;
 #pragma unroll
-                for (int x = 0; x < kTiles; ++x) {
-                    if (!ok || x >= ktiles || !q.seen(kb0 + x * BT, BT)) continue;
-                    if (used[x] == 0)
-                        ok = mbar_wait_bounded(BAR(C::B_K + x), 0, abort_flag, kWaitLimitNs);
-                    else
-                        ok = mbar_wait_bounded(BAR(C::B_SEMPTY + x), (used[x] - 1) & 1, abort_flag,
-                                               kWaitLimitNs);
-                    if (!ok) continue;
-                    tc_fence_after();
+            for (int x = 0; x < kTiles; ++x) {
+                if (!ok || x >= ktiles || !q.seen(kb0 + x * BT, BT)) continue;
+                ok = used[x] == 0 ? wait_warp(BAR(C::B_K + x), 0, abort_flag)
+                                  : wait_warp(BAR(C::B_SEMPTY + x), (used[x] - 1) & 1, abort_flag);
+                if (!ok) continue;
+                tc_fence_after();
+                if (elect_one()) {
                     issue_scores<D>(tmem + x * BT, sb + x * C::kTile, sb + C::OFF_Q + s * C::kTile,
                                     kSlab, idesc);
                     umma_commit(BAR(C::B_SFULL + x));
-                    ++used[x];
                 }
-                umma_commit(BAR(C::B_QEMPTY + s));
+                __syncwarp();
+                ++used[x];
             }
-            if (!ok) {
-                failed = true;
-                *abort_flag = 1;
-            }
-            umma_commit(BAR(C::B_FINAL));
-            int no_abort = 0;
-            mbar_wait_bounded(BAR(C::B_FINAL), 0, &no_abort, kWaitLimitNs);
+            if (elect_one()) umma_commit(BAR(C::B_QEMPTY + s));
+            __syncwarp();
         }
+        if (!ok) {
+            failed = true;
+            *abort_flag = 1;
+        }
+        // every MMA is done before TMEM is released
+        if (elect_one()) umma_commit(BAR(C::B_FINAL));
+        int no_abort = 0;
+        mbar_wait_bounded(BAR(C::B_FINAL), 0, &no_abort, kWaitLimitNs);
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------------------ lse and limits
-        while (q.next()) {
-            const int s = q.n % S;
+        for (bool more = true; more;) {
+            more = q.next();
+            const int n = more ? q.n : q.n + 1, s = n % S;
             float v[4];
             int m[4];
+            if (more) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int f = q.j * BT + e * 32 + lane;
-                const int i = f % p.q_len;
-                const bool real = f < p.G * p.q_len && i < qn;
-                v[e] = real ? -lse_log2(p.lse[row0 + f]) : -INFINITY;
-                m[e] = real ? L - qn + i + 1 : 0;
+                for (int e = 0; e < 4; ++e) {
+                    const int f = q.j * BT + e * 32 + lane;
+                    const int i = f % p.q_len;
+                    const bool real = f < p.G * p.q_len && i < qn;
+                    v[e] = real ? -lse_log2(p.lse[row0 + f]) : -INFINITY;
+                    m[e] = real ? L - qn + i + 1 : 0;
+                }
             }
-            if (q.n >= S && !wait_warp(BAR(C::B_CEMPTY + s), ((q.n / S) - 1) & 1, abort_flag)) {
+            if (n >= S && !wait_warp(BAR(C::B_CEMPTY + s), ((n / S) - 1) & 1, abort_flag)) {
                 failed = true;
                 break;
             }
-            float *nlse = reinterpret_cast<float *>(smem + C::OFF_LSE) + s * BT;
-            int *lim = reinterpret_cast<int *>(smem + C::OFF_LIM) + s * BT;
+            if (more) {
+                float *nlse = reinterpret_cast<float *>(smem + C::OFF_LSE) + s * BT;
+                int *lim = reinterpret_cast<int *>(smem + C::OFF_LIM) + s * BT;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                nlse[e * 32 + lane] = v[e];
-                lim[e * 32 + lane] = m[e];
+                for (int e = 0; e < 4; ++e) {
+                    nlse[e * 32 + lane] = v[e];
+                    lim[e * 32 + lane] = m[e];
+                }
             }
+            if (lane == 0)
+                reinterpret_cast<TileInfo *>(smem + C::OFF_INFO)[s] =
+                    TileInfo{q.lim_min, q.lim_max, q.whole, !more};
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_CFULL + s));
         }
@@ -566,33 +588,40 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
         const uint32_t ts = tmem + x * BT + ((uint32_t)(q4 * 32) << 16);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         int used = 0;
-        while (q.next()) {
-            const int s = q.n % S;
+        for (int n = 0;; ++n) {
+            const int s = n % S;
             // (also for a tile this warpgroup skips: it frees the slot like the others)
-            if (!wait_warp(BAR(C::B_CFULL + s), (q.n / S) & 1, abort_flag)) {
+            if (!wait_warp(BAR(C::B_CFULL + s), (n / S) & 1, abort_flag)) {
                 failed = true;
                 break;
             }
-            if (x < ktiles && q.seen(kb, BT)) {
+            const TileInfo info = reinterpret_cast<const TileInfo *>(smem + C::OFF_INFO)[s];
+            if (info.stop) break;
+            if (x < ktiles && sees(p, info.lim_min, info.lim_max, kb, BT)) {
                 if (!wait_warp(BAR(C::B_SFULL + x), used & 1, abort_flag)) {
                     failed = true;
                     break;
                 }
                 tc_fence_after();
-                const bool masked = !q.whole || kb + BT > q.lim_min ||
-                                    (p.window > 0 && kb < q.lim_max - p.window);
+                const bool masked = !info.whole || kb + BT > info.lim_min ||
+                                    (p.window > 0 && kb < info.lim_max - p.window);
                 const float *nlse = reinterpret_cast<const float *>(smem + C::OFF_LSE) + s * BT;
                 const int *lim = reinterpret_cast<const int *>(smem + C::OFF_LIM) + s * BT;
 #pragma unroll 1
-                for (int c0 = 0; c0 < BT; c0 += 32) {
-                    uint32_t v[32];
+                for (int c0 = 0; c0 < BT; c0 += 64) {
+                    uint32_t v[32], u[32];
                     tmem_ld32(ts + c0, v);
+                    tmem_ld32(ts + c0 + 32, u);
                     tmem_wait_ld32(v);
-                    if (c0 == BT - 32) {  // all read: the next product may overwrite them
+                    tmem_wait_ld32(u);
+                    if (c0 == BT - 64) {
+                        // all read: the next product overwrites them while the last half
+                        // is exponentiated from registers
                         tc_fence_before();
                         mbar_arrive(BAR(C::B_SEMPTY + x));
                     }
                     add_weights<32>(p, v, nlse + c0, lim + c0, t, masked, sum);
+                    add_weights<32>(p, u, nlse + c0 + 32, lim + c0 + 32, t, masked, sum);
                 }
                 ++used;
             }
