@@ -22,7 +22,7 @@
 //   warp 3    TMA producer of the V ring (the same pages).  With one producer for
 //             both rings, its per-block work (page lookups, up to 32 box copies
 //             for 8-token pages) was the longest step of the suffix's pipeline.
-//   warp 1    allocates TMEM; one lane issues the MMAs:
+//   warp 1    allocates TMEM; one elected lane issues the MMAs:
 //               S  = Q K^T  (M=128, N=128, K=D; A and B from smem)  -> TMEM
 //               O += P V    (M=128, N=D, K=128; A = P from TMEM, B = V from smem)
 //             for head_dim D = 64 or 128 (one or two 64-element slabs per row).
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     const uint32_t sb = smem_u32(smem);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
 #define BAR(i) (sb + C::OFF_BAR + 8u * (uint32_t)(i))
 
     // ------------------------------------------------------------ work items
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     bool failed = false;
 
     if (warp == 0 || warp == 3) {
@@ -500,7 +500,8 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // -------------------------------------------------------- MMA issuer
-        if (lane == 0) {
+        {
+            // The warp stays converged, one elected lane issues (elect_one).
             const uint32_t idS = idesc_bf16_f32(128, 128, false, p.negate_scores != 0);
             constexpr uint32_t idPV = idesc_bf16_f32(128, D, true);
             bool ok = true;
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                 if ((skip >> it) & 1) continue;
                 const TcWork &w = PERSIST ? items[it] : w0;
                 const int nb = w.nb;
-                ok = mbar_wait_bounded(BAR(C::B_Q), nq & 1, abort_flag, kWaitLimitNs);
+                ok = wait_warp(BAR(C::B_Q), nq & 1, abort_flag);
                 tc_fence_after();
                 if (!ok) break;
                 // S_x(j) = Q_x K_j^T into S buffer (g + j) % SB of tile x.  Tile 0 waits
@@ -520,8 +521,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                 auto issue_s = [&](int j, int x) -> bool {
                     const int G = g + j, s = G % S;
                     if (x == 0) {
-                        if (!mbar_wait_bounded(BAR(C::B_KFULL + s), (G / S) & 1, abort_flag,
-                                               kWaitLimitNs))
+                        if (!wait_warp(BAR(C::B_KFULL + s), (G / S) & 1, abort_flag))
                             return false;
                         tc_fence_after();
                     }
@@ -530,16 +530,19 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                     // can carry out of.
                     const uint64_t kd = sdesc_sw128(sb + C::OFF_K + s * kTileBytes, 16, 1024);
                     const uint64_t qd = sdesc_sw128(sb + C::OFF_Q + x * kTileBytes, 16, 1024);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
-                        umma_bf16(tmem + C::s_col(x, G % SB), qd + off, kd + off, idS, kk > 0);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
+                            umma_bf16(tmem + C::s_col(x, G % SB), qd + off, kd + off, idS, kk > 0);
+                        }
+                        umma_commit(BAR(C::B_SFULL + x * SB + G % SB));
+                        if (x == NT - 1) {
+                            umma_commit(BAR(C::B_KEMPTY + s));
+                            if (j == nb - 1) umma_commit(BAR(C::B_QEMPTY));
+                        }
                     }
-                    umma_commit(BAR(C::B_SFULL + x * SB + G % SB));
-                    if (x == NT - 1) {
-                        umma_commit(BAR(C::B_KEMPTY + s));
-                        if (j == nb - 1) umma_commit(BAR(C::B_QEMPTY));
-                    }
+                    __syncwarp();
                     return true;
                 };
                 for (int j = 0; ok && j < min(SB, nb); ++j)
@@ -550,23 +553,21 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                     const int G = g + j, s = G % S;
 #pragma unroll
                     for (int x = 0; x < NT; ++x) {
-                        if (!mbar_wait_bounded(BAR(C::B_PFULL + x), G & 1, abort_flag,
-                                               kWaitLimitNs)) {
+                        if (!wait_warp(BAR(C::B_PFULL + x), G & 1, abort_flag)) {
                             ok = false;
                             break;
                         }
                         if (x == 0) {
-                            if (!mbar_wait_bounded(BAR(C::B_VFULL + s), (G / S) & 1, abort_flag,
-                                                   kWaitLimitNs)) {
+                            if (!wait_warp(BAR(C::B_VFULL + s), (G / S) & 1, abort_flag)) {
                                 ok = false;
                                 break;
                             }
                             if (j == nb - 1 && w.tail_fix) {
                                 // Hand the landed last V block to the fix-up warp (only
-                                // this thread observes every phase of the V ring in order).
-                                mbar_arrive(BAR(C::B_TAIL_READY));
-                                if (!mbar_wait_bounded(BAR(C::B_TAIL), ntail & 1, abort_flag,
-                                                       kWaitLimitNs)) {
+                                // this warp observes every phase of the V ring in order).
+                                if (elect_one()) mbar_arrive(BAR(C::B_TAIL_READY));
+                                __syncwarp();
+                                if (!wait_warp(BAR(C::B_TAIL), ntail & 1, abort_flag)) {
                                     ok = false;
                                     break;
                                 }
@@ -576,8 +577,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                         // The item's first PV overwrites O: the previous item's
                         // epilogue must have read it out.
                         if (j == 0 && nq > 0 &&
-                            !mbar_wait_bounded(BAR(C::B_OFREE + x), (nq - 1) & 1, abort_flag,
-                                               kWaitLimitNs)) {
+                            !wait_warp(BAR(C::B_OFREE + x), (nq - 1) & 1, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -588,34 +588,44 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                         // keys 16kk .. 16kk+15 of P sit in columns 32*(kk/2) + 8*(kk%2) ..
                         // +8, their remainders 16 columns further on.  V slice kk starts
                         // 2048 bytes (128 descriptor units) after slice kk-1.
+                        if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            umma_bf16_tmem_a(tmem + C::o_col(x),
-                                             pcol + (kk >> 1) * 32 + (kk & 1) * 8,
-                                             vd + kk * 128u, idPV, (j > 0 || kk > 0) ? 1u : 0u);
+                            for (int kk = 0; kk < 8; ++kk)
+                                umma_bf16_tmem_a(tmem + C::o_col(x),
+                                                 pcol + (kk >> 1) * 32 + (kk & 1) * 8,
+                                                 vd + kk * 128u, idPV,
+                                                 (j > 0 || kk > 0) ? 1u : 0u);
+                        }
+                        __syncwarp();
                         // The softmax's vote for this block (one byte per warp, written
                         // before its P arrival), read once the hi products are queued so
                         // its latency hides there.  The lo product leaves the rows of
                         // warps that did not ask for it unchanged: their lo columns hold
                         // no P.
-                        const uint32_t vote = *reinterpret_cast<volatile uint32_t *>(
-                            smem + C::OFF_VOTE + (x * 2 + (G & 1)) * 4);
+                        const uint32_t vote = uniform(*reinterpret_cast<volatile uint32_t *>(
+                            smem + C::OFF_VOTE + (x * 2 + (G & 1)) * 4));
                         if (w.hilo || vote != 0u) {
                             uint32_t off_lanes[4];
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
                                 off_lanes[q] =
                                     (w.hilo || ((vote >> (8 * q)) & 0xffu)) ? 0u : 0xffffffffu;
+                            if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
-                                umma_bf16_tmem_a_masked(tmem + C::o_col(x),
-                                                        pcol + (kk >> 1) * 32 + 16 + (kk & 1) * 8,
-                                                        vd + kk * 128u, idPV, off_lanes);
+                                for (int kk = 0; kk < 8; ++kk)
+                                    umma_bf16_tmem_a_masked(
+                                        tmem + C::o_col(x), pcol + (kk >> 1) * 32 + 16 + (kk & 1) * 8,
+                                        vd + kk * 128u, idPV, off_lanes);
+                            }
+                            __syncwarp();
                         }
-                        umma_commit(BAR(C::B_PVDONE + x));
                         // The V stage is free once the last tile's PV has read it: release
                         // it before S_x(j + SB) waits for its K block.
-                        if (x == NT - 1) umma_commit(BAR(C::B_VEMPTY + s));
+                        if (elect_one()) {
+                            umma_commit(BAR(C::B_PVDONE + x));
+                            if (x == NT - 1) umma_commit(BAR(C::B_VEMPTY + s));
+                        }
+                        __syncwarp();
                         // Ping-pong: S_x(j + SB) follows PV_x(j) at once, so tile x starts
                         // its next softmax while the other tile's P is still being made.
                         // It writes the S buffer that PV_x(j) reads P_x(j) from; the
@@ -635,7 +645,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                 *abort_flag = 1;
             }
             // Every MMA issued so far completes before TMEM is released.
-            umma_commit(BAR(C::B_FINAL));
+            if (elect_one()) umma_commit(BAR(C::B_FINAL));
             int no_abort = 0;
             mbar_wait_bounded(BAR(C::B_FINAL), 0, &no_abort, kWaitLimitNs);
         }
