@@ -255,9 +255,24 @@ __device__ void tc_direct_item(const TcParams &p, int r, int &u, int &t0, int &t
         const int qi = p.tiles_per_head - 1 - r / per;
         t0 = (rest % heads) * NT * p.tiles_per_head + qi;
         tstep = p.tiles_per_head;
-    } else {
+    } else if (p.row_step || p.B > 32) {
         u = r % units;
         t0 = r / units * NT;  // NT = 2: cross attention's neighbouring tiles of one unit
+        tstep = NT - 1;
+    } else {
+        // Cross attention: the sequences longest-first, so that the CTAs left over when the
+        // others are done are short ones (a whole warp calls this; lane k ranks sequence k).
+        const int per = p.Hkv * ((p.tiles_per_unit + NT - 1) / NT);
+        const int lane = threadIdx.x & 31;
+        const int len = lane < p.B ? p.seq_lens[lane] : -1;
+        int rank = 0;
+        for (int k = 0; k < p.B; ++k) {
+            const int other = __shfl_sync(0xffffffffu, len, k);
+            rank += other > len || (other == len && k < lane);
+        }
+        const int b = __ffs(__ballot_sync(0xffffffffu, lane < p.B && rank == r / per)) - 1;
+        u = b * p.Hkv + r % per % p.Hkv;
+        t0 = r % per / p.Hkv * NT;
         tstep = NT - 1;
     }
 }
