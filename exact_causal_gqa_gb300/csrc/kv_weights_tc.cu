@@ -67,6 +67,11 @@ __device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t k_smem, u
                   qd + (((kk >> 2) * q_slab + (kk & 3) * 32) >> 4), idesc, kk > 0);
 }
 
+// Barrier `id` of `threads` threads (whole warps) of the CTA.
+__device__ __forceinline__ void group_barrier(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // Adds 2^(s2 + neg_lse2[c]) of NC columns of scores; with kMasked, of those columns c that
 // key t is visible to (t < lim[c], and t >= lim[c] - window with a window).
 template <int NC, bool kMasked, bool kCapped>
@@ -120,15 +125,25 @@ struct StreamCfg {
     // beyond, the accumulators and queries leave room for one with a deeper ring.
     static constexpr int kCtas = N <= 32 ? 2 : 1;
     static constexpr int kStages = (N <= 32 ? 3 : N <= 128 ? 5 : 4) * (128 / D);
-    static constexpr int kGroups = N >= 128 ? 2 : 1;  // epilogue warpgroups (alternate tiles)
-    static constexpr int kThreads = 128 + 128 * kGroups;
-    static constexpr uint32_t kCols = 2 * N < 32 ? 32 : 2 * N;  // TMEM: two score buffers
+    // Epilogue warpgroups: kGroups that take turns at the tiles, of kHalves that share a
+    // tile's columns.  From 64 columns on each has a score buffer and products of its own,
+    // so that four of them keep the exponential unit busy while products are under way
+    // (64 sequences x heads, 413K keys, 256 columns: 207 us; 237 us with two 256-column
+    // buffers); fewer columns need one warpgroup, with two buffers.
+    static constexpr int kGroups = N >= 256 ? 2 : N >= 64 ? 4 : 1;
+    static constexpr int kHalves = N >= 256 ? 2 : 1;
+    static constexpr int kBufs = kGroups == 1 ? 2 : kGroups;  // score buffers of a half
+    static constexpr int kPart = N / kHalves;                 // columns of a half
+    static constexpr int kThreads = 128 + 128 * kGroups * kHalves;
+    static constexpr uint32_t kCols = kBufs * N < 32 ? 32 : kBufs * N;  // TMEM
     static constexpr int OFF_Q = kStages * kTile;
     static constexpr int OFF_LSE = OFF_Q + kQ;
     static constexpr int OFF_LIM = OFF_LSE + N * 4;
-    static constexpr int OFF_BAR = OFF_LIM + N * 4;
+    static constexpr int OFF_HALF = OFF_LIM + N * 4;  // [kGroups][128] the second halves' sums
+    static constexpr int OFF_BAR = OFF_HALF + (kHalves == 2 ? kGroups * BT * 4 : 0);
     static constexpr int B_FULL = 0, B_EMPTY = kStages, B_SFULL = 2 * kStages,
-                         B_SEMPTY = B_SFULL + 2, B_FINAL = B_SEMPTY + 2, kBars = B_FINAL + 1;
+                         B_SEMPTY = B_SFULL + kBufs * kHalves,
+                         B_FINAL = B_SEMPTY + kBufs * kHalves, kBars = B_FINAL + 1;
     static constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
     static constexpr int kSmem = OFF_TMEM + 16 + 1024;
     static_assert(kCtas * (kSmem + 1024) <= 233472, "shared memory of an SM");
@@ -177,13 +192,14 @@ __global__ void __launch_bounds__(StreamCfg<D, N>::kThreads, StreamCfg<D, N>::kC
     const int ncols = p.G * qn;                  // packed: column c is row c % qn of head c / qn
     constexpr int kStep = N == 16 ? 16 : 32;     // columns of one TMEM load
     const int nmma = (ncols + kStep - 1) / kStep * kStep;
+    const int halves = nmma > C::kPart ? 2 : 1;  // in use (kHalves at most)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(BAR(C::B_FULL + s), 1);
             mbar_init(BAR(C::B_EMPTY + s), 1);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < C::kBufs * C::kHalves; ++s) {
             mbar_init(BAR(C::B_SFULL + s), 1);
             mbar_init(BAR(C::B_SEMPTY + s), 128);
         }
@@ -241,20 +257,30 @@ __global__ void __launch_bounds__(StreamCfg<D, N>::kThreads, StreamCfg<D, N>::kC
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        const uint32_t idesc = idesc_bf16_f32(128, nmma, false);
+        // (nmma columns in all; the last half used may have fewer than kPart)
+        const uint32_t idesc = idesc_bf16_f32(128, min(nmma, C::kPart), false);
+        const uint32_t idesc1 = idesc_bf16_f32(128, max(nmma - C::kPart, 16), false);
         bool ok = true;
         for (int j = 0; ok && j < tiles; ++j) {
-            const int s = j % S, buf = j & 1;
-            ok = wait_warp(BAR(C::B_FULL + s), (j / S) & 1, abort_flag) &&
-                 (j < 2 || wait_warp(BAR(C::B_SEMPTY + buf), ((j >> 1) - 1) & 1, abort_flag));
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-                issue_scores<D>(tmem + buf * N, sb + s * C::kTile, sb + C::OFF_Q, N * 128, idesc);
-                umma_commit(BAR(C::B_EMPTY + s));
-                umma_commit(BAR(C::B_SFULL + buf));
+            const int s = j % S, buf = j % C::kBufs;
+            ok = wait_warp(BAR(C::B_FULL + s), (j / S) & 1, abort_flag);
+#pragma unroll
+            for (int half = 0; half < C::kHalves; ++half) {
+                if (!ok || half >= halves) continue;
+                const int i = buf * C::kHalves + half;
+                if (j >= C::kBufs)
+                    ok = wait_warp(BAR(C::B_SEMPTY + i), (j / C::kBufs - 1) & 1, abort_flag);
+                if (!ok) continue;
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_scores<D>(tmem + i * C::kPart, sb + s * C::kTile,
+                                    sb + C::OFF_Q + half * C::kPart * 128, N * 128,
+                                    half ? idesc1 : idesc);
+                    umma_commit(BAR(C::B_SFULL + i));
+                    if (half == halves - 1) umma_commit(BAR(C::B_EMPTY + s));
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
         if (!ok) {
             failed = true;
@@ -267,43 +293,76 @@ __global__ void __launch_bounds__(StreamCfg<D, N>::kThreads, StreamCfg<D, N>::kC
         __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ epilogue
-        const int group = (warp - 4) / 4, q4 = warp % 4;
-        const int r = q4 * 32 + lane;
-        for (int j = group; j < tiles; j += C::kGroups) {
-            const int buf = j & 1;
+        const int group = (warp - 4) / 4 % C::kGroups, half = (warp - 4) / 4 / C::kGroups;
+        const int q4 = warp % 4, r = q4 * 32 + lane;
+        const int c_begin = half * C::kPart, c_end = min(nmma, c_begin + C::kPart);
+        float *other = reinterpret_cast<float *>(smem + C::OFF_HALF) + group * BT + r;
+        const int32_t *table = p.page_table + (int64_t)b * p.max_pages;
+        // A tile's page id and old weight are read while the tile before is worked on (one
+        // after the other and in the loop, they were its longest step).
+        const bool reads = half == 0;
+        int id = 0, id_next = 0;
+        float old = 0.f, old_next = 0.f;
+        auto ahead = [&](int j) {
+            const int t = begin + j * BT + r;
+            if (reads && t < end) {
+                id_next = table[t >> lp];
+                old_next = p.accumulate ? w[t] : 0.f;
+            }
+        };
+        ahead(group);
+        for (int j = half < halves ? group : tiles; j < tiles; j += C::kGroups) {
+            const int buf = j % C::kBufs * C::kHalves + half;
             const int kb = begin + j * BT, t = kb + r;
-            const bool mine = t < end && page_ok(p, b, t, lp);
-            const float old = mine && p.accumulate ? w[t] : 0.f;
+            id = id_next;
+            old = old_next;
+            ahead(j + C::kGroups);
             // a tile that every row sees whole needs no limits
             const bool masked = kb + BT > L - qn + 1 || (p.window > 0 && kb < L - p.window);
-            if (!wait_warp(BAR(C::B_SFULL + buf), (j >> 1) & 1, abort_flag)) {
+            if (!wait_warp(BAR(C::B_SFULL + buf), (j / C::kBufs) & 1, abort_flag)) {
                 failed = true;
                 *abort_flag = 1;
-                break;
             }
             tc_fence_after();
-            const uint32_t ts = tmem + buf * N + ((uint32_t)(q4 * 32) << 16);
+            const uint32_t ts = tmem + buf * C::kPart + ((uint32_t)(q4 * 32) << 16);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            // (padding columns are zero rows: 0 times a non-finite key is not 0)
             if (N == 16) {
                 uint32_t s[16];
                 tmem_ld16(ts, s);
                 tmem_wait_ld();
                 tc_fence_before();
                 mbar_arrive(BAR(C::B_SEMPTY + buf));
-                // (padding columns are zero rows: 0 times a non-finite key is not 0)
                 add_weights<16>(p, s, nlse, lim, t, masked || ncols < 16, sum);
             } else {
 #pragma unroll 1
-                for (int c0 = 0; c0 < nmma; c0 += 32) {
-                    uint32_t s[32];
-                    tmem_ld32(ts + c0, s);
+                for (int c0 = c_begin; c0 < c_end; c0 += 64) {
+                    const bool two = c0 + 32 < c_end;
+                    uint32_t s[32], u[32];
+                    tmem_ld32(ts + c0 - c_begin, s);
+                    if (two) tmem_ld32(ts + c0 - c_begin + 32, u);
                     tmem_wait_ld32(s);
+                    if (two) tmem_wait_ld32(u);
+                    if (c0 + 64 >= c_end) {
+                        // all read: the next product overwrites them meanwhile
+                        tc_fence_before();
+                        mbar_arrive(BAR(C::B_SEMPTY + buf));
+                    }
                     add_weights<32>(p, s, nlse + c0, lim + c0, t, masked || c0 + 32 > ncols, sum);
+                    if (two)
+                        add_weights<32>(p, u, nlse + c0 + 32, lim + c0 + 32, t,
+                                        masked || c0 + 64 > ncols, sum);
                 }
-                tc_fence_before();
-                mbar_arrive(BAR(C::B_SEMPTY + buf));
             }
-            if (mine) w[t] = old + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+            float total = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            if (C::kHalves == 2 && halves == 2) {
+                // the second half's sum through shared memory: written, read, free again
+                if (half == 1) *other = total;
+                group_barrier(1 + group, 256);
+                if (half == 0) total += *other;
+                group_barrier(1 + group, 256);
+            }
+            if (reads && t < end && id >= 0 && id < p.num_pages && !failed) w[t] = old + total;
         }
     }
     tc_fence_before();
