@@ -464,9 +464,14 @@ def _frequencies(theta, rot_dim):
 
 def _row_strides(name, t):
     """Element strides (batch, head, token) of a [B][H][n][D] view with contiguous rows."""
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    if t.is_contiguous():
+        return (ctypes.c_int64 * 3)()
+    if t.stride(3) != 1:
         raise ValueError(f"{name} must have contiguous rows of head_dim elements")
-    return (ctypes.c_int64 * 3)(*([0, 0, 0] if t.is_contiguous() else t.stride()[:3]))
+    strides = [0 if size == 1 else stride for size, stride in zip(t.shape[:3], t.stride())]
+    if not any(strides):  # the library reads all-zero strides as dense rows
+        raise ValueError(f"{name} is one row broadcast to all: make it contiguous")
+    return (ctypes.c_int64 * 3)(*strides)
 
 
 def kv_append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, positions, *,

@@ -6,10 +6,22 @@
 // softmax state is needed -- lse normalises every row -- and K is read once.
 //
 // bf16 runs on the tensor cores (kv_weights_tc.cu); this file has the entry point and
-// fp32.  weights_ffma_kernel: a CTA owns 128 keys of one (sequence, kv head), held in shared
-// memory, and walks the columns in tiles of NC.  A thread forms 4 keys x NC / 8
-// columns of scores as whole dot products, exponentiates them and keeps one sum per key;
-// the 8 lanes that share a key add up at the end.
+// fp32.
+//
+// weights_warp_kernel, at most 8 columns (decode): K is read once, straight into registers,
+//   and its bytes are the bound.  A warp takes 8 keys at a time, a lane D / 32 elements of
+//   each; the 8 x NC partial dot products are added across the lanes by halving -- each
+//   step sends half of a lane's values to the lane that keeps them, one shuffle per score
+//   in all -- which leaves every score in one lane, and the columns' weights are added over
+//   neighbouring lanes.  8 sequences of 16384 keys, 8 kv heads of 128: 106 us, 5.1 TB/s
+//   with 4 columns, 90 us for half the bytes with 8 (3.0 TB/s, bound by latency at two
+//   CTAs an SM; 4 keys a warp are slower: 120 and 117 us).
+// weights_ffma_kernel, more columns: a CTA owns 128 keys of one (sequence, kv head), held in
+//   shared memory, and walks the columns in tiles of NC that one of its keys is visible to.
+//   A thread forms 4 keys x NC / 8 columns of scores as whole dot products (packed fp32
+//   pairs), exponentiates them and keeps one sum per key; the 8 lanes that share a key add
+//   up at the end.  Bound by shared-memory reads (12 of 16 bytes per 128 products):
+//   28-33 TFLOP/s.
 #include "kv_weights.cuh"
 
 namespace atlas {
@@ -24,7 +36,7 @@ struct FfmaLayout {
 };
 
 template <int D, int NC>
-__global__ void __launch_bounds__(256) weights_ffma_kernel(const WeightsParams p) {
+__global__ void __launch_bounds__(256, 2) weights_ffma_kernel(const WeightsParams p) {
     using Lay = FfmaLayout<D, NC>;
     constexpr int KS = Lay::KS, CPT = NC / 8;  // columns per thread
     extern __shared__ __align__(16) float smem_f[];
@@ -63,6 +75,12 @@ __global__ void __launch_bounds__(256) weights_ffma_kernel(const WeightsParams p
     const int64_t row0 = ((int64_t)b * p.Hq + (int64_t)hkv * p.G) * p.q_len;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     for (int c0 = 0; c0 < ncols; c0 += NC) {
+        // A tile none of whose rows is real or sees a key of this CTA is passed over.
+        const int i0 = c0 % p.q_len, count = min(NC, ncols - c0);
+        const bool spans = i0 + count > p.q_len;
+        const int lim_min = L - qn + (spans ? 0 : i0) + 1;
+        const int lim_max = L - qn + min(spans ? p.q_len : i0 + count, qn);
+        if ((spans ? 0 : i0) >= qn || !sees(p, lim_min, lim_max, kb, nkeys)) continue;
         __syncthreads();
         if (threadIdx.x < NC) {
             const int f = c0 + (int)threadIdx.x;
@@ -82,12 +100,12 @@ __global__ void __launch_bounds__(256) weights_ffma_kernel(const WeightsParams p
             *reinterpret_cast<float4 *>(sQ + r * KS + d) = x;
         }
         __syncthreads();
-        float s[4][CPT];
+        float2 s[4][CPT];  // even and odd elements' sums
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int c = 0; c < CPT; ++c) s[r][c] = 0.f;
-#pragma unroll 4
+            for (int c = 0; c < CPT; ++c) s[r][c] = make_float2(0.f, 0.f);
+#pragma unroll 2
         for (int d = 0; d < D; d += 4) {
             float4 k4[4];
 #pragma unroll
@@ -98,10 +116,8 @@ __global__ void __launch_bounds__(256) weights_ffma_kernel(const WeightsParams p
                 const float4 q4 = *reinterpret_cast<const float4 *>(sQ + (cg + 8 * c) * KS + d);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    s[r][c] = fmaf(q4.x, k4[r].x, s[r][c]);
-                    s[r][c] = fmaf(q4.y, k4[r].y, s[r][c]);
-                    s[r][c] = fmaf(q4.z, k4[r].z, s[r][c]);
-                    s[r][c] = fmaf(q4.w, k4[r].w, s[r][c]);
+                    s[r][c] = ffma2(make_float2(q4.x, q4.y), make_float2(k4[r].x, k4[r].y), s[r][c]);
+                    s[r][c] = ffma2(make_float2(q4.z, q4.w), make_float2(k4[r].z, k4[r].w), s[r][c]);
                 }
             }
         }
@@ -112,7 +128,7 @@ __global__ void __launch_bounds__(256) weights_ffma_kernel(const WeightsParams p
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int t = kb + kg + 32 * r;
-                sum[r] += t < lim && t >= lo ? ex2(score_log2(p, s[r][c]) - lse2) : 0.f;
+                sum[r] += t < lim && t >= lo ? ex2(score_log2(p, s[r][c].x + s[r][c].y) - lse2) : 0.f;
             }
         }
     }
@@ -127,6 +143,141 @@ __global__ void __launch_bounds__(256) weights_ffma_kernel(const WeightsParams p
             *w = (p.accumulate ? *w : 0.f) + sum[r];
         }
     }
+}
+
+// One warp per 8 keys and step; grid (key ranges, Hkv, B).
+constexpr int kWarpKeys = 8, kWarpThreads = 256;
+
+template <int D, int NC>
+__global__ void __launch_bounds__(kWarpThreads, NC == 8 ? 2 : 3) weights_warp_kernel(const WeightsParams p, const int chunk) {
+    constexpr int DPL = D / 32;  // elements of a row per lane: 2 or 4
+    const int b = blockIdx.z, hkv = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int L = p.seq_lens[b];
+    const int qn = p.q_lens ? p.q_lens[b] : p.q_len;
+    if (bad_lens(p, L, qn)) {
+        if (threadIdx.x == 0 && blockIdx.x == 0) record(p.status, ATLAS_DEV_BAD_SEQLEN);
+        return;
+    }
+    const int first = (int)blockIdx.x * chunk, end = min(L, first + chunk);
+    if (first >= end) return;
+    const int lp = 31 - __clz(p.P);
+    const int64_t row0 = ((int64_t)b * p.Hq + (int64_t)hkv * p.G) * p.q_len;
+    // The columns, packed: column c is row c % qn of head c / qn of the group.
+    const int ncols = p.G * qn;
+    float q[NC][DPL];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const float *src = static_cast<const float *>(p.q) +
+                           (row0 + (c < ncols ? (int64_t)(c / qn) * p.q_len + c % qn : 0)) * D + lane * DPL;
+#pragma unroll
+        for (int e = 0; e < DPL; ++e) q[c][e] = c < ncols ? src[e] : 0.f;
+    }
+    // The columns go through the halving kShare at a time (8 at once held too many
+    // registers); after it a lane holds column i * kShare + share of one key.
+    constexpr int kShare = NC < 4 ? NC : 4, kMine = NC / kShare;
+    constexpr int kSpread = 32 / (kWarpKeys * kShare);  // lanes left over: they hold copies
+    const int key = lane / kSpread / kShare, share = lane / kSpread % kShare;
+    float lse2[kMine];
+    int lim[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int c = i * kShare + share;
+        const bool real = c < ncols;
+        lse2[i] = real ? lse_log2(p.lse[row0 + (int64_t)(c / qn) * p.q_len + c % qn]) : INFINITY;
+        lim[i] = real ? L - qn + c % qn + 1 : 0;
+    }
+    float *w = p.weights + ((int64_t)b * p.Hkv + hkv) * p.row_tokens;
+    const int32_t *table = p.page_table + (int64_t)b * p.max_pages;
+    // Page ids are read by the lanes that own a key, a step ahead, and handed round.
+    auto page_of = [&](int kb) {
+        const int t = kb + key;
+        const int id = t < end ? table[t >> lp] : -1;
+        if (t < end && (id < 0 || id >= p.num_pages) && lane % (kSpread * kShare) == 0)
+            record(p.status, ATLAS_DEV_BAD_PAGE);
+        return id < p.num_pages ? id : -1;
+    };
+    const int step = kWarpThreads / 32 * kWarpKeys;
+    int kb = first + warp * kWarpKeys;
+    int id_next = page_of(kb);
+    for (; kb < end; kb += step) {
+        const int id = id_next, t = kb + key;
+        float x[kWarpKeys][DPL];
+#pragma unroll
+        for (int k = 0; k < kWarpKeys; ++k) {
+            const int page = __shfl_sync(0xffffffffu, id, k * kSpread * kShare);
+            const float *src = static_cast<const float *>(p.k_pages) +
+                               (((int64_t)max(page, 0) * p.Hkv + hkv) * p.P + ((kb + k) & (p.P - 1))) * D +
+                               lane * DPL;
+            if (DPL == 4) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (page >= 0) v = __ldcs(reinterpret_cast<const float4 *>(src));
+                x[k][0] = v.x;
+                x[k][1] = v.y;
+                x[k][2 % DPL] = v.z;
+                x[k][3 % DPL] = v.w;
+            } else {
+                float2 v = make_float2(0.f, 0.f);
+                if (page >= 0) v = __ldcs(reinterpret_cast<const float2 *>(src));
+                x[k][0] = v.x;
+                x[k][1] = v.y;
+            }
+        }
+        const float old = t < end && p.accumulate ? w[t] : 0.f;
+        id_next = page_of(kb + step);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            // Partial dot products, value (key, column) at key * kShare + column.
+            float s[kWarpKeys * kShare];
+#pragma unroll
+            for (int k = 0; k < kWarpKeys; ++k)
+#pragma unroll
+                for (int c = 0; c < kShare; ++c) {
+                    const float *qc = q[i * kShare + c];
+                    float a = qc[0] * x[k][0];
+#pragma unroll
+                    for (int e = 1; e < DPL; ++e) a = fmaf(qc[e], x[k][e], a);
+                    s[k * kShare + c] = a;
+                }
+            // Halving: lane bit `o` keeps the upper or the lower half of the values; once
+            // one is left, the lanes that hold the same one add theirs up.
+            int n = kWarpKeys * kShare;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                if (n > 1) {
+                    n /= 2;
+                    const bool upper = lane & o;
+#pragma unroll
+                    for (int v = 0; v < kWarpKeys * kShare / 2; ++v) {
+                        if (v >= n) break;
+                        const float send = upper ? s[v] : s[v + n];
+                        s[v] = (upper ? s[v + n] : s[v]) + __shfl_xor_sync(0xffffffffu, send, o);
+                    }
+                } else {
+                    s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+                }
+            }
+            const bool sees = t < lim[i] && (p.window == 0 || t >= lim[i] - p.window);
+            sum += sees ? ex2(score_log2(p, s[0]) - lse2[i]) : 0.f;
+        }
+#pragma unroll
+        for (int o = kSpread; o < kSpread * kShare; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (t < end && id >= 0 && lane % (kSpread * kShare) == 0) w[t] = old + sum;
+    }
+}
+
+template <int D, int NC>
+cudaError_t launch_warp(const WeightsParams &p, cudaStream_t stream) {
+    // Key ranges that give each SM its 8 CTAs twice over at the largest context, of at
+    // least one step.
+    const int64_t ctx = (int64_t)p.max_pages * p.P, units = (int64_t)p.B * p.Hkv;
+    const int64_t step = kWarpThreads / 32 * kWarpKeys;
+    const int64_t want = (ctx * units / ((int64_t)device_sm_count() * 16) + step - 1) / step;
+    const int64_t chunk = (want < 1 ? 1 : want > 64 ? 64 : want) * step;
+    const dim3 grid((unsigned)((ctx + chunk - 1) / chunk), (unsigned)p.Hkv, (unsigned)p.B);
+    weights_warp_kernel<D, NC><<<grid, kWarpThreads, 0, stream>>>(p, (int)chunk);
+    return cudaGetLastError();
 }
 
 template <int D, int NC>
@@ -146,6 +297,17 @@ cudaError_t launch_ffma(const WeightsParams &p, cudaStream_t stream) {
     const dim3 grid((unsigned)((ctx + kKeys - 1) / kKeys), (unsigned)p.Hkv, (unsigned)p.B);
     kern<<<grid, 256, Lay::kBytes, stream>>>(p);
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_f32(const WeightsParams &p, cudaStream_t stream) {
+    const int64_t cols = (int64_t)p.G * p.q_len;
+    return cols <= 1    ? launch_warp<D, 1>(p, stream)
+           : cols <= 2  ? launch_warp<D, 2>(p, stream)
+           : cols <= 4  ? launch_warp<D, 4>(p, stream)
+           : cols <= 8  ? launch_warp<D, 8>(p, stream)
+           : cols <= 16 ? launch_ffma<D, 16>(p, stream)
+                        : launch_ffma<D, 64>(p, stream);
 }
 
 atlas_status check(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const atlas_weights *W) {
@@ -236,9 +398,7 @@ atlas_status atlas_kv_weights(const void *q, const void *k_pages, const int32_t 
             return ATLAS_ERR_CUDA;
         err = launch_weights_tc(p, plan, head_dim, tmQ, tmK, stream);
     } else {
-        const bool few = (int64_t)p.G * p.q_len <= 8;
-        err = head_dim == 128 ? (few ? launch_ffma<128, 8>(p, stream) : launch_ffma<128, 32>(p, stream))
-                              : (few ? launch_ffma<64, 8>(p, stream) : launch_ffma<64, 32>(p, stream));
+        err = head_dim == 128 ? launch_f32<128>(p, stream) : launch_f32<64>(p, stream);
     }
     return err == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }

@@ -407,12 +407,6 @@ struct TileCfg {
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-// Whether rows of which the earliest sees keys below lim_min and the latest keys below
-// lim_max see one of [k0, k0 + keys).
-__device__ __forceinline__ bool sees(const WeightsParams &p, int lim_min, int lim_max, int k0, int keys) {
-    return k0 < lim_max && (p.window == 0 || k0 + keys > lim_min - p.window);
-}
-
 // The query tiles first .. end - 1 of a (sequence, kv head) that have a row which sees a
 // key of [kb, kb + kGroupKeys), in order: rows 128 j .. 128 j + 127 of its G * q_len
 // (q head, row) pairs, and the keys their real rows see.  The producer, the MMA warp and

@@ -393,3 +393,155 @@ def test_compact_reports_and_skips(in_place):
         assert torch.equal(kk[at], clean[0][at])
         kk[at], vv[at] = whole[1][at], whole[2][at]
     assert torch.equal(kk, whole[1]) and torch.equal(vv, whole[2])
+
+
+# ------------------------------------------------------------------ streams, graphs, refusals
+def cut(w, k, v, table, lens, budget, **out):
+    kept, new, kept_w = atlas.kv_select(w, lens, budget, keep_first=2, keep_recent=9, **out)
+    atlas.kv_compact(k, v, table, kept, new)
+    return kept, new, kept_w
+
+
+@gpu
+@pytest.mark.parametrize("q_len", [1, 40, 200])
+def test_captured_and_replayed_with_other_lengths(q_len):
+    q, k, dev = problem("bf16", 8, 2, 128, 16, q_len, [900, 700], 21)
+    v_pages = torch.randn_like(dev[1])
+    lse = torch.from_numpy(np.float32(row_lse(widen(q), widen(k), [900, 700], 0.09))).cuda()
+    shape = (2, 2, dev[2].shape[1] * 16)
+    pools0 = dev[1].clone(), v_pages.clone()
+    outs = dict(kept=torch.empty((2, 2, 300), dtype=torch.int32, device="cuda"),
+                new_lens=torch.empty(2, dtype=torch.int32, device="cuda"),
+                kept_weights=torch.empty((2, 2, 300), device="cuda"))
+    w = torch.zeros(shape, device="cuda")
+    stream = torch.cuda.Stream()
+
+    def run():
+        atlas.kv_weights(*dev, lse, 8, 2, 128, 16, 0.09, weights=w, accumulate=False)
+        cut(w, dev[1], v_pages, dev[2], dev[3], 300, **outs)
+
+    with torch.cuda.stream(stream):
+        run()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            run()
+    for lens in ([900, 700], [300, q_len], [640, 333]):
+        torch.cuda.synchronize()
+        lens = torch.tensor([max(x, q_len) for x in lens], dtype=torch.int32)
+        dev[3].copy_(lens)
+        dev[1].copy_(pools0[0])
+        v_pages.copy_(pools0[1])
+        w.fill_(5.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        kk, vv = pools0[0].clone(), pools0[1].clone()
+        ww = atlas.kv_weights(dev[0], kk, *dev[2:], lse, 8, 2, 128, 16, 0.09, accumulate=False,
+                              weights=torch.full(shape, 5.0, device="cuda"))
+        kept, new, kept_w = cut(ww, kk, vv, dev[2], dev[3], 300)
+        assert torch.equal(w, ww) and torch.equal(outs["kept"], kept) and torch.equal(outs["new_lens"], new)
+        assert torch.equal(outs["kept_weights"], kept_w)
+        assert torch.equal(dev[1].isnan(), kk.isnan()) and torch.equal(dev[1].nan_to_num(), kk.nan_to_num())
+        assert torch.equal(v_pages, vv)
+
+
+@gpu
+def test_two_streams_at_once():
+    """Calls on two streams with tensors of their own give what they give alone."""
+    sides = []
+    for seed in (31, 32):
+        q, k, dev = problem("bf16", 8, 1, 64, 32, 150, [3000, 150, 1111], seed)
+        lse = torch.from_numpy(np.float32(row_lse(widen(q), widen(k), [3000, 150, 1111], 0.125))).cuda()
+        alone = atlas.kv_weights(*dev, lse, 8, 1, 64, 32, 0.125)
+        kk, vv = dev[1].nan_to_num(), torch.randn_like(dev[1])
+        pools = kk.clone(), vv.clone()
+        sides.append((dev, lse, alone, kk, vv, pools, cut(alone, kk, vv, dev[2], dev[3], 700)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sides]
+    got = [None, None]
+    for _ in range(5):
+        for i, (dev, lse, alone, kk, vv, pools, want) in enumerate(sides):
+            with torch.cuda.stream(streams[i]):
+                w = atlas.kv_weights(*dev, lse, 8, 1, 64, 32, 0.125)
+                a, b = pools[0].clone(), pools[1].clone()
+                got[i] = w, a, b, cut(w, a, b, dev[2], dev[3], 700)
+    torch.cuda.synchronize()
+    for (dev, lse, alone, kk, vv, pools, want), (w, a, b, out) in zip(sides, got):
+        assert torch.equal(w, alone) and torch.equal(a, kk) and torch.equal(b, vv)
+        assert all(torch.equal(x, y) for x, y in zip(out, want))
+
+
+@gpu
+def test_wrappers_refuse():
+    q, k, dev = problem("bf16", 4, 2, 64, 16, 3, [40, 30], 1)
+    lse = torch.zeros(q.shape[:3], device="cuda")
+    ok = (*dev, lse)
+
+    def swap(i, x):
+        return ok[:i] + (x,) + ok[i + 1:]
+
+    for bad in (swap(0, dev[0].float()), swap(0, dev[0][:, :, :2]), swap(1, dev[1].cpu()), swap(2, dev[2][:1]),
+                swap(2, dev[2].long()), swap(3, dev[3][:1]), swap(4, lse.double()), swap(4, lse[:, :2].contiguous())):
+        with pytest.raises(ValueError):
+            atlas.kv_weights(*bad, 4, 2, 64, 16, 0.1)
+    for kw in (dict(weights=torch.zeros((2, 1, 64), device="cuda")), dict(q_lens=dev[3][:1]),
+               dict(weights=torch.zeros((2, 2, 64), device="cuda", dtype=torch.bfloat16)),
+               dict(weights=torch.zeros((2, 2, 128), device="cuda")[:, :, ::2])):
+        with pytest.raises(ValueError):
+            atlas.kv_weights(*ok, 4, 2, 64, 16, 0.1, **kw)
+    with pytest.raises(ValueError):
+        atlas.kv_weights(*ok, 8, 2, 64, 16, 0.1)               # q has 4 heads
+    w = torch.rand((2, 2, 64), device="cuda")
+    for args in ((w[0], dev[3], 8), (w, dev[3][:1], 8), (w.double(), dev[3], 8)):
+        with pytest.raises(ValueError):
+            atlas.kv_select(*args)
+    for kw in (dict(keep_first=5, keep_recent=4), dict(keep_first=-1)):
+        with pytest.raises(atlas.AtlasError):
+            atlas.kv_select(w, dev[3], 8, **kw)
+    with pytest.raises(atlas.AtlasError):
+        atlas.kv_select(w, dev[3], 0)
+    kept, new, _ = atlas.kv_select(w, dev[3], 8)
+    for args in ((dev[1], dev[1][:1], dev[2], kept, new), (dev[1], dev[1], dev[2], kept[:1], new),
+                 (dev[1], dev[1], dev[2], kept.long(), new), (dev[1], dev[1], dev[2], kept, new[:1])):
+        with pytest.raises(ValueError):
+            atlas.kv_compact(*args)
+    with pytest.raises(ValueError):
+        atlas.kv_compact(dev[1], dev[1].clone(), dev[2], kept, new, new_page_table=dev[2][:1])
+
+
+@gpu
+def test_a_workspace_too_small_is_refused():
+    q, k, dev = problem("bf16", 8, 1, 64, 16, 300, [1000], 2)
+    lse = torch.zeros(q.shape[:3], device="cuda")
+    with pytest.raises(atlas.AtlasError):
+        atlas.kv_weights(*dev, lse, 8, 1, 64, 16, 0.1,
+                         workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@gpu
+def test_far_offsets_in_a_large_pool():
+    """Pages behind 2^31 elements of the pool, for every operator that addresses it."""
+    P, Hkv, D, last = 128, 8, 128, 17000                 # 17000 pages: 2.2e9 bf16 elements
+    kp = torch.zeros((last + 1, Hkv, P, D), dtype=torch.bfloat16, device="cuda")
+    vp = torch.zeros_like(kp)
+    small = torch.tensor([[0, 1, 2]], dtype=torch.int32, device="cuda")
+    far = torch.tensor([[last, last - 1, last - 2]], dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v, q = (torch.randn((1, h, 300, D), generator=g, device="cuda").to(torch.bfloat16) for h in (8, 8, 16))
+    pos = torch.arange(300, dtype=torch.int32, device="cuda")[None]
+    zero, full = (torch.tensor([x], dtype=torch.int32, device="cuda") for x in (0, 300))
+    got = []
+    for table in (small, far):
+        qr = atlas.kv_append_rope(q, k, v, kp, vp, table, zero, pos)
+        lse = torch.empty((1, 16, 300), device="cuda")
+        out = atlas.prefill(qr, kp, vp, table, full, 16, 8, D, P, 0.09, lse=lse)
+        crossed = atlas.cross(qr, kp, vp, table, full, 16, 8, D, P, 0.09)
+        w = atlas.kv_weights(qr, kp, table, full, lse, 16, 8, D, P, 0.09)
+        one = atlas.kv_weights(qr[:, :, -1:].contiguous(), kp, table, full, lse[:, :, -1:].contiguous(), 16, 8, D, P, 0.09)
+        kept, new, _ = atlas.kv_select(w, full, 200)
+        atlas.kv_compact(kp, vp, table, kept, new)
+        got.append((qr, out, crossed, w, one, kept, kp[table[0].long()], vp[table[0].long()]))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    del kp, vp, got
+    torch.cuda.empty_cache()

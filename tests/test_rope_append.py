@@ -298,3 +298,26 @@ def test_wrapper_refuses():
     wide = torch.zeros((2, 4, 3, 256), dtype=torch.bfloat16, device="cuda")[..., ::2]
     with pytest.raises(ValueError):
         atlas.kv_append_rope(*swap(0, wide))
+    with pytest.raises(ValueError):                    # one row for all: strides 0, 0, 0
+        atlas.kv_append_rope(*swap(0, q[:1, :1, :1].expand(2, 4, 3, 128)))
+    odd = torch.zeros(2 * 4 * 3 * 130, dtype=torch.bfloat16, device="cuda").view(2, 4, 3, 130)[..., :128]
+    with pytest.raises(atlas.AtlasError):              # rows that do not start on 16 bytes
+        atlas.kv_append_rope(*swap(0, odd))
+
+
+@gpu
+def test_broadcast_and_sliced_views_are_read_where_they_lie():
+    q, k, v, kp, vp, table, lens, pos = step("bf16", 2, 4, 2, 128, 16, 3, [0, 1], 2, 7)
+    heads = q[:, :1].expand(2, 4, 3, 128)              # one head's rows for all heads
+    a = atlas.kv_append_rope(heads, k, v, kp, vp, table, lens, pos)
+    assert torch.equal(a, atlas.kv_append_rope(heads.contiguous(), k, v, kp, vp, table, lens, pos))
+    wide = torch.zeros((2, 4, 9, 136), dtype=torch.bfloat16, device="cuda")
+    wide[:, :, 3:6, :128] = q
+    b = atlas.kv_append_rope(wide[:, :, 3:6, :128], k, v, kp, vp, table, lens, pos)
+    assert torch.equal(b, atlas.kv_append_rope(q, k, v, kp, vp, table, lens, pos))
+    one = k[:, :, 1:2]                                  # a single token out of several
+    kp2, vp2 = kp.clone(), vp.clone()
+    atlas.kv_append_rope(None, one, v[:, :, 1:2], kp, vp, table, lens, pos[:, :, 1:2].contiguous())
+    atlas.kv_append_rope(None, one.contiguous(), v[:, :, 1:2].contiguous(), kp2, vp2, table, lens,
+                         pos[:, :, 1:2].contiguous())
+    assert torch.equal(kp, kp2) and torch.equal(vp, vp2)
