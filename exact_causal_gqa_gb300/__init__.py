@@ -431,15 +431,15 @@ def _stream(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _check(device, **tensors):
-    """Every given tensor is a contiguous tensor of `device` and of the dtype given."""
-    for name, (t, dtype) in tensors.items():
+def _check(device, *tensors):
+    """Every given (name, tensor, dtype) is contiguous, of `device` and of that dtype."""
+    for name, t, dtype in tensors:
         if t is None:
             continue
-        if t.device != device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}")
+        if t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
 
 
 def _cuda_device(name, t):
@@ -462,16 +462,22 @@ def _frequencies(theta, rot_dim):
                                               for p in range(rot_dim // 2)))
 
 
+_Strides = ctypes.c_int64 * 3
+
+
 def _row_strides(name, t):
-    """Element strides (batch, head, token) of a [B][H][n][D] view with contiguous rows."""
+    """Element strides (batch, head, token) of a [B][H][n][D] view with contiguous rows;
+    all zero for a contiguous one."""
     if t.is_contiguous():
-        return (ctypes.c_int64 * 3)()
-    if t.stride(3) != 1:
+        return _Strides()
+    sb, sh, st, sd = t.stride()
+    if sd != 1:
         raise ValueError(f"{name} must have contiguous rows of head_dim elements")
-    strides = [0 if size == 1 else stride for size, stride in zip(t.shape[:3], t.stride())]
-    if not any(strides):  # the library reads all-zero strides as dense rows
+    nb, nh, nt, _ = t.shape
+    sb, sh, st = sb if nb > 1 else 0, sh if nh > 1 else 0, st if nt > 1 else 0
+    if not (sb or sh or st):  # the library reads all-zero strides as dense rows
         raise ValueError(f"{name} is one row broadcast to all: make it contiguous")
-    return (ctypes.c_int64 * 3)(*strides)
+    return _Strides(sb, sh, st)
 
 
 def kv_append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, positions, *,
@@ -489,49 +495,50 @@ def kv_append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, posi
     than (p, p + rot_dim / 2).  Returns the rotated queries [B][Hq][n][D] (q_out, which
     may be q itself when q is contiguous); None without q."""
     lib = load_library()
-    if k_new.dim() != 4 or v_new.shape != k_new.shape or k_pages.dim() != 4 or \
-            v_pages.shape != k_pages.shape or k_pages.shape[1] != k_new.shape[1] or \
-            k_pages.shape[3] != k_new.shape[3]:
+    shape, pool = k_new.shape, k_pages.shape
+    if len(shape) != 4 or v_new.shape != shape or len(pool) != 4 or v_pages.shape != pool or \
+            pool[1] != shape[1] or pool[3] != shape[3]:
         raise ValueError("k_new/v_new must be [B][Hkv][n][D], pools [pages][Hkv][P][D]")
-    B, Hkv, n, D = k_new.shape
-    dtype = k_pages.dtype
-    if q is not None and (q.dim() != 4 or q.shape[0] != B or q.shape[2:] != k_new.shape[2:]):
-        raise ValueError("q must be [B][Hq][n][D] like k_new")
-    device = _cuda_device("k_pages", k_pages)
-    for name, t in (("q", q), ("k_new", k_new), ("v_new", v_new)):
-        if t is not None and (t.device != device or t.dtype != dtype):
-            raise ValueError(f"{name} must be a {dtype} tensor on {device}")
+    B, Hkv, n, D = shape
+    device, dtype = _cuda_device("k_pages", k_pages), k_pages.dtype
     if positions.dim() == 2:
         positions = positions[None]
-    if positions.dim() != 3 or positions.shape[1:] != (B, n):
+    if positions.shape[1:] != (B, n):
         raise ValueError("positions must be [n_axes][B][n]")
-    _check(device, k_pages=(k_pages, dtype), v_pages=(v_pages, dtype),
-           page_table=(page_table, torch.int32), seq_lens=(seq_lens, torch.int32),
-           positions=(positions, torch.int32), n_new=(n_new, torch.int32),
-           q_out=(q_out, dtype), status=(status, torch.int32))
-    if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.numel() != B or \
+    for name, t in (("k_new", k_new), ("v_new", v_new), ("q", q)):
+        if t is not None and (t.dtype != dtype or t.device != device):
+            raise ValueError(f"{name} must be a {dtype} tensor on {device}")
+    _check(device, ("k_pages", k_pages, dtype), ("v_pages", v_pages, dtype),
+           ("page_table", page_table, torch.int32), ("seq_lens", seq_lens, torch.int32),
+           ("positions", positions, torch.int32), ("n_new", n_new, torch.int32),
+           ("q_out", q_out, dtype), ("status", status, torch.int32))
+    table = page_table.shape
+    if len(table) != 2 or table[0] != B or seq_lens.numel() != B or \
             (n_new is not None and n_new.numel() != B):
         raise ValueError("page_table must be [B][max_pages]; seq_lens and n_new [B]")
     rot_dim = D if rot_dim is None else rot_dim
     for name, x in (("pair_axis", pair_axis), ("inv_freq", inv_freq)):
         if x is not None and len(x) != rot_dim // 2:
             raise ValueError(f"{name} must have rot_dim / 2 entries")
-    if q_out is not None and (q is None or q_out.shape != q.shape):
-        raise ValueError("q_out must have q's shape")
-    if q_out is not None and q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
-        raise ValueError("q_out may be q itself only when q is contiguous")
-    R = _Rope()
-    R.batch, R.max_pages_per_seq, R.num_pages, R.max_new = B, page_table.shape[1], k_pages.shape[0], n
-    R.kv_dtype = _DTYPES.get(dtype, -1)
-    R.k_strides, R.v_strides = _row_strides("k_new", k_new), _row_strides("v_new", v_new)
-    R.n_q_heads = 0
+    R = _Rope(batch=B, max_pages_per_seq=table[1], num_pages=pool[0], max_new=n,
+              kv_dtype=_DTYPES.get(dtype, -1), k_strides=_row_strides("k_new", k_new),
+              v_strides=_row_strides("v_new", v_new), positions=positions.data_ptr(),
+              n_axes=positions.shape[0], rot_dim=rot_dim, interleaved=bool(interleaved),
+              theta=theta)
     if q is not None:
+        rows = q.shape
+        if len(rows) != 4 or rows[0] != B or rows[2:] != (n, D):
+            raise ValueError("q must be [B][Hq][n][D] like k_new")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
-        R.n_q_heads, R.q, R.q_out = q.shape[1], q.data_ptr(), q_out.data_ptr()
+            q_out = torch.empty(rows, dtype=dtype, device=device)
+        elif q_out.shape != rows:
+            raise ValueError("q_out must have q's shape")
+        R.n_q_heads, R.q, R.q_out = rows[1], q.data_ptr(), q_out.data_ptr()
         R.q_strides = _row_strides("q", q)
-    R.positions, R.n_axes = positions.data_ptr(), positions.shape[0]
-    R.rot_dim, R.interleaved, R.theta = rot_dim, int(bool(interleaved)), theta
+        if R.q_out == R.q and not q.is_contiguous():
+            raise ValueError("q_out may be q itself only when q is contiguous")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
     if pair_axis is not None:
         R.pair_axis = ctypes.addressof(_host_array(ctypes.c_int32, tuple(pair_axis)))
     freq = _frequencies(theta, rot_dim) if inv_freq is None else \
@@ -544,7 +551,7 @@ def kv_append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, posi
         rc = lib.atlas_kv_append_rope(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(),
                                       v_pages.data_ptr(), page_table.data_ptr(),
                                       seq_lens.data_ptr(), _ptr(n_new), Hkv, D,
-                                      k_pages.shape[2], ctypes.byref(R))
+                                      pool[2], ctypes.byref(R))
     if rc != 0:
         raise AtlasError(rc, status_string(rc))
     return q_out
@@ -582,10 +589,10 @@ def kv_weights(q, k_pages, page_table, seq_lens, lse, n_q_heads, n_kv_heads, hea
     if weights is None:
         weights = torch.zeros((B, n_kv_heads, page_table.shape[1] * page_tokens), device=q.device)
     device = _cuda_device("q", q)
-    _check(device, q=(q, q.dtype), k_pages=(k_pages, q.dtype), page_table=(page_table, torch.int32),
-           seq_lens=(seq_lens, torch.int32), lse=(lse, torch.float32),
-           weights=(weights, torch.float32), q_lens=(q_lens, torch.int32),
-           status=(status, torch.int32))
+    _check(device, ("q", q, q.dtype), ("k_pages", k_pages, q.dtype),
+           ("page_table", page_table, torch.int32), ("seq_lens", seq_lens, torch.int32),
+           ("lse", lse, torch.float32), ("weights", weights, torch.float32),
+           ("q_lens", q_lens, torch.int32), ("status", status, torch.int32))
     if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.numel() != B or \
             lse.numel() != q.shape[0] * q.shape[1] * q.shape[2] or weights.dim() != 3 or \
             weights.shape[:2] != (B, n_kv_heads) or (q_lens is not None and q_lens.numel() != B):
@@ -633,9 +640,9 @@ def kv_select(weights, seq_lens, budget, *, keep_first=0, keep_recent=0, kept=No
         kept_weights = torch.empty(shape, dtype=torch.float32, device=dev)
     if new_lens is None:
         new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-    _check(dev, weights=(weights, torch.float32), seq_lens=(seq_lens, torch.int32),
-           kept=(kept, torch.int32), kept_weights=(kept_weights, torch.float32),
-           new_lens=(new_lens, torch.int32), status=(status, torch.int32))
+    _check(dev, ("weights", weights, torch.float32), ("seq_lens", seq_lens, torch.int32),
+           ("kept", kept, torch.int32), ("kept_weights", kept_weights, torch.float32),
+           ("new_lens", new_lens, torch.int32), ("status", status, torch.int32))
     if kept.shape != shape or kept_weights.shape != shape or new_lens.numel() != B:
         raise ValueError("kept and kept_weights must be [B][Hkv][budget] and new_lens [B]")
     S = _Select()
@@ -660,10 +667,10 @@ def kv_compact(k_pages, v_pages, page_table, kept, new_lens, *, new_page_table=N
         raise ValueError("pools must be [num_pages][Hkv][P][D]")
     num_pages, Hkv, P, D = k_pages.shape
     device = _cuda_device("k_pages", k_pages)
-    _check(device, k_pages=(k_pages, k_pages.dtype), v_pages=(v_pages, k_pages.dtype),
-           page_table=(page_table, torch.int32), kept=(kept, torch.int32),
-           new_lens=(new_lens, torch.int32), new_page_table=(new_page_table, torch.int32),
-           status=(status, torch.int32))
+    _check(device, ("k_pages", k_pages, k_pages.dtype), ("v_pages", v_pages, k_pages.dtype),
+           ("page_table", page_table, torch.int32), ("kept", kept, torch.int32),
+           ("new_lens", new_lens, torch.int32), ("new_page_table", new_page_table, torch.int32),
+           ("status", status, torch.int32))
     if page_table.dim() != 2 or kept.dim() != 3 or \
             kept.shape[:2] != (page_table.shape[0], Hkv) or \
             new_lens.numel() != page_table.shape[0] or (new_page_table is not None and (

@@ -283,7 +283,7 @@ extern "C" atlas_status atlas_kv_append_rope(const void *k_new, const void *v_ne
         if (!(fabs(f) < HUGE_VAL)) return ATLAS_ERR_INVALID_ARG;
         const double turns = f / 6.283185307179586476925;
         const double part = turns - floor(turns);  // in [0, 1]; 1 only by rounding: no turn
-        p.turn[i] = part < 1.0 ? (uint64_t)ldexp(part, 64) : 0;
+        p.turn[i] = part < 1.0 ? (uint64_t)(part * 18446744073709551616.0) : 0;  // 2^64
     }
     const int64_t per16 = R->kv_dtype == ATLAS_BF16 ? 8 : 4;
     const int64_t n = R->max_new, D = head_dim;
