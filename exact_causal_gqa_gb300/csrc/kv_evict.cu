@@ -205,8 +205,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t bin = (k[e] >> shift) & mask;
-                    int same;
-                    __match_all_sync(0xffffffffu, in[e] ? bin : (uint32_t)kBins, &same);
+                    int same = 0;
+                    if (__all_sync(0xffffffffu, in[e])) __match_all_sync(0xffffffffu, bin, &same);
                     if (in[e] && (!same || lane == 0)) atomicAdd(&h[bin], same ? 32u : 1u);
                 }
             }
@@ -279,16 +279,13 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
     eq_before = __reduce_add_sync(0xffffffffu, eq_before);
     cluster_arrive_relaxed();  // this thread has read what it needs of the others
     uint32_t at = (uint32_t)lo + gt_before + min(want, eq_before);
-    // Exclusive sum over the lanes before this one, and the warp's total.
+    // Sum of v <= 4 over the lanes before this one, and the warp's total, bit by bit.
+    const uint32_t below = (1u << lane) - 1u;
     auto lanes_before = [&](uint32_t v, uint32_t &total) {
-        uint32_t sum = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += x;
-        }
-        total = __shfl_sync(0xffffffffu, sum, 31);
-        return sum - v;
+        const uint32_t b0 = __ballot_sync(0xffffffffu, v & 1), b1 = __ballot_sync(0xffffffffu, v & 2),
+                       b2 = __ballot_sync(0xffffffffu, v & 4);
+        total = __popc(b0) + 2 * __popc(b1) + 4 * __popc(b2);
+        return (uint32_t)(__popc(b0 & below) + 2 * __popc(b1 & below) + 4 * __popc(b2 & below));
     };
     for (int i0 = w0; i0 < w1; i0 += 128) {
         const int i = i0 + 4 * lane;
