@@ -306,8 +306,7 @@ cudaError_t launch_f32(const WeightsParams &p, cudaStream_t stream) {
            : cols <= 2  ? launch_warp<D, 2>(p, stream)
            : cols <= 4  ? launch_warp<D, 4>(p, stream)
            : cols <= 8  ? launch_warp<D, 8>(p, stream)
-           : cols <= 16 ? launch_ffma<D, 16>(p, stream)
-                        : launch_ffma<D, 64>(p, stream);
+                        : launch_ffma<D, 16>(p, stream);
 }
 
 atlas_status check(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const atlas_weights *W) {
@@ -327,11 +326,19 @@ atlas_status check(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const atlas_we
     return ATLAS_OK;
 }
 
-// fp32 has no plan to make: one CTA per 128 keys, no workspace.
-WeightsPlan plan_of(int32_t Hq, int32_t Hkv, int32_t P, const atlas_weights *W) {
-    if (W->dtype == ATLAS_F32) return WeightsPlan{};
-    return weights_tc_plan(W->batch, Hkv, Hq / Hkv, W->q_len, (int64_t)W->max_pages_per_seq * P,
-                           W->sm_count > 0 ? W->sm_count : device_sm_count());
+#ifndef F32TC
+#define F32TC 16
+#endif
+// fp32 with at most this many columns runs without the tensor cores and a plan.
+constexpr int64_t kF32Columns = F32TC;
+
+WeightsPlan plan_of(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const atlas_weights *W) {
+    const int sms = W->sm_count > 0 ? W->sm_count : device_sm_count();
+    const int64_t ctx = (int64_t)W->max_pages_per_seq * P;
+    const int G = Hq / Hkv;
+    if (W->dtype == ATLAS_BF16) return weights_tc_plan(W->batch, Hkv, G, W->q_len, ctx, sms);
+    if ((int64_t)G * W->q_len <= kF32Columns) return WeightsPlan{};
+    return weights_tf32x3_plan(W->batch, Hkv, G, W->q_len, D, ctx, sms);
 }
 
 }  // namespace
@@ -342,7 +349,7 @@ extern "C" {
 size_t atlas_kv_weights_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                                        int32_t page_tokens, const atlas_weights *W) {
     if (atlas::check(n_q_heads, n_kv_heads, head_dim, page_tokens, W) != ATLAS_OK) return SIZE_MAX;
-    return atlas::plan_of(n_q_heads, n_kv_heads, page_tokens, W).ws_bytes;
+    return atlas::plan_of(n_q_heads, n_kv_heads, head_dim, page_tokens, W).ws_bytes;
 }
 
 atlas_status atlas_kv_weights(const void *q, const void *k_pages, const int32_t *page_table,
@@ -359,7 +366,7 @@ atlas_status atlas_kv_weights(const void *q, const void *k_pages, const int32_t 
     if (!(fabsf(scale) < INFINITY)) return ATLAS_ERR_INVALID_ARG;
     const atlas_status st = check(n_q_heads, n_kv_heads, head_dim, page_tokens, W);
     if (st != ATLAS_OK) return st;
-    const WeightsPlan plan = plan_of(n_q_heads, n_kv_heads, page_tokens, W);
+    const WeightsPlan plan = plan_of(n_q_heads, n_kv_heads, head_dim, page_tokens, W);
     if (plan.ws_bytes > 0 && (!W->workspace || W->workspace_bytes < plan.ws_bytes))
         return ATLAS_ERR_WORKSPACE;
     WeightsParams p{};
@@ -388,15 +395,19 @@ atlas_status atlas_kv_weights(const void *q, const void *k_pages, const int32_t 
     const cudaStream_t stream = static_cast<cudaStream_t>(W->stream);
     (void)cudaGetLastError();
     cudaError_t err;
-    if (W->dtype == ATLAS_BF16) {
+    const bool bf16 = W->dtype == ATLAS_BF16;
+    if (bf16 || plan.parts > 0) {
         p.parts = static_cast<float *>(W->workspace);
         p.n_parts = plan.parts;
         p.tiles_per_part = plan.tiles_per_part;
         CUtensorMap tmQ, tmK;
-        if (encode_rows_map(&tmQ, q, (int64_t)p.B * p.Hq * p.q_len, head_dim, 128) != ATLAS_OK ||
-            encode_rows_map(&tmK, k_pages, (int64_t)p.num_pages * p.Hkv * p.P, head_dim, p.P) != ATLAS_OK)
+        if (encode_rows_map(&tmQ, q, (int64_t)p.B * p.Hq * p.q_len, head_dim, 128, !bf16) != ATLAS_OK)
             return ATLAS_ERR_CUDA;
-        err = launch_weights_tc(p, plan, head_dim, tmQ, tmK, stream);
+        if (bf16 && encode_rows_map(&tmK, k_pages, (int64_t)p.num_pages * p.Hkv * p.P, head_dim, p.P) !=
+                        ATLAS_OK)
+            return ATLAS_ERR_CUDA;
+        err = bf16 ? launch_weights_tc(p, plan, head_dim, tmQ, tmK, stream)
+                   : launch_weights_tf32x3(p, head_dim, tmQ, stream);
     } else {
         err = head_dim == 128 ? launch_f32<128>(p, stream) : launch_f32<64>(p, stream);
     }

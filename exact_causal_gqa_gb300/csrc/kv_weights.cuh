@@ -18,7 +18,7 @@ struct WeightsParams {
     int32_t B, Hq, Hkv, G, P, q_len, max_pages, num_pages, row_tokens;
     int32_t accumulate, window;
     float scale_log2, softcap_log2, softcap_inv;
-    float *parts;   // tensor-core path: [n_parts][B * Hkv][max_pages * P] partial sums
+    float *parts;   // tile kernels: [n_parts][B * Hkv][max_pages * P] partial sums
     int32_t n_parts, tiles_per_part;
     uint32_t *status;
 };
@@ -58,15 +58,20 @@ __device__ __forceinline__ float lse_log2(float lse) {
     return lse == -INFINITY ? INFINITY : lse * kLog2e;
 }
 
-// The bf16 kernels (kv_weights_tc.cu): workspace bytes, partial sums per key, launch.
+// How a call on the tensor cores runs, and the workspace it needs.
 struct WeightsPlan {
-    int stream;          // 1: few columns, K streamed past the resident queries
+    int stream;          // bf16: 1: few columns, K streamed past the resident queries
     int chunk_tiles;     // stream: 128-key tiles of a CTA
-    int parts, tiles_per_part;
+    int parts, tiles_per_part;  // tile kernels: query tiles split between CTAs
     size_t ws_bytes;
 };
+// bf16 (kv_weights_tc.cu).
 WeightsPlan weights_tc_plan(int B, int Hkv, int G, int q_len, int64_t ctx, int sms);
 cudaError_t launch_weights_tc(const WeightsParams &p, const WeightsPlan &plan, int D,
                               const CUtensorMap &tmQ, const CUtensorMap &tmK, cudaStream_t stream);
+// fp32 with many columns (kv_weights_tc_f32.cu).
+WeightsPlan weights_tf32x3_plan(int B, int Hkv, int G, int q_len, int D, int64_t ctx, int sms);
+cudaError_t launch_weights_tf32x3(const WeightsParams &p, int D, const CUtensorMap &tmQ,
+                                  cudaStream_t stream);
 
 }  // namespace atlas

@@ -21,17 +21,10 @@
 // Keys on a bad page, or behind the end, only fill lanes of their own, whose results are
 // dropped.  Every mbarrier wait is bounded; a CTA that gives up records
 // ATLAS_DEV_TIMEOUT, lets its copies and MMAs finish, frees TMEM and writes NaN.
-#include "kv_weights.cuh"
+#include "kv_weights_tc.cuh"
 
 namespace atlas {
 namespace {
-
-constexpr int BT = 128;           // keys per tile
-constexpr int kSlab = 128 * 128;  // one 64-element slab of a 128-row bf16 tile
-
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, kWaitLimitNs));
-}
 
 // One tile of 128 keys from kb (keys below `end`) into shared memory, page by page; the
 // whole warp calls it.  Boxes of bad pages are left out (`bar` counts the others' bytes).
@@ -65,55 +58,6 @@ __device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint32_t k_smem, u
     for (int kk = 0; kk < D / 16; ++kk)
         umma_bf16(d_tmem, kd + (((kk >> 2) * kSlab + (kk & 3) * 32) >> 4),
                   qd + (((kk >> 2) * q_slab + (kk & 3) * 32) >> 4), idesc, kk > 0);
-}
-
-// Barrier `id` of `threads` threads (whole warps) of the CTA.
-__device__ __forceinline__ void group_barrier(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// Adds 2^(s2 + neg_lse2[c]) of NC columns of scores; with kMasked, of those columns c that
-// key t is visible to (t < lim[c], and t >= lim[c] - window with a window).
-template <int NC, bool kMasked, bool kCapped>
-__device__ __forceinline__ void add_columns(const WeightsParams &p, const uint32_t (&s)[NC],
-                                            const float *neg_lse2, const int *lim, int t,
-                                            float2 (&sum)[2]) {
-    const float2 sc = make_float2(p.scale_log2, p.scale_log2);
-    const int far = p.window > 0 ? t + p.window : INT32_MAX;
-#pragma unroll
-    for (int c = 0; c < NC; c += 4) {
-        const float4 l4 = *reinterpret_cast<const float4 *>(neg_lse2 + c);
-        float2 a = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-        float2 b = make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-        if (kCapped) {
-            a = make_float2(score_log2(p, a.x) + l4.x, score_log2(p, a.y) + l4.y);
-            b = make_float2(score_log2(p, b.x) + l4.z, score_log2(p, b.y) + l4.w);
-        } else {
-            a = ffma2(a, sc, make_float2(l4.x, l4.y));
-            b = ffma2(b, sc, make_float2(l4.z, l4.w));
-        }
-        if (kMasked) {
-            const int4 m = *reinterpret_cast<const int4 *>(lim + c);
-            a.x = t < m.x && m.x <= far ? a.x : -INFINITY;
-            a.y = t < m.y && m.y <= far ? a.y : -INFINITY;
-            b.x = t < m.z && m.z <= far ? b.x : -INFINITY;
-            b.y = t < m.w && m.w <= far ? b.y : -INFINITY;
-        }
-        sum[0] = fadd2(sum[0], make_float2(ex2(a.x), ex2(a.y)));
-        sum[1] = fadd2(sum[1], make_float2(ex2(b.x), ex2(b.y)));
-    }
-}
-
-// The common case (no cap, every column visible) on a path of its own: compares and
-// selects computed and not used doubled the time of the prompt's kernel.
-template <int NC>
-__device__ __forceinline__ void add_weights(const WeightsParams &p, const uint32_t (&s)[NC],
-                                            const float *neg_lse2, const int *lim, int t, bool masked,
-                                            float2 (&sum)[2]) {
-    const bool capped = p.softcap_log2 > 0.f;
-    if (!masked && !capped) add_columns<NC, false, false>(p, s, neg_lse2, lim, t, sum);
-    else if (!capped) add_columns<NC, true, false>(p, s, neg_lse2, lim, t, sum);
-    else add_columns<NC, true, true>(p, s, neg_lse2, lim, t, sum);
 }
 
 // ---------------------------------------------------------------- few columns
@@ -407,58 +351,6 @@ struct TileCfg {
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-// The query tiles first .. end - 1 of a (sequence, kv head) that have a row which sees a
-// key of [kb, kb + kGroupKeys), in order: rows 128 j .. 128 j + 127 of its G * q_len
-// (q head, row) pairs, and the keys their real rows see.  The producer, the MMA warp and
-// the warp that brings the columns each walk this list.
-struct QueryTiles {
-    const WeightsParams &p;
-    const int L, qn, kb, end;
-    int j, i;              // tile, and its first row's place in its head
-    int n = -1;            // tiles taken before this one: ring position and phase
-    bool started = false;
-    bool whole = false;    // every row is real
-    int lim_min = 0, lim_max = 0;  // keys below: seen by the earliest / latest row
-
-    __device__ __forceinline__ QueryTiles(const WeightsParams &p_, int L_, int qn_, int kb_,
-                                          int first, int end_)
-        : p(p_), L(L_), qn(qn_), kb(kb_), end(end_), j(first - 1),
-          i((int)((int64_t)first * BT % p_.q_len)) {}
-
-    // Moves on to the next tile of the list; false at its end.
-    __device__ __forceinline__ bool next() {
-        for (;;) {
-            if (++j >= end) return false;
-            if (started) {
-                i += BT;
-                if (i >= p.q_len) i = p.q_len >= BT ? i - p.q_len : i % p.q_len;
-            }
-            started = true;
-            const int count = min(BT, p.G * p.q_len - j * BT);
-            const bool spans = i + count > p.q_len;
-            const int i0 = spans ? 0 : i;
-            const int i1 = min(spans ? p.q_len : i + count, qn) - 1;
-            if (i0 >= qn) continue;  // padding rows only
-            whole = count == BT && (qn == p.q_len || (!spans && i + count <= qn));
-            lim_min = L - qn + i0 + 1;
-            lim_max = L - qn + i1 + 1;
-            if (!seen(kb, kGroupKeys)) continue;
-            ++n;
-            return true;
-        }
-    }
-    __device__ __forceinline__ bool seen(int k0, int keys) const {
-        return sees(p, lim_min, lim_max, k0, keys);
-    }
-};
-
-// What the epilogue needs to know of a query tile, worked out once by the warp that
-// brings its columns.
-struct __align__(16) TileInfo {
-    int lim_min, lim_max;  // as in QueryTiles
-    int whole, stop;       // stop: no tile, the list has ended
-};
-
 // grid: items, the key groups of every (sequence, kv head) in ascending order (under a
 // causal mask the first groups have the most rows), the parts of one group together.
 template <int D>
@@ -520,7 +412,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);
     bool failed = false;
-    QueryTiles q(p, L, qn, kb0, q_begin, q_end);
+    QueryTiles q(p, L, qn, kb0, kGroupKeys, q_begin, q_end);
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
@@ -599,41 +491,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 1)
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------------------ lse and limits
-        for (bool more = true; more;) {
-            more = q.next();
-            const int n = more ? q.n : q.n + 1, s = n % S;
-            float v[4];
-            int m[4];
-            if (more) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int f = q.j * BT + e * 32 + lane;
-                    const int i = f % p.q_len;
-                    const bool real = f < p.G * p.q_len && i < qn;
-                    v[e] = real ? -lse_log2(p.lse[row0 + f]) : -INFINITY;
-                    m[e] = real ? L - qn + i + 1 : 0;
-                }
-            }
-            if (n >= S && !wait_warp(BAR(C::B_CEMPTY + s), ((n / S) - 1) & 1, abort_flag)) {
-                failed = true;
-                break;
-            }
-            if (more) {
-                float *nlse = reinterpret_cast<float *>(smem + C::OFF_LSE) + s * BT;
-                int *lim = reinterpret_cast<int *>(smem + C::OFF_LIM) + s * BT;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    nlse[e * 32 + lane] = v[e];
-                    lim[e * 32 + lane] = m[e];
-                }
-            }
-            if (lane == 0)
-                reinterpret_cast<TileInfo *>(smem + C::OFF_INFO)[s] =
-                    TileInfo{q.lim_min, q.lim_max, q.whole, !more};
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(C::B_CFULL + s));
-        }
-        if (failed && lane == 0) *abort_flag = 1;
+        failed = !bring_columns<S>(p, q, row0, smem, C::OFF_LSE, C::OFF_LIM, C::OFF_INFO,
+                                   BAR(C::B_CFULL), BAR(C::B_CEMPTY), 1, abort_flag);
     } else if (warp >= 4) {
         // ------------------------------------------------------------ epilogue
         const int x = (warp - 4) / 4, q4 = warp % 4;
@@ -717,23 +576,13 @@ __global__ void __launch_bounds__(256) weights_join_kernel(const WeightsParams p
     *w = (p.accumulate ? *w : 0.f) + sum;
 }
 
-cudaError_t configure(const void *kern, int bytes, int (&done)[64]) {
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    if (dev < 64 && done[dev]) return cudaSuccess;
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (err == cudaSuccess && dev < 64) done[dev] = 1;
-    return err;
-}
-
 template <int D, int N>
 cudaError_t launch_stream(const WeightsParams &p, int chunk_tiles, const CUtensorMap &tmK,
                           cudaStream_t stream) {
     using C = StreamCfg<D, N>;
     static int done[64] = {0};
     auto kern = weights_stream_kernel<D, N>;
-    const cudaError_t err = configure(reinterpret_cast<const void *>(kern), C::kSmem, done);
+    const cudaError_t err = configure_smem(reinterpret_cast<const void *>(kern), C::kSmem, done);
     if (err != cudaSuccess) return err;
     const int64_t ctx = (int64_t)p.max_pages * p.P, chunk = (int64_t)chunk_tiles * BT;
     const dim3 grid((unsigned)((ctx + chunk - 1) / chunk), (unsigned)p.Hkv, (unsigned)p.B);
@@ -755,45 +604,58 @@ cudaError_t launch_d(const WeightsParams &p, const WeightsPlan &plan, const CUte
     using C = TileCfg<D>;
     static int done[64] = {0};
     auto kern = weights_tile_kernel<D>;
-    cudaError_t err = configure(reinterpret_cast<const void *>(kern), C::kSmem, done);
+    cudaError_t err = configure_smem(reinterpret_cast<const void *>(kern), C::kSmem, done);
     if (err != cudaSuccess) return err;
     const int64_t ctx = (int64_t)p.max_pages * p.P, units = (int64_t)p.B * p.Hkv;
     const int64_t items = (ctx + kGroupKeys - 1) / kGroupKeys * units * p.n_parts;
     if (items > INT32_MAX) return cudaErrorInvalidValue;
     kern<<<(unsigned)items, C::kThreads, C::kSmem, stream>>>(tmQ, tmK, p);
     err = cudaGetLastError();
-    if (err == cudaSuccess && p.n_parts > 1) {
-        weights_join_kernel<<<dim3((unsigned)((ctx + 255) / 256), (unsigned)p.Hkv, (unsigned)p.B), 256,
-                              0, stream>>>(p);
-        err = cudaGetLastError();
-    }
-    return err;
+    return err == cudaSuccess && p.n_parts > 1 ? launch_weights_join(p, stream) : err;
 }
 
 }  // namespace
 
-// A pure function of the call's sizes.
-WeightsPlan weights_tc_plan(int B, int Hkv, int G, int q_len, int64_t ctx, int sms) {
-    WeightsPlan plan{};
-    const int64_t units = (int64_t)B * Hkv, cols = (int64_t)G * q_len;
-    const int64_t tiles = (ctx + BT - 1) / BT;
-    if (cols <= 256) {
-        // Shares of 1 to 32 tiles (4096 keys) that give each SM about 8 CTAs at the
-        // largest context.
-        plan.stream = 1;
-        int64_t chunk = tiles * units / ((int64_t)sms * 8);
-        plan.chunk_tiles = (int)(chunk < 1 ? 1 : chunk > 32 ? 32 : chunk);
-        return plan;
-    }
-    // Query tiles split until there are about 3 items per SM (one 8192-row prompt: 225 us;
-    // 2, 4, 6, 8 items 239, 228, 238, 245 us), none below 8 tiles.
+cudaError_t launch_weights_join(const WeightsParams &p, cudaStream_t stream) {
+    const int64_t ctx = (int64_t)p.max_pages * p.P;
+    weights_join_kernel<<<dim3((unsigned)((ctx + 255) / 256), (unsigned)p.Hkv, (unsigned)p.B), 256, 0,
+                          stream>>>(p);
+    return cudaGetLastError();
+}
+
+// Query tiles of 128 rows split between CTAs of `group_keys` keys until there are about 3
+// items per SM (one 8192-row bf16 prompt: 225 us; 2, 4, 6, 8 items 239, 228, 238, 245 us),
+// none below 8 tiles.
+static void split_query_tiles(WeightsPlan &plan, int64_t units, int64_t cols, int64_t ctx,
+                              int64_t group_keys, int sms) {
     const int64_t nq = (cols + BT - 1) / BT;
-    const int64_t items = (ctx + kGroupKeys - 1) / kGroupKeys * units;
+    const int64_t items = (ctx + group_keys - 1) / group_keys * units;
     int64_t parts = ((int64_t)sms * 3 + items - 1) / items;
     if (parts > (nq + 7) / 8) parts = (nq + 7) / 8;
     plan.tiles_per_part = (int)((nq + parts - 1) / parts);
     plan.parts = (int)((nq + plan.tiles_per_part - 1) / plan.tiles_per_part);
     plan.ws_bytes = plan.parts > 1 ? (size_t)plan.parts * units * ctx * sizeof(float) : 0;
+}
+
+// Pure functions of the call's sizes.
+WeightsPlan weights_tc_plan(int B, int Hkv, int G, int q_len, int64_t ctx, int sms) {
+    WeightsPlan plan{};
+    const int64_t units = (int64_t)B * Hkv, cols = (int64_t)G * q_len;
+    if (cols > 256) {
+        split_query_tiles(plan, units, cols, ctx, kGroupKeys, sms);
+        return plan;
+    }
+    // Shares of 1 to 32 tiles (4096 keys) that give each SM about 8 CTAs at the largest
+    // context.
+    plan.stream = 1;
+    const int64_t chunk = (ctx + BT - 1) / BT * units / ((int64_t)sms * 8);
+    plan.chunk_tiles = (int)(chunk < 1 ? 1 : chunk > 32 ? 32 : chunk);
+    return plan;
+}
+
+WeightsPlan weights_tf32x3_plan(int B, int Hkv, int G, int q_len, int D, int64_t ctx, int sms) {
+    WeightsPlan plan{};
+    split_query_tiles(plan, (int64_t)B * Hkv, (int64_t)G * q_len, ctx, 128 / D * BT, sms);
     return plan;
 }
 

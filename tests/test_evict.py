@@ -147,6 +147,11 @@ WEIGHTS = [
     ("f32", 6, 2, 64, 32, 100, [100, 333], dict(ragged=[100, 50])),
     ("f32", 2, 2, 64, 32, 3, [100, 333], dict(window=2 ** 31 - 1, ragged=[0, 2])),
     ("f32", 4, 2, 128, 16, 65, [400], dict(window=33, softcap=4.0)),
+    ("f32", 4, 1, 128, 64, 200, [200, 1000, 333], dict(ragged=[200, 3, 0])),
+    ("f32", 2, 1, 64, 16, 300, [700, 300, 511], {}),
+    ("f32", 8, 2, 128, 8, 40, [900, 41], dict(window=100)),
+    ("f32", 2, 1, 128, 128, 257, [257, 513], dict(scale=-0.06)),
+    ("f32", 3, 1, 64, 8, 5, [5, 300], {}),
 ]
 
 
