@@ -1,4 +1,4 @@
-// kv_weights.cuh -- what the attention-weight kernels (FFMA, tensor core) share.
+// kv_weights.cuh -- what the attention-weight kernels share.
 #pragma once
 
 #include "internal.h"
@@ -60,7 +60,7 @@ __device__ __forceinline__ float lse_log2(float lse) {
 
 // How a call on the tensor cores runs, and the workspace it needs.
 struct WeightsPlan {
-    int stream;          // bf16: 1: few columns, K streamed past the resident queries
+    int stream;          // 1: few columns, K streamed past the resident queries
     int chunk_tiles;     // stream: 128-key tiles of a CTA
     int parts, tiles_per_part;  // tile kernels: query tiles split between CTAs
     size_t ws_bytes;
@@ -69,9 +69,9 @@ struct WeightsPlan {
 WeightsPlan weights_tc_plan(int B, int Hkv, int G, int q_len, int64_t ctx, int sms);
 cudaError_t launch_weights_tc(const WeightsParams &p, const WeightsPlan &plan, int D,
                               const CUtensorMap &tmQ, const CUtensorMap &tmK, cudaStream_t stream);
-// fp32 with many columns (kv_weights_tc_f32.cu).
+// fp32 with more columns than weights_warp_kernel takes (kv_weights_tc_f32.cu).
 WeightsPlan weights_tf32x3_plan(int B, int Hkv, int G, int q_len, int D, int64_t ctx, int sms);
-cudaError_t launch_weights_tf32x3(const WeightsParams &p, int D, const CUtensorMap &tmQ,
-                                  cudaStream_t stream);
+cudaError_t launch_weights_tf32x3(const WeightsParams &p, const WeightsPlan &plan, int D,
+                                  const CUtensorMap &tmQ, const CUtensorMap &tmK, cudaStream_t stream);
 
 }  // namespace atlas

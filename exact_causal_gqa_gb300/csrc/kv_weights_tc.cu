@@ -653,9 +653,33 @@ WeightsPlan weights_tc_plan(int B, int Hkv, int G, int q_len, int64_t ctx, int s
     return plan;
 }
 
+// fp32.  Up to 256 columns K is streamed past 64 of them at a time, one launch each: at 8
+// sequences x 8 kv heads x 16384 keys of 128, 88 us for up to 16 columns, 105 for 64, 207
+// for 128, 414 for 256; the tile kernel takes 535, 535, 510 and 653 us, but 791 for 384
+// where the passes would take 620 and lose at smaller sizes (1 x 8 x 8192 keys: 45 us each
+// at 256 columns).  More than one pass also needs more key groups than SMs: with fewer the
+// tile kernel is done in one wave (2 x 8 x 1000 keys, 128 columns: 9.9 us, 14.1 by passes).
 WeightsPlan weights_tf32x3_plan(int B, int Hkv, int G, int q_len, int D, int64_t ctx, int sms) {
     WeightsPlan plan{};
-    split_query_tiles(plan, (int64_t)B * Hkv, (int64_t)G * q_len, ctx, 128 / D * BT, sms);
+    const int64_t units = (int64_t)B * Hkv, cols = (int64_t)G * q_len, group_keys = 128 / D * BT;
+    if (cols <= 64 || (cols <= 256 && (ctx + group_keys - 1) / group_keys * units > sms)) {
+        // The share of a CTA, 1 to 32 tiles, that takes least time in whole waves of one
+        // CTA an SM, its start-up counted as two tiles (against shares that give each SM
+        // about four: 88 and 93 us above, 8.7 and 16.5 at 1 x 8 x 8192 keys).
+        plan.stream = 1;
+        const int64_t tiles = (ctx + BT - 1) / BT;
+        int64_t best = INT64_MAX;
+        for (int c = 1; c <= 32; ++c) {
+            const int64_t ctas = (tiles + c - 1) / c * units;
+            const int64_t cost = (ctas + sms - 1) / sms * (c + 2);
+            if (cost < best) {
+                best = cost;
+                plan.chunk_tiles = c;
+            }
+        }
+        return plan;
+    }
+    split_query_tiles(plan, units, cols, ctx, group_keys, sms);
     return plan;
 }
 

@@ -12,6 +12,7 @@ rounds by 2^-24 of itself (below 2^-19).  Rounding errors add up like their squa
 rather than their number, so the tests hold the sums to 2e-5, a fifth of the worst case
 and twice what the attention calls' fp32 outputs are held to."""
 import ctypes
+import functools
 import math
 
 import numpy as np
@@ -152,6 +153,15 @@ WEIGHTS = [
     ("f32", 8, 2, 128, 8, 40, [900, 41], dict(window=100)),
     ("f32", 2, 1, 128, 128, 257, [257, 513], dict(scale=-0.06)),
     ("f32", 3, 1, 64, 8, 5, [5, 300], {}),
+    ("f32", 2, 1, 128, 8, 1, [1, 700], dict(window=300)),
+    ("f32", 2, 2, 64, 64, 2, [2, 129], dict(ragged=[0, 1])),
+    ("f32", 8, 2, 64, 128, 16, [2100, 16, 129], {}),
+    ("f32", 4, 1, 128, 16, 16, [5000, 17], dict(ragged=[16, 0], softcap=3.0)),
+    # more than 64 columns of fp32: planned for few SMs, K goes past them in several launches
+    ("f32", 4, 1, 128, 64, 60, [60, 1000, 333], dict(ragged=[60, 3, 0], sm_count=1)),
+    ("f32", 6, 2, 64, 8, 40, [900, 41], dict(window=100, sm_count=1)),
+    ("f32", 4, 2, 128, 16, 33, [400], dict(window=33, softcap=4.0, sm_count=2)),
+    ("f32", 2, 1, 64, 16, 128, [700, 128, 511], dict(ragged=[128, 33, 128], sm_count=1)),
 ]
 
 
@@ -170,7 +180,8 @@ def test_weights_match_the_plain_form(dtype, Hq, Hkv, D, P, q_len, lens, opt):
     T = dev[2].shape[1] * P + 5                              # rows longer than the table
     rng = np.random.default_rng(1)
     start = torch.from_numpy(rng.random((len(lens), Hkv, T), dtype=np.float32)).cuda()
-    kw = dict(q_lens=None if ragged is None else torch.tensor(ragged, dtype=torch.int32, device="cuda"), **var)
+    kw = dict(q_lens=None if ragged is None else torch.tensor(ragged, dtype=torch.int32, device="cuda"),
+              sm_count=opt.get("sm_count", 0), **var)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     args = (*dev, torch.from_numpy(lse).cuda(), Hq, Hkv, D, P, scale)
     fresh = atlas.kv_weights(*args, weights=start.clone(), accumulate=False, status=status, **kw)
@@ -189,7 +200,7 @@ def test_weights_match_the_plain_form(dtype, Hq, Hkv, D, P, q_len, lens, opt):
 
 
 @gpu
-@pytest.mark.parametrize("dtype,q_len", [("bf16", 1), ("bf16", 70), ("bf16", 300), ("f32", 1), ("f32", 70)])
+@pytest.mark.parametrize("dtype,q_len", [("bf16", 1), ("bf16", 70), ("bf16", 300), ("f32", 1), ("f32", 12), ("f32", 70)])
 def test_weights_of_the_attention_calls_lse_sum_to_the_rows(dtype, q_len):
     """Each row's weights sum to 1, so a (sequence, kv head) collects one per row."""
     q, k, dev = problem(dtype, 8, 2, 128, 16, q_len, [q_len + 400, q_len + 3], 9)
@@ -202,43 +213,45 @@ def test_weights_of_the_attention_calls_lse_sum_to_the_rows(dtype, q_len):
 
 
 @gpu
-@pytest.mark.parametrize("dtype,q_len", [("bf16", 2), ("bf16", 300), ("f32", 2), ("f32", 100)])
-def test_weights_of_rows_that_saw_nothing_and_of_bad_sequences(dtype, q_len):
+@pytest.mark.parametrize("dtype,q_len,sms", [("bf16", 2, 0), ("bf16", 300, 0), ("f32", 1, 0), ("f32", 2, 0),
+                                             ("f32", 100, 0), ("f32", 100, 1)])
+def test_weights_of_rows_that_saw_nothing_and_of_bad_sequences(dtype, q_len, sms):
     lens = [q_len + 50, q_len + 700, q_len + 10]
     q, k, dev = problem(dtype, 4, 2, 64, 16, q_len, lens, 3)
     lse = torch.from_numpy(np.float32(row_lse(widen(q), widen(k), lens, 0.125))).cuda()
     args = (4, 2, 64, 16, 0.125)
-    good = atlas.kv_weights(*dev, lse, *args)
+    kv_weights = functools.partial(atlas.kv_weights, sm_count=sms)
+    good = kv_weights(*dev, lse, *args)
     # one head of the first sequence saw nothing: it adds nothing
     none = lse.clone()
     none[0, 1] = -math.inf
     rest = lse.clone()
     rest[0, 1] = 1e30                                        # exp(s - 1e30) = 0
-    a, b = atlas.kv_weights(*dev, none, *args), atlas.kv_weights(*dev, rest, *args)
+    a, b = kv_weights(*dev, none, *args), kv_weights(*dev, rest, *args)
     assert torch.equal(a, b) and not torch.equal(a[0], good[0]) and torch.equal(a[1:], good[1:])
     for bad in (q_len - 1, -1, good.shape[2] + 1):
         bad_lens = dev[3].clone()
         bad_lens[1] = bad
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
-        w = atlas.kv_weights(*dev[:3], bad_lens, lse, *args, status=status, accumulate=False,
-                             weights=torch.full_like(good, 7.0))
+        w = kv_weights(*dev[:3], bad_lens, lse, *args, status=status, accumulate=False,
+                       weights=torch.full_like(good, 7.0))
         assert int(status.item()) == atlas.DEV_BAD_SEQLEN and (w[1] == 7).all()
         assert torch.equal(w[0, :, :lens[0]], good[0, :, :lens[0]])
         assert torch.equal(w[2, :, :lens[2]], good[2, :, :lens[2]])
     for bad in (-1, 3):
         counts = torch.tensor([q_len, bad if bad < 0 else q_len + 1, q_len], dtype=torch.int32, device="cuda")
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
-        atlas.kv_weights(*dev, lse, *args, status=status, q_lens=counts)
+        kv_weights(*dev, lse, *args, status=status, q_lens=counts)
         assert int(status.item()) == atlas.DEV_BAD_SEQLEN
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     short = torch.zeros((3, 2, lens[1] - 1), device="cuda")  # the weights' rows are too short for it
-    atlas.kv_weights(*dev, lse, *args, status=status, weights=short)
+    kv_weights(*dev, lse, *args, status=status, weights=short)
     assert int(status.item()) == atlas.DEV_BAD_SEQLEN and (short[1] == 0).all()
     table = dev[2].clone()
     table[1, 0] = dev[1].shape[0]
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    w = atlas.kv_weights(dev[0], dev[1], table, dev[3], lse, *args, status=status, accumulate=False,
-                         weights=torch.full_like(good, 7.0))
+    w = kv_weights(dev[0], dev[1], table, dev[3], lse, *args, status=status, accumulate=False,
+                   weights=torch.full_like(good, 7.0))
     assert int(status.item()) == atlas.DEV_BAD_PAGE and (w[1, :, :16] == 7).all()
     assert torch.equal(w[1, :, 512:lens[1]], good[1, :, 512:lens[1]])
     assert torch.equal(w[0, :, :lens[0]], good[0, :, :lens[0]])
