@@ -637,6 +637,24 @@ static void split_query_tiles(WeightsPlan &plan, int64_t units, int64_t cols, in
     plan.ws_bytes = plan.parts > 1 ? (size_t)plan.parts * units * ctx * sizeof(float) : 0;
 }
 
+// Share of a CTA that streams keys: the 1 to 32 tiles (4096 keys) that take least time, in
+// whole waves of `slots` CTAs at the largest context, a CTA's start-up counted as `startup`
+// tiles.
+static int share_tiles(int64_t units, int64_t ctx, int64_t slots, int startup) {
+    const int64_t tiles = (ctx + BT - 1) / BT;
+    int share = 1;
+    int64_t best = INT64_MAX;
+    for (int c = 1; c <= 32; ++c) {
+        const int64_t ctas = (tiles + c - 1) / c * units;
+        const int64_t cost = (ctas + slots - 1) / slots * (c + startup);
+        if (cost < best) {
+            best = cost;
+            share = c;
+        }
+    }
+    return share;
+}
+
 // Pure functions of the call's sizes.
 WeightsPlan weights_tc_plan(int B, int Hkv, int G, int q_len, int64_t ctx, int sms) {
     WeightsPlan plan{};
@@ -645,11 +663,11 @@ WeightsPlan weights_tc_plan(int B, int Hkv, int G, int q_len, int64_t ctx, int s
         split_query_tiles(plan, units, cols, ctx, kGroupKeys, sms);
         return plan;
     }
-    // Shares of 1 to 32 tiles (4096 keys) that give each SM about 8 CTAs at the largest
-    // context.
+    // (start-up counted as four tiles: weights at 8 x 8 x 16384 keys of 128 take 40 / 48 / 53
+    // / 74 us with 32 / 64 / 128 / 256 columns; with shares that give each SM about eight
+    // CTAs 44 / 68 / 81 / 114, and at 4 x 8 x 8192 keys 10 to 23 against 26 to 93)
     plan.stream = 1;
-    const int64_t chunk = (ctx + BT - 1) / BT * units / ((int64_t)sms * 8);
-    plan.chunk_tiles = (int)(chunk < 1 ? 1 : chunk > 32 ? 32 : chunk);
+    plan.chunk_tiles = share_tiles(units, ctx, (int64_t)sms * (cols <= 32 ? 2 : 1), 4);
     return plan;
 }
 
@@ -663,20 +681,9 @@ WeightsPlan weights_tf32x3_plan(int B, int Hkv, int G, int q_len, int D, int64_t
     WeightsPlan plan{};
     const int64_t units = (int64_t)B * Hkv, cols = (int64_t)G * q_len, group_keys = 128 / D * BT;
     if (cols <= 64 || (cols <= 256 && (ctx + group_keys - 1) / group_keys * units > sms)) {
-        // The share of a CTA, 1 to 32 tiles, that takes least time in whole waves of one
-        // CTA an SM, its start-up counted as two tiles (against shares that give each SM
-        // about four: 88 and 93 us above, 8.7 and 16.5 at 1 x 8 x 8192 keys).
+        // (start-up counted as two of its tiles)
         plan.stream = 1;
-        const int64_t tiles = (ctx + BT - 1) / BT;
-        int64_t best = INT64_MAX;
-        for (int c = 1; c <= 32; ++c) {
-            const int64_t ctas = (tiles + c - 1) / c * units;
-            const int64_t cost = (ctas + sms - 1) / sms * (c + 2);
-            if (cost < best) {
-                best = cost;
-                plan.chunk_tiles = c;
-            }
-        }
+        plan.chunk_tiles = share_tiles(units, ctx, sms, 2);
         return plan;
     }
     split_query_tiles(plan, units, cols, ctx, group_keys, sms);
