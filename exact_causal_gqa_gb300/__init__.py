@@ -540,7 +540,8 @@ def kv_append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, posi
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if pair_axis is not None:
-        R.pair_axis = ctypes.addressof(_host_array(ctypes.c_int32, tuple(pair_axis)))
+        axes = _host_array(ctypes.c_int32, tuple(pair_axis))  # (held until the call is over)
+        R.pair_axis = ctypes.addressof(axes)
     freq = _frequencies(theta, rot_dim) if inv_freq is None else \
         (ctypes.c_double * len(inv_freq))(*inv_freq)
     if freq is not None:
@@ -592,6 +593,7 @@ def kv_weights(q, k_pages, page_table, seq_lens, lse, n_q_heads, n_kv_heads, hea
     _check(device, ("q", q, q.dtype), ("k_pages", k_pages, q.dtype),
            ("page_table", page_table, torch.int32), ("seq_lens", seq_lens, torch.int32),
            ("lse", lse, torch.float32), ("weights", weights, torch.float32),
+           ("workspace", workspace, workspace.dtype if workspace is not None else None),
            ("q_lens", q_lens, torch.int32), ("status", status, torch.int32))
     if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.numel() != B or \
             lse.numel() != q.shape[0] * q.shape[1] * q.shape[2] or weights.dim() != 3 or \

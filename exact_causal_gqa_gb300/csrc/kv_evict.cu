@@ -36,6 +36,12 @@ __device__ __forceinline__ void record(uint32_t *status, uint32_t bit) {
     if (status) atomicOr(status, bit);
 }
 
+// Whether `n` bytes from a and `m` bytes from b have any in common.
+bool overlap(const void *a, uint64_t n, const void *b, uint64_t m) {
+    const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + m && y < x + n;
+}
+
 // ---------------------------------------------------------------- selection
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
@@ -540,6 +546,9 @@ atlas_status atlas_kv_select(const float *weights, const int32_t *seq_lens, int3
         S->budget > INT32_MAX / 2 || S->keep_first < 0 || S->keep_recent < 0 ||
         (int64_t)S->keep_first + S->keep_recent > S->budget)
         return ATLAS_ERR_INVALID_ARG;
+    const uint64_t floats = 4ull * S->batch * n_kv_heads;  // bytes per float of a row
+    if (S->kept_weights && overlap(weights, floats * S->row_tokens, S->kept_weights, floats * S->budget))
+        return ATLAS_ERR_INVALID_ARG;
     SelectParams p{};
     p.weights = weights;
     p.seq_lens = seq_lens;
@@ -601,6 +610,9 @@ atlas_status atlas_kv_compact(void *k_pages, void *v_pages, const int32_t *page_
     if (page_tokens < 1 || page_tokens > 128 || (page_tokens & (page_tokens - 1)))
         return ATLAS_ERR_UNSUPPORTED;
     if (C->kv_dtype != ATLAS_F32 && C->kv_dtype != ATLAS_BF16) return ATLAS_ERR_UNSUPPORTED;
+    const uint64_t pool = (uint64_t)C->num_pages * n_kv_heads * page_tokens * head_dim *
+                          (C->kv_dtype == ATLAS_BF16 ? 2 : 4);
+    if (!C->new_page_table && overlap(k_pages, pool, v_pages, pool)) return ATLAS_ERR_INVALID_ARG;
     CompactParams p{};
     p.k_pages = k_pages;
     p.v_pages = v_pages;

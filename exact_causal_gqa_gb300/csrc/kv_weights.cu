@@ -236,11 +236,14 @@ atlas_status atlas_kv_weights(const void *q, const void *k_pages, const int32_t 
         p.parts = static_cast<float *>(W->workspace);
         p.n_parts = plan.parts;
         p.tiles_per_part = plan.tiles_per_part;
-        CUtensorMap tmQ, tmK;
-        if (encode_rows_map(&tmQ, q, (int64_t)p.B * p.Hq * p.q_len, head_dim, 128, !bf16) != ATLAS_OK)
+        // (the stream kernels pack their columns themselves; the fp32 tile kernel reads K so)
+        CUtensorMap tmQ{}, tmK{};
+        if (!plan.stream &&
+            encode_rows_map(&tmQ, q, (int64_t)p.B * p.Hq * p.q_len, head_dim, 128, !bf16) != ATLAS_OK)
             return ATLAS_ERR_CUDA;
-        if (encode_rows_map(&tmK, k_pages, (int64_t)p.num_pages * p.Hkv * p.P, head_dim, p.P, !bf16) !=
-            ATLAS_OK)
+        if ((bf16 || plan.stream) &&
+            encode_rows_map(&tmK, k_pages, (int64_t)p.num_pages * p.Hkv * p.P, head_dim, p.P, !bf16) !=
+                ATLAS_OK)
             return ATLAS_ERR_CUDA;
         err = bf16 ? launch_weights_tc(p, plan, head_dim, tmQ, tmK, stream)
                    : launch_weights_tf32x3(p, plan, head_dim, tmQ, tmK, stream);

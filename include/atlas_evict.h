@@ -92,7 +92,8 @@ typedef struct {
     int32_t *kept;             /* [batch][n_kv_heads][budget], written */
     int32_t *new_lens;         /* [batch], written: min(seq_lens[b], budget) */
     float *kept_weights;       /* optional [batch][n_kv_heads][budget], written: the totals of
-                                  the kept keys; must not overlap weights */
+                                  the kept keys; overlapping weights is
+                                  ATLAS_ERR_INVALID_ARG */
     uint32_t *status_word;
     void *stream;
 } atlas_select;
@@ -129,7 +130,8 @@ typedef struct {
  * from new_lens[b] on are not written, nor are other pages.
  *   In place (new_page_table NULL): each kept row must be strictly ascending (as
  *     atlas_kv_select writes it), and the pages of the batch's sequences must not be
- *     shared with one another or with anyone who still needs them.
+ *     shared with one another or with anyone who still needs them.  The pools must be two
+ *     (overlapping ones are ATLAS_ERR_INVALID_ARG: each would move the other's rows).
  *   Into fresh pages: none of them may be a page that page_table's sequences use; kept
  *     rows may be in any order and repeat.  Shared pages (a common prefix) stay intact.
  * An index outside the sequence's table (in place: also one below its own j) or a

@@ -82,6 +82,8 @@ def call_select(lib, w=0x1000, lens=0x1000, Hkv=2, **kw):
                                 dict(keep_first=2 ** 31 - 1, keep_recent=2 ** 31 - 1),
                                 dict(kept=None), dict(new_lens=None), dict(w=None), dict(lens=None),
                                 dict(Hkv=0), dict(w=0x1001), dict(kept_weights=0x1002),
+                                dict(kept_weights=0x1000), dict(kept_weights=0x1000 + 4 * 2 * 2 * 100 - 4),
+                                dict(kept_weights=0x1000 - 4 * 2 * 2 * 10 + 4),
                                 dict(batch=70000), dict(budget=2 ** 31 - 1)])
 def test_select_refusals(lib, kw):
     assert call_select(lib, **kw) == 1
@@ -97,7 +99,9 @@ def call_compact(lib, ptrs=(0x1000,) * 5, Hkv=2, D=128, P=16, **kw):
     (dict(batch=0), 1), (dict(max_pages_per_seq=0), 1), (dict(num_pages=0), 1), (dict(max_kept=0), 1),
     (dict(new_page_table=0x1000), 1), (dict(Hkv=0), 1), (dict(Hkv=4096), 1), (dict(D=80), 2),
     (dict(P=12), 2), (dict(kv_dtype=3), 2), (dict(ptrs=(0x1008,) + (0x1000,) * 4), 1),
-    (dict(ptrs=(None,) + (0x1000,) * 4), 1), (dict(ptrs=(0x1000,) * 3 + (None, 0x1000)), 1)])
+    (dict(ptrs=(None,) + (0x1000,) * 4), 1),
+    (dict(ptrs=(0x1000,) * 5), 1), (dict(ptrs=(0x10000, 0x10000 + 8 * 2 * 16 * 256 - 16) + (0x1000,) * 3), 1),
+    (dict(ptrs=(0x1000,) * 3 + (None, 0x1000)), 1)])
 def test_compact_refusals(lib, kw, status):
     assert call_compact(lib, **kw) == status
 
@@ -421,9 +425,10 @@ def cut(w, k, v, table, lens, budget, **out):
 
 
 @gpu
-@pytest.mark.parametrize("q_len", [1, 40, 200])
-def test_captured_and_replayed_with_other_lengths(q_len):
-    q, k, dev = problem("bf16", 8, 2, 128, 16, q_len, [900, 700], 21)
+@pytest.mark.parametrize("dtype,q_len", [("bf16", 1), ("bf16", 40), ("bf16", 200), ("f32", 1), ("f32", 16),
+                                         ("f32", 200)])
+def test_captured_and_replayed_with_other_lengths(dtype, q_len):
+    q, k, dev = problem(dtype, 8, 2, 128, 16, q_len, [900, 700], 21)
     v_pages = torch.randn_like(dev[1])
     lse = torch.from_numpy(np.float32(row_lse(widen(q), widen(k), [900, 700], 0.09))).cuda()
     shape = (2, 2, dev[2].shape[1] * 16)
