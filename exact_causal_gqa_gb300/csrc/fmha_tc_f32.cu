@@ -39,7 +39,7 @@
 // Warp roles (384 threads, one CTA per SM):
 //   warp 0     TMA producer: Q once, then K and V blocks page by page through the
 //              page table.
-//   warp 1     allocates TMEM; one lane issues the MMAs:
+//   warp 1     allocates TMEM; one elected lane issues the MMAs:
 //                S  = Qhi K + Qlo K + Qhi Klo        (M=128, N=64, K=D; A from TMEM)
 //                O += P V^T + Plo V^T + P V^Tlo      (M=128, N=D, K=64; A from TMEM)
 //   warps 4-7  softmax, one thread per query row: Q into TMEM (hi, lo) at the start;
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint32_t sb = smem_u32(smem);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
 #define BAR(i) (sb + C::OFF_BAR + 8u * (uint32_t)(i))
 
     // ------------------------------------------------------------ work item
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     bool failed = false;
 
     if (warp == 0) {
@@ -383,80 +383,86 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // -------------------------------------------------------- MMA issuer
-        if (lane == 0) {
+        {
+            // The warp stays converged, one elected lane issues (elect_one).
             constexpr uint32_t idS = idesc_tf32_f32(BM, BN);
             constexpr uint32_t idPV = idesc_tf32_f32(BM, D);
-            bool ok = mbar_wait_bounded(BAR(C::B_QREADY), 0, abort_flag, kWaitLimitNs);
+            bool ok = wait_warp(BAR(C::B_QREADY), 0, abort_flag);
             tc_fence_after();
             const uint64_t klod = sdesc_sw128(sb + C::OFF_KLO, 16, 1024);
             const uint64_t vthd = sdesc_sw128(sb + C::OFF_VTH, 16, 1024);
             const uint64_t vtld = sdesc_sw128(sb + C::OFF_VTL, 16, 1024);
             for (int j = 0; ok && j < nb; ++j) {
                 const int s = j % S;
-                ok = mbar_wait_bounded(BAR(C::B_KFULL + s), (j / S) & 1, abort_flag, kWaitLimitNs) &&
-                     mbar_wait_bounded(BAR(C::B_KLO_READY), j & 1, abort_flag, kWaitLimitNs);
+                ok = wait_warp(BAR(C::B_KFULL + s), (j / S) & 1, abort_flag) &&
+                     wait_warp(BAR(C::B_KLO_READY), j & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 // S = Qlo K + Qhi Klo + Qhi K (small terms first).  K slice kk (8
                 // dims) sits 32 bytes into its 128-byte row, slab kk / 4 one K-slab on.
                 const uint64_t kd = sdesc_sw128(sb + C::OFF_K + s * C::kBlkBytes, 16, 1024);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 8; ++kk) {
-                    const uint32_t off = ((kk >> 2) * C::kKSlab + (kk & 3) * 32) >> 4;
-                    umma_tf32_tmem_a(tmem + C::SC, tmem + C::QL + 8 * kk, kd + off, idS, kk > 0);
-                }
+                    for (int kk = 0; kk < D / 8; ++kk) {
+                        const uint32_t off = ((kk >> 2) * C::kKSlab + (kk & 3) * 32) >> 4;
+                        umma_tf32_tmem_a(tmem + C::SC, tmem + C::QL + 8 * kk, kd + off, idS, kk > 0);
+                    }
 #pragma unroll
-                for (int kk = 0; kk < D / 8; ++kk) {
-                    const uint32_t off = ((kk >> 2) * C::kKSlab + (kk & 3) * 32) >> 4;
-                    umma_tf32_tmem_a(tmem + C::SC, tmem + C::QH + 8 * kk, klod + off, idS, 1u);
-                }
+                    for (int kk = 0; kk < D / 8; ++kk) {
+                        const uint32_t off = ((kk >> 2) * C::kKSlab + (kk & 3) * 32) >> 4;
+                        umma_tf32_tmem_a(tmem + C::SC, tmem + C::QH + 8 * kk, klod + off, idS, 1u);
+                    }
 #pragma unroll
-                for (int kk = 0; kk < D / 8; ++kk) {
-                    const uint32_t off = ((kk >> 2) * C::kKSlab + (kk & 3) * 32) >> 4;
-                    umma_tf32_tmem_a(tmem + C::SC, tmem + C::QH + 8 * kk, kd + off, idS, 1u);
+                    for (int kk = 0; kk < D / 8; ++kk) {
+                        const uint32_t off = ((kk >> 2) * C::kKSlab + (kk & 3) * 32) >> 4;
+                        umma_tf32_tmem_a(tmem + C::SC, tmem + C::QH + 8 * kk, kd + off, idS, 1u);
+                    }
+                    umma_commit(BAR(C::B_SFULL));
+                    umma_commit(BAR(C::B_KEMPTY + s));
+                    umma_commit(BAR(C::B_KLO_FREE));
                 }
-                umma_commit(BAR(C::B_SFULL));
-                umma_commit(BAR(C::B_KEMPTY + s));
-                umma_commit(BAR(C::B_KLO_FREE));
+                __syncwarp();
                 // O += P V^T + Plo V^T + P V^Tlo once the softmax wrote P and the
                 // converter built V^T.  Key slice kk (8 keys) of V^T sits 32 bytes into
                 // its 128-byte row, 32-key slab kk / 4 one V^T-slab further on.
-                ok = mbar_wait_bounded(BAR(C::B_PFULL), j & 1, abort_flag, kWaitLimitNs) &&
-                     mbar_wait_bounded(BAR(C::B_VT_READY), j & 1, abort_flag, kWaitLimitNs);
+                ok = wait_warp(BAR(C::B_PFULL), j & 1, abort_flag) &&
+                     wait_warp(BAR(C::B_VT_READY), j & 1, abort_flag);
                 // A new segment overwrites O: the previous one must have been read out.
                 const bool fresh = j % kSegBlocks == 0;
                 if (ok && fresh && j > 0)
-                    ok = mbar_wait_bounded(BAR(C::B_O_DRAINED), (j / kSegBlocks - 1) & 1,
-                                           abort_flag, kWaitLimitNs);
+                    ok = wait_warp(BAR(C::B_O_DRAINED), (j / kSegBlocks - 1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < BN / 8; ++kk) {
-                    const uint32_t off = ((kk >> 2) * C::kVtSlab + (kk & 3) * 32) >> 4;
-                    umma_tf32_tmem_a(tmem + C::OC, tmem + C::PL + 8 * kk, vthd + off, idPV,
-                                     (!fresh || kk > 0) ? 1u : 0u);
-                }
+                    for (int kk = 0; kk < BN / 8; ++kk) {
+                        const uint32_t off = ((kk >> 2) * C::kVtSlab + (kk & 3) * 32) >> 4;
+                        umma_tf32_tmem_a(tmem + C::OC, tmem + C::PL + 8 * kk, vthd + off, idPV,
+                                         (!fresh || kk > 0) ? 1u : 0u);
+                    }
 #pragma unroll
-                for (int kk = 0; kk < BN / 8; ++kk) {
-                    const uint32_t off = ((kk >> 2) * C::kVtSlab + (kk & 3) * 32) >> 4;
-                    umma_tf32_tmem_a(tmem + C::OC, tmem + C::SC + 8 * kk, vtld + off, idPV, 1u);
-                }
+                    for (int kk = 0; kk < BN / 8; ++kk) {
+                        const uint32_t off = ((kk >> 2) * C::kVtSlab + (kk & 3) * 32) >> 4;
+                        umma_tf32_tmem_a(tmem + C::OC, tmem + C::SC + 8 * kk, vtld + off, idPV, 1u);
+                    }
 #pragma unroll
-                for (int kk = 0; kk < BN / 8; ++kk) {
-                    const uint32_t off = ((kk >> 2) * C::kVtSlab + (kk & 3) * 32) >> 4;
-                    umma_tf32_tmem_a(tmem + C::OC, tmem + C::SC + 8 * kk, vthd + off, idPV, 1u);
+                    for (int kk = 0; kk < BN / 8; ++kk) {
+                        const uint32_t off = ((kk >> 2) * C::kVtSlab + (kk & 3) * 32) >> 4;
+                        umma_tf32_tmem_a(tmem + C::OC, tmem + C::SC + 8 * kk, vthd + off, idPV, 1u);
+                    }
+                    umma_commit(BAR(C::B_PVDONE));
+                    umma_commit(BAR(C::B_VT_FREE));
+                    // a segment followed by another one: the converter folds it
+                    if ((j + 1) % kSegBlocks == 0 && j + 1 < nb) umma_commit(BAR(C::B_SEG_DONE));
                 }
-                umma_commit(BAR(C::B_PVDONE));
-                umma_commit(BAR(C::B_VT_FREE));
-                // a segment followed by another one: the converter folds it
-                if ((j + 1) % kSegBlocks == 0 && j + 1 < nb) umma_commit(BAR(C::B_SEG_DONE));
+                __syncwarp();
             }
             if (!ok) {
                 failed = true;
                 *abort_flag = 1;
             }
             // Every MMA issued so far completes before TMEM is released.
-            umma_commit(BAR(C::B_FINAL));
+            if (elect_one()) umma_commit(BAR(C::B_FINAL));
             int no_abort = 0;
             mbar_wait_bounded(BAR(C::B_FINAL), 0, &no_abort, kWaitLimitNs);
         }
@@ -544,10 +550,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             mbar_arrive(BAR(C::B_VEMPTY + s));
             return true;
         };
-        // Order: V^T of block j; at a segment's first block the previous segment is
-        // read out of TMEM (the next PV overwrites it once every thread here has); K lo
-        // of block j + 1 (S(j + 1) waits for it); then the fold of that segment,
-        // O_run = O_run 2^(m_run - m_seg) + O_seg in fp32, off the S path.
+        // Order: V^T of block j; at a segment's first block the fold of the previous one,
+        // O_run = O_run 2^(m_run - m_seg) + O_seg in fp32 (the next PV overwrites it once
+        // every thread here has read it); K lo of block j + 1 (S(j + 1) waits for it).  The
+        // fold takes 64 columns at a time: holding all 128 until K lo was made kept it off
+        // the S path, but cost registers that were spilled in the conversions (suffix, 16
+        // rows x 8 q heads per kv head at 4K-64K keys: 1.68 -> 0.91 ms; 1500 rows x 32 heads
+        // x 4 sequences on 4000 shared keys 2.85 -> 2.39 ms).
         ok = ok && convert_k(0);
         for (int j = 0; ok && j < nb; ++j) {
             if (!convert_v(j)) {
@@ -556,8 +565,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             }
             const bool fold = j % kSegBlocks == 0 && j > 0;
             const int g = j / kSegBlocks - 1;  // the segment folded at block j
-            uint32_t o[D / 32][32];
-            float m_seg = -INFINITY;
             if (fold) {
                 if (!wait_warp(BAR(C::B_SEG_DONE), g & 1, abort_flag) ||
                     !wait_warp(BAR(C::B_MSEG), g & 1, abort_flag)) {
@@ -565,39 +572,42 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     break;
                 }
                 tc_fence_after();
+                const float m_seg = m_seg_s[(g & 1) * BM + r];
+                const float fr = g == 0 || m_run == -INFINITY ? 0.f : ex2(m_run - m_seg);
+                constexpr int kCols = 64;
 #pragma unroll
-                for (int cc = 0; cc < D / 32; ++cc) tmem_ld32(tq + 32 * cc, o[cc]);
-                tmem_wait_ld();
-                m_seg = m_seg_s[(g & 1) * BM + r];
-                tc_fence_before();
-                mbar_arrive(BAR(C::B_O_DRAINED));
-            }
-            if (j + 1 < nb && !convert_k(j + 1)) {
-                ok = false;
-                break;
-            }
-            if (fold) {
-                if (row_ok) {
-                    const float fr = g == 0 || m_run == -INFINITY ? 0.f : ex2(m_run - m_seg);
+                for (int c0 = 0; c0 < D; c0 += kCols) {
+                    uint32_t o[kCols / 32][32];
+                    float4 *dst = reinterpret_cast<float4 *>(run + c0);
+                    float4 x[kCols / 4];
 #pragma unroll
-                    for (int cc = 0; cc < D / 32; ++cc) {
-                        float4 *dst = reinterpret_cast<float4 *>(run + cc * 32);
+                    for (int cc = 0; cc < kCols / 32; ++cc) tmem_ld32(tq + c0 + 32 * cc, o[cc]);
+                    if (row_ok && g > 0) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 a = make_float4(
-                                __uint_as_float(o[cc][4 * k]), __uint_as_float(o[cc][4 * k + 1]),
-                                __uint_as_float(o[cc][4 * k + 2]), __uint_as_float(o[cc][4 * k + 3]));
-                            if (g == 0) {
-                                dst[k] = a;
-                            } else {
-                                const float4 x = dst[k];
-                                dst[k] = make_float4(fmaf(x.x, fr, a.x), fmaf(x.y, fr, a.y),
-                                                     fmaf(x.z, fr, a.z), fmaf(x.w, fr, a.w));
-                            }
+                        for (int k = 0; k < kCols / 4; ++k) x[k] = dst[k];
+                    }
+                    tmem_wait_ld();
+                    if (c0 + kCols == D) {
+                        tc_fence_before();
+                        mbar_arrive(BAR(C::B_O_DRAINED));
+                    }
+                    if (row_ok) {
+#pragma unroll
+                        for (int k = 0; k < kCols / 4; ++k) {
+                            const uint32_t *e = &o[k / 8][4 * (k % 8)];
+                            const float4 a = make_float4(__uint_as_float(e[0]), __uint_as_float(e[1]),
+                                                         __uint_as_float(e[2]), __uint_as_float(e[3]));
+                            dst[k] = g == 0 ? a
+                                            : make_float4(fmaf(x[k].x, fr, a.x), fmaf(x[k].y, fr, a.y),
+                                                          fmaf(x[k].z, fr, a.z), fmaf(x[k].w, fr, a.w));
                         }
                     }
                 }
                 m_run = m_seg;
+            }
+            if (j + 1 < nb && !convert_k(j + 1)) {
+                ok = false;
+                break;
             }
         }
         if (ok && (nb - 1) / kSegBlocks > 0) {
