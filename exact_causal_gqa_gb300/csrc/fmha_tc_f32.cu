@@ -586,7 +586,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < kCols / 4; ++k) x[k] = dst[k];
                     }
-                    tmem_wait_ld();
+#pragma unroll
+                    for (int cc = 0; cc < kCols / 32; ++cc) tmem_wait_ld32(o[cc]);
                     if (c0 + kCols == D) {
                         tc_fence_before();
                         mbar_arrive(BAR(C::B_O_DRAINED));

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(StreamCfg<D, N>::kThreads, StreamCfg<D, N>::kC
             if (N == 16) {
                 uint32_t s[16];
                 tmem_ld16(ts, s);
-                tmem_wait_ld();
+                tmem_wait_ld16(s);
                 tc_fence_before();
                 mbar_arrive(BAR(C::B_SEMPTY + buf));
                 add_weights<16>(p, s, nlse, lim, t, masked || ncols < 16, sum);

@@ -11,13 +11,13 @@
 // Layout as in the bf16 kernels: keys on M, one per TMEM lane, so that a thread sums along
 // its own columns, and the split keys in tensor memory as A operands.
 //
-// weights_stream_tf32x3_kernel, few columns (decode, observer rows): 64 packed columns, hi
-//   rows above lo rows, stay in shared memory as one B operand; a CTA streams the keys of
+// weights_stream_tf32x3_kernel, few columns (decode, observer rows): 64 packed columns stay
+//   in shared memory as rows of zeros, hi and lo parts; a CTA streams the keys of
 //   its share of the context past them in slabs of 128 keys x 32 elements.  A slab arrives
-//   raw by TMA (nine in flight: 144 KB), a converter thread splits its key's 128 bytes into
-//   one of four TMEM slots, and two products make of it K_hi . [Q_hi | Q_lo] -- main and
-//   small terms side by side -- and K_lo . Q_hi.  Keeping the two sums apart costs one
-//   addition per score in the epilogue and saves a third of the products' instructions.
+//   raw by TMA (seven in flight: 112 KB), a converter thread splits its key's 128 bytes into
+//   one of four TMEM slots, and two products make of it K_hi . [Q_hi | Q_lo] and
+//   K_lo . [0 | Q_hi], main and small terms side by side.  Keeping the two sums apart costs
+//   one addition per score in the epilogue and saves a third of the products.
 //   Bound by K's bytes up to 16 columns (8 sequences x 8 kv heads x 16384 keys of 128: 88
 //   us, 6.1 TB/s; head_dim 64: 58 us, 4.7 TB/s) and by the products at 64 (105 us).  More
 //   columns take a launch per 64, which add up in order.
@@ -64,8 +64,8 @@ struct StreamCfg {
     static constexpr int N = 64;                      // columns of one pass
     static constexpr int kSlabs = D / 32;
     static constexpr int kSlabBytes = BT * 128;       // 32 elements of 128 keys
-    static constexpr int kQSlab = 2 * N * 128;        // 32 elements of the hi and the lo rows
-    static constexpr int S = 9;                       // raw slabs in flight
+    static constexpr int kQSlab = 3 * N * 128;        // 32 elements of zero, hi and lo rows
+    static constexpr int S = 7;                       // raw slabs in flight
     static constexpr int kChunks = 4;                 // split slabs in TMEM
     static constexpr int kThreads = 512;
     static constexpr int OFF_Q = S * kSlabBytes;
@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(StreamCfg<D>::kThreads, 1)
         fence_barrier_init();
     }
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
-    // The columns, packed (column c is row c % qn of head c / qn) and zero-filled to the
-    // product's N: hi parts in rows 0 .. nmma - 1, lo parts below them.
+    // The columns, packed (column c is row c % qn of head c / qn) and zero-filled to nmma:
+    // nmma rows of zeros, then the hi parts, then the lo parts.
     const int64_t row0 = ((int64_t)b * p.Hq + (int64_t)hkv * p.G) * p.q_len;
     for (int i = threadIdx.x; i < nmma * (D / 4); i += C::kThreads) {
         const int c = i / (D / 4), ch = i % (D / 4), f = col0 + c;
@@ -159,8 +159,9 @@ __global__ void __launch_bounds__(StreamCfg<D>::kThreads, 1)
                                                   (row0 + (int64_t)(f / qn) * p.q_len + f % qn) * D + ch * 4);
         const float4 h = make_float4(tf32_hi(v.x), tf32_hi(v.y), tf32_hi(v.z), tf32_hi(v.w));
         uint8_t *slab = smem + C::OFF_Q + (ch / 8) * C::kQSlab;
-        *reinterpret_cast<float4 *>(slab + sw128(c, ch % 8)) = h;
-        *reinterpret_cast<float4 *>(slab + sw128(nmma + c, ch % 8)) =
+        *reinterpret_cast<float4 *>(slab + sw128(c, ch % 8)) = make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(slab + sw128(nmma + c, ch % 8)) = h;
+        *reinterpret_cast<float4 *>(slab + sw128(2 * nmma + c, ch % 8)) =
             make_float4(v.x - h.x, v.y - h.y, v.z - h.z, v.w - h.w);
     }
     for (int c = threadIdx.x; c < C::N; c += C::kThreads) {
@@ -213,7 +214,8 @@ __global__ void __launch_bounds__(StreamCfg<D>::kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        const uint32_t idesc2 = idesc_tf32_f32(128, 2 * nmma), idesc = idesc_tf32_f32(128, nmma);
+        const uint32_t idesc = idesc_tf32_f32(128, 2 * nmma);
+        const uint32_t q_hi = (uint32_t)nmma * 128 >> 4;  // the hi rows, in descriptor units
         bool ok = true;
         for (int g = 0; ok && g < n_slabs; ++g) {
             const int j = g / C::kSlabs, sl = g % C::kSlabs, buf = j & 1, k = g % C::kChunks;
@@ -223,15 +225,17 @@ __global__ void __launch_bounds__(StreamCfg<D>::kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                // K_hi . [Q_hi | Q_lo] into main and small terms at once, then K_lo . Q_hi
+                // K_hi . [Q_hi | Q_lo] and K_lo . [0 | Q_hi] into [main | small] terms: only
+                // products of one accumulator and one shape are sure to run in order, which
+                // K_lo . Q_hi into the small columns alone would not be
                 const uint32_t d = tmem + C::SCORES + buf * 128, a = tmem + 64 * k;
                 const uint64_t qd = sdesc_sw128(sb + C::OFF_Q + sl * C::kQSlab, 16, 1024);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_tf32_tmem_a(d, a + 8 * kk, qd + 2 * kk, idesc2, sl > 0 || kk > 0);
+                    umma_tf32_tmem_a(d, a + 8 * kk, qd + q_hi + 2 * kk, idesc, sl > 0 || kk > 0);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_tf32_tmem_a(d + nmma, a + 32 + 8 * kk, qd + 2 * kk, idesc, 1u);
+                    umma_tf32_tmem_a(d, a + 32 + 8 * kk, qd + 2 * kk, idesc, 1u);
                 umma_commit(BAR(C::B_FREE + k));
                 if (sl == C::kSlabs - 1) umma_commit(BAR(C::B_SFULL + buf));
             }
@@ -268,8 +272,6 @@ __global__ void __launch_bounds__(StreamCfg<D>::kThreads, 1)
                     l[4 * ch + e] = __float_as_uint(x[e] - tf32_hi(x[e]));
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(C::B_EMPTY + s));
             if (g >= C::kChunks && !wait_warp(BAR(C::B_FREE + k), (g / C::kChunks - 1) & 1, abort_flag)) {
                 failed = true;
                 break;
@@ -277,6 +279,11 @@ __global__ void __launch_bounds__(StreamCfg<D>::kThreads, 1)
             tc_fence_after();
             tmem_st32(tl + 64 * k, h);
             tmem_st32(tl + 64 * k + 32, l);
+            // Free the raw slab only now, its values in use: right after the loads, some were
+            // still on their way when the copy of a later slab landed (a few keys wrong in a
+            // million, most on cold data).
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::B_EMPTY + s));
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(BAR(C::B_READY + k));
@@ -318,7 +325,8 @@ __global__ void __launch_bounds__(StreamCfg<D>::kThreads, 1)
                 uint32_t v[16], u[16];
                 tmem_ld16(ts + c0, v);
                 tmem_ld16(ts + nmma + c0, u);
-                tmem_wait_ld();
+                tmem_wait_ld16(v);
+                tmem_wait_ld16(u);
                 if (c0 + 16 >= nmma) {  // all read: the next product may overwrite them
                     tc_fence_before();
                     mbar_arrive(BAR(C::B_SEMPTY + buf));

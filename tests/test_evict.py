@@ -261,6 +261,36 @@ def test_weights_of_rows_that_saw_nothing_and_of_bad_sequences(dtype, q_len, sms
     assert torch.equal(w[0, :, :lens[0]], good[0, :, :lens[0]])
 
 
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,Hkv,G,D,P,q_len,L", [(3, 8, 4, 128, 64, 64, 5000), (3, 8, 4, 64, 64, 64, 5000),
+                                                 (6, 4, 8, 128, 32, 9, 9000), (4, 8, 4, 64, 16, 1, 9000)])
+def test_weights_are_the_same_each_time_whatever_the_caches_hold(dtype, B, Hkv, G, D, P, q_len, L):
+    """Many CTAs streaming a long context, from a cold L2 and from a warm one: copies land
+    late or early, the bits stay, and they are the plain form's within its tolerance."""
+    g = torch.Generator(device="cuda").manual_seed(L + D)
+    pages = -(-L // P)
+    k = torch.randn((B * pages, Hkv, P, D), generator=g, device="cuda").to(DT[dtype])
+    q = torch.randn((B, Hkv * G, q_len, D), generator=g, device="cuda").to(DT[dtype])
+    table = torch.randperm(B * pages, generator=g, device="cuda").int().reshape(B, pages)
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    rows = k[table.long()].transpose(1, 2).reshape(B, Hkv, pages * P, D)[:, :, :L].double()
+    s = (q.double().reshape(B, Hkv, G * q_len, D) @ rows.transpose(2, 3) * D ** -0.5).reshape(B, Hkv, G, q_len, L)
+    pos = torch.arange(L - q_len, L, device="cuda")[:, None]
+    s = s.masked_fill(torch.arange(L, device="cuda")[None] > pos, -math.inf)
+    lse = torch.logsumexp(s, -1).float()
+    want = torch.exp(s - lse.double()[..., None]).sum((2, 3))
+    cold = torch.empty(100_000_000, device="cuda")           # 400 MB: more than the L2
+    first = None
+    for n in range(12):
+        if n % 2 == 0:
+            cold.fill_(n)
+        w = atlas.kv_weights(q, k, table, lens, lse.reshape(B, Hkv * G, q_len), Hkv * G, Hkv, D, P, D ** -0.5)
+        first = w if first is None else first
+        assert torch.equal(w, first)
+    assert ((first[:, :, :L].double() - want).abs() <= W_REL * want + 1e-30).all()
+
+
 # ------------------------------------------------------------------ selection
 def totals(kind, B, Hkv, T, seed):
     r = np.random.default_rng(seed)
