@@ -15,6 +15,11 @@
 // A direct prefill with more tile pairs than SMs runs persistent CTAs instead (the
 // PERSIST instance): one per SM, each walking its share of the tile pairs with every
 // role's barrier phases running on from one item to the next.
+// Cross attention (atlas_attn_cross) runs here too.  Its rows all see the same keys, so any
+// two neighbouring tiles of a (sequence, kv head) share their blocks as a pair, and a direct
+// call takes the sequences longest-first: 4 sequences of up to 1500 rows x 32 heads of 128 on
+// 3000 to 8192 states take 533 us, 1.24 PFLOP/s (567 us in the batch's order), bound as the
+// prefill is by each tile's chain of products and softmax.
 //
 // Warp roles (128 + NT*128 threads, one CTA per SM):
 //   warp 0    TMA producer: the Q tiles once, then K blocks gathered page by page

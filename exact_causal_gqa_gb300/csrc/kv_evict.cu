@@ -10,7 +10,9 @@
 // is taken by lowest index, so the set never depends on timing, and positions in the
 // ascending output are counts of kept keys before (ballots in a warp, sums over warps and
 // CTAs).  Memory: 4 bytes per key in, 8 per kept key out; bound by latency: a load, four
-// cluster barriers, and per digit a pass over the keys in shared memory and a scan.
+// cluster barriers, and per digit a pass over the keys in shared memory and a scan.  8 x 8
+// rows of up to 32768 keys, 4096 kept: 18.5 us; one sequence's 8 rows of 131072 keys, half
+// kept: 23 us.
 //
 // Compaction.  Rows of head_dim elements move between page slots, 16 bytes per thread and
 // step.  Into fresh pages every row is independent.  In place, row j takes row kept[j] >= j:
@@ -21,7 +23,11 @@
 // shares the rows of one (sequence, kv head, K or V): its barrier stands between reading a
 // chunk and writing it, arrived at one chunk ahead, with four chunks in flight (cp.async);
 // indices and page tables come through shared memory, so that nothing but the data's own
-// latency is in the loop.
+// latency is in the loop.  Both are bound by DRAM's turning between reads and writes of
+// 256-byte rows (4.4 to 4.8 TB/s of traffic): 64 sequences' 4096 rows a head into fresh pages
+// (8 x 8 heads of 128 bf16) 44 us; 65536 of 131072 rows in place 116 us (strips of 64 bytes
+// a warp 382, a cp.async ring per CTA 199, clusters of 8 with releasing arrivals 240,
+// relaxed 160, four pieces a thread 121, four stages 116).
 #include "internal.h"
 #include "ptx.cuh"
 

@@ -10,13 +10,19 @@
 //
 // weights_stream_kernel, at most 256 columns (decode, observer rows): the columns stay in
 //   shared memory, packed so that only real rows take part, and a CTA streams the 128-key
-//   tiles of its share of the context past them.  Bound by K's bytes.
+//   tiles of its share of the context past them.  Bound by K's bytes up to 128 columns: 8
+//   sequences x 8 kv heads x 32768 keys of 128 (537 MB) take 82 us with up to 32 columns
+//   (6.5 TB/s), 91 with 64, 95 with 128; beyond, products, exponentials and loads no longer
+//   fit side by side: 115 us with 192, 132 with 256 (leaving out the exponentials 123, the
+//   products 126, both 102).
 // weights_tile_kernel, more columns (a prompt's rows): a CTA keeps 512 keys (four tiles)
 //   and streams 128-row query tiles past them, each loaded once for four products; query
-//   tiles no key of the CTA is visible to are not loaded.  Bound by the exponentials and
-//   the tensor core.  When (sequence, kv head) x 512-key groups alone would not fill the
-//   GPU, the query tiles are split between CTAs; their sums per key go to the workspace
-//   and weights_join_kernel adds them in order.
+//   tiles no key of the CTA is visible to are not loaded.  Bound by the products (operands
+//   from shared memory: 65 clocks per 128 x 128 x 16, as long as one of 64 columns) and the
+//   exponentials, each busy 54 % of the time: an 8192-row prompt of 32 heads over 8 kv heads
+//   of 128 takes 226 us, 1.22 PFLOP/s of scores.  When (sequence, kv head) x 512-key groups
+//   alone would not fill the GPU, the query tiles are split between CTAs; their sums per key
+//   go to the workspace and weights_join_kernel adds them in order.
 //
 // Keys on a bad page, or behind the end, only fill lanes of their own, whose results are
 // dropped.  Every mbarrier wait is bounded; a CTA that gives up records
@@ -672,9 +678,9 @@ WeightsPlan weights_tc_plan(int B, int Hkv, int G, int q_len, int64_t ctx, int s
 }
 
 // fp32.  Up to 256 columns K is streamed past 64 of them at a time, one launch each: at 8
-// sequences x 8 kv heads x 16384 keys of 128, 88 us for up to 16 columns, 105 for 64, 207
-// for 128, 414 for 256; the tile kernel takes 535, 535, 510 and 653 us, but 791 for 384
-// where the passes would take 620 and lose at smaller sizes (1 x 8 x 8192 keys: 45 us each
+// sequences x 8 kv heads x 16384 keys of 128, 88 us for up to 16 columns, 100 for 64, 200
+// for 128, 397 for 256; the tile kernel takes 535, 535, 510 and 653 us, but 791 for 384
+// where the passes would take 600 and lose at smaller sizes (1 x 8 x 8192 keys: 45 us each
 // at 256 columns).  More than one pass also needs more key groups than SMs: with fewer the
 // tile kernel is done in one wave (2 x 8 x 1000 keys, 128 columns: 9.9 us, 14.1 by passes).
 WeightsPlan weights_tf32x3_plan(int B, int Hkv, int G, int q_len, int D, int64_t ctx, int sms) {

@@ -19,7 +19,7 @@
 //   K_lo . [0 | Q_hi], main and small terms side by side.  Keeping the two sums apart costs
 //   one addition per score in the epilogue and saves a third of the products.
 //   Bound by K's bytes up to 16 columns (8 sequences x 8 kv heads x 16384 keys of 128: 88
-//   us, 6.1 TB/s; head_dim 64: 58 us, 4.7 TB/s) and by the products at 64 (105 us).  More
+//   us, 6.1 TB/s; head_dim 64: 58 us, 4.7 TB/s) and by the products at 64 (100 us).  More
 //   columns take a launch per 64, which add up in order.
 //
 // weights_tf32x3_kernel, many columns (a prompt's rows): a CTA keeps 128 / D * 128 keys
@@ -30,7 +30,7 @@
 //   between query tiles, each with an epilogue warpgroup of its own.  Bound by the three
 //   products next to the shared memory that they (B operand), the splitting and the loads
 //   read and write: an 8192-row prompt of 32 heads over 8 kv heads of 128 takes 1.22 ms,
-//   226 TFLOP/s of scores (FFMA tiles: 33).
+//   226 TFLOP/s of scores (9.9 ms with FFMA).
 //
 // Every mbarrier wait is bounded; a CTA that gives up records ATLAS_DEV_TIMEOUT, lets its
 // copies and MMAs finish, frees TMEM and writes NaN.
