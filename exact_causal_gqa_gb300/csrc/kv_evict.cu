@@ -24,8 +24,8 @@
 // chunk and writing it, arrived at one chunk ahead, with four chunks in flight (cp.async);
 // indices and page tables come through shared memory, so that nothing but the data's own
 // latency is in the loop.  Both are bound by DRAM's turning between reads and writes of
-// 256-byte rows (4.4 to 4.8 TB/s of traffic): 64 sequences' 4096 rows a head into fresh pages
-// (8 x 8 heads of 128 bf16) 44 us; 65536 of 131072 rows in place 116 us (strips of 64 bytes
+// 256-byte rows (4.4 to 4.8 TB/s of traffic): 4096 rows of 8 sequences x 8
+// heads of 128 bf16 into fresh pages 44 us; 65536 of 131072 rows in place 116 us (strips of 64 bytes
 // a warp 382, a cp.async ring per CTA 199, clusters of 8 with releasing arrivals 240,
 // relaxed 160, four pieces a thread 121, four stages 116).
 #include "internal.h"
