@@ -20,7 +20,7 @@
 //   tiles no key of the CTA is visible to are not loaded.  Bound by the products (operands
 //   from shared memory: 65 clocks per 128 x 128 x 16, as long as one of 64 columns) and the
 //   exponentials, each busy 54 % of the time: an 8192-row prompt of 32 heads over 8 kv heads
-//   of 128 takes 226 us, 1.22 PFLOP/s of scores.  When (sequence, kv head) x 512-key groups
+//   of 128 takes 222 us, 1.24 PFLOP/s of scores.  When (sequence, kv head) x 512-key groups
 //   alone would not fill the GPU, the query tiles are split between CTAs; their sums per key
 //   go to the workspace and weights_join_kernel adds them in order.
 //
@@ -629,16 +629,30 @@ cudaError_t launch_weights_join(const WeightsParams &p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-// Query tiles of 128 rows split between CTAs of `group_keys` keys until there are about 3
-// items per SM (one 8192-row bf16 prompt: 225 us; 2, 4, 6, 8 items 239, 228, 238, 245 us),
-// none below 8 tiles.
-static void split_query_tiles(WeightsPlan &plan, int64_t units, int64_t cols, int64_t ctx,
-                              int64_t group_keys, int sms) {
+// Query tiles of 128 rows split between CTAs of `group_keys` keys: the number of parts with
+// the least estimated time, in query tiles.  More items than SMs: their tiles (a key group is
+// seen by the rows at and behind it) and start-ups, spread evenly, and a quarter of an item
+// for the tail, the long ones going first; else one item.  `startup` is a CTA's in query
+// tiles: 6 for bf16 (4: the same times; 8 and 12: 7 % more for one 8192-row prompt of 32 / 8
+// heads, 22 % for one of 4096 rows), 3 for fp32 (2 and 4: up to 12 % and 7 % more).  Against
+// about three items an SM of at least 8 tiles: one prompt of 512 / 1024 / 4096 / 8192 rows 20 /
+// 21 / 78 / 228 -> 11 / 16 / 67 / 222 us, in fp32 30 / 36 / 327 / 1220 -> 19 / 38 / 332 / 1206.
+static void split_query_tiles(WeightsPlan &plan, int64_t units, int64_t cols, int q_len, int64_t ctx,
+                              int64_t group_keys, int startup, int sms) {
     const int64_t nq = (cols + BT - 1) / BT;
-    const int64_t items = (ctx + group_keys - 1) / group_keys * units;
-    int64_t parts = ((int64_t)sms * 3 + items - 1) / items;
-    if (parts > (nq + 7) / 8) parts = (nq + 7) / 8;
-    plan.tiles_per_part = (int)((nq + parts - 1) / parts);
+    const int64_t groups = (ctx + group_keys - 1) / group_keys * units;
+    const double seen = (double)groups * nq * (1.0 - 0.5 * q_len / ctx);
+    double best = INFINITY;
+    for (int64_t parts = 1; parts <= nq && parts <= 64; ++parts) {
+        const int64_t tiles = (nq + parts - 1) / parts, items = groups * parts;
+        const double cost = items <= sms ? (double)(tiles + startup)
+                                         : (seen + (double)items * startup) / sms +
+                                               0.25 * (tiles + startup);
+        if (cost < best) {
+            best = cost;
+            plan.tiles_per_part = (int)tiles;
+        }
+    }
     plan.parts = (int)((nq + plan.tiles_per_part - 1) / plan.tiles_per_part);
     plan.ws_bytes = plan.parts > 1 ? (size_t)plan.parts * units * ctx * sizeof(float) : 0;
 }
@@ -666,7 +680,7 @@ WeightsPlan weights_tc_plan(int B, int Hkv, int G, int q_len, int64_t ctx, int s
     WeightsPlan plan{};
     const int64_t units = (int64_t)B * Hkv, cols = (int64_t)G * q_len;
     if (cols > 256) {
-        split_query_tiles(plan, units, cols, ctx, kGroupKeys, sms);
+        split_query_tiles(plan, units, cols, q_len, ctx, kGroupKeys, 6, sms);
         return plan;
     }
     // (start-up counted as four tiles: weights at 8 x 8 x 16384 keys of 128 take 40 / 48 / 53
@@ -692,7 +706,7 @@ WeightsPlan weights_tf32x3_plan(int B, int Hkv, int G, int q_len, int D, int64_t
         plan.chunk_tiles = share_tiles(units, ctx, sms, 2);
         return plan;
     }
-    split_query_tiles(plan, units, cols, ctx, group_keys, sms);
+    split_query_tiles(plan, units, cols, q_len, ctx, group_keys, 3, sms);
     return plan;
 }
 

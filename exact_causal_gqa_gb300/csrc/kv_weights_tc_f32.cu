@@ -29,8 +29,8 @@
 //   Two 128-column score buffers: at head_dim 64 one per key tile, at 128 they alternate
 //   between query tiles, each with an epilogue warpgroup of its own.  Bound by the three
 //   products next to the shared memory that they (B operand), the splitting and the loads
-//   read and write: an 8192-row prompt of 32 heads over 8 kv heads of 128 takes 1.22 ms,
-//   226 TFLOP/s of scores (9.9 ms with FFMA).
+//   read and write: an 8192-row prompt of 32 heads over 8 kv heads of 128 takes 1.21 ms,
+//   228 TFLOP/s of scores (9.9 ms with FFMA).
 //
 // Every mbarrier wait is bounded; a CTA that gives up records ATLAS_DEV_TIMEOUT, lets its
 // copies and MMAs finish, frees TMEM and writes NaN.
