@@ -98,6 +98,31 @@ int device_sm_count() {
     return n;
 }
 
+// Cross attention on the tensor cores: whether one pass over each tile's keys takes less
+// time than splits of `chunk` keys and a merge.  Microseconds of whole waves of CTAs, fitted
+// to 32 measured sizes a type (within a tenth of most): a CTA's start-up, its 128-key blocks
+// (a pair of bf16 tiles takes 1.75 times a single one's), and the merge's launch and bytes.
+// bf16, 32 / 8 heads or 8 / 8 of 128, direct and split: 8 x 300 rows on 1500 states 32 and 59
+// us, 2 x 300 on 1500 31 and 21, 500 rows on 4000 64 and 76, 128 rows on 8192 116 and 38.
+static bool cross_direct(const Plan &plan, const atlas_launch *L, int32_t Hq, int32_t Hkv, int32_t D,
+                         int64_t max_ctx, int64_t chunk, int sms) {
+    const bool f32 = plan.path == Path::TensorCoreF32;
+    const double start = f32 ? 5.0 : 11.0;
+    const double block = f32 ? (D == 128 ? 7.4 : 4.3) : 0.95;
+    const int64_t units = (int64_t)L->batch * Hkv, tiles = units * plan.tiles_per_unit;
+    const bool pairs = !f32 && plan.tiles_per_unit > 1;
+    const int64_t ctas = pairs ? units * ((plan.tiles_per_unit + 1) / 2) : tiles;
+    const int64_t splits = (max_ctx + chunk - 1) / chunk;
+    const double blocks = (double)((max_ctx + 127) / 128);
+    const double per_split = (double)((max_ctx / splits + 127) / 128);
+    const double waves = (double)((ctas + sms - 1) / sms);
+    const double split_waves = (double)((tiles * splits + sms - 1) / sms);
+    const double direct = waves * (start + blocks * block * (pairs ? 1.75 : 1.0));
+    const double bytes = (double)L->batch * Hq * L->q_len * splits * D * 8.0;  // partial sums, out and in
+    const double split = split_waves * (start + per_split * block) + 4.0 + bytes / 5e6;
+    return direct <= split || tiles > 65535;  // (more tiles than a grid of splits takes)
+}
+
 atlas_status make_plan(atlas_kind kind, int32_t Hq, int32_t Hkv, int32_t D, int32_t P,
                        const atlas_launch *L, Plan *plan) {
     if (!L) return ATLAS_ERR_INVALID_ARG;
@@ -157,12 +182,13 @@ atlas_status make_plan(atlas_kind kind, int32_t Hq, int32_t Hkv, int32_t D, int3
         int64_t chunk = 0;
         if (L->split_tokens > 0) {
             chunk = round_up(L->split_tokens, 128);
-        } else if ((tiles < tc_direct_tiles(sms) || L->phase != ATLAS_PHASE_ALL) &&
+        } else if ((cross || tiles < tc_direct_tiles(sms) || L->phase != ATLAS_PHASE_ALL) &&
                    !(L->debug_flags & ATLAS_DEBUG_TC_DIRECT)) {
             const int64_t target = tc_plan_ctas(sms);
             chunk = round_up((work_ctx * tiles + target - 1) / target, 128);
             if (chunk < 1024) chunk = 1024;
             if (chunk > 8192) chunk = 8192;
+            if (cross && cross_direct(*plan, L, Hq, Hkv, D, max_ctx, chunk, sms)) chunk = 0;
         }
         if (chunk > 0) {
             if (chunk > round_up(max_ctx, 128)) chunk = round_up(max_ctx, 128);

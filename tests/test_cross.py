@@ -115,6 +115,14 @@ CASES = [
     ("f32", 8, 2, 128, 16, 33, [0, 1, 64, 777], {}),                      # tf32 products, splits
     ("f32", 4, 1, 64, 32, 130, [0, 65, 300], dict(direct=True, ragged=[130, 0, 31])),
     ("f32", 8, 2, 64, 128, 40, [500, 0], dict(direct=True, sinks=True)),
+    # few tiles on long contexts: automatic splits and the merge
+    ("bf16", 4, 1, 128, 16, 40, [3000, 0, 1, 2900], {}),
+    ("bf16", 4, 1, 64, 64, 40, [2500, 130, 0], dict(sinks=True, ragged=[40, 3, 0])),
+    ("f32", 4, 1, 128, 32, 40, [3000, 0, 1], {}),
+    ("f32", 2, 1, 64, 16, 70, [2600, 40, 0], dict(softcap=5.0)),
+    # many tiles on short ones: direct
+    ("bf16", 8, 8, 128, 32, 300, [300, 0, 41], dict(ragged=[300, 7, 129])),
+    ("f32", 8, 8, 64, 32, 130, [130, 200], {}),
 ]
 
 
