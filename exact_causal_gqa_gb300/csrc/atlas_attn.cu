@@ -67,6 +67,14 @@ constexpr float kHiLoScale = 1.25f;
 // writes its output directly: at that size the merge launch (a few microseconds)
 // costs more than the parallelism the splits add.
 constexpr int64_t kDirectMaxBytes = 256 * 1024;
+// Cross attention of few rows runs in one launch (bf16: one CTA per unit that writes the
+// output; fp32: a cluster of 8 splits) where that fills the GPU, a CTA for each SM at least,
+// up to kCrossFullKeys keys: bf16, 256 units of 600 / 1500 / 3000 keys 24 / 42 / 70 -> 13 / 33
+// / 60 us; fp32, 32 units of 1000 / 3000 / 6000 keys 19 / 36 / 54 -> 16 / 30 / 49.  Beyond, a
+// batch's uneven lengths need the splits.  bf16 also with fewer units up to kCrossKeys keys:
+// without a merge and its workspace a call from Python takes 12 to 17 us, not 20 to 21 (8 to
+// 32 units of 600 to 1000 keys; on the device 10 to 15 and 10 to 11).  [bf16, fp32]
+constexpr int64_t kCrossFullKeys[2] = {4096, 8192}, kCrossKeys[2] = {1024, 0};
 // An fp32 ring-kernel call whose automatic plan has at most this many splits runs
 // them as one thread-block cluster per (sequence, kv head, column tile), merged in
 // distributed shared memory (the portable cluster size limit).
@@ -222,7 +230,11 @@ atlas_status make_plan(atlas_kind kind, int32_t Hq, int32_t Hkv, int32_t D, int3
     int64_t chunk = L->split_tokens;
     const int64_t unit_bytes = max_ctx * 2 * D * (L->kv_dtype == ATLAS_BF16 ? 2 : 4);
     const bool whole_call = chunk == 0 && L->phase == ATLAS_PHASE_ALL && !L->chunk_range;
-    if (whole_call && plan->path == Path::SplitBF16 && unit_bytes <= kDirectMaxBytes) {
+    const int64_t units = (int64_t)L->batch * Hkv * plan->col_tiles;
+    const int f32 = plan->path == Path::SplitF32;
+    const bool fills = units * (f32 ? kClusterMaxSplits : 1) >= sms;
+    const bool one_launch = cross && max_ctx <= (fills ? kCrossFullKeys[f32] : kCrossKeys[f32]);
+    if (whole_call && plan->path == Path::SplitBF16 && (unit_bytes <= kDirectMaxBytes || one_launch)) {
         plan->direct = 1;
         plan->chunk = (int)round_up(max_ctx, kSplitBlockTokens);
         plan->n_chunks = 1;
@@ -230,7 +242,6 @@ atlas_status make_plan(atlas_kind kind, int32_t Hq, int32_t Hkv, int32_t D, int3
         return ATLAS_OK;
     }
     if (chunk == 0) {
-        const int64_t units = (int64_t)L->batch * Hkv * plan->col_tiles;
         const int64_t target =
             plan->path == Path::SplitF32 && cols <= 8 ? f32_ring_plan_ctas(sms) : plan_ctas(sms);
         chunk = round_up((work_ctx * units + target - 1) / target, kSplitBlockTokens);
@@ -238,6 +249,8 @@ atlas_status make_plan(atlas_kind kind, int32_t Hq, int32_t Hkv, int32_t D, int3
         const int64_t min_chunk = plan->path == Path::SplitF32 ? kSplitBlockTokens : 512;
         if (chunk > kMaxSplit) chunk = kMaxSplit;
         if (chunk < min_chunk) chunk = min_chunk;
+        if (one_launch && plan->path == Path::SplitF32 && chunk * kClusterMaxSplits < max_ctx)
+            chunk = round_up((max_ctx + kClusterMaxSplits - 1) / kClusterMaxSplits, kSplitBlockTokens);
     }
     if (chunk > max_ctx) chunk = round_up(max_ctx, kSplitBlockTokens);
     plan->chunk = (int)chunk;

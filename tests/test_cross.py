@@ -115,6 +115,12 @@ CASES = [
     ("f32", 8, 2, 128, 16, 33, [0, 1, 64, 777], {}),                      # tf32 products, splits
     ("f32", 4, 1, 64, 32, 130, [0, 65, 300], dict(direct=True, ragged=[130, 0, 31])),
     ("f32", 8, 2, 64, 128, 40, [500, 0], dict(direct=True, sinks=True)),
+    # few rows: one launch on long contexts when there are many units, else splits and a merge
+    ("bf16", 8, 8, 64, 16, 1, [2000, 0, 1, 700] * 5, {}),
+    ("bf16", 16, 8, 128, 64, 2, [1025, 1, 0, 64] * 5, dict(sinks=True, ragged=[2, 1, 2, 0] * 5)),
+    ("f32", 4, 4, 64, 16, 1, [3000, 0, 65, 700, 1], {}),
+    ("f32", 8, 2, 128, 32, 2, [2048, 0, 1], dict(softcap=4.0)),
+    ("f32", 4, 2, 128, 64, 1, [5000, 0, 3], dict(sinks=True)),
     # few tiles on long contexts: automatic splits and the merge
     ("bf16", 4, 1, 128, 16, 40, [3000, 0, 1, 2900], {}),
     ("bf16", 4, 1, 64, 64, 40, [2500, 130, 0], dict(sinks=True, ragged=[40, 3, 0])),
