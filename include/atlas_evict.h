@@ -132,6 +132,8 @@ typedef struct {
  *     atlas_kv_select writes it), and the pages of the batch's sequences must not be
  *     shared with one another or with anyone who still needs them.  The pools must be two
  *     (overlapping ones are ATLAS_ERR_INVALID_ARG: each would move the other's rows).
+ *     Rows move in order, on at most 16 CTAs per (sequence, kv head): one long sequence of
+ *     few heads is faster into fresh pages.
  *   Into fresh pages: none of them may be a page that page_table's sequences use; kept
  *     rows may be in any order and repeat.  Shared pages (a common prefix) stay intact.
  * An index outside the sequence's table (in place: also one below its own j) or a
