@@ -49,11 +49,15 @@ bool overlap(const void *a, uint64_t n, const void *b, uint64_t m) {
 }
 
 // ---------------------------------------------------------------- selection
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelMaxCtas = 8;    // the portable cluster size
 constexpr int kSelKeys = 8192;    // keys of a CTA, while fewer than 8 CTAs share a row
-constexpr int kBins = 2 * kSelThreads;
+// Rows of at most kSelSmallKeys keys take smaller CTAs, for the same latency or less and more
+// rows at once: 512 threads (8 rows of 1500 keys 7.9 -> 6.7 us, 256 of 4096 16.9 -> 11.6), and
+// 256 when the rows are more than two for each SM (1024 rows of 600 / 2000 / 4000 keys 46 / 49 /
+// 54 us with 1024 threads, 26 / 28 / 35 with 512, 17 / 21 / 29 with 256; but 8 rows of 4096 8.7,
+// 8.4 and 10.4).
+constexpr int kSelSmallKeys = 4096;
+constexpr int kBins = 2048;
 constexpr int kSelCache = 200 * 1024;
 constexpr int kSelAhead = 8;
 
@@ -110,17 +114,18 @@ __device__ __forceinline__ uint2 ld_cluster2(const uint32_t *local, int rank) {
 
 // grid (CTAs of a row's cluster, Hkv, B).  CACHED: the row's keys stay in shared memory;
 // else (rows too long for that) each pass reads the weights again.
-template <bool CACHED>
-__global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectParams p) {
+template <bool CACHED, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const SelectParams p) {
+    constexpr int kWarps = kThreads / 32, kOwn = kBins / kThreads;  // bins of a thread
     extern __shared__ __align__(16) uint32_t cached[];
     __shared__ __align__(8) uint32_t hist[2][kBins];
     __shared__ uint32_t found[2];                 // digit, keys above it
-    __shared__ uint32_t warp_sum[kSelWarps];
-    __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
+    __shared__ uint32_t warp_sum[kWarps];
+    __shared__ uint32_t warp_gt[kWarps], warp_eq[kWarps];
     __shared__ uint32_t cta_gt, cta_eq;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x, ctas = gridDim.x, g = blockIdx.y, b = blockIdx.z;
-    const int all = ctas * kSelThreads, me = rank * kSelThreads + tid;
+    const int all = ctas * kThreads, me = rank * kThreads + tid;
     int L = p.seq_lens[b];
     if (L < 0 || L > p.row_tokens) {
         if (me == 0 && g == 0) record(p.status, ATLAS_DEV_BAD_SEQLEN);
@@ -177,22 +182,23 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
     for (int d = 0; d < 3; ++d) {
         const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
         uint32_t *h = hist[d & 1];
-        h[tid] = h[tid + kSelThreads] = 0u;
+#pragma unroll
+        for (int e = 0; e < kOwn; ++e) h[tid + e * kThreads] = 0u;
         __syncthreads();
         if (d == 0) {
             // Every key votes, on its way into shared memory, kSelAhead loads of a thread at
             // a time.  Equal weights all fall into one bin: a warp that agrees adds once.
-            for (int i0 = 0; i0 < len; i0 += kSelAhead * kSelThreads) {
+            for (int i0 = 0; i0 < len; i0 += kSelAhead * kThreads) {
                 float v[kSelAhead];
 #pragma unroll
                 for (int e = 0; e < kSelAhead; ++e) {
-                    const int i = i0 + e * kSelThreads + tid;
+                    const int i = i0 + e * kThreads + tid;
                     v[e] = i < len ? w[s0 + i] : 0.f;
                 }
 #pragma unroll
                 for (int e = 0; e < kSelAhead; ++e) {
-                    const int i = i0 + e * kSelThreads + tid;
-                    if (i0 + e * kSelThreads >= len) break;
+                    const int i = i0 + e * kThreads + tid;
+                    if (i0 + e * kThreads >= len) break;
                     const uint32_t k = order_key(v[e]);
                     if (CACHED && i < len) cached[i] = k;
                     int same;
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
         } else {
             // Few keys match the digits found, or (many equal weights) whole warps do.
             const uint32_t known = ~0u << (d == 1 ? 21 : 10), mask = d == 1 ? 2047u : 1023u;
-            for (int i0 = 0; i0 < len; i0 += 4 * kSelThreads) {
+            for (int i0 = 0; i0 < len; i0 += 4 * kThreads) {
                 bool in[4];
                 const uint4 k4 = keys_of(i0 + 4 * tid, in);
                 const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
@@ -224,15 +230,22 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
             }
         }
         cluster_barrier();
-        // Thread l owns bins 2047 - 2l and 2046 - 2l: a scan over threads goes from the top.
-        uint32_t first = 0, second = 0;
-#pragma unroll 8
-        for (int r = 0; r < ctas; ++r) {
-            const uint2 v = ld_cluster2(&h[kBins - 2 - 2 * tid], r);
-            first += v.y;
-            second += v.x;
-        }
-        uint32_t above = first + second;  // inclusive over the warp's lanes
+        // Thread l owns the kOwn bins down from 2047 - kOwn l: a scan over threads goes from
+        // the top.
+        uint32_t own[kOwn], sum = 0;  // from the highest bin down
+#pragma unroll
+        for (int e = 0; e < kOwn; ++e) own[e] = 0;
+#pragma unroll (kOwn == 2 ? 8 : 2)
+        for (int r = 0; r < ctas; ++r)
+#pragma unroll
+            for (int e = 0; e < kOwn; e += 2) {
+                const uint2 v = ld_cluster2(&h[kBins - 2 - e - kOwn * tid], r);
+                own[e] += v.y;
+                own[e + 1] += v.x;
+            }
+#pragma unroll
+        for (int e = 0; e < kOwn; ++e) sum += own[e];
+        uint32_t above = sum;  // inclusive over the warp's lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t v = __shfl_up_sync(0xffffffffu, above, o);
@@ -240,11 +253,17 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
         }
         if (lane == 31) warp_sum[warp] = above;
         __syncthreads();
-        above += __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u) - (first + second);
-        if (above < want && above + first + second >= want) {  // exactly one thread
-            const bool top = above + first >= want;
-            found[0] = (uint32_t)(kBins - 1 - 2 * tid - (top ? 0 : 1));
-            found[1] = above + (top ? 0u : first);
+        above += __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u) - sum;
+        if (above < want && above + sum >= want) {  // exactly one thread
+            int e = 0;
+#pragma unroll
+            for (int k = 0; k < kOwn - 1; ++k)
+                if (e == k && above + own[k] < want) {
+                    above += own[k];
+                    ++e;
+                }
+            found[0] = (uint32_t)(kBins - 1 - kOwn * tid - e);
+            found[1] = above;
         }
         __syncthreads();
         prefix |= found[0] << shift;
@@ -254,7 +273,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
     }
     // Keys above `prefix` stay, and the first `want` equal to it.  A warp takes a
     // contiguous part, 128 keys at a time, four consecutive ones to a lane.
-    const int part = ((len + kSelWarps - 1) / kSelWarps + 127) / 128 * 128;
+    const int part = ((len + kWarps - 1) / kWarps + 127) / 128 * 128;
     const int w0 = min(len, warp * part), w1 = min(len, w0 + part);
     uint32_t gt = 0, eq = 0;
     for (int i0 = w0; i0 < w1; i0 += 128) {
@@ -273,8 +292,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const SelectPara
     }
     __syncthreads();
     if (warp == 0) {
-        const uint32_t a = __reduce_add_sync(0xffffffffu, warp_gt[lane]);
-        const uint32_t c = __reduce_add_sync(0xffffffffu, warp_eq[lane]);
+        const uint32_t a = __reduce_add_sync(0xffffffffu, lane < kWarps ? warp_gt[lane] : 0u);
+        const uint32_t c = __reduce_add_sync(0xffffffffu, lane < kWarps ? warp_eq[lane] : 0u);
         if (lane == 0) {
             cta_gt = a;
             cta_eq = c;
@@ -575,12 +594,18 @@ atlas_status atlas_kv_select(const float *weights, const int32_t *seq_lens, int3
         ctas *= 2;
     const int64_t bytes = (((int64_t)p.row_tokens + ctas - 1) / ctas + 3) / 4 * 16;
     const bool cached = bytes <= kSelCache;
-    auto kern = cached ? select_kernel<true> : select_kernel<false>;
+    const int threads = ctas > 1 || p.row_tokens > kSelSmallKeys  ? 1024
+                        : rows > 2 * (int64_t)device_sm_count() ? 256
+                                                                : 512;
+    auto kern = threads == 256   ? select_kernel<true, 256>
+                : threads == 512 ? select_kernel<true, 512>
+                : cached         ? select_kernel<true, 1024>
+                                 : select_kernel<false, 1024>;
     static int configured[64] = {0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return ATLAS_ERR_CUDA;
     if (dev >= 64 || !configured[dev]) {
-        if (cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(select_kernel<true, 1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSelCache) != cudaSuccess)
             return ATLAS_ERR_CUDA;
         if (dev < 64) configured[dev] = 1;
@@ -588,7 +613,7 @@ atlas_status atlas_kv_select(const float *weights, const int32_t *seq_lens, int3
     (void)cudaGetLastError();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, (unsigned)n_kv_heads, (unsigned)S->batch);
-    cfg.blockDim = dim3(kSelThreads, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = cached ? (size_t)bytes : 0;
     cfg.stream = static_cast<cudaStream_t>(S->stream);
     cudaLaunchAttribute attr[1];

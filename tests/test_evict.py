@@ -319,6 +319,10 @@ SELECT = [
     ("plain", 2, 1, 64, [64, 5], 1, 1, 0),
     ("plain", 1, 2, 300, [300], 1000, 0, 0),                # a budget beyond the row
     ("ties", 1, 1, 420000, [419999], 5000, 4, 64),          # too long to stay in shared memory
+    ("plain", 20, 17, 700, [700, 333, 0, 5] * 5, 300, 2, 9),  # more rows than two for each SM
+    ("ties", 39, 8, 300, [300, 299, 13] * 13, 100, 0, 0),
+    ("odd", 1, 2, 4096, [4096], 1000, 3, 0),
+    ("plain", 1, 2, 4097, [4097], 1000, 3, 0),
 ]
 
 
