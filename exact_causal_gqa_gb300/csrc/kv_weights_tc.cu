@@ -637,6 +637,8 @@ cudaError_t launch_weights_join(const WeightsParams &p, cudaStream_t stream) {
 // heads, 22 % for one of 4096 rows), 3 for fp32 (2 and 4: up to 12 % and 7 % more).  Against
 // about three items an SM of at least 8 tiles: one prompt of 512 / 1024 / 4096 / 8192 rows 20 /
 // 21 / 78 / 228 -> 11 / 16 / 67 / 222 us, in fp32 30 / 36 / 327 / 1220 -> 19 / 38 / 332 / 1206.
+// The join counts as half a start-up: left out, small calls took it for 2 us less on the device
+// and 8 more from Python (421 rows x 4 heads x 2 sequences: 10.4 and 22.6 us, now 12.9 and 14.5).
 static void split_query_tiles(WeightsPlan &plan, int64_t units, int64_t cols, int q_len, int64_t ctx,
                               int64_t group_keys, int startup, int sms) {
     const int64_t nq = (cols + BT - 1) / BT;
@@ -645,9 +647,10 @@ static void split_query_tiles(WeightsPlan &plan, int64_t units, int64_t cols, in
     double best = INFINITY;
     for (int64_t parts = 1; parts <= nq && parts <= 64; ++parts) {
         const int64_t tiles = (nq + parts - 1) / parts, items = groups * parts;
-        const double cost = items <= sms ? (double)(tiles + startup)
+        const double work = items <= sms ? (double)(tiles + startup)
                                          : (seen + (double)items * startup) / sms +
                                                0.25 * (tiles + startup);
+        const double cost = work + (parts > 1 ? 0.5 * startup : 0.0);  // the join
         if (cost < best) {
             best = cost;
             plan.tiles_per_part = (int)tiles;
