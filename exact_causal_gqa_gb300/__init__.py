@@ -628,7 +628,8 @@ def kv_select(weights, seq_lens, budget, *, keep_first=0, keep_recent=0, kept=No
     """The keys of each (sequence, kv head) that stay under the budget: the first and the
     most recent ones, the others by weights [B][Hkv][row_tokens] (atlas_kv_select).
     Returns kept int32 [B][Hkv][budget] (ascending, then -1), new_lens int32 [B] and
-    kept_weights [B][Hkv][budget], the totals to go on with after kv_compact."""
+    kept_weights [B][Hkv][budget], the totals to go on with after kv_compact.  Outputs given
+    may not overlap weights, seq_lens (new_lens is not seq_lens) or one another."""
     lib = load_library()
     if weights.dim() != 3 or seq_lens.numel() != weights.shape[0]:
         raise ValueError("weights must be [B][Hkv][row_tokens] and seq_lens [B]")

@@ -571,9 +571,23 @@ atlas_status atlas_kv_select(const float *weights, const int32_t *seq_lens, int3
         S->budget > INT32_MAX / 2 || S->keep_first < 0 || S->keep_recent < 0 ||
         (int64_t)S->keep_first + S->keep_recent > S->budget)
         return ATLAS_ERR_INVALID_ARG;
-    const uint64_t floats = 4ull * S->batch * n_kv_heads;  // bytes per float of a row
-    if (S->kept_weights && overlap(weights, floats * S->row_tokens, S->kept_weights, floats * S->budget))
-        return ATLAS_ERR_INVALID_ARG;
+    // CTAs write lengths and kept keys while others still read the lengths and the totals: a
+    // CTA that read a shortened length would leave the cluster barriers of its row.
+    const uint64_t rows_bytes = 4ull * S->batch * n_kv_heads, lens_bytes = 4ull * S->batch;
+    const struct {
+        const void *at;
+        uint64_t bytes;
+    } outputs[] = {{S->new_lens, lens_bytes},
+                   {S->kept, rows_bytes * S->budget},
+                   {S->kept_weights, S->kept_weights ? rows_bytes * S->budget : 0}};
+    for (int i = 0; i < 3; ++i) {
+        if (overlap(outputs[i].at, outputs[i].bytes, seq_lens, lens_bytes) ||
+            overlap(outputs[i].at, outputs[i].bytes, weights, rows_bytes * S->row_tokens))
+            return ATLAS_ERR_INVALID_ARG;
+        for (int k = 0; k < i; ++k)
+            if (overlap(outputs[i].at, outputs[i].bytes, outputs[k].at, outputs[k].bytes))
+                return ATLAS_ERR_INVALID_ARG;
+    }
     SelectParams p{};
     p.weights = weights;
     p.seq_lens = seq_lens;

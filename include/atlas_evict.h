@@ -92,8 +92,7 @@ typedef struct {
     int32_t *kept;             /* [batch][n_kv_heads][budget], written */
     int32_t *new_lens;         /* [batch], written: min(seq_lens[b], budget) */
     float *kept_weights;       /* optional [batch][n_kv_heads][budget], written: the totals of
-                                  the kept keys; overlapping weights is
-                                  ATLAS_ERR_INVALID_ARG */
+                                  the kept keys */
     uint32_t *status_word;
     void *stream;
 } atlas_select;
@@ -104,7 +103,9 @@ typedef struct {
  * between the ones with the largest weights, equal weights by the lower index (-0 equals
  * 0; a NaN counts as -inf).  kept holds their indices in ascending order, then -1 up to
  * the budget; kept_weights the totals, then 0.  A seq_len below 0 or above row_tokens
- * sets ATLAS_DEV_BAD_SEQLEN and counts as 0.
+ * sets ATLAS_DEV_BAD_SEQLEN and counts as 0.  kept, new_lens and kept_weights that overlap
+ * weights, seq_lens (lengths updated in place) or one another are ATLAS_ERR_INVALID_ARG:
+ * all of a row's CTAs read them while others write.
  */
 atlas_status atlas_kv_select(const float *weights, const int32_t *seq_lens, int32_t n_kv_heads,
                              const atlas_select *S);

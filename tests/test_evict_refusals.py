@@ -1,0 +1,78 @@
+"""What atlas_kv_select refuses on the host, one field away from a call
+it accepts.
+
+Every pointer of the accepted call has an address of its own, far from the others', so
+that a refusal can only come from the field that was changed.  The addresses are no
+memory: where a GPU is visible, a call that the library failed to refuse would reach it
+with them, so these tests run on machines without one, where an accepted call ends with
+ATLAS_ERR_CUDA (4), the launch having no device."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+import exact_causal_gqa_gb300 as atlas
+from exact_causal_gqa_gb300 import _build
+
+pytestmark = pytest.mark.skipif(torch.cuda.is_available() or os.path.exists("/dev/nvidiactl"),
+                                reason="calls with made-up addresses: only where no GPU can get them")
+
+INVALID, NO_DEVICE = 1, 4
+FAR = 1 << 32  # between any two addresses: more than any range here
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return atlas.load_library()
+
+
+def at(k, offset=0):
+    return (k + 1) * FAR + offset
+
+
+# ------------------------------------------------------------------ selection
+B, HKV, T, BUDGET = 2, 2, 100, 10
+ROWS = 4 * B * HKV  # bytes of one float or int32 of every row
+WEIGHTS, LENS, KEPT, NEW, KEPT_W = (at(k) for k in range(5))
+
+
+def select(lib, w=WEIGHTS, lens=LENS, Hkv=HKV, **kw):
+    S = atlas._Select()
+    for k, v in {**dict(batch=B, row_tokens=T, budget=BUDGET, keep_first=1, keep_recent=2, kept=KEPT,
+                        new_lens=NEW, kept_weights=KEPT_W), **kw}.items():
+        setattr(S, k, v)
+    return lib.atlas_kv_select(w, lens, Hkv, ctypes.byref(S))
+
+
+def test_select_accepts_the_call_the_others_differ_from(lib):
+    assert select(lib) == NO_DEVICE
+    assert select(lib, kept_weights=None) == NO_DEVICE
+    assert select(lib, keep_first=8) == NO_DEVICE and select(lib, keep_recent=9) == NO_DEVICE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(w=None), dict(lens=None), dict(kept=None), dict(new_lens=None),
+    dict(w=WEIGHTS + 1), dict(kept=KEPT + 2), dict(kept_weights=KEPT_W + 3),
+    dict(batch=0), dict(batch=65536), dict(Hkv=0), dict(Hkv=65536), dict(row_tokens=0),
+    dict(row_tokens=2 ** 31 - 1), dict(budget=0), dict(budget=2 ** 31 - 1), dict(keep_first=-1),
+    dict(keep_recent=-1), dict(keep_first=9), dict(keep_first=2 ** 31 - 1, keep_recent=2 ** 31 - 1)])
+def test_select_refuses(lib, kw):
+    assert select(lib, **kw) == INVALID
+
+
+# Outputs over an input or another output: the same address, or the last or the first four
+# bytes of a range alone; and next to it, which is fine.
+@pytest.mark.parametrize("name,start,size,own", [
+    ("new_lens", LENS, 4 * B, 4 * B),                  # lengths updated in place: other CTAs read them
+    ("new_lens", WEIGHTS, ROWS * T, 4 * B), ("new_lens", KEPT, ROWS * BUDGET, 4 * B),
+    ("new_lens", KEPT_W, ROWS * BUDGET, 4 * B),
+    ("kept", LENS, 4 * B, ROWS * BUDGET), ("kept", WEIGHTS, ROWS * T, ROWS * BUDGET),
+    ("kept", KEPT_W, ROWS * BUDGET, ROWS * BUDGET),
+    ("kept_weights", LENS, 4 * B, ROWS * BUDGET), ("kept_weights", WEIGHTS, ROWS * T, ROWS * BUDGET)])
+def test_select_refuses_outputs_over_anything_else(lib, name, start, size, own):
+    for where in (start, start + size - 4, start - own + 4):
+        assert select(lib, **{name: where}) == INVALID, hex(where)
+    for where in (start + size, start - own):
+        assert select(lib, **{name: where}) == NO_DEVICE, hex(where)
