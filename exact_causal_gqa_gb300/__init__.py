@@ -132,7 +132,8 @@ class _Weights(ctypes.Structure):
 class _Select(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("row_tokens", ctypes.c_int32),
                 ("budget", ctypes.c_int32), ("keep_first", ctypes.c_int32),
-                ("keep_recent", ctypes.c_int32), ("kept", ctypes.c_void_p),
+                ("keep_recent", ctypes.c_int32), ("kept_row_tokens", ctypes.c_int32),
+                ("kept", ctypes.c_void_p),
                 ("new_lens", ctypes.c_void_p), ("kept_weights", ctypes.c_void_p),
                 ("status_word", ctypes.c_void_p), ("stream", ctypes.c_void_p)]
 
@@ -624,12 +625,15 @@ def kv_weights(q, k_pages, page_table, seq_lens, lse, n_q_heads, n_kv_heads, hea
 
 
 def kv_select(weights, seq_lens, budget, *, keep_first=0, keep_recent=0, kept=None, new_lens=None,
-              kept_weights=None, status=None):
+              kept_weights=None, kept_row_tokens=None, status=None):
     """The keys of each (sequence, kv head) that stay under the budget: the first and the
     most recent ones, the others by weights [B][Hkv][row_tokens] (atlas_kv_select).
     Returns kept int32 [B][Hkv][budget] (ascending, then -1), new_lens int32 [B] and
-    kept_weights [B][Hkv][budget], the totals to go on with after kv_compact.  Outputs given
-    may not overlap weights, seq_lens (new_lens is not seq_lens) or one another."""
+    kept_weights [B][Hkv][kept_row_tokens], the totals of the kept keys, then 0: what
+    kv_weights goes on adding to after kv_compact.  kept_row_tokens (default: budget, or the
+    row length of kept_weights) must leave room for the keys to come: kv_weights skips a
+    sequence longer than its rows and reports it in the status word alone.  Outputs given may
+    not overlap weights, seq_lens (new_lens is not seq_lens) or one another."""
     lib = load_library()
     if weights.dim() != 3 or seq_lens.numel() != weights.shape[0]:
         raise ValueError("weights must be [B][Hkv][row_tokens] and seq_lens [B]")
@@ -640,17 +644,21 @@ def kv_select(weights, seq_lens, budget, *, keep_first=0, keep_recent=0, kept=No
     if kept is None:
         kept = torch.empty(shape, dtype=torch.int32, device=dev)
     if kept_weights is None:
-        kept_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+        row = shape[2] if kept_row_tokens is None else int(kept_row_tokens)
+        kept_weights = torch.empty((B, Hkv, max(row, 0)), dtype=torch.float32, device=dev)
     if new_lens is None:
         new_lens = torch.empty(B, dtype=torch.int32, device=dev)
     _check(dev, ("weights", weights, torch.float32), ("seq_lens", seq_lens, torch.int32),
            ("kept", kept, torch.int32), ("kept_weights", kept_weights, torch.float32),
            ("new_lens", new_lens, torch.int32), ("status", status, torch.int32))
-    if kept.shape != shape or kept_weights.shape != shape or new_lens.numel() != B:
-        raise ValueError("kept and kept_weights must be [B][Hkv][budget] and new_lens [B]")
+    room = kept_weights.shape
+    if kept.shape != shape or len(room) != 3 or room[:2] != shape[:2] or room[2] < shape[2] or \
+            kept_row_tokens not in (None, room[2]) or new_lens.numel() != B:
+        raise ValueError("kept must be [B][Hkv][budget], kept_weights [B][Hkv][kept_row_tokens] "
+                         "of at least budget, and new_lens [B]")
     S = _Select()
     S.batch, S.row_tokens, S.budget = B, T, budget
-    S.keep_first, S.keep_recent = keep_first, keep_recent
+    S.keep_first, S.keep_recent, S.kept_row_tokens = keep_first, keep_recent, room[2]
     S.kept, S.new_lens, S.kept_weights = kept.data_ptr(), new_lens.data_ptr(), kept_weights.data_ptr()
     S.status_word = _ptr(status)
     S.stream = _stream(dev)

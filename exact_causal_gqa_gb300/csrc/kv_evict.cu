@@ -67,6 +67,7 @@ struct SelectParams {
     int32_t Hkv, row_tokens, budget, first, recent;
     int32_t *kept, *new_lens;
     float *kept_weights;
+    int32_t kept_row;  // floats per row of it, budget or more
     uint32_t *status;
 };
 
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
     const int64_t row = (int64_t)b * p.Hkv + g;
     const float *w = p.weights + row * p.row_tokens;
     int32_t *kept = p.kept + row * p.budget;
-    float *kept_w = p.kept_weights ? p.kept_weights + row * p.budget : nullptr;
+    float *kept_w = p.kept_weights ? p.kept_weights + row * p.kept_row : nullptr;
     // Keys that stay whatever their weight: all of them, or the first and the recent ones.
     const bool whole = L <= p.budget;
     const int lo = whole ? L : p.first, hi = whole ? L : L - p.recent;
@@ -146,10 +147,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
     // The entries that no weight decides.  Written last: the cluster barrier before would
     // wait for them to reach L2.
     auto fixed = [&] {
-        for (int j = n + me; j < p.budget; j += all) {
-            kept[j] = -1;
-            if (kept_w) kept_w[j] = 0.f;
-        }
+        for (int j = n + me; j < p.budget; j += all) kept[j] = -1;
+        if (kept_w)
+            for (int j = n + me; j < p.kept_row; j += all) kept_w[j] = 0.f;
         for (int j = me; j < lo + (L - hi); j += all) {
             const int t = j < lo ? j : hi + (j - lo);
             const int at = j < lo ? j : n - (L - hi) + (j - lo);
@@ -571,6 +571,8 @@ atlas_status atlas_kv_select(const float *weights, const int32_t *seq_lens, int3
         S->budget > INT32_MAX / 2 || S->keep_first < 0 || S->keep_recent < 0 ||
         (int64_t)S->keep_first + S->keep_recent > S->budget)
         return ATLAS_ERR_INVALID_ARG;
+    const int32_t kept_row = S->kept_row_tokens == 0 ? S->budget : S->kept_row_tokens;
+    if (kept_row < S->budget || kept_row > INT32_MAX / 2) return ATLAS_ERR_INVALID_ARG;
     // CTAs write lengths and kept keys while others still read the lengths and the totals: a
     // CTA that read a shortened length would leave the cluster barriers of its row.
     const uint64_t rows_bytes = 4ull * S->batch * n_kv_heads, lens_bytes = 4ull * S->batch;
@@ -579,7 +581,7 @@ atlas_status atlas_kv_select(const float *weights, const int32_t *seq_lens, int3
         uint64_t bytes;
     } outputs[] = {{S->new_lens, lens_bytes},
                    {S->kept, rows_bytes * S->budget},
-                   {S->kept_weights, S->kept_weights ? rows_bytes * S->budget : 0}};
+                   {S->kept_weights, S->kept_weights ? rows_bytes * kept_row : 0}};
     for (int i = 0; i < 3; ++i) {
         if (overlap(outputs[i].at, outputs[i].bytes, seq_lens, lens_bytes) ||
             overlap(outputs[i].at, outputs[i].bytes, weights, rows_bytes * S->row_tokens))
@@ -599,6 +601,7 @@ atlas_status atlas_kv_select(const float *weights, const int32_t *seq_lens, int3
     p.kept = S->kept;
     p.new_lens = S->new_lens;
     p.kept_weights = S->kept_weights;
+    p.kept_row = kept_row;
     p.status = S->status_word;
     // More CTAs per row as long as one wave holds them all.
     const int64_t rows = (int64_t)S->batch * n_kv_heads;

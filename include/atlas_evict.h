@@ -89,10 +89,12 @@ typedef struct {
     int32_t budget;            /* keys to keep, >= 1 */
     int32_t keep_first;        /* the first keep_first keys always stay, */
     int32_t keep_recent;       /* and the last keep_recent; together at most budget */
+    int32_t kept_row_tokens;   /* floats per row of kept_weights: 0 (budget of them) or at least
+                                  budget, with room for the keys that are to come */
     int32_t *kept;             /* [batch][n_kv_heads][budget], written */
     int32_t *new_lens;         /* [batch], written: min(seq_lens[b], budget) */
-    float *kept_weights;       /* optional [batch][n_kv_heads][budget], written: the totals of
-                                  the kept keys */
+    float *kept_weights;       /* optional [batch][n_kv_heads][kept_row_tokens], written: the
+                                  totals of the kept keys */
     uint32_t *status_word;
     void *stream;
 } atlas_select;
@@ -102,7 +104,9 @@ typedef struct {
  * seq_lens[b] <= budget; else the first keep_first, the last keep_recent, and of those
  * between the ones with the largest weights, equal weights by the lower index (-0 equals
  * 0; a NaN counts as -inf).  kept holds their indices in ascending order, then -1 up to
- * the budget; kept_weights the totals, then 0.  A seq_len below 0 or above row_tokens
+ * the budget; kept_weights the totals, then 0 to the row's end: the weights that
+ * atlas_kv_weights goes on adding to after atlas_kv_compact, if its rows (row_tokens there)
+ * have room for the longest seq_len to come.  A seq_len below 0 or above row_tokens
  * sets ATLAS_DEV_BAD_SEQLEN and counts as 0.  kept, new_lens and kept_weights that overlap
  * weights, seq_lens (lengths updated in place) or one another are ATLAS_ERR_INVALID_ARG:
  * all of a row's CTAs read them while others write.

@@ -48,6 +48,8 @@ def select(lib, w=WEIGHTS, lens=LENS, Hkv=HKV, **kw):
 
 def test_select_accepts_the_call_the_others_differ_from(lib):
     assert select(lib) == NO_DEVICE
+    assert select(lib, kept_row_tokens=BUDGET) == NO_DEVICE
+    assert select(lib, kept_row_tokens=T + 1) == NO_DEVICE
     assert select(lib, kept_weights=None) == NO_DEVICE
     assert select(lib, keep_first=8) == NO_DEVICE and select(lib, keep_recent=9) == NO_DEVICE
 
@@ -57,7 +59,8 @@ def test_select_accepts_the_call_the_others_differ_from(lib):
     dict(w=WEIGHTS + 1), dict(kept=KEPT + 2), dict(kept_weights=KEPT_W + 3),
     dict(batch=0), dict(batch=65536), dict(Hkv=0), dict(Hkv=65536), dict(row_tokens=0),
     dict(row_tokens=2 ** 31 - 1), dict(budget=0), dict(budget=2 ** 31 - 1), dict(keep_first=-1),
-    dict(keep_recent=-1), dict(keep_first=9), dict(keep_first=2 ** 31 - 1, keep_recent=2 ** 31 - 1)])
+    dict(keep_recent=-1), dict(keep_first=9), dict(keep_first=2 ** 31 - 1, keep_recent=2 ** 31 - 1),
+    dict(kept_row_tokens=-1), dict(kept_row_tokens=BUDGET - 1), dict(kept_row_tokens=2 ** 31 - 1)])
 def test_select_refuses(lib, kw):
     assert select(lib, **kw) == INVALID
 
@@ -76,3 +79,16 @@ def test_select_refuses_outputs_over_anything_else(lib, name, start, size, own):
         assert select(lib, **{name: where}) == INVALID, hex(where)
     for where in (start + size, start - own):
         assert select(lib, **{name: where}) == NO_DEVICE, hex(where)
+
+
+def test_select_counts_the_rows_of_kept_weights_as_wide_as_they_are(lib):
+    wide = dict(kept_row_tokens=BUDGET + 3)
+    for name, end in (("new_lens", KEPT_W + ROWS * (BUDGET + 3)), ("kept", KEPT_W + ROWS * (BUDGET + 3))):
+        assert select(lib, **{name: end - 4}, **wide) == INVALID
+        assert select(lib, **{name: end}, **wide) == NO_DEVICE
+
+
+def test_the_row_length_took_no_new_place_in_the_struct():
+    """It lies where the struct was padded: callers built before it was there pass 0."""
+    assert atlas._Select.kept_row_tokens.offset == 20 and atlas._Select.kept.offset == 24
+    assert ctypes.sizeof(atlas._Select) == 64
