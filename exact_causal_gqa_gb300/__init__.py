@@ -288,7 +288,6 @@ def _call(kind: str, q, k_pages, v_pages, page_table, seq_lens, n_q_heads, n_kv_
     ``phase`` and ``chunk_range`` (int32 CUDA tensor [B][2]) spread one call over
     several launches sharing ``workspace`` (atlas_launch.phase).  ``sm_count`` > 0
     plans for that many SMs instead of the device's (atlas_launch.sm_count)."""
-    lib = load_library()
     for name, t in (("q", q), ("k_pages", k_pages), ("v_pages", v_pages),
                     ("page_table", page_table), ("seq_lens", seq_lens)):
         if not t.is_cuda or not t.is_contiguous():
@@ -312,6 +311,18 @@ def _call(kind: str, q, k_pages, v_pages, page_table, seq_lens, n_q_heads, n_kv_
     if q_lens is not None and (not q_lens.is_cuda or q_lens.dtype != torch.int32 or
                                q_lens.numel() != q.shape[0]):
         raise ValueError("q_lens must be an int32 CUDA tensor [batch]")
+    return _enqueue(kind, q, k_pages, v_pages, page_table, seq_lens, n_q_heads, n_kv_heads,
+                    head_dim, page_tokens, scale, out, out_dtype, lse, workspace, status,
+                    split_tokens, debug_flags, events, window, softcap, sinks, q_lens,
+                    chunk_range, phase, sm_count)
+
+
+def _enqueue(kind, q, k_pages, v_pages, page_table, seq_lens, n_q_heads, n_kv_heads, head_dim,
+             page_tokens, scale, out, out_dtype, lse, workspace, status, split_tokens=0,
+             debug_flags=0, events=None, window=0, softcap=0.0, sinks=None, q_lens=None,
+             chunk_range=None, phase=PHASE_ALL, sm_count=0):
+    """An attention call whose tensors have been checked."""
+    lib = load_library()
     stream = _stream(q.device)
     L = _launch(q, k_pages, page_table, out_dtype, out, lse, None, status, stream,
                 split_tokens, debug_flags,
@@ -372,12 +383,41 @@ def prefill(q, k_pages, v_pages, page_table, seq_lens, n_q_heads, n_kv_heads, he
 
 
 def cross(q, k_pages, v_pages, page_table, enc_lens, n_q_heads, n_kv_heads, head_dim,
-          page_tokens, scale, **kw):
+          page_tokens, scale, *, out=None, out_dtype=None, lse=None, workspace=None, status=None,
+          sinks=None, q_lens=None, **options):
     """Attention of q_len decoder rows to all enc_lens[b] encoder states of their
-    sequence (no causal mask; enc_lens[b] == 0 gives rows of 0 and lse -inf)."""
-    with _on(_cuda_device("q", q)):
-        return _call("cross", q, k_pages, v_pages, page_table, enc_lens, n_q_heads, n_kv_heads,
-                     head_dim, page_tokens, scale, **kw)
+    sequence (no causal mask; enc_lens[b] == 0 gives rows of 0 and lse -inf).  The pools,
+    table and lengths are the encoder's; q [B][Hq][q_len][D] and lse [B][Hq][q_len] the
+    decoder's.  Other options are those of the causal calls."""
+    device, dtype, shape = _cuda_device("q", q), q.dtype, q.shape
+    pool = k_pages.shape
+    if len(shape) != 4 or shape[1] != n_q_heads or shape[3] != head_dim or len(pool) != 4 or \
+            pool[1:] != (n_kv_heads, page_tokens, head_dim) or v_pages.shape != pool:
+        raise ValueError("q must be [B][Hq][q_len][D] and the pools [num_pages][Hkv][P][D], of the "
+                         "sizes given")
+    B, _, n, _ = shape
+    if out is None:
+        out_dtype = out_dtype or dtype
+        out = torch.empty(shape, dtype=out_dtype, device=device)
+    else:
+        out_dtype = out_dtype or out.dtype
+    _check(device, ("q", q, dtype), ("k_pages", k_pages, dtype), ("v_pages", v_pages, dtype),
+           ("page_table", page_table, torch.int32), ("enc_lens", enc_lens, torch.int32),
+           ("out", out, out_dtype), ("lse", lse, torch.float32), ("status", status, torch.int32),
+           ("sinks", sinks, torch.float32), ("q_lens", q_lens, torch.int32),
+           ("workspace", workspace, None if workspace is None else workspace.dtype))
+    table = page_table.shape
+    if len(table) != 2 or table[0] != B or enc_lens.numel() != B or out.shape != shape or \
+            (lse is not None and lse.numel() != B * n_q_heads * n) or \
+            (sinks is not None and sinks.numel() != n_q_heads) or \
+            (q_lens is not None and q_lens.numel() != B) or \
+            (status is not None and status.numel() < 1):
+        raise ValueError("page_table must be [B][max_pages], enc_lens and q_lens [B], out like q, "
+                         "lse [B][Hq][q_len], sinks [Hq], status one word")
+    with _on(device):
+        return _enqueue("cross", q, k_pages, v_pages, page_table, enc_lens, n_q_heads, n_kv_heads,
+                        head_dim, page_tokens, scale, out, out_dtype, lse, workspace, status,
+                        sinks=sinks, q_lens=q_lens, **options)
 
 
 def run(problem, **kw):
