@@ -8,12 +8,13 @@
 //   (x, y) -> (x cos z - y sin z,  y cos z + x sin z),   in fp32, rounded once.
 // Far positions make z large (1e6 rad and more), where an fp32 product has lost the
 // angle.  Here z is taken in turns, as a 64-bit fraction of one turn: the host rounds
-// f_p / 2 pi mod 1 to F_p / 2^64, and the integer product position * F_p mod 2^64 is the
-// exact fraction of a turn of that F_p -- the 64-bit wrap is the range reduction, two
-// integer multiplies where an fp64 product would cost a slow pipe.  What is left is
-// |position| times the rounding of f_p / 2 pi (2^-53 of it): below 2^-24 turns for any
-// int32 position and |f_p| <= 1.  The top two bits (rounded) give the quadrant and the
-// rest an angle within an eighth of a turn, for sincospif.
+// f_p / 2 pi, less its nearest whole number, to F_p / 2^64, and the integer product
+// position * F_p mod 2^64 is the exact fraction of a turn of that F_p -- the 64-bit wrap is
+// the range reduction, two integer multiplies where an fp64 product would cost a slow pipe.
+// What is left is |position| times the rounding of f_p / 2 pi (2^-53 of it, twice): below
+// 2^-24 turns for any int32 position and |f_p| <= 1 of either sign (0.7 of that over random
+// frequencies).  The top two bits (rounded) give the quadrant and the rest an angle within
+// an eighth of a turn, for sincospif.
 //
 // What bounds it: memory, (read + write) of every row of q, k and v once.  A CTA takes
 // kMaxTokens neighbouring tokens: it puts their cosines and sines (shared by all heads)
@@ -85,8 +86,11 @@ __device__ __forceinline__ float narrow<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// cos and sin of `turn` / 2^64 turns: the nearest quarter turn and a remainder within
-// an eighth of a turn either side, whose fp32 form is exact to 2^-24 of itself.
+// cos and sin of `turn` / 2^64 turns: the nearest quarter turn and a remainder within an
+// eighth of a turn either side.  The low 32 bits are dropped, 2^-32 turns at most, and the
+// rest's fp32 form rounds by 2^-24 of it, 2^-27 turns at most: small next to a turn, which
+// is what counts for an angle, though the angles of the slowest pairs at the first
+// positions (2e-7 turns) keep but ten bits of their own.
 __device__ __forceinline__ void cos_sin_turns(uint64_t turn, float &c, float &s) {
     const uint32_t top = (uint32_t)(turn >> 32);
     const uint32_t quarter = (top + (1u << 29)) >> 30;
@@ -281,9 +285,12 @@ extern "C" atlas_status atlas_kv_append_rope(const void *k_new, const void *v_ne
         if (!R->inv_freq && !(R->theta > 0.0 && R->theta < HUGE_VAL)) return ATLAS_ERR_INVALID_ARG;
         const double f = R->inv_freq ? R->inv_freq[i] : pow(R->theta, -2.0 * i / R->rot_dim);
         if (!(fabs(f) < HUGE_VAL)) return ATLAS_ERR_INVALID_ARG;
+        // The nearest whole turn off, not the one below: that would leave a small negative
+        // frequency next to 1, with the last bit of 1 for its own.
         const double turns = f / 6.283185307179586476925;
-        const double part = turns - floor(turns);  // in [0, 1]; 1 only by rounding: no turn
-        p.turn[i] = part < 1.0 ? (uint64_t)(part * 18446744073709551616.0) : 0;  // 2^64
+        const double part = turns - rint(turns);  // exact, at most half a turn either way
+        const uint64_t size = (uint64_t)(fabs(part) * 18446744073709551616.0);  // 2^64
+        p.turn[i] = part < 0.0 ? 0 - size : size;
     }
     const int64_t per16 = R->kv_dtype == ATLAS_BF16 ? 8 : 4;
     const int64_t n = R->max_new, D = head_dim;
