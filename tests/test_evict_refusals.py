@@ -1,5 +1,5 @@
-"""What atlas_kv_select refuses on the host, one field away from a call
-it accepts.
+"""What atlas_kv_select and atlas_kv_compact refuse on the host, one field away from a call
+they accept.
 
 Every pointer of the accepted call has an address of its own, far from the others', so
 that a refusal can only come from the field that was changed.  The addresses are no
@@ -18,7 +18,7 @@ from exact_causal_gqa_gb300 import _build
 pytestmark = pytest.mark.skipif(torch.cuda.is_available() or os.path.exists("/dev/nvidiactl"),
                                 reason="calls with made-up addresses: only where no GPU can get them")
 
-INVALID, NO_DEVICE = 1, 4
+INVALID, UNSUPPORTED, NO_DEVICE = 1, 2, 4
 FAR = 1 << 32  # between any two addresses: more than any range here
 
 
@@ -92,3 +92,50 @@ def test_the_row_length_took_no_new_place_in_the_struct():
     """It lies where the struct was padded: callers built before it was there pass 0."""
     assert atlas._Select.kept_row_tokens.offset == 20 and atlas._Select.kept.offset == 24
     assert ctypes.sizeof(atlas._Select) == 64
+
+
+# ------------------------------------------------------------------ compaction
+K, V, TABLE, INDEX, COUNT, FRESH = (at(k) for k in range(8, 14))
+POOL = 8 * 2 * 16 * 128 * 2  # bytes: pages, kv heads, tokens, head_dim, bf16
+
+
+def compact(lib, k=K, v=V, table=TABLE, kept=INDEX, lens=COUNT, Hkv=2, D=128, P=16, **kw):
+    C = atlas._Compact()
+    for key, value in {**dict(batch=2, max_pages_per_seq=4, num_pages=8, max_kept=10, kv_dtype=1),
+                       **kw}.items():
+        setattr(C, key, value)
+    return lib.atlas_kv_compact(k, v, table, kept, lens, Hkv, D, P, ctypes.byref(C))
+
+
+FRESH_PAGES = dict(new_page_table=FRESH, new_max_pages=1)
+
+
+@pytest.mark.parametrize("kw", [{}, FRESH_PAGES])
+def test_compact_accepts_the_call_the_others_differ_from(lib, kw):
+    assert compact(lib, **kw) == NO_DEVICE
+    assert compact(lib, Hkv=4095, **kw) == NO_DEVICE
+    assert compact(lib, D=64, P=1, kv_dtype=0, **kw) == NO_DEVICE
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(table=None), INVALID),
+    (dict(kept=None), INVALID), (dict(lens=None), INVALID), (dict(k=K + 8), INVALID),
+    (dict(v=V + 4), INVALID), (dict(batch=0), INVALID), (dict(batch=65536), INVALID),
+    (dict(max_pages_per_seq=0), INVALID), (dict(max_pages_per_seq=2 ** 30), INVALID),
+    (dict(num_pages=0), INVALID), (dict(max_kept=0), INVALID), (dict(max_kept=2 ** 31 - 1), INVALID),
+    (dict(Hkv=0), INVALID), (dict(Hkv=4096), INVALID), (dict(D=80), UNSUPPORTED),
+    (dict(P=12), UNSUPPORTED), (dict(P=256), UNSUPPORTED), (dict(kv_dtype=3), UNSUPPORTED)])
+@pytest.mark.parametrize("where", [{}, FRESH_PAGES])
+def test_compact_refuses(lib, kw, status, where):
+    assert compact(lib, **{**where, **kw}) == status
+
+
+def test_compact_refuses_fresh_pages_without_a_row_length(lib):
+    assert compact(lib, new_page_table=FRESH) == INVALID
+
+
+def test_compact_in_place_refuses_overlapping_pools(lib):
+    for v in (K, K + POOL - 16, K - POOL + 16):
+        assert compact(lib, v=v) == INVALID
+    for v in (K + POOL, K - POOL):
+        assert compact(lib, v=v) == NO_DEVICE
