@@ -324,7 +324,8 @@ atlas_status run(atlas_kind kind, const void *q, const void *k_pages, const void
         (!L->out && L->phase != ATLAS_PHASE_CHUNKS))
         return ATLAS_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(L->out) ||
-        !aligned16(L->workspace))
+        !aligned16(L->workspace) ||
+        !aligned4({page_table, seq_lens, L->lse, L->sinks, L->q_lens, L->chunk_range, L->status_word}))
         return ATLAS_ERR_INVALID_ARG;
     if (!(scale == scale) || scale == INFINITY || scale == -INFINITY) return ATLAS_ERR_INVALID_ARG;
     if (L->window < 0 || !(L->softcap >= 0.f) || L->softcap == INFINITY)

@@ -6,9 +6,18 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "atlas_attn.h"
 
 namespace atlas {
+
+// Whether every pointer can be read as 32-bit words (a null one can).
+inline bool aligned4(std::initializer_list<const void *> pointers) {
+    uintptr_t bits = 0;
+    for (const void *p : pointers) bits |= reinterpret_cast<uintptr_t>(p);
+    return (bits & 3u) == 0;
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

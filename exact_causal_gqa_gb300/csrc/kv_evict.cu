@@ -563,8 +563,7 @@ atlas_status atlas_kv_select(const float *weights, const int32_t *seq_lens, int3
                              const atlas_select *S) {
     using namespace atlas;
     if (!weights || !seq_lens || !S || !S->kept || !S->new_lens) return ATLAS_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(S->kept) |
-         reinterpret_cast<uintptr_t>(S->kept_weights)) & 3u)
+    if (!aligned4({weights, seq_lens, S->kept, S->new_lens, S->kept_weights, S->status_word}))
         return ATLAS_ERR_INVALID_ARG;
     if (S->batch < 1 || S->batch > 65535 || n_kv_heads < 1 || n_kv_heads > 65535 ||
         S->row_tokens < 1 || S->row_tokens > INT32_MAX / 2 || S->budget < 1 ||
@@ -647,7 +646,8 @@ atlas_status atlas_kv_compact(void *k_pages, void *v_pages, const int32_t *page_
                               int32_t head_dim, int32_t page_tokens, const atlas_compact *C) {
     using namespace atlas;
     if (!k_pages || !v_pages || !page_table || !kept || !new_lens || !C) return ATLAS_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 15u)
+    if (((reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 15u) ||
+        !aligned4({page_table, kept, new_lens, C->new_page_table, C->status_word}))
         return ATLAS_ERR_INVALID_ARG;
     if (C->batch < 1 || C->batch > 65535 || C->max_pages_per_seq < 1 || C->num_pages < 1 ||
         C->max_kept < 1 || n_kv_heads < 1 || n_kv_heads > 4095 ||

@@ -197,7 +197,7 @@ atlas_status atlas_kv_weights(const void *q, const void *k_pages, const int32_t 
         return ATLAS_ERR_INVALID_ARG;
     if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_pages) |
           reinterpret_cast<uintptr_t>(W->workspace)) & 15u) ||
-        (reinterpret_cast<uintptr_t>(W->weights) & 3u))
+        !aligned4({page_table, seq_lens, lse, W->weights, W->q_lens, W->status_word}))
         return ATLAS_ERR_INVALID_ARG;
     if (!(fabsf(scale) < INFINITY)) return ATLAS_ERR_INVALID_ARG;
     const atlas_status st = check(n_q_heads, n_kv_heads, head_dim, page_tokens, W);

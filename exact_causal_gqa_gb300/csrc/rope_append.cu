@@ -266,7 +266,8 @@ extern "C" atlas_status atlas_kv_append_rope(const void *k_new, const void *v_ne
         return ATLAS_ERR_UNSUPPORTED;
     if (R->kv_dtype != ATLAS_F32 && R->kv_dtype != ATLAS_BF16) return ATLAS_ERR_UNSUPPORTED;
     if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) ||
-        (R->n_q_heads > 0 && (!aligned16(R->q) || !aligned16(R->q_out))))
+        (R->n_q_heads > 0 && (!aligned16(R->q) || !aligned16(R->q_out))) ||
+        !aligned4({page_table, seq_lens, n_new, R->positions, R->status_word}))
         return ATLAS_ERR_INVALID_ARG;
     if (R->n_axes < 1 || R->n_axes > ATLAS_ROPE_MAX_AXES || R->rot_dim < 2 || R->rot_dim % 2 ||
         R->rot_dim > head_dim || (R->interleaved != 0 && R->interleaved != 1))

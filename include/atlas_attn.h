@@ -28,7 +28,7 @@
  *   ferrox-core crate index: causal_gqa_attention_paged (decode) and
  *     causal_gqa_attention_prefill (prefill) name the two ends of this family.
  *
- * Layouts (all dense, row-major, C order; every pointer 16-byte aligned):
+ * Layouts (all dense, row-major, C order):
  *   q, out        [batch][n_q_heads][q_len][head_dim]
  *   k_pages,
  *   v_pages       [num_pages][n_kv_heads][page_tokens][head_dim]
@@ -36,6 +36,9 @@
  *                 last page are never read
  *   seq_lens      int32 [batch]; keys visible to the last query row
  *   lse           float [batch][n_q_heads][q_len]
+ * A tensor of q, out, K or V or a workspace that is not 16-byte aligned, and a 32-bit
+ * array (page_table, seq_lens, lse, ...) that is not 4-byte aligned, is
+ * ATLAS_ERR_INVALID_ARG.
  *
  * Ownership and asynchrony.  Every tensor pointer is a DEVICE pointer owned by
  * the caller; q, pools, page_table and seq_lens are only read.  The library

@@ -57,6 +57,7 @@ def test_select_accepts_the_call_the_others_differ_from(lib):
 @pytest.mark.parametrize("kw", [
     dict(w=None), dict(lens=None), dict(kept=None), dict(new_lens=None),
     dict(w=WEIGHTS + 1), dict(kept=KEPT + 2), dict(kept_weights=KEPT_W + 3),
+    dict(lens=LENS + 2), dict(new_lens=NEW + 1), dict(status_word=at(6, 2)),
     dict(batch=0), dict(batch=65536), dict(Hkv=0), dict(Hkv=65536), dict(row_tokens=0),
     dict(row_tokens=2 ** 31 - 1), dict(budget=0), dict(budget=2 ** 31 - 1), dict(keep_first=-1),
     dict(keep_recent=-1), dict(keep_first=9), dict(keep_first=2 ** 31 - 1, keep_recent=2 ** 31 - 1),
@@ -120,7 +121,8 @@ def test_compact_accepts_the_call_the_others_differ_from(lib, kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(table=None), INVALID),
     (dict(kept=None), INVALID), (dict(lens=None), INVALID), (dict(k=K + 8), INVALID),
-    (dict(v=V + 4), INVALID), (dict(batch=0), INVALID), (dict(batch=65536), INVALID),
+    (dict(v=V + 4), INVALID), (dict(table=TABLE + 2), INVALID), (dict(kept=INDEX + 1), INVALID),
+    (dict(lens=COUNT + 2), INVALID), (dict(status_word=at(6, 1)), INVALID), (dict(batch=0), INVALID), (dict(batch=65536), INVALID),
     (dict(max_pages_per_seq=0), INVALID), (dict(max_pages_per_seq=2 ** 30), INVALID),
     (dict(num_pages=0), INVALID), (dict(max_kept=0), INVALID), (dict(max_kept=2 ** 31 - 1), INVALID),
     (dict(Hkv=0), INVALID), (dict(Hkv=4096), INVALID), (dict(D=80), UNSUPPORTED),
@@ -132,6 +134,7 @@ def test_compact_refuses(lib, kw, status, where):
 
 def test_compact_refuses_fresh_pages_without_a_row_length(lib):
     assert compact(lib, new_page_table=FRESH) == INVALID
+    assert compact(lib, new_page_table=FRESH + 2, new_max_pages=1) == INVALID
 
 
 def test_compact_in_place_refuses_overlapping_pools(lib):
