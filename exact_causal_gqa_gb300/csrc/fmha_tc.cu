@@ -19,7 +19,10 @@
 // two neighbouring tiles of a (sequence, kv head) share their blocks as a pair, and a direct
 // call takes the sequences longest-first: 4 sequences of up to 1500 rows x 32 heads of 128 on
 // 3000 to 8192 states take 533 us, 1.24 PFLOP/s (567 us in the batch's order), bound as the
-// prefill is by each tile's chain of products and softmax.
+// prefill is by each tile's chain of products and softmax.  Batches of more than 32 sequences
+// keep the batch's order: the ranking takes one lane for each.  Over thousands of states no key
+// weighs much and P is rounded to bf16 throughout: outputs differ from fp64 by 1.6e-3 root mean
+// square, 2.3e-3 once stored as bf16, which alone rounds by 1.66e-3.
 //
 // Warp roles (128 + NT*128 threads, one CTA per SM):
 //   warp 0    TMA producer: the Q tiles once, then K blocks gathered page by page

@@ -49,7 +49,12 @@
  * Supported: head_dim 64 or 128; page_tokens a power of two in [8, 128];
  *   n_q_heads a multiple of n_kv_heads;
  *   q/K/V float32 -> out float32, or q/K/V bfloat16 -> out bfloat16 or float32.
- *   Accumulation and softmax state are float32 in every mode.
+ *   Accumulation and softmax state are float32 in every mode.  bf16 calls with more than
+ *   16 query rows per (sequence, kv head) multiply V by weights rounded to bf16 where no
+ *   key weighs more than a twelfth of its row, and by two bf16 parts of them elsewhere:
+ *   their outputs are off by 1.6e-3 root mean square of the outputs' own (at most 2^-8 /
+ *   sqrt 3), as much as the bf16 store rounds by.  fp32 calls of that size take three tf32
+ *   products, about 20 bits of a term.
  *
  * Errors.  Host-side checks return a status before anything is enqueued.
  * Data-dependent problems are found on the device: a page id outside
