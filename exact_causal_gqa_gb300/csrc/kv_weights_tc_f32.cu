@@ -6,7 +6,8 @@
 //   K_hi . Q_hi + (K_hi . Q_lo + K_lo . Q_hi),
 // three tf32 products into fp32 accumulators, the small terms apart from the main one or
 // before it: about 20 bits of each term, where a single tf32 product keeps 10.  Weights
-// differ from 64-bit ones by 2e-7 to 6e-7 of their value.
+// differ from 64-bit ones by 2e-7 to 6e-7 of their value.  An infinite element has no
+// such parts (inf - inf): its key's weight is NaN, the other keys' are as ever.
 //
 // Layout as in the bf16 kernels: keys on M, one per TMEM lane, so that a thread sums along
 // its own columns, and the split keys in tensor memory as A operands.

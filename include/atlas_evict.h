@@ -69,7 +69,11 @@ typedef struct {
  * (seq_len < rows, > max_pages_per_seq * page_tokens or > row_tokens) sets
  * ATLAS_DEV_BAD_SEQLEN and a page id outside [0, num_pages) ATLAS_DEV_BAD_PAGE; the
  * weights of that sequence (of the keys on that page) are left as they were.
- * ATLAS_DEV_TIMEOUT leaves the keys concerned NaN.
+ * ATLAS_DEV_TIMEOUT leaves the keys concerned NaN.  Infinities and NaN in K are not
+ * scanned for and stay with their key: its weight is exp of its scores (0, infinite or
+ * NaN), or NaN in float32 calls with more than two rows per (sequence, kv head), whose
+ * scores are sums of tf32 parts; other keys' weights do not depend on it, a key that no
+ * row sees gets 0 whatever it holds, and atlas_kv_select counts NaN as -inf.
  * Supported sizes and types are those of the attention calls.
  */
 atlas_status atlas_kv_weights(const void *q, const void *k_pages, const int32_t *page_table,
