@@ -765,8 +765,8 @@ def run_host(kind: str, q, k_pages, v_pages, page_table, seq_lens, n_q_heads, n_
     device on the current stream, runs the kernels, and copies the result back.
     Returns the host output tensor (``host_out`` if given)."""
     dev = [t.to(device, non_blocking=True) for t in (q, k_pages, v_pages, page_table, seq_lens)]
-    out = _call(kind, *dev, n_q_heads, n_kv_heads, head_dim, page_tokens, scale,
-                out_dtype=out_dtype, **kw)
+    call = cross if kind == "cross" else functools.partial(_call, kind)
+    out = call(*dev, n_q_heads, n_kv_heads, head_dim, page_tokens, scale, out_dtype=out_dtype, **kw)
     if host_out is None:
         host_out = torch.empty(out.shape, dtype=out.dtype, pin_memory=True)
     host_out.copy_(out, non_blocking=True)

@@ -92,3 +92,15 @@ def test_the_library_refuses_what_has_no_meaning_here():
             atlas.cross(**call("cuda"), **kw)
     with pytest.raises(TypeError):
         atlas.cross(**call("cuda"), windows=4)
+
+
+@pytest.mark.gpu
+def test_from_host_tensors_the_same_is_refused():
+    x = call("cpu")
+    args = [x[n] for n in ("q", "k_pages", "v_pages", "page_table", "enc_lens")]
+    sizes = HQ, HKV, D, P, 0.1
+    got = atlas.run_host("cross", *args, *sizes)
+    assert torch.equal(got, atlas.cross(*(t.cuda() for t in args), *sizes).cpu())
+    for k, bad in ((3, args[3][:2]), (4, args[4][:2]), (2, args[2].float()), (1, args[1][:, :1])):
+        with pytest.raises(ValueError):
+            atlas.run_host("cross", *args[:k], bad, *args[k + 1:], *sizes)
