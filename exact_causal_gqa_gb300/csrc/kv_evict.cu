@@ -9,10 +9,12 @@
 // the k-th largest lies in and how many are still wanted there.  What equals the last key
 // is taken by lowest index, so the set never depends on timing, and positions in the
 // ascending output are counts of kept keys before (ballots in a warp, sums over warps and
-// CTAs).  Memory: 4 bytes per key in, 8 per kept key out; bound by latency: a load, four
-// cluster barriers, and per digit a pass over the keys in shared memory and a scan.  8 x 8
-// rows of up to 32768 keys, 4096 kept: 18.5 us; one sequence's 8 rows of 131072 keys, half
-// kept: 23 us.
+// CTAs).  Memory: 4 bytes per key in, 8 per kept key out, 1 to 2 us of bytes for long rows.
+// Two rows of 600 keys take 6.3 us: a load, four cluster barriers, three scans.  What long
+// rows take beyond that grows with the keys of a CTA, each of which five passes look at (one
+// from memory, four in shared memory): 8 x 8 rows of up to 32768 keys (16384 a CTA), 4096
+// kept, 18.5 us; one sequence's 8 rows of 131072 keys (64 CTAs, the rest of the GPU idle),
+// half kept, 23 us.
 //
 // Compaction.  Rows of head_dim elements move between page slots, 16 bytes per thread and
 // step.  Into fresh pages every row is independent.  In place, row j takes row kept[j] >= j:
@@ -23,11 +25,13 @@
 // shares the rows of one (sequence, kv head, K or V): its barrier stands between reading a
 // chunk and writing it, arrived at one chunk ahead, with four chunks in flight (cp.async);
 // indices and page tables come through shared memory, so that nothing but the data's own
-// latency is in the loop.  Both are bound by DRAM's turning between reads and writes of
-// 256-byte rows (4.4 to 4.8 TB/s of traffic): 4096 rows of 8 sequences x 8
-// heads of 128 bf16 into fresh pages 44 us; 65536 of 131072 rows in place 116 us (strips of 64 bytes
-// a warp 382, a cp.async ring per CTA 199, clusters of 8 with releasing arrivals 240,
-// relaxed 160, four pieces a thread 121, four stages 116).
+// latency is in the loop.
+// Times: 65536 of 131072 rows of 8 heads of 128 bf16 (537 MB read and written) take 89 us
+// into fresh pages, 6.0 TB/s of DRAM traffic, and 116 to 119 in place: the order costs the
+// rest, the clusters going through their chunks in step (64 bf16: 52 and 95 us, 128 fp32: 165
+// and 199).  4096 rows of 8 sequences x 8 heads of 128 bf16 into fresh pages: 44 us.  Variants
+// in place: strips of 64 bytes a warp 382, a cp.async ring per CTA 199, clusters of 8 with
+// releasing arrivals 240, relaxed 160, four pieces a thread 121, four stages 116.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -521,9 +525,13 @@ __global__ void __launch_bounds__(kShiftThreads, 2) compact_shift_kernel(const C
 #pragma unroll 1
     for (int c = 0; c < S - 1; ++c) load(c, c);
     cp_async_wait<S - 2>();
-    // The barrier only has to keep writes behind reads that have already delivered their
-    // data (cp.async has landed): relaxed arrivals, which do not wait for the writes of
-    // the chunk before (a release did, for most of the kernel's time).
+    // The barrier only has to keep writes behind reads, never reads behind writes: a row is
+    // read once, before any chunk that writes it.  Arrivals are relaxed, so that they do not
+    // wait for the writes of the chunk before (a release did, for most of the kernel's time).
+    // The memory model orders nothing across a relaxed arrival; what is relied on is that a
+    // thread arrives only after cp.async.wait_group has told it that its data lie in shared
+    // memory, where no later write to their source can reach them, and that no thread passes
+    // the barrier, to issue such a write, before all have arrived.
     cluster_arrive_relaxed();  // this thread has read chunk 0
     int slot = 0, ahead = S - 1;  // the slots of chunks c and c + S - 1
 #pragma unroll 1

@@ -23,7 +23,8 @@
  *
  * Layouts, ownership, asynchrony and errors are those of atlas_attn.h: device pointers
  * owned by the caller, everything enqueued on `stream`, host checks before anything is
- * launched, data-dependent problems as ATLAS_DEV_* bits in *status_word.
+ * launched, data-dependent problems as ATLAS_DEV_* bits in *status_word.  What a call writes
+ * may not overlap what it reads, or another of its outputs, but where a call says so.
  */
 #ifndef ATLAS_EVICT_H
 #define ATLAS_EVICT_H
@@ -143,8 +144,8 @@ typedef struct {
  *     (overlapping ones are ATLAS_ERR_INVALID_ARG: each would move the other's rows).
  *     Rows move in order, on at most 16 CTAs per (sequence, kv head): one long sequence of
  *     few heads is faster into fresh pages.
- *   Into fresh pages: none of them may be a page that page_table's sequences use; kept
- *     rows may be in any order and repeat.  Shared pages (a common prefix) stay intact.
+ *   Into fresh pages: all different, and none of them a page that page_table's sequences
+ *     use; kept rows may be in any order and repeat.  Shared pages (a common prefix) stay intact.
  * An index outside the sequence's table (in place: also one below its own j) or a
  * new_lens[b] that does not fit sets ATLAS_DEV_BAD_SEQLEN, a bad page id
  * ATLAS_DEV_BAD_PAGE; the rows concerned are skipped.
