@@ -12,6 +12,7 @@ Functions (same names as the C entry points):
   suffix(...)   the last q_len positions as queries   -> atlas_attn_suffix
   prefill(...)  causal self-attention of a prompt     -> atlas_attn_prefill
   cross(...)    decoder rows over an encoder's states -> atlas_attn_cross
+  shared(...)   rows of sequences that share prefixes -> atlas_attn_shared
   kv_append(...)  new tokens' K/V into their pages    -> atlas_kv_append
   kv_append_rope(...)  the same, with rotary positions of several axes applied to the
                 new keys and the step's queries       -> atlas_kv_append_rope
@@ -33,11 +34,11 @@ import torch
 
 from . import _build
 
-__all__ = ["AtlasError", "decode", "suffix", "prefill", "cross", "kv_append",
+__all__ = ["AtlasError", "decode", "suffix", "prefill", "cross", "shared", "kv_append",
            "kv_append_rope", "kv_weights", "kv_select", "kv_compact", "workspace_size", "run_host",
            "library_path", "DEV_BAD_PAGE", "DEV_BAD_SEQLEN", "DEV_TIMEOUT",
            "DEBUG_WITHHOLD_STAGE", "KIND_DECODE", "KIND_SUFFIX", "KIND_PREFILL",
-           "KIND_CROSS", "rope_sections"]
+           "KIND_CROSS", "rope_sections", "shared_workspace_size"]
 
 KIND_DECODE, KIND_SUFFIX, KIND_PREFILL, KIND_CROSS = 0, 1, 2, 3
 _KINDS = {"decode": KIND_DECODE, "suffix": KIND_SUFFIX, "prefill": KIND_PREFILL,
@@ -74,6 +75,12 @@ class _Launch(ctypes.Structure):
                 ("sm_count", ctypes.c_int32)]
 
 PHASE_ALL, PHASE_CHUNKS, PHASE_MERGE = 0, 1, 2
+
+
+class _Shared(ctypes.Structure):
+    _fields_ = [("prefix_table", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
+                ("group_starts", ctypes.c_void_p), ("n_groups", ctypes.c_int32),
+                ("max_prefix_pages", ctypes.c_int32)]
 
 
 class _PoolConfig(ctypes.Structure):
@@ -171,6 +178,11 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
+    lib.atlas_attn_shared.argtypes = args[:-1] + [ctypes.POINTER(_Shared), ctypes.POINTER(_Launch)]
+    lib.atlas_attn_shared.restype = ctypes.c_int
+    lib.atlas_attn_shared_workspace_size.argtypes = [ctypes.c_int32] * 4 + [
+        ctypes.POINTER(_Shared), ctypes.POINTER(_Launch)]
+    lib.atlas_attn_shared_workspace_size.restype = ctypes.c_size_t
     lib.atlas_attn_workspace_size.argtypes = [ctypes.c_int] + [ctypes.c_int32] * 4 + [
         ctypes.POINTER(_Launch)]
     lib.atlas_attn_workspace_size.restype = ctypes.c_size_t
@@ -418,6 +430,84 @@ def cross(q, k_pages, v_pages, page_table, enc_lens, n_q_heads, n_kv_heads, head
         return _enqueue("cross", q, k_pages, v_pages, page_table, enc_lens, n_q_heads, n_kv_heads,
                         head_dim, page_tokens, scale, out, out_dtype, lse, workspace, status,
                         sinks=sinks, q_lens=q_lens, **options)
+
+
+def shared(q, k_pages, v_pages, prefix_table, prefix_lens, group_starts, page_table, seq_lens,
+           n_q_heads, n_kv_heads, head_dim, page_tokens, scale, *, out=None, out_dtype=None,
+           lse=None, workspace=None, status=None, split_tokens=0, events=None, softcap=0.0,
+           sinks=None, q_lens=None, sm_count=0):
+    """Attention of the last q_len positions of each sequence to its own cache (page_table
+    [B][max_pages], seq_lens [B]: as for suffix) and to all of its group's prefix: sequences
+    group_starts[n] <= b < group_starts[n + 1] share the prefix_lens[n] keys of prefix_table[n]
+    [n_groups][max_prefix_pages] (atlas_attn_shared).  Other options are those of the causal
+    calls; ``workspace``: at least shared_workspace_size(...) bytes."""
+    device, dtype, shape, pool = _cuda_device("q", q), q.dtype, q.shape, k_pages.shape
+    if len(shape) != 4 or shape[1] != n_q_heads or shape[3] != head_dim or len(pool) != 4 or \
+            pool[1:] != (n_kv_heads, page_tokens, head_dim) or v_pages.shape != pool:
+        raise ValueError("q must be [B][Hq][q_len][D] and the pools [num_pages][Hkv][P][D], of the "
+                         "sizes given")
+    B, _, n, _ = shape
+    if out is None:
+        out_dtype = out_dtype or dtype
+        out = torch.empty(shape, dtype=out_dtype, device=device)
+    else:
+        out_dtype = out_dtype or out.dtype
+    i32 = torch.int32
+    _check(device, ("q", q, dtype), ("k_pages", k_pages, dtype), ("v_pages", v_pages, dtype),
+           ("prefix_table", prefix_table, i32), ("prefix_lens", prefix_lens, i32),
+           ("group_starts", group_starts, i32), ("page_table", page_table, i32),
+           ("seq_lens", seq_lens, i32), ("out", out, out_dtype), ("lse", lse, torch.float32),
+           ("status", status, i32), ("sinks", sinks, torch.float32), ("q_lens", q_lens, i32),
+           ("workspace", workspace, None if workspace is None else workspace.dtype))
+    table, prefixes = page_table.shape, prefix_table.shape
+    if len(table) != 2 or table[0] != B or seq_lens.numel() != B or len(prefixes) != 2 or \
+            prefix_lens.numel() != prefixes[0] or group_starts.numel() != prefixes[0] + 1 or \
+            out.shape != shape or (lse is not None and lse.numel() != B * n_q_heads * n) or \
+            (sinks is not None and sinks.numel() != n_q_heads) or \
+            (q_lens is not None and q_lens.numel() != B) or \
+            (status is not None and status.numel() < 1):
+        raise ValueError("page_table must be [B][max_pages], prefix_table [n_groups][max_prefix_pages], "
+                         "prefix_lens [n_groups], group_starts [n_groups + 1], seq_lens and q_lens "
+                         "[B], out like q, lse [B][Hq][q_len], sinks [Hq], status one word")
+    lib = load_library()
+    L = _launch(q, k_pages, page_table, out_dtype, out, lse, None, status, _stream(device),
+                split_tokens, 0, None if events is None else ctypes.cast(events, ctypes.c_void_p).value,
+                0, softcap, sinks, q_lens, None, PHASE_ALL, sm_count)
+    S = _Shared(prefix_table.data_ptr(), prefix_lens.data_ptr(), group_starts.data_ptr(),
+                prefixes[0], prefixes[1])
+    with _on(device):
+        if workspace is None:
+            need = lib.atlas_attn_shared_workspace_size(n_q_heads, n_kv_heads, head_dim, page_tokens,
+                                                        ctypes.byref(S), ctypes.byref(L))
+            if need < ctypes.c_size_t(-1).value:
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        L.workspace = _ptr(workspace)
+        L.workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        rc = lib.atlas_attn_shared(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                   page_table.data_ptr(), seq_lens.data_ptr(), n_q_heads,
+                                   n_kv_heads, head_dim, page_tokens, float(scale),
+                                   ctypes.byref(S), ctypes.byref(L))
+    if rc != 0:
+        raise AtlasError(rc, status_string(rc))
+    return out
+
+
+def shared_workspace_size(q_shape, n_q_heads, n_kv_heads, head_dim, page_tokens, max_pages_per_seq,
+                          n_groups, max_prefix_pages, num_pages, dtype=torch.bfloat16,
+                          out_dtype=None, split_tokens=0) -> int:
+    """Workspace bytes a shared() call needs (from shapes and the split size only)."""
+    L = _Launch()
+    L.batch, L.q_len = q_shape[0], q_shape[2]
+    L.max_pages_per_seq, L.num_pages = max_pages_per_seq, num_pages
+    L.q_dtype = L.kv_dtype = _DTYPES.get(dtype, -1)
+    L.out_dtype = _DTYPES.get(out_dtype or dtype, -1)
+    L.split_tokens = split_tokens
+    S = _Shared(n_groups=n_groups, max_prefix_pages=max_prefix_pages)
+    n = load_library().atlas_attn_shared_workspace_size(n_q_heads, n_kv_heads, head_dim, page_tokens,
+                                                        ctypes.byref(S), ctypes.byref(L))
+    if n == ctypes.c_size_t(-1).value:
+        raise AtlasError(1, "invalid arguments for shared_workspace_size")
+    return n
 
 
 def run(problem, **kw):

@@ -54,14 +54,6 @@ int64_t f32_ring_plan_ctas(int sms) { return (int64_t)sms * 3 * 4; }
 // writes the output directly once a call has at least SMs x 2 query tiles.
 int64_t tc_plan_ctas(int sms) { return (int64_t)sms * 3; }
 int64_t tc_direct_tiles(int sms) { return (int64_t)sms * 2; }
-// Query tiles whose rows see fewer keys than this use a hi + lo split of P:
-// with few keys (or a peaked softmax) a single bf16 rounding of P moves the
-// output by up to 2^-8 |v| (bf16 keeps 8 significant bits).  Scores sharper than
-// unit-variance inputs at scale 1/sqrt(D) (|scale| sqrt(D) above kHiLoScale) use
-// the split on every tile.  Elsewhere the kernel decides per block (fmha_tc.cu).
-constexpr int kHiLoBelow = 512;
-constexpr float kHiLoScale = 1.25f;
-
 // A bf16 decode-like call whose whole context per (sequence, kv head) holds at most
 // this many K/V bytes runs as one split per (sequence, kv head, column tile) that
 // writes its output directly: at that size the merge launch (a few microseconds)
@@ -317,9 +309,11 @@ atlas_status encode_pool_map(CUtensorMap *map, const void *pool, int32_t num_pag
     return r == CUDA_SUCCESS ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 
-atlas_status run(atlas_kind kind, const void *q, const void *k_pages, const void *v_pages,
-                 const int32_t *page_table, const int32_t *seq_lens, int32_t Hq, int32_t Hkv,
-                 int32_t D, int32_t P, float scale, const atlas_launch *L) {
+}  // namespace
+
+atlas_status run_attention(atlas_kind kind, const void *q, const void *k_pages, const void *v_pages,
+                           const int32_t *page_table, const int32_t *seq_lens, int32_t Hq,
+                           int32_t Hkv, int32_t D, int32_t P, float scale, const atlas_launch *L) {
     if (!q || !k_pages || !v_pages || !page_table || !seq_lens || !L ||
         (!L->out && L->phase != ATLAS_PHASE_CHUNKS))
         return ATLAS_ERR_INVALID_ARG;
@@ -416,7 +410,7 @@ atlas_status run(atlas_kind kind, const void *q, const void *k_pages, const void
         tp.balanced = plan.balanced;
         tp.require_full = kind == ATLAS_KIND_PREFILL;
         tp.row_step = sp.row_step;
-        tp.hilo_below = fabsf(scale) * sqrtf((float)D) > kHiLoScale ? INT32_MAX : kHiLoBelow;
+        tp.hilo_below = hilo_below(scale, D);
         tp.negate_scores = scale < 0.f;
         tp.scale_log2 = fabsf(scale) * kLog2e;
         tp.window = L->window;
@@ -488,7 +482,6 @@ atlas_status run(atlas_kind kind, const void *q, const void *k_pages, const void
     return ATLAS_OK;
 }
 
-}  // namespace
 }  // namespace atlas
 
 extern "C" {
@@ -497,32 +490,32 @@ atlas_status atlas_attn_decode(const void *q, const void *k_pages, const void *v
                                const int32_t *page_table, const int32_t *seq_lens,
                                int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                                int32_t page_tokens, float scale, const atlas_launch *L) {
-    return atlas::run(ATLAS_KIND_DECODE, q, k_pages, v_pages, page_table, seq_lens, n_q_heads,
-                      n_kv_heads, head_dim, page_tokens, scale, L);
+    return atlas::run_attention(ATLAS_KIND_DECODE, q, k_pages, v_pages, page_table, seq_lens,
+                                n_q_heads, n_kv_heads, head_dim, page_tokens, scale, L);
 }
 
 atlas_status atlas_attn_suffix(const void *q, const void *k_pages, const void *v_pages,
                                const int32_t *page_table, const int32_t *seq_lens,
                                int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                                int32_t page_tokens, float scale, const atlas_launch *L) {
-    return atlas::run(ATLAS_KIND_SUFFIX, q, k_pages, v_pages, page_table, seq_lens, n_q_heads,
-                      n_kv_heads, head_dim, page_tokens, scale, L);
+    return atlas::run_attention(ATLAS_KIND_SUFFIX, q, k_pages, v_pages, page_table, seq_lens,
+                                n_q_heads, n_kv_heads, head_dim, page_tokens, scale, L);
 }
 
 atlas_status atlas_attn_prefill(const void *q, const void *k_pages, const void *v_pages,
                                 const int32_t *page_table, const int32_t *seq_lens,
                                 int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                                 int32_t page_tokens, float scale, const atlas_launch *L) {
-    return atlas::run(ATLAS_KIND_PREFILL, q, k_pages, v_pages, page_table, seq_lens, n_q_heads,
-                      n_kv_heads, head_dim, page_tokens, scale, L);
+    return atlas::run_attention(ATLAS_KIND_PREFILL, q, k_pages, v_pages, page_table, seq_lens,
+                                n_q_heads, n_kv_heads, head_dim, page_tokens, scale, L);
 }
 
 atlas_status atlas_attn_cross(const void *q, const void *k_pages, const void *v_pages,
                               const int32_t *page_table, const int32_t *enc_lens,
                               int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                               int32_t page_tokens, float scale, const atlas_launch *L) {
-    return atlas::run(ATLAS_KIND_CROSS, q, k_pages, v_pages, page_table, enc_lens, n_q_heads,
-                      n_kv_heads, head_dim, page_tokens, scale, L);
+    return atlas::run_attention(ATLAS_KIND_CROSS, q, k_pages, v_pages, page_table, enc_lens,
+                                n_q_heads, n_kv_heads, head_dim, page_tokens, scale, L);
 }
 
 atlas_status atlas_kv_append(const void *k_new, const void *v_new, void *k_pages, void *v_pages,

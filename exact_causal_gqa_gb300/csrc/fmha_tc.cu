@@ -49,6 +49,7 @@
 // lets its copies and MMAs finish, frees TMEM and writes NaN.
 #include "internal.h"
 #include "ptx.cuh"
+#include "shared_prefix.cuh"
 #include "tc_order.cuh"
 
 #include <math.h>
@@ -291,7 +292,8 @@ __device__ __forceinline__ int tc_persist_item(int k, int i, int ctas) {
     return i * ctas + ((i & 1) ? ctas - 1 - k : k);
 }
 
-template <int NT, int D, bool PERSIST>
+// SHARED: the splits of prefixes that groups of sequences share (shared_prefix.cuh).
+template <int NT, int D, bool PERSIST, bool SHARED = false>
 __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     fmha_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const TcParams p) {
@@ -316,7 +318,33 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     // current item's last blocks and epilogue.
     int n_items = 1;
     TcWork w0{};
-    if (PERSIST) {
+    int seq0 = 0;  // SHARED: the first sequence of the item's group
+    // The merge that follows a SHARED grid reads the sequences' own splits too, which the
+    // grid before this one writes: one CTA at least must not end before that grid has.
+    auto before_exit = [&]() {
+        if (SHARED && blockIdx.x == 0) wait_for_previous_grid();
+    };
+    if (SHARED) {
+        const SharedItem it = shared_item(p, blockIdx.x, NT, reinterpret_cast<int *>(smem + C::OFF_V));
+        if (it.group < 0) {
+            before_exit();
+            return;
+        }
+        __syncthreads();  // (the scratch is the V ring)
+        seq0 = it.seq0;
+        w0.b = it.group;
+        w0.hkv = it.hkv;
+        w0.c = it.split;
+        w0.t0 = it.tile;
+        w0.tstep = NT - 1;
+        w0.rows_unit = it.seqs * p.G * p.q_len;
+        w0.kv_begin = it.split * p.chunk;
+        w0.kv_end = min(it.len, w0.kv_begin + p.chunk);
+        w0.nb = (w0.kv_end - w0.kv_begin + BN - 1) / BN;
+        w0.hilo = it.len < p.hilo_below;
+        w0.tail_first = w0.kv_end - (w0.kv_begin + (w0.nb - 1) * BN);
+        w0.tail_fix = w0.tail_first < BN;
+    } else if (PERSIST) {
         const int total = p.B * p.Hkv * (p.G / NT) * p.tiles_per_head;
         n_items = 0;
         while (n_items < kMaxItems && tc_persist_item(blockIdx.x, n_items, gridDim.x) < total)
@@ -350,6 +378,15 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             return;
         w0 = tc_work<NT>(p, u, c, t0, tstep, split_keys);
     }
+    // Output row of tile row f of an item, and whether it is a query.
+    auto row_of = [&](const TcWork &w, int f) -> int64_t {
+        if constexpr (SHARED) return shared_row(p, seq0, w.hkv, f);
+        else return tile_row(p, w.b, w.hkv, f);
+    };
+    auto is_query = [&](const TcWork &w, int f) -> bool {
+        if constexpr (SHARED) return shared_real(p, seq0, w.rows_unit, f);
+        else return f < w.rows_unit && f % p.q_len < w.qn;
+    };
     TcWork *const items = reinterpret_cast<TcWork *>(smem + C::OFF_ITEMS);
     // Items not computed (bit set): a bad seq_len or a page id outside the pool (rows
     // NaN), or nothing to compute.  The page ids of every item's key range are
@@ -403,23 +440,25 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             if (threadIdx.x == 0 && p.status) atomicOr(p.status, ATLAS_DEV_BAD_PAGE);
             if (threadIdx.x < NT * BM) {
                 const int f = (w.t0 + (int)(threadIdx.x / BM) * w.tstep) * BM + threadIdx.x % BM;
-                if (f < w.rows_unit && f % p.q_len < w.qn) {
+                if (is_query(w, f)) {
                     if (!p.split) {
                         nan_row<D>(p, w.b, w.hkv, f);
                     } else {
-                        float *ml =
-                            p.ws_ml + (tile_row(p, w.b, w.hkv, f) * p.n_chunks + w.c) * 2;
+                        float *ml = p.ws_ml + (row_of(w, f) * p.n_chunks + w.c) * 2;
                         ml[0] = ml[1] = __int_as_float(0x7fc00000);
                     }
                 }
             }
         }
     }
-    if (skip == (n_items == 64 ? ~0ull : (1ull << n_items) - 1)) return;
+    if (skip == (n_items == 64 ? ~0ull : (1ull << n_items) - 1)) {
+        before_exit();
+        return;
+    }
 
     // ------------------------------------------------------------ setup
     if (threadIdx.x == 0) {
-        mbar_init(BAR(C::B_Q), 1);
+        mbar_init(BAR(C::B_Q), SHARED ? NT * BM : 1);
         for (int s = 0; s < S; ++s) {
             mbar_init(BAR(C::B_KFULL + s), 1);
             mbar_init(BAR(C::B_KEMPTY + s), 1);
@@ -456,7 +495,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         const int kv = warp == 0 ? 0 : 1;
         if (lane == 0) {
             prefetch_tmap(kv == 0 ? &tmK : &tmV);
-            if (kv == 0) prefetch_tmap(&tmQ);
+            if (kv == 0 && !SHARED) prefetch_tmap(&tmQ);
         }
         const CUtensorMap *map = kv == 0 ? &tmK : &tmV;
         const uint32_t ring = sb + (kv == 0 ? C::OFF_K : C::OFF_V);
@@ -468,7 +507,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         for (int it = 0; it < n_items && !failed; ++it) {
             if ((skip >> it) & 1) continue;
             const TcWork &w = PERSIST ? items[it] : w0;
-            if (kv == 0) {
+            if (kv == 0 && !SHARED) {
                 // The previous item's Q tiles are free once its last S products are done.
                 if (nq > 0 && !wait_warp(BAR(C::B_QEMPTY), (nq - 1) & 1, abort_flag)) {
                     failed = true;
@@ -709,20 +748,41 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;  // 32-byte stores
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
         const uint32_t to = tl + C::o_col(x);
+        if constexpr (SHARED) {
+            // Q rows of many sequences: each warp copies its own 32 rows to where the tile's
+            // TMA load would put them (rows past the group's last are zero).
+            constexpr int kChunks = D / 8;  // 16-byte chunks of a row
+            const uint32_t qt = sb + C::OFF_Q + x * kTileBytes;
+#pragma unroll 4
+            for (int k = lane; k < 32 * kChunks; k += 32) {
+                const int row = q4 * 32 + k / kChunks, ch = k % kChunks;
+                const int f = (w0.t0 + x * w0.tstep) * BM + row;
+                const bool in = f < w0.rows_unit;
+                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
+                                           row_of(w0, in ? f : 0) * D + ch * 8;
+                cp_async16(qt + (ch / 8) * kSlab + sw128(row, ch % 8), src, in ? 16u : 0u);
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            fence_proxy_async_smem();
+            mbar_arrive(BAR(C::B_Q));
+        }
         bool ok = true;
         int g = 0;  // blocks of earlier items
         int it = 0;
         for (; ok && it < n_items; ++it) {
         if ((skip >> it) & 1) continue;
         const TcWork &w = PERSIST ? items[it] : w0;
-        const int b = w.b, hkv = w.hkv, c = w.c, kv_begin = w.kv_begin, nb = w.nb;
+        const int c = w.c, kv_begin = w.kv_begin, nb = w.nb;
         const bool hilo = w.hilo;
         const int f = (w.t0 + x * w.tstep) * BM + r;
-        const bool valid = f < w.rows_unit && f % p.q_len < w.qn;  // padding rows: no queries
-        const int i = valid ? f % p.q_len : 0;
-        const int lim_row = valid ? min(w.L - p.q_len + p.row_step * i + 1, w.kv_end) : 0;
+        const bool valid = is_query(w, f);  // padding rows: no queries
+        const int i = valid && !SHARED ? f % p.q_len : 0;
+        const int lim_row = !valid   ? 0
+                            : SHARED ? w.kv_end  // a prefix: every row sees all of it
+                                     : min(w.L - p.q_len + p.row_step * i + 1, w.kv_end);
         const int lo_row =
-            (valid && p.window > 0) ? max(0, w.L - p.q_len + i + 1 - p.window) : 0;
+            (valid && !SHARED && p.window > 0) ? max(0, w.L - p.q_len + i + 1 - p.window) : 0;
         float m_used = -INFINITY, l = 0.f;
         float log2_l = -INFINITY;  // log2(l), refreshed at the end of each block
         for (int j = 0; j < nb; ++j) {
@@ -963,7 +1023,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         // ---------------------------------------------------- epilogue
         tc_fence_after();
         if (ok) {
-            const int64_t row = tile_row(p, b, hkv, valid ? f : 0);
+            const int64_t row = row_of(w, valid ? f : 0);
             // Direct mode folds the sink (one more state: m = sink log2 e, l = 1,
             // acc = 0) here; split mode leaves it to the merge.
             float osc = 1.f;  // factor on acc
@@ -1093,10 +1153,10 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             }
         } else if (valid) {
             if (p.split) {
-                const int64_t slot = tile_row(p, b, hkv, f) * p.n_chunks + c;
+                const int64_t slot = row_of(w, f) * p.n_chunks + c;
                 p.ws_ml[slot * 2] = p.ws_ml[slot * 2 + 1] = __int_as_float(0x7fc00000);
             } else {
-                nan_row<D>(p, b, hkv, f);
+                nan_row<D>(p, w.b, w.hkv, f);
             }
         }
         g += nb;
@@ -1106,9 +1166,9 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             if ((skip >> it) & 1) continue;
             const TcWork &w = PERSIST ? items[it] : w0;
             const int f = (w.t0 + x * w.tstep) * BM + r;
-            if (f >= w.rows_unit || f % p.q_len >= w.qn) continue;
+            if (!is_query(w, f)) continue;
             if (p.split) {
-                float *ml = p.ws_ml + (tile_row(p, w.b, w.hkv, f) * p.n_chunks + w.c) * 2;
+                float *ml = p.ws_ml + (row_of(w, f) * p.n_chunks + w.c) * 2;
                 ml[0] = ml[1] = __int_as_float(0x7fc00000);
             } else {
                 nan_row<D>(p, w.b, w.hkv, f);
@@ -1123,6 +1183,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    before_exit();
 #undef BAR
 }
 
@@ -1172,7 +1233,34 @@ cudaError_t launch_instance(const TcParams &p, const CUtensorMap &tmQ, const CUt
     return cudaGetLastError();
 }
 
+template <int NT, int D>
+cudaError_t launch_shared_instance(const TcParams &p, int64_t ctas, const CUtensorMap &tmK,
+                                   const CUtensorMap &tmV, cudaStream_t stream) {
+    using C = Cfg<NT, D>;
+    auto kern = fmha_tc_kernel<NT, D, false, true>;
+    static int configured[64] = {0};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev >= 64 || !configured[dev]) {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (err != cudaSuccess) return err;
+        if (dev < 64) configured[dev] = 1;
+    }
+    return launch_dependent(kern, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, stream, tmK, tmK,
+                            tmV, p);
+}
+
 }  // namespace
+
+cudaError_t launch_shared_tc(const TcParams &p, int tiles, int64_t ctas, const CUtensorMap &tmK,
+                             const CUtensorMap &tmV, cudaStream_t stream) {
+    if (p.D == 64)
+        return tiles == 2 ? launch_shared_instance<2, 64>(p, ctas, tmK, tmV, stream)
+                          : launch_shared_instance<1, 64>(p, ctas, tmK, tmV, stream);
+    return tiles == 2 ? launch_shared_instance<2, 128>(p, ctas, tmK, tmV, stream)
+                      : launch_shared_instance<1, 128>(p, ctas, tmK, tmV, stream);
+}
 
 cudaError_t launch_fmha_tc(const TcParams &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,
                            const CUtensorMap &tmV, cudaStream_t stream) {

@@ -57,6 +57,7 @@
 // lets its copies and MMAs finish, frees TMEM and writes NaN.
 #include "internal.h"
 #include "ptx.cuh"
+#include "shared_prefix.cuh"
 #include "tc_order.cuh"
 
 #include <math.h>
@@ -179,7 +180,8 @@ __device__ void empty_row(const TcParams &p, int b, int hkv, int f) {
     if (p.lse) p.lse[row] = sink;
 }
 
-template <int D>
+// SHARED: the splits of prefixes that groups of sequences share (shared_prefix.cuh).
+template <int D, bool SHARED = false>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     fmha_tf32x3_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const TcParams p) {
@@ -197,9 +199,24 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 
     // ------------------------------------------------------------ work item
     const int units = p.B * p.Hkv;
-    int u, c, t0;
+    int u = 0, c, t0;
+    SharedItem shared{};
+    // The merge that follows a SHARED grid reads the sequences' own splits too, which the
+    // grid before this one writes: one CTA at least must not end before that grid has.
+    auto before_exit = [&]() {
+        if (SHARED && blockIdx.x == 0) wait_for_previous_grid();
+    };
     int split_keys = p.chunk;  // keys per split (split mode)
-    if (p.split && p.balanced) {
+    if (SHARED) {
+        shared = shared_item(p, blockIdx.x, 1, reinterpret_cast<int *>(smem + C::OFF_V));
+        if (shared.group < 0) {
+            before_exit();
+            return;
+        }
+        __syncthreads();  // (the scratch is the raw V ring)
+        c = shared.split;
+        t0 = shared.tile;
+    } else if (p.split && p.balanced) {
         // longest-first work item (the raw V ring is free until the producer starts)
         const TcItem it = tc_balanced_item(p, blockIdx.x + blockIdx.y * gridDim.x,
                                            reinterpret_cast<int *>(smem + C::OFF_V));
@@ -226,19 +243,29 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             t0 = r / units;
         }
     }
-    const int b = u / p.Hkv, hkv = u % p.Hkv;
-    if (p.split && p.chunk_range && (c < p.chunk_range[2 * b] || c >= p.chunk_range[2 * b + 1]))
+    // (SHARED: b is the group)
+    const int b = SHARED ? shared.group : u / p.Hkv, hkv = SHARED ? shared.hkv : u % p.Hkv;
+    if (!SHARED && p.split && p.chunk_range && (c < p.chunk_range[2 * b] || c >= p.chunk_range[2 * b + 1]))
         return;
-    const int seq_len = p.seq_lens[b];
-    const int qn = p.q_lens ? p.q_lens[b] : p.q_len;
-    const int rows_unit = p.G * p.q_len;
+    const int seq_len = SHARED ? shared.len : p.seq_lens[b];
+    const int qn = p.q_lens && !SHARED ? p.q_lens[b] : p.q_len;
+    const int rows_unit = (SHARED ? shared.seqs : 1) * p.G * p.q_len;
+    // Output row of tile row f, and whether it is a query.
+    auto row_of = [&](int f) -> int64_t {
+        if constexpr (SHARED) return shared_row(p, shared.seq0, hkv, f);
+        else return tile_row(p, b, hkv, f);
+    };
+    auto is_query = [&](int f) -> bool {
+        if constexpr (SHARED) return shared_real(p, shared.seq0, rows_unit, f);
+        else return f < rows_unit && f % p.q_len < qn;
+    };
     const int f0 = t0 * BM;
     const int f_last = min(f0 + BM, rows_unit) - 1;
     const bool spans = (f_last / p.q_len) != (f0 / p.q_len);
     const int i_min = spans ? 0 : f0 % p.q_len;
 
-    if (qn < 0 || qn > p.q_len || seq_len < p.row_step * qn || seq_len > p.max_pages * p.P ||
-        (p.require_full && seq_len != qn)) {
+    if (!SHARED && (qn < 0 || qn > p.q_len || seq_len < p.row_step * qn || seq_len > p.max_pages * p.P ||
+        (p.require_full && seq_len != qn))) {
         if (threadIdx.x == 0 && c == 0 && p.status) atomicOr(p.status, ATLAS_DEV_BAD_SEQLEN);
         const int rows_valid = (qn >= 0 && qn <= p.q_len) ? qn : p.q_len;
         if (!p.split && threadIdx.x < BM) {
@@ -247,12 +274,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         return;  // split mode: the merge writes NaN rows for this sequence
     }
-    if (i_min >= qn) return;  // only padding rows of a ragged sequence
+    if (!SHARED && i_min >= qn) return;  // only padding rows of a ragged sequence
     const int i_max = min(spans ? p.q_len - 1 : f_last % p.q_len, qn - 1);
     // Row i sees L - q_len + row_step * i + 1 keys: the suffix rule, or (cross attention)
     // all seq_len encoder states.
     const int L = seq_len + p.q_len - (p.row_step ? qn : 1);
-    const int kv_hi = L - p.q_len + p.row_step * i_max + 1;
+    const int kv_hi = SHARED ? seq_len : L - p.q_len + p.row_step * i_max + 1;
     if (kv_hi == 0) {  // no encoder states (split mode: the merge writes these rows)
         if (!p.split && threadIdx.x < BM) {
             const int f = f0 + threadIdx.x;
@@ -279,15 +306,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             if (threadIdx.x == 0 && p.status) atomicOr(p.status, ATLAS_DEV_BAD_PAGE);
             if (threadIdx.x < BM) {
                 const int f = f0 + threadIdx.x;
-                if (f < rows_unit && f % p.q_len < qn) {
+                if (is_query(f)) {
                     if (!p.split) {
                         nan_row<D>(p, b, hkv, f);
                     } else {
-                        float *ml = p.ws_ml + (tile_row(p, b, hkv, f) * p.n_chunks + c) * 2;
+                        float *ml = p.ws_ml + (row_of(f) * p.n_chunks + c) * 2;
                         ml[0] = ml[1] = __int_as_float(0x7fc00000);
                     }
                 }
             }
+            before_exit();
             return;
         }
     }
@@ -327,14 +355,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     if (warp == 0) {
         // -------------------------------------------------------- TMA producer
         if (lane == 0) {
-            prefetch_tmap(&tmQ);
             prefetch_tmap(&tmK);
             prefetch_tmap(&tmV);
-            mbar_arrive_expect_tx(BAR(C::B_Q), BM * D * 4);
-            const int qrow = (int)tile_row(p, b, hkv, f0);
+            if (!SHARED) {
+                prefetch_tmap(&tmQ);
+                mbar_arrive_expect_tx(BAR(C::B_Q), BM * D * 4);
+                const int qrow = (int)tile_row(p, b, hkv, f0);
 #pragma unroll
-            for (int sl = 0; sl < C::kSlabs; ++sl)
-                tma_load_2d(sb + C::OFF_Q + sl * C::kQSlab, &tmQ, 32 * sl, qrow, BAR(C::B_Q));
+                for (int sl = 0; sl < C::kSlabs; ++sl)
+                    tma_load_2d(sb + C::OFF_Q + sl * C::kQSlab, &tmQ, 32 * sl, qrow, BAR(C::B_Q));
+            }
         }
         PageIdCache pages{p.page_table + (int64_t)b * p.max_pages, (kv_end - 1) / p.P};
         const int BR = p.P < BN ? p.P : BN;
@@ -376,7 +406,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (failed && lane == 0) {
             *abort_flag = 1;
             int no_abort = 0;
-            mbar_wait_bounded(BAR(C::B_Q), 0, &no_abort, kWaitLimitNs);
+            if (!SHARED) mbar_wait_bounded(BAR(C::B_Q), 0, &no_abort, kWaitLimitNs);
             for (int j = max(0, issued_k - S); j < issued_k; ++j)
                 mbar_wait_bounded(BAR(C::B_KFULL + j % S), (j / S) & 1, &no_abort, kWaitLimitNs);
             for (int j = max(0, issued_v - S); j < issued_v; ++j)
@@ -476,11 +506,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const int r = (warp % 4) * 32 + lane;
         const uint32_t tq = tmem + ((uint32_t)((warp % 4) * 32) << 16) + C::OC;
         const int fr_row = f0 + r;
-        const bool row_ok = fr_row < rows_unit && fr_row % p.q_len < qn;
+        const bool row_ok = is_query(fr_row);
         // the running sum lives in this row's own output row or split slot
         float *run = p.split
-                         ? p.ws_acc + (tile_row(p, b, hkv, row_ok ? fr_row : 0) * p.n_chunks + c) * D
-                         : static_cast<float *>(p.out) + tile_row(p, b, hkv, row_ok ? fr_row : 0) * D;
+                         ? p.ws_acc + (row_of(row_ok ? fr_row : 0) * p.n_chunks + c) * D
+                         : static_cast<float *>(p.out) + row_of(row_ok ? fr_row : 0) * D;
         const float *m_seg_s = reinterpret_cast<const float *>(smem + C::OFF_MSEG);
         float *m_run_s = reinterpret_cast<float *>(smem + C::OFF_MRUN);
         float m_run = -INFINITY;
@@ -626,14 +656,21 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const int q4 = warp % 4;  // TMEM lane quadrant
         const int r = q4 * 32 + lane;
         const int f = f0 + r;
-        const bool valid = f < rows_unit && f % p.q_len < qn;
-        const int i = valid ? f % p.q_len : 0;
-        const int lim_row = valid ? min(L - p.q_len + p.row_step * i + 1, kv_end) : 0;
-        const int lo_row = (valid && p.window > 0) ? max(0, L - p.q_len + i + 1 - p.window) : 0;
+        const bool valid = is_query(f);
+        const int i = valid && !SHARED ? f % p.q_len : 0;
+        const int lim_row = !valid   ? 0
+                            : SHARED ? kv_end  // a prefix: every row sees all of it
+                                     : min(L - p.q_len + p.row_step * i + 1, kv_end);
+        const int lo_row =
+            (valid && !SHARED && p.window > 0) ? max(0, L - p.q_len + i + 1 - p.window) : 0;
         const bool capped = p.softcap_log2 > 0.f;
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
         const uint32_t to = tl + C::OC;
-        bool ok = wait_warp(BAR(C::B_Q), 0, abort_flag);
+        // (SHARED: the row is read where it lies; its tile's rows are of many sequences)
+        const bool in_group = SHARED && f < rows_unit;
+        const float *q_row = SHARED ? static_cast<const float *>(p.q) + row_of(in_group ? f : 0) * D
+                                    : nullptr;
+        bool ok = SHARED || wait_warp(BAR(C::B_Q), 0, abort_flag);
         if (ok) {
             // Q row r into TMEM: hi and lo (negated for a negative scale, which is
             // exact), 32 dims per slab.
@@ -643,8 +680,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 uint32_t hv[32], lv[32];
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch) {
-                    const float4 x = *reinterpret_cast<const float4 *>(
-                        smem + C::OFF_Q + sl * C::kQSlab + sw128(r, ch));
+                    float4 x;
+                    if constexpr (SHARED)
+                        x = in_group ? *reinterpret_cast<const float4 *>(q_row + 32 * sl + 4 * ch)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                    else
+                        x = *reinterpret_cast<const float4 *>(
+                            smem + C::OFF_Q + sl * C::kQSlab + sw128(r, ch));
                     const float xs[4] = {x.x * sgn, x.y * sgn, x.z * sgn, x.w * sgn};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -791,7 +833,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         // ---------------------------------------------------- epilogue
         tc_fence_after();
         if (ok) {
-            const int64_t row = tile_row(p, b, hkv, valid ? f : 0);
+            const int64_t row = row_of(valid ? f : 0);
             const float m_pre = m_used;  // the max O is relative to (before the sink)
             float osc = 1.f;  // direct mode folds the sink: m = sink log2 e, l = 1, acc = 0
             if (!p.split && p.sinks && valid) {
@@ -841,7 +883,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             }
         } else if (valid) {
             if (p.split) {
-                const int64_t slot = tile_row(p, b, hkv, f) * p.n_chunks + c;
+                const int64_t slot = row_of(f) * p.n_chunks + c;
                 p.ws_ml[slot * 2] = p.ws_ml[slot * 2 + 1] = __int_as_float(0x7fc00000);
             } else {
                 nan_row<D>(p, b, hkv, f);
@@ -856,6 +898,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    before_exit();
 #undef BAR
 }
 
@@ -879,7 +922,31 @@ cudaError_t launch_instance(const TcParams &p, const CUtensorMap &tmQ, const CUt
     return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t launch_shared_instance(const TcParams &p, int64_t ctas, const CUtensorMap &tmK,
+                                   const CUtensorMap &tmV, cudaStream_t stream) {
+    using C = Cfg<D>;
+    auto kern = fmha_tf32x3_kernel<D, true>;
+    static int configured[64] = {0};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev >= 64 || !configured[dev]) {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (err != cudaSuccess) return err;
+        if (dev < 64) configured[dev] = 1;
+    }
+    return launch_dependent(kern, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, stream, tmK, tmK,
+                            tmV, p);
+}
+
 }  // namespace
+
+cudaError_t launch_shared_tc_f32(const TcParams &p, int64_t ctas, const CUtensorMap &tmK,
+                                 const CUtensorMap &tmV, cudaStream_t stream) {
+    return p.D == 64 ? launch_shared_instance<64>(p, ctas, tmK, tmV, stream)
+                     : launch_shared_instance<128>(p, ctas, tmK, tmV, stream);
+}
 
 cudaError_t launch_fmha_tc_f32(const TcParams &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,
                                const CUtensorMap &tmV, cudaStream_t stream) {

@@ -4,6 +4,8 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <limits.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <initializer_list>
@@ -26,6 +28,17 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // Keys per pipeline stage of the split-KV kernels.
 constexpr int kSplitBlockTokens = 64;
+
+// Query tiles whose rows see fewer keys than this use a hi + lo split of P:
+// with few keys (or a peaked softmax) a single bf16 rounding of P moves the
+// output by up to 2^-8 |v| (bf16 keeps 8 significant bits).  Scores sharper than
+// unit-variance inputs at scale 1/sqrt(D) (|scale| sqrt(D) above kHiLoScale) use
+// the split on every tile.  Elsewhere the kernel decides per block (fmha_tc.cu).
+constexpr int kHiLoBelow = 512;
+constexpr float kHiLoScale = 1.25f;
+inline int hilo_below(float scale, int D) {
+    return fabsf(scale) * sqrtf((float)D) > kHiLoScale ? INT32_MAX : kHiLoBelow;
+}
 
 // Balanced split geometry of the tensor-core path: a context of L keys is cut into
 // n = ceil(L / chunk) splits of round_up(ceil(L / n), 128) keys (the last one
@@ -81,6 +94,11 @@ struct SplitParams {
     const float *sinks;         // [Hq] natural-log logits or null (direct mode only)
 };
 
+// A call's kernels (atlas_attn.cu); the entry points are this and a kind.
+atlas_status run_attention(atlas_kind kind, const void *q, const void *k_pages, const void *v_pages,
+                           const int32_t *page_table, const int32_t *seq_lens, int32_t Hq,
+                           int32_t Hkv, int32_t D, int32_t P, float scale, const atlas_launch *L);
+
 struct MergeParams {
     const int32_t *seq_lens;
     int32_t B, Hq, D, q_len, max_pages, P, chunk, n_chunks, require_full;
@@ -96,6 +114,17 @@ struct MergeParams {
     float *lse;
     int32_t sms;            // SM count: sizes the warps per row
     int32_t warps_per_row;  // set by launch_merge
+};
+
+// The same with the splits of the sequence's shared prefix (shared_prefix.cu) as further
+// states of each row.
+struct SharedMergeParams : MergeParams {
+    const int32_t *group_starts;  // [n_groups + 1]
+    const int32_t *prefix_lens;   // [n_groups]
+    int32_t n_groups, max_prefix;
+    int32_t pre_chunk, n_pre;     // keys per split, splits of the longest prefix
+    const float *pre_acc;         // [B*Hq*q_len][n_pre][D]
+    const float *pre_ml;          // [B*Hq*q_len][n_pre][2]
 };
 
 // Tensor-core (tcgen05 / TMEM) path for many query rows per (sequence, kv head):
@@ -130,6 +159,12 @@ struct TcParams {
     float *ws_acc, *ws_ml;
     uint32_t *status;
     int32_t sms;         // SM count (sizes the persistent prefill grid)
+    // Prefixes shared by groups of sequences (split mode; shared_prefix.cuh): page_table,
+    // seq_lens and max_pages are the prefixes', one row for each group, the tiles' rows
+    // those of all of a group's sequences.
+    const int32_t *group_starts;  // [n_groups + 1] first sequences, or null
+    int32_t n_groups;
+    const void *q;                // read row by row there (no tensor map)
 };
 
 // Paged KV append (kv_append.cu).
@@ -144,6 +179,12 @@ cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream);
 
 cudaError_t launch_fmha_tc(const TcParams &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,
                            const CUtensorMap &tmV, cudaStream_t stream);
+// The splits of shared prefixes, `ctas` of them at most, with `tiles` (1 or 2; fp32: 1)
+// query tiles to a CTA.
+cudaError_t launch_shared_tc(const TcParams &p, int tiles, int64_t ctas, const CUtensorMap &tmK,
+                             const CUtensorMap &tmV, cudaStream_t stream);
+cudaError_t launch_shared_tc_f32(const TcParams &p, int64_t ctas, const CUtensorMap &tmK,
+                                 const CUtensorMap &tmV, cudaStream_t stream);
 // The same for fp32 q/K/V: three tf32 products per fp32 product (fmha_tc_f32.cu).
 cudaError_t launch_fmha_tc_f32(const TcParams &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,
                                const CUtensorMap &tmV, cudaStream_t stream);
@@ -163,6 +204,7 @@ cudaError_t launch_split_bf16(const SplitParams &p, const CUtensorMap &tmK, cons
 int split_f32_cols_per_cta(int G, int q_len);
 cudaError_t launch_split_f32(const SplitParams &p, cudaStream_t stream);
 cudaError_t launch_merge(const MergeParams &p, cudaStream_t stream);
+cudaError_t launch_shared_merge(const SharedMergeParams &p, cudaStream_t stream);
 
 // Multiprocessor count of the current device (cached per device); 152 (one
 // GB300) when no device is visible.

@@ -18,6 +18,7 @@
 #include "ptx.cuh"
 
 #include <math.h>
+#include <type_traits>
 
 namespace atlas {
 namespace {
@@ -25,8 +26,35 @@ namespace {
 constexpr int kWarps = 4;  // warps per CTA: 4 / W rows
 constexpr int kGroup = 8;  // splits of one warp whose loads are in flight together
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) merge_kernel(const MergeParams p) {
+// Splits of the prefix that sequence b's group shares (0 outside all groups), -1 if there is
+// no telling: the prefix's length is out of range, or any group's borders are or descend.  All
+// lanes of a warp call this with the same b; lane k looks at groups k, k + 32, ...
+__device__ int prefix_splits(const SharedMergeParams &p, int b) {
+    int splits = 0;
+    for (int n0 = 0; n0 < p.n_groups; n0 += 32) {
+        const int n = n0 + (int)(threadIdx.x % 32);
+        bool mine = false, wrong = false;
+        int s = 0;
+        if (n < p.n_groups) {
+            const int a = p.group_starts[n], z = p.group_starts[n + 1];
+            wrong = a < 0 || z < a || z > p.B;
+            mine = a <= b && b < z;
+            if (mine) {
+                const int len = p.prefix_lens[n];
+                s = len < 0 || len > p.max_prefix ? -1 : (len + p.pre_chunk - 1) / p.pre_chunk;
+            }
+        }
+        if (__any_sync(0xffffffffu, wrong)) return -1;
+        const unsigned who = __ballot_sync(0xffffffffu, mine);
+        if (who != 0) splits = __shfl_sync(0xffffffffu, s, __ffs(who) - 1);
+    }
+    return splits;
+}
+
+template <int D, typename Params>
+__global__ void __launch_bounds__(kWarps * 32) merge_kernel(const Params p) {
+    // a call with shared prefixes: their splits follow the sequence's own
+    constexpr bool kShared = std::is_same<Params, SharedMergeParams>::value;
     constexpr int DPL = D / 32;
     const int warp = (int)(threadIdx.x / 32), lane = (int)(threadIdx.x % 32);
     const int W = p.warps_per_row;
@@ -39,8 +67,10 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const MergeParams p)
     const int b = bh / p.Hq;
     const int L = active ? p.seq_lens[b] : 0;
     const int qn = !active ? 0 : p.q_lens ? p.q_lens[b] : p.q_len;  // ragged: rows of b
+    int n_pre = 0;
+    if constexpr (kShared) n_pre = active ? prefix_splits(p, b) : 0;
     const bool bad_len = qn < 0 || qn > p.q_len || L < p.row_step * qn || L > p.max_pages * p.P ||
-                         (p.require_full && L != qn);
+                         (p.require_full && L != qn) || n_pre < 0;
     if (!bad_len && i >= qn) active = false;  // padding row: not a query, not written
     if (W == 1 && !active) return;            // (W > 1: every warp reaches the exchange)
     // the split kernel that wrote the partials has completed, its writes visible
@@ -58,7 +88,8 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const MergeParams p)
         const int chunk =
             p.balanced ? balanced_split(min(L, p.max_pages * p.P), p.chunk) : p.chunk;
         const int first = p.window > 0 ? max(0, visible - p.window) / chunk : 0;
-        const int nsplit = (visible + chunk - 1) / chunk;
+        const int n_own = (visible + chunk - 1) / chunk;
+        const int nsplit = n_own + n_pre;
         const float *ml = p.ws_ml + (int64_t)row * p.n_chunks * 2;
         if (p.sinks && sub == 0) {
             M = p.sinks[bh - b * p.Hq] * kLog2e;
@@ -66,6 +97,18 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const MergeParams p)
             has_nan = isnan(M);
         }
         const float *wa = p.ws_acc + (int64_t)row * p.n_chunks * D + lane * DPL;
+        // state s of the row: its own splits, then the prefix's
+        auto ml_of = [&](int s) -> const float * {
+            if constexpr (kShared)
+                if (s >= n_own) return p.pre_ml + ((int64_t)row * p.n_pre + s - n_own) * 2;
+            return ml + 2 * s;
+        };
+        auto acc_of = [&](int s) -> const float * {
+            if constexpr (kShared)
+                if (s >= n_own)
+                    return p.pre_acc + ((int64_t)row * p.n_pre + s - n_own) * D + lane * DPL;
+            return wa + (int64_t)s * D;
+        };
         // [kWarps][kGroup][32 lanes] x 16 bytes (D = 128): each lane's slice of a
         // split lands here, so no registers are held while the loads are in flight
         __shared__ __align__(16) uint8_t stage[D == 128 ? kWarps * kGroup * 512 : 16];
@@ -76,7 +119,7 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const MergeParams p)
 #pragma unroll
                 for (int u = 0; u < kGroup; ++u)
                     if (s0 + u * W < nsplit)
-                        cp_async16(my_stage + u * 512, wa + (int64_t)(s0 + u * W) * D, 16);
+                        cp_async16(my_stage + u * 512, acc_of(s0 + u * W), 16);
                 cp_async_commit();
             }
 #pragma unroll
@@ -87,10 +130,10 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const MergeParams p)
 #pragma unroll
                 for (int j = 0; j < DPL; ++j) a[u][j] = 0.f;
                 if (s < nsplit) {
-                    m[u] = ml[2 * s];
-                    l[u] = ml[2 * s + 1];
+                    m[u] = ml_of(s)[0];
+                    l[u] = ml_of(s)[1];
                     if (DPL != 4) {
-                        const float2 v = *reinterpret_cast<const float2 *>(wa + (int64_t)s * D);
+                        const float2 v = *reinterpret_cast<const float2 *>(acc_of(s));
                         a[u][0] = v.x;
                         a[u][1 % DPL] = v.y;
                     }
@@ -195,16 +238,17 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const MergeParams p)
 
 }  // namespace
 
-cudaError_t launch_merge(const MergeParams &p, cudaStream_t stream) {
+template <typename Params>
+static cudaError_t launch(const Params &p, int states, cudaStream_t stream) {
     const int64_t rows = (int64_t)p.B * p.Hq * p.q_len;
     if (rows >= INT32_MAX) return cudaErrorInvalidValue;  // make_plan refuses these
     // Several warps per row when the rows alone would leave most warp slots empty
     // and there are splits to share.
-    MergeParams q = p;
+    Params q = p;
     const int64_t target = (int64_t)(p.sms > 0 ? p.sms : 1) * 16;
     q.warps_per_row = 1;
     while (q.warps_per_row < kWarps && rows * q.warps_per_row < target &&
-           p.n_chunks >= 2 * q.warps_per_row)
+           states >= 2 * q.warps_per_row)
         q.warps_per_row *= 2;
     const int64_t rows_per_cta = kWarps / q.warps_per_row;
     cudaLaunchConfig_t cfg = {};
@@ -216,8 +260,16 @@ cudaError_t launch_merge(const MergeParams &p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return p.D == 128 ? cudaLaunchKernelEx(&cfg, merge_kernel<128>, q)
-                      : cudaLaunchKernelEx(&cfg, merge_kernel<64>, q);
+    return p.D == 128 ? cudaLaunchKernelEx(&cfg, merge_kernel<128, Params>, q)
+                      : cudaLaunchKernelEx(&cfg, merge_kernel<64, Params>, q);
+}
+
+cudaError_t launch_merge(const MergeParams &p, cudaStream_t stream) {
+    return launch(p, p.n_chunks, stream);
+}
+
+cudaError_t launch_shared_merge(const SharedMergeParams &p, cudaStream_t stream) {
+    return launch(p, p.n_chunks + p.n_pre, stream);
 }
 
 }  // namespace atlas

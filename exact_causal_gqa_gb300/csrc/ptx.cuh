@@ -92,6 +92,12 @@ __device__ __forceinline__ void allow_dependent_launch() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Wait until the grid before this one in the stream, whose programmatic dependent this one
+// is, has completed and its writes are visible.
+__device__ __forceinline__ void wait_for_previous_grid() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- cp.async
 // 16-byte global -> shared copy; with src_bytes = 0 the destination is zero-filled
 // and nothing is read.

@@ -1,0 +1,198 @@
+// shared_prefix.cu -- attention of a batch whose sequences share prefixes
+// (include/atlas_shared.h): checks, the plan, and three launches.
+//
+//   1. the sequences' own keys: the split kernels of the causal calls as they stand, partial
+//      states (m, l, acc) of each row and split to the workspace;
+//   2. the prefixes: the tensor-core kernels with the rows of all of a group's sequences
+//      gathered into tiles (shared_prefix.cuh), partial states likewise.  Launched as a
+//      dependent of 1, whose results it does not need: its CTAs take the SMs as those of 1
+//      leave them;
+//   3. the merge of a row's states of both kinds.
+//
+// Keys of a prefix are read once for each 128 or 256 rows of a kv head instead of once for
+// each sequence, from L2 for all tiles but the first.
+#include "internal.h"
+#include "atlas_shared.h"
+
+#include <limits.h>
+#include <math.h>
+#include <algorithm>
+
+namespace atlas {
+namespace {
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+struct SharedPlan {
+    Plan own;
+    int tiles;             // query tiles to a CTA
+    int chunk, n_pre;      // keys per prefix split, splits of the longest prefix
+    int64_t ctas;          // most (group, kv head, split, tiles) items
+    size_t acc_at, ml_at;  // the prefixes' states in the workspace
+    size_t bytes;
+};
+
+atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const atlas_shared *S,
+                         const atlas_launch *L, SharedPlan *plan) {
+    if (!S || !L) return ATLAS_ERR_INVALID_ARG;
+    if (L->window != 0) return ATLAS_ERR_INVALID_ARG;
+    if (L->phase != ATLAS_PHASE_ALL || L->chunk_range) return ATLAS_ERR_UNSUPPORTED;
+    atlas_launch own = *L;
+    own.phase = ATLAS_PHASE_CHUNKS;  // partial states only, whatever the sizes
+    own.debug_flags &= ~ATLAS_DEBUG_TC_DIRECT;
+    const atlas_status st = make_plan(ATLAS_KIND_SUFFIX, Hq, Hkv, D, P, &own, &plan->own);
+    if (st != ATLAS_OK) return st;
+    if (S->n_groups < 1 || S->n_groups > L->batch || S->max_prefix_pages < 1)
+        return ATLAS_ERR_INVALID_ARG;
+    const int64_t max_prefix = (int64_t)S->max_prefix_pages * P;
+    if (max_prefix > INT32_MAX / 2) return ATLAS_ERR_INVALID_ARG;
+
+    const int sms = L->sm_count > 0 ? L->sm_count : device_sm_count();
+    const int64_t rows = (int64_t)L->batch * (Hq / Hkv) * L->q_len;  // of one kv head, all groups
+    const bool f32 = L->kv_dtype == ATLAS_F32;
+    plan->tiles = !f32 && rows > 128 * (int64_t)S->n_groups ? 2 : 1;
+    // CTAs of one split: a group's last may be partly filled
+    const int64_t cta_rows = 128 * plan->tiles;
+    const int64_t units = (rows / cta_rows + S->n_groups) * Hkv;
+    const int64_t likely = std::max<int64_t>((rows + cta_rows - 1) / cta_rows, S->n_groups) * Hkv;
+    int64_t chunk = round_up(L->split_tokens, 128);
+    if (chunk == 0) {
+        const int64_t splits = std::max<int64_t>(1, sms * 3 / likely);
+        chunk = std::max<int64_t>(512, round_up((max_prefix + splits - 1) / splits, 128));
+    }
+    chunk = std::min(chunk, round_up(max_prefix, 128));
+    plan->chunk = (int)chunk;
+    plan->n_pre = (int)((max_prefix + chunk - 1) / chunk);
+    plan->ctas = units * plan->n_pre;
+    if (plan->ctas >= INT32_MAX) return ATLAS_ERR_UNSUPPORTED;
+    const int64_t out_rows = (int64_t)L->batch * Hq * L->q_len;
+    plan->acc_at = (size_t)round_up((int64_t)plan->own.ws_bytes, 256);
+    plan->ml_at = plan->acc_at + (size_t)round_up(out_rows * plan->n_pre * D * 4, 256);
+    plan->bytes = plan->ml_at + (size_t)out_rows * plan->n_pre * 8;
+    return ATLAS_OK;
+}
+
+}  // namespace
+}  // namespace atlas
+
+extern "C" size_t atlas_attn_shared_workspace_size(int32_t n_q_heads, int32_t n_kv_heads,
+                                                   int32_t head_dim, int32_t page_tokens,
+                                                   const atlas_shared *S, const atlas_launch *L) {
+    atlas::SharedPlan plan;
+    return atlas::shared_plan(n_q_heads, n_kv_heads, head_dim, page_tokens, S, L, &plan) == ATLAS_OK
+               ? plan.bytes
+               : SIZE_MAX;
+}
+
+extern "C" atlas_status atlas_attn_shared(const void *q, const void *k_pages, const void *v_pages,
+                                          const int32_t *page_table, const int32_t *seq_lens,
+                                          int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                          int32_t page_tokens, float scale, const atlas_shared *S,
+                                          const atlas_launch *L) {
+    using namespace atlas;
+    // (the whole call's checks come before its first launch)
+    if (!q || !k_pages || !v_pages || !page_table || !seq_lens || !S || !L || !S->prefix_table ||
+        !S->prefix_lens || !S->group_starts || !L->out)
+        return ATLAS_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(L->out) ||
+        !aligned16(L->workspace) ||
+        !aligned4({page_table, seq_lens, S->prefix_table, S->prefix_lens, S->group_starts, L->lse,
+                   L->sinks, L->q_lens, L->status_word}))
+        return ATLAS_ERR_INVALID_ARG;
+    if (!(fabsf(scale) < INFINITY) || !(L->softcap >= 0.f) || L->softcap == INFINITY)
+        return ATLAS_ERR_INVALID_ARG;
+    const int32_t Hq = n_q_heads, Hkv = n_kv_heads, D = head_dim, P = page_tokens;
+    SharedPlan plan;
+    atlas_status st = shared_plan(Hq, Hkv, D, P, S, L, &plan);
+    if (st != ATLAS_OK) return st;
+    if (!L->workspace || L->workspace_bytes < plan.bytes) return ATLAS_ERR_WORKSPACE;
+    cudaStream_t stream = static_cast<cudaStream_t>(L->stream);
+    cudaEvent_t ev[3] = {nullptr, nullptr, nullptr};
+    if (L->events)
+        for (int i = 0; i < 3; ++i) ev[i] = static_cast<cudaEvent_t>(L->events[i]);
+
+    const bool f32 = L->kv_dtype == ATLAS_F32;
+    const int bn = f32 ? 64 : 128;  // keys per block of the kernel
+    CUtensorMap tmK, tmV;
+    st = encode_rows_map(&tmK, k_pages, (int64_t)L->num_pages * Hkv * P, D, std::min(P, bn), f32);
+    if (st == ATLAS_OK)
+        st = encode_rows_map(&tmV, v_pages, (int64_t)L->num_pages * Hkv * P, D, std::min(P, bn), f32);
+    if (st != ATLAS_OK) return st;
+
+    atlas_launch own = *L;
+    own.phase = ATLAS_PHASE_CHUNKS;
+    own.debug_flags &= ~ATLAS_DEBUG_TC_DIRECT;
+    own.events = nullptr;
+    own.workspace_bytes = plan.own.ws_bytes;
+    if (ev[0] && cudaEventRecord(ev[0], stream) != cudaSuccess) return ATLAS_ERR_CUDA;
+    st = run_attention(ATLAS_KIND_SUFFIX, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P,
+                       scale, &own);
+    if (st != ATLAS_OK) return st;
+
+    float *pre_acc = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.acc_at);
+    float *pre_ml = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.ml_at);
+    TcParams tp{};
+    tp.page_table = S->prefix_table;
+    tp.seq_lens = S->prefix_lens;
+    tp.B = L->batch;
+    tp.Hq = Hq;
+    tp.Hkv = Hkv;
+    tp.G = Hq / Hkv;
+    tp.D = D;
+    tp.P = P;
+    tp.q_len = L->q_len;
+    tp.max_pages = S->max_prefix_pages;
+    tp.num_pages = L->num_pages;
+    tp.split = 1;
+    tp.chunk = plan.chunk;
+    tp.n_chunks = plan.n_pre;
+    tp.hilo_below = plan.tiles == 1 ? INT32_MAX : hilo_below(scale, D);
+    tp.negate_scores = scale < 0.f;
+    tp.scale_log2 = fabsf(scale) * kLog2e;
+    tp.softcap_log2 = L->softcap > 0.f ? L->softcap * kLog2e : 0.f;
+    tp.softcap_inv = L->softcap > 0.f ? fabsf(scale) / L->softcap : 0.f;
+    tp.q_lens = L->q_lens;
+    tp.ws_acc = pre_acc;
+    tp.ws_ml = pre_ml;
+    tp.status = L->status_word;
+    tp.sms = L->sm_count > 0 ? L->sm_count : device_sm_count();
+    tp.group_starts = S->group_starts;
+    tp.n_groups = S->n_groups;
+    tp.q = q;
+    cudaError_t err = f32 ? launch_shared_tc_f32(tp, plan.ctas, tmK, tmV, stream)
+                          : launch_shared_tc(tp, plan.tiles, plan.ctas, tmK, tmV, stream);
+    if (err != cudaSuccess) return ATLAS_ERR_CUDA;
+    if (ev[1] && cudaEventRecord(ev[1], stream) != cudaSuccess) return ATLAS_ERR_CUDA;
+
+    SharedMergeParams mp{};
+    mp.seq_lens = seq_lens;
+    mp.B = L->batch;
+    mp.Hq = Hq;
+    mp.D = D;
+    mp.q_len = L->q_len;
+    mp.max_pages = L->max_pages_per_seq;
+    mp.P = P;
+    mp.chunk = plan.own.chunk;
+    mp.n_chunks = plan.own.n_chunks;
+    mp.row_step = 1;
+    mp.sinks = L->sinks;
+    mp.q_lens = L->q_lens;
+    mp.ws_acc = static_cast<float *>(L->workspace);
+    mp.ws_ml = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.own.ml_offset);
+    mp.out = L->out;
+    mp.out_bf16 = L->out_dtype == ATLAS_BF16;
+    mp.lse = L->lse;
+    mp.sms = tp.sms;
+    mp.group_starts = S->group_starts;
+    mp.prefix_lens = S->prefix_lens;
+    mp.n_groups = S->n_groups;
+    mp.max_prefix = S->max_prefix_pages * P;
+    mp.pre_chunk = plan.chunk;
+    mp.n_pre = plan.n_pre;
+    mp.pre_acc = pre_acc;
+    mp.pre_ml = pre_ml;
+    if (launch_shared_merge(mp, stream) != cudaSuccess) return ATLAS_ERR_CUDA;
+    if (ev[2] && cudaEventRecord(ev[2], stream) != cudaSuccess) return ATLAS_ERR_CUDA;
+    return ATLAS_OK;
+}

@@ -1,0 +1,109 @@
+// shared_prefix.cuh -- work items and rows of prefixes that groups of sequences share, for
+// the tensor-core kernels (bf16 and fp32).
+//
+// A prefix's keys are seen by every row of every sequence of its group, so the rows of one
+// kv head -- (sequence, q head of the kv head, query row), in that order -- form one long
+// list that is cut into 128-row tiles: a tile's rows may belong to many sequences, and each
+// K/V block is read once for all of them.  The items of a call are (group, kv head, split of
+// the prefix, tiles of one CTA), tiles fastest, so that the CTAs which read the same keys run
+// side by side and all but the first find them in L2.  Group sizes and prefix lengths are
+// known on the device alone: each CTA counts the items of all groups (one lane for each) and
+// finds its own; the grid covers the most that the call's sizes allow, and the CTAs behind
+// the last item leave.
+#pragma once
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace atlas {
+
+struct SharedItem {
+    int group, hkv, split, tile;  // group < 0: no item for this CTA
+    int seq0, seqs, len;          // the group's sequences and its prefix's keys
+};
+
+// All threads of the CTA call this (it synchronises the CTA); `scratch`: 7 ints of shared
+// memory.  Item 0 reports groups that are out of range; they have no items.
+__device__ inline SharedItem shared_item(const TcParams &p, int item, int tiles_per_cta, int *scratch) {
+    if (threadIdx.x < 32) {
+        const int lane = (int)threadIdx.x;
+        if (lane == 0) scratch[0] = -1;
+        __syncwarp();
+        int64_t base = 0;  // items of the groups before these (64 bits: starts out of order repeat)
+        bool bad = false;
+        for (int n0 = 0; n0 < p.n_groups; n0 += 32) {
+            const int n = n0 + lane;
+            int seq0 = 0, seqs = 0, len = 0, ctas = 0, items = 0;
+            if (n < p.n_groups) {
+                seq0 = p.group_starts[n];
+                const int end = p.group_starts[n + 1];
+                len = p.seq_lens[n];
+                if (seq0 < 0 || end < seq0 || end > p.B || len < 0 || len > p.max_pages * p.P) {
+                    bad = true;
+                } else {
+                    seqs = end - seq0;
+                    const int64_t rows = (int64_t)seqs * p.G * p.q_len;
+                    ctas = (int)((rows + 128 * tiles_per_cta - 1) / (128 * tiles_per_cta));
+                    items = ctas * (int)(((int64_t)len + p.chunk - 1) / p.chunk) * p.Hkv;
+                }
+            }
+            int64_t upto = items;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+                if (lane >= d) upto += x;
+            }
+            const int64_t first = base + upto - items;
+            if (item >= first && item < first + items) {
+                const int at = (int)(item - first);
+                const int rest = at / ctas;
+                const int splits = items / (ctas * p.Hkv);
+                scratch[0] = n;
+                scratch[1] = rest / splits;
+                scratch[2] = rest % splits;
+                scratch[3] = at % ctas * tiles_per_cta;
+                scratch[4] = seq0;
+                scratch[5] = seqs;
+                scratch[6] = len;
+            }
+            base += __shfl_sync(0xffffffffu, upto, 31);
+            if (base > item && item > 0) break;
+        }
+        if (bad && item == 0 && p.status) atomicOr(p.status, ATLAS_DEV_BAD_SEQLEN);
+    }
+    __syncthreads();
+    return {scratch[0], scratch[1], scratch[2], scratch[3], scratch[4], scratch[5], scratch[6]};
+}
+
+// Output row of tile row f of a group whose first sequence is seq0.
+__device__ __forceinline__ int64_t shared_row(const TcParams &p, int seq0, int hkv, int f) {
+    const int per = p.G * p.q_len, s = f / per;
+    return ((int64_t)(seq0 + s) * p.Hq + (int64_t)hkv * p.G) * p.q_len + (f - s * per);
+}
+
+// Whether tile row f is a query: inside the group, and not padding of a ragged sequence.
+__device__ __forceinline__ bool shared_real(const TcParams &p, int seq0, int rows, int f) {
+    if (f >= rows) return false;
+    const int per = p.G * p.q_len, s = f / per;
+    return !p.q_lens || (f - s * per) % p.q_len < p.q_lens[seq0 + s];
+}
+
+// A launch that may start as soon as every CTA of the grid before it in the stream has
+// started or ended.
+template <typename... Args>
+cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t stream, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace atlas

@@ -1,0 +1,339 @@
+"""Attention of sequences that share prefixes (atlas_attn_shared) against a plain fp64 form:
+groups of all sizes, prefixes and own caches from one key on, ragged rows, every kernel path.
+
+Tolerances are those of the causal calls (gpu_helpers), since the arithmetic is theirs: fp32
+1e-5 of the largest |out|, bf16 inputs with fp32 output 2e-3, a bf16 output the rounding of the
+fp32 one.  lse: fp32 2e-5, bf16 1e-4, as there."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import exact_causal_gqa_gb300 as atlas
+from exact_causal_gqa_gb300 import _build
+from tests.gpu_helpers import BF16_ABS, F32_REL
+from tests.operator_refs import widen
+from tests.paging import page_kv
+from tests.serving_refs import shared_rows
+
+SIZE_MAX = ctypes.c_size_t(-1).value
+gpu = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# ------------------------------------------------------------------ host side
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return atlas.load_library()
+
+
+def launch(**kw):
+    L = atlas._Launch()
+    L.batch, L.max_pages_per_seq, L.num_pages, L.q_len = 4, 8, 64, 1
+    L.q_dtype = L.kv_dtype = L.out_dtype = 1
+    L.out = 0x1000
+    for k, v in kw.items():
+        setattr(L, k, v)
+    return L
+
+
+def prefixes(**kw):
+    S = atlas._Shared(0x1000, 0x1000, 0x1000, 2, 16)
+    for k, v in kw.items():
+        setattr(S, k, v)
+    return S
+
+
+def ws(lib, S=None, Hq=8, Hkv=2, D=128, P=16, **kw):
+    return lib.atlas_attn_shared_workspace_size(Hq, Hkv, D, P, ctypes.byref(S or prefixes()),
+                                                ctypes.byref(launch(**kw)))
+
+
+def call(lib, S, L, ptrs=(0x1000,) * 5, scale=0.1):
+    return lib.atlas_attn_shared(*ptrs, 8, 2, 128, 16, ctypes.c_float(scale),
+                                 ctypes.byref(S) if S else None, ctypes.byref(L) if L else None)
+
+
+@pytest.mark.parametrize("S,kw", [
+    (None, dict(window=4)), (None, dict(window=-1)), (None, dict(phase=1)), (None, dict(phase=2)),
+    (None, dict(chunk_range=0x1000)), (None, dict(Hq=7)), (None, dict(D=96)), (None, dict(P=12)),
+    (None, dict(q_len=0)), (None, dict(batch=0)), (None, dict(q_len=129)), (None, dict(sm_count=-1)),
+    (None, dict(split_tokens=32)), (None, dict(q_dtype=0)), (None, dict(out_dtype=2)),
+    (dict(n_groups=0), {}), (dict(n_groups=5), {}), (dict(n_groups=-1), {}),
+    (dict(max_prefix_pages=0), {}), (dict(max_prefix_pages=-1), {}),
+    (dict(max_prefix_pages=1 << 30), {})])
+def test_refusals(lib, S, kw):
+    assert ws(lib, **kw, S=prefixes(**(S or {}))) == SIZE_MAX
+
+
+def test_workspace_holds_the_states_of_both_parts(lib):
+    # rows of 128 floats and (m, l): own 128 keys in splits of 64, prefix 256 in splits of 128
+    rows, own, pre = 4 * 8, 2, 2
+    n = ws(lib, split_tokens=64)
+    acc = rows * 128 * 4
+    own_bytes = (own * acc + rows * own * 8 + 255) // 256 * 256
+    assert n == own_bytes + pre * acc + rows * pre * 8
+    assert ws(lib) != SIZE_MAX and ws(lib, batch=4, S=prefixes(n_groups=4)) != SIZE_MAX
+    assert atlas.shared_workspace_size((4, 8, 1, 128), 8, 2, 128, 16, 8, 2, 16, 64, split_tokens=64) == n
+    with pytest.raises(atlas.AtlasError):
+        atlas.shared_workspace_size((4, 8, 1, 128), 8, 2, 128, 16, 8, 5, 16, 64)
+
+
+def test_arguments_are_checked_before_any_launch(lib):
+    need = ws(lib)
+    good = dict(workspace=0x1000, workspace_bytes=need)
+    assert call(lib, None, launch(**good)) == 1 and call(lib, prefixes(), None) == 1
+    for name in ("prefix_table", "prefix_lens", "group_starts"):
+        assert call(lib, prefixes(**{name: None}), launch(**good)) == 1
+        assert call(lib, prefixes(**{name: 0x1002}), launch(**good)) == 1
+    for k in range(5):
+        assert call(lib, prefixes(), launch(**good), tuple(None if j == k else 0x1000 for j in range(5))) == 1
+    for k in range(3):
+        assert call(lib, prefixes(), launch(**good), tuple(0x1008 if j == k else 0x1000 for j in range(5))) == 1
+    assert call(lib, prefixes(), launch(**good, lse=0x1001)) == 1
+    assert call(lib, prefixes(), launch(**{**good, "out": None})) == 1
+    assert call(lib, prefixes(), launch(**{**good, "out": 0x1008})) == 1
+    assert call(lib, prefixes(), launch(workspace=0x1000, workspace_bytes=need - 1)) == 3
+    assert call(lib, prefixes(), launch()) == 3
+    assert call(lib, prefixes(), launch(workspace=0x1008, workspace_bytes=need)) == 1
+    for scale in (float("inf"), float("nan"), -float("inf")):
+        assert call(lib, prefixes(), launch(**good), scale=scale) == 1
+    assert call(lib, prefixes(), launch(**good, softcap=-1.0)) == 1
+    assert call(lib, prefixes(), launch(**good, softcap=float("inf"))) == 1
+    assert call(lib, prefixes(), launch(**good, window=3)) == 1
+    assert call(lib, prefixes(), launch(**good, phase=1)) == 2
+
+
+def test_the_plain_form_on_a_case_worked_by_hand():
+    # prefix scores 0, ln 2 over values 1, 2; own score ln 3 over 3: weights 1/6, 2/6, 3/6
+    pk, pv = np.array([0.0, np.log(2)]).reshape(1, 2, 1), np.array([1.0, 2.0]).reshape(1, 2, 1)
+    k, v = np.full((2, 1, 1, 1), np.log(3)), np.full((2, 1, 1, 1), 3.0)
+    out, lse = shared_rows(np.ones((2, 2, 1, 1)), [(pk, pv)], [0, 1], k, v, [1, 1], 1.0)
+    assert np.allclose(out[0], 14 / 6) and np.allclose(lse[0], np.log(6))
+    assert np.allclose(out[1], 3) and np.allclose(lse[1], np.log(3))    # in no group
+
+
+# ------------------------------------------------------------------ on the GPU
+class Case:
+    """Random inputs of a call; pages of own caches and prefixes mixed in one pool, everything
+    behind their ends NaN, table entries behind them out of range."""
+
+    def __init__(self, dtype, Hq, Hkv, D, P, q_len, starts, pre, lens, seed, ragged=None):
+        r = np.random.default_rng(seed)
+
+        def normal(*shape):
+            return torch.from_numpy(r.standard_normal(shape, dtype=np.float32)).to(DT[dtype])
+
+        B, n = len(lens), len(pre)
+        self.q = normal(B, Hq, q_len, D)
+        T = max(list(lens) + list(pre) + [1])
+        self.k, self.v = normal(B + n, Hkv, T, D), normal(B + n, Hkv, T, D)
+        kp, vp, table = page_kv(self.k.float().numpy(), self.v.float().numpy(), list(lens) + list(pre),
+                                P, seed=seed, pad_page=10 ** 6, extra_pages=2)
+        width = [max(1, -(-max(x) // P)) for x in (lens, pre)]
+        self.sizes = Hq, Hkv, D, P
+        self.lens, self.pre, self.starts, self.ragged = list(lens), list(pre), list(starts), ragged
+        i32 = dict(dtype=torch.int32, device="cuda")
+        self.args = [self.q.cuda(), *(torch.from_numpy(x).to(DT[dtype]).cuda() for x in (kp, vp)),
+                     torch.from_numpy(table[B:, : width[1]].copy()).cuda(), torch.tensor(self.pre, **i32),
+                     torch.tensor(self.starts, **i32), torch.from_numpy(table[:B, : width[0]].copy()).cuda(),
+                     torch.tensor(self.lens, **i32)]
+        self.q_lens = None if ragged is None else torch.tensor(ragged, **i32)
+
+    def __call__(self, scale, **kw):
+        return atlas.shared(*self.args, *self.sizes, scale, q_lens=self.q_lens, **kw)
+
+    def expected(self, scale, sinks=None, softcap=0.0):
+        B = len(self.lens)
+        k, v = widen(self.k), widen(self.v)
+        parts = [(k[B + n, :, : self.pre[n]], v[B + n, :, : self.pre[n]]) for n in range(len(self.pre))]
+        return shared_rows(widen(self.q), parts, self.starts, k[:B], v[:B], self.lens, scale,
+                           self.ragged, sinks, softcap)
+
+
+CASES = [
+    # dtype, Hq, Hkv, D, P, q_len, starts, prefix lengths, own lengths, options
+    ("bf16", 8, 2, 128, 16, 1, [0, 3], [300], [1, 17, 40], {}),
+    ("bf16", 8, 2, 128, 16, 1, [0, 1], [1], [1], {}),                              # one key and one key
+    ("bf16", 4, 4, 64, 64, 1, [0, 2, 5], [129, 1000], [1, 64, 65, 3, 200], dict(sinks=True)),
+    ("bf16", 8, 1, 128, 8, 1, [0, 20], [700], list(range(1, 21)), {}),             # 160 rows: a pair of tiles
+    ("bf16", 8, 2, 64, 16, 3, [0, 0, 4, 4], [50, 77, 5], [3, 4, 60, 9], {}),        # empty groups
+    ("bf16", 4, 2, 128, 32, 1, [1, 3], [90], [5, 6, 7, 8], {}),                    # some in no group
+    ("bf16", 6, 2, 64, 16, 5, [0, 2, 4], [0, 260], [5, 9, 30, 77], dict(ragged=[5, 1, 0, 3])),
+    ("bf16", 12, 4, 128, 128, 2, [0, 1, 2, 3], [128, 127, 129], [2, 128, 300], dict(softcap=3.0, scale=-0.07)),
+    ("bf16", 8, 2, 128, 16, 40, [0, 3], [513], [40, 41, 90], {}),                  # 480 rows, own tiles too
+    ("bf16", 4, 1, 64, 64, 150, [0, 2, 3], [200, 64], [150, 333, 151], dict(ragged=[150, 9, 131])),
+    ("bf16", 8, 2, 128, 16, 1, [0, 40], [1025], [1 + 5 * b % 33 for b in range(40)], dict(split_tokens=64)),
+    ("bf16", 16, 2, 128, 16, 1, [0, 2], [3000], [100, 2], dict(split_tokens=128, sinks=True)),
+    ("bf16", 2, 1, 64, 16, 1, list(range(0, 41)), [3 * n % 50 for n in range(40)], [1 + n % 7 for n in range(40)], {}),
+    ("f32", 8, 2, 128, 16, 1, [0, 3], [300], [1, 17, 40], {}),
+    ("f32", 4, 4, 64, 32, 1, [0, 1, 4], [1, 1000], [1, 64, 65, 3], dict(sinks=True)),
+    ("f32", 8, 1, 64, 8, 2, [0, 20], [700], list(range(2, 22)), {}),               # three tiles
+    ("f32", 6, 2, 128, 16, 5, [0, 2, 4], [0, 260], [5, 9, 30, 77], dict(ragged=[5, 1, 0, 3])),
+    ("f32", 4, 2, 64, 128, 33, [0, 1, 2], [129, 65], [33, 300], dict(softcap=4.0, scale=-0.11)),
+    ("f32", 8, 2, 128, 64, 1, [1, 2], [2100], [5, 70], dict(split_tokens=192)),
+]
+
+
+def check(x, dtype, scale, **opt):
+    sinks = torch.linspace(-1, 3, x.sizes[0]) if opt.get("sinks") else None
+    ref, ref_lse = x.expected(scale, None if sinks is None else widen(sinks), opt.get("softcap", 0.0))
+    kw = dict(split_tokens=opt.get("split_tokens", 0), softcap=opt.get("softcap", 0.0),
+              sinks=None if sinks is None else sinks.cuda())
+    out = torch.full(x.q.shape, 99.0, dtype=torch.float32, device="cuda")
+    lse = torch.full(x.q.shape[:3], 99.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert x(scale, out=out, lse=lse, status=status, **kw) is out
+    assert int(status.item()) == 0
+    got, got_lse = widen(out), widen(lse)
+    real = ~np.isnan(ref_lse)
+    assert (got[~real] == 99).all() and (got_lse[~real] == 99).all()   # padding rows stay
+    assert np.isfinite(got).all()
+    tol = F32_REL * np.abs(ref[real]).max() if dtype == "f32" else BF16_ABS
+    assert np.abs(got[real] - ref[real]).max() <= tol
+    assert np.abs(got_lse[real] - ref_lse[real]).max() <= (2e-5 if dtype == "f32" else 1e-4)
+    if dtype == "bf16":                                                # the bf16 output rounds it
+        low = torch.full(x.q.shape, 99.0, dtype=torch.bfloat16, device="cuda")
+        x(scale, out=low, **kw)
+        assert torch.equal(low, out.to(torch.bfloat16))
+
+
+@gpu
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,P,q_len,starts,pre,lens,opt", CASES)
+def test_matches_the_plain_form(dtype, Hq, Hkv, D, P, q_len, starts, pre, lens, opt):
+    x = Case(dtype, Hq, Hkv, D, P, q_len, starts, pre, lens, 200 + q_len, opt.get("ragged"))
+    check(x, dtype, **{"scale": D ** -0.5, **opt})
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,q_len", [(5, 1), (3, 24)])
+def test_no_prefix_is_a_suffix(dtype, B, q_len):
+    """Prefixes of no keys leave the states of the sequences' own splits: with the same split
+    size the merge gives the suffix call's bits."""
+    lens = [q_len + 31 * b for b in range(B)]
+    x = Case(dtype, 8, 2, 128, 16, q_len, [0, 2, B], [0, 0], lens, 3)
+    a = x(0.09, split_tokens=64)
+    q, kp, vp, _, _, _, table, own = x.args
+    assert torch.equal(a, atlas.suffix(q, kp, vp, table, own, *x.sizes, 0.09, split_tokens=64))
+
+
+@gpu
+def test_the_order_of_the_groups_changes_no_bits():
+    """A sequence's result depends on its own group alone."""
+    x = Case("bf16", 8, 2, 128, 16, 1, [0, 2, 5], [300, 90], [9, 8, 7, 6, 5], 4)
+    a = x(0.09)
+    q, kp, vp, ptab, plen, starts, table, own = x.args
+    at = torch.tensor([2, 3, 4, 0, 1], device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    b = atlas.shared(q[at].contiguous(), kp, vp, ptab.flip(0).contiguous(), plen.flip(0).contiguous(),
+                     torch.tensor([0, 3, 5], **i32), table[at].contiguous(), own[at].contiguous(), *x.sizes, 0.09)
+    assert torch.equal(a[at], b)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,q_len", [("bf16", 1), ("bf16", 40), ("f32", 1), ("f32", 40)])
+def test_bad_lengths_groups_and_pages_are_reported(dtype, q_len):
+    x = Case(dtype, 8, 2, 64, 16, q_len, [0, 2, 4], [100, 70], [50, 41, 60, 77], 8)
+    good = x(0.1)
+
+    def again(k, value, bit, nan):
+        args = list(x.args)
+        args[k] = torch.tensor(value, dtype=torch.int32, device="cuda") if isinstance(value, list) else value
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = atlas.shared(*args, *x.sizes, 0.1, status=status)
+        assert int(status.item()) == bit
+        for b in range(4):
+            if b in nan:
+                assert torch.isnan(out[b]).all()
+            else:
+                assert torch.equal(out[b], good[b])
+
+    for bad in (-1, x.args[3].shape[1] * 16 + 1):
+        again(4, [100, bad], atlas.DEV_BAD_SEQLEN, (2, 3))
+    for bad in (q_len - 1, x.args[6].shape[1] * 16 + 1):
+        again(7, [50, bad, 60, 77], atlas.DEV_BAD_SEQLEN, (1,))
+    for starts in ([-1, 2, 4], [0, 2, 5], [2, 0, 4], [0, 4, 2], [0, 2 ** 31 - 1, 4], [0, -(2 ** 31), 4]):
+        again(5, starts, atlas.DEV_BAD_SEQLEN, (0, 1, 2, 3))
+    for k, row, nan in ((3, 0, (0, 1)), (6, 3, (3,))):
+        for page in (-5, x.args[1].shape[0]):
+            table = x.args[k].clone()
+            table[row, 1] = page
+            again(k, table, atlas.DEV_BAD_PAGE, nan)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,q_len", [("bf16", 1), ("bf16", 24), ("f32", 1)])
+def test_captured_and_replayed_with_other_groups_and_lengths(dtype, q_len):
+    x = Case(dtype, 8, 2, 128, 16, q_len, [0, 2, 4], [500, 100], [40, 41, 60, 77], 9)
+    q, kp, vp, ptab, plen, starts, table, own = x.args
+    out = torch.empty_like(q)
+    space = torch.empty(atlas.shared_workspace_size(q.shape, 8, 2, 128, 16, table.shape[1], 2, ptab.shape[1],
+                                                    kp.shape[0], dtype=DT[dtype]),
+                        dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        x(0.09, out=out, workspace=space)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            x(0.09, out=out, workspace=space)
+    for p, s, o in (([500, 100], [0, 2, 4], [40, 41, 60, 77]), ([0, 100], [0, 3, 4], [24, 33, 25, 70]),
+                    ([1, 0], [4, 4, 4], [40, 30, 24, 25])):
+        torch.cuda.synchronize()
+        for t, value in ((plen, p), (starts, s), (own, o)):
+            t.copy_(torch.tensor(value, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, x(0.09))
+
+
+def test_tensors_on_the_host():
+    i32 = dict(dtype=torch.int32)
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+        atlas.shared(torch.ones(2, 8, 1, 64), torch.ones(4, 2, 16, 64), torch.ones(4, 2, 16, 64),
+                     torch.zeros((1, 1), **i32), torch.zeros(1, **i32), torch.zeros(2, **i32),
+                     torch.zeros((2, 1), **i32), torch.ones(2, **i32), 8, 2, 64, 16, 0.1)
+
+
+def apart(t):
+    """The same shape and values, not contiguous."""
+    return torch.stack([t, t], -1)[..., 0]
+
+
+NAMES = ["q", "k_pages", "v_pages", "prefix_table", "prefix_lens", "group_starts", "page_table", "seq_lens"]
+BAD = [(n, f) for n in NAMES for f in (apart, torch.Tensor.cpu, torch.Tensor.double, lambda t: t[:1])] + [
+    ("q", lambda t: t[:, :4].contiguous()), ("q", lambda t: t[0]), ("k_pages", lambda t: t[:, :1].contiguous()),
+    ("group_starts", lambda t: t[:-1]), ("prefix_table", lambda t: t[0]), ("page_table", lambda t: t[0])]
+
+
+@gpu
+@pytest.mark.parametrize("k", range(len(BAD)), ids=[f"{n}{i}" for i, (n, _) in enumerate(BAD)])
+def test_one_wrong_tensor(k):
+    x = Case("bf16", 8, 2, 64, 16, 2, [0, 2, 4], [100, 70], [50, 41, 60, 77], 8)
+    name, change = BAD[k]
+    at = NAMES.index(name)
+    out, lse = torch.zeros_like(x.args[0]), torch.zeros(x.q.shape[:3], device="cuda")
+    x.args[at] = change(x.args[at])
+    with pytest.raises(ValueError):
+        x(0.1, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and (lse == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("name,make", [
+    ("out", lambda: torch.zeros(4, 8, 1, 64, device="cuda", dtype=torch.bfloat16)),
+    ("out", lambda: torch.zeros(4, 8, 2, 64, dtype=torch.bfloat16)),
+    ("lse", lambda: torch.zeros(4, 8, 1, device="cuda")), ("lse", lambda: torch.zeros(4, 8, 2, device="cuda").double()),
+    ("status", lambda: torch.zeros(0, dtype=torch.int32, device="cuda")),
+    ("sinks", lambda: torch.zeros(2, device="cuda")), ("sinks", lambda: torch.zeros(8)),
+    ("workspace", lambda: torch.zeros(1 << 22, dtype=torch.uint8))])
+def test_one_wrong_option(name, make):
+    x = Case("bf16", 8, 2, 64, 16, 2, [0, 2, 4], [100, 70], [50, 41, 60, 77], 8)
+    with pytest.raises(ValueError):
+        x(0.1, **{name: make()})
+    with pytest.raises(atlas.AtlasError):
+        x(0.1, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
