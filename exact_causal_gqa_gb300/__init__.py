@@ -16,9 +16,12 @@ Functions (same names as the C entry points):
   kv_append(...)  new tokens' K/V into their pages    -> atlas_kv_append
   kv_append_rope(...)  the same, with rotary positions of several axes applied to the
                 new keys and the step's queries       -> atlas_kv_append_rope
+  kv_append_norm_rope(...)  that, after a norm of each head's queries and keys
+                                                      -> atlas_kv_append_norm_rope
   kv_weights(...)  attention weight each cached key received -> atlas_kv_weights
   kv_select(...)   the keys that stay under a budget  -> atlas_kv_select
   kv_compact(...)  pages with only those keys left    -> atlas_kv_compact
+  kv_resize(...)   page tables and slots from the sequences' lengths -> atlas_kv_resize
   workspace_size(kind, ...)                            -> atlas_attn_workspace_size
   run_host(kind, ...)  host tensors in, host tensor out (copies on the stream)
 """
@@ -35,15 +38,16 @@ import torch
 from . import _build
 
 __all__ = ["AtlasError", "decode", "suffix", "prefill", "cross", "shared", "kv_append",
-           "kv_append_rope", "kv_weights", "kv_select", "kv_compact", "workspace_size", "run_host",
-           "library_path", "DEV_BAD_PAGE", "DEV_BAD_SEQLEN", "DEV_TIMEOUT",
+           "kv_append_rope", "kv_append_norm_rope", "kv_weights", "kv_select", "kv_compact", "kv_resize",
+           "workspace_size", "run_host",
+           "library_path", "DEV_BAD_PAGE", "DEV_BAD_SEQLEN", "DEV_TIMEOUT", "DEV_NO_PAGES",
            "DEBUG_WITHHOLD_STAGE", "KIND_DECODE", "KIND_SUFFIX", "KIND_PREFILL",
            "KIND_CROSS", "rope_sections", "shared_workspace_size"]
 
 KIND_DECODE, KIND_SUFFIX, KIND_PREFILL, KIND_CROSS = 0, 1, 2, 3
 _KINDS = {"decode": KIND_DECODE, "suffix": KIND_SUFFIX, "prefill": KIND_PREFILL,
           "cross": KIND_CROSS}
-DEV_BAD_PAGE, DEV_BAD_SEQLEN, DEV_TIMEOUT = 1, 2, 4
+DEV_BAD_PAGE, DEV_BAD_SEQLEN, DEV_TIMEOUT, DEV_NO_PAGES = 1, 2, 4, 8
 DEBUG_WITHHOLD_STAGE = 1
 DEBUG_TC_DIRECT = 2
 _F32, _BF16 = 0, 1
@@ -125,6 +129,12 @@ class _Rope(ctypes.Structure):
                 ("status_word", ctypes.c_void_p), ("stream", ctypes.c_void_p)]
 
 
+class _Norm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("weight_dtype", ctypes.c_int), ("per_head", ctypes.c_int32),
+                ("weight_offset", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 class _Weights(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32), ("q_len", ctypes.c_int32),
@@ -151,6 +161,13 @@ class _Compact(ctypes.Structure):
                 ("kv_dtype", ctypes.c_int), ("new_page_table", ctypes.c_void_p),
                 ("new_max_pages", ctypes.c_int32), ("status_word", ctypes.c_void_p),
                 ("stream", ctypes.c_void_p)]
+
+
+class _Resize(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("n_new", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("status_word", ctypes.c_void_p), ("stream", ctypes.c_void_p)]
 
 
 _lib = None
@@ -192,6 +209,9 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.atlas_kv_append_rope.argtypes = [ctypes.c_void_p] * 7 + [ctypes.c_int32] * 3 + [
         ctypes.POINTER(_Rope)]
     lib.atlas_kv_append_rope.restype = ctypes.c_int
+    lib.atlas_kv_append_norm_rope.argtypes = [ctypes.c_void_p] * 7 + [ctypes.c_int32] * 3 + [
+        ctypes.POINTER(_Rope), ctypes.POINTER(_Norm)]
+    lib.atlas_kv_append_norm_rope.restype = ctypes.c_int
     lib.atlas_kv_weights.argtypes = [ctypes.c_void_p] * 5 + [ctypes.c_int32] * 4 + [
         ctypes.c_float, ctypes.POINTER(_Weights)]
     lib.atlas_kv_weights.restype = ctypes.c_int
@@ -204,6 +224,8 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.atlas_kv_compact.argtypes = [ctypes.c_void_p] * 5 + [ctypes.c_int32] * 3 + [
         ctypes.POINTER(_Compact)]
     lib.atlas_kv_compact.restype = ctypes.c_int
+    lib.atlas_kv_resize.argtypes = [ctypes.c_void_p] * 5 + [ctypes.c_int32, ctypes.POINTER(_Resize)]
+    lib.atlas_kv_resize.restype = ctypes.c_int
     lib.atlas_attn_status_string.argtypes = [ctypes.c_int]
     lib.atlas_attn_status_string.restype = ctypes.c_char_p
     lib.atlas_attn_split_tokens.argtypes = [ctypes.c_int] + [ctypes.c_int32] * 4 + [
@@ -625,6 +647,45 @@ def kv_append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, posi
     position (default theta ** (-2 p / rot_dim)); interleaved: pairs (2p, 2p + 1) rather
     than (p, p + rot_dim / 2).  Returns the rotated queries [B][Hq][n][D] (q_out, which
     may be q itself when q is contiguous); None without q."""
+    return _append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, positions, theta,
+                        inv_freq, rot_dim, pair_axis, interleaved, n_new, q_out, status, None)
+
+
+def kv_append_norm_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, positions, *,
+                        q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, theta=10000.0,
+                        inv_freq=None, rot_dim=None, pair_axis=None, interleaved=False, n_new=None,
+                        q_out=None, status=None):
+    """kv_append_rope with a root-mean-square norm of each head's queries and new keys before
+    the rotation, in the same pass (atlas_kv_append_norm_rope): each row is divided by
+    sqrt(mean of its squares + eps) and multiplied by its weights + weight_offset.  q_weight and
+    k_weight: [D], or [Hq][D] and [Hkv][D] for weights of each head (both alike), of the pools'
+    dtype or float32; None: ones."""
+    return _append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, positions, theta,
+                        inv_freq, rot_dim, pair_axis, interleaved, n_new, q_out, status,
+                        (q_weight, k_weight, eps, weight_offset))
+
+
+def _norm(device, dtype, q_weight, k_weight, eps, offset, Hq, Hkv, D):
+    """The atlas_qk_norm of checked weights."""
+    given = [w for w in (q_weight, k_weight) if w is not None]
+    N = _Norm(eps=eps, weight_offset=offset, weight_dtype=_DTYPES[torch.float32])
+    if given:
+        kind = given[0].dtype
+        if kind not in (dtype, torch.float32):
+            raise ValueError(f"q_weight and k_weight must be {dtype} or {torch.float32}")
+        _check(device, ("q_weight", q_weight, kind), ("k_weight", k_weight, kind))
+        per_head = given[0].dim() == 2
+        for name, w, heads in (("q_weight", q_weight, Hq), ("k_weight", k_weight, Hkv)):
+            if w is not None and w.shape != ((heads, D) if per_head else (D,)) and \
+                    not (heads is None and w.dim() == 1 + per_head and w.shape[-1] == D):
+                raise ValueError(f"{name} must be [head_dim], or [heads][head_dim] like the other")
+        N.weight_dtype, N.per_head = _DTYPES.get(kind, -1), int(per_head)
+        N.q_weight, N.k_weight = _ptr(q_weight), _ptr(k_weight)
+    return N
+
+
+def _append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, positions, theta, inv_freq,
+                 rot_dim, pair_axis, interleaved, n_new, q_out, status, norm):
     lib = load_library()
     shape, pool = k_new.shape, k_pages.shape
     if len(shape) != 4 or v_new.shape != shape or len(pool) != 4 or v_pages.shape != pool or \
@@ -679,11 +740,15 @@ def kv_append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, posi
         R.inv_freq = ctypes.addressof(freq)
     R.status_word = _ptr(status)
     R.stream = _stream(device)
-    with _on(device):
-        rc = lib.atlas_kv_append_rope(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(),
-                                      v_pages.data_ptr(), page_table.data_ptr(),
-                                      seq_lens.data_ptr(), _ptr(n_new), Hkv, D,
-                                      pool[2], ctypes.byref(R))
+    args = (k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+            page_table.data_ptr(), seq_lens.data_ptr(), _ptr(n_new), Hkv, D, pool[2], ctypes.byref(R))
+    if norm is None:
+        with _on(device):
+            rc = lib.atlas_kv_append_rope(*args)
+    else:
+        N = _norm(device, dtype, *norm, None if q is None else q.shape[1], Hkv, D)
+        with _on(device):
+            rc = lib.atlas_kv_append_norm_rope(*args, ctypes.byref(N))
     if rc != 0:
         raise AtlasError(rc, status_string(rc))
     return q_out
@@ -829,6 +894,46 @@ def kv_compact(k_pages, v_pages, page_table, kept, new_lens, *, new_page_table=N
                                   kept.data_ptr(), new_lens.data_ptr(), Hkv, D, P, ctypes.byref(C))
     if rc != 0:
         raise AtlasError(rc, status_string(rc))
+
+
+def kv_resize(page_table, n_pages, seq_lens, free_pages, free_state, page_tokens, *, n_new=None,
+              slots=None, max_new=None, status=None):
+    """Give every sequence the pages that seq_lens [B] needs (atlas_kv_resize): those it lacks
+    come from the ring free_pages [num_pages], free_state [2] = first entry and count, into
+    page_table [B][max_pages] behind its n_pages [B]; those it has too many of go back to the
+    ring.  All int32; page_table, n_pages, free_pages and free_state are updated in place.
+    slots (or max_new, for a new one): [B][max_new], written with the places page * page_tokens
+    + offset of each sequence's last n_new[b] tokens (None: max_new of them), then -1.  Returns
+    slots (None without)."""
+    lib = load_library()
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B][max_pages]")
+    B, width = page_table.shape
+    device, i32 = _cuda_device("page_table", page_table), torch.int32
+    if slots is None and max_new:
+        slots = torch.empty((B, max_new), dtype=i32, device=device)
+    if n_new is not None and slots is None:
+        raise ValueError("n_new needs slots or max_new")
+    _check(device, ("page_table", page_table, i32), ("n_pages", n_pages, i32),
+           ("seq_lens", seq_lens, i32), ("free_pages", free_pages, i32),
+           ("free_state", free_state, i32), ("n_new", n_new, i32), ("slots", slots, i32),
+           ("status", status, i32))
+    if n_pages.numel() != B or seq_lens.numel() != B or free_state.numel() != 2 or \
+            (n_new is not None and n_new.numel() != B) or (status is not None and status.numel() < 1) or \
+            (slots is not None and (slots.dim() != 2 or slots.shape[0] != B or
+                                    max_new not in (None, slots.shape[1]))):
+        raise ValueError("n_pages, seq_lens and n_new must be [B], free_state [2], slots "
+                         "[B][max_new], status one word")
+    Z = _Resize(batch=B, max_pages_per_seq=width, num_pages=free_pages.numel(),
+                max_new=0 if slots is None else slots.shape[1], n_new=_ptr(n_new),
+                slots=_ptr(slots), status_word=_ptr(status), stream=_stream(device))
+    with _on(device):
+        rc = lib.atlas_kv_resize(page_table.data_ptr(), n_pages.data_ptr(), seq_lens.data_ptr(),
+                                 free_pages.data_ptr(), free_state.data_ptr(), page_tokens,
+                                 ctypes.byref(Z))
+    if rc != 0:
+        raise AtlasError(rc, status_string(rc))
+    return slots
 
 
 class EventTimer:

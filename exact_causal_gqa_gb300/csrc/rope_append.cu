@@ -28,10 +28,18 @@
 // 149 us, a slot of one token for all heads per thread 197 us; 1, 4, 8, 16, 32 tokens
 // per CTA 139, 128, 133, 143, 169 us.  Few tokens (a decode step) leave too few CTAs: the
 // heads are then shared between CTAs (grid.y).
+//
+// With norms (atlas_kv_append_norm_rope) each row of q and k is first divided by its root
+// mean square and multiplied by its weights, in the same pass and without a rounding between:
+//   y_j = x_j (mean_i x_i^2 + eps)^(-1/2) (w_j + offset),
+// the sum of squares in fp32 over the row's slots, which sit in neighbouring lanes, by
+// log2(slots) exchanges.
 #include "internal.h"
 
 #include <cuda_bf16.h>
 #include <math.h>
+
+#include <type_traits>
 
 namespace atlas {
 namespace {
@@ -49,6 +57,9 @@ struct RopeParams {
     int32_t pairs;                // rotated pairs of a row; the D - 2 pairs others are copied
     int32_t interleaved;
     int32_t tokens_per_cta, heads_per_cta;
+    const void *q_weight, *k_weight;  // norms: [D] or [heads][D], or null (ones)
+    int32_t weight_step;              // elements from head to head: 0 or D
+    float weight_offset, eps;
     uint32_t *status;
     uint64_t turn[kMaxPairs];     // f_p / 2 pi mod 1, times 2^64
     uint8_t axis[kMaxPairs];
@@ -102,14 +113,51 @@ __device__ __forceinline__ void cos_sin_turns(uint64_t turn, float &c, float &s)
     s = (quarter & 2) ? -b : b;
 }
 
+// V weights from element e of head h's row on.
+template <typename W, int V>
+__device__ __forceinline__ void load_weights(const RopeParams &p, const void *weights, int h, int e,
+                                             float (&w)[V]) {
+    if (!weights) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[i] = 1.f;
+        return;
+    }
+    const W *at = static_cast<const W *>(weights) + h * p.weight_step + e;
+    constexpr int N = sizeof(W) * V > 16 ? 16 / sizeof(W) : V;  // at most 16 bytes a load
+#pragma unroll
+    for (int i = 0; i < V; i += N) {
+        const Vec<W, N> x = load_vec<W, N>(at + i);
+#pragma unroll
+        for (int k = 0; k < N; ++k) w[i + k] = widen(x.e[k]) + p.weight_offset;
+    }
+}
+
+// What a row is multiplied by to have a root mean square of one: `factor`, then a power of two,
+// `pre`.  sum(scale) is the sum of the squares of the row's elements times scale.  In fp32
+// that of large elements overflows, and that of small ones is lost where no eps covers it:
+// such rows are summed again times 2^-80 or 2^80.
+template <typename Sum>
+__device__ __forceinline__ void norm_factor(const RopeParams &p, Sum sum, float &pre, float &factor) {
+    const float s = sum(1.f), eps = p.eps;
+    const float per = 1.f / (float)p.D;
+    pre = 1.f;
+    if (!(s < 0x1p120f)) pre = 0x1p-80f;
+    else if (s < 0x1p-90f && eps < 0x1p-100f) pre = 0x1p80f;
+    // (2^-160 and 2^160 as two factors; eps times the former is nothing next to 2^120)
+    factor = rsqrtf(pre == 1.f ? s * per + eps : sum(pre) * per + eps * pre * pre);
+}
+
 // Element offsets of a token's rows of head 0; cache < 0: no slot (reported).
 struct TokenRows {
     int64_t q, k, v, q_out, cache;
     bool any;  // a real token
 };
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const __grid_constant__ RopeParams p) {
+// W: the norms' weights, or void for none.
+template <typename T, int V, typename W>
+__global__ void __launch_bounds__(kThreads, std::is_void<W>::value ? 8 : 5)
+    rope_append_kernel(const __grid_constant__ RopeParams p) {
+    constexpr bool kNorm = !std::is_void<W>::value;
     __shared__ __align__(16) float cs[kMaxTokens][2][kMaxPairs];  // cosines, sines
     __shared__ TokenRows rows[kMaxTokens];
     const int token0 = (int)blockIdx.x * p.tokens_per_cta;
@@ -182,7 +230,61 @@ __global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const __grid_c
         const int e0 = turned && !p.interleaved ? pair0 : 2 * pair0;
         const int e1 = turned && !p.interleaved ? pair0 + p.pairs : e0 + V;
         X x0 = load_vec<T, V>(src + e0), x1 = load_vec<T, V>(src + e1);
-        if (turned && h < p.Hq + p.Hkv) {
+        if constexpr (kNorm) {
+            if (h < p.Hq + p.Hkv) {
+                // (the lanes of one row: 32 at most, and all of them are here)
+                float w0[V], w1[V];
+                const bool is_q = h < p.Hq;
+                const void *weights = is_q ? p.q_weight : p.k_weight;
+                load_weights<W, V>(p, weights, is_q ? h : h - p.Hq, e0, w0);
+                load_weights<W, V>(p, weights, is_q ? h : h - p.Hq, e1, w1);
+                const int slots = 1 << lg_slots;
+                const unsigned mask = (slots == 32 ? ~0u : (1u << slots) - 1u)
+                                      << (threadIdx.x % 32 & ~(slots - 1));
+                float pre, factor;
+                norm_factor(p, [&](float scale) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float a = widen(x0.e[i]) * scale, b = widen(x1.e[i]) * scale;
+                        s = fmaf(a, a, fmaf(b, b, s));
+                    }
+                    for (int d = 1; d < slots; d *= 2) s += __shfl_xor_sync(mask, s, d);
+                    return s;
+                }, pre, factor);
+                float y0[V], y1[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    y0[i] = widen(x0.e[i]) * factor * pre * w0[i];
+                    y1[i] = widen(x1.e[i]) * factor * pre * w1[i];
+                }
+                if (turned) {
+                    const float *c = cs[k][0] + pair0, *s = cs[k][1] + pair0;
+                    if (!p.interleaved) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            const float x = y0[i], y = y1[i];
+                            y0[i] = x * c[i] - y * s[i];
+                            y1[i] = y * c[i] + x * s[i];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {  // pair i of 2 V consecutive elements
+                            float &a = 2 * i < V ? y0[2 * i % V] : y1[2 * i % V];
+                            float &b = 2 * i + 1 < V ? y0[(2 * i + 1) % V] : y1[(2 * i + 1) % V];
+                            const float x = a, y = b;
+                            a = x * c[i] - y * s[i];
+                            b = y * c[i] + x * s[i];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    x0.e[i] = narrow<T>(y0[i]);
+                    x1.e[i] = narrow<T>(y1[i]);
+                }
+            }
+        } else if (turned && h < p.Hq + p.Hkv) {
             const float *c = cs[k][0] + pair0, *s = cs[k][1] + pair0;
             X y0, y1;
             if (!p.interleaved) {
@@ -210,7 +312,84 @@ __global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const __grid_c
     }
 }
 
-template <typename T, int V>
+// Norms where the rotated part is an odd number of pairs: no vector of two divides its halves,
+// and single elements would spread a row of 128 over two warps.  Here a warp has a row, a lane
+// one or two of its units (a pair; past the rotated part two neighbouring elements), element by
+// element.  blockIdx.x: a token; a warp's heads follow one another by blockDim / 32.
+template <typename T, typename W>
+__global__ void __launch_bounds__(kThreads) norm_rope_rows_kernel(const __grid_constant__ RopeParams p) {
+    const int b = (int)blockIdx.x / p.n, j = (int)blockIdx.x % p.n;
+    const int lane = threadIdx.x % 32, units = p.D / 64;
+    const int count = p.n_new ? p.n_new[b] : p.n;
+    if (count < 0 || count > p.n) {
+        if (threadIdx.x == 0 && p.status) atomicOr(p.status, ATLAS_DEV_BAD_SEQLEN);
+        return;
+    }
+    if (j >= count) return;
+    const int64_t t = (int64_t)p.seq_lens[b] + j;
+    int64_t cache = -1;
+    uint32_t bad = 0;
+    if (t < 0 || t >= (int64_t)p.max_pages * p.P) {
+        bad = ATLAS_DEV_BAD_SEQLEN;
+    } else {
+        const int page = p.page_table[(int64_t)b * p.max_pages + t / p.P];
+        if (page < 0 || page >= p.num_pages) bad = ATLAS_DEV_BAD_PAGE;
+        else cache = ((int64_t)page * p.Hkv * p.P + t % p.P) * p.D;
+    }
+    if (bad && threadIdx.x == 0 && p.status) atomicOr(p.status, bad);
+    float c[2] = {1.f, 1.f}, s[2] = {0.f, 0.f};
+    int e0[2], e1[2];
+    for (int i = 0; i < units; ++i) {
+        const int u = lane + 32 * i;
+        const bool turned = u < p.pairs;
+        e0[i] = turned && !p.interleaved ? u : 2 * u;
+        e1[i] = turned && !p.interleaved ? u + p.pairs : 2 * u + 1;
+        if (!turned) continue;
+        const int32_t pos = p.positions[(int64_t)p.axis[u] * p.B * p.n + blockIdx.x];
+        cos_sin_turns((uint64_t)(int64_t)pos * p.turn[u], c[i], s[i]);
+    }
+    for (int h = threadIdx.x / 32; h < p.Hq + 2 * p.Hkv; h += blockDim.x / 32) {
+        const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
+        const int hh = is_q ? h : is_k ? h - p.Hq : h - p.Hq - p.Hkv;
+        if (!is_q && cache < 0) continue;
+        const int64_t *st = is_q ? p.qs : is_k ? p.ks : p.vs;
+        const T *src = static_cast<const T *>(is_q ? p.q : is_k ? p.k_new : p.v_new) + b * st[0] +
+                       hh * st[1] + j * st[2];
+        T *dst = is_q ? static_cast<T *>(p.q_out) + (((int64_t)b * p.Hq + hh) * p.n + j) * p.D
+                      : static_cast<T *>(is_k ? p.k_pages : p.v_pages) + cache + (int64_t)hh * p.P * p.D;
+        float x[2] = {0.f, 0.f}, y[2] = {0.f, 0.f};
+        for (int i = 0; i < units; ++i) {
+            x[i] = widen(src[e0[i]]);
+            y[i] = widen(src[e1[i]]);
+        }
+        if (is_q || is_k) {
+            float pre, factor;
+            norm_factor(p, [&](float scale) {
+                float sum = 0.f;
+                for (int i = 0; i < 2; ++i) {
+                    const float a = x[i] * scale, z = y[i] * scale;
+                    sum = fmaf(a, a, fmaf(z, z, sum));
+                }
+                for (int d = 1; d < 32; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                return sum;
+            }, pre, factor);
+            for (int i = 0; i < units; ++i) {
+                float w0[1], w1[1];
+                load_weights<W, 1>(p, is_q ? p.q_weight : p.k_weight, hh, e0[i], w0);
+                load_weights<W, 1>(p, is_q ? p.q_weight : p.k_weight, hh, e1[i], w1);
+                const float a = x[i] * factor * pre * w0[0], z = y[i] * factor * pre * w1[0];
+                x[i] = a * c[i] - z * s[i];
+                y[i] = z * c[i] + a * s[i];
+            }
+        }
+        for (int i = 0; i < units; ++i) {
+            dst[e0[i]] = narrow<T>(x[i]);
+            dst[e1[i]] = narrow<T>(y[i]);
+        }
+    }
+}
+
+template <typename T, int V, typename W = void>
 cudaError_t launch(RopeParams &p, cudaStream_t stream) {
     const int64_t tokens = (int64_t)p.B * p.n;
     const int heads = p.Hq + 2 * p.Hkv;
@@ -225,8 +404,20 @@ cudaError_t launch(RopeParams &p, cudaStream_t stream) {
     if (groups > most) groups = most;
     p.heads_per_cta = (int)((heads + groups - 1) / groups);
     const dim3 grid((unsigned)ctas, (unsigned)((heads + p.heads_per_cta - 1) / p.heads_per_cta));
-    rope_append_kernel<T, V><<<grid, kThreads, 0, stream>>>(p);
+    rope_append_kernel<T, V, W><<<grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
+}
+
+// With norms, weights of type W.
+template <typename T, typename W>
+cudaError_t launch_norm(RopeParams &p, cudaStream_t stream) {
+    if (p.pairs % 2) {
+        norm_rope_rows_kernel<T, W><<<(unsigned)(p.B * p.n), kThreads, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
+    if constexpr (sizeof(T) == 2)
+        if (p.pairs % 8 == 0) return launch<T, 8, W>(p, stream);
+    return p.pairs % 4 == 0 ? launch<T, 4, W>(p, stream) : launch<T, 2, W>(p, stream);
 }
 
 // A stride triple (batch, head, token) in elements; all zero means dense rows.
@@ -247,15 +438,11 @@ bool take_strides(const int64_t given[3], int64_t heads, int64_t n, int64_t D, i
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-}  // namespace
-}  // namespace atlas
-
-extern "C" atlas_status atlas_kv_append_rope(const void *k_new, const void *v_new, void *k_pages,
-                                             void *v_pages, const int32_t *page_table,
-                                             const int32_t *seq_lens, const int32_t *n_new,
-                                             int32_t n_kv_heads, int32_t head_dim,
-                                             int32_t page_tokens, const atlas_rope *R) {
-    using namespace atlas;
+// The call without norms (N null) and with them.
+atlas_status append_rope(const void *k_new, const void *v_new, void *k_pages, void *v_pages,
+                         const int32_t *page_table, const int32_t *seq_lens, const int32_t *n_new,
+                         int32_t n_kv_heads, int32_t head_dim, int32_t page_tokens,
+                         const atlas_rope *R, const atlas_qk_norm *N) {
     if (!R || !k_new || !v_new || !k_pages || !v_pages || !page_table || !seq_lens || !R->positions)
         return ATLAS_ERR_INVALID_ARG;
     if (R->batch < 1 || R->max_pages_per_seq < 1 || R->num_pages < 1 || R->max_new < 0 ||
@@ -299,6 +486,19 @@ extern "C" atlas_status atlas_kv_append_rope(const void *k_new, const void *v_ne
         !take_strides(R->k_strides, n_kv_heads, n, D, per16, p.ks) ||
         !take_strides(R->v_strides, n_kv_heads, n, D, per16, p.vs))
         return ATLAS_ERR_INVALID_ARG;
+    if (N) {
+        if (!(N->eps >= 0.f) || N->eps == INFINITY || !(fabsf(N->weight_offset) < INFINITY) ||
+            (N->per_head != 0 && N->per_head != 1) || !aligned16(N->q_weight) ||
+            !aligned16(N->k_weight))
+            return ATLAS_ERR_INVALID_ARG;
+        if (N->weight_dtype != R->kv_dtype && N->weight_dtype != ATLAS_F32)
+            return ATLAS_ERR_UNSUPPORTED;
+        p.q_weight = N->q_weight;
+        p.k_weight = N->k_weight;
+        p.weight_step = N->per_head ? head_dim : 0;
+        p.weight_offset = N->weight_offset;
+        p.eps = N->eps;
+    }
     if (R->max_new == 0) return ATLAS_OK;
     p.q = R->q;
     p.q_out = R->q_out;
@@ -325,7 +525,12 @@ extern "C" atlas_status atlas_kv_append_rope(const void *k_new, const void *v_ne
     const cudaStream_t stream = static_cast<cudaStream_t>(R->stream);
     (void)cudaGetLastError();
     cudaError_t err;
-    if (R->kv_dtype == ATLAS_BF16) {
+    if (N) {
+        using T = __nv_bfloat16;
+        err = R->kv_dtype == ATLAS_F32       ? launch_norm<float, float>(p, stream)
+              : N->weight_dtype == ATLAS_F32 ? launch_norm<T, float>(p, stream)
+                                             : launch_norm<T, T>(p, stream);
+    } else if (R->kv_dtype == ATLAS_BF16) {
         using T = __nv_bfloat16;
         err = pairs % 8 == 0   ? launch<T, 8>(p, stream)
               : pairs % 4 == 0 ? launch<T, 4>(p, stream)
@@ -337,4 +542,27 @@ extern "C" atlas_status atlas_kv_append_rope(const void *k_new, const void *v_ne
                                : launch<float, 1>(p, stream);
     }
     return err == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace atlas
+
+extern "C" atlas_status atlas_kv_append_rope(const void *k_new, const void *v_new, void *k_pages,
+                                             void *v_pages, const int32_t *page_table,
+                                             const int32_t *seq_lens, const int32_t *n_new,
+                                             int32_t n_kv_heads, int32_t head_dim,
+                                             int32_t page_tokens, const atlas_rope *R) {
+    return atlas::append_rope(k_new, v_new, k_pages, v_pages, page_table, seq_lens, n_new,
+                              n_kv_heads, head_dim, page_tokens, R, nullptr);
+}
+
+extern "C" atlas_status atlas_kv_append_norm_rope(const void *k_new, const void *v_new, void *k_pages,
+                                                  void *v_pages, const int32_t *page_table,
+                                                  const int32_t *seq_lens, const int32_t *n_new,
+                                                  int32_t n_kv_heads, int32_t head_dim,
+                                                  int32_t page_tokens, const atlas_rope *R,
+                                                  const atlas_qk_norm *N) {
+    if (!N) return ATLAS_ERR_INVALID_ARG;
+    return atlas::append_rope(k_new, v_new, k_pages, v_pages, page_table, seq_lens, n_new,
+                              n_kv_heads, head_dim, page_tokens, R, N);
 }

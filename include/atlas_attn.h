@@ -336,6 +336,32 @@ atlas_status atlas_kv_append_rope(const void *k_new, const void *v_new, void *k_
                                   int32_t n_kv_heads, int32_t head_dim, int32_t page_tokens,
                                   const atlas_rope *R);
 
+/* Norms of atlas_kv_append_norm_rope. */
+typedef struct {
+    const void *q_weight;      /* device, read, 16-byte aligned: [head_dim], or with per_head */
+    const void *k_weight;      /* [n_q_heads][head_dim] and [n_kv_heads][head_dim]; NULL: ones */
+    atlas_dtype weight_dtype;  /* of both: kv_dtype, or ATLAS_F32 */
+    int32_t per_head;          /* 0: one row of weights for all heads; 1: a row for each */
+    float weight_offset;       /* added to every weight that is given: 0, or 1 for weights stored
+                                  less one (finite) */
+    float eps;                 /* added to the mean of the squares; >= 0, finite */
+} atlas_qk_norm;
+
+/*
+ * atlas_kv_append_norm_rope: atlas_kv_append_rope with a norm of each head's queries and new
+ * keys before the rotation, in the same pass: each row x of q or k (all head_dim elements,
+ * rotated or not) becomes
+ *   y_j = x_j (mean_i x_i^2 + eps)^(-1/2) (w_j + weight_offset),
+ * computed in float32 and not rounded before its rotation; v is copied as it is.  Elements of
+ * any finite size are normed right (their squares need not fit float32); a row of zeros
+ * without eps is NaN, as the formula says.  Everything else as for atlas_kv_append_rope.
+ */
+atlas_status atlas_kv_append_norm_rope(const void *k_new, const void *v_new, void *k_pages,
+                                       void *v_pages, const int32_t *page_table,
+                                       const int32_t *seq_lens, const int32_t *n_new,
+                                       int32_t n_kv_heads, int32_t head_dim, int32_t page_tokens,
+                                       const atlas_rope *R, const atlas_qk_norm *N);
+
 /* Static, human-readable text for a status code. */
 const char *atlas_attn_status_string(atlas_status status);
 
