@@ -50,6 +50,7 @@ _KINDS = {"decode": KIND_DECODE, "suffix": KIND_SUFFIX, "prefill": KIND_PREFILL,
 DEV_BAD_PAGE, DEV_BAD_SEQLEN, DEV_TIMEOUT, DEV_NO_PAGES = 1, 2, 4, 8
 DEBUG_WITHHOLD_STAGE = 1
 DEBUG_TC_DIRECT = 2
+DEBUG_SHARED_SPLIT, DEBUG_SHARED_TC = 4, 8
 _F32, _BF16 = 0, 1
 _DTYPES = {torch.float32: _F32, torch.bfloat16: _BF16}
 STATUS_NAMES = {0: "ATLAS_OK", 1: "ATLAS_ERR_INVALID_ARG", 2: "ATLAS_ERR_UNSUPPORTED",
@@ -456,8 +457,8 @@ def cross(q, k_pages, v_pages, page_table, enc_lens, n_q_heads, n_kv_heads, head
 
 def shared(q, k_pages, v_pages, prefix_table, prefix_lens, group_starts, page_table, seq_lens,
            n_q_heads, n_kv_heads, head_dim, page_tokens, scale, *, out=None, out_dtype=None,
-           lse=None, workspace=None, status=None, split_tokens=0, events=None, softcap=0.0,
-           sinks=None, q_lens=None, sm_count=0):
+           lse=None, workspace=None, status=None, split_tokens=0, debug_flags=0, events=None,
+           softcap=0.0, sinks=None, q_lens=None, sm_count=0):
     """Attention of the last q_len positions of each sequence to its own cache (page_table
     [B][max_pages], seq_lens [B]: as for suffix) and to all of its group's prefix: sequences
     group_starts[n] <= b < group_starts[n + 1] share the prefix_lens[n] keys of prefix_table[n]
@@ -493,8 +494,8 @@ def shared(q, k_pages, v_pages, prefix_table, prefix_lens, group_starts, page_ta
                          "[B], out like q, lse [B][Hq][q_len], sinks [Hq], status one word")
     lib = load_library()
     L = _launch(q, k_pages, page_table, out_dtype, out, lse, None, status, _stream(device),
-                split_tokens, 0, None if events is None else ctypes.cast(events, ctypes.c_void_p).value,
-                0, softcap, sinks, q_lens, None, PHASE_ALL, sm_count)
+                split_tokens, debug_flags,
+                None if events is None else ctypes.cast(events, ctypes.c_void_p).value, 0, softcap, sinks, q_lens, None, PHASE_ALL, sm_count)
     S = _Shared(prefix_table.data_ptr(), prefix_lens.data_ptr(), group_starts.data_ptr(),
                 prefixes[0], prefixes[1])
     with _on(device):
@@ -516,14 +517,14 @@ def shared(q, k_pages, v_pages, prefix_table, prefix_lens, group_starts, page_ta
 
 def shared_workspace_size(q_shape, n_q_heads, n_kv_heads, head_dim, page_tokens, max_pages_per_seq,
                           n_groups, max_prefix_pages, num_pages, dtype=torch.bfloat16,
-                          out_dtype=None, split_tokens=0) -> int:
+                          out_dtype=None, split_tokens=0, debug_flags=0) -> int:
     """Workspace bytes a shared() call needs (from shapes and the split size only)."""
     L = _Launch()
     L.batch, L.q_len = q_shape[0], q_shape[2]
     L.max_pages_per_seq, L.num_pages = max_pages_per_seq, num_pages
     L.q_dtype = L.kv_dtype = _DTYPES.get(dtype, -1)
     L.out_dtype = _DTYPES.get(out_dtype or dtype, -1)
-    L.split_tokens = split_tokens
+    L.split_tokens, L.debug_flags = split_tokens, debug_flags
     S = _Shared(n_groups=n_groups, max_prefix_pages=max_prefix_pages)
     n = load_library().atlas_attn_shared_workspace_size(n_q_heads, n_kv_heads, head_dim, page_tokens,
                                                         ctypes.byref(S), ctypes.byref(L))

@@ -275,8 +275,6 @@ atlas_status encode_rows_map(CUtensorMap *map, const void *base, int64_t rows, i
     return r == CUDA_SUCCESS ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 
-namespace {
-
 // View of a page pool (rows = num_pages*Hkv*P, D bf16 per row, 128-byte swizzle)
 // for the split kernel.  Pages of fewer than 64 tokens: a 3-D view [D/64 slabs]
 // [rows][64 elements] whose box is one page's P rows x all slabs, so one TMA load
@@ -308,8 +306,6 @@ atlas_status encode_pool_map(CUtensorMap *map, const void *pool, int32_t num_pag
     }
     return r == CUDA_SUCCESS ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
-
-}  // namespace
 
 atlas_status run_attention(atlas_kind kind, const void *q, const void *k_pages, const void *v_pages,
                            const int32_t *page_table, const int32_t *seq_lens, int32_t Hq,

@@ -325,7 +325,10 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         if (SHARED && blockIdx.x == 0) wait_for_previous_grid();
     };
     if (SHARED) {
-        const SharedItem it = shared_item(p, blockIdx.x, NT, reinterpret_cast<int *>(smem + C::OFF_V));
+        const SharedGroups groups{p.group_starts, p.seq_lens, p.n_groups, p.B,   p.max_pages * p.P,
+                                  p.G * p.q_len,  NT * BM,    p.chunk,    p.Hkv, p.status};
+        const SharedItem it =
+            shared_item(groups, blockIdx.x, reinterpret_cast<int *>(smem + C::OFF_V));
         if (it.group < 0) {
             before_exit();
             return;
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         w0.b = it.group;
         w0.hkv = it.hkv;
         w0.c = it.split;
-        w0.t0 = it.tile;
+        w0.t0 = it.tile * NT;
         w0.tstep = NT - 1;
         w0.rows_unit = it.seqs * p.G * p.q_len;
         w0.kv_begin = it.split * p.chunk;

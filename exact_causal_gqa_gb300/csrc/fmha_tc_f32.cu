@@ -208,7 +208,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     };
     int split_keys = p.chunk;  // keys per split (split mode)
     if (SHARED) {
-        shared = shared_item(p, blockIdx.x, 1, reinterpret_cast<int *>(smem + C::OFF_V));
+        const SharedGroups groups{p.group_starts, p.seq_lens, p.n_groups, p.B,   p.max_pages * p.P,
+                                  p.G * p.q_len,  BM,         p.chunk,    p.Hkv, p.status};
+        shared = shared_item(groups, blockIdx.x, reinterpret_cast<int *>(smem + C::OFF_V));
         if (shared.group < 0) {
             before_exit();
             return;

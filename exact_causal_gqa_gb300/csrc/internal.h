@@ -94,6 +94,19 @@ struct SplitParams {
     const float *sinks;         // [Hq] natural-log logits or null (direct mode only)
 };
 
+// The split-KV kernels' call with shared prefixes in the same launch (shared_prefix.cu): CTAs
+// below own_items are the sequences' own splits, the others take the prefixes'.
+struct SharedSplitParams : SplitParams {
+    const int32_t *prefix_table;  // [n_groups][max_prefix_pages]
+    const int32_t *prefix_lens;   // [n_groups]
+    const int32_t *group_starts;  // [n_groups + 1]
+    int32_t n_groups, max_prefix_pages;
+    int32_t pre_chunk, n_pre;     // keys per split, splits of the longest prefix
+    int32_t own_items;            // n_chunks * Hkv * col_tiles * B
+    int32_t cols;                 // columns per CTA: bf16 8 or 16, fp32 4, 8 or 16
+    float *pre_acc, *pre_ml;      // as SharedMergeParams
+};
+
 // A call's kernels (atlas_attn.cu); the entry points are this and a kind.
 atlas_status run_attention(atlas_kind kind, const void *q, const void *k_pages, const void *v_pages,
                            const int32_t *page_table, const int32_t *seq_lens, int32_t Hq,
@@ -203,6 +216,13 @@ cudaError_t launch_split_bf16(const SplitParams &p, const CUtensorMap &tmK, cons
 // fp32 with few columns: 4, 8 or 16 columns per CTA by G x q_len.
 int split_f32_cols_per_cta(int G, int q_len);
 cudaError_t launch_split_f32(const SplitParams &p, cudaStream_t stream);
+// `ctas`: the own items and the most that the prefixes may be.
+cudaError_t launch_shared_split_bf16(const SharedSplitParams &p, int64_t ctas, const CUtensorMap &tmK,
+                                     const CUtensorMap &tmV, cudaStream_t stream);
+cudaError_t launch_shared_split_f32(const SharedSplitParams &p, int64_t ctas, cudaStream_t stream);
+// Tensor map of a page pool for the bf16 split kernel.
+atlas_status encode_pool_map(CUtensorMap *map, const void *pool, int32_t num_pages, int32_t Hkv,
+                             int32_t P, int32_t D);
 cudaError_t launch_merge(const MergeParams &p, cudaStream_t stream);
 cudaError_t launch_shared_merge(const SharedMergeParams &p, cudaStream_t stream);
 

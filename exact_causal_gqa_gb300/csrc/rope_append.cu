@@ -153,18 +153,49 @@ struct TokenRows {
     bool any;  // a real token
 };
 
-// W: the norms' weights, or void for none.
-template <typename T, int V, typename W>
-__global__ void __launch_bounds__(kThreads, std::is_void<W>::value ? 8 : 5)
+// The elements of unit u of a row: a pair of the rotated part, or two neighbours behind it.
+__device__ __forceinline__ void unit_elements(const RopeParams &p, int u, int &e0, int &e1) {
+    const bool halves = u < p.pairs && !p.interleaved;
+    e0 = halves ? u : 2 * u;
+    e1 = halves ? u + p.pairs : 2 * u + 1;
+}
+
+// W: the norms' weights, or void for none.  FOLD: one row of weights for all heads, folded into
+// the cosines and sines: a unit's (w0 cos, w1 sin, w1 cos, w0 sin) for q and for k.
+template <typename T, int V, typename W, bool FOLD = false>
+__global__ void __launch_bounds__(kThreads, std::is_void<W>::value ? 8 : FOLD ? 8 : 5)
     rope_append_kernel(const __grid_constant__ RopeParams p) {
     constexpr bool kNorm = !std::is_void<W>::value;
-    __shared__ __align__(16) float cs[kMaxTokens][2][kMaxPairs];  // cosines, sines
+    __shared__ __align__(16) float cs[FOLD ? 1 : kMaxTokens][2][kMaxPairs];  // cosines, sines
+    // unit u of a slot of V at [u % V][slot]: neighbouring lanes read neighbouring vectors
+    __shared__ float4 folded[FOLD ? kMaxTokens : 1][2][FOLD ? kMaxPairs : 1];
     __shared__ TokenRows rows[kMaxTokens];
     const int token0 = (int)blockIdx.x * p.tokens_per_cta;
     const int tokens = min(p.tokens_per_cta, p.B * p.n - token0);  // B * n < 2^31
     const int h0 = (int)blockIdx.y * p.heads_per_cta;
     const int h1 = min(p.Hq + 2 * p.Hkv, h0 + p.heads_per_cta);
 
+    if constexpr (FOLD) {
+        const int units = p.D / 2;
+        for (int i = threadIdx.x; i < tokens * units && h0 < p.Hq + p.Hkv; i += kThreads) {
+            const int k = i / units, u = i - k * units;
+            float c = 1.f, s = 0.f;
+            if (u < p.pairs) {
+                const int32_t pos = p.positions[(int64_t)p.axis[u] * p.B * p.n + token0 + k];
+                cos_sin_turns((uint64_t)(int64_t)pos * p.turn[u], c, s);
+            }
+            int e0, e1;
+            unit_elements(p, u, e0, e1);
+            const int at = u % V * (units / V) + u / V;
+            float w0[1], w1[1];
+            load_weights<W, 1>(p, p.q_weight, 0, e0, w0);
+            load_weights<W, 1>(p, p.q_weight, 0, e1, w1);
+            folded[k][0][at] = make_float4(w0[0] * c, w1[0] * s, w1[0] * c, w0[0] * s);
+            load_weights<W, 1>(p, p.k_weight, 0, e0, w0);
+            load_weights<W, 1>(p, p.k_weight, 0, e1, w1);
+            folded[k][1][at] = make_float4(w0[0] * c, w1[0] * s, w1[0] * c, w0[0] * s);
+        }
+    } else
     for (int i = threadIdx.x; i < tokens * p.pairs && h0 < p.Hq + p.Hkv; i += kThreads) {
         const int k = i / p.pairs, pair = i - k * p.pairs;
         const int32_t pos = p.positions[(int64_t)p.axis[pair] * p.B * p.n + token0 + k];
@@ -233,11 +264,7 @@ __global__ void __launch_bounds__(kThreads, std::is_void<W>::value ? 8 : 5)
         if constexpr (kNorm) {
             if (h < p.Hq + p.Hkv) {
                 // (the lanes of one row: 32 at most, and all of them are here)
-                float w0[V], w1[V];
                 const bool is_q = h < p.Hq;
-                const void *weights = is_q ? p.q_weight : p.k_weight;
-                load_weights<W, V>(p, weights, is_q ? h : h - p.Hq, e0, w0);
-                load_weights<W, V>(p, weights, is_q ? h : h - p.Hq, e1, w1);
                 const int slots = 1 << lg_slots;
                 const unsigned mask = (slots == 32 ? ~0u : (1u << slots) - 1u)
                                       << (threadIdx.x % 32 & ~(slots - 1));
@@ -252,6 +279,40 @@ __global__ void __launch_bounds__(kThreads, std::is_void<W>::value ? 8 : 5)
                     for (int d = 1; d < slots; d *= 2) s += __shfl_xor_sync(mask, s, d);
                     return s;
                 }, pre, factor);
+                if constexpr (FOLD) {
+                    const float4 *t = folded[k][is_q ? 0 : 1] + slot;
+                    auto emit = [&](auto halves, auto rotate) {
+                        X y0, y1;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            // the unit's elements: one of each vector, or two of one
+                            const int a = halves ? i : 2 * i % V, b = halves ? i : (2 * i + 1) % V;
+                            const X &from_a = halves || 2 * i < V ? x0 : x1;
+                            const X &from_b = halves || 2 * i >= V ? x1 : x0;
+                            X &to_a = halves || 2 * i < V ? y0 : y1;
+                            X &to_b = halves || 2 * i >= V ? y1 : y0;
+                            const float x = widen(from_a.e[a]) * factor, y = widen(from_b.e[b]) * factor;
+                            const float4 f = t[i << lg_slots];
+                            float u = x * f.x, v = y * f.z;
+                            if (rotate) {
+                                u -= y * f.y;
+                                v += x * f.w;
+                            }
+                            to_a.e[a] = narrow<T>(u * pre);
+                            to_b.e[b] = narrow<T>(v * pre);
+                        }
+                        store_vec<T, V>(dst + e0, y0);
+                        store_vec<T, V>(dst + e1, y1);
+                    };
+                    if (!turned) emit(std::false_type{}, std::false_type{});
+                    else if (p.interleaved) emit(std::false_type{}, std::true_type{});
+                    else emit(std::true_type{}, std::true_type{});
+                    continue;
+                }
+                float w0[V], w1[V];
+                const void *weights = is_q ? p.q_weight : p.k_weight;
+                load_weights<W, V>(p, weights, is_q ? h : h - p.Hq, e0, w0);
+                load_weights<W, V>(p, weights, is_q ? h : h - p.Hq, e1, w1);
                 float y0[V], y1[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
@@ -389,7 +450,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_rows_kernel(const __grid_c
     }
 }
 
-template <typename T, int V, typename W = void>
+template <typename T, int V, typename W = void, bool FOLD = false>
 cudaError_t launch(RopeParams &p, cudaStream_t stream) {
     const int64_t tokens = (int64_t)p.B * p.n;
     const int heads = p.Hq + 2 * p.Hkv;
@@ -404,7 +465,7 @@ cudaError_t launch(RopeParams &p, cudaStream_t stream) {
     if (groups > most) groups = most;
     p.heads_per_cta = (int)((heads + groups - 1) / groups);
     const dim3 grid((unsigned)ctas, (unsigned)((heads + p.heads_per_cta - 1) / p.heads_per_cta));
-    rope_append_kernel<T, V, W><<<grid, kThreads, 0, stream>>>(p);
+    rope_append_kernel<T, V, W, FOLD><<<grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -415,9 +476,14 @@ cudaError_t launch_norm(RopeParams &p, cudaStream_t stream) {
         norm_rope_rows_kernel<T, W><<<(unsigned)(p.B * p.n), kThreads, 0, stream>>>(p);
         return cudaGetLastError();
     }
+    if (p.weight_step) {
+        if constexpr (sizeof(T) == 2)
+            if (p.pairs % 8 == 0) return launch<T, 8, W>(p, stream);
+        return p.pairs % 4 == 0 ? launch<T, 4, W>(p, stream) : launch<T, 2, W>(p, stream);
+    }
     if constexpr (sizeof(T) == 2)
-        if (p.pairs % 8 == 0) return launch<T, 8, W>(p, stream);
-    return p.pairs % 4 == 0 ? launch<T, 4, W>(p, stream) : launch<T, 2, W>(p, stream);
+        if (p.pairs % 8 == 0) return launch<T, 8, W, true>(p, stream);
+    return p.pairs % 4 == 0 ? launch<T, 4, W, true>(p, stream) : launch<T, 2, W, true>(p, stream);
 }
 
 // A stride triple (batch, head, token) in elements; all zero means dense rows.

@@ -1,16 +1,16 @@
 // shared_prefix.cu -- attention of a batch whose sequences share prefixes
-// (include/atlas_shared.h): checks, the plan, and three launches.
+// (include/atlas_shared.h): checks, the plan, and the launches.
 //
-//   1. the sequences' own keys: the split kernels of the causal calls as they stand, partial
-//      states (m, l, acc) of each row and split to the workspace;
-//   2. the prefixes: the tensor-core kernels with the rows of all of a group's sequences
-//      gathered into tiles (shared_prefix.cuh), partial states likewise.  Launched as a
-//      dependent of 1, whose results it does not need: its CTAs take the SMs as those of 1
-//      leave them;
-//   3. the merge of a row's states of both kinds.
-//
-// Keys of a prefix are read once for each 128 or 256 rows of a kv head instead of once for
-// each sequence, from L2 for all tiles but the first.
+// A row's softmax runs over two sets of keys, its sequence's own and its group's prefix.  Each
+// set is cut into splits whose partial states (m, l, acc) go to the workspace, and one merge
+// joins a row's states of both kinds.  Two ways to the prefixes' states:
+//   split kernels: the own splits and those of the prefixes are CTAs of one launch of the
+//     decode kernels (split_kv.cu).  A CTA has up to 16 of a group's rows, so a prefix is read
+//     once for each 16 rows, from L2 for all but the first;
+//   tensor cores: after the own splits, on the split kernels or the tensor cores by the rows
+//     of one sequence, the tensor-core kernels take the prefixes with 128 or 256 of a group's
+//     rows to a CTA (shared_prefix.cuh).  They are launched as a dependent of the own splits,
+//     whose results they do not need: their CTAs take the SMs as those leave them.
 #include "internal.h"
 #include "atlas_shared.h"
 
@@ -26,12 +26,21 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 struct SharedPlan {
     Plan own;
-    int tiles;             // query tiles to a CTA
+    bool split;            // the split kernels, in one launch
+    int tiles;             // tensor cores: query tiles to a CTA; split kernels: columns
     int chunk, n_pre;      // keys per prefix split, splits of the longest prefix
-    int64_t ctas;          // most (group, kv head, split, tiles) items
+    int64_t ctas;          // most (group, kv head, split, rows of a CTA) items
     size_t acc_at, ml_at;  // the prefixes' states in the workspace
     size_t bytes;
 };
+
+// Whether the split kernels take less time: the prefix once for each CTA's rows, against a
+// second launch's start and the prefix once.
+bool split_pays(double prefix_bytes, int64_t tiles, double flops, bool f32) {
+    const double rate = 6.5e6, start = 9.0;  // bytes and floating point operations a microsecond
+    const double tc = start + std::max(prefix_bytes / rate, flops / (f32 ? 1.2e8 : 9e8));
+    return (double)tiles * prefix_bytes / rate <= tc;
+}
 
 atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const atlas_shared *S,
                          const atlas_launch *L, SharedPlan *plan) {
@@ -49,15 +58,27 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     if (max_prefix > INT32_MAX / 2) return ATLAS_ERR_INVALID_ARG;
 
     const int sms = L->sm_count > 0 ? L->sm_count : device_sm_count();
-    const int64_t rows = (int64_t)L->batch * (Hq / Hkv) * L->q_len;  // of one kv head, all groups
+    const int G = Hq / Hkv;
+    const int64_t rows = (int64_t)L->batch * G * L->q_len;  // of one kv head, all groups
+    const int64_t group_rows = (rows + S->n_groups - 1) / S->n_groups;
     const bool f32 = L->kv_dtype == ATLAS_F32;
-    plan->tiles = !f32 && rows > 128 * (int64_t)S->n_groups ? 2 : 1;
+    const bool few = plan->own.path == Path::SplitBF16 || plan->own.path == Path::SplitF32;
+    const int cols = f32 ? (group_rows <= 4 ? 4 : 8) : group_rows <= 8 ? 8 : 16;
+    const double bytes = 2.0 * S->n_groups * max_prefix * Hkv * D * (f32 ? 4 : 2);
+    plan->split = few && split_pays(bytes, (group_rows + cols - 1) / cols,
+                                    4.0 * D * rows * Hkv * max_prefix, f32);
+    if (few && (L->debug_flags & ATLAS_DEBUG_SHARED_SPLIT)) plan->split = true;
+    if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->split = false;
+    plan->tiles = plan->split ? cols : !f32 && group_rows > 128 ? 2 : 1;
     // CTAs of one split: a group's last may be partly filled
-    const int64_t cta_rows = 128 * plan->tiles;
+    const int64_t cta_rows = plan->split ? cols : 128 * plan->tiles;
     const int64_t units = (rows / cta_rows + S->n_groups) * Hkv;
     const int64_t likely = std::max<int64_t>((rows + cta_rows - 1) / cta_rows, S->n_groups) * Hkv;
     int64_t chunk = round_up(L->split_tokens, 128);
-    if (chunk == 0) {
+    if (chunk == 0 && plan->split) {
+        chunk = round_up((max_prefix * likely + sms * 4 - 1) / (sms * 4), 128);
+        chunk = std::min<int64_t>(std::max<int64_t>(chunk, 256), 2560);
+    } else if (chunk == 0) {
         const int64_t splits = std::max<int64_t>(1, sms * 3 / likely);
         chunk = std::max<int64_t>(512, round_up((max_prefix + splits - 1) / splits, 128));
     }
@@ -65,12 +86,124 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     plan->chunk = (int)chunk;
     plan->n_pre = (int)((max_prefix + chunk - 1) / chunk);
     plan->ctas = units * plan->n_pre;
+    if (plan->split) {
+        plan->own.col_tiles = (G * L->q_len + cols - 1) / cols;
+        plan->ctas += (int64_t)plan->own.n_chunks * Hkv * plan->own.col_tiles * L->batch;
+    }
     if (plan->ctas >= INT32_MAX) return ATLAS_ERR_UNSUPPORTED;
     const int64_t out_rows = (int64_t)L->batch * Hq * L->q_len;
     plan->acc_at = (size_t)round_up((int64_t)plan->own.ws_bytes, 256);
     plan->ml_at = plan->acc_at + (size_t)round_up(out_rows * plan->n_pre * D * 4, 256);
     plan->bytes = plan->ml_at + (size_t)out_rows * plan->n_pre * 8;
     return ATLAS_OK;
+}
+
+// The own splits and the prefixes' in one launch.
+cudaError_t launch_split(const SharedPlan &plan, const void *q, const void *k_pages,
+                         const void *v_pages, const int32_t *page_table, const int32_t *seq_lens,
+                         int32_t Hq, int32_t Hkv, int32_t D, int32_t P, float scale,
+                         const atlas_shared *S, const atlas_launch *L, float *pre_acc,
+                         float *pre_ml) {
+    SharedSplitParams p{};
+    p.q = q;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.page_table = page_table;
+    p.seq_lens = seq_lens;
+    p.B = L->batch;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.D = D;
+    p.P = P;
+    p.q_len = L->q_len;
+    p.max_pages = L->max_pages_per_seq;
+    p.num_pages = L->num_pages;
+    p.chunk = plan.own.chunk;
+    p.n_chunks = plan.own.n_chunks;
+    p.col_tiles = plan.own.col_tiles;
+    p.row_step = 1;
+    p.scale_log2 = scale * kLog2e;
+    p.softcap_log2 = L->softcap > 0.f ? L->softcap * kLog2e : 0.f;
+    p.softcap_inv = L->softcap > 0.f ? scale / L->softcap : 0.f;
+    p.q_lens = L->q_lens;
+    p.ws_acc = static_cast<float *>(L->workspace);
+    p.ws_ml = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.own.ml_offset);
+    p.status = L->status_word;
+    p.debug_flags = L->debug_flags;
+    p.prefix_table = S->prefix_table;
+    p.prefix_lens = S->prefix_lens;
+    p.group_starts = S->group_starts;
+    p.n_groups = S->n_groups;
+    p.max_prefix_pages = S->max_prefix_pages;
+    p.pre_chunk = plan.chunk;
+    p.n_pre = plan.n_pre;
+    p.own_items = plan.own.n_chunks * Hkv * plan.own.col_tiles * L->batch;
+    p.cols = plan.tiles;
+    p.pre_acc = pre_acc;
+    p.pre_ml = pre_ml;
+    cudaStream_t stream = static_cast<cudaStream_t>(L->stream);
+    if (L->kv_dtype == ATLAS_F32) return launch_shared_split_f32(p, plan.ctas, stream);
+    CUtensorMap tmK, tmV;
+    if (encode_pool_map(&tmK, k_pages, L->num_pages, Hkv, P, D) != ATLAS_OK ||
+        encode_pool_map(&tmV, v_pages, L->num_pages, Hkv, P, D) != ATLAS_OK)
+        return cudaErrorUnknown;
+    return launch_shared_split_bf16(p, plan.ctas, tmK, tmV, stream);
+}
+
+// The own splits, then the prefixes' on the tensor cores.
+atlas_status launch_tc(const SharedPlan &plan, const void *q, const void *k_pages,
+                       const void *v_pages, const int32_t *page_table, const int32_t *seq_lens,
+                       int32_t Hq, int32_t Hkv, int32_t D, int32_t P, float scale,
+                       const atlas_shared *S, const atlas_launch *L, float *pre_acc, float *pre_ml) {
+    const bool f32 = L->kv_dtype == ATLAS_F32;
+    const int bn = f32 ? 64 : 128;  // keys per block of the kernel
+    CUtensorMap tmK, tmV;
+    atlas_status st = encode_rows_map(&tmK, k_pages, (int64_t)L->num_pages * Hkv * P, D, std::min(P, bn), f32);
+    if (st == ATLAS_OK)
+        st = encode_rows_map(&tmV, v_pages, (int64_t)L->num_pages * Hkv * P, D, std::min(P, bn), f32);
+    if (st != ATLAS_OK) return st;
+
+    atlas_launch own = *L;
+    own.phase = ATLAS_PHASE_CHUNKS;
+    own.debug_flags &= ~ATLAS_DEBUG_TC_DIRECT;
+    own.events = nullptr;
+    own.workspace_bytes = plan.own.ws_bytes;
+    st = run_attention(ATLAS_KIND_SUFFIX, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P,
+                       scale, &own);
+    if (st != ATLAS_OK) return st;
+
+    TcParams tp{};
+    tp.page_table = S->prefix_table;
+    tp.seq_lens = S->prefix_lens;
+    tp.B = L->batch;
+    tp.Hq = Hq;
+    tp.Hkv = Hkv;
+    tp.G = Hq / Hkv;
+    tp.D = D;
+    tp.P = P;
+    tp.q_len = L->q_len;
+    tp.max_pages = S->max_prefix_pages;
+    tp.num_pages = L->num_pages;
+    tp.split = 1;
+    tp.chunk = plan.chunk;
+    tp.n_chunks = plan.n_pre;
+    tp.hilo_below = plan.tiles == 1 ? INT32_MAX : hilo_below(scale, D);
+    tp.negate_scores = scale < 0.f;
+    tp.scale_log2 = fabsf(scale) * kLog2e;
+    tp.softcap_log2 = L->softcap > 0.f ? L->softcap * kLog2e : 0.f;
+    tp.softcap_inv = L->softcap > 0.f ? fabsf(scale) / L->softcap : 0.f;
+    tp.q_lens = L->q_lens;
+    tp.ws_acc = pre_acc;
+    tp.ws_ml = pre_ml;
+    tp.status = L->status_word;
+    tp.group_starts = S->group_starts;
+    tp.n_groups = S->n_groups;
+    tp.q = q;
+    cudaStream_t stream = static_cast<cudaStream_t>(L->stream);
+    const cudaError_t err = f32 ? launch_shared_tc_f32(tp, plan.ctas, tmK, tmV, stream)
+                                : launch_shared_tc(tp, plan.tiles, plan.ctas, tmK, tmV, stream);
+    return err == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 
 }  // namespace
@@ -112,57 +245,19 @@ extern "C" atlas_status atlas_attn_shared(const void *q, const void *k_pages, co
     if (L->events)
         for (int i = 0; i < 3; ++i) ev[i] = static_cast<cudaEvent_t>(L->events[i]);
 
-    const bool f32 = L->kv_dtype == ATLAS_F32;
-    const int bn = f32 ? 64 : 128;  // keys per block of the kernel
-    CUtensorMap tmK, tmV;
-    st = encode_rows_map(&tmK, k_pages, (int64_t)L->num_pages * Hkv * P, D, std::min(P, bn), f32);
-    if (st == ATLAS_OK)
-        st = encode_rows_map(&tmV, v_pages, (int64_t)L->num_pages * Hkv * P, D, std::min(P, bn), f32);
-    if (st != ATLAS_OK) return st;
-
-    atlas_launch own = *L;
-    own.phase = ATLAS_PHASE_CHUNKS;
-    own.debug_flags &= ~ATLAS_DEBUG_TC_DIRECT;
-    own.events = nullptr;
-    own.workspace_bytes = plan.own.ws_bytes;
+    (void)cudaGetLastError();
     if (ev[0] && cudaEventRecord(ev[0], stream) != cudaSuccess) return ATLAS_ERR_CUDA;
-    st = run_attention(ATLAS_KIND_SUFFIX, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P,
-                       scale, &own);
-    if (st != ATLAS_OK) return st;
-
     float *pre_acc = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.acc_at);
     float *pre_ml = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.ml_at);
-    TcParams tp{};
-    tp.page_table = S->prefix_table;
-    tp.seq_lens = S->prefix_lens;
-    tp.B = L->batch;
-    tp.Hq = Hq;
-    tp.Hkv = Hkv;
-    tp.G = Hq / Hkv;
-    tp.D = D;
-    tp.P = P;
-    tp.q_len = L->q_len;
-    tp.max_pages = S->max_prefix_pages;
-    tp.num_pages = L->num_pages;
-    tp.split = 1;
-    tp.chunk = plan.chunk;
-    tp.n_chunks = plan.n_pre;
-    tp.hilo_below = plan.tiles == 1 ? INT32_MAX : hilo_below(scale, D);
-    tp.negate_scores = scale < 0.f;
-    tp.scale_log2 = fabsf(scale) * kLog2e;
-    tp.softcap_log2 = L->softcap > 0.f ? L->softcap * kLog2e : 0.f;
-    tp.softcap_inv = L->softcap > 0.f ? fabsf(scale) / L->softcap : 0.f;
-    tp.q_lens = L->q_lens;
-    tp.ws_acc = pre_acc;
-    tp.ws_ml = pre_ml;
-    tp.status = L->status_word;
-    tp.sms = L->sm_count > 0 ? L->sm_count : device_sm_count();
-    tp.group_starts = S->group_starts;
-    tp.n_groups = S->n_groups;
-    tp.q = q;
-    cudaError_t err = f32 ? launch_shared_tc_f32(tp, plan.ctas, tmK, tmV, stream)
-                          : launch_shared_tc(tp, plan.tiles, plan.ctas, tmK, tmV, stream);
-    if (err != cudaSuccess) return ATLAS_ERR_CUDA;
+    if (plan.split) {
+        if (launch_split(plan, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P, scale, S, L,
+                         pre_acc, pre_ml) != cudaSuccess)
+            return ATLAS_ERR_CUDA;
+    } else {
+        st = launch_tc(plan, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P, scale, S, L,
+                       pre_acc, pre_ml);
+        if (st != ATLAS_OK) return st;
+    }
     if (ev[1] && cudaEventRecord(ev[1], stream) != cudaSuccess) return ATLAS_ERR_CUDA;
 
     SharedMergeParams mp{};
@@ -183,7 +278,7 @@ extern "C" atlas_status atlas_attn_shared(const void *q, const void *k_pages, co
     mp.out = L->out;
     mp.out_bf16 = L->out_dtype == ATLAS_BF16;
     mp.lse = L->lse;
-    mp.sms = tp.sms;
+    mp.sms = L->sm_count > 0 ? L->sm_count : device_sm_count();
     mp.group_starts = S->group_starts;
     mp.prefix_lens = S->prefix_lens;
     mp.n_groups = S->n_groups;

@@ -18,32 +18,40 @@
 namespace atlas {
 
 struct SharedItem {
-    int group, hkv, split, tile;  // group < 0: no item for this CTA
+    int group, hkv, split, tile;  // group < 0: no item for this CTA; tile: the CTA's rows
     int seq0, seqs, len;          // the group's sequences and its prefix's keys
+};
+
+// What the items are counted from.
+struct SharedGroups {
+    const int32_t *starts, *lens;  // [n + 1], [n]
+    int n, B, max_len;
+    int rows, cta_rows;            // rows of a sequence (G * q_len), and of a CTA
+    int chunk, Hkv;
+    uint32_t *status;
 };
 
 // All threads of the CTA call this (it synchronises the CTA); `scratch`: 7 ints of shared
 // memory.  Item 0 reports groups that are out of range; they have no items.
-__device__ inline SharedItem shared_item(const TcParams &p, int item, int tiles_per_cta, int *scratch) {
+__device__ inline SharedItem shared_item(const SharedGroups &p, int item, int *scratch) {
     if (threadIdx.x < 32) {
         const int lane = (int)threadIdx.x;
         if (lane == 0) scratch[0] = -1;
         __syncwarp();
         int64_t base = 0;  // items of the groups before these (64 bits: starts out of order repeat)
         bool bad = false;
-        for (int n0 = 0; n0 < p.n_groups; n0 += 32) {
+        for (int n0 = 0; n0 < p.n; n0 += 32) {
             const int n = n0 + lane;
             int seq0 = 0, seqs = 0, len = 0, ctas = 0, items = 0;
-            if (n < p.n_groups) {
-                seq0 = p.group_starts[n];
-                const int end = p.group_starts[n + 1];
-                len = p.seq_lens[n];
-                if (seq0 < 0 || end < seq0 || end > p.B || len < 0 || len > p.max_pages * p.P) {
+            if (n < p.n) {
+                seq0 = p.starts[n];
+                const int end = p.starts[n + 1];
+                len = p.lens[n];
+                if (seq0 < 0 || end < seq0 || end > p.B || len < 0 || len > p.max_len) {
                     bad = true;
                 } else {
                     seqs = end - seq0;
-                    const int64_t rows = (int64_t)seqs * p.G * p.q_len;
-                    ctas = (int)((rows + 128 * tiles_per_cta - 1) / (128 * tiles_per_cta));
+                    ctas = (int)(((int64_t)seqs * p.rows + p.cta_rows - 1) / p.cta_rows);
                     items = ctas * (int)(((int64_t)len + p.chunk - 1) / p.chunk) * p.Hkv;
                 }
             }
@@ -61,7 +69,7 @@ __device__ inline SharedItem shared_item(const TcParams &p, int item, int tiles_
                 scratch[0] = n;
                 scratch[1] = rest / splits;
                 scratch[2] = rest % splits;
-                scratch[3] = at % ctas * tiles_per_cta;
+                scratch[3] = at % ctas;
                 scratch[4] = seq0;
                 scratch[5] = seqs;
                 scratch[6] = len;
@@ -76,13 +84,15 @@ __device__ inline SharedItem shared_item(const TcParams &p, int item, int tiles_
 }
 
 // Output row of tile row f of a group whose first sequence is seq0.
-__device__ __forceinline__ int64_t shared_row(const TcParams &p, int seq0, int hkv, int f) {
+template <typename Params>
+__device__ __forceinline__ int64_t shared_row(const Params &p, int seq0, int hkv, int f) {
     const int per = p.G * p.q_len, s = f / per;
     return ((int64_t)(seq0 + s) * p.Hq + (int64_t)hkv * p.G) * p.q_len + (f - s * per);
 }
 
 // Whether tile row f is a query: inside the group, and not padding of a ragged sequence.
-__device__ __forceinline__ bool shared_real(const TcParams &p, int seq0, int rows, int f) {
+template <typename Params>
+__device__ __forceinline__ bool shared_real(const Params &p, int seq0, int rows, int f) {
     if (f >= rows) return false;
     const int per = p.G * p.q_len, s = f / per;
     return !p.q_lens || (f - s * per) % p.q_len < p.q_lens[seq0 + s];

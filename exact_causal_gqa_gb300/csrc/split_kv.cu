@@ -20,8 +20,10 @@
 // Column max / sum reductions are quad shuffles.
 #include "internal.h"
 #include "ptx.cuh"
+#include "shared_prefix.cuh"
 
 #include <math.h>
+#include <type_traits>
 
 namespace atlas {
 namespace {
@@ -104,6 +106,84 @@ __device__ void direct_empty_rows(const SplitParams &p, int b, int hkv, int col0
     }
 }
 
+// Where a CTA works: a split of a sequence's own keys, or (prefix) one of the keys that a
+// group of sequences shares; there b is the group.
+struct SplitCta {
+    int chunk, hkv, ct, b;
+    bool prefix;
+    int seq0, rows, len;  // prefix: the group's first sequence, its rows, the prefix's keys
+};
+
+template <typename Params>
+constexpr bool kShared = std::is_same<Params, SharedSplitParams>::value;
+
+// All threads call this (with shared prefixes it synchronises the CTA).  chunk < 0: no work.
+template <int NCOLS, typename Params>
+__device__ SplitCta split_cta(const Params &p) {
+    if constexpr (kShared<Params>) {
+        __shared__ int scratch[7];
+        int i = (int)blockIdx.x;
+        if (i < p.own_items) {
+            const int chunk = i % p.n_chunks, y = i / p.n_chunks % (p.Hkv * p.col_tiles);
+            return {chunk, y / p.col_tiles, y % p.col_tiles, i / p.n_chunks / (p.Hkv * p.col_tiles),
+                    false, 0, 0, 0};
+        }
+        const SharedGroups groups{p.group_starts, p.prefix_lens, p.n_groups,  p.B,   p.max_prefix_pages * p.P,
+                                  p.G * p.q_len,  NCOLS,         p.pre_chunk, p.Hkv, p.status};
+        const SharedItem it = shared_item(groups, i - p.own_items, scratch);
+        if (it.group < 0) return {-1, 0, 0, 0, true, 0, 0, 0};
+        return {it.split, it.hkv, it.tile, it.group, true, it.seq0, it.seqs * p.G * p.q_len, it.len};
+    } else {
+        return {(int)blockIdx.x, (int)blockIdx.y / p.col_tiles, (int)blockIdx.y % p.col_tiles,
+                (int)blockIdx.z, false, 0, 0, 0};
+    }
+}
+
+// Output row of column n, and whether it is a query (not padding of a ragged batch).
+template <typename Params>
+__device__ __forceinline__ int64_t cta_row(const Params &p, const SplitCta &at, int n) {
+    if constexpr (kShared<Params>)
+        if (at.prefix) return shared_row(p, at.seq0, at.hkv, n);
+    return column_row(p, at.b, at.hkv, n);
+}
+template <typename Params>
+__device__ __forceinline__ bool cta_query(const Params &p, const SplitCta &at, int n, int qn) {
+    if constexpr (kShared<Params>)
+        if (at.prefix) return shared_real(p, at.seq0, at.rows, n);
+    return n % p.q_len < qn;
+}
+// Its visible keys: [cta_first, min(kv_end, cta_visible)).
+template <typename Params>
+__device__ __forceinline__ int cta_visible(const Params &p, const SplitCta &at, int L, int n) {
+    if constexpr (kShared<Params>)
+        if (at.prefix) return at.len;
+    return column_visible(p, L, n);
+}
+template <typename Params>
+__device__ __forceinline__ int cta_first(const Params &p, const SplitCta &at, int L, int n) {
+    if constexpr (kShared<Params>) return 0;  // (no window)
+    else return column_first(p, L, n);
+}
+template <typename Params>
+__device__ __forceinline__ const int32_t *cta_table(const Params &p, const SplitCta &at) {
+    if constexpr (kShared<Params>)
+        if (at.prefix) return p.prefix_table + (int64_t)at.b * p.max_prefix_pages;
+    return p.page_table + (int64_t)at.b * p.max_pages;
+}
+// The partial state of a row: (m, l) and acc.
+template <typename Params>
+__device__ __forceinline__ float *cta_ml(const Params &p, const SplitCta &at, int64_t row) {
+    if constexpr (kShared<Params>)
+        if (at.prefix) return p.pre_ml + (row * p.n_pre + at.chunk) * 2;
+    return p.ws_ml + (row * p.n_chunks + at.chunk) * 2;
+}
+template <int D, typename Params>
+__device__ __forceinline__ float *cta_acc(const Params &p, const SplitCta &at, int64_t row) {
+    if constexpr (kShared<Params>)
+        if (at.prefix) return p.pre_acc + (row * p.n_pre + at.chunk) * D;
+    return p.ws_acc + (row * p.n_chunks + at.chunk) * D;
+}
+
 // Shared prologue: decides whether this CTA has work.  Returns false when the
 // CTA must exit (nothing visible, or an error that has been recorded).
 // Returns L as shifted_len: with it, row i (< qn) of a ragged causal sequence
@@ -114,22 +194,69 @@ constexpr int kNoWork = 1;   // nothing of this split is visible to its columns
 constexpr int kBadPage = 2;  // a page id outside the pool (recorded)
 constexpr int kBadLen = 3;   // the sequence's seq_len / q_lens are invalid (recorded)
 
-template <int NCOLS>
-__device__ bool split_prologue(const SplitParams &p, int ct, int &L, int &kv_begin, int &kv_end,
-                               int &col0, int &ncols, int &qn, int &why) {
-    const int b = blockIdx.z;
-    const int hkv = blockIdx.y / p.col_tiles;
+// Keys of a split.
+template <typename Params>
+__device__ __forceinline__ int split_keys(const Params &p, const SplitCta &at) {
+    if constexpr (kShared<Params>)
+        if (at.prefix) return p.pre_chunk;
+    return p.chunk;
+}
+
+// Whether the split's pages are all in the pool; else its rows' states are NaN (why: kBadPage).
+template <int NCOLS, typename Params>
+__device__ bool split_pages_good(const Params &p, const SplitCta &at, int kv_begin, int kv_end,
+                                 int col0, int ncols, int qn, int &why) {
+    const int32_t *table = cta_table(p, at);
+    // Every page id this split will touch must be inside the pool.
+    const int pg0 = kv_begin / p.P, pg1 = (kv_end - 1) / p.P;
+    bool bad = false;
+    for (int pg = pg0 + (int)threadIdx.x; pg <= pg1; pg += blockDim.x) {
+        const int id = table[pg];
+        bad |= (id < 0 || id >= p.num_pages);
+    }
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) record(p.status, ATLAS_DEV_BAD_PAGE);
+        why = kBadPage;
+        if (p.direct) {
+            direct_nan_rows(p, at.b, at.hkv, col0, ncols, qn, false);
+            return false;
+        }
+        if (p.cluster) return false;  // a NaN state for this split, merged in the cluster
+        for (int c = threadIdx.x; c < ncols; c += blockDim.x) {
+            float *ml = cta_ml(p, at, cta_row(p, at, col0 + c));
+            ml[0] = __int_as_float(0x7fc00000);
+            ml[1] = __int_as_float(0x7fc00000);
+        }
+        return false;
+    }
+    return true;
+}
+
+template <int NCOLS, typename Params>
+__device__ bool split_prologue(const Params &p, const SplitCta &at, int &L, int &kv_begin,
+                               int &kv_end, int &col0, int &ncols, int &qn, int &why) {
+    const int b = at.b, hkv = at.hkv, ct = at.ct;
     // A pass of a call spread over several launches computes some splits only.
     if (p.chunk_range &&
-        ((int)blockIdx.x < p.chunk_range[2 * b] || (int)blockIdx.x >= p.chunk_range[2 * b + 1]))
+        (at.chunk < p.chunk_range[2 * b] || at.chunk >= p.chunk_range[2 * b + 1]))
         return false;
+    if (kShared<Params> && at.prefix) {
+        col0 = ct * NCOLS;
+        ncols = min(NCOLS, at.rows - col0);
+        kv_begin = at.chunk * split_keys(p, at);
+        kv_end = min(at.len, kv_begin + split_keys(p, at));
+        L = at.len;
+        qn = p.q_len;
+        why = kNoWork;
+        return split_pages_good<NCOLS>(p, at, kv_begin, kv_end, col0, ncols, qn, why);
+    }
     L = p.seq_lens[b];
     qn = p.q_lens ? p.q_lens[b] : p.q_len;
     col0 = ct * NCOLS;
     ncols = min(NCOLS, p.G * p.q_len - col0);
     why = kNoWork;
     if (seq_len_bad(p, L, qn)) {
-        if (threadIdx.x == 0 && blockIdx.x == 0) record(p.status, ATLAS_DEV_BAD_SEQLEN);
+        if (threadIdx.x == 0 && at.chunk == 0) record(p.status, ATLAS_DEV_BAD_SEQLEN);
         // split mode: the merge writes NaN rows for this sequence; cluster mode:
         // the cluster's rank 0 does
         if (p.direct) direct_nan_rows(p, b, hkv, col0, ncols, qn, true);
@@ -153,33 +280,10 @@ __device__ bool split_prologue(const SplitParams &p, int ct, int &L, int &kv_beg
     const int kv_hi = L - p.q_len + p.row_step * i_max + 1;
     // Keys below every column's window are skipped whole (64-key blocks).
     const int kv_lo = p.window > 0 ? max(0, L - p.q_len + i_min + 1 - p.window) : 0;
-    kv_begin = max((int)blockIdx.x * p.chunk, kv_lo / kSplitBlockTokens * kSplitBlockTokens);
-    kv_end = min(kv_hi, (int)blockIdx.x * p.chunk + p.chunk);
+    kv_begin = max(at.chunk * p.chunk, kv_lo / kSplitBlockTokens * kSplitBlockTokens);
+    kv_end = min(kv_hi, at.chunk * p.chunk + p.chunk);
     if (kv_begin >= kv_end) return false;
-
-    // Every page id this split will touch must be inside the pool.
-    const int pg0 = kv_begin / p.P, pg1 = (kv_end - 1) / p.P;
-    bool bad = false;
-    for (int pg = pg0 + (int)threadIdx.x; pg <= pg1; pg += blockDim.x) {
-        const int id = p.page_table[(int64_t)b * p.max_pages + pg];
-        bad |= (id < 0 || id >= p.num_pages);
-    }
-    if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) record(p.status, ATLAS_DEV_BAD_PAGE);
-        why = kBadPage;
-        if (p.direct) {
-            direct_nan_rows(p, b, hkv, col0, ncols, qn, false);
-            return false;
-        }
-        if (p.cluster) return false;  // a NaN state for this split, merged in the cluster
-        for (int c = threadIdx.x; c < ncols; c += blockDim.x) {
-            float *ml = p.ws_ml + (column_row(p, b, hkv, col0 + c) * p.n_chunks + blockIdx.x) * 2;
-            ml[0] = __int_as_float(0x7fc00000);
-            ml[1] = __int_as_float(0x7fc00000);
-        }
-        return false;
-    }
-    return true;
+    return split_pages_good<NCOLS>(p, at, kv_begin, kv_end, col0, ncols, qn, why);
 }
 
 // Combine the per-warp states held in shared memory and write this split's
@@ -190,31 +294,26 @@ __device__ bool split_prologue(const SplitParams &p, int ct, int &L, int &kv_beg
 // padding rows of a ragged batch are not written.
 // Cluster mode: the state (acc[D], m, l) of each column goes to `part` in this
 // CTA's shared memory ([NCOLS][D + 2]) for the cluster merge.
-template <int W, int NCOLS, int D>
-__device__ void write_partials(const SplitParams &p, const float *cm, const float *cl,
+template <int W, int NCOLS, int D, typename Params>
+__device__ void write_partials(const Params &p, const SplitCta &at, const float *cm, const float *cl,
                                const float *cacc, int col0, int ncols, int qn, bool failed,
                                float *part = nullptr) {
-    const int b = blockIdx.z;
-    const int hkv = blockIdx.y / p.col_tiles;
     if (p.direct && failed) {
-        direct_nan_rows(p, b, hkv, col0, ncols, qn, false);
+        direct_nan_rows(p, at.b, at.hkv, col0, ncols, qn, false);
         return;
     }
     for (int idx = threadIdx.x; idx < NCOLS * D; idx += blockDim.x) {
         const int c = idx / D, d = idx % D;
         if (c >= ncols) continue;
-        const int64_t row = column_row(p, b, hkv, col0 + c);
-        const int64_t slot = row * p.n_chunks + blockIdx.x;
+        const int64_t row = cta_row(p, at, col0 + c);
+        float *const ml = cta_ml(p, at, row);
         if (part && failed) {
             part[c * (D + 2) + d] = __int_as_float(0x7fc00000);
             if (d == 0) part[c * (D + 2) + D] = part[c * (D + 2) + D + 1] = __int_as_float(0x7fc00000);
             continue;
         }
         if (failed) {
-            if (d == 0) {
-                p.ws_ml[slot * 2] = __int_as_float(0x7fc00000);
-                p.ws_ml[slot * 2 + 1] = __int_as_float(0x7fc00000);
-            }
+            if (d == 0) ml[0] = ml[1] = __int_as_float(0x7fc00000);
             continue;
         }
         float M = -INFINITY;
@@ -258,10 +357,10 @@ __device__ void write_partials(const SplitParams &p, const float *cm, const floa
             if (d == 0 && p.lse) p.lse[row] = lse;
             continue;
         }
-        p.ws_acc[slot * D + d] = a;
+        cta_acc<D>(p, at, row)[d] = a;
         if (d == 0) {
-            p.ws_ml[slot * 2] = M;
-            p.ws_ml[slot * 2 + 1] = l;
+            ml[0] = M;
+            ml[1] = l;
         }
     }
 }
@@ -296,10 +395,10 @@ struct SplitLayout {
     static_assert(kCombine <= kBars, "combine scratch must fit in the ring");
 };
 
-template <int D, int NT, int STAGES>
+template <int D, int NT, int STAGES, typename Params = SplitParams>
 __global__ void __launch_bounds__(kSplitThreads, 2)
     split_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const SplitParams p) {
+                      const __grid_constant__ CUtensorMap tmV, const Params p) {
     allow_dependent_launch();  // the merge may start its CTAs (it waits for this grid)
     using Lay = SplitLayout<D, NT, STAGES>;
     constexpr int NCOLS = NT * 8;
@@ -315,13 +414,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::kFlags);
 
     int L, kv_begin, kv_end, col0, ncols, qn, why;
-    if (!split_prologue<NCOLS>(p, blockIdx.y % p.col_tiles, L, kv_begin, kv_end, col0, ncols,
-                               qn, why))
-        return;
+    const SplitCta at = split_cta<NCOLS>(p);
+    if (kShared<Params> && at.chunk < 0) return;
+    if (!split_prologue<NCOLS>(p, at, L, kv_begin, kv_end, col0, ncols, qn, why)) return;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int b = blockIdx.z;
-    const int hkv = blockIdx.y / p.col_tiles;
+    const int hkv = at.hkv;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full0 + 8 * s, 1);
@@ -351,7 +449,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         const int BR = p.P < BT ? p.P : BT;  // rows per box
         const int subs = BT / BR;           // boxes per block (<= 8)
         const int lp = 31 - __clz(p.P);     // log2(P)
-        PageIdCache pages{p.page_table + (int64_t)b * p.max_pages, (kv_end - 1) >> lp};
+        PageIdCache pages{cta_table(p, at), (kv_end - 1) >> lp};
         int issued = 0;
         for (int j = 0; j < nblocks; ++j) {
             const int s = j % STAGES;
@@ -415,7 +513,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             const int c = nt * 8 + lane / 4;
             const __nv_bfloat16 *qrow = nullptr;
             if (c < ncols) qrow = static_cast<const __nv_bfloat16 *>(p.q) +
-                                   column_row(p, b, hkv, col0 + c) * D;
+                                   cta_row(p, at, col0 + c) * D;
 #pragma unroll
             for (int kk = 0; kk < KSTEPS; ++kk) {
                 const int d0 = kk * 16 + 2 * (lane % 4);
@@ -431,9 +529,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int c = nt * 8 + 2 * (lane % 4) + e;
-                const bool real = c < ncols && (col0 + c) % p.q_len < qn;
-                lim[nt][e] = real ? min(kv_end, column_visible(p, L, col0 + c)) : 0;
-                lo[nt][e] = real ? column_first(p, L, col0 + c) : 0;
+                const bool real = c < ncols && cta_query(p, at, col0 + c, qn);
+                lim[nt][e] = real ? min(kv_end, cta_visible(p, at, L, col0 + c)) : 0;
+                lo[nt][e] = real ? cta_first(p, at, L, col0 + c) : 0;
                 m_run[nt][e] = -INFINITY;
                 l_run[nt][e] = 0.f;
             }
@@ -597,7 +695,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             }
     }
     __syncthreads();
-    write_partials<kConsumerWarps, NCOLS, D>(p, cm, cl, cacc, col0, ncols, qn, any_failed);
+    write_partials<kConsumerWarps, NCOLS, D>(p, at, cm, cl, cacc, col0, ncols, qn, any_failed);
 }
 
 // ---------------------------------------------------------------- cluster merge
@@ -753,9 +851,9 @@ struct F32Layout {
     static_assert(2 * W * NC + W * NC * D <= W * kWarp, "combine scratch fits the rings");
 };
 
-template <int D, int NC>
+template <int D, int NC, typename Params = SplitParams>
 __global__ void __launch_bounds__(F32Layout<D, NC>::W * 32, F32Layout<D, NC>::kMinCtas)
-    split_f32_kernel(const SplitParams p) {
+    split_f32_kernel(const Params p) {
     allow_dependent_launch();  // the merge may start its CTAs (it waits for this grid)
     using Lay = F32Layout<D, NC>;
     constexpr int W = Lay::W, BK = kF32Keys, DPL = D / 32, NQ = NC / 4, DV4 = D / 4;
@@ -766,33 +864,35 @@ __global__ void __launch_bounds__(F32Layout<D, NC>::W * 32, F32Layout<D, NC>::kM
     if (p.cluster) cluster_arrive_relaxed();  // first phase, waited on before any remote write
     float *part = p.cluster ? slots + cluster_ctarank() * (NC * (D + 2)) : nullptr;
 
-    const int b = blockIdx.z;
-    const int hkv = blockIdx.y / p.col_tiles;
+    const SplitCta at = split_cta<NC>(p);
+    if (kShared<Params> && at.chunk < 0) return;
+    const int b = at.b, hkv = at.hkv;
     // A short call is a chain of dependent memory round trips, so the reads that do
     // not depend on seq_len start now, before the prologue waits for it: the CTA's
     // query rows (cp.async; columns past the tile's end are zero-filled, padding rows
     // of a ragged batch load too and are masked with their keys) and, into L2, the
     // page-table entries of this split.
-    const int seq_len_b = p.seq_lens[b];
+    const int seq_len_b = kShared<Params> && at.prefix ? at.len : p.seq_lens[b];
     {
-        const int c0 = (int)(blockIdx.y % p.col_tiles) * NC;
-        const int nc = min(NC, p.G * p.q_len - c0);
+        const int c0 = at.ct * NC;
+        const int nc = min(NC, (kShared<Params> && at.prefix ? at.rows : p.G * p.q_len) - c0);
         for (int idx = threadIdx.x; idx < NC * DV4; idx += W * 32) {
             const int c = idx / DV4, d4 = idx % DV4;
             const bool in = c < nc;
             const float *src = static_cast<const float *>(p.q) +
-                               column_row(p, b, hkv, c0 + (in ? c : 0)) * D + 4 * d4;
+                               cta_row(p, at, c0 + (in ? c : 0)) * D + 4 * d4;
             cp_async16(smem_u32(sQ + c * Lay::KS + 4 * d4), src, in ? 16u : 0u);
         }
         cp_async_commit();
-        const int pg0 = (int)blockIdx.x * p.chunk / p.P;
-        const int npg = min(p.chunk / p.P, p.max_pages - pg0);
-        if ((int)threadIdx.x * 32 < npg)
-            prefetch_l2(p.page_table + (int64_t)b * p.max_pages + pg0 + threadIdx.x * 32);
+        const int pg0 = at.chunk * split_keys(p, at) / p.P;
+        int max_pages = p.max_pages;
+        if constexpr (kShared<Params>)
+            if (at.prefix) max_pages = p.max_prefix_pages;
+        const int npg = min(split_keys(p, at) / p.P, max_pages - pg0);
+        if ((int)threadIdx.x * 32 < npg) prefetch_l2(cta_table(p, at) + pg0 + threadIdx.x * 32);
     }
     int L = 0, kv_begin = 0, kv_end = 0, col0 = 0, ncols = 0, qn = 0, why = 0;
-    const bool work = split_prologue<NC>(p, blockIdx.y % p.col_tiles, L, kv_begin, kv_end, col0,
-                                         ncols, qn, why);
+    const bool work = split_prologue<NC>(p, at, L, kv_begin, kv_end, col0, ncols, qn, why);
     if (!work) cp_async_wait<0>();  // no copy in flight when the CTA leaves
     if (!work && !p.cluster) return;
     if (!work) {
@@ -806,14 +906,14 @@ __global__ void __launch_bounds__(F32Layout<D, NC>::W * 32, F32Layout<D, NC>::kM
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const float *kp = static_cast<const float *>(p.k_pages);
     const float *vp = static_cast<const float *>(p.v_pages);
-    const int32_t *ptab = p.page_table + (int64_t)b * p.max_pages;
+    const int32_t *ptab = cta_table(p, at);
 
     int lim[NC], lo[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const bool ok = c < ncols && (col0 + c) % p.q_len < qn;
-        lim[c] = ok ? min(kv_end, column_visible(p, L, col0 + c)) : kv_begin;
-        lo[c] = ok ? column_first(p, L, col0 + c) : 0;
+        const bool ok = c < ncols && cta_query(p, at, col0 + c, qn);
+        lim[c] = ok ? min(kv_end, cta_visible(p, at, L, col0 + c)) : kv_begin;
+        lo[c] = ok ? cta_first(p, at, L, col0 + c) : 0;
     }
 
     float *wK = sW + warp * Lay::kWarp;
@@ -982,18 +1082,18 @@ __global__ void __launch_bounds__(F32Layout<D, NC>::W * 32, F32Layout<D, NC>::kM
         for (int e = 0; e < DPL; ++e) cacc[(warp * NC + c) * D + lane * DPL + e] = acc[c][e];
     __syncthreads();
     if (p.cluster) {
-        write_partials<W, NC, D>(p, cm, cl, cacc, col0, ncols, qn, false, part);
+        write_partials<W, NC, D>(p, at, cm, cl, cacc, col0, ncols, qn, false, part);
         cluster_merge<NC, D>(p, slots, col0, ncols, qn, false, seq_len_b);
         return;
     }
-    write_partials<W, NC, D>(p, cm, cl, cacc, col0, ncols, qn, false);
+    write_partials<W, NC, D>(p, at, cm, cl, cacc, col0, ncols, qn, false);
 }
 
-template <int D, int NT, int STAGES>
-cudaError_t launch_bf16_instance(const SplitParams &p, const CUtensorMap &tmK,
+template <int D, int NT, int STAGES, typename Params>
+cudaError_t launch_bf16_instance(const Params &p, dim3 grid, const CUtensorMap &tmK,
                                  const CUtensorMap &tmV, cudaStream_t stream) {
     using Lay = SplitLayout<D, NT, STAGES>;
-    auto kern = split_bf16_kernel<D, NT, STAGES>;
+    auto kern = split_bf16_kernel<D, NT, STAGES, Params>;
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -1003,9 +1103,19 @@ cudaError_t launch_bf16_instance(const SplitParams &p, const CUtensorMap &tmK,
         if (err != cudaSuccess) return err;
         configured[dev] = 1;
     }
-    dim3 grid(p.n_chunks, p.Hkv * p.col_tiles, p.B);
     kern<<<grid, kSplitThreads, Lay::kBytes, stream>>>(tmK, tmV, p);
     return cudaGetLastError();
+}
+
+template <typename Params>
+cudaError_t launch_bf16(const Params &p, bool wide, dim3 grid, const CUtensorMap &tmK,
+                        const CUtensorMap &tmV, cudaStream_t stream) {
+    if (p.D == 128) {
+        return wide ? launch_bf16_instance<128, 2, 3>(p, grid, tmK, tmV, stream)
+                    : launch_bf16_instance<128, 1, 3>(p, grid, tmK, tmV, stream);
+    }
+    return wide ? launch_bf16_instance<64, 2, 4>(p, grid, tmK, tmV, stream)
+                : launch_bf16_instance<64, 1, 4>(p, grid, tmK, tmV, stream);
 }
 
 }  // namespace
@@ -1014,19 +1124,19 @@ int split_bf16_cols_per_cta(int G, int q_len) { return G * q_len <= 8 ? 8 : 16; 
 
 cudaError_t launch_split_bf16(const SplitParams &p, const CUtensorMap &tmK, const CUtensorMap &tmV,
                               cudaStream_t stream) {
-    const bool wide = split_bf16_cols_per_cta(p.G, p.q_len) == 16;
-    if (p.D == 128) {
-        return wide ? launch_bf16_instance<128, 2, 3>(p, tmK, tmV, stream)
-                    : launch_bf16_instance<128, 1, 3>(p, tmK, tmV, stream);
-    }
-    return wide ? launch_bf16_instance<64, 2, 4>(p, tmK, tmV, stream)
-                : launch_bf16_instance<64, 1, 4>(p, tmK, tmV, stream);
+    return launch_bf16(p, split_bf16_cols_per_cta(p.G, p.q_len) == 16,
+                       dim3(p.n_chunks, p.Hkv * p.col_tiles, p.B), tmK, tmV, stream);
 }
 
-template <int D, int NC>
-cudaError_t launch_f32_instance(const SplitParams &p, cudaStream_t stream) {
+cudaError_t launch_shared_split_bf16(const SharedSplitParams &p, int64_t ctas, const CUtensorMap &tmK,
+                                     const CUtensorMap &tmV, cudaStream_t stream) {
+    return launch_bf16(p, p.cols == 16, dim3((unsigned)ctas), tmK, tmV, stream);
+}
+
+template <int D, int NC, typename Params>
+cudaError_t launch_f32_instance(const Params &p, dim3 grid, cudaStream_t stream) {
     using Lay = F32Layout<D, NC>;
-    auto kern = split_f32_kernel<D, NC>;
+    auto kern = split_f32_kernel<D, NC, Params>;
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -1037,7 +1147,6 @@ cudaError_t launch_f32_instance(const SplitParams &p, cudaStream_t stream) {
         if (err != cudaSuccess) return err;
         configured[dev] = 1;
     }
-    dim3 grid(p.n_chunks, p.Hkv * p.col_tiles, p.B);
     if (!p.cluster) {
         kern<<<grid, Lay::W * 32, Lay::kBytes, stream>>>(p);
         return cudaGetLastError();
@@ -1063,16 +1172,25 @@ int split_f32_cols_per_cta(int G, int q_len) {
     return n <= 4 ? 4 : n <= 8 ? 8 : 16;
 }
 
-cudaError_t launch_split_f32(const SplitParams &p, cudaStream_t stream) {
-    const int nc = split_f32_cols_per_cta(p.G, p.q_len);
+template <typename Params>
+static cudaError_t launch_f32(const Params &p, int nc, dim3 grid, cudaStream_t stream) {
     if (p.D == 128) {
-        return nc == 4   ? launch_f32_instance<128, 4>(p, stream)
-               : nc == 8 ? launch_f32_instance<128, 8>(p, stream)
-                         : launch_f32_instance<128, 16>(p, stream);
+        return nc == 4   ? launch_f32_instance<128, 4>(p, grid, stream)
+               : nc == 8 ? launch_f32_instance<128, 8>(p, grid, stream)
+                         : launch_f32_instance<128, 16>(p, grid, stream);
     }
-    return nc == 4   ? launch_f32_instance<64, 4>(p, stream)
-           : nc == 8 ? launch_f32_instance<64, 8>(p, stream)
-                     : launch_f32_instance<64, 16>(p, stream);
+    return nc == 4   ? launch_f32_instance<64, 4>(p, grid, stream)
+           : nc == 8 ? launch_f32_instance<64, 8>(p, grid, stream)
+                     : launch_f32_instance<64, 16>(p, grid, stream);
+}
+
+cudaError_t launch_split_f32(const SplitParams &p, cudaStream_t stream) {
+    return launch_f32(p, split_f32_cols_per_cta(p.G, p.q_len),
+                      dim3(p.n_chunks, p.Hkv * p.col_tiles, p.B), stream);
+}
+
+cudaError_t launch_shared_split_f32(const SharedSplitParams &p, int64_t ctas, cudaStream_t stream) {
+    return launch_f32(p, p.cols, dim3((unsigned)ctas), stream);
 }
 
 }  // namespace atlas

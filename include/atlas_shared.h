@@ -25,6 +25,11 @@
 extern "C" {
 #endif
 
+/* Test-only bits of atlas_launch.debug_flags: prefixes on the split kernel, in one launch with the
+ * sequences' own keys (at most 16 rows to a sequence and kv head), or on the tensor-core one. */
+#define ATLAS_DEBUG_SHARED_SPLIT 4u
+#define ATLAS_DEBUG_SHARED_TC 8u
+
 /* The shared prefixes of a call: group n is the neighbouring sequences group_starts[n] <= b <
  * group_starts[n + 1], and their prefix the first prefix_lens[n] keys of prefix_table[n]. */
 typedef struct {

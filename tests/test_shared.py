@@ -181,7 +181,7 @@ def check(x, dtype, scale, **opt):
     sinks = torch.linspace(-1, 3, x.sizes[0]) if opt.get("sinks") else None
     ref, ref_lse = x.expected(scale, None if sinks is None else widen(sinks), opt.get("softcap", 0.0))
     kw = dict(split_tokens=opt.get("split_tokens", 0), softcap=opt.get("softcap", 0.0),
-              sinks=None if sinks is None else sinks.cuda())
+              debug_flags=opt.get("path", 0), sinks=None if sinks is None else sinks.cuda())
     out = torch.full(x.q.shape, 99.0, dtype=torch.float32, device="cuda")
     lse = torch.full(x.q.shape[:3], 99.0, device="cuda")
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -201,10 +201,11 @@ def check(x, dtype, scale, **opt):
 
 
 @gpu
+@pytest.mark.parametrize("path", [0, atlas.DEBUG_SHARED_SPLIT, atlas.DEBUG_SHARED_TC])
 @pytest.mark.parametrize("dtype,Hq,Hkv,D,P,q_len,starts,pre,lens,opt", CASES)
-def test_matches_the_plain_form(dtype, Hq, Hkv, D, P, q_len, starts, pre, lens, opt):
+def test_matches_the_plain_form(dtype, Hq, Hkv, D, P, q_len, starts, pre, lens, opt, path):
     x = Case(dtype, Hq, Hkv, D, P, q_len, starts, pre, lens, 200 + q_len, opt.get("ragged"))
-    check(x, dtype, **{"scale": D ** -0.5, **opt})
+    check(x, dtype, **{"scale": D ** -0.5, **opt}, path=path)
 
 
 @gpu
@@ -234,16 +235,17 @@ def test_the_order_of_the_groups_changes_no_bits():
 
 
 @gpu
-@pytest.mark.parametrize("dtype,q_len", [("bf16", 1), ("bf16", 40), ("f32", 1), ("f32", 40)])
-def test_bad_lengths_groups_and_pages_are_reported(dtype, q_len):
+@pytest.mark.parametrize("dtype,q_len,path", [("bf16", 1, 4), ("bf16", 1, 8), ("bf16", 40, 0), ("f32", 1, 4),
+                                              ("f32", 1, 8), ("f32", 40, 0)])
+def test_bad_lengths_groups_and_pages_are_reported(dtype, q_len, path):
     x = Case(dtype, 8, 2, 64, 16, q_len, [0, 2, 4], [100, 70], [50, 41, 60, 77], 8)
-    good = x(0.1)
+    good = x(0.1, debug_flags=path)
 
     def again(k, value, bit, nan):
         args = list(x.args)
         args[k] = torch.tensor(value, dtype=torch.int32, device="cuda") if isinstance(value, list) else value
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
-        out = atlas.shared(*args, *x.sizes, 0.1, status=status)
+        out = atlas.shared(*args, *x.sizes, 0.1, status=status, debug_flags=path)
         assert int(status.item()) == bit
         for b in range(4):
             if b in nan:
