@@ -31,6 +31,7 @@ import contextlib
 import ctypes
 import functools
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -171,7 +172,30 @@ class _Resize(ctypes.Structure):
                 ("status_word", ctypes.c_void_p), ("stream", ctypes.c_void_p)]
 
 
-_lib = None
+# The structures of calls whose time on the host counts, packed in one step (ctypes sets field by
+# field); native alignment lays them out as the declarations above.
+_pack_launch = struct.Struct("iiiiiiiPPPQPPiIPifPPPii").pack
+_pack_shared = struct.Struct("PPPii").pack
+_pack_rope = struct.Struct("iiiiiiPPqqqqqqqqqPiiiPPdPP").pack
+_pack_norm = struct.Struct("PPiiff").pack
+_lib = _fast = None
+
+
+class _Fast:
+    """Entry points that take packed structures."""
+
+    def __init__(self, lib):
+        pointers, ints = [ctypes.c_void_p] * 7, [ctypes.c_int32] * 3
+        for name, args, result in (
+                ("atlas_attn_shared", pointers[:5] + [ctypes.c_int32] * 4 + [ctypes.c_float] + pointers[:2],
+                 ctypes.c_int),
+                ("atlas_attn_shared_workspace_size", [ctypes.c_int32] * 4 + pointers[:2], ctypes.c_size_t),
+                ("atlas_kv_append_rope", pointers + ints + pointers[:1], ctypes.c_int),
+                ("atlas_kv_append_norm_rope", pointers + ints + pointers[:2], ctypes.c_int)):
+            fn = lib[name]  # (a function object of its own)
+            fn.argtypes, fn.restype = args, result
+            setattr(self, name[6:], fn)
+
 
 
 def library_path() -> str:
@@ -180,7 +204,7 @@ def library_path() -> str:
 
 def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
     """Load libatlas_attn.so; raises if it has not been built (no fallback)."""
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     if not os.path.exists(_build.LIB):
@@ -250,12 +274,16 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
                                                             ctypes.c_int32, ctypes.c_int32,
                                                             ctypes.c_void_p, ctypes.c_void_p]
     lib.atlas_pool_fill.restype = ctypes.c_int
-    _lib = lib
+    _lib, _fast = lib, _Fast(lib)
     return lib
 
 
 def status_string(status: int) -> str:
     return load_library().atlas_attn_status_string(status).decode()
+
+
+def _address(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -475,13 +503,17 @@ def shared(q, k_pages, v_pages, prefix_table, prefix_lens, group_starts, page_ta
         out = torch.empty(shape, dtype=out_dtype, device=device)
     else:
         out_dtype = out_dtype or out.dtype
-    i32 = torch.int32
-    _check(device, ("q", q, dtype), ("k_pages", k_pages, dtype), ("v_pages", v_pages, dtype),
-           ("prefix_table", prefix_table, i32), ("prefix_lens", prefix_lens, i32),
-           ("group_starts", group_starts, i32), ("page_table", page_table, i32),
-           ("seq_lens", seq_lens, i32), ("out", out, out_dtype), ("lse", lse, torch.float32),
-           ("status", status, i32), ("sinks", sinks, torch.float32), ("q_lens", q_lens, i32),
-           ("workspace", workspace, None if workspace is None else workspace.dtype))
+    i32, f32, index = torch.int32, torch.float32, device.index
+    if not _fits(index, (q, dtype), (k_pages, dtype), (v_pages, dtype), (prefix_table, i32),
+                 (prefix_lens, i32), (group_starts, i32), (page_table, i32), (seq_lens, i32),
+                 (out, out_dtype), (lse, f32), (status, i32), (sinks, f32), (q_lens, i32),
+                 (workspace, None if workspace is None else workspace.dtype)):
+        _check(device, ("q", q, dtype), ("k_pages", k_pages, dtype), ("v_pages", v_pages, dtype),
+               ("prefix_table", prefix_table, i32), ("prefix_lens", prefix_lens, i32),
+               ("group_starts", group_starts, i32), ("page_table", page_table, i32),
+               ("seq_lens", seq_lens, i32), ("out", out, out_dtype), ("lse", lse, f32),
+               ("status", status, i32), ("sinks", sinks, f32), ("q_lens", q_lens, i32),
+               ("workspace", workspace, None if workspace is None else workspace.dtype))
     table, prefixes = page_table.shape, prefix_table.shape
     if len(table) != 2 or table[0] != B or seq_lens.numel() != B or len(prefixes) != 2 or \
             prefix_lens.numel() != prefixes[0] or group_starts.numel() != prefixes[0] + 1 or \
@@ -492,24 +524,25 @@ def shared(q, k_pages, v_pages, prefix_table, prefix_lens, group_starts, page_ta
         raise ValueError("page_table must be [B][max_pages], prefix_table [n_groups][max_prefix_pages], "
                          "prefix_lens [n_groups], group_starts [n_groups + 1], seq_lens and q_lens "
                          "[B], out like q, lse [B][Hq][q_len], sinks [Hq], status one word")
-    lib = load_library()
-    L = _launch(q, k_pages, page_table, out_dtype, out, lse, None, status, _stream(device),
-                split_tokens, debug_flags,
-                None if events is None else ctypes.cast(events, ctypes.c_void_p).value, 0, softcap, sinks, q_lens, None, PHASE_ALL, sm_count)
-    S = _Shared(prefix_table.data_ptr(), prefix_lens.data_ptr(), group_starts.data_ptr(),
-                prefixes[0], prefixes[1])
+    load_library()
+    kind = _DTYPES.get(dtype, -1)
+    S = _pack_shared(prefix_table.data_ptr(), prefix_lens.data_ptr(), group_starts.data_ptr(),
+                     prefixes[0], prefixes[1])
+    L = [B, table[1], pool[0], n, kind, kind, _DTYPES.get(out_dtype, -1), out.data_ptr(), _address(lse),
+         0, 0, _address(status), _stream(device) or 0, split_tokens, debug_flags,
+         0 if events is None else ctypes.cast(events, ctypes.c_void_p).value, 0, softcap,
+         _address(sinks), _address(q_lens), 0, PHASE_ALL, sm_count]
     with _on(device):
         if workspace is None:
-            need = lib.atlas_attn_shared_workspace_size(n_q_heads, n_kv_heads, head_dim, page_tokens,
-                                                        ctypes.byref(S), ctypes.byref(L))
+            need = _fast.attn_shared_workspace_size(n_q_heads, n_kv_heads, head_dim, page_tokens, S,
+                                                    _pack_launch(*L))
             if need < ctypes.c_size_t(-1).value:
                 workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        L.workspace = _ptr(workspace)
-        L.workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        rc = lib.atlas_attn_shared(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                                   page_table.data_ptr(), seq_lens.data_ptr(), n_q_heads,
-                                   n_kv_heads, head_dim, page_tokens, float(scale),
-                                   ctypes.byref(S), ctypes.byref(L))
+        if workspace is not None:
+            L[9], L[10] = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        rc = _fast.attn_shared(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                               page_table.data_ptr(), seq_lens.data_ptr(), n_q_heads, n_kv_heads,
+                               head_dim, page_tokens, scale, S, _pack_launch(*L))
     if rc != 0:
         raise AtlasError(rc, status_string(rc))
     return out
@@ -596,6 +629,14 @@ def _check(device, *tensors):
             raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
 
 
+def _fits(index, *tensors):
+    """Whether _check would pass them: (tensor or None, dtype) each, on the device of that index."""
+    for t, dtype in tensors:
+        if t is not None and (t.dtype is not dtype or t.get_device() != index or not t.is_contiguous()):
+            return False
+    return True
+
+
 def _cuda_device(name, t):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -616,14 +657,14 @@ def _frequencies(theta, rot_dim):
                                               for p in range(rot_dim // 2)))
 
 
-_Strides = ctypes.c_int64 * 3
+_DENSE = (0, 0, 0)
 
 
 def _row_strides(name, t):
     """Element strides (batch, head, token) of a [B][H][n][D] view with contiguous rows;
     all zero for a contiguous one."""
     if t.is_contiguous():
-        return _Strides()
+        return _DENSE
     sb, sh, st, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must have contiguous rows of head_dim elements")
@@ -631,7 +672,7 @@ def _row_strides(name, t):
     sb, sh, st = sb if nb > 1 else 0, sh if nh > 1 else 0, st if nt > 1 else 0
     if not (sb or sh or st):  # the library reads all-zero strides as dense rows
         raise ValueError(f"{name} is one row broadcast to all: make it contiguous")
-    return _Strides(sb, sh, st)
+    return sb, sh, st
 
 
 def kv_append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, positions, *,
@@ -667,22 +708,20 @@ def kv_append_norm_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens,
 
 
 def _norm(device, dtype, q_weight, k_weight, eps, offset, Hq, Hkv, D):
-    """The atlas_qk_norm of checked weights."""
-    given = [w for w in (q_weight, k_weight) if w is not None]
-    N = _Norm(eps=eps, weight_offset=offset, weight_dtype=_DTYPES[torch.float32])
-    if given:
-        kind = given[0].dtype
-        if kind not in (dtype, torch.float32):
-            raise ValueError(f"q_weight and k_weight must be {dtype} or {torch.float32}")
+    """The packed atlas_qk_norm of checked weights."""
+    first = q_weight if q_weight is not None else k_weight
+    if first is None:
+        return _pack_norm(0, 0, _F32, 0, offset, eps)
+    kind, per_head = first.dtype, first.dim() == 2
+    if kind is not dtype and kind is not torch.float32:
+        raise ValueError(f"q_weight and k_weight must be {dtype} or {torch.float32}")
+    if not _fits(device.index, (q_weight, kind), (k_weight, kind)):
         _check(device, ("q_weight", q_weight, kind), ("k_weight", k_weight, kind))
-        per_head = given[0].dim() == 2
-        for name, w, heads in (("q_weight", q_weight, Hq), ("k_weight", k_weight, Hkv)):
-            if w is not None and w.shape != ((heads, D) if per_head else (D,)) and \
-                    not (heads is None and w.dim() == 1 + per_head and w.shape[-1] == D):
-                raise ValueError(f"{name} must be [head_dim], or [heads][head_dim] like the other")
-        N.weight_dtype, N.per_head = _DTYPES.get(kind, -1), int(per_head)
-        N.q_weight, N.k_weight = _ptr(q_weight), _ptr(k_weight)
-    return N
+    for name, w, heads in (("q_weight", q_weight, Hq), ("k_weight", k_weight, Hkv)):
+        if w is not None and w.shape != ((heads, D) if per_head else (D,)) and \
+                not (heads is None and w.dim() == 1 + per_head and w.shape[-1] == D):
+            raise ValueError(f"{name} must be [head_dim], or [heads][head_dim] like the other")
+    return _pack_norm(_address(q_weight), _address(k_weight), _DTYPES.get(kind, -1), per_head, offset, eps)
 
 
 def _append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, positions, theta, inv_freq,
@@ -698,13 +737,16 @@ def _append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, positi
         positions = positions[None]
     if positions.shape[1:] != (B, n):
         raise ValueError("positions must be [n_axes][B][n]")
+    index, i32 = device.index, torch.int32
     for name, t in (("k_new", k_new), ("v_new", v_new), ("q", q)):
-        if t is not None and (t.dtype != dtype or t.device != device):
+        if t is not None and (t.dtype is not dtype or t.get_device() != index):
             raise ValueError(f"{name} must be a {dtype} tensor on {device}")
-    _check(device, ("k_pages", k_pages, dtype), ("v_pages", v_pages, dtype),
-           ("page_table", page_table, torch.int32), ("seq_lens", seq_lens, torch.int32),
-           ("positions", positions, torch.int32), ("n_new", n_new, torch.int32),
-           ("q_out", q_out, dtype), ("status", status, torch.int32))
+    if not _fits(index, (k_pages, dtype), (v_pages, dtype), (page_table, i32), (seq_lens, i32),
+                 (positions, i32), (n_new, i32), (q_out, dtype), (status, i32)):
+        _check(device, ("k_pages", k_pages, dtype), ("v_pages", v_pages, dtype),
+               ("page_table", page_table, i32), ("seq_lens", seq_lens, i32),
+               ("positions", positions, i32), ("n_new", n_new, i32), ("q_out", q_out, dtype),
+               ("status", status, i32))
     table = page_table.shape
     if len(table) != 2 or table[0] != B or seq_lens.numel() != B or \
             (n_new is not None and n_new.numel() != B):
@@ -713,11 +755,8 @@ def _append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, positi
     for name, x in (("pair_axis", pair_axis), ("inv_freq", inv_freq)):
         if x is not None and len(x) != rot_dim // 2:
             raise ValueError(f"{name} must have rot_dim / 2 entries")
-    R = _Rope(batch=B, max_pages_per_seq=table[1], num_pages=pool[0], max_new=n,
-              kv_dtype=_DTYPES.get(dtype, -1), k_strides=_row_strides("k_new", k_new),
-              v_strides=_row_strides("v_new", v_new), positions=positions.data_ptr(),
-              n_axes=positions.shape[0], rot_dim=rot_dim, interleaved=bool(interleaved),
-              theta=theta)
+    n_q_heads = q_at = q_out_at = 0
+    q_strides = _DENSE
     if q is not None:
         rows = q.shape
         if len(rows) != 4 or rows[0] != B or rows[2:] != (n, D):
@@ -726,30 +765,30 @@ def _append_rope(q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, positi
             q_out = torch.empty(rows, dtype=dtype, device=device)
         elif q_out.shape != rows:
             raise ValueError("q_out must have q's shape")
-        R.n_q_heads, R.q, R.q_out = rows[1], q.data_ptr(), q_out.data_ptr()
-        R.q_strides = _row_strides("q", q)
-        if R.q_out == R.q and not q.is_contiguous():
+        n_q_heads, q_at, q_out_at, q_strides = rows[1], q.data_ptr(), q_out.data_ptr(), _row_strides("q", q)
+        if q_out_at == q_at and not q.is_contiguous():
             raise ValueError("q_out may be q itself only when q is contiguous")
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    if pair_axis is not None:
-        axes = _host_array(ctypes.c_int32, tuple(pair_axis))  # (held until the call is over)
-        R.pair_axis = ctypes.addressof(axes)
+    # (the host arrays are held until the call is over)
+    axes = None if pair_axis is None else _host_array(ctypes.c_int32, tuple(pair_axis))
     freq = _frequencies(theta, rot_dim) if inv_freq is None else \
         (ctypes.c_double * len(inv_freq))(*inv_freq)
-    if freq is not None:
-        R.inv_freq = ctypes.addressof(freq)
-    R.status_word = _ptr(status)
-    R.stream = _stream(device)
+    R = _pack_rope(B, table[1], pool[0], n, _DTYPES.get(dtype, -1), n_q_heads, q_at, q_out_at,
+                   *q_strides, *_row_strides("k_new", k_new), *_row_strides("v_new", v_new),
+                   positions.data_ptr(), positions.shape[0], rot_dim, bool(interleaved),
+                   0 if axes is None else ctypes.addressof(axes),
+                   0 if freq is None else ctypes.addressof(freq), theta, _address(status),
+                   _stream(device) or 0)
     args = (k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-            page_table.data_ptr(), seq_lens.data_ptr(), _ptr(n_new), Hkv, D, pool[2], ctypes.byref(R))
+            page_table.data_ptr(), seq_lens.data_ptr(), _ptr(n_new), Hkv, D, pool[2], R)
     if norm is None:
         with _on(device):
-            rc = lib.atlas_kv_append_rope(*args)
+            rc = _fast.kv_append_rope(*args)
     else:
-        N = _norm(device, dtype, *norm, None if q is None else q.shape[1], Hkv, D)
+        N = _norm(device, dtype, *norm, None if q is None else n_q_heads, Hkv, D)
         with _on(device):
-            rc = lib.atlas_kv_append_norm_rope(*args, ctypes.byref(N))
+            rc = _fast.kv_append_norm_rope(*args, N)
     if rc != 0:
         raise AtlasError(rc, status_string(rc))
     return q_out
