@@ -53,6 +53,7 @@
 #include "tc_order.cuh"
 
 #include <math.h>
+#include <type_traits>
 
 namespace atlas {
 namespace {
@@ -60,6 +61,8 @@ namespace {
 constexpr int BM = 128;  // query rows per tile
 constexpr int BN = 128;  // keys per block
 constexpr int kMaxItems = 64;  // work items of one CTA in persistent mode
+// ... and with shared prefixes (what is left of shared memory)
+constexpr int shared_items(int tiles) { return tiles == 2 ? 48 : 32; }
 constexpr int kSlab = 128 * 128;  // one 64-element slab of a 128-row bf16 tile (128-byte rows)
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when the max grows 256x
@@ -81,11 +84,13 @@ struct TcWork {
     int kv_begin, kv_end, nb;  // key range and its 128-key blocks
     bool hilo, tail_fix;       // hi + lo P on every block; last block partly past kv_end
     int tail_first;            // first key row of the last block past kv_end
+    int n_pre, pre_len;        // SHARED: blocks of the tile that are the prefix's, its keys,
+    int blk0, own_len, group;  // the item's first block, own keys, whose prefix
     int state;                 // 0: compute; 1: nothing to compute; 2: bad seq_len;
                                // 3: no encoder states (direct mode writes the empty rows)
 };
 
-template <int NT, int D>
+template <int NT, int D, bool SHARED = false>
 struct Cfg {
     static_assert(D == 64 || D == 128, "head_dim 64 or 128");
     static constexpr int kSlabs = D / 64;             // 64-element slabs per row
@@ -126,9 +131,11 @@ struct Cfg {
     static constexpr int OFF_VOTE = OFF_FLAG + 8;
     // the CTA's work items (persistent mode: up to kMaxItems), written once at the start
     static constexpr int kItemSlots = NT == 2 ? kMaxItems : 1;
+    static constexpr int kItemBytes = SHARED ? shared_items(NT) * (int)sizeof(SharedSeg)
+                                             : kItemSlots * (int)sizeof(TcWork);
     static constexpr int OFF_MASK = OFF_VOTE + 16;  // [2] words: items with a bad page id
     static constexpr int OFF_ITEMS = OFF_MASK + 8;
-    static constexpr int kSmem = OFF_ITEMS + kItemSlots * (int)sizeof(TcWork) + 1024;  // + slack
+    static constexpr int kSmem = OFF_ITEMS + kItemBytes + 1024;  // + slack
     static_assert(kSmem <= 232448, "shared memory budget");
     // TMEM columns: NT=2 -> [S0 | O0 | S1 | O1]; NT=1 -> [S(buf 0) | S(buf 1) | O]
     __device__ static constexpr uint32_t s_col(int x, int b) {
@@ -159,10 +166,9 @@ __device__ __forceinline__ int64_t tile_row(const TcParams &p, int b, int hkv, i
     return ((int64_t)b * p.Hq + (int64_t)hkv * p.G) * p.q_len + f;
 }
 
-// NaN for row f of (b, hkv) in direct mode.
+// NaN for an output row.
 template <int D>
-__device__ void nan_row(const TcParams &p, int b, int hkv, int f) {
-    const int64_t row = tile_row(p, b, hkv, f);
+__device__ void nan_out_row(const TcParams &p, int64_t row) {
     const float nan = __int_as_float(0x7fc00000);
     if (p.out_bf16) {
         uint4 v;
@@ -174,6 +180,12 @@ __device__ void nan_row(const TcParams &p, int b, int hkv, int f) {
         for (int k = 0; k < D / 4; ++k) o[k] = make_float4(nan, nan, nan, nan);
     }
     if (p.lse) p.lse[row] = nan;
+}
+
+// NaN for row f of (b, hkv) in direct mode.
+template <int D>
+__device__ void nan_row(const TcParams &p, int b, int hkv, int f) {
+    nan_out_row<D>(p, tile_row(p, b, hkv, f));
 }
 
 // Row f of (b, hkv) of cross attention over no encoder states, direct mode: 0, with
@@ -292,13 +304,14 @@ __device__ __forceinline__ int tc_persist_item(int k, int i, int ctas) {
     return i * ctas + ((i & 1) ? ctas - 1 - k : k);
 }
 
-// SHARED: the splits of prefixes that groups of sequences share (shared_prefix.cuh).
+// SHARED: pieces of tiles over prefixes that groups of sequences share, and perhaps the
+// sequences' own keys behind them (shared_prefix.cuh), each CTA's one after the other as PERSIST.
 template <int NT, int D, bool PERSIST, bool SHARED = false>
 __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     fmha_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const TcParams p) {
     allow_dependent_launch();  // the merge may start its CTAs (it waits for this grid)
-    using C = Cfg<NT, D>;
+    using C = Cfg<NT, D, SHARED>;
     constexpr int S = C::kStages, SB = C::kSB;
     constexpr int kTileBytes = C::kTileBytes;
     extern __shared__ uint8_t smem_raw[];
@@ -318,35 +331,25 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     // current item's last blocks and epilogue.
     int n_items = 1;
     TcWork w0{};
-    int seq0 = 0;  // SHARED: the first sequence of the item's group
-    // The merge that follows a SHARED grid reads the sequences' own splits too, which the
-    // grid before this one writes: one CTA at least must not end before that grid has.
+    SharedSeg *const segs = reinterpret_cast<SharedSeg *>(smem + C::OFF_ITEMS);
+    // The merge that follows a SHARED grid of prefixes reads the sequences' own splits too,
+    // which the grid before this one writes: one CTA at least must not end before that grid has.
     auto before_exit = [&]() {
         if (SHARED && blockIdx.x == 0) wait_for_previous_grid();
     };
-    if (SHARED) {
-        const SharedGroups groups{p.group_starts, p.seq_lens, p.n_groups, p.B,   p.max_pages * p.P,
-                                  p.G * p.q_len,  NT * BM,    p.chunk,    p.Hkv, p.status};
-        const SharedItem it =
-            shared_item(groups, blockIdx.x, reinterpret_cast<int *>(smem + C::OFF_V));
-        if (it.group < 0) {
+    if constexpr (SHARED) {
+        int *const count = reinterpret_cast<int *>(smem + C::OFF_FLAG);
+        if (warp == 0) {
+            const int n = shared_segs(p, blockIdx.x, segs);
+            if (lane == 0) *count = n;
+        }
+        __syncthreads();
+        n_items = *count;
+        if (n_items == 0) {
             before_exit();
             return;
         }
-        __syncthreads();  // (the scratch is the V ring)
-        seq0 = it.seq0;
-        w0.b = it.group;
-        w0.hkv = it.hkv;
-        w0.c = it.split;
-        w0.t0 = it.tile * NT;
-        w0.tstep = NT - 1;
-        w0.rows_unit = it.seqs * p.G * p.q_len;
-        w0.kv_begin = it.split * p.chunk;
-        w0.kv_end = min(it.len, w0.kv_begin + p.chunk);
-        w0.nb = (w0.kv_end - w0.kv_begin + BN - 1) / BN;
-        w0.hilo = it.len < p.hilo_below;
-        w0.tail_first = w0.kv_end - (w0.kv_begin + (w0.nb - 1) * BN);
-        w0.tail_fix = w0.tail_first < BN;
+        __syncthreads();  // (the word is the abort flag from here on)
     } else if (PERSIST) {
         const int total = p.B * p.Hkv * (p.G / NT) * p.tiles_per_head;
         n_items = 0;
@@ -383,14 +386,54 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     }
     // Output row of tile row f of an item, and whether it is a query.
     auto row_of = [&](const TcWork &w, int f) -> int64_t {
-        if constexpr (SHARED) return shared_row(p, seq0, w.hkv, f);
+        if constexpr (SHARED) return unit_row(p, w.b, w.hkv, f);
         else return tile_row(p, w.b, w.hkv, f);
     };
     auto is_query = [&](const TcWork &w, int f) -> bool {
-        if constexpr (SHARED) return shared_real(p, seq0, w.rows_unit, f);
+        if constexpr (SHARED) return f < w.rows_unit;
         else return f < w.rows_unit && f % p.q_len < w.qn;
     };
     TcWork *const items = reinterpret_cast<TcWork *>(smem + C::OFF_ITEMS);
+    using Item = std::conditional_t<SHARED, TcWork, const TcWork &>;
+    auto item = [&](int it) -> Item {
+        if constexpr (SHARED) {
+            const SharedSeg &s = segs[it];
+            TcWork w{};
+            w.b = s.unit;
+            w.hkv = s.hkv;
+            w.c = s.state;  // -1: all of the tile, its output is written here
+            w.t0 = s.row0 / BM;
+            w.tstep = NT - 1;
+            w.qn = p.st.whole ? (p.q_lens ? p.q_lens[s.unit] : p.q_len) : 1;
+            w.rows_unit = s.rows;
+            w.n_pre = (s.len + BN - 1) / BN;
+            w.pre_len = s.len;
+            w.own_len = s.own;
+            w.blk0 = s.blk0;
+            w.group = s.group;
+            w.nb = s.nb;
+            w.L = p.st.whole ? p.seq_lens[s.unit] : 0;
+            w.hilo = s.len + max(0, w.L - w.qn) < p.hilo_below;
+            return w;
+        } else if constexpr (PERSIST) {
+            return items[it];
+        } else {
+            return w0;
+        }
+    };
+    // Where a tile row's partial state goes.  (SHARED over whole tiles: each CTA has two places of
+    // tile_rows rows, for the tile that it goes on with and the one that it leaves off.)
+    auto slot_of = [&](const TcWork &w, int64_t row, int f) -> int64_t {
+        if constexpr (SHARED)
+            if (p.st.whole)
+                return ((int64_t)blockIdx.x * 2 + (w.blk0 == 0)) * p.st.tile_rows + f - w.t0 * BM;
+        return row * p.n_chunks + w.c;
+    };
+    // SHARED: keys of block j of an item, counted from the block's first key.
+    auto block_keys = [&](const TcWork &w, int j) -> int {
+        const int jb = w.blk0 + j;
+        return min(BN, jb < w.n_pre ? w.pre_len - jb * BN : w.own_len - (jb - w.n_pre) * BN);
+    };
     // Items not computed (bit set): a bad seq_len or a page id outside the pool (rows
     // NaN), or nothing to compute.  The page ids of every item's key range are
     // checked by the whole CTA at once; the result is the same in every thread.
@@ -398,7 +441,21 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     if (threadIdx.x == 0) bad_words[0] = bad_words[1] = 0u;
     __syncthreads();
     uint64_t skip = 0, bad = 0;
-    for (int it = 0; it < n_items; ++it) {
+    for (int it = 0; SHARED && it < n_items; ++it) {
+        const TcWork w = item(it);
+        const int blk1 = w.blk0 + w.nb;
+        for (int part = 0; part < 2; ++part) {  // pages of the prefix, then the sequence's own
+            const int first = part ? max(w.blk0 - w.n_pre, 0) : w.blk0;
+            const int keys = part ? min(w.own_len, (blk1 - w.n_pre) * BN) : min(w.pre_len, blk1 * BN);
+            const int32_t *table = part ? p.page_table + (int64_t)w.b * p.max_pages
+                                        : p.st.prefix_table + (int64_t)w.group * p.st.max_prefix_pages;
+            for (int pg = first * BN / p.P + (int)threadIdx.x; pg * p.P < keys; pg += blockDim.x) {
+                const int id = table[pg];
+                if (id < 0 || id >= p.num_pages) bad |= 1ull << it;
+            }
+        }
+    }
+    for (int it = 0; !SHARED && it < n_items; ++it) {
         TcWork w = w0;
         if (PERSIST) {
             int u, t0, tstep;
@@ -425,7 +482,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     skip |= bad_page;
     for (int it = 0; skip && it < n_items; ++it) {
         if (!((skip >> it) & 1)) continue;
-        const TcWork &w = PERSIST ? items[it] : w0;
+        Item w = item(it);
         if (w.state == 2) {
             if (threadIdx.x == 0 && w.c == 0 && p.status) atomicOr(p.status, ATLAS_DEV_BAD_SEQLEN);
             const int rows_valid = (w.qn >= 0 && w.qn <= p.q_len) ? w.qn : p.q_len;
@@ -444,10 +501,12 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             if (threadIdx.x < NT * BM) {
                 const int f = (w.t0 + (int)(threadIdx.x / BM) * w.tstep) * BM + threadIdx.x % BM;
                 if (is_query(w, f)) {
-                    if (!p.split) {
+                    if (SHARED ? w.c < 0 : !p.split) {
+                        if constexpr (SHARED) nan_out_row<D>(p, row_of(w, f));
+                        else
                         nan_row<D>(p, w.b, w.hkv, f);
                     } else {
-                        float *ml = p.ws_ml + (row_of(w, f) * p.n_chunks + w.c) * 2;
+                        float *ml = p.ws_ml + slot_of(w, row_of(w, f), f) * 2;
                         ml[0] = ml[1] = __int_as_float(0x7fc00000);
                     }
                 }
@@ -509,7 +568,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         int nq = 0;  // Q tile pairs loaded so far
         for (int it = 0; it < n_items && !failed; ++it) {
             if ((skip >> it) & 1) continue;
-            const TcWork &w = PERSIST ? items[it] : w0;
+            Item w = item(it);
             if (kv == 0 && !SHARED) {
                 // The previous item's Q tiles are free once its last S products are done.
                 if (nq > 0 && !wait_warp(BAR(C::B_QEMPTY), (nq - 1) & 1, abort_flag)) {
@@ -528,11 +587,23 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                 }
                 ++nq;
             }
-            PageIdCache pages{p.page_table + (int64_t)w.b * p.max_pages, (w.kv_end - 1) >> lp};
+            PageIdCache pages{p.page_table + (int64_t)w.b * p.max_pages,
+                              ((SHARED ? w.own_len : w.kv_end) - 1) >> lp};
+            if (SHARED && w.blk0 < w.n_pre)
+                pages = PageIdCache{p.st.prefix_table + (int64_t)w.group * p.st.max_prefix_pages,
+                                    (w.pre_len - 1) >> lp};
             for (int j = 0; j < w.nb; ++j) {
                 const int s = g % S, use = g / S;
-                const int kb = w.kv_begin + j * BN;
-                const int nbox = (min(BN, w.kv_end - kb) + p.P - 1) >> lp;  // <= 16
+                int kb = w.kv_begin + j * BN;
+                if constexpr (SHARED) {
+                    const int jb = w.blk0 + j;
+                    if (j > 0 && jb == w.n_pre)  // from the prefix to the sequence's own keys
+                        pages = PageIdCache{p.page_table + (int64_t)w.b * p.max_pages,
+                                            (w.own_len - 1) >> lp};
+                    kb = (jb < w.n_pre ? jb : jb - w.n_pre) * BN;
+                }
+                const int keys = SHARED ? block_keys(w, j) : min(BN, w.kv_end - kb);
+                const int nbox = (keys + p.P - 1) >> lp;  // <= 16
                 const int y =
                     (pages.get_line(kb >> lp, lane < nbox ? lane : 0) * p.Hkv + w.hkv) << lp;
                 if (use > 0 && !wait_warp(BAR(bar_empty + s), (use - 1) & 1, abort_flag)) {
@@ -575,7 +646,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             int ntail = 0;  // tail fix-ups so far
             for (int it = 0; ok && it < n_items; ++it) {
                 if ((skip >> it) & 1) continue;
-                const TcWork &w = PERSIST ? items[it] : w0;
+                Item w = item(it);
                 const int nb = w.nb;
                 ok = wait_warp(BAR(C::B_Q), nq & 1, abort_flag);
                 tc_fence_after();
@@ -627,7 +698,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                                 ok = false;
                                 break;
                             }
-                            if (j == nb - 1 && w.tail_fix) {
+                            if (SHARED ? block_keys(w, j) < BN : j == nb - 1 && w.tail_fix) {
                                 // Hand the landed last V block to the fix-up warp (only
                                 // this warp observes every phase of the V ring in order).
                                 if (elect_one()) mbar_arrive(BAR(C::B_TAIL_READY));
@@ -720,14 +791,17 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         int g = 0, ntail = 0;
         for (int it = 0; it < n_items && !failed; ++it) {
             if ((skip >> it) & 1) continue;
-            const TcWork &w = PERSIST ? items[it] : w0;
-            if (w.tail_fix) {
-                const int s = (g + w.nb - 1) % S;
+            Item w = item(it);
+            // (SHARED: the prefix's last block may end before its 128th key too)
+            for (int j = SHARED ? 0 : w.nb - 1; j < w.nb; ++j) {
+                const int first = SHARED ? block_keys(w, j) : w.tail_fix ? w.tail_first : BN;
+                if (first == BN) continue;
+                const int s = (g + j) % S;
                 if (wait_warp(BAR(C::B_TAIL_READY), ntail & 1, abort_flag)) {
                     const uint32_t vbase = sb + C::OFF_V + s * kTileBytes;
                     constexpr int kChunks = 8 * C::kSlabs;  // 16-byte chunks per V row
-                    for (int idx = lane; idx < (BN - w.tail_first) * kChunks; idx += 32) {
-                        const int row = w.tail_first + idx / kChunks, q = idx % kChunks;
+                    for (int idx = lane; idx < (BN - first) * kChunks; idx += 32) {
+                        const int row = first + idx / kChunks, q = idx % kChunks;
                         st_shared_v4(vbase + (q / 8) * kSlab + row * 128 + (q % 8) * 16, 0u, 0u,
                                      0u, 0u);
                     }
@@ -737,6 +811,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                     ++ntail;
                 } else {
                     failed = true;
+                    break;
                 }
             }
             g += w.nb;
@@ -748,41 +823,53 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         const int q4 = warp % 4;                      // TMEM lane quadrant
         const int r = q4 * 32 + lane;
         const bool capped = p.softcap_log2 > 0.f;
-        const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;  // 32-byte stores
+        const bool out32 =  // 32-byte stores
+            ((reinterpret_cast<uintptr_t>(p.out) | (SHARED ? reinterpret_cast<uintptr_t>(p.ws_acc) : 0)) & 31) == 0;
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
         const uint32_t to = tl + C::o_col(x);
-        if constexpr (SHARED) {
-            // Q rows of many sequences: each warp copies its own 32 rows to where the tile's
-            // TMA load would put them (rows past the group's last are zero).
+        // SHARED: Q rows of many sequences; each warp copies its own 32 rows to where the tile's
+        // TMA load would put them (rows past the unit's last are zero).
+        auto copy_q = [&](const TcWork &w) {
             constexpr int kChunks = D / 8;  // 16-byte chunks of a row
             const uint32_t qt = sb + C::OFF_Q + x * kTileBytes;
 #pragma unroll 4
             for (int k = lane; k < 32 * kChunks; k += 32) {
                 const int row = q4 * 32 + k / kChunks, ch = k % kChunks;
-                const int f = (w0.t0 + x * w0.tstep) * BM + row;
-                const bool in = f < w0.rows_unit;
+                const int f = (w.t0 + x * w.tstep) * BM + row;
+                const bool in = f < w.rows_unit;
                 const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
-                                           row_of(w0, in ? f : 0) * D + ch * 8;
+                                           row_of(w, in ? f : 0) * D + ch * 8;
                 cp_async16(qt + (ch / 8) * kSlab + sw128(row, ch % 8), src, in ? 16u : 0u);
             }
             cp_async_commit();
+        };
+        auto q_copied = [&]() {
             cp_async_wait<0>();
             fence_proxy_async_smem();
             mbar_arrive(BAR(C::B_Q));
+        };
+        int nq = 0;  // SHARED: items whose Q has been copied
+        if (SHARED) {
+            int first = 0;
+            while ((skip >> first) & 1) ++first;
+            copy_q(item(first));
+            q_copied();
+            nq = 1;
         }
         bool ok = true;
         int g = 0;  // blocks of earlier items
         int it = 0;
         for (; ok && it < n_items; ++it) {
         if ((skip >> it) & 1) continue;
-        const TcWork &w = PERSIST ? items[it] : w0;
+        Item w = item(it);
         const int c = w.c, kv_begin = w.kv_begin, nb = w.nb;
         const bool hilo = w.hilo;
         const int f = (w.t0 + x * w.tstep) * BM + r;
         const bool valid = is_query(w, f);  // padding rows: no queries
-        const int i = valid && !SHARED ? f % p.q_len : 0;
+        const int i = valid ? f % (SHARED ? w.qn : p.q_len) : 0;
+        // (SHARED: own keys; of a prefix every row sees all)
         const int lim_row = !valid   ? 0
-                            : SHARED ? w.kv_end  // a prefix: every row sees all of it
+                            : SHARED ? w.L - w.qn + i + 1
                                      : min(w.L - p.q_len + p.row_step * i + 1, w.kv_end);
         const int lo_row =
             (valid && !SHARED && p.window > 0) ? max(0, w.L - p.q_len + i + 1 - p.window) : 0;
@@ -797,8 +884,13 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             }
             tc_fence_after();
             const uint32_t ts = tl + C::s_col(x, bsel);
-            const int nvis = lim_row - (kv_begin + j * BN);  // visible columns: [nlo, nvis)
-            const int nlo = lo_row - (kv_begin + j * BN);
+            int nvis = lim_row - (kv_begin + j * BN);  // visible columns: [nlo, nvis)
+            int nlo = lo_row - (kv_begin + j * BN);
+            if constexpr (SHARED) {
+                const int jb = w.blk0 + j;
+                nlo = 0;
+                nvis = !valid ? 0 : jb < w.n_pre ? w.pre_len - jb * BN : lim_row - (jb - w.n_pre) * BN;
+            }
             // Padding rows of a ragged batch never reach the output: they may take the
             // unmasked path (their O and l are garbage but stay in their own row).
             const bool all_visible = __all_sync(0xffffffffu, !valid || (nvis >= BN && nlo <= 0));
@@ -1018,7 +1110,23 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             tc_fence_before();
             mbar_arrive(BAR(C::B_PFULL + x));
         }
-        if (ok && !wait_warp(BAR(C::B_PVDONE + x), (g + nb - 1) & 1, abort_flag)) ok = false;
+        if constexpr (SHARED) {
+            // The next item's Q, once this one's last S products are done: on its way while the
+            // last PV product and the epilogue are.
+            int next = it + 1;
+            while (next < n_items && ((skip >> next) & 1)) ++next;
+            if (ok && next < n_items) {
+                ok = wait_warp(BAR(C::B_QEMPTY), (nq - 1) & 1, abort_flag);
+                if (ok) copy_q(item(next));
+                if (ok) ok = wait_warp(BAR(C::B_PVDONE + x), (g + nb - 1) & 1, abort_flag);
+                q_copied();
+                ++nq;
+            } else if (ok) {
+                ok = wait_warp(BAR(C::B_PVDONE + x), (g + nb - 1) & 1, abort_flag);
+            }
+        } else if (ok && !wait_warp(BAR(C::B_PVDONE + x), (g + nb - 1) & 1, abort_flag)) {
+            ok = false;
+        }
         if (!ok) {
             failed = true;
             *abort_flag = 1;
@@ -1029,16 +1137,17 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             const int64_t row = row_of(w, valid ? f : 0);
             // Direct mode folds the sink (one more state: m = sink log2 e, l = 1,
             // acc = 0) here; split mode leaves it to the merge.
+            const bool part = SHARED ? c >= 0 : p.split != 0;  // a partial state, or the output
             float osc = 1.f;  // factor on acc
-            if (!p.split && p.sinks && valid) {
+            if (!part && p.sinks && valid) {
                 const float sink2 = p.sinks[(row / p.q_len) % p.Hq] * kLog2e;
                 const float M = fmaxf(m_used, sink2);
                 osc = ex2(m_used - M);
                 l = l * osc + ex2(sink2 - M);
                 m_used = M;
             }
-            const float inv = p.split ? 1.f : osc / l;
-            const int64_t slot = row * p.n_chunks + c;
+            const float inv = part ? 1.f : osc / l;
+            const int64_t slot = slot_of(w, row, f);
             // The warp's 32 rows go through shared memory so that each global store
             // instruction writes whole rows: lane r holds row r of the warp, whose
             // 16-byte chunk c sits at chunk c ^ (r & 7) of its staging row, so that
@@ -1061,10 +1170,13 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                     // straight from registers (direct mode), in 32-byte stores when the
                     // output allows (each fills a whole sector of its row).
                     if (!valid) continue;
-                    uint8_t *dst = static_cast<uint8_t *>(p.out) +
-                                   (row * D + cc * 32) * (p.out_bf16 ? 2 : 4);
+                    const bool narrow = p.out_bf16 && !(SHARED && part);
+                    uint8_t *dst = SHARED && part ? reinterpret_cast<uint8_t *>(p.ws_acc) +
+                                                        (slot * D + cc * 32) * 4
+                                                  : static_cast<uint8_t *>(p.out) +
+                                                        (row * D + cc * 32) * (p.out_bf16 ? 2 : 4);
                     auto f = [&](int e) { return __uint_as_float(o[e]) * inv; };
-                    if (p.out_bf16) {
+                    if (narrow) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {  // 16 columns = 32 bytes each
                             const uint4 a = make_uint4(
@@ -1147,7 +1259,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                 if (off >= 0) *reinterpret_cast<uint4 *>(dst_base + off + ch * 16) = v;
             }
             if (valid) {
-                if (p.split) {
+                if (part) {
                     p.ws_ml[slot * 2] = m_used;
                     p.ws_ml[slot * 2 + 1] = l;
                 } else if (p.lse) {
@@ -1155,11 +1267,11 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                 }
             }
         } else if (valid) {
-            if (p.split) {
-                const int64_t slot = row_of(w, f) * p.n_chunks + c;
+            if (SHARED ? c >= 0 : p.split) {
+                const int64_t slot = slot_of(w, row_of(w, f), f);
                 p.ws_ml[slot * 2] = p.ws_ml[slot * 2 + 1] = __int_as_float(0x7fc00000);
             } else {
-                nan_row<D>(p, w.b, w.hkv, f);
+                nan_out_row<D>(p, row_of(w, f));
             }
         }
         g += nb;
@@ -1167,14 +1279,14 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         // After an abort, the items this warpgroup did not reach: their rows NaN.
         for (; it < n_items; ++it) {
             if ((skip >> it) & 1) continue;
-            const TcWork &w = PERSIST ? items[it] : w0;
+            Item w = item(it);
             const int f = (w.t0 + x * w.tstep) * BM + r;
             if (!is_query(w, f)) continue;
-            if (p.split) {
-                float *ml = p.ws_ml + (row_of(w, f) * p.n_chunks + w.c) * 2;
+            if (SHARED ? w.c >= 0 : p.split) {
+                float *ml = p.ws_ml + slot_of(w, row_of(w, f), f) * 2;
                 ml[0] = ml[1] = __int_as_float(0x7fc00000);
             } else {
-                nan_row<D>(p, w.b, w.hkv, f);
+                nan_out_row<D>(p, row_of(w, f));
             }
         }
     }
@@ -1239,8 +1351,8 @@ cudaError_t launch_instance(const TcParams &p, const CUtensorMap &tmQ, const CUt
 template <int NT, int D>
 cudaError_t launch_shared_instance(const TcParams &p, int64_t ctas, const CUtensorMap &tmK,
                                    const CUtensorMap &tmV, cudaStream_t stream) {
-    using C = Cfg<NT, D>;
-    auto kern = fmha_tc_kernel<NT, D, false, true>;
+    using C = Cfg<NT, D, true>;
+    auto kern = fmha_tc_kernel<NT, D, true, true>;
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -1250,19 +1362,26 @@ cudaError_t launch_shared_instance(const TcParams &p, int64_t ctas, const CUtens
         if (err != cudaSuccess) return err;
         if (dev < 64) configured[dev] = 1;
     }
+    if (p.st.whole) {  // nothing runs beside it
+        kern<<<(unsigned)ctas, C::kThreads, C::kSmem, stream>>>(tmK, tmK, tmV, p);
+        return cudaGetLastError();
+    }
     return launch_dependent(kern, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, stream, tmK, tmK,
                             tmV, p);
 }
 
 }  // namespace
 
-cudaError_t launch_shared_tc(const TcParams &p, int tiles, int64_t ctas, const CUtensorMap &tmK,
+int shared_tc_items(int tiles) { return shared_items(tiles); }
+
+cudaError_t launch_shared_tc(const TcParams &p, int64_t ctas, const CUtensorMap &tmK,
                              const CUtensorMap &tmV, cudaStream_t stream) {
+    const bool pair = p.st.tile_rows == 2 * BM;
     if (p.D == 64)
-        return tiles == 2 ? launch_shared_instance<2, 64>(p, ctas, tmK, tmV, stream)
-                          : launch_shared_instance<1, 64>(p, ctas, tmK, tmV, stream);
-    return tiles == 2 ? launch_shared_instance<2, 128>(p, ctas, tmK, tmV, stream)
-                      : launch_shared_instance<1, 128>(p, ctas, tmK, tmV, stream);
+        return pair ? launch_shared_instance<2, 64>(p, ctas, tmK, tmV, stream)
+                    : launch_shared_instance<1, 64>(p, ctas, tmK, tmV, stream);
+    return pair ? launch_shared_instance<2, 128>(p, ctas, tmK, tmV, stream)
+                : launch_shared_instance<1, 128>(p, ctas, tmK, tmV, stream);
 }
 
 cudaError_t launch_fmha_tc(const TcParams &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,

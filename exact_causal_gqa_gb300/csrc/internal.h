@@ -129,15 +129,43 @@ struct MergeParams {
     int32_t warps_per_row;  // set by launch_merge
 };
 
+// The tiles of a call with shared prefixes on the tensor cores, cut evenly among CTAs
+// (shared_prefix.cuh).  Arrays in the workspace, written by the plan kernel.
+struct SharedStream {
+    // by the host
+    const int32_t *prefix_table, *prefix_lens, *group_starts;
+    int32_t n_groups, max_prefix_pages;
+    int32_t whole;       // 0: units are groups, their prefixes alone; 1: units are sequences,
+                         // their prefix and their own keys
+    int32_t units;       // n_groups or batch
+    int32_t tile_rows;   // rows of a CTA's tiles: 128 or 256
+    int32_t max_items;   // (tile, key range) pieces of one CTA at most
+    int32_t max_states;  // CTAs that a tile may be cut among at most
+    int32_t sms;
+    // by the plan kernel
+    int32_t *head;       // [4]: blocks of a CTA, blocks of all, 1 if the groups are out of range
+    int32_t *first;      // [units + 1] blocks of the units before
+    int32_t *tiles;      // [units] tiles of one kv head
+    int32_t *blocks;     // [units] blocks of a tile; -1: out of range, its rows are NaN
+    int32_t *weight;     // [units] blocks that a tile counts for (short ones count for more)
+    int32_t *rows;       // [units] rows of one kv head
+    int32_t *group;      // [batch] the sequence's group, or -1
+    int32_t *before;     // [batch + 1] rows of one kv head of the sequences before
+    int32_t *list;       // ragged groups: [batch * G * q_len] the rows (of kv head 0), or null
+};
+
 // The same with the splits of the sequence's shared prefix (shared_prefix.cu) as further
 // states of each row.
 struct SharedMergeParams : MergeParams {
     const int32_t *group_starts;  // [n_groups + 1]
     const int32_t *prefix_lens;   // [n_groups]
     int32_t n_groups, max_prefix;
-    int32_t pre_chunk, n_pre;     // keys per split, splits of the longest prefix
+    int32_t pre_chunk, n_pre;     // keys per split, splits of the longest prefix (pre_chunk 0:
+                                  // the tiles of st, n_pre states at most)
     const float *pre_acc;         // [B*Hq*q_len][n_pre][D]
     const float *pre_ml;          // [B*Hq*q_len][n_pre][2]
+    int32_t G;
+    SharedStream st;
 };
 
 // Tensor-core (tcgen05 / TMEM) path for many query rows per (sequence, kv head):
@@ -172,12 +200,13 @@ struct TcParams {
     float *ws_acc, *ws_ml;
     uint32_t *status;
     int32_t sms;         // SM count (sizes the persistent prefill grid)
-    // Prefixes shared by groups of sequences (split mode; shared_prefix.cuh): page_table,
-    // seq_lens and max_pages are the prefixes', one row for each group, the tiles' rows
-    // those of all of a group's sequences.
+    // Prefixes shared by groups of sequences.  fp32 (split mode): page_table, seq_lens and
+    // max_pages are the prefixes', one row for each group, the tiles' rows those of all of a
+    // group's sequences; bf16: the tiles of st.
     const int32_t *group_starts;  // [n_groups + 1] first sequences, or null
     int32_t n_groups;
     const void *q;                // read row by row there (no tensor map)
+    SharedStream st;
 };
 
 // Paged KV append (kv_append.cu).
@@ -192,9 +221,13 @@ cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream);
 
 cudaError_t launch_fmha_tc(const TcParams &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,
                            const CUtensorMap &tmV, cudaStream_t stream);
-// The splits of shared prefixes, `ctas` of them at most, with `tiles` (1 or 2; fp32: 1)
-// query tiles to a CTA.
-cudaError_t launch_shared_tc(const TcParams &p, int tiles, int64_t ctas, const CUtensorMap &tmK,
+// The tiles of p.st (bf16; with st.whole the call's output, else partial states and a
+// dependent of the launch before), or the splits of shared prefixes, `ctas` of them at most.
+// p.st's arrays, one CTA; and the output rows of the tiles that are cut (st.whole).
+cudaError_t launch_shared_plan(const TcParams &p, cudaStream_t stream);
+cudaError_t launch_shared_cut_merge(const TcParams &p, int64_t ctas, cudaStream_t stream);
+int shared_tc_items(int tiles);  // st.max_items for that many tiles of 128 rows to a CTA
+cudaError_t launch_shared_tc(const TcParams &p, int64_t ctas, const CUtensorMap &tmK,
                              const CUtensorMap &tmV, cudaStream_t stream);
 cudaError_t launch_shared_tc_f32(const TcParams &p, int64_t ctas, const CUtensorMap &tmK,
                                  const CUtensorMap &tmV, cudaStream_t stream);

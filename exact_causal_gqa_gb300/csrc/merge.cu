@@ -51,6 +51,21 @@ __device__ int prefix_splits(const SharedMergeParams &p, int b) {
     return splits;
 }
 
+// The same where the prefixes are tiles of the line that p.st says (shared_prefix.cuh): the
+// states of the tile that row i of head h of sequence b is in.
+__device__ int tile_states(const SharedMergeParams &p, int b, int h, int i, int qn) {
+    const SharedStream &st = p.st;
+    if (st.head[2]) return -1;
+    const int u = st.group[b];
+    if (u < 0) return 0;
+    const int nb = st.blocks[u];
+    if (nb <= 0 || qn <= 0 || i >= qn) return nb < 0 ? -1 : 0;
+    const int f = st.before[b] - st.before[st.group_starts[u]] + h % p.G * qn + i;
+    const int first = st.first[u] + (h / p.G * st.tiles[u] + f / st.tile_rows) * st.weight[u];
+    const int per = st.head[0];
+    return (first + nb - 1) / per - first / per + 1;
+}
+
 template <int D, typename Params>
 __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const Params p) {
     // a call with shared prefixes: their splits follow the sequence's own
@@ -68,7 +83,8 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const Params p) {
     const int L = active ? p.seq_lens[b] : 0;
     const int qn = !active ? 0 : p.q_lens ? p.q_lens[b] : p.q_len;  // ragged: rows of b
     int n_pre = 0;
-    if constexpr (kShared) n_pre = active ? prefix_splits(p, b) : 0;
+    if constexpr (kShared)
+        n_pre = !active ? 0 : p.pre_chunk ? prefix_splits(p, b) : tile_states(p, b, bh - b * p.Hq, i, qn);
     const bool bad_len = qn < 0 || qn > p.q_len || L < p.row_step * qn || L > p.max_pages * p.P ||
                          (p.require_full && L != qn) || n_pre < 0;
     if (!bad_len && i >= qn) active = false;  // padding row: not a query, not written

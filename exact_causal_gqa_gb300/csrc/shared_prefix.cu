@@ -11,6 +11,9 @@
 //     of one sequence, the tensor-core kernels take the prefixes with 128 or 256 of a group's
 //     rows to a CTA (shared_prefix.cuh).  They are launched as a dependent of the own splits,
 //     whose results they do not need: their CTAs take the SMs as those leave them.
+// bf16 sequences whose rows fill tiles by themselves have no use for a gather.  Their tiles walk
+// the prefix's blocks and go on with the sequence's own, in one launch, and write the output;
+// only tiles that a cut between two CTAs goes through are merged.
 #include "internal.h"
 #include "atlas_shared.h"
 
@@ -27,12 +30,18 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 struct SharedPlan {
     Plan own;
     bool split;            // the split kernels, in one launch
+    bool whole, stream;    // bf16 on the tensor cores: whole tiles, or the prefixes' (both: stream)
     int tiles;             // tensor cores: query tiles to a CTA; split kernels: columns
-    int chunk, n_pre;      // keys per prefix split, splits of the longest prefix
-    int64_t ctas;          // most (group, kv head, split, rows of a CTA) items
-    size_t acc_at, ml_at;  // the prefixes' states in the workspace
+    int chunk, n_pre;      // keys per prefix split, splits of the longest prefix (stream: states
+                           // of a tile at most)
+    int64_t ctas;          // most (group, kv head, split, rows of a CTA) items, or CTAs
+    size_t acc_at, ml_at;  // the prefixes' states in the workspace (whole: the cut tiles')
+    size_t plan_at;        // stream: its arrays
     size_t bytes;
 };
+
+// Rows of one sequence and kv head from which its tiles are its own.
+constexpr int64_t kWholeRows = 128;
 
 // Whether the split kernels take less time: the prefix once for each CTA's rows, against a
 // second launch's start and the prefix once.
@@ -69,11 +78,40 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
                                     4.0 * D * rows * Hkv * max_prefix, f32);
     if (few && (L->debug_flags & ATLAS_DEBUG_SHARED_SPLIT)) plan->split = true;
     if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->split = false;
-    plan->tiles = plan->split ? cols : !f32 && group_rows > 128 ? 2 : 1;
+    const int64_t seq_rows = (int64_t)G * L->q_len;
+    plan->stream = !f32 && !plan->split;
+    plan->whole = plan->stream && seq_rows >= kWholeRows && L->split_tokens == 0;
+    if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->whole = false;
+    if (L->debug_flags & ATLAS_DEBUG_SHARED_WHOLE) plan->whole = plan->stream;
+    const int64_t tile_of = plan->whole ? seq_rows : group_rows;
+    plan->tiles = plan->split ? cols : !f32 && tile_of > 128 ? 2 : 1;
     // CTAs of one split: a group's last may be partly filled
     const int64_t cta_rows = plan->split ? cols : 128 * plan->tiles;
-    const int64_t units = (rows / cta_rows + S->n_groups) * Hkv;
+    const int64_t units = (plan->whole ? L->batch * ((seq_rows + cta_rows - 1) / cta_rows)
+                                       : rows / cta_rows + S->n_groups) * Hkv;
     const int64_t likely = std::max<int64_t>((rows + cta_rows - 1) / cta_rows, S->n_groups) * Hkv;
+    const int64_t out_rows = (int64_t)L->batch * Hq * L->q_len;
+    plan->acc_at = plan->whole ? 0 : (size_t)round_up((int64_t)plan->own.ws_bytes, 256);
+    if (plan->stream) {
+        // At most this many states of a tile: what the likely number of tiles leaves to each,
+        // and some more where groups are uneven.
+        const int64_t blocks = (max_prefix + 127) / 128 +
+                               (plan->whole ? ((int64_t)L->max_pages_per_seq * P + 127) / 128 : 0);
+        if (L->split_tokens > 0) plan->n_pre = (int)((max_prefix + L->split_tokens - 1) / L->split_tokens + 2);
+        else plan->n_pre = (int)std::min<int64_t>(blocks / 4 + 3, sms / likely + 6);
+        plan->chunk = 0;
+        // (short tiles that count as more blocks make for more CTAs than SMs)
+        plan->ctas = sms + units / 15 + 2;
+        if ((double)units * (double)blocks * (1.0 + (double)units / (sms * 30.0)) + 1e6 >= INT32_MAX)
+            return ATLAS_ERR_UNSUPPORTED;  // (the line of blocks is counted in 32 bits)
+        const int64_t states = plan->whole ? plan->ctas * 2 * cta_rows : out_rows * plan->n_pre;
+        plan->ml_at = plan->acc_at + (size_t)round_up(states * D * 4, 256);
+        plan->plan_at = plan->ml_at + (size_t)round_up(states * 8, 256);
+        const int64_t n = plan->whole ? L->batch : S->n_groups;
+        plan->bytes = plan->plan_at + 4 * (size_t)(4 + 5 * n + 1 + 2 * (int64_t)L->batch + 1 +
+                                                   (plan->whole ? 0 : rows));
+        return ATLAS_OK;
+    }
     int64_t chunk = round_up(L->split_tokens, 128);
     if (chunk == 0 && plan->split) {
         chunk = round_up((max_prefix * likely + sms * 4 - 1) / (sms * 4), 128);
@@ -91,8 +129,6 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
         plan->ctas += (int64_t)plan->own.n_chunks * Hkv * plan->own.col_tiles * L->batch;
     }
     if (plan->ctas >= INT32_MAX) return ATLAS_ERR_UNSUPPORTED;
-    const int64_t out_rows = (int64_t)L->batch * Hq * L->q_len;
-    plan->acc_at = (size_t)round_up((int64_t)plan->own.ws_bytes, 256);
     plan->ml_at = plan->acc_at + (size_t)round_up(out_rows * plan->n_pre * D * 4, 256);
     plan->bytes = plan->ml_at + (size_t)out_rows * plan->n_pre * 8;
     return ATLAS_OK;
@@ -151,19 +187,92 @@ cudaError_t launch_split(const SharedPlan &plan, const void *q, const void *k_pa
     return launch_shared_split_bf16(p, plan.ctas, tmK, tmV, stream);
 }
 
+// The tensor-core kernels' view of a call.
+atlas_status tc_params(const SharedPlan &plan, const void *q, const void *k_pages,
+                       const void *v_pages, int32_t Hq, int32_t Hkv, int32_t D, int32_t P,
+                       float scale, const atlas_launch *L, float *acc, float *ml, TcParams *tp,
+                       CUtensorMap *tmK, CUtensorMap *tmV) {
+    const bool f32 = L->kv_dtype == ATLAS_F32;
+    const int bn = f32 ? 64 : 128;  // keys per block of the kernel
+    atlas_status st = encode_rows_map(tmK, k_pages, (int64_t)L->num_pages * Hkv * P, D, std::min(P, bn), f32);
+    if (st == ATLAS_OK)
+        st = encode_rows_map(tmV, v_pages, (int64_t)L->num_pages * Hkv * P, D, std::min(P, bn), f32);
+    tp->B = L->batch;
+    tp->Hq = Hq;
+    tp->Hkv = Hkv;
+    tp->G = Hq / Hkv;
+    tp->D = D;
+    tp->P = P;
+    tp->q_len = L->q_len;
+    tp->num_pages = L->num_pages;
+    tp->split = 1;
+    tp->row_step = 1;
+    tp->chunk = plan.chunk;
+    tp->n_chunks = plan.n_pre;
+    tp->hilo_below = plan.tiles == 1 ? INT32_MAX : hilo_below(scale, D);
+    tp->negate_scores = scale < 0.f;
+    tp->scale_log2 = fabsf(scale) * kLog2e;
+    tp->softcap_log2 = L->softcap > 0.f ? L->softcap * kLog2e : 0.f;
+    tp->softcap_inv = L->softcap > 0.f ? fabsf(scale) / L->softcap : 0.f;
+    tp->sinks = L->sinks;
+    tp->q_lens = L->q_lens;
+    tp->out = L->out;
+    tp->out_bf16 = L->out_dtype == ATLAS_BF16;
+    tp->lse = L->lse;
+    tp->ws_acc = acc;
+    tp->ws_ml = ml;
+    tp->status = L->status_word;
+    tp->q = q;
+    return st;
+}
+
+// The arrays of a stream, in the workspace.
+SharedStream stream_arrays(const SharedPlan &plan, int32_t G, const atlas_shared *S, const atlas_launch *L) {
+    SharedStream st{};
+    st.prefix_table = S->prefix_table;
+    st.prefix_lens = S->prefix_lens;
+    st.group_starts = S->group_starts;
+    st.n_groups = S->n_groups;
+    st.max_prefix_pages = S->max_prefix_pages;
+    st.whole = plan.whole;
+    st.units = plan.whole ? L->batch : S->n_groups;
+    st.tile_rows = 128 * plan.tiles;
+    st.max_items = shared_tc_items(plan.tiles);
+    st.max_states = plan.n_pre;
+    st.sms = L->sm_count > 0 ? L->sm_count : device_sm_count();
+    int32_t *at = reinterpret_cast<int32_t *>(static_cast<char *>(L->workspace) + plan.plan_at);
+    auto take = [&](int64_t n) {
+        int32_t *x = at;
+        at += n;
+        return x;
+    };
+    st.head = take(4);
+    st.first = take(st.units + 1);
+    st.tiles = take(st.units);
+    st.blocks = take(st.units);
+    st.weight = take(st.units);
+    st.rows = take(st.units);
+    st.group = take(L->batch);
+    st.before = take(L->batch + 1);
+    st.list = !plan.whole && L->q_lens ? take((int64_t)L->batch * G * L->q_len) : nullptr;
+    return st;
+}
+
 // The own splits, then the prefixes' on the tensor cores.
 atlas_status launch_tc(const SharedPlan &plan, const void *q, const void *k_pages,
                        const void *v_pages, const int32_t *page_table, const int32_t *seq_lens,
                        int32_t Hq, int32_t Hkv, int32_t D, int32_t P, float scale,
                        const atlas_shared *S, const atlas_launch *L, float *pre_acc, float *pre_ml) {
-    const bool f32 = L->kv_dtype == ATLAS_F32;
-    const int bn = f32 ? 64 : 128;  // keys per block of the kernel
     CUtensorMap tmK, tmV;
-    atlas_status st = encode_rows_map(&tmK, k_pages, (int64_t)L->num_pages * Hkv * P, D, std::min(P, bn), f32);
-    if (st == ATLAS_OK)
-        st = encode_rows_map(&tmV, v_pages, (int64_t)L->num_pages * Hkv * P, D, std::min(P, bn), f32);
+    TcParams tp{};
+    atlas_status st = tc_params(plan, q, k_pages, v_pages, Hq, Hkv, D, P, scale, L, pre_acc, pre_ml,
+                                &tp, &tmK, &tmV);
     if (st != ATLAS_OK) return st;
-
+    cudaStream_t stream = static_cast<cudaStream_t>(L->stream);
+    if (plan.stream) {
+        tp.st = stream_arrays(plan, Hq / Hkv, S, L);
+        if (launch_shared_plan(tp, stream) != cudaSuccess) return ATLAS_ERR_CUDA;
+    }
     atlas_launch own = *L;
     own.phase = ATLAS_PHASE_CHUNKS;
     own.debug_flags &= ~ATLAS_DEBUG_TC_DIRECT;
@@ -172,38 +281,37 @@ atlas_status launch_tc(const SharedPlan &plan, const void *q, const void *k_page
     st = run_attention(ATLAS_KIND_SUFFIX, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P,
                        scale, &own);
     if (st != ATLAS_OK) return st;
-
-    TcParams tp{};
+    if (plan.stream) return launch_shared_tc(tp, plan.ctas, tmK, tmV, stream) == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
     tp.page_table = S->prefix_table;
     tp.seq_lens = S->prefix_lens;
-    tp.B = L->batch;
-    tp.Hq = Hq;
-    tp.Hkv = Hkv;
-    tp.G = Hq / Hkv;
-    tp.D = D;
-    tp.P = P;
-    tp.q_len = L->q_len;
     tp.max_pages = S->max_prefix_pages;
-    tp.num_pages = L->num_pages;
-    tp.split = 1;
-    tp.chunk = plan.chunk;
-    tp.n_chunks = plan.n_pre;
-    tp.hilo_below = plan.tiles == 1 ? INT32_MAX : hilo_below(scale, D);
-    tp.negate_scores = scale < 0.f;
-    tp.scale_log2 = fabsf(scale) * kLog2e;
-    tp.softcap_log2 = L->softcap > 0.f ? L->softcap * kLog2e : 0.f;
-    tp.softcap_inv = L->softcap > 0.f ? fabsf(scale) / L->softcap : 0.f;
-    tp.q_lens = L->q_lens;
-    tp.ws_acc = pre_acc;
-    tp.ws_ml = pre_ml;
-    tp.status = L->status_word;
     tp.group_starts = S->group_starts;
     tp.n_groups = S->n_groups;
-    tp.q = q;
+    return launch_shared_tc_f32(tp, plan.ctas, tmK, tmV, stream) == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
+}
+
+// Whole tiles: the prefixes and the sequences' own keys, the output, and the merge of what is cut.
+atlas_status launch_whole(const SharedPlan &plan, const void *q, const void *k_pages,
+                          const void *v_pages, const int32_t *page_table, const int32_t *seq_lens,
+                          int32_t Hq, int32_t Hkv, int32_t D, int32_t P, float scale,
+                          const atlas_shared *S, const atlas_launch *L, float *acc, float *ml,
+                          cudaEvent_t between) {
+    CUtensorMap tmK, tmV;
+    TcParams tp{};
+    const atlas_status st = tc_params(plan, q, k_pages, v_pages, Hq, Hkv, D, P, scale, L, acc, ml, &tp,
+                                      &tmK, &tmV);
+    if (st != ATLAS_OK) return st;
+    tp.page_table = page_table;
+    tp.seq_lens = seq_lens;
+    tp.max_pages = L->max_pages_per_seq;
+    tp.st = stream_arrays(plan, Hq / Hkv, S, L);
     cudaStream_t stream = static_cast<cudaStream_t>(L->stream);
-    const cudaError_t err = f32 ? launch_shared_tc_f32(tp, plan.ctas, tmK, tmV, stream)
-                                : launch_shared_tc(tp, plan.tiles, plan.ctas, tmK, tmV, stream);
-    return err == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
+    if (launch_shared_plan(tp, stream) != cudaSuccess ||
+        launch_shared_tc(tp, plan.ctas, tmK, tmV, stream) != cudaSuccess ||
+        (between && cudaEventRecord(between, stream) != cudaSuccess) ||
+        launch_shared_cut_merge(tp, plan.ctas, stream) != cudaSuccess)
+        return ATLAS_ERR_CUDA;
+    return ATLAS_OK;
 }
 
 }  // namespace
@@ -249,6 +357,13 @@ extern "C" atlas_status atlas_attn_shared(const void *q, const void *k_pages, co
     if (ev[0] && cudaEventRecord(ev[0], stream) != cudaSuccess) return ATLAS_ERR_CUDA;
     float *pre_acc = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.acc_at);
     float *pre_ml = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.ml_at);
+    if (plan.whole) {
+        st = launch_whole(plan, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P, scale, S, L,
+                          pre_acc, pre_ml, ev[1]);
+        if (st != ATLAS_OK) return st;
+        if (ev[2] && cudaEventRecord(ev[2], stream) != cudaSuccess) return ATLAS_ERR_CUDA;
+        return ATLAS_OK;
+    }
     if (plan.split) {
         if (launch_split(plan, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P, scale, S, L,
                          pre_acc, pre_ml) != cudaSuccess)
@@ -287,6 +402,8 @@ extern "C" atlas_status atlas_attn_shared(const void *q, const void *k_pages, co
     mp.n_pre = plan.n_pre;
     mp.pre_acc = pre_acc;
     mp.pre_ml = pre_ml;
+    mp.G = Hq / Hkv;
+    if (plan.stream) mp.st = stream_arrays(plan, mp.G, S, L);
     if (launch_shared_merge(mp, stream) != cudaSuccess) return ATLAS_ERR_CUDA;
     if (ev[2] && cudaEventRecord(ev[2], stream) != cudaSuccess) return ATLAS_ERR_CUDA;
     return ATLAS_OK;

@@ -98,6 +98,121 @@ __device__ __forceinline__ bool shared_real(const Params &p, int seq0, int rows,
     return !p.q_lens || (f - s * per) % p.q_len < p.q_lens[seq0 + s];
 }
 
+// ---------------------------------------------------------------- evenly cut tiles (bf16)
+// A unit -- a group with its prefix (st.whole 0), or a sequence with its prefix and its own keys
+// (1) -- has tiles of st.tile_rows rows for each kv head, and a tile has 128-key blocks: the
+// prefix's, the last of them perhaps in part, then the sequence's own.  All blocks of all tiles
+// stand in one line, tile after tile, and CTA x takes blocks [x n, (x + 1) n) of it, n chosen so
+// that every SM gets one CTA: whatever the lengths, all end together.  A tile that is cut leaves
+// partial states of its rows, one for each CTA that has blocks of it.
+
+// A CTA's piece of a tile.
+struct SharedSeg {
+    int unit, hkv, row0;   // the tile's first row (of the unit's, in one kv head)
+    int rows;              // the unit's rows
+    int blk0, nb;          // blocks [blk0, blk0 + nb) of the tile
+    int state;             // index of its partial state; -1: the tile is not cut
+    int len, own;          // keys of the prefix, own keys that the tile's rows see at most
+    int group;             // whose prefix (-1: none)
+};
+
+// Own keys (with st.whole) that a tile's rows see at most: rows are q heads times query rows.
+__device__ __forceinline__ int tile_own_keys(int seq_len, int qn, int row0, int row_end) {
+    const int last = row_end - 1;  // (the tile's last row)
+    const int i = last / qn != row0 / qn ? qn - 1 : last % qn;
+    return seq_len - qn + i + 1;
+}
+
+struct SharedTile {
+    int unit, hkv, tile, first;  // first: its first block in the line
+};
+
+// The tile that has a block of the line (a block before its end).  A whole warp calls this with
+// the same block; lane k looks at units k, k + 32, ...
+__device__ __forceinline__ SharedTile tile_of(const SharedStream &st, int block) {
+    SharedTile t{};
+    for (int u0 = 0; u0 < st.units; u0 += 32) {
+        const int u = u0 + (int)(threadIdx.x % 32);
+        const bool here = u < st.units && st.first[u] <= block && block < st.first[u + 1];
+        const unsigned who = __ballot_sync(0xffffffffu, here);
+        if (who) {
+            t.unit = u0 + __ffs(who) - 1;
+            break;
+        }
+    }
+    const int weight = st.weight[t.unit], tiles = st.tiles[t.unit];
+    const int at = (block - st.first[t.unit]) / weight;
+    t.hkv = at / tiles;
+    t.tile = at % tiles;
+    t.first = st.first[t.unit] + at * weight;
+    return t;
+}
+
+// Blocks of a tile that have keys for its rows.
+template <typename Params>
+__device__ __forceinline__ int tile_blocks(const Params &p, const SharedTile &t, SharedSeg &s) {
+    const SharedStream &st = p.st;
+    s.unit = t.unit;
+    s.hkv = t.hkv;
+    s.row0 = t.tile * st.tile_rows;
+    s.rows = st.rows[t.unit];
+    s.group = st.whole ? st.group[t.unit] : t.unit;
+    s.len = s.group >= 0 ? st.prefix_lens[s.group] : 0;
+    s.own = 0;
+    if (st.whole)
+        s.own = tile_own_keys(p.seq_lens[t.unit], p.q_lens ? p.q_lens[t.unit] : p.q_len, s.row0,
+                              min(s.row0 + st.tile_rows, s.rows));
+    return (s.len + 127) / 128 + (s.own + 127) / 128;
+}
+
+// The pieces of CTA `cta`: one warp calls this.  Returns their number.
+template <typename Params>
+__device__ inline int shared_segs(const Params &p, int cta, SharedSeg *segs) {
+    const SharedStream &st = p.st;
+    const int per = st.head[0], all = st.head[1];
+    if ((int64_t)cta * per >= all) return 0;
+    const int end = (int)min((int64_t)all, (int64_t)(cta + 1) * per);
+    int n = 0;
+    SharedTile t{};
+    bool any = false;
+    for (int s = cta * per; s < end && n < st.max_items;) {
+        if (!any || s >= st.first[t.unit + 1]) {
+            t = tile_of(st, s);
+        } else {  // the next of the same unit
+            t.first = s;
+            if (++t.tile == st.tiles[t.unit]) {
+                t.tile = 0;
+                ++t.hkv;
+            }
+        }
+        any = true;
+        SharedSeg g;
+        const int nb = tile_blocks(p, t, g), stop = min(end, t.first + st.weight[t.unit]);
+        g.blk0 = s - t.first;
+        g.nb = min(stop - t.first, nb) - g.blk0;
+        g.state = t.first / per == (t.first + nb - 1) / per && st.whole ? -1 : cta - t.first / per;
+        if (g.nb > 0) {
+            if (threadIdx.x % 32 == 0) segs[n] = g;
+            ++n;
+        }
+        s = stop;
+    }
+    return n;
+}
+
+// Output row of row f of a unit.
+template <typename Params>
+__device__ __forceinline__ int64_t unit_row(const Params &p, int unit, int hkv, int f) {
+    const SharedStream &st = p.st;
+    if (st.whole) {
+        const int qn = p.q_lens ? p.q_lens[unit] : p.q_len, g = f / qn;
+        return ((int64_t)unit * p.Hq + hkv * p.G + g) * p.q_len + (f - g * qn);
+    }
+    const int seq0 = st.group_starts[unit];
+    if (st.list) return (int64_t)st.list[st.before[seq0] + f] + (int64_t)hkv * p.G * p.q_len;
+    return shared_row(p, seq0, hkv, f);
+}
+
 // A launch that may start as soon as every CTA of the grid before it in the stream has
 // started or ended.
 template <typename... Args>

@@ -1,0 +1,262 @@
+// shared_stream.cu -- the line of blocks that a call with shared prefixes is cut into
+// (shared_prefix.cuh): the plan kernel, which works it out on the device from the groups and
+// lengths, and the merge of the tiles that the cuts go through.
+#include "internal.h"
+#include "ptx.cuh"
+#include "shared_prefix.cuh"
+
+#include <math.h>
+
+namespace atlas {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kMinBlocks = 4;  // blocks of a CTA at least: below, its start outweighs them
+
+// Inclusive sums of x over the CTA, and the total.
+__device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t &total) {
+    __shared__ int64_t sums[kPlanThreads / 32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int64_t a = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += a;
+    }
+    __syncthreads();  // (the sums of the scan before this one have been read)
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t s = sums[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t a = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += a;
+        }
+        sums[lane] = s;
+    }
+    __syncthreads();
+    total = sums[kPlanThreads / 32 - 1];
+    return x + (warp ? sums[warp - 1] : 0);
+}
+
+__device__ __forceinline__ int plan_max(int x) {
+    __shared__ int most;
+    if (threadIdx.x == 0) most = 0;
+    __syncthreads();
+    x = __reduce_max_sync(0xffffffffu, x);
+    if (threadIdx.x % 32 == 0) atomicMax(&most, x);
+    __syncthreads();
+    return most;
+}
+
+// One CTA: a few arrays of a few hundred entries, 2 to 3 us, before the kernels that read them.
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParams p) {
+    const SharedStream &st = p.st;
+    const int tid = (int)threadIdx.x;
+    bool wrong = false;
+    for (int n = tid; n < st.n_groups; n += kPlanThreads) {
+        const int a = st.group_starts[n], z = st.group_starts[n + 1];
+        wrong |= a < 0 || z < a || z > p.B;
+    }
+    const bool bad = __syncthreads_or(wrong) != 0;
+    uint32_t flags = bad ? ATLAS_DEV_BAD_SEQLEN : 0u;
+
+    // sequences: their groups, and the rows before them
+    int64_t carry = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        int rows = 0;
+        if (b < p.B) {
+            int group = -1;
+            if (!bad) {
+                int lo = -1, hi = st.n_groups - 1;  // the last group that starts at b or before
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) / 2;
+                    if (st.group_starts[mid] <= b) lo = mid;
+                    else hi = mid - 1;
+                }
+                if (lo >= 0 && b < st.group_starts[lo + 1]) group = lo;
+            }
+            st.group[b] = group;
+            const int qn = p.q_lens ? p.q_lens[b] : p.q_len;
+            const int len = st.whole ? p.seq_lens[b] : 0;
+            bool good = qn >= 0 && qn <= p.q_len && !bad;
+            if (st.whole) {
+                int pre = 0;
+                if (group >= 0) {
+                    pre = st.prefix_lens[group];
+                    good = good && pre >= 0 && pre <= st.max_prefix_pages * p.P;
+                }
+                good = good && len >= qn && len <= p.max_pages * p.P;
+                st.blocks[b] = good ? (pre + 127) / 128 + (len + 127) / 128 : -1;
+                if (!good) flags |= ATLAS_DEV_BAD_SEQLEN;
+            }
+            rows = good ? p.G * qn : 0;
+            if (st.whole) st.rows[b] = rows;
+            // (the rows of a group, head after head of one query's: the merge counts alike)
+        }
+        int64_t total;
+        const int64_t upto = plan_scan(rows, total);
+        if (b < p.B) st.before[b] = (int)(carry + upto - rows);
+        carry += total;
+    }
+    if (tid == 0) st.before[p.B] = (int)carry;
+    __syncthreads();
+
+    // units: their tiles, and what all of them have
+    int most = 0;
+    int64_t all = 0;
+    for (int u0 = 0; u0 < st.units; u0 += kPlanThreads) {
+        const int u = u0 + tid;
+        int64_t blocks = 0;
+        if (u < st.units) {
+            if (!st.whole) {
+                const int len = st.prefix_lens[u];
+                const bool good = len >= 0 && len <= st.max_prefix_pages * p.P && !bad;
+                if (!good) flags |= ATLAS_DEV_BAD_SEQLEN;
+                st.rows[u] = good ? st.before[st.group_starts[u + 1]] - st.before[st.group_starts[u]] : 0;
+                st.blocks[u] = good ? (len + 127) / 128 : -1;
+            }
+            const int tiles = (st.rows[u] + st.tile_rows - 1) / st.tile_rows;
+            st.tiles[u] = tiles;
+            const int nb = max(st.blocks[u], 0);
+            if (tiles > 0) most = max(most, nb);
+            blocks = (int64_t)tiles * p.Hkv * nb;
+        }
+        int64_t total;
+        plan_scan(blocks, total);
+        all += total;
+    }
+    most = plan_max(most);
+    // Blocks of a CTA: one CTA for each SM, few enough states of a tile, and few enough pieces of
+    // a CTA, for which short tiles count as more blocks than they have.
+    int64_t per = (all + st.sms - 1) / st.sms;
+    per = max(per, (int64_t)kMinBlocks);
+    per = max(per, (int64_t)((most + st.max_states - 3) / (st.max_states - 2)));
+    const int least = (int)((per + st.max_items - 3) / (st.max_items - 2));
+    carry = 0;
+    for (int u0 = 0; u0 < st.units; u0 += kPlanThreads) {
+        const int u = u0 + tid;
+        int64_t blocks = 0;
+        if (u < st.units) {
+            const int nb = st.blocks[u] > 0 && st.tiles[u] > 0 ? max(st.blocks[u], least) : 0;
+            st.weight[u] = max(nb, 1);
+            blocks = (int64_t)st.tiles[u] * p.Hkv * nb;
+        }
+        int64_t total;
+        const int64_t upto = plan_scan(blocks, total);
+        if (u < st.units) st.first[u] = (int)(carry + upto - blocks);
+        carry += total;
+    }
+    if (tid == 0) {
+        st.first[st.units] = (int)carry;
+        st.head[0] = (int)per;
+        st.head[1] = (int)carry;
+        st.head[2] = bad;
+    }
+    if (flags && p.status) atomicOr(p.status, flags);
+
+    // ragged groups: their rows one after the other, no padding between
+    if (st.list && p.q_lens) {
+        const int lane = tid % 32;
+        for (int b = tid / 32; b < p.B; b += kPlanThreads / 32) {
+            const int at = st.before[b], rows = st.before[b + 1] - at;
+            const int qn = rows / p.G;
+            for (int r = lane; r < rows; r += 32) {
+                const int g = r / qn;
+                st.list[at + r] = (b * p.Hq + g) * p.q_len + (r - g * qn);
+            }
+        }
+    }
+}
+
+// The tiles that are cut (st.whole): the CTA's share of the rows of the tile that the line's
+// cut before block x n goes through, if that is the tile's first cut; and NaN for the sequences
+// that are out of range.
+constexpr int kCutWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kCutWarps * 32) shared_cut_merge_kernel(const TcParams p, int ctas) {
+    constexpr int E = D / 32;
+    const SharedStream &st = p.st;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    wait_for_previous_grid();
+    auto put = [&](int64_t row, const float (&o)[E], float lse) {
+        if (p.out_bf16) {
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; e += 2)
+                *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(o[e], o[e + 1]);
+        } else {
+            float *out = static_cast<float *>(p.out) + row * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; e += 2)
+                *reinterpret_cast<float2 *>(out + e) = make_float2(o[e], o[e + 1]);
+        }
+        if (lane == 0 && p.lse) p.lse[row] = lse;
+    };
+    if ((int)blockIdx.x >= ctas) {
+        const int b = (int)blockIdx.x - ctas;
+        if (st.blocks[b] >= 0) return;
+        const float nan = __int_as_float(0x7fc00000);
+        float o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = nan;
+        const int qn = p.q_lens ? p.q_lens[b] : p.q_len;
+        const int rows = qn >= 0 && qn <= p.q_len ? qn : p.q_len;
+        for (int64_t r = (int64_t)blockIdx.y * kCutWarps + warp; r < (int64_t)p.Hq * p.q_len;
+             r += (int64_t)gridDim.y * kCutWarps)
+            if (r % p.q_len < rows) put((int64_t)b * p.Hq * p.q_len + r, o, nan);
+        return;
+    }
+    const int per = st.head[0], x = (int)blockIdx.x + 1, block = x * per;
+    if ((int64_t)x * per >= st.head[1]) return;
+    const SharedTile t = tile_of(st, block);
+    if (t.first / per != x - 1 || t.first == block) return;  // not cut here first
+    SharedSeg s;
+    const int nb = tile_blocks(p, t, s);
+    const int states = (t.first + nb - 1) / per - (x - 1) + 1;
+    const int f = s.row0 + (int)blockIdx.y * kCutWarps + warp;
+    if (states < 2 || f >= s.rows) return;
+    // the first state is that of a tile's start, the others those of their CTAs' first pieces
+    auto slot = [&](int k) { return ((int64_t)(x - 1 + k) * 2 + (k == 0)) * st.tile_rows + f - s.row0; };
+    const int64_t row = unit_row(p, t.unit, t.hkv, f);
+    float M = p.sinks ? p.sinks[s.hkv * p.G + f / (s.rows / p.G)] * kLog2e : -INFINITY;
+    bool has_nan = isnan(M);
+    float sum = p.sinks ? 1.f : 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int k = 0; k < states; ++k) {
+        const float m = p.ws_ml[slot(k) * 2], l = p.ws_ml[slot(k) * 2 + 1];
+        if (isnan(m) || isnan(l)) has_nan = true;
+        if (!(l > 0.f)) continue;
+        const float top = fmaxf(M, m), old = M == -INFINITY ? 0.f : ex2(M - top), w = ex2(m - top);
+        const float *a = p.ws_acc + slot(k) * D + lane * E;
+        sum = fmaf(w, l, sum * old);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(w, a[e], o[e] * old);
+        M = top;
+    }
+    const float nan = __int_as_float(0x7fc00000);
+    const bool none = has_nan || M == -INFINITY;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = none ? nan : o[e] / sum;
+    put(row, o, none ? nan : kLn2 * (M + log2f(sum)));
+}
+
+}  // namespace
+
+cudaError_t launch_shared_plan(const TcParams &p, cudaStream_t stream) {
+    shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_shared_cut_merge(const TcParams &p, int64_t ctas, cudaStream_t stream) {
+    const dim3 grid((unsigned)(ctas + p.B), (unsigned)(p.st.tile_rows / kCutWarps));
+    return p.D == 128 ? launch_dependent(shared_cut_merge_kernel<128>, grid, dim3(kCutWarps * 32), 0,
+                                         stream, p, (int)ctas)
+                      : launch_dependent(shared_cut_merge_kernel<64>, grid, dim3(kCutWarps * 32), 0,
+                                         stream, p, (int)ctas);
+}
+
+}  // namespace atlas

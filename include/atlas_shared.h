@@ -29,6 +29,8 @@ extern "C" {
  * sequences' own keys (at most 16 rows to a sequence and kv head), or on the tensor-core one. */
 #define ATLAS_DEBUG_SHARED_SPLIT 4u
 #define ATLAS_DEBUG_SHARED_TC 8u
+/* ... (with it) bf16 sequences in tiles of their own, over the prefix and their own keys. */
+#define ATLAS_DEBUG_SHARED_WHOLE 16u
 
 /* The shared prefixes of a call: group n is the neighbouring sequences group_starts[n] <= b <
  * group_starts[n + 1], and their prefix the first prefix_lens[n] keys of prefix_table[n]. */

@@ -174,6 +174,13 @@ CASES = [
     ("f32", 6, 2, 128, 16, 5, [0, 2, 4], [0, 260], [5, 9, 30, 77], dict(ragged=[5, 1, 0, 3])),
     ("f32", 4, 2, 64, 128, 33, [0, 1, 2], [129, 65], [33, 300], dict(softcap=4.0, scale=-0.11)),
     ("f32", 8, 2, 128, 64, 1, [1, 2], [2100], [5, 70], dict(split_tokens=192)),
+    # more tiles than a CTA each: pieces that go on, are cut, and are whole
+    ("bf16", 8, 2, 128, 16, 1, [0, 30, 33, 64], [9000, 700, 3100], [1 + 7 * b % 90 for b in range(64)], {}),
+    ("bf16", 8, 8, 64, 64, 3, [0, 1, 100], [2000, 5000], [3 + b % 70 for b in range(100)], dict(ragged=[b % 4 for b in range(100)])),
+    ("bf16", 4, 2, 128, 32, 130, [0, 3, 5], [3000, 129], [130, 200, 700, 131, 2000], dict(sinks=True)),
+    ("bf16", 8, 8, 128, 16, 64, [0, 12], [4500], [64 + 9 * b for b in range(12)], dict(ragged=[64 - 5 * b for b in range(12)])),
+    ("bf16", 2, 2, 64, 8, 300, [0, 1, 2], [640, 9], [300, 411], dict(softcap=6.0)),
+    ("bf16", 40, 40, 64, 16, 1, list(range(0, 71, 2)), [1 + n % 3 for n in range(35)], [1 + b % 3 for b in range(70)], {}),
 ]
 
 
@@ -201,7 +208,8 @@ def check(x, dtype, scale, **opt):
 
 
 @gpu
-@pytest.mark.parametrize("path", [0, atlas.DEBUG_SHARED_SPLIT, atlas.DEBUG_SHARED_TC])
+@pytest.mark.parametrize("path", [0, atlas.DEBUG_SHARED_SPLIT, atlas.DEBUG_SHARED_TC,
+                                  atlas.DEBUG_SHARED_WHOLE | atlas.DEBUG_SHARED_TC])
 @pytest.mark.parametrize("dtype,Hq,Hkv,D,P,q_len,starts,pre,lens,opt", CASES)
 def test_matches_the_plain_form(dtype, Hq, Hkv, D, P, q_len, starts, pre, lens, opt, path):
     x = Case(dtype, Hq, Hkv, D, P, q_len, starts, pre, lens, 200 + q_len, opt.get("ragged"))
@@ -235,8 +243,8 @@ def test_the_order_of_the_groups_changes_no_bits():
 
 
 @gpu
-@pytest.mark.parametrize("dtype,q_len,path", [("bf16", 1, 4), ("bf16", 1, 8), ("bf16", 40, 0), ("f32", 1, 4),
-                                              ("f32", 1, 8), ("f32", 40, 0)])
+@pytest.mark.parametrize("dtype,q_len,path", [("bf16", 1, 4), ("bf16", 1, 8), ("bf16", 1, 24), ("bf16", 40, 8),
+                                              ("bf16", 40, 16), ("f32", 1, 4), ("f32", 1, 8), ("f32", 40, 0)])
 def test_bad_lengths_groups_and_pages_are_reported(dtype, q_len, path):
     x = Case(dtype, 8, 2, 64, 16, q_len, [0, 2, 4], [100, 70], [50, 41, 60, 77], 8)
     good = x(0.1, debug_flags=path)
