@@ -832,14 +832,15 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         auto copy_q = [&](const TcWork &w) {
             constexpr int kChunks = D / 8;  // 16-byte chunks of a row
             const uint32_t qt = sb + C::OFF_Q + x * kTileBytes;
-#pragma unroll 4
-            for (int k = lane; k < 32 * kChunks; k += 32) {
-                const int row = q4 * 32 + k / kChunks, ch = k % kChunks;
-                const int f = (w.t0 + x * w.tstep) * BM + row;
-                const bool in = f < w.rows_unit;
+            const int f = (w.t0 + x * w.tstep) * BM + r;
+            const int64_t mine = f < w.rows_unit ? row_of(w, f) : -1;  // (one lookup a lane)
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) {
+                const int at = k * (32 / kChunks) + lane / kChunks, ch = lane % kChunks;
+                const int64_t row = __shfl_sync(0xffffffffu, mine, at);
                 const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
-                                           row_of(w, in ? f : 0) * D + ch * 8;
-                cp_async16(qt + (ch / 8) * kSlab + sw128(row, ch % 8), src, in ? 16u : 0u);
+                                           (row < 0 ? 0 : row) * D + ch * 8;
+                cp_async16(qt + (ch / 8) * kSlab + sw128(q4 * 32 + at, ch % 8), src, row < 0 ? 0u : 16u);
             }
             cp_async_commit();
         };
@@ -848,7 +849,8 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             fence_proxy_async_smem();
             mbar_arrive(BAR(C::B_Q));
         };
-        int nq = 0;  // SHARED: items whose Q has been copied
+        int nq = 0;         // SHARED: items whose Q has been copied
+        bool last = false;  // SHARED: no item after this one
         if (SHARED) {
             int first = 0;
             while ((skip >> first) & 1) ++first;
@@ -1115,7 +1117,8 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             // last PV product and the epilogue are.
             int next = it + 1;
             while (next < n_items && ((skip >> next) & 1)) ++next;
-            if (ok && next < n_items) {
+            last = next == n_items;
+            if (ok && !last) {
                 ok = wait_warp(BAR(C::B_QEMPTY), (nq - 1) & 1, abort_flag);
                 if (ok) copy_q(item(next));
                 if (ok) ok = wait_warp(BAR(C::B_PVDONE + x), (g + nb - 1) & 1, abort_flag);
@@ -1156,7 +1159,9 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             // the other tile's last PV, whose V stage and P lie outside this tile's
             // staging area (tile 0: the Q tiles; tile 1: the V stages, written once its
             // own PV is done).
-            const bool wide = p.split || !p.out_bf16;  // fp32 rows, else bf16 rows
+            // (SHARED: only after the CTA's last item, where nothing lands any more.)
+            const bool staged = SHARED && last;
+            const bool wide = (SHARED ? part : p.split) || !p.out_bf16;  // fp32 rows, else bf16 rows
             const int rb = wide ? D * 4 : D * 2;       // bytes per output row
             const uint32_t stage = sb + (uint32_t)(x * 4 + q4) * (32u * D * 4u);
             const uint32_t my_row = stage + (uint32_t)lane * rb;
@@ -1165,7 +1170,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                 uint32_t o[32];
                 tmem_ld32(to + cc * 32, o);
                 tmem_wait_ld();
-                if (PERSIST) {
+                if (PERSIST && !staged) {
                     // The next item's Q and K/V are landing in shared memory: rows go
                     // straight from registers (direct mode), in 32-byte stores when the
                     // output allows (each fills a whole sector of its row).
@@ -1245,14 +1250,15 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             __syncwarp();
             // Byte offset of this thread's row in its destination, -1 for a row that
             // is not written.
-            uint8_t *const dst_base = p.split ? reinterpret_cast<uint8_t *>(p.ws_acc)
-                                              : static_cast<uint8_t *>(p.out);
-            const int64_t my_off = !valid ? -1 : (p.split ? slot : row) * (int64_t)rb;
+            const bool to_ws = SHARED ? part : p.split != 0;
+            uint8_t *const dst_base = to_ws ? reinterpret_cast<uint8_t *>(p.ws_acc)
+                                            : static_cast<uint8_t *>(p.out);
+            const int64_t my_off = !valid ? -1 : (to_ws ? slot : row) * (int64_t)rb;
             const int cpr = rb / 16;       // 16-byte chunks per row: 8, 16 or 32
             const int rpi = 32 / cpr;      // rows per store instruction
             const int ch = lane % cpr;     // this lane's chunk of its row
 #pragma unroll 1
-            for (int r0 = 0; r0 < 32 && !PERSIST; r0 += rpi) {
+            for (int r0 = 0; r0 < 32 && (!PERSIST || staged); r0 += rpi) {
                 const int r = r0 + lane / cpr;
                 const int64_t off = __shfl_sync(0xffffffffu, my_off, r);
                 const uint4 v = ld_shared_v4(stage + (uint32_t)(r * rb + ((ch ^ (r & 7)) * 16)));
