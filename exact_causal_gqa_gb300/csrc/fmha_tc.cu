@@ -62,7 +62,7 @@ constexpr int BM = 128;  // query rows per tile
 constexpr int BN = 128;  // keys per block
 constexpr int kMaxItems = 64;  // work items of one CTA in persistent mode
 // ... and with shared prefixes (what is left of shared memory)
-constexpr int shared_items(int tiles) { return tiles == 2 ? 48 : 32; }
+constexpr int shared_items(int tiles) { return tiles == 2 ? 40 : 32; }
 constexpr int kSlab = 128 * 128;  // one 64-element slab of a 128-row bf16 tile (128-byte rows)
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when the max grows 256x
@@ -135,7 +135,10 @@ struct Cfg {
                                              : kItemSlots * (int)sizeof(TcWork);
     static constexpr int OFF_MASK = OFF_VOTE + 16;  // [2] words: items with a bad page id
     static constexpr int OFF_ITEMS = OFF_MASK + 8;
-    static constexpr int kSmem = OFF_ITEMS + kItemBytes + 1024;  // + slack
+    // SHARED, two tiles: 32 rows x 128 bytes for each softmax warp's output on its way
+    static constexpr int OFF_STAGE = (OFF_ITEMS + kItemBytes + 127) / 128 * 128;
+    static constexpr int kStageBytes = SHARED && NT == 2 ? 8 * 4096 : 0;
+    static constexpr int kSmem = OFF_STAGE + kStageBytes + 1024;  // + slack
     static_assert(kSmem <= 232448, "shared memory budget");
     // TMEM columns: NT=2 -> [S0 | O0 | S1 | O1]; NT=1 -> [S(buf 0) | S(buf 1) | O]
     __device__ static constexpr uint32_t s_col(int x, int b) {
@@ -332,12 +335,14 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     int n_items = 1;
     TcWork w0{};
     SharedSeg *const segs = reinterpret_cast<SharedSeg *>(smem + C::OFF_ITEMS);
-    // The merge that follows a SHARED grid of prefixes reads the sequences' own splits too,
-    // which the grid before this one writes: one CTA at least must not end before that grid has.
+    // A SHARED grid follows the plan's, whose arrays it reads, or that of the sequences' own
+    // splits.  Then the merge behind it reads those too: one CTA at least must not end before
+    // that grid has.
     auto before_exit = [&]() {
-        if (SHARED && blockIdx.x == 0) wait_for_previous_grid();
+        if (SHARED && !p.st.wait_first && blockIdx.x == 0) wait_for_previous_grid();
     };
     if constexpr (SHARED) {
+        if (p.st.wait_first) wait_for_previous_grid();
         int *const count = reinterpret_cast<int *>(smem + C::OFF_FLAG);
         if (warp == 0) {
             const int n = shared_segs(p, blockIdx.x, segs);
@@ -428,6 +433,11 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             if (p.st.whole)
                 return ((int64_t)blockIdx.x * 2 + (w.blk0 == 0)) * p.st.tile_rows + f - w.t0 * BM;
         return row * p.n_chunks + w.c;
+    };
+    // SHARED: an item whose rows end in the first of its two tiles.  The second tile's part of
+    // tensor memory is then the first's second S buffer, as with one tile to a CTA.
+    auto single = [&](const TcWork &w) -> bool {
+        return SHARED && NT == 2 && (w.t0 + 1) * BM >= w.rows_unit;
     };
     // SHARED: keys of block j of an item, counted from the block's first key.
     auto block_keys = [&](const TcWork &w, int j) -> int {
@@ -644,13 +654,28 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             int g = 0;      // blocks of earlier items
             int nq = 0;     // items so far
             int ntail = 0;  // tail fix-ups so far
+            int g1 = 0, nq1 = 0;  // SHARED: the same of items with a second tile
             for (int it = 0; ok && it < n_items; ++it) {
                 if ((skip >> it) & 1) continue;
                 Item w = item(it);
                 const int nb = w.nb;
+                const bool one = single(w);
+                // (two compiled forms: with one tile of the item's pair, or as it stands)
+                auto run_item = [&](auto only) {
+                constexpr bool kOne = decltype(only)::value;
+                constexpr int kBufs = kOne ? 2 : SB, kTiles = kOne ? 1 : NT;
+                // S (and P) columns of block j of tile x, the barrier that says S is full, and
+                // the tile's blocks so far
+                auto s_at = [&](int j, int x) {
+                    return tmem + (kOne ? C::s_col(j & 1, 0) : C::s_col(x, (g + j) % SB));
+                };
+                auto full_at = [&](int j, int x) {
+                    return BAR(C::B_SFULL + (kOne ? (j & 1) : x * SB + (g + j) % SB));
+                };
+                auto blocks_of = [&](int x) { return SHARED && x > 0 ? g1 : g; };
                 ok = wait_warp(BAR(C::B_Q), nq & 1, abort_flag);
                 tc_fence_after();
-                if (!ok) break;
+                if (!ok) return;
                 // S_x(j) = Q_x K_j^T into S buffer (g + j) % SB of tile x.  Tile 0 waits
                 // for K_j; the last tile releases its stage, and after the item's last
                 // block also the Q tiles.
@@ -670,10 +695,10 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint32_t off = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
-                            umma_bf16(tmem + C::s_col(x, G % SB), qd + off, kd + off, idS, kk > 0);
+                            umma_bf16(s_at(j, x), qd + off, kd + off, idS, kk > 0);
                         }
-                        umma_commit(BAR(C::B_SFULL + x * SB + G % SB));
-                        if (x == NT - 1) {
+                        umma_commit(full_at(j, x));
+                        if (x == kTiles - 1) {
                             umma_commit(BAR(C::B_KEMPTY + s));
                             if (j == nb - 1) umma_commit(BAR(C::B_QEMPTY));
                         }
@@ -681,15 +706,17 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                     __syncwarp();
                     return true;
                 };
-                for (int j = 0; ok && j < min(SB, nb); ++j)
+                for (int j = 0; ok && j < min(kBufs, nb); ++j)
 #pragma unroll
                     for (int x = 0; x < NT; ++x)
-                        if (ok) ok = issue_s(j, x);
+                        if (ok && x < kTiles) ok = issue_s(j, x);
                 for (int j = 0; ok && j < nb; ++j) {
                     const int G = g + j, s = G % S;
 #pragma unroll
                     for (int x = 0; x < NT; ++x) {
-                        if (!wait_warp(BAR(C::B_PFULL + x), G & 1, abort_flag)) {
+                        if (x >= kTiles) break;
+                        const int Gx = blocks_of(x) + j;  // block count of this tile: its phases
+                        if (!wait_warp(BAR(C::B_PFULL + x), Gx & 1, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -712,15 +739,16 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                         }
                         // The item's first PV overwrites O: the previous item's
                         // epilogue must have read it out.
-                        if (j == 0 && nq > 0 &&
-                            !wait_warp(BAR(C::B_OFREE + x), (nq - 1) & 1, abort_flag)) {
+                        const int before = SHARED && x > 0 ? nq1 : nq;
+                        if (j == 0 && before > 0 &&
+                            !wait_warp(BAR(C::B_OFREE + x), (before - 1) & 1, abort_flag)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         const uint64_t vd =
                             sdesc_sw128(sb + C::OFF_V + s * kTileBytes, kSlab, 1024);
-                        const uint32_t pcol = tmem + C::s_col(x, G % SB);
+                        const uint32_t pcol = s_at(j, x);
                         // keys 16kk .. 16kk+15 of P sit in columns 32*(kk/2) + 8*(kk%2) ..
                         // +8, their remainders 16 columns further on.  V slice kk starts
                         // 2048 bytes (128 descriptor units) after slice kk-1.
@@ -739,7 +767,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                         // warps that did not ask for it unchanged: their lo columns hold
                         // no P.
                         const uint32_t vote = uniform(*reinterpret_cast<volatile uint32_t *>(
-                            smem + C::OFF_VOTE + (x * 2 + (G & 1)) * 4));
+                            smem + C::OFF_VOTE + (x * 2 + (Gx & 1)) * 4));
                         if (w.hilo || vote != 0u) {
                             uint32_t off_lanes[4];
 #pragma unroll
@@ -759,7 +787,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                         // it before S_x(j + SB) waits for its K block.
                         if (elect_one()) {
                             umma_commit(BAR(C::B_PVDONE + x));
-                            if (x == NT - 1) umma_commit(BAR(C::B_VEMPTY + s));
+                            if (x == kTiles - 1) umma_commit(BAR(C::B_VEMPTY + s));
                         }
                         __syncwarp();
                         // Ping-pong: S_x(j + SB) follows PV_x(j) at once, so tile x starts
@@ -767,14 +795,24 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                         // It writes the S buffer that PV_x(j) reads P_x(j) from; the
                         // tcgen05.mma operations of one thread run in issue order, so
                         // PV_x(j) has read its operand before S_x(j + SB) writes there.
-                        if (j + SB < nb && !issue_s(j + SB, x)) {
+                        if (j + kBufs < nb && !issue_s(j + kBufs, x)) {
                             ok = false;
                             break;
                         }
                     }
                 }
+                };
+                if (one) {
+                    if constexpr (SHARED && NT == 2) run_item(std::true_type{});
+                } else {
+                    run_item(std::false_type{});
+                }
                 g += nb;
                 ++nq;
+                if (!one) {
+                    g1 += nb;
+                    ++nq1;
+                }
             }
             if (!ok) {
                 failed = true;
@@ -860,6 +898,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         }
         bool ok = true;
         int g = 0;  // blocks of earlier items
+        int full[2] = {0, 0};  // SHARED: times that the S buffers have been filled
         int it = 0;
         for (; ok && it < n_items; ++it) {
         if ((skip >> it) & 1) continue;
@@ -877,21 +916,33 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             (valid && !SHARED && p.window > 0) ? max(0, w.L - p.q_len + i + 1 - p.window) : 0;
         float m_used = -INFINITY, l = 0.f;
         float log2_l = -INFINITY;  // log2(l), refreshed at the end of each block
-        for (int j = 0; j < nb; ++j) {
+        // SHARED: keys of the block at hand and behind it that the row sees, of the prefix up to
+        // block own_from, then its own
+        const int own_from = SHARED ? w.n_pre - w.blk0 : 0;
+        int left = !valid || !SHARED ? 0
+                   : own_from > 0    ? w.pre_len - w.blk0 * BN
+                                     : lim_row + own_from * BN;
+        const bool one = single(w);           // SHARED: no second tile,
+        const bool idle = one && x > 0;       // and this warpgroup has none
+        for (int j = 0; j < nb && !idle; ++j) {
             const int G = g + j;  // block count over the CTA's items: barrier phases
-            const int bsel = G % SB;
-            if (!wait_warp(BAR(C::B_SFULL + x * SB + bsel), (G / SB) & 1, abort_flag)) {
+            const int bsel = one ? j & 1 : G % SB;
+            const uint32_t s_full = BAR(C::B_SFULL + (one ? bsel : x * SB + bsel));
+            const int filled = !SHARED || NT == 1 ? G / SB : one ? (bsel ? full[1] : full[0]) + j / 2
+                                                   : (x ? full[1] : full[0]) + j;
+            if (!wait_warp(s_full, filled & 1, abort_flag)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const uint32_t ts = tl + C::s_col(x, bsel);
+            const uint32_t ts = tl + (one ? C::s_col(bsel, 0) : C::s_col(x, bsel));
             int nvis = lim_row - (kv_begin + j * BN);  // visible columns: [nlo, nvis)
             int nlo = lo_row - (kv_begin + j * BN);
             if constexpr (SHARED) {
-                const int jb = w.blk0 + j;
+                if (j == own_from && j > 0) left = lim_row;
                 nlo = 0;
-                nvis = !valid ? 0 : jb < w.n_pre ? w.pre_len - jb * BN : lim_row - (jb - w.n_pre) * BN;
+                nvis = left;
+                left -= BN;
             }
             // Padding rows of a ragged batch never reach the output: they may take the
             // unmasked path (their O and l are garbage but stay in their own row).
@@ -1092,7 +1143,8 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             // PV(j-1) off the critical path.  With one S buffer S(j) was issued after
             // PV(j-1) by the same thread, and its commit tracks every earlier MMA, so
             // S being full already says so.
-            if (SB > 1 && j > 0 && !wait_warp(BAR(C::B_PVDONE + x), (G - 1) & 1, abort_flag)) {
+            if ((SB > 1 || one) && j > 0 &&
+                !wait_warp(BAR(C::B_PVDONE + x), (G - 1) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -1121,12 +1173,15 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             if (ok && !last) {
                 ok = wait_warp(BAR(C::B_QEMPTY), (nq - 1) & 1, abort_flag);
                 if (ok) copy_q(item(next));
-                if (ok) ok = wait_warp(BAR(C::B_PVDONE + x), (g + nb - 1) & 1, abort_flag);
+                if (ok && !idle) ok = wait_warp(BAR(C::B_PVDONE + x), (g + nb - 1) & 1, abort_flag);
                 q_copied();
                 ++nq;
-            } else if (ok) {
+            } else if (ok && !idle) {
                 ok = wait_warp(BAR(C::B_PVDONE + x), (g + nb - 1) & 1, abort_flag);
             }
+            full[0] += one ? (nb + 1) / 2 : nb;
+            full[1] += one ? nb / 2 : nb;
+            if (idle && ok) continue;
         } else if (ok && !wait_warp(BAR(C::B_PVDONE + x), (g + nb - 1) & 1, abort_flag)) {
             ok = false;
         }
@@ -1137,6 +1192,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         // ---------------------------------------------------- epilogue
         tc_fence_after();
         if (ok) {
+            Item w = item(it);  // (from shared memory again: not held over the blocks)
             const int64_t row = row_of(w, valid ? f : 0);
             // Direct mode folds the sink (one more state: m = sink log2 e, l = 1,
             // acc = 0) here; split mode leaves it to the merge.
@@ -1160,7 +1216,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             // staging area (tile 0: the Q tiles; tile 1: the V stages, written once its
             // own PV is done).
             // (SHARED: only after the CTA's last item, where nothing lands any more.)
-            const bool staged = SHARED && last;
+            const bool staged = SHARED && NT == 1 && last;
             const bool wide = (SHARED ? part : p.split) || !p.out_bf16;  // fp32 rows, else bf16 rows
             const int rb = wide ? D * 4 : D * 2;       // bytes per output row
             const uint32_t stage = sb + (uint32_t)(x * 4 + q4) * (32u * D * 4u);
@@ -1170,6 +1226,47 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                 uint32_t o[32];
                 tmem_ld32(to + cc * 32, o);
                 tmem_wait_ld();
+                if constexpr (SHARED && NT == 2) {
+                    // 32 columns of the warp's rows through the warp's own staging: whole lines
+                    // to global memory, 4 rows (fp32) or 8 rows (bf16) an instruction.
+                    const uint32_t mine = sb + C::OFF_STAGE + (uint32_t)(x * 4 + q4) * 4096u;
+                    const int per_row = wide ? 8 : 4, lg = wide ? 3 : 2;  // 16-byte chunks
+                    __syncwarp();
+                    if (wide) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            st_shared_v4(mine + lane * 128 + ((k ^ (lane & 7)) << 4),
+                                         __float_as_uint(__uint_as_float(o[4 * k]) * inv),
+                                         __float_as_uint(__uint_as_float(o[4 * k + 1]) * inv),
+                                         __float_as_uint(__uint_as_float(o[4 * k + 2]) * inv),
+                                         __float_as_uint(__uint_as_float(o[4 * k + 3]) * inv));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            st_shared_v4(mine + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4),
+                                         pack_bf16(__uint_as_float(o[8 * k + 0]) * inv,
+                                                   __uint_as_float(o[8 * k + 1]) * inv),
+                                         pack_bf16(__uint_as_float(o[8 * k + 2]) * inv,
+                                                   __uint_as_float(o[8 * k + 3]) * inv),
+                                         pack_bf16(__uint_as_float(o[8 * k + 4]) * inv,
+                                                   __uint_as_float(o[8 * k + 5]) * inv),
+                                         pack_bf16(__uint_as_float(o[8 * k + 6]) * inv,
+                                                   __uint_as_float(o[8 * k + 7]) * inv));
+                    }
+                    __syncwarp();
+                    uint8_t *const to = part ? reinterpret_cast<uint8_t *>(p.ws_acc) : static_cast<uint8_t *>(p.out);
+                    const int64_t my = valid ? (part ? slot : row) : -1;
+#pragma unroll 2
+                    for (int k = 0; k < per_row; ++k) {
+                        const int at = (k << (5 - lg)) + (lane >> lg), ch = lane & (per_row - 1);
+                        const int64_t dst = __shfl_sync(0xffffffffu, my, at);
+                        const uint4 v = ld_shared_v4(mine + (wide ? at * 128 + ((ch ^ (at & 7)) << 4)
+                                                                  : at * 64 + ((ch ^ ((at >> 1) & 3)) << 4)));
+                        if (dst >= 0)
+                            *reinterpret_cast<uint4 *>(to + ((dst * D + cc * 32) << (wide ? 2 : 1)) + ch * 16) = v;
+                    }
+                    continue;
+                }
                 if (PERSIST && !staged) {
                     // The next item's Q and K/V are landing in shared memory: rows go
                     // straight from registers (direct mode), in 32-byte stores when the
@@ -1367,10 +1464,6 @@ cudaError_t launch_shared_instance(const TcParams &p, int64_t ctas, const CUtens
         err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (err != cudaSuccess) return err;
         if (dev < 64) configured[dev] = 1;
-    }
-    if (p.st.whole) {  // nothing runs beside it
-        kern<<<(unsigned)ctas, C::kThreads, C::kSmem, stream>>>(tmK, tmK, tmV, p);
-        return cudaGetLastError();
     }
     return launch_dependent(kern, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, stream, tmK, tmK,
                             tmV, p);

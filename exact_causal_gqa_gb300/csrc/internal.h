@@ -105,6 +105,8 @@ struct SharedSplitParams : SplitParams {
     int32_t own_items;            // n_chunks * Hkv * col_tiles * B
     int32_t cols;                 // columns per CTA: bf16 8 or 16, fp32 4, 8 or 16
     float *pre_acc, *pre_ml;      // as SharedMergeParams
+    const int32_t *order;         // the own items' sequences, longest first, or null (the batch's)
+    int32_t after_prefix;         // 1: a dependent of the prefixes' launch (own items alone)
 };
 
 // A call's kernels (atlas_attn.cu); the entry points are this and a kind.
@@ -143,8 +145,9 @@ struct SharedStream {
     int32_t max_states;  // CTAs that a tile may be cut among at most
     int32_t sms;
     // by the plan kernel
-    int32_t *head;       // [4]: blocks of a CTA, blocks of all, 1 if the groups are out of range
-    int32_t *first;      // [units + 1] blocks of the units before
+    int32_t *head;       // [4]: a CTA's length of the line, all of it, 1 if the groups are out of range
+    int32_t *first;      // [units + 1] where the units begin
+    int32_t *head_cost;  // [units] length of one kv head's tiles
     int32_t *tiles;      // [units] tiles of one kv head
     int32_t *blocks;     // [units] blocks of a tile; -1: out of range, its rows are NaN
     int32_t *weight;     // [units] blocks that a tile counts for (short ones count for more)
@@ -152,6 +155,15 @@ struct SharedStream {
     int32_t *group;      // [batch] the sequence's group, or -1
     int32_t *before;     // [batch + 1] rows of one kv head of the sequences before
     int32_t *list;       // ragged groups: [batch * G * q_len] the rows (of kv head 0), or null
+    int32_t *order;      // [batch] the sequences, those of most own keys first
+    int32_t *info;       // [batch][8]: what the merge wants to know of a sequence (SeqInfo)
+    int32_t wait_first;  // 1: wait for the grid before at the start, 0: at the end
+};
+// SharedStream::info, for the place of a row's tile in the line.
+struct SeqInfo {
+    int32_t blocks;      // of a tile; 0: no prefix; -1: out of range, the rows are NaN
+    int32_t row0;        // rows of the group before it: row f = row0 + q head * query rows + row
+    int32_t rows, first, head_cost, weight, per, pad;
 };
 
 // The same with the splits of the sequence's shared prefix (shared_prefix.cu) as further

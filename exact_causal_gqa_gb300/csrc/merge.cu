@@ -16,6 +16,7 @@
 // length, and wait (griddepcontrol.wait) before the first partial is read.
 #include "internal.h"
 #include "ptx.cuh"
+#include "shared_prefix.cuh"
 
 #include <math.h>
 #include <type_traits>
@@ -54,16 +55,13 @@ __device__ int prefix_splits(const SharedMergeParams &p, int b) {
 // The same where the prefixes are tiles of the line that p.st says (shared_prefix.cuh): the
 // states of the tile that row i of head h of sequence b is in.
 __device__ int tile_states(const SharedMergeParams &p, int b, int h, int i, int qn) {
-    const SharedStream &st = p.st;
-    if (st.head[2]) return -1;
-    const int u = st.group[b];
-    if (u < 0) return 0;
-    const int nb = st.blocks[u];
-    if (nb <= 0 || qn <= 0 || i >= qn) return nb < 0 ? -1 : 0;
-    const int f = st.before[b] - st.before[st.group_starts[u]] + h % p.G * qn + i;
-    const int first = st.first[u] + (h / p.G * st.tiles[u] + f / st.tile_rows) * st.weight[u];
-    const int per = st.head[0];
-    return (first + nb - 1) / per - first / per + 1;
+    const SeqInfo s = reinterpret_cast<const SeqInfo *>(p.st.info)[b];
+    if (s.blocks <= 0 || i >= qn) return s.blocks < 0 ? -1 : 0;
+    const int f = s.row0 + h % p.G * qn + i;
+    const int tile = f / p.st.tile_rows, full = p.st.tile_rows == 256 ? kPairCost : kSingleCost;
+    const int first = s.first + h / p.G * s.head_cost + tile * full * s.weight;
+    const int last = first + (s.blocks - 1) * block_cost(p.st, tile, s.rows);
+    return last / s.per - first / s.per + 1;
 }
 
 template <int D, typename Params>

@@ -7,15 +7,17 @@
 //   split kernels: the own splits and those of the prefixes are CTAs of one launch of the
 //     decode kernels (split_kv.cu).  A CTA has up to 16 of a group's rows, so a prefix is read
 //     once for each 16 rows, from L2 for all but the first;
-//   tensor cores: after the own splits, on the split kernels or the tensor cores by the rows
-//     of one sequence, the tensor-core kernels take the prefixes with 128 or 256 of a group's
-//     rows to a CTA (shared_prefix.cuh).  They are launched as a dependent of the own splits,
-//     whose results they do not need: their CTAs take the SMs as those leave them.
+//   tensor cores: the tensor-core kernels take the prefixes with 128 or 256 of a group's rows
+//     to a CTA (shared_prefix.cuh).  The own splits, on the split kernels or the tensor cores by
+//     the rows of one sequence, are a launch of their own beside that one: the second of the two
+//     is a dependent of the first, whose results it does not need, and its CTAs take the SMs as
+//     those of the first leave them.
 // bf16 sequences whose rows fill tiles by themselves have no use for a gather.  Their tiles walk
 // the prefix's blocks and go on with the sequence's own, in one launch, and write the output;
 // only tiles that a cut between two CTAs goes through are merged.
 #include "internal.h"
 #include "atlas_shared.h"
+#include "shared_prefix.cuh"
 
 #include <limits.h>
 #include <math.h>
@@ -101,14 +103,15 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
         else plan->n_pre = (int)std::min<int64_t>(blocks / 4 + 3, sms / likely + 6);
         plan->chunk = 0;
         // (short tiles that count as more blocks make for more CTAs than SMs)
-        plan->ctas = sms + units / 15 + 2;
-        if ((double)units * (double)blocks * (1.0 + (double)units / (sms * 30.0)) + 1e6 >= INT32_MAX)
-            return ATLAS_ERR_UNSUPPORTED;  // (the line of blocks is counted in 32 bits)
+        plan->ctas = sms + units / 10 + 2;
+        const double line = (double)units * kPairCost * (double)(blocks + kTileBlocks);
+        if (line * (1.0 + (double)units / (sms * 30.0)) + 1e6 >= INT32_MAX)
+            return ATLAS_ERR_UNSUPPORTED;  // (places in the line have 32 bits)
         const int64_t states = plan->whole ? plan->ctas * 2 * cta_rows : out_rows * plan->n_pre;
         plan->ml_at = plan->acc_at + (size_t)round_up(states * D * 4, 256);
         plan->plan_at = plan->ml_at + (size_t)round_up(states * 8, 256);
         const int64_t n = plan->whole ? L->batch : S->n_groups;
-        plan->bytes = plan->plan_at + 4 * (size_t)(4 + 5 * n + 1 + 2 * (int64_t)L->batch + 1 +
+        plan->bytes = plan->plan_at + 4 * (size_t)(11 * (int64_t)L->batch + 4 + 6 * n + 2 +
                                                    (plan->whole ? 0 : rows));
         return ATLAS_OK;
     }
@@ -134,12 +137,13 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     return ATLAS_OK;
 }
 
-// The own splits and the prefixes' in one launch.
+// The own splits and the prefixes' in one launch; or (order given) the own ones alone, behind
+// the launch of the prefixes and in that order.
 cudaError_t launch_split(const SharedPlan &plan, const void *q, const void *k_pages,
                          const void *v_pages, const int32_t *page_table, const int32_t *seq_lens,
                          int32_t Hq, int32_t Hkv, int32_t D, int32_t P, float scale,
                          const atlas_shared *S, const atlas_launch *L, float *pre_acc,
-                         float *pre_ml) {
+                         float *pre_ml, const int32_t *order = nullptr) {
     SharedSplitParams p{};
     p.q = q;
     p.k_pages = k_pages;
@@ -175,16 +179,19 @@ cudaError_t launch_split(const SharedPlan &plan, const void *q, const void *k_pa
     p.pre_chunk = plan.chunk;
     p.n_pre = plan.n_pre;
     p.own_items = plan.own.n_chunks * Hkv * plan.own.col_tiles * L->batch;
-    p.cols = plan.tiles;
+    p.cols = order ? split_bf16_cols_per_cta(p.G, p.q_len) : plan.tiles;
+    p.order = order;
+    p.after_prefix = order != nullptr;
+    const int64_t ctas = order ? p.own_items : plan.ctas;
     p.pre_acc = pre_acc;
     p.pre_ml = pre_ml;
     cudaStream_t stream = static_cast<cudaStream_t>(L->stream);
-    if (L->kv_dtype == ATLAS_F32) return launch_shared_split_f32(p, plan.ctas, stream);
+    if (L->kv_dtype == ATLAS_F32) return launch_shared_split_f32(p, ctas, stream);
     CUtensorMap tmK, tmV;
     if (encode_pool_map(&tmK, k_pages, L->num_pages, Hkv, P, D) != ATLAS_OK ||
         encode_pool_map(&tmV, v_pages, L->num_pages, Hkv, P, D) != ATLAS_OK)
         return cudaErrorUnknown;
-    return launch_shared_split_bf16(p, plan.ctas, tmK, tmV, stream);
+    return launch_shared_split_bf16(p, ctas, tmK, tmV, stream);
 }
 
 // The tensor-core kernels' view of a call.
@@ -246,14 +253,17 @@ SharedStream stream_arrays(const SharedPlan &plan, int32_t G, const atlas_shared
         at += n;
         return x;
     };
+    st.info = take(8 * (int64_t)L->batch);  // (16-byte loads: first)
     st.head = take(4);
     st.first = take(st.units + 1);
+    st.head_cost = take(st.units);
     st.tiles = take(st.units);
     st.blocks = take(st.units);
     st.weight = take(st.units);
     st.rows = take(st.units);
     st.group = take(L->batch);
     st.before = take(L->batch + 1);
+    st.order = take(L->batch);
     st.list = !plan.whole && L->q_lens ? take((int64_t)L->batch * G * L->q_len) : nullptr;
     return st;
 }
@@ -271,7 +281,18 @@ atlas_status launch_tc(const SharedPlan &plan, const void *q, const void *k_page
     cudaStream_t stream = static_cast<cudaStream_t>(L->stream);
     if (plan.stream) {
         tp.st = stream_arrays(plan, Hq / Hkv, S, L);
+        tp.seq_lens = seq_lens;
         if (launch_shared_plan(tp, stream) != cudaSuccess) return ATLAS_ERR_CUDA;
+        if (plan.own.path == Path::SplitBF16) {
+            // The prefixes' CTAs, which take equally long, then the own splits, the longest
+            // first: the SMs that the former leave are filled to the end.
+            tp.st.wait_first = 1;
+            return launch_shared_tc(tp, plan.ctas, tmK, tmV, stream) == cudaSuccess &&
+                           launch_split(plan, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P,
+                                        scale, S, L, pre_acc, pre_ml, tp.st.order) == cudaSuccess
+                       ? ATLAS_OK
+                       : ATLAS_ERR_CUDA;
+        }
     }
     atlas_launch own = *L;
     own.phase = ATLAS_PHASE_CHUNKS;
@@ -305,6 +326,7 @@ atlas_status launch_whole(const SharedPlan &plan, const void *q, const void *k_p
     tp.seq_lens = seq_lens;
     tp.max_pages = L->max_pages_per_seq;
     tp.st = stream_arrays(plan, Hq / Hkv, S, L);
+    tp.st.wait_first = 1;
     cudaStream_t stream = static_cast<cudaStream_t>(L->stream);
     if (launch_shared_plan(tp, stream) != cudaSuccess ||
         launch_shared_tc(tp, plan.ctas, tmK, tmV, stream) != cudaSuccess ||

@@ -101,10 +101,21 @@ __device__ __forceinline__ bool shared_real(const Params &p, int seq0, int rows,
 // ---------------------------------------------------------------- evenly cut tiles (bf16)
 // A unit -- a group with its prefix (st.whole 0), or a sequence with its prefix and its own keys
 // (1) -- has tiles of st.tile_rows rows for each kv head, and a tile has 128-key blocks: the
-// prefix's, the last of them perhaps in part, then the sequence's own.  All blocks of all tiles
-// stand in one line, tile after tile, and CTA x takes blocks [x n, (x + 1) n) of it, n chosen so
-// that every SM gets one CTA: whatever the lengths, all end together.  A tile that is cut leaves
-// partial states of its rows, one for each CTA that has blocks of it.
+// prefix's, the last of them perhaps in part, then the sequence's own.  The blocks of all tiles
+// stand in one line, tile after tile, each as long as it takes; CTA x has those that begin in
+// [x n, (x + 1) n) of it, n chosen so that every SM gets one CTA: whatever the lengths, all end
+// together.  A tile that is cut leaves partial states of its rows, one for each CTA that has
+// blocks of it.
+//
+// Lengths on the line, measured: a block of a 256-row tile (a pair of MMA tiles) 2.0 us, of one
+// whose rows end in its first half 1.1 us, and what a tile takes besides (its queries, the first
+// products, the epilogue) about two blocks.
+constexpr int kPairCost = 7, kSingleCost = 4, kTileBlocks = 2;
+
+// Length of a tile's block.
+__device__ __forceinline__ int block_cost(const SharedStream &st, int tile, int rows) {
+    return st.tile_rows == 256 && rows - tile * 256 > 128 ? kPairCost : kSingleCost;
+}
 
 // A CTA's piece of a tile.
 struct SharedSeg {
@@ -124,28 +135,43 @@ __device__ __forceinline__ int tile_own_keys(int seq_len, int qn, int row0, int 
 }
 
 struct SharedTile {
-    int unit, hkv, tile, first;  // first: its first block in the line
+    int unit, hkv, tile;
+    int first, cost, end;  // where it begins in the line, the length of its blocks, where it ends
 };
 
-// The tile that has a block of the line (a block before its end).  A whole warp calls this with
-// the same block; lane k looks at units k, k + 32, ...
-__device__ __forceinline__ SharedTile tile_of(const SharedStream &st, int block) {
+// Tiles of 256 rows but a unit's last, which may be a single.
+__device__ __forceinline__ void place_tile(const SharedStream &st, SharedTile &t) {
+    const int weight = st.weight[t.unit], rows = st.rows[t.unit];
+    const int full = st.tile_rows == 256 ? kPairCost : kSingleCost;
+    t.first = st.first[t.unit] + t.hkv * st.head_cost[t.unit] + t.tile * full * weight;
+    t.cost = block_cost(st, t.tile, rows);
+    t.end = t.first + t.cost * weight;
+}
+
+// The tile at a place of the line (before its end).  A whole warp calls this with the same place;
+// lane k looks at units k, k + 32, ...
+__device__ __forceinline__ SharedTile tile_of(const SharedStream &st, int place) {
     SharedTile t{};
     for (int u0 = 0; u0 < st.units; u0 += 32) {
         const int u = u0 + (int)(threadIdx.x % 32);
-        const bool here = u < st.units && st.first[u] <= block && block < st.first[u + 1];
+        const bool here = u < st.units && st.first[u] <= place && place < st.first[u + 1];
         const unsigned who = __ballot_sync(0xffffffffu, here);
         if (who) {
             t.unit = u0 + __ffs(who) - 1;
             break;
         }
     }
-    const int weight = st.weight[t.unit], tiles = st.tiles[t.unit];
-    const int at = (block - st.first[t.unit]) / weight;
-    t.hkv = at / tiles;
-    t.tile = at % tiles;
-    t.first = st.first[t.unit] + at * weight;
+    const int at = place - st.first[t.unit], per_head = st.head_cost[t.unit];
+    const int full = (st.tile_rows == 256 ? kPairCost : kSingleCost) * st.weight[t.unit];
+    t.hkv = at / per_head;
+    t.tile = min((at - t.hkv * per_head) / full, st.tiles[t.unit] - 1);
+    place_tile(st, t);
     return t;
+}
+
+// The first of a tile's blocks that begins at the place or behind it.
+__device__ __forceinline__ int block_from(const SharedTile &t, int place) {
+    return (max(place - t.first, 0) + t.cost - 1) / t.cost;
 }
 
 // Blocks of a tile that have keys for its rows.
@@ -172,30 +198,30 @@ __device__ inline int shared_segs(const Params &p, int cta, SharedSeg *segs) {
     const int per = st.head[0], all = st.head[1];
     if ((int64_t)cta * per >= all) return 0;
     const int end = (int)min((int64_t)all, (int64_t)(cta + 1) * per);
-    int n = 0;
-    SharedTile t{};
-    bool any = false;
-    for (int s = cta * per; s < end && n < st.max_items;) {
-        if (!any || s >= st.first[t.unit + 1]) {
-            t = tile_of(st, s);
-        } else {  // the next of the same unit
-            t.first = s;
-            if (++t.tile == st.tiles[t.unit]) {
-                t.tile = 0;
-                ++t.hkv;
-            }
-        }
-        any = true;
+    int n = 0, s = cta * per;
+    SharedTile t = tile_of(st, s);
+    while (n < st.max_items) {
         SharedSeg g;
-        const int nb = tile_blocks(p, t, g), stop = min(end, t.first + st.weight[t.unit]);
-        g.blk0 = s - t.first;
-        g.nb = min(stop - t.first, nb) - g.blk0;
-        g.state = t.first / per == (t.first + nb - 1) / per && st.whole ? -1 : cta - t.first / per;
+        const int nb = tile_blocks(p, t, g);
+        g.blk0 = block_from(t, s);
+        g.nb = min(block_from(t, min(end, t.end)), nb) - g.blk0;
+        const int home = t.first / per;
+        g.state = st.whole && home == (t.first + (nb - 1) * t.cost) / per ? -1 : cta - home;
         if (g.nb > 0) {
             if (threadIdx.x % 32 == 0) segs[n] = g;
             ++n;
         }
-        s = stop;
+        s = t.end;
+        if (s >= end) break;
+        if (s >= st.first[t.unit + 1]) {
+            t = tile_of(st, s);
+            continue;
+        }
+        if (++t.tile == st.tiles[t.unit]) {  // the next of the same unit
+            t.tile = 0;
+            ++t.hkv;
+        }
+        place_tile(st, t);
     }
     return n;
 }

@@ -11,7 +11,7 @@ namespace atlas {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kMinBlocks = 4;  // blocks of a CTA at least: below, its start outweighs them
+constexpr int kMinBlocks = 4;  // a CTA's share at least: below, its start outweighs it
 
 // Inclusive sums of x over the CTA, and the total.
 __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t &total) {
@@ -51,8 +51,15 @@ __device__ __forceinline__ int plan_max(int x) {
 
 // One CTA: a few arrays of a few hundred entries, 2 to 3 us, before the kernels that read them.
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParams p) {
+    allow_dependent_launch();
     const SharedStream &st = p.st;
     const int tid = (int)threadIdx.x;
+    // What later steps read back, in shared memory where the batch is not too long for it.
+    __shared__ int s_before[kPlanThreads + 1], s_group[kPlanThreads], s_rows[kPlanThreads],
+        s_blocks[kPlanThreads];
+    const bool small = p.B <= kPlanThreads;
+    int *const before = small ? s_before : st.before, *const group_of = small ? s_group : st.group;
+    int *const rows_of = small ? s_rows : st.rows, *const blocks_of = small ? s_blocks : st.blocks;
     bool wrong = false;
     for (int n = tid; n < st.n_groups; n += kPlanThreads) {
         const int a = st.group_starts[n], z = st.group_starts[n + 1];
@@ -77,6 +84,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
                 }
                 if (lo >= 0 && b < st.group_starts[lo + 1]) group = lo;
             }
+            group_of[b] = group;
             st.group[b] = group;
             const int qn = p.q_lens ? p.q_lens[b] : p.q_len;
             const int len = st.whole ? p.seq_lens[b] : 0;
@@ -88,24 +96,30 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
                     good = good && pre >= 0 && pre <= st.max_prefix_pages * p.P;
                 }
                 good = good && len >= qn && len <= p.max_pages * p.P;
-                st.blocks[b] = good ? (pre + 127) / 128 + (len + 127) / 128 : -1;
+                blocks_of[b] = good ? (pre + 127) / 128 + (len + 127) / 128 : -1;
+                st.blocks[b] = blocks_of[b];
                 if (!good) flags |= ATLAS_DEV_BAD_SEQLEN;
             }
             rows = good ? p.G * qn : 0;
-            if (st.whole) st.rows[b] = rows;
+            if (st.whole) rows_of[b] = st.rows[b] = rows;
             // (the rows of a group, head after head of one query's: the merge counts alike)
         }
         int64_t total;
         const int64_t upto = plan_scan(rows, total);
-        if (b < p.B) st.before[b] = (int)(carry + upto - rows);
+        if (b < p.B) before[b] = st.before[b] = (int)(carry + upto - rows);
         carry += total;
     }
-    if (tid == 0) st.before[p.B] = (int)carry;
+    if (tid == 0) before[p.B] = st.before[p.B] = (int)carry;
     __syncthreads();
 
     // units: their tiles, and what all of them have
     int most = 0;
     int64_t all = 0;
+    auto head_cost = [&](int rows, int nb) {  // tiles of one kv head, each counting as nb blocks
+        if (st.tile_rows != 256) return (rows + 127) / 128 * kSingleCost * nb;
+        const int last = rows % 256;
+        return (rows / 256 * kPairCost + (last == 0 ? 0 : last <= 128 ? kSingleCost : kPairCost)) * nb;
+    };
     for (int u0 = 0; u0 < st.units; u0 += kPlanThreads) {
         const int u = u0 + tid;
         int64_t blocks = 0;
@@ -114,34 +128,39 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
                 const int len = st.prefix_lens[u];
                 const bool good = len >= 0 && len <= st.max_prefix_pages * p.P && !bad;
                 if (!good) flags |= ATLAS_DEV_BAD_SEQLEN;
-                st.rows[u] = good ? st.before[st.group_starts[u + 1]] - st.before[st.group_starts[u]] : 0;
-                st.blocks[u] = good ? (len + 127) / 128 : -1;
+                rows_of[u] = st.rows[u] =
+                    good ? before[st.group_starts[u + 1]] - before[st.group_starts[u]] : 0;
+                blocks_of[u] = st.blocks[u] = good ? (len + 127) / 128 : -1;
             }
-            const int tiles = (st.rows[u] + st.tile_rows - 1) / st.tile_rows;
+            const int tiles = (rows_of[u] + st.tile_rows - 1) / st.tile_rows;
             st.tiles[u] = tiles;
-            const int nb = max(st.blocks[u], 0);
-            if (tiles > 0) most = max(most, nb);
-            blocks = (int64_t)tiles * p.Hkv * nb;
+            const int nb = max(blocks_of[u], 0);
+            if (tiles > 0) {
+                most = max(most, nb);
+                if (nb > 0) blocks = (int64_t)head_cost(rows_of[u], nb + kTileBlocks) * p.Hkv;
+            }
         }
         int64_t total;
         plan_scan(blocks, total);
         all += total;
     }
     most = plan_max(most);
-    // Blocks of a CTA: one CTA for each SM, few enough states of a tile, and few enough pieces of
-    // a CTA, for which short tiles count as more blocks than they have.
+    // A CTA's share: one CTA for each SM, few enough states of a tile, and few enough pieces of a
+    // CTA, for which short tiles count as more blocks than they have.
     int64_t per = (all + st.sms - 1) / st.sms;
-    per = max(per, (int64_t)kMinBlocks);
-    per = max(per, (int64_t)((most + st.max_states - 3) / (st.max_states - 2)));
-    const int least = (int)((per + st.max_items - 3) / (st.max_items - 2));
+    per = max(per, (int64_t)kMinBlocks * kPairCost);
+    per = max(per, (int64_t)((most + st.max_states - 3) / (st.max_states - 2)) * kPairCost);
+    const int least = (int)((per + kSingleCost * (st.max_items - 2) - 1) / (kSingleCost * (st.max_items - 2)));
     carry = 0;
     for (int u0 = 0; u0 < st.units; u0 += kPlanThreads) {
         const int u = u0 + tid;
         int64_t blocks = 0;
         if (u < st.units) {
-            const int nb = st.blocks[u] > 0 && st.tiles[u] > 0 ? max(st.blocks[u], least) : 0;
-            st.weight[u] = max(nb, 1);
-            blocks = (int64_t)st.tiles[u] * p.Hkv * nb;
+            const int tiles = (rows_of[u] + st.tile_rows - 1) / st.tile_rows;
+            const int nb = blocks_of[u] > 0 && tiles > 0 ? max(blocks_of[u] + kTileBlocks, least) : 0;
+            st.weight[u] = nb;
+            st.head_cost[u] = nb > 0 ? head_cost(rows_of[u], nb) : 1;
+            blocks = nb > 0 ? (int64_t)st.head_cost[u] * p.Hkv : 0;
         }
         int64_t total;
         const int64_t upto = plan_scan(blocks, total);
@@ -155,12 +174,46 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
         st.head[2] = bad;
     }
     if (flags && p.status) atomicOr(p.status, flags);
+    if (!st.whole) {
+        __syncthreads();  // (first, weight and tiles of every unit are there)
+        for (int b = tid; b < p.B; b += kPlanThreads) {
+            const int u = group_of[b];
+            SeqInfo s{};
+            if (bad) s.blocks = -1;
+            else if (u >= 0) {
+                s.blocks = blocks_of[u];
+                s.row0 = before[b] - before[st.group_starts[u]];
+                s.first = st.first[u];
+                s.rows = rows_of[u];
+                s.head_cost = st.head_cost[u];
+                s.weight = st.weight[u];
+                s.per = (int)per;
+            }
+            reinterpret_cast<SeqInfo *>(st.info)[b] = s;
+        }
+        // The order of the sequences' own splits: the longest first, so that the CTAs left over
+        // when the others are done are short ones.
+        if (small) {
+            __syncthreads();  // (rows and blocks have been read)
+            int *const lens = s_rows;
+            const int mine = tid < p.B ? p.seq_lens[tid] : 0;
+            lens[tid] = mine;
+            __syncthreads();
+            if (tid < p.B) {
+                int rank = 0;
+                for (int k = 0; k < p.B; ++k) rank += lens[k] > mine || (lens[k] == mine && k < tid);
+                st.order[rank] = tid;
+            }
+        } else {
+            for (int b = tid; b < p.B; b += kPlanThreads) st.order[b] = b;
+        }
+    }
 
     // ragged groups: their rows one after the other, no padding between
     if (st.list && p.q_lens) {
         const int lane = tid % 32;
         for (int b = tid / 32; b < p.B; b += kPlanThreads / 32) {
-            const int at = st.before[b], rows = st.before[b + 1] - at;
+            const int at = before[b], rows = before[b + 1] - at;
             const int qn = rows / p.G;
             for (int r = lane; r < rows; r += 32) {
                 const int g = r / qn;
@@ -177,7 +230,7 @@ constexpr int kCutWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kCutWarps * 32) shared_cut_merge_kernel(const TcParams p, int ctas) {
-    constexpr int E = D / 32;
+    constexpr int E = D / 32;  // (a lane's elements: one vector load)
     const SharedStream &st = p.st;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     wait_for_previous_grid();
@@ -209,13 +262,13 @@ __global__ void __launch_bounds__(kCutWarps * 32) shared_cut_merge_kernel(const 
             if (r % p.q_len < rows) put((int64_t)b * p.Hq * p.q_len + r, o, nan);
         return;
     }
-    const int per = st.head[0], x = (int)blockIdx.x + 1, block = x * per;
+    const int per = st.head[0], x = (int)blockIdx.x + 1;
     if ((int64_t)x * per >= st.head[1]) return;
-    const SharedTile t = tile_of(st, block);
-    if (t.first / per != x - 1 || t.first == block) return;  // not cut here first
+    const SharedTile t = tile_of(st, x * per);
+    if (t.first / per != x - 1) return;  // not cut here first
     SharedSeg s;
     const int nb = tile_blocks(p, t, s);
-    const int states = (t.first + nb - 1) / per - (x - 1) + 1;
+    const int states = (t.first + (nb - 1) * t.cost) / per - (x - 1) + 1;
     const int f = s.row0 + (int)blockIdx.y * kCutWarps + warp;
     if (states < 2 || f >= s.rows) return;
     // the first state is that of a tile's start, the others those of their CTAs' first pieces
@@ -226,16 +279,39 @@ __global__ void __launch_bounds__(kCutWarps * 32) shared_cut_merge_kernel(const 
     float sum = p.sinks ? 1.f : 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int k = 0; k < states; ++k) {
-        const float m = p.ws_ml[slot(k) * 2], l = p.ws_ml[slot(k) * 2 + 1];
-        if (isnan(m) || isnan(l)) has_nan = true;
-        if (!(l > 0.f)) continue;
-        const float top = fmaxf(M, m), old = M == -INFINITY ? 0.f : ex2(M - top), w = ex2(m - top);
-        const float *a = p.ws_acc + slot(k) * D + lane * E;
-        sum = fmaf(w, l, sum * old);
+    // Lane k has the weight of state k, of 32 at a time; the accumulators' loads of a few states
+    // are in flight together.
+    for (int k0 = 0; k0 < states; k0 += 32) {
+        const int k = k0 + lane;
+        float m = -INFINITY, l = 0.f;
+        if (k < states) {
+            const float2 ml = *reinterpret_cast<const float2 *>(p.ws_ml + slot(k) * 2);
+            m = ml.x;
+            l = ml.y;
+        }
+        has_nan |= __any_sync(0xffffffffu, isnan(m) || isnan(l));
+        float top = l > 0.f ? m : -INFINITY;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(w, a[e], o[e] * old);
+        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = fmaxf(M, top);
+        const float old = M == -INFINITY ? 0.f : ex2(M - top), w = l > 0.f ? ex2(m - top) : 0.f;
         M = top;
+        float add = w * l;
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) add += __shfl_xor_sync(0xffffffffu, add, d);
+        sum = sum * old + add;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= old;
+#pragma unroll 4
+        for (int j = 0; j < min(32, states - k0); ++j) {
+            const float wj = __shfl_sync(0xffffffffu, w, j);
+            const float *at = p.ws_acc + slot(k0 + j) * D + lane * E;
+            float a[E];
+            if constexpr (E == 4) *reinterpret_cast<float4 *>(a) = *reinterpret_cast<const float4 *>(at);
+            else *reinterpret_cast<float2 *>(a) = *reinterpret_cast<const float2 *>(at);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(wj, a[e], o[e]);
+        }
     }
     const float nan = __int_as_float(0x7fc00000);
     const bool none = has_nan || M == -INFINITY;

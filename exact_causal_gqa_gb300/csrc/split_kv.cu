@@ -125,8 +125,8 @@ __device__ SplitCta split_cta(const Params &p) {
         int i = (int)blockIdx.x;
         if (i < p.own_items) {
             const int chunk = i % p.n_chunks, y = i / p.n_chunks % (p.Hkv * p.col_tiles);
-            return {chunk, y / p.col_tiles, y % p.col_tiles, i / p.n_chunks / (p.Hkv * p.col_tiles),
-                    false, 0, 0, 0};
+            const int b = i / p.n_chunks / (p.Hkv * p.col_tiles);
+            return {chunk, y / p.col_tiles, y % p.col_tiles, p.order ? p.order[b] : b, false, 0, 0, 0};
         }
         const SharedGroups groups{p.group_starts, p.prefix_lens, p.n_groups,  p.B,   p.max_prefix_pages * p.P,
                                   p.G * p.q_len,  NCOLS,         p.pre_chunk, p.Hkv, p.status};
@@ -414,9 +414,18 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Lay::kFlags);
 
     int L, kv_begin, kv_end, col0, ncols, qn, why;
+    // The merge that follows reads the prefixes' states too, which the grid before this one
+    // writes: one CTA at least must not end before that grid has.
+    auto before_exit = [&]() {
+        if constexpr (kShared<Params>)
+            if (p.after_prefix && blockIdx.x == 0) wait_for_previous_grid();
+    };
     const SplitCta at = split_cta<NCOLS>(p);
-    if (kShared<Params> && at.chunk < 0) return;
-    if (!split_prologue<NCOLS>(p, at, L, kv_begin, kv_end, col0, ncols, qn, why)) return;
+    if ((kShared<Params> && at.chunk < 0) ||
+        !split_prologue<NCOLS>(p, at, L, kv_begin, kv_end, col0, ncols, qn, why)) {
+        before_exit();
+        return;
+    }
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int hkv = at.hkv;
@@ -696,6 +705,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     }
     __syncthreads();
     write_partials<kConsumerWarps, NCOLS, D>(p, at, cm, cl, cacc, col0, ncols, qn, any_failed);
+    before_exit();
 }
 
 // ---------------------------------------------------------------- cluster merge
@@ -1103,6 +1113,9 @@ cudaError_t launch_bf16_instance(const Params &p, dim3 grid, const CUtensorMap &
         if (err != cudaSuccess) return err;
         configured[dev] = 1;
     }
+    if constexpr (kShared<Params>)
+        if (p.after_prefix)
+            return launch_dependent(kern, grid, dim3(kSplitThreads), Lay::kBytes, stream, tmK, tmV, p);
     kern<<<grid, kSplitThreads, Lay::kBytes, stream>>>(tmK, tmV, p);
     return cudaGetLastError();
 }

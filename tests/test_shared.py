@@ -258,9 +258,14 @@ def test_bad_lengths_groups_and_pages_are_reported(dtype, q_len, path):
         for b in range(4):
             if b in nan:
                 assert torch.isnan(out[b]).all()
+            elif dtype == "bf16" and path != atlas.DEBUG_SHARED_SPLIT:
+                # the tiles are cut elsewhere when a sequence drops out: both results are within
+                # the bound of the same exact rows, |out| <= 4 here, so twice that apart at most
+                assert float((out[b].float() - good[b].float()).abs().max()) <= 2 * (BF16_ABS + 2.0 ** -8 * 4)
             else:
                 assert torch.equal(out[b], good[b])
 
+    assert float(good.float().abs().max()) <= 4
     for bad in (-1, x.args[3].shape[1] * 16 + 1):
         again(4, [100, bad], atlas.DEV_BAD_SEQLEN, (2, 3))
     for bad in (q_len - 1, x.args[6].shape[1] * 16 + 1):
