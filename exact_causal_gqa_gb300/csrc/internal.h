@@ -158,6 +158,8 @@ struct SharedStream {
     int32_t *order;      // [batch] the sequences, those of most own keys first
     int32_t *info;       // [batch][8]: what the merge wants to know of a sequence (SeqInfo)
     int32_t wait_first;  // 1: wait for the grid before at the start, 0: at the end
+    float own_rate;      // bytes a microsecond that an SM takes of the own keys' splits, which run
+                         // beside the tiles; 0: nothing runs beside them
 };
 // SharedStream::info, for the place of a row's tile in the line.
 struct SeqInfo {

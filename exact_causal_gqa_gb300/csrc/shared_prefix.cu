@@ -42,8 +42,18 @@ struct SharedPlan {
     size_t bytes;
 };
 
+// Keys of the own splits beside the tiles.
+int64_t own_split(int64_t max_ctx) {
+    const int64_t splits = (max_ctx + 4095) / 4096;
+    return round_up((max_ctx + splits - 1) / splits, 64);
+}
+
 // Rows of one sequence and kv head from which its tiles are its own.
 constexpr int64_t kWholeRows = 128;
+
+// Bytes a microsecond that the split kernels of 8 and of 16 columns take on one SM, when not all
+// SMs ask for memory.
+constexpr float kOwnRate = 70e3f, kOwnRateWide = 50e3f;
 
 // Whether the split kernels take less time: the prefix once for each CTA's rows, against a
 // second launch's start and the prefix once.
@@ -85,6 +95,14 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     plan->whole = plan->stream && seq_rows >= kWholeRows && L->split_tokens == 0;
     if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->whole = false;
     if (L->debug_flags & ATLAS_DEBUG_SHARED_WHOLE) plan->whole = plan->stream;
+    if (plan->stream && !plan->whole && few && L->split_tokens == 0 &&
+        (int64_t)L->batch * Hkv * plan->own.col_tiles >= 2 * (int64_t)sms) {
+        // The own splits run beside the tiles, the longest first: where there are enough
+        // sequences they are best left whole (up to 4096 keys).
+        own.split_tokens = (int32_t)own_split((int64_t)L->max_pages_per_seq * P);
+        if (make_plan(ATLAS_KIND_SUFFIX, Hq, Hkv, D, P, &own, &plan->own) != ATLAS_OK)
+            return ATLAS_ERR_UNSUPPORTED;
+    }
     const int64_t tile_of = plan->whole ? seq_rows : group_rows;
     plan->tiles = plan->split ? cols : !f32 && tile_of > 128 ? 2 : 1;
     // CTAs of one split: a group's last may be partly filled
@@ -280,13 +298,16 @@ atlas_status launch_tc(const SharedPlan &plan, const void *q, const void *k_page
     if (st != ATLAS_OK) return st;
     cudaStream_t stream = static_cast<cudaStream_t>(L->stream);
     if (plan.stream) {
+        const bool beside = plan.own.path == Path::SplitBF16;
         tp.st = stream_arrays(plan, Hq / Hkv, S, L);
+        tp.st.wait_first = beside;
+        tp.st.own_rate = !beside ? 0.f : Hq / Hkv * L->q_len <= 8 ? kOwnRate : kOwnRateWide;
         tp.seq_lens = seq_lens;
+        tp.max_pages = L->max_pages_per_seq;
         if (launch_shared_plan(tp, stream) != cudaSuccess) return ATLAS_ERR_CUDA;
-        if (plan.own.path == Path::SplitBF16) {
+        if (beside) {
             // The prefixes' CTAs, which take equally long, then the own splits, the longest
             // first: the SMs that the former leave are filled to the end.
-            tp.st.wait_first = 1;
             return launch_shared_tc(tp, plan.ctas, tmK, tmV, stream) == cudaSuccess &&
                            launch_split(plan, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P,
                                         scale, S, L, pre_acc, pre_ml, tp.st.order) == cudaSuccess

@@ -39,6 +39,19 @@ __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t &total) {
     return x + (warp ? sums[warp - 1] : 0);
 }
 
+// (the threads' shares in a fixed order: the same sum every time)
+__device__ __forceinline__ float plan_sum(float x) {
+    __shared__ float sums[kPlanThreads / 32];
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+    if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = x;
+    __syncthreads();
+    x = sums[threadIdx.x % 32];
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
 __device__ __forceinline__ int plan_max(int x) {
     __shared__ int most;
     if (threadIdx.x == 0) most = 0;
@@ -47,6 +60,30 @@ __device__ __forceinline__ int plan_max(int x) {
     if (threadIdx.x % 32 == 0) atomicMax(&most, x);
     __syncthreads();
     return most;
+}
+
+// SMs for the tiles when the sequences' own splits run beside them, on the other SMs and in the
+// end on all: the number for which both are done the soonest.  The tiles are bound by their
+// products and the splits by memory, so that neither gains from all SMs: 64 sequences of up to
+// 2048 own keys behind 32768 shared ones take 113 us with 152 CTAs of tiles, 99 with 96, 108 with
+// 64.  Times measured: a pair's block 2 us and a CTA's start and end 12; memory 6 MB a
+// microsecond at most.
+__device__ int ctas_beside(const TcParams &p, float line, float own_keys) {
+    __shared__ unsigned long long best;
+    if (threadIdx.x == 0) best = ~0ull;
+    __syncthreads();
+    const int n = (int)threadIdx.x + 1, sms = p.st.sms;
+    if (n <= sms) {
+        const float tiles = 12.f + line * (2.6f / kPairCost) / (float)n;
+        const float bytes = own_keys * (float)p.Hkv * (float)p.D * 4.f;
+        const float beside = fminf(6e6f, (float)(sms - n) * p.st.own_rate);
+        const float after = fminf(6e6f, (float)sms * p.st.own_rate);
+        const float t = tiles + fmaxf(0.f, bytes - beside * tiles) / after;
+        // (positive floats compare as integers; of equal times the larger number)
+        atomicMin(&best, ((unsigned long long)__float_as_uint(t) << 32) | (unsigned)(kPlanThreads - n));
+    }
+    __syncthreads();
+    return kPlanThreads - (int)(best & 0xffffffffu);
 }
 
 // One CTA: a few arrays of a few hundred entries, 2 to 3 us, before the kernels that read them.
@@ -70,6 +107,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
 
     // sequences: their groups, and the rows before them
     int64_t carry = 0;
+    float own_keys = 0.f;
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int rows = 0;
@@ -87,7 +125,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
             group_of[b] = group;
             st.group[b] = group;
             const int qn = p.q_lens ? p.q_lens[b] : p.q_len;
-            const int len = st.whole ? p.seq_lens[b] : 0;
+            const int len = p.seq_lens[b];
+            if (len > 0 && len <= p.max_pages * p.P) own_keys += (float)len;
             bool good = qn >= 0 && qn <= p.q_len && !bad;
             if (st.whole) {
                 int pre = 0;
@@ -110,7 +149,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
         carry += total;
     }
     if (tid == 0) before[p.B] = st.before[p.B] = (int)carry;
-    __syncthreads();
+    own_keys = plan_sum(own_keys);
 
     // units: their tiles, and what all of them have
     int most = 0;
@@ -147,7 +186,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
     most = plan_max(most);
     // A CTA's share: one CTA for each SM, few enough states of a tile, and few enough pieces of a
     // CTA, for which short tiles count as more blocks than they have.
-    int64_t per = (all + st.sms - 1) / st.sms;
+    const int ctas = st.own_rate > 0.f ? ctas_beside(p, (float)all, own_keys) : st.sms;
+    int64_t per = (all + ctas - 1) / ctas;
     per = max(per, (int64_t)kMinBlocks * kPairCost);
     per = max(per, (int64_t)((most + st.max_states - 3) / (st.max_states - 2)) * kPairCost);
     const int least = (int)((per + kSingleCost * (st.max_items - 2) - 1) / (kSingleCost * (st.max_items - 2)));
