@@ -25,6 +25,9 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kClusterCtas = 8;  // the portable cluster size
+// Entries of table and slots up to which a call is one cluster (what it moves is known on the
+// device alone).
+constexpr int64_t kOneLaunch = 1 << 17;
 
 struct ResizeParams {
     int32_t *table, *n_pages, *ring, *state;
@@ -61,19 +64,20 @@ __device__ __forceinline__ void cluster_sync() {
         "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Inclusive sums of x over the CTA's threads, and the total (below 2^31: batch * max_pages is).
-__device__ __forceinline__ int scan(int x, int &total) {
-    __shared__ int sums[kWarps];
+// Inclusive sums of need (low half) and back (high half) over the CTA's threads, and the totals.
+// (Each is below 2^31, as batch * max_pages is, so the halves do not meet.)
+__device__ __forceinline__ uint64_t scan(uint64_t x, uint64_t &total) {
+    __shared__ uint64_t sums[kWarps];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
-        const int a = __shfl_up_sync(0xffffffffu, x, d);
+        const uint64_t a = __shfl_up_sync(0xffffffffu, x, d);
         if (lane >= d) x += a;
     }
     __syncthreads();  // (the sums of the scan before this one have been read)
     if (lane == 31) sums[warp] = x;
     __syncthreads();
-    int before = 0;
+    uint64_t before = 0;
     total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -83,30 +87,49 @@ __device__ __forceinline__ int scan(int x, int &total) {
     return x + before;
 }
 
-// The sums of one round of sequences.
-struct Round {
-    Move m;
-    int need, back;    // inclusive sums over the batch
-    bool lacks;        // its need does not fit
-};
+__device__ __forceinline__ int largest(int x) {
+    __shared__ int most;
+    __syncthreads();
+    if (threadIdx.x == 0) most = 0;
+    __syncthreads();
+    x = __reduce_max_sync(0xffffffffu, x);
+    if (threadIdx.x % 32 == 0) atomicMax(&most, x);
+    __syncthreads();
+    return most;
+}
 
 struct Totals {
     int need = 0, back = 0;  // sums over the rounds so far
     int taken = 0;           // pages taken by the sequences that are served
 };
 
+// One sequence's place in the sums.
+struct Round {
+    Move m;
+    int need, back;  // inclusive sums over the batch
+    int moves;       // inclusive sum of the round's moves
+    int all;         // moves of the round
+    bool lacks;      // its need does not fit
+};
+
 __device__ __forceinline__ Round take_round(const ResizeParams &p, int b, int count, Totals &t) {
     Round r;
     r.m = move_of(p, b);
-    int need, back;
-    r.need = t.need + scan(r.m.need(), need);
-    r.back = t.back + scan(r.m.back(), back);
+    uint64_t total;
+    const uint64_t upto = scan((uint64_t)r.m.need() | (uint64_t)r.m.back() << 32, total);
+    const int need = (int)(uint32_t)upto, back = (int)(upto >> 32);
+    r.need = t.need + need;
+    r.back = t.back + back;
     r.lacks = r.m.need() > 0 && r.need > count;
-    t.need += need;
-    t.back += back;
-    int served;
-    scan(r.lacks ? 0 : r.m.need(), served);
-    t.taken += served;
+    // Those that are served are the first ones: pages taken up to a sequence are its sum of needs
+    // while that fits, then what the last one served left it at.
+    int fits = (int)(uint32_t)total;
+    if (t.need + fits > count) fits = largest(r.need <= count ? need : 0);
+    r.moves = min(need, fits) + back;
+    r.all = fits + (int)(total >> 32);
+    t.need += (int)(uint32_t)total;
+    t.back += (int)(total >> 32);
+    t.taken += fits;
     return r;
 }
 
@@ -115,15 +138,18 @@ __device__ __forceinline__ int wrapped(int64_t at, int num) {
 }
 
 // Whether the ring's state is one, and has room for all that comes back.
-__device__ bool ring_fits(const ResizeParams &p, int head, int count) {
-    if (head < 0 || head >= p.num_pages || count < 0 || count > p.num_pages) return false;
+__device__ bool ring_fits(const ResizeParams &p, int head, int count, int64_t back) {
+    return head >= 0 && head < p.num_pages && count >= 0 && count <= p.num_pages &&
+           back <= p.num_pages - count;
+}
+__device__ int64_t all_back(const ResizeParams &p) {
     int64_t back = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-        int total;
-        scan(move_of(p, b0 + (int)threadIdx.x).back(), total);
-        back += total;
+        uint64_t total;
+        scan((uint64_t)move_of(p, b0 + (int)threadIdx.x).back(), total);
+        back += (int64_t)total;
     }
-    return back <= p.num_pages - count;
+    return back;
 }
 
 // The new n_pages and state (one CTA, after everyone's last read of the old ones).
@@ -140,71 +166,102 @@ __device__ void finish(const ResizeParams &p, int head, int count) {
     }
 }
 
+constexpr int kAtOnce = 4;  // moves and slots of a thread whose loads are in flight together
+
 template <bool ONE_LAUNCH>
 __global__ void __launch_bounds__(kThreads) kv_resize_kernel(const ResizeParams p) {
-    __shared__ int s_moves[kThreads];             // inclusive sums of the round's moves
-    __shared__ int s_n[kThreads], s_want[kThreads], s_from[kThreads], s_len[kThreads], s_fresh[kThreads];
+    // The round's sequences: inclusive sums of their moves, pages held and wanted, where their
+    // pages stand in the ring (behind those of the sequences before), lengths, new tokens.
+    __shared__ int s_moves[kThreads], s_n[kThreads], s_want[kThreads], s_from[kThreads],
+        s_len[kThreads], s_fresh[kThreads];
     if (!ONE_LAUNCH) allow_dependent_launch();
     const int threads = (int)(gridDim.x * kThreads), me = (int)(blockIdx.x * kThreads + threadIdx.x);
+    const int tid = (int)threadIdx.x, lp = 31 - __clz(p.P);
     const int head = p.state[0], count = p.state[1];
-    const bool fits = ring_fits(p, head, count);
-    uint32_t flags = fits ? 0u : ATLAS_DEV_BAD_PAGE;
+    // (a batch of one round finds out below)
+    bool fits = p.B <= kThreads || ring_fits(p, head, count, all_back(p));
+    uint32_t flags = 0;
     Totals t;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-        const int tid = (int)threadIdx.x;
         const Round r = take_round(p, b0 + tid, count, t);
-        const bool moves = fits && !r.lacks;
+        if (p.B <= kThreads) fits = ring_fits(p, head, count, t.back);
         if (r.m.bad) flags |= ATLAS_DEV_BAD_SEQLEN;
         if (r.lacks && fits) flags |= ATLAS_DEV_NO_PAGES;
-        int total;
-        s_moves[tid] = scan(moves ? r.m.need() + r.m.back() : 0, total);
+        const bool moves = fits && !r.lacks;
+        s_moves[tid] = r.moves;
         s_n[tid] = r.m.n;
         s_want[tid] = moves ? r.m.want : r.m.n;
-        // where its pages stand in the ring: behind those of the sequences before it
         s_from[tid] = r.m.need() ? r.need - r.m.need() : r.back - r.m.back();
         s_len[tid] = r.m.len;
         s_fresh[tid] = moves && !r.m.bad ? r.m.fresh : 0;
         __syncthreads();
-        for (int e = me; e < total; e += threads) {
-            int lo = 0, hi = kThreads - 1;  // the first sequence whose sum is above e
-            while (lo < hi) {
-                const int mid = (lo + hi) / 2;
-                if (s_moves[mid] > e) hi = mid;
-                else lo = mid + 1;
+        const int total = fits ? r.all : 0;
+        for (int e0 = me; e0 < total; e0 += threads * kAtOnce) {
+            int32_t *from[kAtOnce], *to[kAtOnce];
+            int id[kAtOnce];
+            bool back[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int e = e0 + u * threads;
+                if (e >= total) continue;
+                int lo = 0, hi = kThreads - 1;  // the first sequence whose sum is above e
+                while (lo < hi) {
+                    const int mid = (lo + hi) / 2;
+                    if (s_moves[mid] > e) hi = mid;
+                    else lo = mid + 1;
+                }
+                const int k = e - (lo ? s_moves[lo - 1] : 0), n = s_n[lo], want = s_want[lo];
+                int32_t *row = p.table + (int64_t)(b0 + lo) * p.max_pages;
+                back[u] = want < n;
+                if (back[u]) {
+                    from[u] = row + want + k;
+                    to[u] = p.ring + wrapped((int64_t)head + count + s_from[lo] + k, p.num_pages);
+                } else {
+                    from[u] = p.ring + wrapped((int64_t)head + s_from[lo] + k, p.num_pages);
+                    to[u] = row + n + k;
+                }
+                id[u] = *from[u];
             }
-            const int k = e - (lo ? s_moves[lo - 1] : 0), n = s_n[lo], want = s_want[lo];
-            int32_t *row = p.table + (int64_t)(b0 + lo) * p.max_pages;
-            int id;
-            if (want > n) {
-                id = p.ring[wrapped((int64_t)head + s_from[lo] + k, p.num_pages)];
-                row[n + k] = id;
-            } else {
-                id = row[want + k];
-                p.ring[wrapped((int64_t)head + count + s_from[lo] + k, p.num_pages)] = id;
-                row[want + k] = -1;
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                if (e0 + u * threads >= total) continue;
+                *to[u] = id[u];
+                if (back[u]) *from[u] = -1;
+                if (id[u] < 0 || id[u] >= p.num_pages) flags |= ATLAS_DEV_BAD_PAGE;
             }
-            if (id < 0 || id >= p.num_pages) flags |= ATLAS_DEV_BAD_PAGE;
         }
         // The slots of new tokens: pages that were there from the table, those that are taken
         // now from the ring, so that nothing written in this call is read in it.
-        const int rows = min(kThreads, p.B - b0);
-        if (p.slots) {
-            for (int e = me; e < rows * p.max_new; e += threads) {
+        const int slots = p.slots ? min(kThreads, p.B - b0) * p.max_new : 0;
+        for (int e0 = me; e0 < slots; e0 += threads * kAtOnce) {
+            int id[kAtOnce], at[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int e = e0 + u * threads;
+                at[u] = -1;
+                if (e >= slots) continue;
                 const int s = e / p.max_new, i = e - s * p.max_new;
+                if (i >= s_fresh[s]) continue;
+                at[u] = s_len[s] - s_fresh[s] + i;
+                const int j = at[u] >> lp;
+                id[u] = j < s_n[s] ? p.table[(int64_t)(b0 + s) * p.max_pages + j]
+                                   : p.ring[wrapped((int64_t)head + s_from[s] + j - s_n[s], p.num_pages)];
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int e = e0 + u * threads;
+                if (e >= slots) continue;
                 int slot = -1;
-                if (i < s_fresh[s]) {
-                    const int at = s_len[s] - s_fresh[s] + i, j = at / p.P;
-                    const int id = j < s_n[s] ? p.table[(int64_t)(b0 + s) * p.max_pages + j]
-                                              : p.ring[wrapped((int64_t)head + s_from[s] + j - s_n[s],
-                                                               p.num_pages)];
-                    if (id < 0 || id >= p.num_pages) flags |= ATLAS_DEV_BAD_PAGE;
-                    else slot = id * p.P + at % p.P;
+                if (at[u] >= 0) {
+                    if (id[u] < 0 || id[u] >= p.num_pages) flags |= ATLAS_DEV_BAD_PAGE;
+                    else slot = id[u] * p.P + (at[u] & (p.P - 1));
                 }
                 p.slots[(int64_t)b0 * p.max_new + e] = slot;
             }
         }
-        __syncthreads();  // the round's arrays are rewritten
+        if (b0 + kThreads < p.B) __syncthreads();  // the round's arrays are rewritten
     }
+    if (!fits) flags |= ATLAS_DEV_BAD_PAGE;
     flags = __reduce_or_sync(0xffffffffu, flags);
     if (flags && threadIdx.x % 32 == 0 && p.status) atomicOr(p.status, flags);
     if (ONE_LAUNCH) {
@@ -216,10 +273,9 @@ __global__ void __launch_bounds__(kThreads) kv_resize_kernel(const ResizeParams 
 __global__ void __launch_bounds__(kThreads) kv_resize_finish_kernel(const ResizeParams p) {
     wait_for_previous_grid();
     const int head = p.state[0], count = p.state[1];
-    if (ring_fits(p, head, count)) {
-        __syncthreads();  // (every thread has read the state)
-        finish(p, head, count);
-    }
+    const int64_t back = all_back(p);
+    __syncthreads();  // (every thread has read the state)
+    if (ring_fits(p, head, count, back)) finish(p, head, count);
 }
 
 bool apart(const void *a, int64_t na, const void *b, int64_t nb) {
@@ -281,7 +337,7 @@ extern "C" atlas_status atlas_kv_resize(int32_t *page_table, int32_t *n_pages,
     cudaLaunchAttribute attr[1];
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (most <= (int64_t)1 << 18) {
+    if (most <= kOneLaunch) {
         const int ctas = most <= kThreads ? 1 : kClusterCtas;
         cfg.gridDim = dim3(ctas);
         attr[0].id = cudaLaunchAttributeClusterDimension;
