@@ -313,7 +313,11 @@ template <int NT, int D, bool PERSIST, bool SHARED = false>
 __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     fmha_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const TcParams p) {
-    allow_dependent_launch();  // the merge may start its CTAs (it waits for this grid)
+    // The merge may start its CTAs (it waits for this grid).  A SHARED grid that the own splits
+    // follow reads what the plan's grid before it wrote, and so do those: they may start once
+    // that is there.
+    if (SHARED && p.st.wait_first) wait_for_previous_grid();
+    allow_dependent_launch();
     using C = Cfg<NT, D, SHARED>;
     constexpr int S = C::kStages, SB = C::kSB;
     constexpr int kTileBytes = C::kTileBytes;
@@ -342,19 +346,15 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         if (SHARED && !p.st.wait_first && blockIdx.x == 0) wait_for_previous_grid();
     };
     if constexpr (SHARED) {
-        if (p.st.wait_first) wait_for_previous_grid();
-        int *const count = reinterpret_cast<int *>(smem + C::OFF_FLAG);
-        if (warp == 0) {
-            const int n = shared_segs(p, blockIdx.x, segs);
-            if (lane == 0) *count = n;
-        }
-        __syncthreads();
-        n_items = *count;
+        n_items = (int64_t)blockIdx.x * p.st.head[0] < p.st.head[1] ? p.st.counts[blockIdx.x] : 0;
+        const int32_t *from = reinterpret_cast<const int32_t *>(p.st.segs + (int64_t)blockIdx.x * p.st.max_items);
+        for (int i = threadIdx.x; i < p.st.max_items * (int)(sizeof(SharedSeg) / 4); i += blockDim.x)
+            reinterpret_cast<int32_t *>(segs)[i] = from[i];
         if (n_items == 0) {
             before_exit();
             return;
         }
-        __syncthreads();  // (the word is the abort flag from here on)
+        __syncthreads();
     } else if (PERSIST) {
         const int total = p.B * p.Hkv * (p.G / NT) * p.tiles_per_head;
         n_items = 0;

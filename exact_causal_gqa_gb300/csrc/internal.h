@@ -131,6 +131,16 @@ struct MergeParams {
     int32_t warps_per_row;  // set by launch_merge
 };
 
+// A CTA's piece of a tile.
+struct SharedSeg {
+    int unit, hkv, row0;   // the tile's first row (of the unit's, in one kv head)
+    int rows;              // the unit's rows
+    int blk0, nb;          // blocks [blk0, blk0 + nb) of the tile
+    int state;             // index of its partial state; -1: the tile is not cut
+    int len, own;          // keys of the prefix, own keys that the tile's rows see at most
+    int group;             // whose prefix (-1: none)
+};
+
 // The tiles of a call with shared prefixes on the tensor cores, cut evenly among CTAs
 // (shared_prefix.cuh).  Arrays in the workspace, written by the plan kernel.
 struct SharedStream {
@@ -148,16 +158,18 @@ struct SharedStream {
     int32_t *head;       // [4]: a CTA's length of the line, all of it, 1 if the groups are out of range
     int32_t *first;      // [units + 1] where the units begin
     int32_t *head_cost;  // [units] length of one kv head's tiles
-    int32_t *tiles;      // [units] tiles of one kv head
     int32_t *blocks;     // [units] blocks of a tile; -1: out of range, its rows are NaN
     int32_t *weight;     // [units] blocks that a tile counts for (short ones count for more)
     int32_t *rows;       // [units] rows of one kv head
     int32_t *group;      // [batch] the sequence's group, or -1
     int32_t *before;     // [batch + 1] rows of one kv head of the sequences before
     int32_t *list;       // ragged groups: [batch * G * q_len] the rows (of kv head 0), or null
+    SharedSeg *segs;     // [CTAs][max_items] the CTAs' pieces,
+    int32_t *counts;     // [CTAs] and how many
     int32_t *order;      // [batch] the sequences, those of most own keys first
     int32_t *info;       // [batch][8]: what the merge wants to know of a sequence (SeqInfo)
-    int32_t wait_first;  // 1: wait for the grid before at the start, 0: at the end
+    int32_t wait_first;  // 1: wait for the grid before at the start, 0: at the end (the plan's is
+                         // done by then)
     float own_rate;      // bytes a microsecond that an SM takes of the own keys' splits, which run
                          // beside the tiles; 0: nothing runs beside them
 };

@@ -42,6 +42,9 @@ struct SharedPlan {
     size_t bytes;
 };
 
+// CTAs of a wave of the split kernels, in hundredths of the SMs, and a CTA's keys at least.
+constexpr int64_t kSplitWave = 200, kSplitWaveF32 = 300, kMinSplit = 128, kMinSplitF32 = 64;
+
 // Keys of the own splits beside the tiles.
 int64_t own_split(int64_t max_ctx) {
     const int64_t splits = (max_ctx + 4095) / 4096;
@@ -129,19 +132,30 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
         plan->ml_at = plan->acc_at + (size_t)round_up(states * D * 4, 256);
         plan->plan_at = plan->ml_at + (size_t)round_up(states * 8, 256);
         const int64_t n = plan->whole ? L->batch : S->n_groups;
-        plan->bytes = plan->plan_at + 4 * (size_t)(11 * (int64_t)L->batch + 4 + 6 * n + 2 +
-                                                   (plan->whole ? 0 : rows));
+        const int64_t segs = 1 + shared_tc_items(plan->tiles) * (int64_t)(sizeof(SharedSeg) / 4);
+        plan->bytes = plan->plan_at + 4 * (size_t)(11 * (int64_t)L->batch + 4 + 5 * n + 2 +
+                                                   plan->ctas * segs + (plan->whole ? 0 : rows));
         return ATLAS_OK;
     }
-    int64_t chunk = round_up(L->split_tokens, 128);
+    int64_t chunk = plan->split ? L->split_tokens : round_up(L->split_tokens, 128);
     if (chunk == 0 && plan->split) {
-        chunk = round_up((max_prefix * likely + sms * 4 - 1) / (sms * 4), 128);
-        chunk = std::min<int64_t>(std::max<int64_t>(chunk, 256), 2560);
+        // One wave of CTAs, all with as many keys: the own keys (half of the most there may be)
+        // and the prefixes' for each CTA's rows, on the CTAs that are resident.
+        const int64_t own_units = (int64_t)L->batch * Hkv * ((G * L->q_len + cols - 1) / cols);
+        const int64_t max_ctx = (int64_t)L->max_pages_per_seq * P;
+        const int64_t slots = sms * (f32 ? kSplitWaveF32 : kSplitWave) / 100;
+        const int64_t keys = own_units * max_ctx / 2 + likely * max_prefix;
+        chunk = round_up((keys + slots - 1) / slots, 64);
+        chunk = std::min<int64_t>(std::max<int64_t>(chunk, f32 ? kMinSplitF32 : kMinSplit), 2560);
+        own.split_tokens = (int32_t)chunk;
+        if (make_plan(ATLAS_KIND_SUFFIX, Hq, Hkv, D, P, &own, &plan->own) != ATLAS_OK)
+            return ATLAS_ERR_UNSUPPORTED;
+        plan->acc_at = (size_t)round_up((int64_t)plan->own.ws_bytes, 256);
     } else if (chunk == 0) {
         const int64_t splits = std::max<int64_t>(1, sms * 3 / likely);
         chunk = std::max<int64_t>(512, round_up((max_prefix + splits - 1) / splits, 128));
     }
-    chunk = std::min(chunk, round_up(max_prefix, 128));
+    chunk = std::min(chunk, round_up(max_prefix, plan->split ? 64 : 128));
     plan->chunk = (int)chunk;
     plan->n_pre = (int)((max_prefix + chunk - 1) / chunk);
     plan->ctas = units * plan->n_pre;
@@ -275,13 +289,14 @@ SharedStream stream_arrays(const SharedPlan &plan, int32_t G, const atlas_shared
     st.head = take(4);
     st.first = take(st.units + 1);
     st.head_cost = take(st.units);
-    st.tiles = take(st.units);
     st.blocks = take(st.units);
     st.weight = take(st.units);
     st.rows = take(st.units);
     st.group = take(L->batch);
     st.before = take(L->batch + 1);
     st.order = take(L->batch);
+    st.counts = take(plan.ctas);
+    st.segs = reinterpret_cast<SharedSeg *>(take(plan.ctas * st.max_items * (int64_t)(sizeof(SharedSeg) / 4)));
     st.list = !plan.whole && L->q_lens ? take((int64_t)L->batch * G * L->q_len) : nullptr;
     return st;
 }

@@ -117,16 +117,6 @@ __device__ __forceinline__ int block_cost(const SharedStream &st, int tile, int 
     return st.tile_rows == 256 && rows - tile * 256 > 128 ? kPairCost : kSingleCost;
 }
 
-// A CTA's piece of a tile.
-struct SharedSeg {
-    int unit, hkv, row0;   // the tile's first row (of the unit's, in one kv head)
-    int rows;              // the unit's rows
-    int blk0, nb;          // blocks [blk0, blk0 + nb) of the tile
-    int state;             // index of its partial state; -1: the tile is not cut
-    int len, own;          // keys of the prefix, own keys that the tile's rows see at most
-    int group;             // whose prefix (-1: none)
-};
-
 // Own keys (with st.whole) that a tile's rows see at most: rows are q heads times query rows.
 __device__ __forceinline__ int tile_own_keys(int seq_len, int qn, int row0, int row_end) {
     const int last = row_end - 1;  // (the tile's last row)
@@ -164,7 +154,8 @@ __device__ __forceinline__ SharedTile tile_of(const SharedStream &st, int place)
     const int at = place - st.first[t.unit], per_head = st.head_cost[t.unit];
     const int full = (st.tile_rows == 256 ? kPairCost : kSingleCost) * st.weight[t.unit];
     t.hkv = at / per_head;
-    t.tile = min((at - t.hkv * per_head) / full, st.tiles[t.unit] - 1);
+    t.tile = min((at - t.hkv * per_head) / full,
+                 (st.rows[t.unit] + st.tile_rows - 1) / st.tile_rows - 1);
     place_tile(st, t);
     return t;
 }
@@ -189,41 +180,6 @@ __device__ __forceinline__ int tile_blocks(const Params &p, const SharedTile &t,
         s.own = tile_own_keys(p.seq_lens[t.unit], p.q_lens ? p.q_lens[t.unit] : p.q_len, s.row0,
                               min(s.row0 + st.tile_rows, s.rows));
     return (s.len + 127) / 128 + (s.own + 127) / 128;
-}
-
-// The pieces of CTA `cta`: one warp calls this.  Returns their number.
-template <typename Params>
-__device__ inline int shared_segs(const Params &p, int cta, SharedSeg *segs) {
-    const SharedStream &st = p.st;
-    const int per = st.head[0], all = st.head[1];
-    if ((int64_t)cta * per >= all) return 0;
-    const int end = (int)min((int64_t)all, (int64_t)(cta + 1) * per);
-    int n = 0, s = cta * per;
-    SharedTile t = tile_of(st, s);
-    while (n < st.max_items) {
-        SharedSeg g;
-        const int nb = tile_blocks(p, t, g);
-        g.blk0 = block_from(t, s);
-        g.nb = min(block_from(t, min(end, t.end)), nb) - g.blk0;
-        const int home = t.first / per;
-        g.state = st.whole && home == (t.first + (nb - 1) * t.cost) / per ? -1 : cta - home;
-        if (g.nb > 0) {
-            if (threadIdx.x % 32 == 0) segs[n] = g;
-            ++n;
-        }
-        s = t.end;
-        if (s >= end) break;
-        if (s >= st.first[t.unit + 1]) {
-            t = tile_of(st, s);
-            continue;
-        }
-        if (++t.tile == st.tiles[t.unit]) {  // the next of the same unit
-            t.tile = 0;
-            ++t.hkv;
-        }
-        place_tile(st, t);
-    }
-    return n;
 }
 
 // Output row of row f of a unit.

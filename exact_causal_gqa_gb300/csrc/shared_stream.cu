@@ -10,7 +10,7 @@
 namespace atlas {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
 constexpr int kMinBlocks = 4;  // a CTA's share at least: below, its start outweighs it
 
 // Inclusive sums of x over the CTA, and the total.
@@ -25,234 +25,275 @@ __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t &total) {
     __syncthreads();  // (the sums of the scan before this one have been read)
     if (lane == 31) sums[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-        int64_t s = sums[lane];
+    int64_t before = 0;
+    total = 0;
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int64_t a = __shfl_up_sync(0xffffffffu, s, d);
-            if (lane >= d) s += a;
-        }
-        sums[lane] = s;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
     }
-    __syncthreads();
-    total = sums[kPlanThreads / 32 - 1];
-    return x + (warp ? sums[warp - 1] : 0);
-}
-
-// (the threads' shares in a fixed order: the same sum every time)
-__device__ __forceinline__ float plan_sum(float x) {
-    __shared__ float sums[kPlanThreads / 32];
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
-    if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = x;
-    __syncthreads();
-    x = sums[threadIdx.x % 32];
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
-    return x;
-}
-
-__device__ __forceinline__ int plan_max(int x) {
-    __shared__ int most;
-    if (threadIdx.x == 0) most = 0;
-    __syncthreads();
-    x = __reduce_max_sync(0xffffffffu, x);
-    if (threadIdx.x % 32 == 0) atomicMax(&most, x);
-    __syncthreads();
-    return most;
+    return x + before;
 }
 
 // SMs for the tiles when the sequences' own splits run beside them, on the other SMs and in the
 // end on all: the number for which both are done the soonest.  The tiles are bound by their
 // products and the splits by memory, so that neither gains from all SMs: 64 sequences of up to
 // 2048 own keys behind 32768 shared ones take 113 us with 152 CTAs of tiles, 99 with 96, 108 with
-// 64.  Times measured: a pair's block 2 us and a CTA's start and end 12; memory 6 MB a
-// microsecond at most.
+// 64.  Times measured: a pair's block 2.6 us beside the splits and a CTA's start and end 12;
+// memory 6 MB a microsecond at most.
 __device__ int ctas_beside(const TcParams &p, float line, float own_keys) {
     __shared__ unsigned long long best;
     if (threadIdx.x == 0) best = ~0ull;
     __syncthreads();
-    const int n = (int)threadIdx.x + 1, sms = p.st.sms;
-    if (n <= sms) {
+    const int sms = p.st.sms;
+    for (int n = (int)threadIdx.x + 1; n <= sms; n += kPlanThreads) {
         const float tiles = 12.f + line * (2.6f / kPairCost) / (float)n;
         const float bytes = own_keys * (float)p.Hkv * (float)p.D * 4.f;
         const float beside = fminf(6e6f, (float)(sms - n) * p.st.own_rate);
         const float after = fminf(6e6f, (float)sms * p.st.own_rate);
         const float t = tiles + fmaxf(0.f, bytes - beside * tiles) / after;
         // (positive floats compare as integers; of equal times the larger number)
-        atomicMin(&best, ((unsigned long long)__float_as_uint(t) << 32) | (unsigned)(kPlanThreads - n));
+        atomicMin(&best, ((unsigned long long)__float_as_uint(t) << 32) | (unsigned)(sms - n));
     }
     __syncthreads();
-    return kPlanThreads - (int)(best & 0xffffffffu);
+    return sms - (int)(best & 0xffffffffu);
 }
 
-// One CTA: a few arrays of a few hundred entries, 2 to 3 us, before the kernels that read them.
+// One CTA, before the kernels that read what it writes: a few microseconds, the latency of the
+// loads at its start and of the sums.  Batches of up to kPlanThreads sequences keep every array
+// in shared memory on the way (longer ones in the workspace).
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParams p) {
     allow_dependent_launch();
+    constexpr int N = kPlanThreads;
+    __shared__ int s_starts[N + 1], s_pre[N], s_len[N], s_before[N + 1], s_group[N], s_rows[N],
+        s_blocks[N], s_weight[N], s_cost[N], s_first[N + 1];
     const SharedStream &st = p.st;
     const int tid = (int)threadIdx.x;
-    // What later steps read back, in shared memory where the batch is not too long for it.
-    __shared__ int s_before[kPlanThreads + 1], s_group[kPlanThreads], s_rows[kPlanThreads],
-        s_blocks[kPlanThreads];
-    const bool small = p.B <= kPlanThreads;
+    const bool small = p.B <= N;  // (and as many groups at most)
+    const int *const starts = small ? s_starts : st.group_starts;
+    const int *const pre_lens = small ? s_pre : st.prefix_lens, *const lens = small ? s_len : p.seq_lens;
     int *const before = small ? s_before : st.before, *const group_of = small ? s_group : st.group;
     int *const rows_of = small ? s_rows : st.rows, *const blocks_of = small ? s_blocks : st.blocks;
+    int *const weight_of = small ? s_weight : st.weight, *const cost_of = small ? s_cost : st.head_cost;
+    int *const first_of = small ? s_first : st.first;
+    const int max_prefix = st.max_prefix_pages * p.P, max_ctx = p.max_pages * p.P;
+
     bool wrong = false;
-    for (int n = tid; n < st.n_groups; n += kPlanThreads) {
+    for (int n = tid; n < st.n_groups; n += N) {
         const int a = st.group_starts[n], z = st.group_starts[n + 1];
         wrong |= a < 0 || z < a || z > p.B;
+        if (small) {
+            s_starts[n] = a;
+            s_starts[n + 1] = z;  // (the same value from two threads)
+            s_pre[n] = st.prefix_lens[n];
+        }
+    }
+    int my_qn = 0, mine = 0;
+    if (tid < p.B) {
+        my_qn = p.q_lens ? p.q_lens[tid] : p.q_len;
+        mine = p.seq_lens[tid];
+        if (small) s_len[tid] = mine;
     }
     const bool bad = __syncthreads_or(wrong) != 0;
     uint32_t flags = bad ? ATLAS_DEV_BAD_SEQLEN : 0u;
 
     // sequences: their groups, and the rows before them
-    int64_t carry = 0;
-    float own_keys = 0.f;
-    for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    int64_t carry = 0, own_keys = 0;
+    for (int b0 = 0; b0 < p.B; b0 += N) {
         const int b = b0 + tid;
-        int rows = 0;
+        int rows = 0, own = 0;
         if (b < p.B) {
             int group = -1;
             if (!bad) {
                 int lo = -1, hi = st.n_groups - 1;  // the last group that starts at b or before
                 while (lo < hi) {
                     const int mid = (lo + hi + 1) / 2;
-                    if (st.group_starts[mid] <= b) lo = mid;
+                    if (starts[mid] <= b) lo = mid;
                     else hi = mid - 1;
                 }
-                if (lo >= 0 && b < st.group_starts[lo + 1]) group = lo;
+                if (lo >= 0 && b < starts[lo + 1]) group = lo;
             }
             group_of[b] = group;
-            st.group[b] = group;
-            const int qn = p.q_lens ? p.q_lens[b] : p.q_len;
-            const int len = p.seq_lens[b];
-            if (len > 0 && len <= p.max_pages * p.P) own_keys += (float)len;
+            const int qn = b0 == 0 ? my_qn : p.q_lens ? p.q_lens[b] : p.q_len;
+            const int len = b0 == 0 ? mine : p.seq_lens[b];
+            if (len > 0 && len <= max_ctx) own = len;
             bool good = qn >= 0 && qn <= p.q_len && !bad;
             if (st.whole) {
-                int pre = 0;
-                if (group >= 0) {
-                    pre = st.prefix_lens[group];
-                    good = good && pre >= 0 && pre <= st.max_prefix_pages * p.P;
-                }
-                good = good && len >= qn && len <= p.max_pages * p.P;
+                const int pre = group >= 0 ? pre_lens[group] : 0;
+                good = good && pre >= 0 && pre <= max_prefix && len >= qn && len <= max_ctx;
                 blocks_of[b] = good ? (pre + 127) / 128 + (len + 127) / 128 : -1;
-                st.blocks[b] = blocks_of[b];
                 if (!good) flags |= ATLAS_DEV_BAD_SEQLEN;
+                rows_of[b] = good ? p.G * qn : 0;
             }
             rows = good ? p.G * qn : 0;
-            if (st.whole) rows_of[b] = st.rows[b] = rows;
-            // (the rows of a group, head after head of one query's: the merge counts alike)
         }
+        // (both sums in one scan: rows below 2^31, own keys below 2^31 a round)
         int64_t total;
-        const int64_t upto = plan_scan(rows, total);
-        if (b < p.B) before[b] = st.before[b] = (int)(carry + upto - rows);
-        carry += total;
+        const int64_t upto = plan_scan((int64_t)rows << 32 | (uint32_t)own, total);
+        if (b < p.B) before[b] = (int)(carry + (upto >> 32) - rows);
+        carry += total >> 32;
+        own_keys += (uint32_t)total;
     }
-    if (tid == 0) before[p.B] = st.before[p.B] = (int)carry;
-    own_keys = plan_sum(own_keys);
+    if (tid == 0) before[p.B] = (int)carry;
+    __syncthreads();
 
-    // units: their tiles, and what all of them have
-    int most = 0;
-    int64_t all = 0;
+    // units: their rows and blocks, and what all of them have
     auto head_cost = [&](int rows, int nb) {  // tiles of one kv head, each counting as nb blocks
         if (st.tile_rows != 256) return (rows + 127) / 128 * kSingleCost * nb;
         const int last = rows % 256;
         return (rows / 256 * kPairCost + (last == 0 ? 0 : last <= 128 ? kSingleCost : kPairCost)) * nb;
     };
-    for (int u0 = 0; u0 < st.units; u0 += kPlanThreads) {
+    __shared__ int s_most;
+    if (tid == 0) s_most = 0;
+    int64_t all = 0;
+    for (int u0 = 0; u0 < st.units; u0 += N) {
         const int u = u0 + tid;
-        int64_t blocks = 0;
+        int64_t length = 0;
+        int nb = 0;
         if (u < st.units) {
             if (!st.whole) {
-                const int len = st.prefix_lens[u];
-                const bool good = len >= 0 && len <= st.max_prefix_pages * p.P && !bad;
+                const int len = pre_lens[u];
+                const bool good = len >= 0 && len <= max_prefix && !bad;
                 if (!good) flags |= ATLAS_DEV_BAD_SEQLEN;
-                rows_of[u] = st.rows[u] =
-                    good ? before[st.group_starts[u + 1]] - before[st.group_starts[u]] : 0;
-                blocks_of[u] = st.blocks[u] = good ? (len + 127) / 128 : -1;
+                rows_of[u] = good ? before[starts[u + 1]] - before[starts[u]] : 0;
+                blocks_of[u] = good ? (len + 127) / 128 : -1;
             }
-            const int tiles = (rows_of[u] + st.tile_rows - 1) / st.tile_rows;
-            st.tiles[u] = tiles;
-            const int nb = max(blocks_of[u], 0);
-            if (tiles > 0) {
-                most = max(most, nb);
-                if (nb > 0) blocks = (int64_t)head_cost(rows_of[u], nb + kTileBlocks) * p.Hkv;
+            if (rows_of[u] > 0 && blocks_of[u] > 0) {
+                nb = blocks_of[u];
+                length = (int64_t)head_cost(rows_of[u], nb + kTileBlocks) * p.Hkv;
             }
         }
+        nb = __reduce_max_sync(0xffffffffu, nb);
         int64_t total;
-        plan_scan(blocks, total);
+        plan_scan(length, total);
+        if (tid % 32 == 0 && nb > 0) atomicMax(&s_most, nb);  // (zeroed before the scan's barriers)
         all += total;
     }
-    most = plan_max(most);
+    __syncthreads();
+    const int most = s_most;
     // A CTA's share: one CTA for each SM, few enough states of a tile, and few enough pieces of a
     // CTA, for which short tiles count as more blocks than they have.
-    const int ctas = st.own_rate > 0.f ? ctas_beside(p, (float)all, own_keys) : st.sms;
-    int64_t per = (all + ctas - 1) / ctas;
-    per = max(per, (int64_t)kMinBlocks * kPairCost);
-    per = max(per, (int64_t)((most + st.max_states - 3) / (st.max_states - 2)) * kPairCost);
-    const int least = (int)((per + kSingleCost * (st.max_items - 2) - 1) / (kSingleCost * (st.max_items - 2)));
+    const int ctas = st.own_rate > 0.f ? ctas_beside(p, (float)all, (float)own_keys) : st.sms;
+    int64_t per64 = (all + ctas - 1) / ctas;
+    per64 = max(per64, (int64_t)kMinBlocks * kPairCost);
+    per64 = max(per64, (int64_t)((most + st.max_states - 3) / (st.max_states - 2)) * kPairCost);
+    const int per = (int)per64;
+    const int least = (per + kSingleCost * (st.max_items - 2) - 1) / (kSingleCost * (st.max_items - 2));
     carry = 0;
-    for (int u0 = 0; u0 < st.units; u0 += kPlanThreads) {
+    for (int u0 = 0; u0 < st.units; u0 += N) {
         const int u = u0 + tid;
-        int64_t blocks = 0;
+        int64_t length = 0;
         if (u < st.units) {
-            const int tiles = (rows_of[u] + st.tile_rows - 1) / st.tile_rows;
-            const int nb = blocks_of[u] > 0 && tiles > 0 ? max(blocks_of[u] + kTileBlocks, least) : 0;
-            st.weight[u] = nb;
-            st.head_cost[u] = nb > 0 ? head_cost(rows_of[u], nb) : 1;
-            blocks = nb > 0 ? (int64_t)st.head_cost[u] * p.Hkv : 0;
+            const bool some = rows_of[u] > 0 && blocks_of[u] > 0;
+            const int nb = some ? max(blocks_of[u] + kTileBlocks, least) : 0;
+            weight_of[u] = nb;
+            cost_of[u] = some ? head_cost(rows_of[u], nb) : 1;
+            length = some ? (int64_t)cost_of[u] * p.Hkv : 0;
         }
         int64_t total;
-        const int64_t upto = plan_scan(blocks, total);
-        if (u < st.units) st.first[u] = (int)(carry + upto - blocks);
+        const int64_t upto = plan_scan(length, total);
+        if (u < st.units) first_of[u] = (int)(carry + upto - length);
         carry += total;
     }
+    const int line = (int)carry;
     if (tid == 0) {
-        st.first[st.units] = (int)carry;
-        st.head[0] = (int)per;
-        st.head[1] = (int)carry;
+        first_of[st.units] = line;
+        st.head[0] = per;
+        st.head[1] = line;
         st.head[2] = bad;
     }
     if (flags && p.status) atomicOr(p.status, flags);
+    __syncthreads();
+    if (small) {  // what the kernels behind read
+        for (int u = tid; u < st.units; u += N) {
+            st.rows[u] = rows_of[u];
+            st.blocks[u] = blocks_of[u];
+            st.weight[u] = weight_of[u];
+            st.head_cost[u] = cost_of[u];
+            st.first[u] = first_of[u];
+        }
+        if (tid == 0) st.first[st.units] = line;
+        if (tid < p.B) {
+            st.before[tid] = before[tid];
+            st.group[tid] = group_of[tid];
+        }
+        if (tid == 0) st.before[p.B] = before[p.B];
+    }
     if (!st.whole) {
-        __syncthreads();  // (first, weight and tiles of every unit are there)
-        for (int b = tid; b < p.B; b += kPlanThreads) {
+        for (int b = tid; b < p.B; b += N) {
             const int u = group_of[b];
             SeqInfo s{};
             if (bad) s.blocks = -1;
             else if (u >= 0) {
                 s.blocks = blocks_of[u];
-                s.row0 = before[b] - before[st.group_starts[u]];
-                s.first = st.first[u];
+                s.row0 = before[b] - before[starts[u]];
+                s.first = first_of[u];
                 s.rows = rows_of[u];
-                s.head_cost = st.head_cost[u];
-                s.weight = st.weight[u];
-                s.per = (int)per;
+                s.head_cost = cost_of[u];
+                s.weight = weight_of[u];
+                s.per = per;
             }
             reinterpret_cast<SeqInfo *>(st.info)[b] = s;
         }
         // The order of the sequences' own splits: the longest first, so that the CTAs left over
         // when the others are done are short ones.
         if (small) {
-            __syncthreads();  // (rows and blocks have been read)
-            int *const lens = s_rows;
-            const int mine = tid < p.B ? p.seq_lens[tid] : 0;
-            lens[tid] = mine;
-            __syncthreads();
             if (tid < p.B) {
                 int rank = 0;
+#pragma unroll 8
                 for (int k = 0; k < p.B; ++k) rank += lens[k] > mine || (lens[k] == mine && k < tid);
                 st.order[rank] = tid;
             }
         } else {
-            for (int b = tid; b < p.B; b += kPlanThreads) st.order[b] = b;
+            for (int b = tid; b < p.B; b += N) st.order[b] = b;
         }
+    }
+    // The CTAs' pieces, a CTA to a thread.
+    for (int64_t x = tid; x * per < line; x += N) {
+        const int end = (int)min((int64_t)line, (x + 1) * per);
+        SharedSeg *const segs = st.segs + x * st.max_items;
+        int n = 0, s = (int)x * per, lo = 0, hi = st.units - 1;
+        while (lo < hi) {  // the last unit that begins at s or before and is not empty
+            const int mid = (lo + hi + 1) / 2;
+            if (first_of[mid] <= s) lo = mid;
+            else hi = mid - 1;
+        }
+        int unit = lo;
+        const int full = st.tile_rows == 256 ? kPairCost : kSingleCost;
+        while (s < end && n < st.max_items) {
+            while (s >= first_of[unit + 1]) ++unit;
+            const int weight = weight_of[unit], rows = rows_of[unit];
+            const int tiles = (rows + st.tile_rows - 1) / st.tile_rows;
+            const int at = s - first_of[unit], hkv = at / cost_of[unit];
+            const int tile = min((at - hkv * cost_of[unit]) / (full * weight), tiles - 1);
+            SharedTile t{unit, hkv, tile, first_of[unit] + hkv * cost_of[unit] + tile * full * weight,
+                         block_cost(st, tile, rows), 0};
+            t.end = t.first + t.cost * weight;
+            SharedSeg g;
+            g.unit = unit;
+            g.hkv = hkv;
+            g.row0 = tile * st.tile_rows;
+            g.rows = rows;
+            g.group = st.whole ? group_of[unit] : unit;
+            g.len = g.group >= 0 ? pre_lens[g.group] : 0;
+            g.own = 0;
+            if (st.whole)
+                g.own = tile_own_keys(lens[unit], rows / p.G, g.row0, min(g.row0 + st.tile_rows, rows));
+            const int nb = (g.len + 127) / 128 + (g.own + 127) / 128;
+            g.blk0 = block_from(t, s);
+            g.nb = min(block_from(t, min(end, t.end)), nb) - g.blk0;
+            const int home = t.first / per;
+            g.state = st.whole && home == (t.first + (nb - 1) * t.cost) / per ? -1 : (int)x - home;
+            if (g.nb > 0) segs[n++] = g;
+            s = t.end;
+        }
+        st.counts[x] = n;
     }
 
     // ragged groups: their rows one after the other, no padding between
     if (st.list && p.q_lens) {
         const int lane = tid % 32;
-        for (int b = tid / 32; b < p.B; b += kPlanThreads / 32) {
+        for (int b = tid / 32; b < p.B; b += N / 32) {
             const int at = before[b], rows = before[b + 1] - at;
             const int qn = rows / p.G;
             for (int r = lane; r < rows; r += 32) {

@@ -69,8 +69,8 @@ def test_refusals(lib, S, kw):
 
 
 def test_workspace_holds_the_states_of_both_parts(lib):
-    # rows of 128 floats and (m, l): own 128 keys in splits of 64, prefix 256 in splits of 128
-    rows, own, pre = 4 * 8, 2, 2
+    # rows of 128 floats and (m, l): own 128 keys and a prefix of 256 in splits of 64
+    rows, own, pre = 4 * 8, 2, 4
     n = ws(lib, split_tokens=64)
     acc = rows * 128 * 4
     own_bytes = (own * acc + rows * own * 8 + 255) // 256 * 256
