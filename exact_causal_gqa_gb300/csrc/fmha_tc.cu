@@ -97,6 +97,9 @@ struct Cfg {
     static constexpr int kTileBytes = 128 * D * 2;    // a 128-row bf16 tile (Q, K or V)
     // K/V ring depth: the same bytes in flight for either head_dim
     static constexpr int kStages = (NT == 2 ? 2 : 3) * (128 / D);
+    // (SHARED pairs: a stage of V more.  Its loads come from memory beside others', and V, wanted
+    // a product later than K but freed as much later, has the least time for them.)
+    static constexpr int kStagesV = kStages + (SHARED && NT == 2 ? 128 / D : 0);
     static constexpr int kSB = NT == 2 ? 1 : 2;      // S buffers per tile
     // warps 0-3: K producer (and Q), MMA issuer, tail fix-up, V producer; then NT softmax
     // warpgroups.  Each SMSP holds 16K registers and 3 of the 12 warps (NT = 2):
@@ -107,15 +110,15 @@ struct Cfg {
     // V stages below K stages: the PV product's MN-major B descriptor strides by a
     // 16 KB slab, and every address it can form stays inside the allocation.
     static constexpr int OFF_V = OFF_Q + NT * kTileBytes;
-    static constexpr int OFF_K = OFF_V + kStages * kTileBytes;
+    static constexpr int OFF_K = OFF_V + kStagesV * kTileBytes;
     static constexpr int OFF_BAR = OFF_K + kStages * kTileBytes;
     // barrier indices
     static constexpr int B_Q = 0;
     static constexpr int B_KFULL = 1;
     static constexpr int B_KEMPTY = B_KFULL + kStages;
     static constexpr int B_VFULL = B_KEMPTY + kStages;
-    static constexpr int B_VEMPTY = B_VFULL + kStages;
-    static constexpr int B_SFULL = B_VEMPTY + kStages;  // [NT][kSB]
+    static constexpr int B_VEMPTY = B_VFULL + kStagesV;
+    static constexpr int B_SFULL = B_VEMPTY + kStagesV;  // [NT][kSB]
     static constexpr int B_PFULL = B_SFULL + NT * kSB;  // [NT]
     static constexpr int B_PVDONE = B_PFULL + NT;       // [NT]
     static constexpr int B_TAIL_READY = B_PVDONE + NT;  // single use
@@ -135,10 +138,7 @@ struct Cfg {
                                              : kItemSlots * (int)sizeof(TcWork);
     static constexpr int OFF_MASK = OFF_VOTE + 16;  // [2] words: items with a bad page id
     static constexpr int OFF_ITEMS = OFF_MASK + 8;
-    // SHARED, two tiles: 32 rows x 128 bytes for each softmax warp's output on its way
-    static constexpr int OFF_STAGE = (OFF_ITEMS + kItemBytes + 127) / 128 * 128;
-    static constexpr int kStageBytes = SHARED && NT == 2 ? 8 * 4096 : 0;
-    static constexpr int kSmem = OFF_STAGE + kStageBytes + 1024;  // + slack
+    static constexpr int kSmem = OFF_ITEMS + kItemBytes + 1024;  // + slack
     static_assert(kSmem <= 232448, "shared memory budget");
     // TMEM columns: NT=2 -> [S0 | O0 | S1 | O1]; NT=1 -> [S(buf 0) | S(buf 1) | O]
     __device__ static constexpr uint32_t s_col(int x, int b) {
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     if (SHARED && p.st.wait_first) wait_for_previous_grid();
     allow_dependent_launch();
     using C = Cfg<NT, D, SHARED>;
-    constexpr int S = C::kStages, SB = C::kSB;
+    constexpr int S = C::kStages, SV = C::kStagesV, SB = C::kSB;
     constexpr int kTileBytes = C::kTileBytes;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -534,6 +534,8 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         for (int s = 0; s < S; ++s) {
             mbar_init(BAR(C::B_KFULL + s), 1);
             mbar_init(BAR(C::B_KEMPTY + s), 1);
+        }
+        for (int s = 0; s < SV; ++s) {
             mbar_init(BAR(C::B_VFULL + s), 1);
             mbar_init(BAR(C::B_VEMPTY + s), 1);
         }
@@ -573,6 +575,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         const uint32_t ring = sb + (kv == 0 ? C::OFF_K : C::OFF_V);
         const int bar_full = kv == 0 ? C::B_KFULL : C::B_VFULL;
         const int bar_empty = kv == 0 ? C::B_KEMPTY : C::B_VEMPTY;
+        const int depth = kv == 0 ? S : SV;
         const int lp = 31 - __clz(p.P);  // log2(P)
         int g = 0;   // blocks of this ring issued so far (all items)
         int nq = 0;  // Q tile pairs loaded so far
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                 pages = PageIdCache{p.st.prefix_table + (int64_t)w.group * p.st.max_prefix_pages,
                                     (w.pre_len - 1) >> lp};
             for (int j = 0; j < w.nb; ++j) {
-                const int s = g % S, use = g / S;
+                const int s = g % depth, use = g / depth;
                 int kb = w.kv_begin + j * BN;
                 if constexpr (SHARED) {
                     const int jb = w.blk0 + j;
@@ -640,8 +643,8 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             // Let the copies in flight land before the CTA's shared memory goes away.
             if (kv == 0 && nq > 0)
                 mbar_wait_bounded(BAR(C::B_Q), (nq - 1) & 1, &no_abort, kWaitLimitNs);
-            for (int k = max(0, g - S); k < g; ++k)
-                mbar_wait_bounded(BAR(bar_full + k % S), (k / S) & 1, &no_abort, kWaitLimitNs);
+            for (int k = max(0, g - depth); k < g; ++k)
+                mbar_wait_bounded(BAR(bar_full + k % depth), (k / depth) & 1, &no_abort, kWaitLimitNs);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -711,7 +714,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                     for (int x = 0; x < NT; ++x)
                         if (ok && x < kTiles) ok = issue_s(j, x);
                 for (int j = 0; ok && j < nb; ++j) {
-                    const int G = g + j, s = G % S;
+                    const int G = g + j, s = G % SV;
 #pragma unroll
                     for (int x = 0; x < NT; ++x) {
                         if (x >= kTiles) break;
@@ -721,7 +724,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                             break;
                         }
                         if (x == 0) {
-                            if (!wait_warp(BAR(C::B_VFULL + s), (G / S) & 1, abort_flag)) {
+                            if (!wait_warp(BAR(C::B_VFULL + s), (G / SV) & 1, abort_flag)) {
                                 ok = false;
                                 break;
                             }
@@ -834,7 +837,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             for (int j = SHARED ? 0 : w.nb - 1; j < w.nb; ++j) {
                 const int first = SHARED ? block_keys(w, j) : w.tail_fix ? w.tail_first : BN;
                 if (first == BN) continue;
-                const int s = (g + j) % S;
+                const int s = (g + j) % SV;
                 if (wait_warp(BAR(C::B_TAIL_READY), ntail & 1, abort_flag)) {
                     const uint32_t vbase = sb + C::OFF_V + s * kTileBytes;
                     constexpr int kChunks = 8 * C::kSlabs;  // 16-byte chunks per V row
@@ -867,17 +870,19 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         const uint32_t to = tl + C::o_col(x);
         // SHARED: Q rows of many sequences; each warp copies its own 32 rows to where the tile's
         // TMA load would put them (rows past the unit's last are zero).
+        int next_row = -1;  // this thread's output row of the tile whose Q was copied last
         auto copy_q = [&](const TcWork &w) {
             constexpr int kChunks = D / 8;  // 16-byte chunks of a row
             const uint32_t qt = sb + C::OFF_Q + x * kTileBytes;
             const int f = (w.t0 + x * w.tstep) * BM + r;
-            const int64_t mine = f < w.rows_unit ? row_of(w, f) : -1;  // (one lookup a lane)
+            const int mine = f < w.rows_unit ? (int)row_of(w, f) : -1;  // (one lookup a lane)
+            next_row = mine;
 #pragma unroll
             for (int k = 0; k < kChunks; ++k) {
                 const int at = k * (32 / kChunks) + lane / kChunks, ch = lane % kChunks;
-                const int64_t row = __shfl_sync(0xffffffffu, mine, at);
+                const int row = __shfl_sync(0xffffffffu, mine, at);
                 const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
-                                           (row < 0 ? 0 : row) * D + ch * 8;
+                                           (int64_t)max(row, 0) * D + ch * 8;
                 cp_async16(qt + (ch / 8) * kSlab + sw128(q4 * 32 + at, ch % 8), src, row < 0 ? 0u : 16u);
             }
             cp_async_commit();
@@ -922,6 +927,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         int left = !valid || !SHARED ? 0
                    : own_from > 0    ? w.pre_len - w.blk0 * BN
                                      : lim_row + own_from * BN;
+        const int my_row = next_row;          // (SHARED)
         const bool one = single(w);           // SHARED: no second tile,
         const bool idle = one && x > 0;       // and this warpgroup has none
         for (int j = 0; j < nb && !idle; ++j) {
@@ -1193,7 +1199,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         tc_fence_after();
         if (ok) {
             Item w = item(it);  // (from shared memory again: not held over the blocks)
-            const int64_t row = row_of(w, valid ? f : 0);
+            const int64_t row = SHARED ? max(my_row, 0) : row_of(w, valid ? f : 0);
             // Direct mode folds the sink (one more state: m = sink log2 e, l = 1,
             // acc = 0) here; split mode leaves it to the merge.
             const bool part = SHARED ? c >= 0 : p.split != 0;  // a partial state, or the output
@@ -1216,7 +1222,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             // staging area (tile 0: the Q tiles; tile 1: the V stages, written once its
             // own PV is done).
             // (SHARED: only after the CTA's last item, where nothing lands any more.)
-            const bool staged = SHARED && NT == 1 && last;
+            const bool staged = SHARED && last;
             const bool wide = (SHARED ? part : p.split) || !p.out_bf16;  // fp32 rows, else bf16 rows
             const int rb = wide ? D * 4 : D * 2;       // bytes per output row
             const uint32_t stage = sb + (uint32_t)(x * 4 + q4) * (32u * D * 4u);
@@ -1226,47 +1232,6 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                 uint32_t o[32];
                 tmem_ld32(to + cc * 32, o);
                 tmem_wait_ld();
-                if constexpr (SHARED && NT == 2) {
-                    // 32 columns of the warp's rows through the warp's own staging: whole lines
-                    // to global memory, 4 rows (fp32) or 8 rows (bf16) an instruction.
-                    const uint32_t mine = sb + C::OFF_STAGE + (uint32_t)(x * 4 + q4) * 4096u;
-                    const int per_row = wide ? 8 : 4, lg = wide ? 3 : 2;  // 16-byte chunks
-                    __syncwarp();
-                    if (wide) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            st_shared_v4(mine + lane * 128 + ((k ^ (lane & 7)) << 4),
-                                         __float_as_uint(__uint_as_float(o[4 * k]) * inv),
-                                         __float_as_uint(__uint_as_float(o[4 * k + 1]) * inv),
-                                         __float_as_uint(__uint_as_float(o[4 * k + 2]) * inv),
-                                         __float_as_uint(__uint_as_float(o[4 * k + 3]) * inv));
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            st_shared_v4(mine + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4),
-                                         pack_bf16(__uint_as_float(o[8 * k + 0]) * inv,
-                                                   __uint_as_float(o[8 * k + 1]) * inv),
-                                         pack_bf16(__uint_as_float(o[8 * k + 2]) * inv,
-                                                   __uint_as_float(o[8 * k + 3]) * inv),
-                                         pack_bf16(__uint_as_float(o[8 * k + 4]) * inv,
-                                                   __uint_as_float(o[8 * k + 5]) * inv),
-                                         pack_bf16(__uint_as_float(o[8 * k + 6]) * inv,
-                                                   __uint_as_float(o[8 * k + 7]) * inv));
-                    }
-                    __syncwarp();
-                    uint8_t *const to = part ? reinterpret_cast<uint8_t *>(p.ws_acc) : static_cast<uint8_t *>(p.out);
-                    const int64_t my = valid ? (part ? slot : row) : -1;
-#pragma unroll 2
-                    for (int k = 0; k < per_row; ++k) {
-                        const int at = (k << (5 - lg)) + (lane >> lg), ch = lane & (per_row - 1);
-                        const int64_t dst = __shfl_sync(0xffffffffu, my, at);
-                        const uint4 v = ld_shared_v4(mine + (wide ? at * 128 + ((ch ^ (at & 7)) << 4)
-                                                                  : at * 64 + ((ch ^ ((at >> 1) & 3)) << 4)));
-                        if (dst >= 0)
-                            *reinterpret_cast<uint4 *>(to + ((dst * D + cc * 32) << (wide ? 2 : 1)) + ch * 16) = v;
-                    }
-                    continue;
-                }
                 if (PERSIST && !staged) {
                     // The next item's Q and K/V are landing in shared memory: rows go
                     // straight from registers (direct mode), in 32-byte stores when the

@@ -58,12 +58,16 @@ constexpr int64_t kWholeRows = 128;
 // SMs ask for memory.
 constexpr float kOwnRate = 70e3f, kOwnRateWide = 50e3f;
 
-// Whether the split kernels take less time: the prefix once for each CTA's rows, against a
-// second launch's start and the prefix once.
+// Whether the split kernels take less time: the prefixes once for each CTA's rows, against the
+// plan's launch, a longer start, and the prefixes once.  Fitted to 36 measured sizes: bf16, 32 / 8
+// heads of 128, one prefix, split kernels and tensor cores: 8 sequences behind 1024 keys 22 and 42
+// us, behind 32768 59 and 73; 16 behind 8192 46 and 48; 32 behind 8192 72 and 48; 64 behind 1024 44
+// and 44, behind 32768 315 and 83.  fp32: 8 behind 1024 28 and 48, behind 8192 79 and 56.
 bool split_pays(double prefix_bytes, int64_t tiles, double flops, bool f32) {
-    const double rate = 6.5e6, start = 9.0;  // bytes and floating point operations a microsecond
-    const double tc = start + std::max(prefix_bytes / rate, flops / (f32 ? 1.2e8 : 9e8));
-    return (double)tiles * prefix_bytes / rate <= tc;
+    // bytes and floating point operations a microsecond
+    const double tc = f32 ? 22.0 + std::max(prefix_bytes / 2.9e6, flops / 1.2e8)
+                          : 18.0 + std::max(prefix_bytes / 5e6, flops / 9e8);
+    return (double)tiles * prefix_bytes / (f32 ? 5e6 : 6e6) <= tc;
 }
 
 atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const atlas_shared *S,

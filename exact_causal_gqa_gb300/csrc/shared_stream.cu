@@ -11,7 +11,7 @@ namespace atlas {
 namespace {
 
 constexpr int kPlanThreads = 512;
-constexpr int kMinBlocks = 4;  // a CTA's share at least: below, its start outweighs it
+constexpr int kMinBlocks = 2;  // a CTA's share at least: below, its start outweighs it
 
 // Inclusive sums of x over the CTA, and the total.
 __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t &total) {
