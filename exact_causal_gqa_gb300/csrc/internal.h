@@ -141,6 +141,12 @@ struct SharedSeg {
     int group;             // whose prefix (-1: none)
 };
 
+// A tile over whole keys (st.whole) that is cut first behind the CTA that it begins in: its rows,
+// and the CTAs that have blocks of it (0: none is).
+struct SharedCut {
+    int unit, hkv, row0, rows, states;
+};
+
 // The tiles of a call with shared prefixes on the tensor cores, cut evenly among CTAs
 // (shared_prefix.cuh).  Arrays in the workspace, written by the plan kernel.
 struct SharedStream {
@@ -166,6 +172,7 @@ struct SharedStream {
     int32_t *list;       // ragged groups: [batch * G * q_len] the rows (of kv head 0), or null
     SharedSeg *segs;     // [CTAs][max_items] the CTAs' pieces,
     int32_t *counts;     // [CTAs] and how many
+    SharedCut *cuts;     // whole: [CTAs] the tile that is cut behind each
     int32_t *order;      // [batch] the sequences, those of most own keys first
     int32_t *info;       // [batch][8]: what the merge wants to know of a sequence (SeqInfo)
     int32_t wait_first;  // 1: wait for the grid before at the start, 0: at the end (the plan's is

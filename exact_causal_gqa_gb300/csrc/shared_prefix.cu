@@ -136,7 +136,8 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
         plan->ml_at = plan->acc_at + (size_t)round_up(states * D * 4, 256);
         plan->plan_at = plan->ml_at + (size_t)round_up(states * 8, 256);
         const int64_t n = plan->whole ? L->batch : S->n_groups;
-        const int64_t segs = 1 + shared_tc_items(plan->tiles) * (int64_t)(sizeof(SharedSeg) / 4);
+        const int64_t segs = 1 + shared_tc_items(plan->tiles) * (int64_t)(sizeof(SharedSeg) / 4) +
+                             (int64_t)(sizeof(SharedCut) / 4);
         plan->bytes = plan->plan_at + 4 * (size_t)(11 * (int64_t)L->batch + 4 + 5 * n + 2 +
                                                    plan->ctas * segs + (plan->whole ? 0 : rows));
         return ATLAS_OK;
@@ -301,6 +302,7 @@ SharedStream stream_arrays(const SharedPlan &plan, int32_t G, const atlas_shared
     st.order = take(L->batch);
     st.counts = take(plan.ctas);
     st.segs = reinterpret_cast<SharedSeg *>(take(plan.ctas * st.max_items * (int64_t)(sizeof(SharedSeg) / 4)));
+    st.cuts = reinterpret_cast<SharedCut *>(take(plan.ctas * (int64_t)(sizeof(SharedCut) / 4)));
     st.list = !plan.whole && L->q_lens ? take((int64_t)L->batch * G * L->q_len) : nullptr;
     return st;
 }

@@ -125,61 +125,12 @@ __device__ __forceinline__ int tile_own_keys(int seq_len, int qn, int row0, int 
 }
 
 struct SharedTile {
-    int unit, hkv, tile;
-    int first, cost, end;  // where it begins in the line, the length of its blocks, where it ends
+    int tile, first, cost, end;  // where it begins in the line, the length of its blocks, its end
 };
-
-// Tiles of 256 rows but a unit's last, which may be a single.
-__device__ __forceinline__ void place_tile(const SharedStream &st, SharedTile &t) {
-    const int weight = st.weight[t.unit], rows = st.rows[t.unit];
-    const int full = st.tile_rows == 256 ? kPairCost : kSingleCost;
-    t.first = st.first[t.unit] + t.hkv * st.head_cost[t.unit] + t.tile * full * weight;
-    t.cost = block_cost(st, t.tile, rows);
-    t.end = t.first + t.cost * weight;
-}
-
-// The tile at a place of the line (before its end).  A whole warp calls this with the same place;
-// lane k looks at units k, k + 32, ...
-__device__ __forceinline__ SharedTile tile_of(const SharedStream &st, int place) {
-    SharedTile t{};
-    for (int u0 = 0; u0 < st.units; u0 += 32) {
-        const int u = u0 + (int)(threadIdx.x % 32);
-        const bool here = u < st.units && st.first[u] <= place && place < st.first[u + 1];
-        const unsigned who = __ballot_sync(0xffffffffu, here);
-        if (who) {
-            t.unit = u0 + __ffs(who) - 1;
-            break;
-        }
-    }
-    const int at = place - st.first[t.unit], per_head = st.head_cost[t.unit];
-    const int full = (st.tile_rows == 256 ? kPairCost : kSingleCost) * st.weight[t.unit];
-    t.hkv = at / per_head;
-    t.tile = min((at - t.hkv * per_head) / full,
-                 (st.rows[t.unit] + st.tile_rows - 1) / st.tile_rows - 1);
-    place_tile(st, t);
-    return t;
-}
 
 // The first of a tile's blocks that begins at the place or behind it.
 __device__ __forceinline__ int block_from(const SharedTile &t, int place) {
     return (max(place - t.first, 0) + t.cost - 1) / t.cost;
-}
-
-// Blocks of a tile that have keys for its rows.
-template <typename Params>
-__device__ __forceinline__ int tile_blocks(const Params &p, const SharedTile &t, SharedSeg &s) {
-    const SharedStream &st = p.st;
-    s.unit = t.unit;
-    s.hkv = t.hkv;
-    s.row0 = t.tile * st.tile_rows;
-    s.rows = st.rows[t.unit];
-    s.group = st.whole ? st.group[t.unit] : t.unit;
-    s.len = s.group >= 0 ? st.prefix_lens[s.group] : 0;
-    s.own = 0;
-    if (st.whole)
-        s.own = tile_own_keys(p.seq_lens[t.unit], p.q_lens ? p.q_lens[t.unit] : p.q_len, s.row0,
-                              min(s.row0 + st.tile_rows, s.rows));
-    return (s.len + 127) / 128 + (s.own + 127) / 128;
 }
 
 // Output row of row f of a unit.

@@ -6,6 +6,7 @@
 #include "shared_prefix.cuh"
 
 #include <math.h>
+#include <type_traits>
 
 namespace atlas {
 namespace {
@@ -42,10 +43,9 @@ __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t &total) {
 // 64.  Times measured: a pair's block 2.6 us beside the splits and a CTA's start and end 12;
 // memory 6 MB a microsecond at most.
 __device__ int ctas_beside(const TcParams &p, float line, float own_keys) {
-    __shared__ unsigned long long best;
-    if (threadIdx.x == 0) best = ~0ull;
-    __syncthreads();
+    __shared__ uint64_t best[kPlanThreads / 32];
     const int sms = p.st.sms;
+    uint64_t mine = ~0ull;
     for (int n = (int)threadIdx.x + 1; n <= sms; n += kPlanThreads) {
         const float tiles = 12.f + line * (2.6f / kPairCost) / (float)n;
         const float bytes = own_keys * (float)p.Hkv * (float)p.D * 4.f;
@@ -53,10 +53,15 @@ __device__ int ctas_beside(const TcParams &p, float line, float own_keys) {
         const float after = fminf(6e6f, (float)sms * p.st.own_rate);
         const float t = tiles + fmaxf(0.f, bytes - beside * tiles) / after;
         // (positive floats compare as integers; of equal times the larger number)
-        atomicMin(&best, ((unsigned long long)__float_as_uint(t) << 32) | (unsigned)(sms - n));
+        mine = min(mine, ((uint64_t)__float_as_uint(t) << 32) | (unsigned)(sms - n));
     }
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) mine = min(mine, __shfl_xor_sync(0xffffffffu, mine, d));
+    if (threadIdx.x % 32 == 0) best[threadIdx.x / 32] = mine;
     __syncthreads();
-    return sms - (int)(best & 0xffffffffu);
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) mine = min(mine, best[w]);
+    return sms - (int)(mine & 0xffffffffu);
 }
 
 // One CTA, before the kernels that read what it writes: a few microseconds, the latency of the
@@ -204,23 +209,78 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
     }
     if (flags && p.status) atomicOr(p.status, flags);
     __syncthreads();
-    if (small) {  // what the kernels behind read
-        for (int u = tid; u < st.units; u += N) {
-            st.rows[u] = rows_of[u];
-            st.blocks[u] = blocks_of[u];
-            st.weight[u] = weight_of[u];
-            st.head_cost[u] = cost_of[u];
-            st.first[u] = first_of[u];
+    // What the kernels behind read, by three groups of warps side by side.
+    constexpr int kSegThreads = 192, kInfoThreads = 128, kListThreads = N - kSegThreads - kInfoThreads;
+    if (tid < kSegThreads) {
+        // The CTAs' pieces, a CTA to a thread, and the tiles that begin in the CTA before and are cut.
+        const int full = st.tile_rows == 256 ? kPairCost : kSingleCost;
+        for (int64_t x = tid; x * per < line; x += kSegThreads) {
+            const int begin = (int)(x * per), end = (int)min((int64_t)line, (x + 1) * per);
+            SharedSeg *const segs = st.segs + x * st.max_items;
+            int n = 0, s = begin, lo = 0, hi = st.units - 1;
+            while (lo < hi) {  // the last unit that begins at s or before
+                const int mid = (lo + hi + 1) / 2;
+                if (first_of[mid] <= s) lo = mid;
+                else hi = mid - 1;
+            }
+            SharedSeg g;
+            SharedTile t;
+            int tiles = 0, weight = 0;
+            for (g.unit = lo - 1; s < end && n < st.max_items; s = t.end) {
+                if (g.unit < lo || s >= first_of[g.unit + 1]) {  // a unit's first, or the CTA's
+                    do ++g.unit;
+                    while (s >= first_of[g.unit + 1]);
+                    lo = g.unit;
+                    weight = weight_of[g.unit];
+                    g.rows = rows_of[g.unit];
+                    tiles = (g.rows + st.tile_rows - 1) / st.tile_rows;
+                    const int at = s - first_of[g.unit];
+                    g.hkv = at / cost_of[g.unit];
+                    t.tile = min((at - g.hkv * cost_of[g.unit]) / (full * weight), tiles - 1);
+                    g.group = st.whole ? group_of[g.unit] : g.unit;
+                    g.len = g.group >= 0 ? pre_lens[g.group] : 0;
+                } else if (++t.tile == tiles) {
+                    t.tile = 0;
+                    ++g.hkv;
+                }
+                t.cost = block_cost(st, t.tile, g.rows);
+                t.first = first_of[g.unit] + g.hkv * cost_of[g.unit] + t.tile * full * weight;
+                t.end = t.first + t.cost * weight;
+                g.row0 = t.tile * st.tile_rows;
+                g.own = !st.whole ? 0
+                                  : tile_own_keys(lens[g.unit], g.rows / p.G, g.row0,
+                                                  min(g.row0 + st.tile_rows, g.rows));
+                const int nb = (g.len + 127) / 128 + (g.own + 127) / 128;
+                g.blk0 = block_from(t, s);
+                g.nb = min(block_from(t, min(end, t.end)), nb) - g.blk0;
+                const int home = t.first / per, last = (t.first + (nb - 1) * t.cost) / per;
+                g.state = st.whole && home == last ? -1 : (int)x - home;
+                if (st.whole && s == begin && x > 0) {
+                    const bool cut = t.first < begin && home == x - 1 && last > home;
+                    st.cuts[x - 1] = {g.unit, g.hkv, g.row0, g.rows, cut ? last - home + 1 : 0};
+                }
+                if (g.nb > 0) segs[n++] = g;
+            }
+            st.counts[x] = n;
         }
-        if (tid == 0) st.first[st.units] = line;
-        if (tid < p.B) {
-            st.before[tid] = before[tid];
-            st.group[tid] = group_of[tid];
+    } else if (tid < kSegThreads + kInfoThreads) {
+        const int me = tid - kSegThreads;
+        if (!small) {
+            for (int b = me; b < p.B && !st.whole; b += kInfoThreads) st.order[b] = b;
+        } else {
+            // The order of the sequences' own splits: the longest first, so that the CTAs left
+            // over when the others are done are short ones.
+            for (int b = me; b < p.B && !st.whole; b += kInfoThreads) {
+                const int mine = lens[b];
+                int rank = 0;
+#pragma unroll 8
+                for (int k = 0; k < p.B; ++k) rank += lens[k] > mine || (lens[k] == mine && k < b);
+                st.order[rank] = b;
+            }
+            for (int b = me; b <= p.B; b += kInfoThreads) st.before[b] = before[b];
+            for (int u = me; u < st.units && st.whole; u += kInfoThreads) st.blocks[u] = blocks_of[u];
         }
-        if (tid == 0) st.before[p.B] = before[p.B];
-    }
-    if (!st.whole) {
-        for (int b = tid; b < p.B; b += N) {
+        for (int b = me; b < p.B && !st.whole; b += kInfoThreads) {
             const int u = group_of[b];
             SeqInfo s{};
             if (bad) s.blocks = -1;
@@ -235,65 +295,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
             }
             reinterpret_cast<SeqInfo *>(st.info)[b] = s;
         }
-        // The order of the sequences' own splits: the longest first, so that the CTAs left over
-        // when the others are done are short ones.
-        if (small) {
-            if (tid < p.B) {
-                int rank = 0;
-#pragma unroll 8
-                for (int k = 0; k < p.B; ++k) rank += lens[k] > mine || (lens[k] == mine && k < tid);
-                st.order[rank] = tid;
-            }
-        } else {
-            for (int b = tid; b < p.B; b += N) st.order[b] = b;
-        }
-    }
-    // The CTAs' pieces, a CTA to a thread.
-    for (int64_t x = tid; x * per < line; x += N) {
-        const int end = (int)min((int64_t)line, (x + 1) * per);
-        SharedSeg *const segs = st.segs + x * st.max_items;
-        int n = 0, s = (int)x * per, lo = 0, hi = st.units - 1;
-        while (lo < hi) {  // the last unit that begins at s or before and is not empty
-            const int mid = (lo + hi + 1) / 2;
-            if (first_of[mid] <= s) lo = mid;
-            else hi = mid - 1;
-        }
-        int unit = lo;
-        const int full = st.tile_rows == 256 ? kPairCost : kSingleCost;
-        while (s < end && n < st.max_items) {
-            while (s >= first_of[unit + 1]) ++unit;
-            const int weight = weight_of[unit], rows = rows_of[unit];
-            const int tiles = (rows + st.tile_rows - 1) / st.tile_rows;
-            const int at = s - first_of[unit], hkv = at / cost_of[unit];
-            const int tile = min((at - hkv * cost_of[unit]) / (full * weight), tiles - 1);
-            SharedTile t{unit, hkv, tile, first_of[unit] + hkv * cost_of[unit] + tile * full * weight,
-                         block_cost(st, tile, rows), 0};
-            t.end = t.first + t.cost * weight;
-            SharedSeg g;
-            g.unit = unit;
-            g.hkv = hkv;
-            g.row0 = tile * st.tile_rows;
-            g.rows = rows;
-            g.group = st.whole ? group_of[unit] : unit;
-            g.len = g.group >= 0 ? pre_lens[g.group] : 0;
-            g.own = 0;
-            if (st.whole)
-                g.own = tile_own_keys(lens[unit], rows / p.G, g.row0, min(g.row0 + st.tile_rows, rows));
-            const int nb = (g.len + 127) / 128 + (g.own + 127) / 128;
-            g.blk0 = block_from(t, s);
-            g.nb = min(block_from(t, min(end, t.end)), nb) - g.blk0;
-            const int home = t.first / per;
-            g.state = st.whole && home == (t.first + (nb - 1) * t.cost) / per ? -1 : (int)x - home;
-            if (g.nb > 0) segs[n++] = g;
-            s = t.end;
-        }
-        st.counts[x] = n;
-    }
-
-    // ragged groups: their rows one after the other, no padding between
-    if (st.list && p.q_lens) {
+    } else if (st.list && p.q_lens) {
+        // ragged groups: their rows one after the other, no padding between
         const int lane = tid % 32;
-        for (int b = tid / 32; b < p.B; b += N / 32) {
+        for (int b = (tid - kSegThreads - kInfoThreads) / 32; b < p.B; b += kListThreads / 32) {
             const int at = before[b], rows = before[b + 1] - at;
             const int qn = rows / p.G;
             for (int r = lane; r < rows; r += 32) {
@@ -304,38 +309,35 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
     }
 }
 
-// The tiles that are cut (st.whole): the CTA's share of the rows of the tile that the line's
-// cut before block x n goes through, if that is the tile's first cut; and NaN for the sequences
-// that are out of range.
-constexpr int kCutWarps = 8;
+// The tiles that are cut (st.whole): kCutRows rows a warp of the tile that the line is cut in
+// before CTA blockIdx.x + 1, if that is the tile's first cut; and NaN for the sequences that are
+// out of range.
+constexpr int kCutWarps = 8, kCutRows = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kCutWarps * 32) shared_cut_merge_kernel(const TcParams p, int ctas) {
     constexpr int E = D / 32;  // (a lane's elements: one vector load)
+    using Part = std::conditional_t<E == 4, float4, float2>;
     const SharedStream &st = p.st;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     wait_for_previous_grid();
-    auto put = [&](int64_t row, const float (&o)[E], float lse) {
+    const float nan = __int_as_float(0x7fc00000);
+    auto put = [&](int64_t row, const float *o, float lse) {
         if (p.out_bf16) {
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row * D + lane * E;
 #pragma unroll
             for (int e = 0; e < E; e += 2)
                 *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(o[e], o[e + 1]);
         } else {
-            float *out = static_cast<float *>(p.out) + row * D + lane * E;
-#pragma unroll
-            for (int e = 0; e < E; e += 2)
-                *reinterpret_cast<float2 *>(out + e) = make_float2(o[e], o[e + 1]);
+            *reinterpret_cast<Part *>(static_cast<float *>(p.out) + row * D + lane * E) =
+                *reinterpret_cast<const Part *>(o);
         }
         if (lane == 0 && p.lse) p.lse[row] = lse;
     };
     if ((int)blockIdx.x >= ctas) {
         const int b = (int)blockIdx.x - ctas;
         if (st.blocks[b] >= 0) return;
-        const float nan = __int_as_float(0x7fc00000);
-        float o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = nan;
+        const float o[4] = {nan, nan, nan, nan};
         const int qn = p.q_lens ? p.q_lens[b] : p.q_len;
         const int rows = qn >= 0 && qn <= p.q_len ? qn : p.q_len;
         for (int64_t r = (int64_t)blockIdx.y * kCutWarps + warp; r < (int64_t)p.Hq * p.q_len;
@@ -343,62 +345,59 @@ __global__ void __launch_bounds__(kCutWarps * 32) shared_cut_merge_kernel(const 
             if (r % p.q_len < rows) put((int64_t)b * p.Hq * p.q_len + r, o, nan);
         return;
     }
-    const int per = st.head[0], x = (int)blockIdx.x + 1;
-    if ((int64_t)x * per >= st.head[1]) return;
-    const SharedTile t = tile_of(st, x * per);
-    if (t.first / per != x - 1) return;  // not cut here first
-    SharedSeg s;
-    const int nb = tile_blocks(p, t, s);
-    const int states = (t.first + (nb - 1) * t.cost) / per - (x - 1) + 1;
-    const int f = s.row0 + (int)blockIdx.y * kCutWarps + warp;
-    if (states < 2 || f >= s.rows) return;
-    // the first state is that of a tile's start, the others those of their CTAs' first pieces
-    auto slot = [&](int k) { return ((int64_t)(x - 1 + k) * 2 + (k == 0)) * st.tile_rows + f - s.row0; };
-    const int64_t row = unit_row(p, t.unit, t.hkv, f);
-    float M = p.sinks ? p.sinks[s.hkv * p.G + f / (s.rows / p.G)] * kLog2e : -INFINITY;
-    bool has_nan = isnan(M);
-    float sum = p.sinks ? 1.f : 0.f, o[E];
+    const int x = (int)blockIdx.x;  // the CTA that the tile begins in
+    const SharedCut cut = st.cuts[x];
+    if (((int64_t)x + 1) * st.head[0] >= st.head[1] || cut.states < 2) return;
+    const int f0 = cut.row0 + ((int)blockIdx.y * kCutWarps + warp) * kCutRows;
+    if (f0 >= cut.rows) return;
+    const int qn = cut.rows / p.G;
+    float M[kCutRows], sum[kCutRows];
+    __align__(16) float o[kCutRows][E];
+    bool has_nan[kCutRows];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    // Lane k has the weight of state k, of 32 at a time; the accumulators' loads of a few states
-    // are in flight together.
-    for (int k0 = 0; k0 < states; k0 += 32) {
-        const int k = k0 + lane;
-        float m = -INFINITY, l = 0.f;
-        if (k < states) {
-            const float2 ml = *reinterpret_cast<const float2 *>(p.ws_ml + slot(k) * 2);
-            m = ml.x;
-            l = ml.y;
+    for (int r = 0; r < kCutRows; ++r) {
+        const int f = min(f0 + r, cut.rows - 1);  // (rows past the last are not stored)
+        M[r] = p.sinks ? p.sinks[cut.hkv * p.G + f / qn] * kLog2e : -INFINITY;
+        has_nan[r] = isnan(M[r]);
+        sum[r] = p.sinks ? 1.f : 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[r][e] = 0.f;
+    }
+    for (int k = 0; k < cut.states; ++k) {
+        // the first state is that of a tile's start, the others those of their CTAs' first pieces
+        const int64_t slot = ((int64_t)(x + k) * 2 + (k == 0)) * st.tile_rows + f0 - cut.row0;
+        float2 ml[kCutRows];
+        __align__(16) float a[kCutRows][E];
+#pragma unroll
+        for (int r = 0; r < kCutRows; ++r) {
+            ml[r] = make_float2(0.f, 0.f);
+            if (f0 + r >= cut.rows) continue;
+            ml[r] = *reinterpret_cast<const float2 *>(p.ws_ml + (slot + r) * 2);
+            *reinterpret_cast<Part *>(a[r]) =
+                *reinterpret_cast<const Part *>(p.ws_acc + (slot + r) * D + lane * E);
         }
-        has_nan |= __any_sync(0xffffffffu, isnan(m) || isnan(l));
-        float top = l > 0.f ? m : -INFINITY;
 #pragma unroll
-        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        top = fmaxf(M, top);
-        const float old = M == -INFINITY ? 0.f : ex2(M - top), w = l > 0.f ? ex2(m - top) : 0.f;
-        M = top;
-        float add = w * l;
+        for (int r = 0; r < kCutRows; ++r) {
+            if (isnan(ml[r].x) || isnan(ml[r].y)) has_nan[r] = true;
+            if (!(ml[r].y > 0.f)) continue;
+            const float top = fmaxf(M[r], ml[r].x);
+            const float old = M[r] == -INFINITY ? 0.f : ex2(M[r] - top), w = ex2(ml[r].x - top);
+            sum[r] = fmaf(w, ml[r].y, sum[r] * old);
 #pragma unroll
-        for (int d = 16; d > 0; d /= 2) add += __shfl_xor_sync(0xffffffffu, add, d);
-        sum = sum * old + add;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] *= old;
-#pragma unroll 4
-        for (int j = 0; j < min(32, states - k0); ++j) {
-            const float wj = __shfl_sync(0xffffffffu, w, j);
-            const float *at = p.ws_acc + slot(k0 + j) * D + lane * E;
-            float a[E];
-            if constexpr (E == 4) *reinterpret_cast<float4 *>(a) = *reinterpret_cast<const float4 *>(at);
-            else *reinterpret_cast<float2 *>(a) = *reinterpret_cast<const float2 *>(at);
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = fmaf(wj, a[e], o[e]);
+            for (int e = 0; e < E; ++e) o[r][e] = fmaf(w, a[r][e], o[r][e] * old);
+            M[r] = top;
         }
     }
-    const float nan = __int_as_float(0x7fc00000);
-    const bool none = has_nan || M == -INFINITY;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = none ? nan : o[e] / sum;
-    put(row, o, none ? nan : kLn2 * (M + log2f(sum)));
+    for (int r = 0; r < kCutRows; ++r) {
+        if (f0 + r >= cut.rows) break;
+        const bool none = has_nan[r] || M[r] == -INFINITY;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[r][e] = none ? nan : o[r][e] / sum[r];
+        const int g = (f0 + r) / qn;
+        put(((int64_t)cut.unit * p.Hq + cut.hkv * p.G + g) * p.q_len + (f0 + r - g * qn), o[r],
+            none ? nan : kLn2 * (M[r] + log2f(sum[r])));
+    }
 }
 
 }  // namespace
@@ -409,7 +408,7 @@ cudaError_t launch_shared_plan(const TcParams &p, cudaStream_t stream) {
 }
 
 cudaError_t launch_shared_cut_merge(const TcParams &p, int64_t ctas, cudaStream_t stream) {
-    const dim3 grid((unsigned)(ctas + p.B), (unsigned)(p.st.tile_rows / kCutWarps));
+    const dim3 grid((unsigned)(ctas + p.B), (unsigned)(p.st.tile_rows / (kCutWarps * kCutRows)));
     return p.D == 128 ? launch_dependent(shared_cut_merge_kernel<128>, grid, dim3(kCutWarps * 32), 0,
                                          stream, p, (int)ctas)
                       : launch_dependent(shared_cut_merge_kernel<64>, grid, dim3(kCutWarps * 32), 0,
