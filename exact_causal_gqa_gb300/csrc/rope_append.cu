@@ -32,8 +32,7 @@
 // With norms (atlas_kv_append_norm_rope) each row of q and k is first divided by its root
 // mean square and multiplied by its weights, in the same pass and without a rounding between:
 //   y_j = x_j (mean_i x_i^2 + eps)^(-1/2) (w_j + offset),
-// the sum of squares in fp32 over the row's slots, which sit in neighbouring lanes, by
-// log2(slots) exchanges.
+// the sum of squares in fp32 over the row's lanes, by exchanges between them.
 #include "internal.h"
 
 #include <cuda_bf16.h>
@@ -153,79 +152,51 @@ struct TokenRows {
     bool any;  // a real token
 };
 
-// The elements of unit u of a row: a pair of the rotated part, or two neighbours behind it.
-__device__ __forceinline__ void unit_elements(const RopeParams &p, int u, int &e0, int &e1) {
-    const bool halves = u < p.pairs && !p.interleaved;
-    e0 = halves ? u : 2 * u;
-    e1 = halves ? u + p.pairs : 2 * u + 1;
+// Where a token's rows are read and written; what is out of range is reported.  `caches`: the
+// caller writes keys or values.
+__device__ __forceinline__ TokenRows token_rows(const RopeParams &p, int token, bool caches) {
+    const int b = token / p.n, j = token % p.n;
+    const int count = p.n_new ? p.n_new[b] : p.n;
+    uint32_t bad = 0;
+    TokenRows r;
+    r.any = count >= 0 && count <= p.n && j < count;
+    if (count < 0 || count > p.n) bad = ATLAS_DEV_BAD_SEQLEN;
+    r.q = b * p.qs[0] + j * p.qs[2];
+    r.k = b * p.ks[0] + j * p.ks[2];
+    r.v = b * p.vs[0] + j * p.vs[2];
+    r.q_out = ((int64_t)b * p.Hq * p.n + j) * p.D;
+    r.cache = -1;
+    if (r.any && caches) {
+        const int64_t t = (int64_t)p.seq_lens[b] + j;
+        if (t < 0 || t >= (int64_t)p.max_pages * p.P) {
+            bad = ATLAS_DEV_BAD_SEQLEN;
+        } else {
+            const int lp = 31 - __clz(p.P);  // page_tokens is a power of two
+            const int page = p.page_table[(int64_t)b * p.max_pages + (t >> lp)];
+            if (page < 0 || page >= p.num_pages) bad = ATLAS_DEV_BAD_PAGE;
+            else r.cache = ((int64_t)page * p.Hkv * p.P + (t & (p.P - 1))) * p.D;
+        }
+    }
+    if (bad && p.status) atomicOr(p.status, bad);
+    return r;
 }
 
-// W: the norms' weights, or void for none.  FOLD: one row of weights for all heads, folded into
-// the cosines and sines: a unit's (w0 cos, w1 sin, w1 cos, w0 sin) for q and for k.
-template <typename T, int V, typename W, bool FOLD = false>
-__global__ void __launch_bounds__(kThreads, std::is_void<W>::value ? 8 : FOLD ? 8 : 5)
-    rope_append_kernel(const __grid_constant__ RopeParams p) {
-    constexpr bool kNorm = !std::is_void<W>::value;
-    __shared__ __align__(16) float cs[FOLD ? 1 : kMaxTokens][2][kMaxPairs];  // cosines, sines
-    // unit u of a slot of V at [u % V][slot]: neighbouring lanes read neighbouring vectors
-    __shared__ float4 folded[FOLD ? kMaxTokens : 1][2][FOLD ? kMaxPairs : 1];
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const __grid_constant__ RopeParams p) {
+    __shared__ __align__(16) float cs[kMaxTokens][2][kMaxPairs];  // cosines, sines
     __shared__ TokenRows rows[kMaxTokens];
     const int token0 = (int)blockIdx.x * p.tokens_per_cta;
     const int tokens = min(p.tokens_per_cta, p.B * p.n - token0);  // B * n < 2^31
     const int h0 = (int)blockIdx.y * p.heads_per_cta;
     const int h1 = min(p.Hq + 2 * p.Hkv, h0 + p.heads_per_cta);
 
-    if constexpr (FOLD) {
-        const int units = p.D / 2;
-        for (int i = threadIdx.x; i < tokens * units && h0 < p.Hq + p.Hkv; i += kThreads) {
-            const int k = i / units, u = i - k * units;
-            float c = 1.f, s = 0.f;
-            if (u < p.pairs) {
-                const int32_t pos = p.positions[(int64_t)p.axis[u] * p.B * p.n + token0 + k];
-                cos_sin_turns((uint64_t)(int64_t)pos * p.turn[u], c, s);
-            }
-            int e0, e1;
-            unit_elements(p, u, e0, e1);
-            const int at = u % V * (units / V) + u / V;
-            float w0[1], w1[1];
-            load_weights<W, 1>(p, p.q_weight, 0, e0, w0);
-            load_weights<W, 1>(p, p.q_weight, 0, e1, w1);
-            folded[k][0][at] = make_float4(w0[0] * c, w1[0] * s, w1[0] * c, w0[0] * s);
-            load_weights<W, 1>(p, p.k_weight, 0, e0, w0);
-            load_weights<W, 1>(p, p.k_weight, 0, e1, w1);
-            folded[k][1][at] = make_float4(w0[0] * c, w1[0] * s, w1[0] * c, w0[0] * s);
-        }
-    } else
     for (int i = threadIdx.x; i < tokens * p.pairs && h0 < p.Hq + p.Hkv; i += kThreads) {
         const int k = i / p.pairs, pair = i - k * p.pairs;
         const int32_t pos = p.positions[(int64_t)p.axis[pair] * p.B * p.n + token0 + k];
         cos_sin_turns((uint64_t)(int64_t)pos * p.turn[pair], cs[k][0][pair], cs[k][1][pair]);
     }
     if ((int)threadIdx.x < tokens) {
-        const int b = (token0 + (int)threadIdx.x) / p.n, j = (token0 + (int)threadIdx.x) % p.n;
-        const int count = p.n_new ? p.n_new[b] : p.n;
-        uint32_t bad = 0;
-        TokenRows r;
-        r.any = count >= 0 && count <= p.n && j < count;
-        if (count < 0 || count > p.n) bad = ATLAS_DEV_BAD_SEQLEN;
-        r.q = b * p.qs[0] + j * p.qs[2];
-        r.k = b * p.ks[0] + j * p.ks[2];
-        r.v = b * p.vs[0] + j * p.vs[2];
-        r.q_out = ((int64_t)b * p.Hq * p.n + j) * p.D;
-        r.cache = -1;
-        if (r.any && h1 > p.Hq) {
-            const int64_t t = (int64_t)p.seq_lens[b] + j;
-            if (t < 0 || t >= (int64_t)p.max_pages * p.P) {
-                bad = ATLAS_DEV_BAD_SEQLEN;
-            } else {
-                const int lp = 31 - __clz(p.P);  // page_tokens is a power of two
-                const int page = p.page_table[(int64_t)b * p.max_pages + (t >> lp)];
-                if (page < 0 || page >= p.num_pages) bad = ATLAS_DEV_BAD_PAGE;
-                else r.cache = ((int64_t)page * p.Hkv * p.P + (t & (p.P - 1))) * p.D;
-            }
-        }
-        if (bad && p.status) atomicOr(p.status, bad);
-        rows[threadIdx.x] = r;
+        rows[threadIdx.x] = token_rows(p, token0 + (int)threadIdx.x, h1 > p.Hq);
     }
     __syncthreads();
 
@@ -261,91 +232,7 @@ __global__ void __launch_bounds__(kThreads, std::is_void<W>::value ? 8 : FOLD ? 
         const int e0 = turned && !p.interleaved ? pair0 : 2 * pair0;
         const int e1 = turned && !p.interleaved ? pair0 + p.pairs : e0 + V;
         X x0 = load_vec<T, V>(src + e0), x1 = load_vec<T, V>(src + e1);
-        if constexpr (kNorm) {
-            if (h < p.Hq + p.Hkv) {
-                // (the lanes of one row: 32 at most, and all of them are here)
-                const bool is_q = h < p.Hq;
-                const int slots = 1 << lg_slots;
-                const unsigned mask = (slots == 32 ? ~0u : (1u << slots) - 1u)
-                                      << (threadIdx.x % 32 & ~(slots - 1));
-                float pre, factor;
-                norm_factor(p, [&](float scale) {
-                    float s = 0.f;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float a = widen(x0.e[i]) * scale, b = widen(x1.e[i]) * scale;
-                        s = fmaf(a, a, fmaf(b, b, s));
-                    }
-                    for (int d = 1; d < slots; d *= 2) s += __shfl_xor_sync(mask, s, d);
-                    return s;
-                }, pre, factor);
-                if constexpr (FOLD) {
-                    const float4 *t = folded[k][is_q ? 0 : 1] + slot;
-                    auto emit = [&](auto halves, auto rotate) {
-                        X y0, y1;
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            // the unit's elements: one of each vector, or two of one
-                            const int a = halves ? i : 2 * i % V, b = halves ? i : (2 * i + 1) % V;
-                            const X &from_a = halves || 2 * i < V ? x0 : x1;
-                            const X &from_b = halves || 2 * i >= V ? x1 : x0;
-                            X &to_a = halves || 2 * i < V ? y0 : y1;
-                            X &to_b = halves || 2 * i >= V ? y1 : y0;
-                            const float x = widen(from_a.e[a]) * factor, y = widen(from_b.e[b]) * factor;
-                            const float4 f = t[i << lg_slots];
-                            float u = x * f.x, v = y * f.z;
-                            if (rotate) {
-                                u -= y * f.y;
-                                v += x * f.w;
-                            }
-                            to_a.e[a] = narrow<T>(u * pre);
-                            to_b.e[b] = narrow<T>(v * pre);
-                        }
-                        store_vec<T, V>(dst + e0, y0);
-                        store_vec<T, V>(dst + e1, y1);
-                    };
-                    if (!turned) emit(std::false_type{}, std::false_type{});
-                    else if (p.interleaved) emit(std::false_type{}, std::true_type{});
-                    else emit(std::true_type{}, std::true_type{});
-                    continue;
-                }
-                float w0[V], w1[V];
-                const void *weights = is_q ? p.q_weight : p.k_weight;
-                load_weights<W, V>(p, weights, is_q ? h : h - p.Hq, e0, w0);
-                load_weights<W, V>(p, weights, is_q ? h : h - p.Hq, e1, w1);
-                float y0[V], y1[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    y0[i] = widen(x0.e[i]) * factor * pre * w0[i];
-                    y1[i] = widen(x1.e[i]) * factor * pre * w1[i];
-                }
-                if (turned) {
-                    const float *c = cs[k][0] + pair0, *s = cs[k][1] + pair0;
-                    if (!p.interleaved) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            const float x = y0[i], y = y1[i];
-                            y0[i] = x * c[i] - y * s[i];
-                            y1[i] = y * c[i] + x * s[i];
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {  // pair i of 2 V consecutive elements
-                            float &a = 2 * i < V ? y0[2 * i % V] : y1[2 * i % V];
-                            float &b = 2 * i + 1 < V ? y0[(2 * i + 1) % V] : y1[(2 * i + 1) % V];
-                            const float x = a, y = b;
-                            a = x * c[i] - y * s[i];
-                            b = y * c[i] + x * s[i];
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    x0.e[i] = narrow<T>(y0[i]);
-                    x1.e[i] = narrow<T>(y1[i]);
-                }
-            }
-        } else if (turned && h < p.Hq + p.Hkv) {
+        if (turned && h < p.Hq + p.Hkv) {
             const float *c = cs[k][0] + pair0, *s = cs[k][1] + pair0;
             X y0, y1;
             if (!p.interleaved) {
@@ -373,99 +260,263 @@ __global__ void __launch_bounds__(kThreads, std::is_void<W>::value ? 8 : FOLD ? 
     }
 }
 
-// Norms where the rotated part is an odd number of pairs: no vector of two divides its halves,
-// and single elements would spread a row of 128 over two warps.  Here a warp has a row, a lane
-// one or two of its units (a pair; past the rotated part two neighbouring elements), element by
-// element.  blockIdx.x: a token; a warp's heads follow one another by blockDim / 32.
-template <typename T, typename W>
-__global__ void __launch_bounds__(kThreads) norm_rope_rows_kernel(const __grid_constant__ RopeParams p) {
-    const int b = (int)blockIdx.x / p.n, j = (int)blockIdx.x % p.n;
-    const int lane = threadIdx.x % 32, units = p.D / 64;
-    const int count = p.n_new ? p.n_new[b] : p.n;
-    if (count < 0 || count > p.n) {
-        if (threadIdx.x == 0 && p.status) atomicOr(p.status, ATLAS_DEV_BAD_SEQLEN);
-        return;
-    }
-    if (j >= count) return;
-    const int64_t t = (int64_t)p.seq_lens[b] + j;
-    int64_t cache = -1;
-    uint32_t bad = 0;
-    if (t < 0 || t >= (int64_t)p.max_pages * p.P) {
-        bad = ATLAS_DEV_BAD_SEQLEN;
-    } else {
-        const int page = p.page_table[(int64_t)b * p.max_pages + t / p.P];
-        if (page < 0 || page >= p.num_pages) bad = ATLAS_DEV_BAD_PAGE;
-        else cache = ((int64_t)page * p.Hkv * p.P + t % p.P) * p.D;
-    }
-    if (bad && threadIdx.x == 0 && p.status) atomicOr(p.status, bad);
-    float c[2] = {1.f, 1.f}, s[2] = {0.f, 0.f};
-    int e0[2], e1[2];
-    for (int i = 0; i < units; ++i) {
-        const int u = lane + 32 * i;
-        const bool turned = u < p.pairs;
-        e0[i] = turned && !p.interleaved ? u : 2 * u;
-        e1[i] = turned && !p.interleaved ? u + p.pairs : 2 * u + 1;
-        if (!turned) continue;
-        const int32_t pos = p.positions[(int64_t)p.axis[u] * p.B * p.n + blockIdx.x];
-        cos_sin_turns((uint64_t)(int64_t)pos * p.turn[u], c[i], s[i]);
-    }
-    for (int h = threadIdx.x / 32; h < p.Hq + 2 * p.Hkv; h += blockDim.x / 32) {
-        const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
-        const int hh = is_q ? h : is_k ? h - p.Hq : h - p.Hq - p.Hkv;
-        if (!is_q && cache < 0) continue;
-        const int64_t *st = is_q ? p.qs : is_k ? p.ks : p.vs;
-        const T *src = static_cast<const T *>(is_q ? p.q : is_k ? p.k_new : p.v_new) + b * st[0] +
-                       hh * st[1] + j * st[2];
-        T *dst = is_q ? static_cast<T *>(p.q_out) + (((int64_t)b * p.Hq + hh) * p.n + j) * p.D
-                      : static_cast<T *>(is_k ? p.k_pages : p.v_pages) + cache + (int64_t)hh * p.P * p.D;
-        float x[2] = {0.f, 0.f}, y[2] = {0.f, 0.f};
-        for (int i = 0; i < units; ++i) {
-            x[i] = widen(src[e0[i]]);
-            y[i] = widen(src[e1[i]]);
+// ---------------------------------------------------------------- with norms
+constexpr int kNormTokens = 2;
+
+// Slots and CTAs as above.  A unit (x, y) -- a pair, or past the rotated part two neighbours --
+// becomes
+//   (x w0 cos - y w1 sin, y w1 cos + x w0 sin),
+// four factors that the CTA works out once for each token, for q and for k, when all heads share
+// their weights (PER_HEAD: cosines and sines alone).
+// What bounds it: 4 x 8192 tokens of 32 + 8 + 8 heads of 128 bf16 (806 MB) take 140 us, 5.8 TB/s
+// (85 % of the measured copy; fp32 rows 125 us, 95 %): reading the factors keeps the L1 pipe at
+// 80 %, and the rows' loads need all 2048 threads of an SM.  Two heads a thread halve the factors'
+// reads and cost that occupancy: 150 us; factors in registers, a warp to a token, 224 us; the
+// rows through a cp.async ring 183 us; 6 and 5 CTAs an SM 157 and 166 us.  Weights of each head
+// are read row by row: 204 us.
+template <typename T, int V, typename W, bool PER_HEAD>
+__global__ void __launch_bounds__(kThreads, PER_HEAD ? 5 : 8)
+    norm_rope_kernel(const __grid_constant__ RopeParams p) {
+    using X = Vec<T, V>;
+    // unit u of a slot of V at [u % V][slot]: neighbouring lanes read neighbouring vectors
+    __shared__ float4 turns[kNormTokens][PER_HEAD ? 1 : 2][kMaxPairs];
+    __shared__ TokenRows rows[kNormTokens];
+    const int token0 = (int)blockIdx.x * p.tokens_per_cta;
+    const int tokens = min(p.tokens_per_cta, p.B * p.n - token0);
+    const int h0 = (int)blockIdx.y * p.heads_per_cta;
+    const int h1 = min(p.Hq + 2 * p.Hkv, h0 + p.heads_per_cta);
+    const int lg_slots = 30 - __clz(p.D) - (V == 8 ? 3 : V == 4 ? 2 : 1), slots = 1 << lg_slots;
+    const int units = p.D / 2;
+    for (int i = threadIdx.x; i < tokens * units && h0 < p.Hq + p.Hkv; i += kThreads) {
+        const int k = i / units, u = i - k * units;
+        float c = 1.f, s = 0.f;
+        if (u < p.pairs) {
+            const int32_t pos = p.positions[(int64_t)p.axis[u] * p.B * p.n + token0 + k];
+            cos_sin_turns((uint64_t)(int64_t)pos * p.turn[u], c, s);
         }
-        if (is_q || is_k) {
-            float pre, factor;
-            norm_factor(p, [&](float scale) {
-                float sum = 0.f;
-                for (int i = 0; i < 2; ++i) {
-                    const float a = x[i] * scale, z = y[i] * scale;
-                    sum = fmaf(a, a, fmaf(z, z, sum));
-                }
-                for (int d = 1; d < 32; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                return sum;
-            }, pre, factor);
-            for (int i = 0; i < units; ++i) {
+        const int at = u % V * slots + u / V;
+        if constexpr (PER_HEAD) {
+            turns[k][0][at] = make_float4(c, s, c, s);
+        } else {
+            const bool halves = u < p.pairs && !p.interleaved;
+            const int e0 = halves ? u : 2 * u, e1 = halves ? u + p.pairs : 2 * u + 1;
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
                 float w0[1], w1[1];
-                load_weights<W, 1>(p, is_q ? p.q_weight : p.k_weight, hh, e0[i], w0);
-                load_weights<W, 1>(p, is_q ? p.q_weight : p.k_weight, hh, e1[i], w1);
-                const float a = x[i] * factor * pre * w0[0], z = y[i] * factor * pre * w1[0];
-                x[i] = a * c[i] - z * s[i];
-                y[i] = z * c[i] + a * s[i];
+                load_weights<W, 1>(p, which ? p.k_weight : p.q_weight, 0, e0, w0);
+                load_weights<W, 1>(p, which ? p.k_weight : p.q_weight, 0, e1, w1);
+                turns[k][which][at] = make_float4(w0[0] * c, w1[0] * s, w1[0] * c, w0[0] * s);
             }
         }
-        for (int i = 0; i < units; ++i) {
-            dst[e0[i]] = narrow<T>(x[i]);
-            dst[e1[i]] = narrow<T>(y[i]);
+    }
+    if ((int)threadIdx.x < tokens)
+        rows[threadIdx.x] = token_rows(p, token0 + (int)threadIdx.x, h1 > p.Hq);
+    __syncthreads();
+
+    const int per_token = (h1 - h0) << lg_slots;
+    for (int k = 0, item = threadIdx.x;; item += kThreads) {
+        while (k < tokens && item >= per_token) {
+            item -= per_token;
+            ++k;
         }
+        if (k >= tokens) break;
+        const TokenRows &r = rows[k];
+        const int h = h0 + (item >> lg_slots), slot = item & (slots - 1);
+        if (!r.any || (h >= p.Hq && r.cache < 0)) continue;
+        const T *src;
+        T *dst;
+        if (h < p.Hq) {
+            src = static_cast<const T *>(p.q) + r.q + h * p.qs[1];
+            dst = static_cast<T *>(p.q_out) + r.q_out + (int64_t)h * p.n * p.D;
+        } else if (h < p.Hq + p.Hkv) {
+            src = static_cast<const T *>(p.k_new) + r.k + (h - p.Hq) * p.ks[1];
+            dst = static_cast<T *>(p.k_pages) + r.cache + (int64_t)(h - p.Hq) * p.P * p.D;
+        } else {
+            src = static_cast<const T *>(p.v_new) + r.v + (h - p.Hq - p.Hkv) * p.vs[1];
+            dst = static_cast<T *>(p.v_pages) + r.cache + (int64_t)(h - p.Hq - p.Hkv) * p.P * p.D;
+        }
+        // The slot's two vectors: of its units' first and second elements, or (pairs side by
+        // side, and past the rotated part) of 2 V neighbours.
+        const bool turned = slot * V < p.pairs, halves = turned && !p.interleaved;
+        const int e0 = halves ? slot * V : 2 * slot * V, e1 = halves ? e0 + p.pairs : e0 + V;
+        X x0 = load_vec<T, V>(src + e0), x1 = load_vec<T, V>(src + e1);
+        if (h >= p.Hq + p.Hkv) {
+            store_vec<T, V>(dst + e0, x0);
+            store_vec<T, V>(dst + e1, x1);
+            continue;
+        }
+        // (the lanes of one row: 32 at most, and all of them are here)
+        const bool is_q = h < p.Hq;
+        const unsigned mask = (slots == 32 ? ~0u : (1u << slots) - 1u) << (threadIdx.x % 32 & ~(slots - 1));
+        float pre, factor;
+        norm_factor(p, [&](float scale) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float a = widen(x0.e[i]) * scale, b = widen(x1.e[i]) * scale;
+                s = fmaf(a, a, fmaf(b, b, s));
+            }
+            for (int d = 1; d < slots; d *= 2) s += __shfl_xor_sync(mask, s, d);
+            return s;
+        }, pre, factor);
+        const float4 *t = turns[k][PER_HEAD || is_q ? 0 : 1] + slot;
+        auto emit = [&](auto split, auto rotate) {
+            float w0[V], w1[V];
+            if constexpr (PER_HEAD) {
+                const void *weights = is_q ? p.q_weight : p.k_weight;
+                load_weights<W, V>(p, weights, is_q ? h : h - p.Hq, e0, w0);
+                load_weights<W, V>(p, weights, is_q ? h : h - p.Hq, e1, w1);
+            }
+            X y0, y1;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                // the unit's elements: one of each vector, or two of one
+                const int a = split ? i : 2 * i % V, b = split ? i : (2 * i + 1) % V;
+                const bool a0 = split || 2 * i < V, b0 = !split && 2 * i < V;
+                float x = widen((a0 ? x0 : x1).e[a]) * factor, y = widen((b0 ? x0 : x1).e[b]) * factor;
+                if constexpr (PER_HEAD) {
+                    x *= (a0 ? w0 : w1)[a];
+                    y *= (b0 ? w0 : w1)[b];
+                }
+                const float4 f = t[i << lg_slots];
+                float u = x * f.x, v = y * f.z;
+                if (rotate) {
+                    u -= y * f.y;
+                    v += x * f.w;
+                }
+                (a0 ? y0 : y1).e[a] = narrow<T>(u * pre);
+                (b0 ? y0 : y1).e[b] = narrow<T>(v * pre);
+            }
+            store_vec<T, V>(dst + e0, y0);
+            store_vec<T, V>(dst + e1, y1);
+        };
+        if (!turned) emit(std::false_type{}, std::false_type{});
+        else if (p.interleaved) emit(std::false_type{}, std::true_type{});
+        else emit(std::true_type{}, std::true_type{});
     }
 }
 
-template <typename T, int V, typename W = void, bool FOLD = false>
-cudaError_t launch(RopeParams &p, cudaStream_t stream) {
+// Norms where the rotated part is an odd number of pairs, whose halves no vector of two divides.
+// A lane has 16 bytes of a row, whatever they hold; elements of the rotated part find their
+// partners through shared memory (pairs side by side are in one vector).
+template <typename T, typename W>
+__global__ void __launch_bounds__(kThreads, 5) norm_rope_odd_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int V = 16 / (int)sizeof(T);
+    using X = Vec<T, V>;
+    __shared__ float2 turns[kNormTokens][kMaxPairs];  // cosine, sine
+    __shared__ TokenRows rows[kNormTokens];
+    __shared__ float normed[kThreads * V];            // each row's elements, at its lanes' places
+    const int token0 = (int)blockIdx.x * p.tokens_per_cta;
+    const int tokens = min(p.tokens_per_cta, p.B * p.n - token0);
+    const int h0 = (int)blockIdx.y * p.heads_per_cta;
+    const int h1 = min(p.Hq + 2 * p.Hkv, h0 + p.heads_per_cta);
+    const int lanes = p.D / V, lg = 31 - __clz(lanes);
+    for (int i = threadIdx.x; i < tokens * p.pairs && h0 < p.Hq + p.Hkv; i += kThreads) {
+        const int k = i / p.pairs, u = i - k * p.pairs;
+        const int32_t pos = p.positions[(int64_t)p.axis[u] * p.B * p.n + token0 + k];
+        cos_sin_turns((uint64_t)(int64_t)pos * p.turn[u], turns[k][u].x, turns[k][u].y);
+    }
+    if ((int)threadIdx.x < tokens)
+        rows[threadIdx.x] = token_rows(p, token0 + (int)threadIdx.x, h1 > p.Hq);
+    __syncthreads();
+
+    const int lane = threadIdx.x & (lanes - 1), e0 = lane * V;
+    const unsigned mask = (lanes == 32 ? ~0u : (1u << lanes) - 1u) << (threadIdx.x % 32 & ~(lanes - 1));
+    float *const row = normed + (threadIdx.x - lane) * V;
+    const bool inside = p.interleaved != 0;
+    const int per_token = (h1 - h0) << lg;
+    for (int k = 0, item = threadIdx.x;; item += kThreads) {
+        while (k < tokens && item >= per_token) {
+            item -= per_token;
+            ++k;
+        }
+        if (k >= tokens) break;
+        const TokenRows &r = rows[k];
+        const int h = h0 + (item >> lg);
+        if (!r.any || (h >= p.Hq && r.cache < 0)) continue;
+        const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
+        const int hh = is_q ? h : h - p.Hq - (is_k ? 0 : p.Hkv);
+        const T *src = is_q   ? static_cast<const T *>(p.q) + r.q + hh * p.qs[1]
+                       : is_k ? static_cast<const T *>(p.k_new) + r.k + hh * p.ks[1]
+                              : static_cast<const T *>(p.v_new) + r.v + hh * p.vs[1];
+        T *dst = is_q ? static_cast<T *>(p.q_out) + r.q_out + (int64_t)hh * p.n * p.D
+                      : static_cast<T *>(is_k ? p.k_pages : p.v_pages) + r.cache + (int64_t)hh * p.P * p.D;
+        X x = load_vec<T, V>(src + e0);
+        if (is_q || is_k) {
+            float pre, factor, w[V], y[V];
+            load_weights<W, V>(p, is_q ? p.q_weight : p.k_weight, hh, e0, w);
+            norm_factor(p, [&](float scale) {
+                float s = 0.f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float a = widen(x.e[i]) * scale;
+                    s = fmaf(a, a, s);
+                }
+                for (int d = 1; d < lanes; d *= 2) s += __shfl_xor_sync(mask, s, d);
+                return s;
+            }, pre, factor);
+#pragma unroll
+            for (int i = 0; i < V; ++i) y[i] = widen(x.e[i]) * factor * w[i];
+            const bool turned = e0 < 2 * p.pairs;
+            if (!inside) {  // partners in other lanes' vectors
+                if (turned) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) row[e0 + i] = y[i];
+                }
+                __syncwarp(mask);
+            }
+            if (turned) {
+                float out[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int e = e0 + i;
+                    out[i] = y[i];
+                    if (e >= 2 * p.pairs) continue;
+                    const bool first = p.interleaved ? i % 2 == 0 : e < p.pairs;
+                    const float2 a = turns[k][p.interleaved ? e / 2 : first ? e : e - p.pairs];
+                    const float other = p.interleaved ? y[i ^ 1] : row[first ? e + p.pairs : e - p.pairs];
+                    out[i] = first ? y[i] * a.x - other * a.y : y[i] * a.x + other * a.y;
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) y[i] = out[i];
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) x.e[i] = narrow<T>(y[i] * pre);
+            if (!inside) __syncwarp(mask);  // (the places are written again)
+        }
+        store_vec<T, V>(dst + e0, x);
+    }
+}
+
+// Tokens and heads of a CTA, and the grid; a row has `lanes` items.
+dim3 cut(RopeParams &p, int lanes, int max_tokens) {
     const int64_t tokens = (int64_t)p.B * p.n;
     const int heads = p.Hq + 2 * p.Hkv;
-    // kMaxTokens tokens per CTA while that leaves eight CTAs for each SM; with fewer
+    // max_tokens tokens per CTA while that leaves eight CTAs for each SM; with fewer
     // than that of single tokens, the heads in as many groups as it takes.
     const int64_t want = (int64_t)device_sm_count() * 8;
-    p.tokens_per_cta = tokens >= want * kMaxTokens ? kMaxTokens : 1;
+    p.tokens_per_cta = tokens >= want * max_tokens ? max_tokens : 1;
     const int64_t ctas = (tokens + p.tokens_per_cta - 1) / p.tokens_per_cta;
     int64_t groups = (want + ctas - 1) / ctas;
     // (a group has at least one item for each thread)
-    const int64_t most = ((int64_t)heads * (p.D / (2 * V)) + kThreads - 1) / kThreads;
+    const int64_t most = ((int64_t)heads * lanes + kThreads - 1) / kThreads;
     if (groups > most) groups = most;
     p.heads_per_cta = (int)((heads + groups - 1) / groups);
-    const dim3 grid((unsigned)ctas, (unsigned)((heads + p.heads_per_cta - 1) / p.heads_per_cta));
-    rope_append_kernel<T, V, W, FOLD><<<grid, kThreads, 0, stream>>>(p);
+    return dim3((unsigned)ctas, (unsigned)((heads + p.heads_per_cta - 1) / p.heads_per_cta));
+}
+
+template <typename T, int V>
+cudaError_t launch(RopeParams &p, cudaStream_t stream) {
+    const dim3 grid = cut(p, p.D / (2 * V), kMaxTokens);
+    rope_append_kernel<T, V><<<grid, kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, int V, typename W>
+cudaError_t launch_norm_vectors(RopeParams &p, cudaStream_t stream) {
+    const dim3 grid = cut(p, p.D / (2 * V), kNormTokens);
+    if (p.weight_step) norm_rope_kernel<T, V, W, true><<<grid, kThreads, 0, stream>>>(p);
+    else norm_rope_kernel<T, V, W, false><<<grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -473,17 +524,14 @@ cudaError_t launch(RopeParams &p, cudaStream_t stream) {
 template <typename T, typename W>
 cudaError_t launch_norm(RopeParams &p, cudaStream_t stream) {
     if (p.pairs % 2) {
-        norm_rope_rows_kernel<T, W><<<(unsigned)(p.B * p.n), kThreads, 0, stream>>>(p);
+        const dim3 grid = cut(p, p.D * (int)sizeof(T) / 16, kNormTokens);
+        norm_rope_odd_kernel<T, W><<<grid, kThreads, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    if (p.weight_step) {
-        if constexpr (sizeof(T) == 2)
-            if (p.pairs % 8 == 0) return launch<T, 8, W>(p, stream);
-        return p.pairs % 4 == 0 ? launch<T, 4, W>(p, stream) : launch<T, 2, W>(p, stream);
-    }
     if constexpr (sizeof(T) == 2)
-        if (p.pairs % 8 == 0) return launch<T, 8, W, true>(p, stream);
-    return p.pairs % 4 == 0 ? launch<T, 4, W, true>(p, stream) : launch<T, 2, W, true>(p, stream);
+        if (p.pairs % 8 == 0) return launch_norm_vectors<T, 8, W>(p, stream);
+    return p.pairs % 4 == 0 ? launch_norm_vectors<T, 4, W>(p, stream)
+                            : launch_norm_vectors<T, 2, W>(p, stream);
 }
 
 // A stride triple (batch, head, token) in elements; all zero means dense rows.
