@@ -161,7 +161,7 @@ struct SharedStream {
     int32_t max_states;  // CTAs that a tile may be cut among at most
     int32_t sms;
     // by the plan kernel
-    int32_t *head;       // [4]: a CTA's length of the line, all of it, 1 if the groups are out of range
+    int32_t *head;       // [2]: a CTA's length of the line, and all of it
     int32_t *first;      // [units + 1] where the units begin
     int32_t *head_cost;  // [units] length of one kv head's tiles
     int32_t *blocks;     // [units] blocks of a tile; -1: out of range, its rows are NaN

@@ -55,7 +55,13 @@ __device__ int prefix_splits(const SharedMergeParams &p, int b) {
 // The same where the prefixes are tiles of the line that p.st says (shared_prefix.cuh): the
 // states of the tile that row i of head h of sequence b is in.
 __device__ int tile_states(const SharedMergeParams &p, int b, int h, int i, int qn) {
-    const SeqInfo s = reinterpret_cast<const SeqInfo *>(p.st.info)[b];
+    // (read before the wait: the plan's grid is done, but not one that this grid waits for, so
+    // past the L1)
+    const int4 *const at = reinterpret_cast<const int4 *>(p.st.info) + 2 * b;
+    int4 raw[2] = {__ldcg(at), __ldcg(at + 1)};
+    SeqInfo s;
+    static_assert(sizeof(s) == sizeof(raw), "");
+    memcpy(&s, raw, sizeof(s));
     if (s.blocks <= 0 || i >= qn) return s.blocks < 0 ? -1 : 0;
     const int f = s.row0 + h % p.G * qn + i;
     const int tile = f / p.st.tile_rows, full = p.st.tile_rows == 256 ? kPairCost : kSingleCost;

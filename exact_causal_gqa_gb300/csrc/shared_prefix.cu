@@ -85,7 +85,7 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     const int64_t max_prefix = (int64_t)S->max_prefix_pages * P;
     if (max_prefix > INT32_MAX / 2) return ATLAS_ERR_INVALID_ARG;
 
-    const int sms = L->sm_count > 0 ? L->sm_count : device_sm_count();
+    const int64_t sms = L->sm_count > 0 ? L->sm_count : device_sm_count();
     const int G = Hq / Hkv;
     const int64_t rows = (int64_t)L->batch * G * L->q_len;  // of one kv head, all groups
     const int64_t group_rows = (rows + S->n_groups - 1) / S->n_groups;
@@ -103,13 +103,15 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->whole = false;
     if (L->debug_flags & ATLAS_DEBUG_SHARED_WHOLE) plan->whole = plan->stream;
     if (plan->stream && !plan->whole && few && L->split_tokens == 0 &&
-        (int64_t)L->batch * Hkv * plan->own.col_tiles >= 2 * (int64_t)sms) {
+        (int64_t)L->batch * Hkv * plan->own.col_tiles >= 2 * sms) {
         // The own splits run beside the tiles, the longest first: where there are enough
         // sequences they are best left whole (up to 4096 keys).
         own.split_tokens = (int32_t)own_split((int64_t)L->max_pages_per_seq * P);
         if (make_plan(ATLAS_KIND_SUFFIX, Hq, Hkv, D, P, &own, &plan->own) != ATLAS_OK)
             return ATLAS_ERR_UNSUPPORTED;
     }
+    if (few && (int64_t)plan->own.n_chunks * Hkv * plan->own.col_tiles * L->batch >= INT32_MAX)
+        return ATLAS_ERR_UNSUPPORTED;  // (the own splits' CTAs)
     const int64_t tile_of = plan->whole ? seq_rows : group_rows;
     plan->tiles = plan->split ? cols : !f32 && tile_of > 128 ? 2 : 1;
     // CTAs of one split: a group's last may be partly filled
@@ -130,7 +132,7 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
         // (short tiles that count as more blocks make for more CTAs than SMs)
         plan->ctas = sms + units / 10 + 2;
         const double line = (double)units * kPairCost * (double)(blocks + kTileBlocks);
-        if (line * (1.0 + (double)units / (sms * 30.0)) + 1e6 >= INT32_MAX)
+        if (line * (1.0 + (double)units / (sms * 14.0)) + 1e6 >= INT32_MAX)
             return ATLAS_ERR_UNSUPPORTED;  // (places in the line have 32 bits)
         const int64_t states = plan->whole ? plan->ctas * 2 * cta_rows : out_rows * plan->n_pre;
         plan->ml_at = plan->acc_at + (size_t)round_up(states * D * 4, 256);
@@ -138,7 +140,7 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
         const int64_t n = plan->whole ? L->batch : S->n_groups;
         const int64_t segs = 1 + shared_tc_items(plan->tiles) * (int64_t)(sizeof(SharedSeg) / 4) +
                              (int64_t)(sizeof(SharedCut) / 4);
-        plan->bytes = plan->plan_at + 4 * (size_t)(11 * (int64_t)L->batch + 4 + 5 * n + 2 +
+        plan->bytes = plan->plan_at + 4 * (size_t)(11 * (int64_t)L->batch + 1 + 2 + 5 * n + 1 +
                                                    plan->ctas * segs + (plan->whole ? 0 : rows));
         return ATLAS_OK;
     }
@@ -291,7 +293,7 @@ SharedStream stream_arrays(const SharedPlan &plan, int32_t G, const atlas_shared
         return x;
     };
     st.info = take(8 * (int64_t)L->batch);  // (16-byte loads: first)
-    st.head = take(4);
+    st.head = take(2);
     st.first = take(st.units + 1);
     st.head_cost = take(st.units);
     st.blocks = take(st.units);

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
             group_of[b] = group;
             const int qn = b0 == 0 ? my_qn : p.q_lens ? p.q_lens[b] : p.q_len;
             const int len = b0 == 0 ? mine : p.seq_lens[b];
-            if (len > 0 && len <= max_ctx) own = len;
+            if (len > 0 && len <= max_ctx) own = min(len, 1 << 22);  // (an estimate's)
             bool good = qn >= 0 && qn <= p.q_len && !bad;
             if (st.whole) {
                 const int pre = group >= 0 ? pre_lens[group] : 0;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
             }
             rows = good ? p.G * qn : 0;
         }
-        // (both sums in one scan: rows below 2^31, own keys below 2^31 a round)
+        // (both sums in one scan: rows below 2^31, own keys 512 * 2^22 a round at most)
         int64_t total;
         const int64_t upto = plan_scan((int64_t)rows << 32 | (uint32_t)own, total);
         if (b < p.B) before[b] = (int)(carry + (upto >> 32) - rows);
@@ -178,7 +178,11 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
     const int most = s_most;
     // A CTA's share: one CTA for each SM, few enough states of a tile, and few enough pieces of a
     // CTA, for which short tiles count as more blocks than they have.
-    const int ctas = st.own_rate > 0.f ? ctas_beside(p, (float)all, (float)own_keys) : st.sms;
+    int ctas = st.own_rate > 0.f ? ctas_beside(p, (float)all, (float)own_keys) : st.sms;
+    // (What the short tiles add is a fourteenth of a share each at most.  The host has seen that
+    // the line has room for that with a CTA for each SM; with fewer it is seen here.)
+    const float tiles = ((float)before[p.B] / (float)st.tile_rows + (float)st.units) * (float)p.Hkv;
+    if ((float)all * (1.f + tiles / (14.f * (float)ctas)) > 2e9f) ctas = st.sms;
     int64_t per64 = (all + ctas - 1) / ctas;
     per64 = max(per64, (int64_t)kMinBlocks * kPairCost);
     per64 = max(per64, (int64_t)((most + st.max_states - 3) / (st.max_states - 2)) * kPairCost);
@@ -205,7 +209,6 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
         first_of[st.units] = line;
         st.head[0] = per;
         st.head[1] = line;
-        st.head[2] = bad;
     }
     if (flags && p.status) atomicOr(p.status, flags);
     __syncthreads();

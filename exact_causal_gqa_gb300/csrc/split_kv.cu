@@ -126,7 +126,7 @@ __device__ SplitCta split_cta(const Params &p) {
         if (i < p.own_items) {
             const int chunk = i % p.n_chunks, y = i / p.n_chunks % (p.Hkv * p.col_tiles);
             const int b = i / p.n_chunks / (p.Hkv * p.col_tiles);
-            return {chunk, y / p.col_tiles, y % p.col_tiles, p.order ? p.order[b] : b, false, 0, 0, 0};
+            return {chunk, y / p.col_tiles, y % p.col_tiles, p.order ? __ldcg(p.order + b) : b, false, 0, 0, 0};
         }
         const SharedGroups groups{p.group_starts, p.prefix_lens, p.n_groups,  p.B,   p.max_prefix_pages * p.P,
                                   p.G * p.q_len,  NCOLS,         p.pre_chunk, p.Hkv, p.status};
