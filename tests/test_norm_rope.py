@@ -231,6 +231,78 @@ def test_bad_pages_and_lengths_are_reported_and_skipped(rot):
         assert (out[1] == 7).all() if change[0] == "n_new" else torch.equal(out[1], good_q[1])
 
 
+@gpu
+@pytest.mark.parametrize("rot", [128, 62])
+@pytest.mark.parametrize("per_head", [False, True])
+def test_captured_and_replayed_with_other_lengths(rot, per_head):
+    q, k, v, kp, vp, table, lens, pos = step("bf16", 3, 4, 2, 128, 16, 5, [5, 16, 30], 1, 8)
+    r = np.random.default_rng(4)
+    wq, wk = (weights(r, H, 128, per_head, torch.bfloat16) for H in (4, 2))
+    counts = torch.full_like(lens, 5)
+    kw = dict(q_weight=wq, k_weight=wk, rot_dim=rot, n_new=counts)
+    out = torch.zeros_like(q)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        atlas.kv_append_norm_rope(q, k, v, kp, vp, table, lens, pos, q_out=out, **kw)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            atlas.kv_append_norm_rope(q, k, v, kp, vp, table, lens, pos, q_out=out, **kw)
+    for past, n in (([5, 16, 30], [5, 5, 5]), ([0, 2, 9], [1, 5, 0]), ([40, 42, 15], [5, 1, 3])):
+        torch.cuda.synchronize()
+        pools = []
+        for _ in range(2):
+            for t in (kp, vp, out):
+                t.fill_(1.0)
+            lens.copy_(torch.tensor(past, dtype=torch.int32))
+            counts.copy_(torch.tensor(n, dtype=torch.int32))
+            if not pools:
+                graph.replay()
+            else:
+                atlas.kv_append_norm_rope(q, k, v, kp, vp, table, lens, pos, q_out=out, **kw)
+            torch.cuda.synchronize()
+            pools.append([t.clone() for t in (kp, vp, out)])
+        assert all(torch.equal(a, b) for a, b in zip(*pools))
+        assert not (pools[0][0] == 1).all()
+
+
+@gpu
+@pytest.mark.parametrize("rot", [128, 62])
+def test_pages_whose_offsets_pass_32_bits(rot):
+    q, k, v, kp, vp, table, lens, pos = step("bf16", 3, 4, 2, 128, 128, 5, [5, 16, 200], 1, 8)
+    n = kp.shape[0]
+    num = (1 << 32) // (2 * 128 * 128) + 2 * n
+    far = [torch.empty((num, *kp.shape[1:]), dtype=kp.dtype, device="cuda") for _ in range(2)]
+    for a, b in zip(far, (kp, vp)):
+        a[num - n:] = b
+    a = atlas.kv_append_norm_rope(q, k, v, kp, vp, table, lens, pos, rot_dim=rot)
+    b = atlas.kv_append_norm_rope(q, k, v, *far, table + (num - n), lens, pos, rot_dim=rot)
+    assert torch.equal(a, b)
+    assert torch.equal(far[0][num - n:], kp) and torch.equal(far[1][num - n:], vp)
+
+
+@gpu
+@pytest.mark.parametrize("per_head,rot", [(False, 128), (True, 128), (False, 62)])
+def test_many_tokens_are_as_one_by_one(per_head, rot):
+    """Two tokens a CTA, and the last CTA with one: the bits of calls of one token."""
+    B, n = 3, 901
+    q, k, v, kp, vp, table, lens, pos = step("bf16", B, 4, 2, 128, 16, n, [5, 16, 30], 1, 8)
+    r = np.random.default_rng(4)
+    wq, wk = (weights(r, H, 128, per_head, torch.float32) for H in (4, 2))
+    kw = dict(q_weight=wq, k_weight=wk, rot_dim=rot)
+    pools = kp.clone(), vp.clone()
+    out = atlas.kv_append_norm_rope(q, k, v, kp, vp, table, lens, pos, **kw)
+    for i in (0, 1, 450, 899, 900):
+        one = atlas.kv_append_norm_rope(*(t[:, :, i:i + 1] for t in (q, k, v)), *pools, table, lens + i,
+                                        pos[:, :, i:i + 1].contiguous(), **kw)
+        assert torch.equal(one, out[:, :, i:i + 1])
+        for b in range(B):
+            t = int(lens[b]) + i
+            page = int(table[b, t // 16])
+            for x, y in zip(pools, (kp, vp)):
+                assert torch.equal(x[page, :, t % 16], y[page, :, t % 16])
+
+
 def apart(t):
     return torch.stack([t, t], -1)[..., 0]
 

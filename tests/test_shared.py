@@ -231,7 +231,7 @@ def test_no_prefix_is_a_suffix(dtype, B, q_len):
 
 @gpu
 def test_the_order_of_the_groups_changes_no_bits():
-    """A sequence's result depends on its own group alone."""
+    """On the split kernels a sequence's result depends on its own group alone."""
     x = Case("bf16", 8, 2, 128, 16, 1, [0, 2, 5], [300, 90], [9, 8, 7, 6, 5], 4)
     a = x(0.09)
     q, kp, vp, ptab, plen, starts, table, own = x.args
@@ -303,6 +303,101 @@ def test_captured_and_replayed_with_other_groups_and_lengths(dtype, q_len):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, x(0.09))
+
+
+PATHS = [0, atlas.DEBUG_SHARED_SPLIT, atlas.DEBUG_SHARED_TC, atlas.DEBUG_SHARED_WHOLE | atlas.DEBUG_SHARED_TC]
+
+
+@gpu
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,q_len,ragged", [
+    ("bf16", 2, 1, 64, 1, False), ("bf16", 2, 1, 128, 3, True), ("f32", 2, 1, 64, 2, True)])
+def test_more_sequences_and_groups_than_the_plan_has_threads(dtype, Hq, Hkv, D, q_len, ragged, path):
+    """1300 sequences in 601 groups: of none, of one, of few, and one of 600; some in none."""
+    starts = [0, 0, 600] + [600 + min(n, 500) for n in range(1, 598)] + [1200, 1290]
+    pre = [(0, 40, 130, 7)[n % 4] for n in range(len(starts) - 1)]
+    pre[1] = 300
+    lens = [q_len + b * 7 % 40 for b in range(1300)]
+    x = Case(dtype, Hq, Hkv, D, 8, q_len, starts, pre, lens, 17,
+             [b % (q_len + 1) for b in range(1300)] if ragged else None)
+    check(x, dtype, D ** -0.5, path=path)
+
+
+@gpu
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_query_at_all(dtype, path):
+    x = Case(dtype, 8, 2, 64, 16, 3, [0, 2, 4], [100, 70], [50, 41, 60, 77], 8, [0, 0, 0, 0])
+    out = torch.full_like(x.args[0], 7.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x(0.1, out=out, status=status, debug_flags=path)
+    assert (out == 7).all() and int(status.item()) == 0
+
+
+@gpu
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_same_pages_twice(dtype, path):
+    """Two groups behind the same prompt, and a sequence whose own pages are a prefix's too."""
+    x = Case(dtype, 8, 2, 64, 16, 1, [0, 2, 4], [300, 300], [50, 41, 60, 300], 12)
+    x.args[3][1] = x.args[3][0]
+    x.args[6][3] = x.args[3][0]
+    for t in (x.k, x.v):
+        t[5] = t[4]
+        t[3] = t[4]
+    check(x, dtype, 0.125, path=path)
+
+
+@gpu
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype,D,q_len", [("bf16", 128, 1), ("bf16", 64, 40), ("f32", 128, 1)])
+def test_pages_whose_offsets_pass_32_bits(dtype, D, q_len, path):
+    """The same pages at the end of a pool of more than 2^32 elements."""
+    x = Case(dtype, 4, 2, D, 128, q_len, [0, 2, 3], [300, 129], [50, 141, 260], 12)
+    q, kp, vp, ptab, plen, starts, table, own = x.args
+    near = x(0.1, debug_flags=path)
+    n = kp.shape[0]
+    num = (1 << 32) // (2 * 128 * D) + 2 * n
+    far = [torch.empty((num, *kp.shape[1:]), dtype=kp.dtype, device="cuda") for _ in range(2)]
+    for a, b in zip(far, (kp, vp)):
+        a[num - n:] = b
+    moved = [torch.where(t < n, t + (num - n), t) for t in (ptab, table)]
+    out = atlas.shared(q, *far, moved[0], plen, starts, moved[1], own, *x.sizes, 0.1, debug_flags=path)
+    assert torch.equal(out, near)
+
+
+@gpu
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype,q_len", [("bf16", 1), ("bf16", 40), ("f32", 2)])
+def test_calls_on_two_streams_at_once(dtype, q_len, path):
+    """Each with its own workspace: the bits are those of calls one after the other."""
+    x = [Case(dtype, 8, 2, 128, 16, q_len, [0, 30, 40], [2000, 300], [q_len + b for b in range(40)], s) for s in (1, 2)]
+    want = [c(0.09, debug_flags=path) for c in x]
+    streams = [torch.cuda.Stream() for _ in x]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(6):
+        for c, s, g in zip(x, streams, got):
+            with torch.cuda.stream(s):
+                g.append(c(0.09, debug_flags=path))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, y) for y in g)
+
+
+@gpu
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_fewer_sms_and_events(dtype, path):
+    x = Case(dtype, 8, 2, 128, 16, 1, [0, 30, 40], [2000, 300], [1 + b for b in range(40)], 5)
+    ref, _ = x.expected(0.09)
+    timer = atlas.EventTimer()
+    tol = F32_REL * np.abs(ref).max() if dtype == "f32" else BF16_ABS
+    for sms in (1, 7, 1000):
+        out = x(0.09, debug_flags=path, sm_count=sms, events=timer.handles, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        assert np.abs(widen(out) - ref).max() <= tol
+        assert timer.main_ms() > 0 and timer.merge_ms() > 0
 
 
 def test_tensors_on_the_host():
