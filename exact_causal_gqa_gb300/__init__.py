@@ -178,6 +178,7 @@ _pack_launch = struct.Struct("iiiiiiiPPPQPPiIPifPPPii").pack
 _pack_shared = struct.Struct("PPPii").pack
 _pack_rope = struct.Struct("iiiiiiPPqqqqqqqqqPiiiPPdPP").pack
 _pack_norm = struct.Struct("PPiiff").pack
+_pack_resize = struct.Struct("iiiiPPPP").pack
 _lib = _fast = None
 
 
@@ -191,11 +192,11 @@ class _Fast:
                  ctypes.c_int),
                 ("atlas_attn_shared_workspace_size", [ctypes.c_int32] * 4 + pointers[:2], ctypes.c_size_t),
                 ("atlas_kv_append_rope", pointers + ints + pointers[:1], ctypes.c_int),
-                ("atlas_kv_append_norm_rope", pointers + ints + pointers[:2], ctypes.c_int)):
+                ("atlas_kv_append_norm_rope", pointers + ints + pointers[:2], ctypes.c_int),
+                ("atlas_kv_resize", pointers[:5] + ints[:1] + pointers[:1], ctypes.c_int)):
             fn = lib[name]  # (a function object of its own)
             fn.argtypes, fn.restype = args, result
             setattr(self, name[6:], fn)
-
 
 
 def library_path() -> str:
@@ -945,7 +946,7 @@ def kv_resize(page_table, n_pages, seq_lens, free_pages, free_state, page_tokens
     slots (or max_new, for a new one): [B][max_new], written with the places page * page_tokens
     + offset of each sequence's last n_new[b] tokens (None: max_new of them), then -1.  Returns
     slots (None without)."""
-    lib = load_library()
+    load_library()
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B][max_pages]")
     B, width = page_table.shape
@@ -954,23 +955,23 @@ def kv_resize(page_table, n_pages, seq_lens, free_pages, free_state, page_tokens
         slots = torch.empty((B, max_new), dtype=i32, device=device)
     if n_new is not None and slots is None:
         raise ValueError("n_new needs slots or max_new")
-    _check(device, ("page_table", page_table, i32), ("n_pages", n_pages, i32),
-           ("seq_lens", seq_lens, i32), ("free_pages", free_pages, i32),
-           ("free_state", free_state, i32), ("n_new", n_new, i32), ("slots", slots, i32),
-           ("status", status, i32))
+    if not _fits(device.index, (page_table, i32), (n_pages, i32), (seq_lens, i32), (free_pages, i32),
+                 (free_state, i32), (n_new, i32), (slots, i32), (status, i32)):
+        _check(device, ("page_table", page_table, i32), ("n_pages", n_pages, i32),
+               ("seq_lens", seq_lens, i32), ("free_pages", free_pages, i32),
+               ("free_state", free_state, i32), ("n_new", n_new, i32), ("slots", slots, i32),
+               ("status", status, i32))
     if n_pages.numel() != B or seq_lens.numel() != B or free_state.numel() != 2 or \
             (n_new is not None and n_new.numel() != B) or (status is not None and status.numel() < 1) or \
             (slots is not None and (slots.dim() != 2 or slots.shape[0] != B or
                                     max_new not in (None, slots.shape[1]))):
         raise ValueError("n_pages, seq_lens and n_new must be [B], free_state [2], slots "
                          "[B][max_new], status one word")
-    Z = _Resize(batch=B, max_pages_per_seq=width, num_pages=free_pages.numel(),
-                max_new=0 if slots is None else slots.shape[1], n_new=_ptr(n_new),
-                slots=_ptr(slots), status_word=_ptr(status), stream=_stream(device))
+    Z = _pack_resize(B, width, free_pages.numel(), 0 if slots is None else slots.shape[1],
+                     _address(n_new), _address(slots), _address(status), _stream(device) or 0)
     with _on(device):
-        rc = lib.atlas_kv_resize(page_table.data_ptr(), n_pages.data_ptr(), seq_lens.data_ptr(),
-                                 free_pages.data_ptr(), free_state.data_ptr(), page_tokens,
-                                 ctypes.byref(Z))
+        rc = _fast.kv_resize(page_table.data_ptr(), n_pages.data_ptr(), seq_lens.data_ptr(),
+                             free_pages.data_ptr(), free_state.data_ptr(), page_tokens, Z)
     if rc != 0:
         raise AtlasError(rc, status_string(rc))
     return slots

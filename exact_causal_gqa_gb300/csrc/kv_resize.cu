@@ -15,6 +15,10 @@
 // a single CTA after it.  Every CTA works the sums out for itself, kThreads sequences a round,
 // one to a thread; then a round's moves are one list, cut evenly among all threads, which find
 // the sequence of a list entry in the sums by bisection.
+//
+// What bounds it: latencies -- the launch, the sums' barriers, a move's dependent loads, of which
+// a thread has kAtOnce in flight.  A call where 32 sequences gain or lose a page or two takes 4.2 us,
+// one where half of 256 sequences of up to 8192 pages arrive or leave (0.5 million moves) 9.9.
 #include "internal.h"
 #include "atlas_pages.h"
 #include "ptx.cuh"
@@ -26,7 +30,9 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kClusterCtas = 8;  // the portable cluster size
 // Entries of table and slots up to which a call is one cluster (what it moves is known on the
-// device alone).
+// device alone).  Cluster and grid: 2^16 entries, few moves 4.2 and 5.3 us, half of the batch
+// arriving 6.4 and 5.6; 2^17 entries 4.4 and 5.6, 8.9 and 5.8; 2^18 4.4 and 5.6, 14.6 and 6.0.  Most
+// steps move little.
 constexpr int64_t kOneLaunch = 1 << 17;
 
 struct ResizeParams {

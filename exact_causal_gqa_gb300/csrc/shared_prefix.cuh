@@ -1,15 +1,16 @@
-// shared_prefix.cuh -- work items and rows of prefixes that groups of sequences share, for
-// the tensor-core kernels (bf16 and fp32).
+// shared_prefix.cuh -- work items and rows of prefixes that groups of sequences share.
 //
 // A prefix's keys are seen by every row of every sequence of its group, so the rows of one
 // kv head -- (sequence, q head of the kv head, query row), in that order -- form one long
-// list that is cut into 128-row tiles: a tile's rows may belong to many sequences, and each
-// K/V block is read once for all of them.  The items of a call are (group, kv head, split of
-// the prefix, tiles of one CTA), tiles fastest, so that the CTAs which read the same keys run
-// side by side and all but the first find them in L2.  Group sizes and prefix lengths are
-// known on the device alone: each CTA counts the items of all groups (one lane for each) and
-// finds its own; the grid covers the most that the call's sizes allow, and the CTAs behind
-// the last item leave.
+// list that is cut into tiles: a tile's rows may belong to many sequences, and each K/V block
+// is read once for all of them.  Group sizes and prefix lengths are known on the device alone.
+//
+// The split kernels (tiles of 4 to 16 rows) and the fp32 tensor-core kernel (128) have items
+// (group, kv head, split of the prefix, tile), tiles fastest, so that the CTAs which read the
+// same keys run side by side and all but the first find them in L2.  Each CTA counts the items
+// of all groups, one lane for each, and finds its own; the grid covers the most that the call's
+// sizes allow, and the CTAs behind the last item leave.  The bf16 tensor-core kernel (128 or 256)
+// has its items from a plan: below.
 #pragma once
 
 #include "internal.h"

@@ -18,6 +18,9 @@
 //   O^T[D x 8 cols]       += V^T[D x 16] . P^T[16 x 8]    (ldmatrix.trans; P^T via movmatrix)
 // P is fed as bf16 hi + lo parts, so the PV product keeps ~16 bits of P.
 // Column max / sum reductions are quad shuffles.
+//
+// Calls with shared prefixes (atlas_attn_shared) run the same kernels on one grid of own splits and
+// splits of prefixes, whose columns are a group's rows (SharedSplitParams).
 #include "internal.h"
 #include "ptx.cuh"
 #include "shared_prefix.cuh"

@@ -61,7 +61,7 @@ typedef struct {
  * n_pages out of range, or an n_new below 0 or above max_new or seq_lens[b] sets
  * ATLAS_DEV_BAD_SEQLEN and leaves that sequence as it is.  A free_state out of range, or more
  * pages given back than the ring has room for, sets ATLAS_DEV_BAD_PAGE and moves nothing at
- * all.  A page id outside [0, num_pages) that is taken, given back or asked for a slot sets
+ * all; every slot is -1 then.  A page id outside [0, num_pages) that is taken, given back or asked for a slot sets
  * ATLAS_DEV_BAD_PAGE; ids are passed on as they are, and such a slot is -1.
  * page_table, n_pages, free_pages, free_state and slots are written and may not overlap one
  * another or what is read (ATLAS_ERR_INVALID_ARG).

@@ -25,8 +25,8 @@
 extern "C" {
 #endif
 
-/* Test-only bits of atlas_launch.debug_flags: prefixes on the split kernel, in one launch with the
- * sequences' own keys (at most 16 rows to a sequence and kv head), or on the tensor-core one. */
+/* Test-only bits of atlas_launch.debug_flags: prefixes on the split kernels, in one launch with the
+ * sequences' own keys (at most 16 rows to a sequence and kv head), or on the tensor-core ones. */
 #define ATLAS_DEBUG_SHARED_SPLIT 4u
 #define ATLAS_DEBUG_SHARED_TC 8u
 /* ... (with it) bf16 sequences in tiles of their own, over the prefix and their own keys. */
@@ -54,17 +54,28 @@ typedef struct {
  * t <= seq_lens[b] - q_len + i (the suffix rule of atlas_attn.h: the rows are the last q_len
  * positions of its own cache, page_table[b] and seq_lens[b], which do not count the prefix).
  * It is what atlas_attn_suffix returns for the two parts in one cache, to rounding.  q_len is 1
- * for a decode step.  Softcap, sinks (counted once), ragged q_lens, the fixed split size and
- * sm_count are those of atlas_launch; its three events are recorded before the splits, after
- * them and after the merge.  A window is ATLAS_ERR_INVALID_ARG (it would cut the prefix off),
- * a phase other than ATLAS_PHASE_ALL or a chunk_range ATLAS_ERR_UNSUPPORTED.
+ * for a decode step.  Softcap, sinks (counted once), ragged q_lens and sm_count are those of
+ * atlas_launch; its three events are recorded before the splits, after them and after the
+ * merge.  split_tokens fixes the splits of the own keys and of prefixes on the split kernels; on
+ * the bf16 tensor-core kernels, which cut a prefix where the SMs' shares end, it bounds the parts
+ * of a prefix instead (max_prefix_pages * page_tokens / split_tokens + 2).  A window is
+ * ATLAS_ERR_INVALID_ARG (it would cut the prefix off), a phase other than ATLAS_PHASE_ALL or a
+ * chunk_range ATLAS_ERR_UNSUPPORTED.  `out` may not overlap what the call reads.
+ * The same call on the same arrays gives the same bits.  On the split kernels a sequence's bits
+ * depend on its own group alone (and on the sizes that the call is planned from); on the bf16
+ * tensor-core kernels also on the other groups and lengths of the batch and on sm_count, which
+ * decide where the shares of the SMs end.
  * On the device: group_starts out of order or out of range set ATLAS_DEV_BAD_SEQLEN and leave
  * every row NaN; a prefix length out of range does so for its group, a bad seq_len or q_len
  * for its sequence; a page id outside the pool sets ATLAS_DEV_BAD_PAGE and leaves the rows
  * that read it NaN.
- * Precision: bf16 prefixes are multiplied as bf16 parts of the weights, two where a call has at
- * most 128 rows to a (group, kv head) -- there the second costs nothing -- or where few keys
- * carry a row, and one elsewhere, as in atlas_attn.h for many rows.
+ * Precision: the split kernels are those of atlas_attn_decode (bf16 weights as two bf16 parts,
+ * fp32 products for fp32).  The bf16 tensor-core kernels take the weights as two bf16 parts where
+ * the tiles have 128 rows (at most 128 to a group and kv head, on average), where the second costs
+ * nothing, or where few keys carry a row, and as one elsewhere, as atlas_attn_prefill does.  The
+ * fp32 one takes three tf32 products for each, within the 1e-5 of the largest value that holds for
+ * all fp32 calls; its sums, which the tensor cores cut off and do not round, are about 1e-6 off in
+ * the root mean square where fp32 products are 4e-7.
  */
 atlas_status atlas_attn_shared(const void *q, const void *k_pages, const void *v_pages,
                                const int32_t *page_table, const int32_t *seq_lens,
