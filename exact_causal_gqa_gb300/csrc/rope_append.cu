@@ -261,10 +261,11 @@ __global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------- with norms
-constexpr int kNormTokens = 2;
+// Tokens of a CTA: 2, and 4 where a row costs more (below: 8 take no less).
+constexpr int kNormTokens = 2, kMoreTokens = 4;
 
-// Slots and CTAs as above.  A unit (x, y) -- a pair, or past the rotated part two neighbours --
-// becomes
+// Slots and CTAs as above, where 16 bytes divide the rotated part's halves.  A unit (x, y) -- a
+// pair, or past the rotated part two elements of a slot -- becomes
 //   (x w0 cos - y w1 sin, y w1 cos + x w0 sin),
 // four factors that the CTA works out once for each token, for q and for k, when all heads share
 // their weights (PER_HEAD: cosines and sines alone).
@@ -273,14 +274,18 @@ constexpr int kNormTokens = 2;
 // 80 %, and the rows' loads need all 2048 threads of an SM.  Two heads a thread halve the factors'
 // reads and cost that occupancy: 150 us; factors in registers, a warp to a token, 224 us; the
 // rows through a cp.async ring 183 us; 6 and 5 CTAs an SM 157 and 166 us.  Weights of each head
-// are read row by row: 204 us.
-template <typename T, int V, typename W, bool PER_HEAD>
+// are read row by row: 188 us, 195 with two tokens a CTA.  Rows that are rotated as a whole (WHOLE)
+// have kernels of their own: with the choice in them 145 us.  Half a row 150, and 159 where its two
+// parts were two branches of a warp.
+template <typename T, int V, typename W, bool PER_HEAD, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, PER_HEAD ? 5 : 8)
     norm_rope_kernel(const __grid_constant__ RopeParams p) {
     using X = Vec<T, V>;
     // unit u of a slot of V at [u % V][slot]: neighbouring lanes read neighbouring vectors
-    __shared__ float4 turns[kNormTokens][PER_HEAD ? 1 : 2][kMaxPairs];
-    __shared__ TokenRows rows[kNormTokens];
+    using Turn = std::conditional_t<PER_HEAD, float2, float4>;
+    constexpr int kTokens = PER_HEAD ? kMoreTokens : kNormTokens;
+    __shared__ Turn turns[kTokens][PER_HEAD ? 1 : 2][kMaxPairs];
+    __shared__ TokenRows rows[kTokens];
     const int token0 = (int)blockIdx.x * p.tokens_per_cta;
     const int tokens = min(p.tokens_per_cta, p.B * p.n - token0);
     const int h0 = (int)blockIdx.y * p.heads_per_cta;
@@ -296,10 +301,11 @@ __global__ void __launch_bounds__(kThreads, PER_HEAD ? 5 : 8)
         }
         const int at = u % V * slots + u / V;
         if constexpr (PER_HEAD) {
-            turns[k][0][at] = make_float4(c, s, c, s);
+            turns[k][0][at] = make_float2(c, s);
         } else {
-            const bool halves = u < p.pairs && !p.interleaved;
-            const int e0 = halves ? u : 2 * u, e1 = halves ? u + p.pairs : 2 * u + 1;
+            // (without pairs side by side a slot's units are of its first and second vector)
+            const int e0 = p.interleaved ? 2 * u : u < p.pairs ? u : u + u / V * V;
+            const int e1 = p.interleaved ? 2 * u + 1 : u < p.pairs ? u + p.pairs : e0 + V;
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
                 float w0[1], w1[1];
@@ -337,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, PER_HEAD ? 5 : 8)
         }
         // The slot's two vectors: of its units' first and second elements, or (pairs side by
         // side, and past the rotated part) of 2 V neighbours.
-        const bool turned = slot * V < p.pairs, halves = turned && !p.interleaved;
+        const bool turned = WHOLE || slot * V < p.pairs, halves = turned && !p.interleaved;
         const int e0 = halves ? slot * V : 2 * slot * V, e1 = halves ? e0 + p.pairs : e0 + V;
         X x0 = load_vec<T, V>(src + e0), x1 = load_vec<T, V>(src + e1);
         if (h >= p.Hq + p.Hkv) {
@@ -359,8 +365,9 @@ __global__ void __launch_bounds__(kThreads, PER_HEAD ? 5 : 8)
             for (int d = 1; d < slots; d *= 2) s += __shfl_xor_sync(mask, s, d);
             return s;
         }, pre, factor);
-        const float4 *t = turns[k][PER_HEAD || is_q ? 0 : 1] + slot;
-        auto emit = [&](auto split, auto rotate) {
+        const Turn *t = turns[k][PER_HEAD || is_q ? 0 : 1] + slot;
+        auto emit = [&](auto split) {
+            const bool rotate = WHOLE || turned;
             float w0[V], w1[V];
             if constexpr (PER_HEAD) {
                 const void *weights = is_q ? p.q_weight : p.k_weight;
@@ -374,15 +381,16 @@ __global__ void __launch_bounds__(kThreads, PER_HEAD ? 5 : 8)
                 const int a = split ? i : 2 * i % V, b = split ? i : (2 * i + 1) % V;
                 const bool a0 = split || 2 * i < V, b0 = !split && 2 * i < V;
                 float x = widen((a0 ? x0 : x1).e[a]) * factor, y = widen((b0 ? x0 : x1).e[b]) * factor;
+                const Turn f = t[i << lg_slots];
+                float u, v;
                 if constexpr (PER_HEAD) {
                     x *= (a0 ? w0 : w1)[a];
                     y *= (b0 ? w0 : w1)[b];
-                }
-                const float4 f = t[i << lg_slots];
-                float u = x * f.x, v = y * f.z;
-                if (rotate) {
-                    u -= y * f.y;
-                    v += x * f.w;
+                    u = rotate ? x * f.x - y * f.y : x;
+                    v = rotate ? y * f.x + x * f.y : y;
+                } else {
+                    u = rotate ? x * f.x - y * f.y : x * f.x;
+                    v = rotate ? y * f.z + x * f.w : y * f.z;
                 }
                 (a0 ? y0 : y1).e[a] = narrow<T>(u * pre);
                 (b0 ? y0 : y1).e[b] = narrow<T>(v * pre);
@@ -390,41 +398,74 @@ __global__ void __launch_bounds__(kThreads, PER_HEAD ? 5 : 8)
             store_vec<T, V>(dst + e0, y0);
             store_vec<T, V>(dst + e1, y1);
         };
-        if (!turned) emit(std::false_type{}, std::false_type{});
-        else if (p.interleaved) emit(std::false_type{}, std::true_type{});
-        else emit(std::true_type{}, std::true_type{});
+        if (p.interleaved) emit(std::false_type{});
+        else emit(std::true_type{});
     }
 }
 
-// Norms where the rotated part is an odd number of pairs, whose halves no vector of two divides.
-// A lane has 16 bytes of a row, whatever they hold; elements of the rotated part find their
-// partners through shared memory (pairs side by side are in one vector).
-template <typename T, typename W>
-__global__ void __launch_bounds__(kThreads, 5) norm_rope_odd_kernel(const __grid_constant__ RopeParams p) {
+// Norms where the halves of the rotated part are no multiple of 16 bytes.  A slot is 16 bytes of
+// each half of the row, whatever they hold; with x, y an element and its partner, both over the
+// row's root mean square, it becomes x A + y B, where A and B hold weights, cosine and sine
+// (outside the rotated part the weight and 0).  Partners are exchanged through shared memory, at
+// places where neighbouring lanes' elements stand side by side; `place` says where an element's
+// partner is.
+// What bounds it: the same rows take 184 us (4.4 TB/s) with 6 of 128 elements rotated, 211 with 126,
+// 167 with pairs side by side: instructions, 42 registers a thread at 6 CTAs (5: 198, 215, 178; 8,
+// which spill: 256, 304, 196).  A slot of 16 bytes, weights read row by row, took 300.  Rotated parts
+// of 4 or 8 bytes' multiples gain nothing from narrower vectors: 24 of 64 elements 55 us, 58 before.
+template <typename T, typename W, bool PER_HEAD>
+__global__ void __launch_bounds__(kThreads, 6) norm_rope_any_kernel(const __grid_constant__ RopeParams p) {
     constexpr int V = 16 / (int)sizeof(T);
     using X = Vec<T, V>;
-    __shared__ float2 turns[kNormTokens][kMaxPairs];  // cosine, sine
-    __shared__ TokenRows rows[kNormTokens];
-    __shared__ float normed[kThreads * V];            // each row's elements, at its lanes' places
+    using Places = Vec<uint16_t, V>;
+    __shared__ float2 turns[kMoreTokens][PER_HEAD ? 1 : 2][2 * kMaxPairs];  // A, B at [half][i][slot]
+    __shared__ __align__(16) uint16_t place[2 * kMaxPairs];
+    __shared__ float normed[2 * V * kThreads];  // [half][i][thread]
+    __shared__ TokenRows rows[kMoreTokens];
     const int token0 = (int)blockIdx.x * p.tokens_per_cta;
     const int tokens = min(p.tokens_per_cta, p.B * p.n - token0);
     const int h0 = (int)blockIdx.y * p.heads_per_cta;
     const int h1 = min(p.Hq + 2 * p.Hkv, h0 + p.heads_per_cta);
-    const int lanes = p.D / V, lg = 31 - __clz(lanes);
-    for (int i = threadIdx.x; i < tokens * p.pairs && h0 < p.Hq + p.Hkv; i += kThreads) {
-        const int k = i / p.pairs, u = i - k * p.pairs;
-        const int32_t pos = p.positions[(int64_t)p.axis[u] * p.B * p.n + token0 + k];
-        cos_sin_turns((uint64_t)(int64_t)pos * p.turn[u], turns[k][u].x, turns[k][u].y);
+    const int half = p.D / 2, slots = half / V, lg = 31 - __clz(slots);
+    auto at_of = [&](int e) {  // [half][i][slot], V and slots powers of two
+        return ((e >= half ? V : 0) + e % V) * slots + (e & (half - 1)) / V;
+    };
+    for (int i = threadIdx.x; i < tokens * half && h0 < p.Hq + p.Hkv; i += kThreads) {
+        const int k = i / half, u = i - k * half;
+        const bool turned = u < p.pairs;
+        const bool apart = turned && !p.interleaved;
+        const int e0 = apart ? u : 2 * u, e1 = apart ? u + p.pairs : 2 * u + 1;
+        float c = 1.f, s = 0.f;
+        if (turned) {
+            const int32_t pos = p.positions[(int64_t)p.axis[u] * p.B * p.n + token0 + k];
+            cos_sin_turns((uint64_t)(int64_t)pos * p.turn[u], c, s);
+        }
+#pragma unroll
+        for (int which = 0; which < (PER_HEAD ? 1 : 2); ++which) {
+            float w0[1] = {1.f}, w1[1] = {1.f};
+            if constexpr (!PER_HEAD) {
+                load_weights<W, 1>(p, which ? p.k_weight : p.q_weight, 0, e0, w0);
+                load_weights<W, 1>(p, which ? p.k_weight : p.q_weight, 0, e1, w1);
+            }
+            turns[k][which][at_of(e0)] = make_float2(w0[0] * c, -w1[0] * s);
+            turns[k][which][at_of(e1)] = make_float2(w1[0] * c, w0[0] * s);
+        }
+        if (k == 0) {
+            auto place_of = [&](int e) {
+                return (uint16_t)(((e >= half ? V : 0) + e % V) * kThreads + (e & (half - 1)) / V);
+            };
+            place[e0] = place_of(turned ? e1 : e0);
+            place[e1] = place_of(turned ? e0 : e1);
+        }
     }
     if ((int)threadIdx.x < tokens)
         rows[threadIdx.x] = token_rows(p, token0 + (int)threadIdx.x, h1 > p.Hq);
     __syncthreads();
 
-    const int lane = threadIdx.x & (lanes - 1), e0 = lane * V;
-    const unsigned mask = (lanes == 32 ? ~0u : (1u << lanes) - 1u) << (threadIdx.x % 32 & ~(lanes - 1));
-    float *const row = normed + (threadIdx.x - lane) * V;
-    const bool inside = p.interleaved != 0;
+    const int slot = threadIdx.x & (slots - 1);
+    const unsigned mask = (slots == 32 ? ~0u : (1u << slots) - 1u) << (threadIdx.x % 32 & ~(slots - 1));
     const int per_token = (h1 - h0) << lg;
+    const bool both = 2 * p.pairs > half;  // the second half has a rotated part too
     for (int k = 0, item = threadIdx.x;; item += kThreads) {
         while (k < tokens && item >= per_token) {
             item -= per_token;
@@ -434,57 +475,66 @@ __global__ void __launch_bounds__(kThreads, 5) norm_rope_odd_kernel(const __grid
         const TokenRows &r = rows[k];
         const int h = h0 + (item >> lg);
         if (!r.any || (h >= p.Hq && r.cache < 0)) continue;
-        const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
-        const int hh = is_q ? h : h - p.Hq - (is_k ? 0 : p.Hkv);
-        const T *src = is_q   ? static_cast<const T *>(p.q) + r.q + hh * p.qs[1]
-                       : is_k ? static_cast<const T *>(p.k_new) + r.k + hh * p.ks[1]
-                              : static_cast<const T *>(p.v_new) + r.v + hh * p.vs[1];
-        T *dst = is_q ? static_cast<T *>(p.q_out) + r.q_out + (int64_t)hh * p.n * p.D
-                      : static_cast<T *>(is_k ? p.k_pages : p.v_pages) + r.cache + (int64_t)hh * p.P * p.D;
-        X x = load_vec<T, V>(src + e0);
-        if (is_q || is_k) {
-            float pre, factor, w[V], y[V];
-            load_weights<W, V>(p, is_q ? p.q_weight : p.k_weight, hh, e0, w);
+        const T *src;
+        T *dst;
+        if (h < p.Hq) {
+            src = static_cast<const T *>(p.q) + r.q + h * p.qs[1];
+            dst = static_cast<T *>(p.q_out) + r.q_out + (int64_t)h * p.n * p.D;
+        } else if (h < p.Hq + p.Hkv) {
+            src = static_cast<const T *>(p.k_new) + r.k + (h - p.Hq) * p.ks[1];
+            dst = static_cast<T *>(p.k_pages) + r.cache + (int64_t)(h - p.Hq) * p.P * p.D;
+        } else {
+            src = static_cast<const T *>(p.v_new) + r.v + (h - p.Hq - p.Hkv) * p.vs[1];
+            dst = static_cast<T *>(p.v_pages) + r.cache + (int64_t)(h - p.Hq - p.Hkv) * p.P * p.D;
+        }
+        const int e0 = slot * V;
+        X x[2] = {load_vec<T, V>(src + e0), load_vec<T, V>(src + half + e0)};
+        if (h < p.Hq + p.Hkv) {
+            const bool is_q = h < p.Hq;
+            float pre, factor;
             norm_factor(p, [&](float scale) {
                 float s = 0.f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float a = widen(x.e[i]) * scale;
-                    s = fmaf(a, a, s);
+                    const float a = widen(x[0].e[i]) * scale, b = widen(x[1].e[i]) * scale;
+                    s = fmaf(a, a, fmaf(b, b, s));
                 }
-                for (int d = 1; d < lanes; d *= 2) s += __shfl_xor_sync(mask, s, d);
+                for (int d = 1; d < slots; d *= 2) s += __shfl_xor_sync(mask, s, d);
                 return s;
             }, pre, factor);
+            float y[2][V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) y[i] = widen(x.e[i]) * factor * w[i];
-            const bool turned = e0 < 2 * p.pairs;
-            if (!inside) {  // partners in other lanes' vectors
-                if (turned) {
+            for (int j = 0; j < 2; ++j) {
+                if constexpr (PER_HEAD)
+                    load_weights<W, V>(p, is_q ? p.q_weight : p.k_weight, is_q ? h : h - p.Hq, j * half + e0, y[j]);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) row[e0 + i] = y[i];
+                for (int i = 0; i < V; ++i)
+                    y[j][i] = PER_HEAD ? widen(x[j].e[i]) * factor * y[j][i] : widen(x[j].e[i]) * factor;
+                if (!p.interleaved && (j == 0 || both)) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) normed[(j * V + i) * kThreads + threadIdx.x] = y[j][i];
                 }
-                __syncwarp(mask);
             }
-            if (turned) {
-                float out[V];
+            if (!p.interleaved) __syncwarp(mask);
+            const float2 *t = turns[k][PER_HEAD || is_q ? 0 : 1] + slot;
+            const float *const row = normed + threadIdx.x - slot;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bool plain = j == 1 && !both;
+                Places at;
+                if (!p.interleaved && !plain) at = load_vec<uint16_t, V>(place + j * half + e0);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const int e = e0 + i;
-                    out[i] = y[i];
-                    if (e >= 2 * p.pairs) continue;
-                    const bool first = p.interleaved ? i % 2 == 0 : e < p.pairs;
-                    const float2 a = turns[k][p.interleaved ? e / 2 : first ? e : e - p.pairs];
-                    const float other = p.interleaved ? y[i ^ 1] : row[first ? e + p.pairs : e - p.pairs];
-                    out[i] = first ? y[i] * a.x - other * a.y : y[i] * a.x + other * a.y;
+                    const float2 f = t[(j * V + i) << lg];
+                    float out = y[j][i] * f.x;
+                    if (!plain) out = fmaf(p.interleaved ? y[j][i ^ 1] : row[at.e[i]], f.y, out);
+                    x[j].e[i] = narrow<T>(out * pre);
                 }
-#pragma unroll
-                for (int i = 0; i < V; ++i) y[i] = out[i];
             }
-#pragma unroll
-            for (int i = 0; i < V; ++i) x.e[i] = narrow<T>(y[i] * pre);
-            if (!inside) __syncwarp(mask);  // (the places are written again)
+            if (!p.interleaved) __syncwarp(mask);  // (the places are written again)
         }
-        store_vec<T, V>(dst + e0, x);
+        store_vec<T, V>(dst + e0, x[0]);
+        store_vec<T, V>(dst + half + e0, x[1]);
     }
 }
 
@@ -514,24 +564,24 @@ cudaError_t launch(RopeParams &p, cudaStream_t stream) {
 
 template <typename T, int V, typename W>
 cudaError_t launch_norm_vectors(RopeParams &p, cudaStream_t stream) {
-    const dim3 grid = cut(p, p.D / (2 * V), kNormTokens);
-    if (p.weight_step) norm_rope_kernel<T, V, W, true><<<grid, kThreads, 0, stream>>>(p);
-    else norm_rope_kernel<T, V, W, false><<<grid, kThreads, 0, stream>>>(p);
+    const dim3 grid = cut(p, p.D / (2 * V), p.weight_step ? kMoreTokens : kNormTokens);
+    auto kern = 2 * p.pairs == p.D ? p.weight_step ? norm_rope_kernel<T, V, W, true, true>
+                                                   : norm_rope_kernel<T, V, W, false, true>
+                : p.weight_step    ? norm_rope_kernel<T, V, W, true, false>
+                                   : norm_rope_kernel<T, V, W, false, false>;
+    kern<<<grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 // With norms, weights of type W.
 template <typename T, typename W>
 cudaError_t launch_norm(RopeParams &p, cudaStream_t stream) {
-    if (p.pairs % 2) {
-        const dim3 grid = cut(p, p.D * (int)sizeof(T) / 16, kNormTokens);
-        norm_rope_odd_kernel<T, W><<<grid, kThreads, 0, stream>>>(p);
-        return cudaGetLastError();
-    }
-    if constexpr (sizeof(T) == 2)
-        if (p.pairs % 8 == 0) return launch_norm_vectors<T, 8, W>(p, stream);
-    return p.pairs % 4 == 0 ? launch_norm_vectors<T, 4, W>(p, stream)
-                            : launch_norm_vectors<T, 2, W>(p, stream);
+    constexpr int V = 16 / (int)sizeof(T);
+    if (p.pairs % V == 0) return launch_norm_vectors<T, V, W>(p, stream);
+    const dim3 grid = cut(p, p.D / (2 * V), kMoreTokens);
+    if (p.weight_step) norm_rope_any_kernel<T, W, true><<<grid, kThreads, 0, stream>>>(p);
+    else norm_rope_any_kernel<T, W, false><<<grid, kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 // A stride triple (batch, head, token) in elements; all zero means dense rows.
