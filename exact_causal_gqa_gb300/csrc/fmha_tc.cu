@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     if constexpr (SHARED) {
         n_items = (int64_t)blockIdx.x * p.st.head[0] < p.st.head[1] ? p.st.counts[blockIdx.x] : 0;
         const int32_t *from = reinterpret_cast<const int32_t *>(p.st.segs + (int64_t)blockIdx.x * p.st.max_items);
+        // (all places, whatever their number is: both come with one wait)
         for (int i = threadIdx.x; i < p.st.max_items * (int)(sizeof(SharedSeg) / 4); i += blockDim.x)
             reinterpret_cast<int32_t *>(segs)[i] = from[i];
         if (n_items == 0) {
@@ -451,7 +452,9 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     if (threadIdx.x == 0) bad_words[0] = bad_words[1] = 0u;
     __syncthreads();
     uint64_t skip = 0, bad = 0;
-    for (int it = 0; SHARED && it < n_items; ++it) {
+    // (SHARED: the items side by side, as many warps to each as there are)
+    const int per_item = SHARED ? max(1, C::kThreads / 32 / n_items) : 1;
+    for (int it = warp / per_item; SHARED && it < n_items; it += C::kThreads / 32 / per_item) {
         const TcWork w = item(it);
         const int blk1 = w.blk0 + w.nb;
         for (int part = 0; part < 2; ++part) {  // pages of the prefix, then the sequence's own
@@ -459,7 +462,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             const int keys = part ? min(w.own_len, (blk1 - w.n_pre) * BN) : min(w.pre_len, blk1 * BN);
             const int32_t *table = part ? p.page_table + (int64_t)w.b * p.max_pages
                                         : p.st.prefix_table + (int64_t)w.group * p.st.max_prefix_pages;
-            for (int pg = first * BN / p.P + (int)threadIdx.x; pg * p.P < keys; pg += blockDim.x) {
+            for (int pg = first * BN / p.P + warp % per_item * 32 + lane; pg * p.P < keys; pg += 32 * per_item) {
                 const int id = table[pg];
                 if (id < 0 || id >= p.num_pages) bad |= 1ull << it;
             }

@@ -9,12 +9,12 @@
 //     once for each 16 rows, from L2 for all but the first;
 //   tensor cores: the tensor-core kernels take the prefixes with 128 or 256 of a group's rows
 //     to a CTA (shared_prefix.cuh).  The own splits, on the split kernels or the tensor cores by
-//     the rows of one sequence, are a launch of their own beside that one: the second of the two
+//     a sequence's rows and keys, are a launch of their own beside that one: the second of the two
 //     is a dependent of the first, whose results it does not need, and its CTAs take the SMs as
 //     those of the first leave them.
-// bf16 sequences whose rows fill tiles by themselves have no use for a gather.  Their tiles walk
-// the prefix's blocks and go on with the sequence's own, in one launch, and write the output;
-// only tiles that a cut between two CTAs goes through are merged.
+// bf16 sequences whose rows fill tiles by themselves have little use for a gather (whole_pays).
+// Their tiles walk the prefix's blocks and go on with the sequence's own, in one launch, and write
+// the output; only tiles that a cut between two CTAs goes through are merged.
 #include "internal.h"
 #include "atlas_shared.h"
 #include "shared_prefix.cuh"
@@ -51,9 +51,6 @@ int64_t own_split(int64_t max_ctx) {
     return round_up((max_ctx + splits - 1) / splits, 64);
 }
 
-// Rows of one sequence and kv head from which its tiles are its own.
-constexpr int64_t kWholeRows = 128;
-
 // Bytes a microsecond that the split kernels of 8 and of 16 columns take on one SM, when not all
 // SMs ask for memory.
 constexpr float kOwnRate = 70e3f, kOwnRateWide = 50e3f;
@@ -68,6 +65,26 @@ bool split_pays(double prefix_bytes, int64_t tiles, double flops, bool f32) {
     const double tc = f32 ? 22.0 + std::max(prefix_bytes / 2.9e6, flops / 1.2e8)
                           : 18.0 + std::max(prefix_bytes / 5e6, flops / 9e8);
     return (double)tiles * prefix_bytes / (f32 ? 5e6 : 6e6) <= tc;
+}
+
+// Rows and own keys of a sequence up to which the own keys of more than 16 rows are splits of the
+// decode kernels (a CTA for each 16 rows) all the same: 64 sequences of 32 rows, up to 120 keys 73
+// us and 79 on the tensor cores, up to 1000 103 and 107, up to 2500 148 and 134; of 48 rows 107 and
+// 97 with 120.
+constexpr int64_t kOwnSplitRows = 32, kOwnSplitKeys = 1024;
+
+// Whether tiles over whole keys take less time than the prefixes' tiles, which many sequences'
+// rows fill, beside the own ones: a block of a prefix 2.0 us for 256 rows, and 1.1 where a sequence's
+// end in the first half, against 9.5 for each own tile of 128 rows on the tensor cores, which has a
+// launch, a start and states to itself there, or 2.6 where the own keys are splits.  Fitted to 98
+// sizes of 20 to 264 rows, prefixes of 300 to 16000 keys and 100 or 800 own ones (32 / 8 heads of
+// 128), of which three lose more than 6 %; whole tiles and others: 128 sequences, 1500 keys, 264
+// rows 403 and 510 us, 64 rows 164 and 176, 20 rows 146 and 102; 16, 16000 keys, 264 rows 367 and 291.
+bool whole_pays(int64_t rows, int64_t max_prefix, bool own_splits) {
+    const int64_t pairs = rows / 256 + (rows % 256 > 128), single = rows % 256 > 0 && rows % 256 <= 128;
+    const double more = 2.0 * (double)pairs + 1.1 * (double)single - (double)rows / 128.0;
+    return (double)((max_prefix + 127) / 128) * more <=
+           (own_splits ? 2.6 : 9.5) * (double)((rows + 127) / 128);
 }
 
 atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const atlas_shared *S,
@@ -99,18 +116,31 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->split = false;
     const int64_t seq_rows = (int64_t)G * L->q_len;
     plan->stream = !f32 && !plan->split;
-    plan->whole = plan->stream && seq_rows >= kWholeRows && L->split_tokens == 0;
+    const int64_t max_ctx = (int64_t)L->max_pages_per_seq * P;
+    const bool own_splits = seq_rows <= kOwnSplitRows && max_ctx <= kOwnSplitKeys;
+    plan->whole = plan->stream && !few && L->split_tokens == 0 && whole_pays(seq_rows, max_prefix, own_splits);
     if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->whole = false;
     if (L->debug_flags & ATLAS_DEBUG_SHARED_WHOLE) plan->whole = plan->stream;
     if (plan->stream && !plan->whole && few && L->split_tokens == 0 &&
         (int64_t)L->batch * Hkv * plan->own.col_tiles >= 2 * sms) {
         // The own splits run beside the tiles, the longest first: where there are enough
         // sequences they are best left whole (up to 4096 keys).
-        own.split_tokens = (int32_t)own_split((int64_t)L->max_pages_per_seq * P);
+        own.split_tokens = (int32_t)own_split(max_ctx);
         if (make_plan(ATLAS_KIND_SUFFIX, Hq, Hkv, D, P, &own, &plan->own) != ATLAS_OK)
             return ATLAS_ERR_UNSUPPORTED;
     }
-    if (few && (int64_t)plan->own.n_chunks * Hkv * plan->own.col_tiles * L->batch >= INT32_MAX)
+    if (plan->stream && !plan->whole && !few && L->split_tokens == 0 && own_splits) {
+        const int64_t out = (int64_t)L->batch * Hq * L->q_len;
+        plan->own.path = Path::SplitBF16;
+        plan->own.col_tiles = (int)((seq_rows + 15) / 16);
+        plan->own.chunk = (int)own_split(max_ctx);
+        plan->own.n_chunks = (int)((max_ctx + plan->own.chunk - 1) / plan->own.chunk);
+        plan->own.acc_bytes = (size_t)out * plan->own.n_chunks * D * sizeof(float);
+        plan->own.ml_offset = (size_t)round_up((int64_t)plan->own.acc_bytes, 256);
+        plan->own.ws_bytes = plan->own.ml_offset + (size_t)out * plan->own.n_chunks * 2 * sizeof(float);
+    }
+    const bool own_cols = plan->own.path == Path::SplitBF16 || plan->own.path == Path::SplitF32;
+    if (own_cols && (int64_t)plan->own.n_chunks * Hkv * plan->own.col_tiles * L->batch >= INT32_MAX)
         return ATLAS_ERR_UNSUPPORTED;  // (the own splits' CTAs)
     const int64_t tile_of = plan->whole ? seq_rows : group_rows;
     plan->tiles = plan->split ? cols : !f32 && tile_of > 128 ? 2 : 1;
@@ -125,14 +155,14 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
         // At most this many states of a tile: what the likely number of tiles leaves to each,
         // and some more where groups are uneven.
         const int64_t blocks = (max_prefix + 127) / 128 +
-                               (plan->whole ? ((int64_t)L->max_pages_per_seq * P + 127) / 128 : 0);
+                               (plan->whole ? (max_ctx + 127) / 128 : 0);
         if (L->split_tokens > 0) plan->n_pre = (int)((max_prefix + L->split_tokens - 1) / L->split_tokens + 2);
         else plan->n_pre = (int)std::min<int64_t>(blocks / 4 + 3, sms / likely + 6);
         plan->chunk = 0;
         // (short tiles that count as more blocks make for more CTAs than SMs)
         plan->ctas = sms + units / 10 + 2;
         const double line = (double)units * kPairCost * (double)(blocks + kTileBlocks);
-        if (line * (1.0 + (double)units / (sms * 14.0)) + 1e6 >= INT32_MAX)
+        if (line * (1.0 + (double)units / (sms * 13.0)) + 1e6 >= INT32_MAX)
             return ATLAS_ERR_UNSUPPORTED;  // (places in the line have 32 bits)
         const int64_t states = plan->whole ? plan->ctas * 2 * cta_rows : out_rows * plan->n_pre;
         plan->ml_at = plan->acc_at + (size_t)round_up(states * D * 4, 256);
@@ -149,7 +179,6 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
         // One wave of CTAs, all with as many keys: the own keys (half of the most there may be)
         // and the prefixes' for each CTA's rows, on the CTAs that are resident.
         const int64_t own_units = (int64_t)L->batch * Hkv * ((G * L->q_len + cols - 1) / cols);
-        const int64_t max_ctx = (int64_t)L->max_pages_per_seq * P;
         const int64_t slots = sms * (f32 ? kSplitWaveF32 : kSplitWave) / 100;
         const int64_t keys = own_units * max_ctx / 2 + likely * max_prefix;
         chunk = round_up((keys + slots - 1) / slots, 64);
@@ -324,7 +353,7 @@ atlas_status launch_tc(const SharedPlan &plan, const void *q, const void *k_page
         const bool beside = plan.own.path == Path::SplitBF16;
         tp.st = stream_arrays(plan, Hq / Hkv, S, L);
         tp.st.wait_first = beside;
-        tp.st.own_rate = !beside ? 0.f : Hq / Hkv * L->q_len <= 8 ? kOwnRate : kOwnRateWide;
+        tp.st.own_rate = !beside ? 0.f : Hq / Hkv * L->q_len <= 8 ? kOwnRate : kOwnRateWide / plan.own.col_tiles;
         tp.seq_lens = seq_lens;
         tp.max_pages = L->max_pages_per_seq;
         if (launch_shared_plan(tp, stream) != cudaSuccess) return ATLAS_ERR_CUDA;

@@ -151,9 +151,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
     __shared__ int s_most;
     if (tid == 0) s_most = 0;
     int64_t all = 0;
+    int n_tiles = 0;
     for (int u0 = 0; u0 < st.units; u0 += N) {
         const int u = u0 + tid;
-        int64_t length = 0;
+        int64_t length = 0, tiles = 0;
         int nb = 0;
         if (u < st.units) {
             if (!st.whole) {
@@ -166,28 +167,35 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
             if (rows_of[u] > 0 && blocks_of[u] > 0) {
                 nb = blocks_of[u];
                 length = (int64_t)head_cost(rows_of[u], nb + kTileBlocks) * p.Hkv;
+                tiles = (int64_t)((rows_of[u] + st.tile_rows - 1) / st.tile_rows) * p.Hkv;
             }
         }
         nb = __reduce_max_sync(0xffffffffu, nb);
         int64_t total;
-        plan_scan(length, total);
+        plan_scan(tiles << 36 | length, total);  // (lengths below 2^31 in all, tiles below 2^26)
+        n_tiles += (int)(total >> 36);
+        total &= (1ll << 36) - 1;
         if (tid % 32 == 0 && nb > 0) atomicMax(&s_most, nb);  // (zeroed before the scan's barriers)
         all += total;
     }
     __syncthreads();
     const int most = s_most;
-    // A CTA's share: one CTA for each SM, few enough states of a tile, and few enough pieces of a
-    // CTA, for which short tiles count as more blocks than they have.
+    // A CTA's share: one CTA for each SM (two, three for very many tiles), few enough states of a
+    // tile, and few enough pieces of a CTA, for which short tiles count as more blocks than they
+    // have.  Shares grow by what that adds, up to an eighth: a few CTAs more than SMs would wait for
+    // one to end (57 sequences of 256 rows, 256 to 1792 own keys: 708 us, not 451).
     int ctas = st.own_rate > 0.f ? ctas_beside(p, (float)all, (float)own_keys) : st.sms;
-    // (What the short tiles add is a fourteenth of a share each at most.  The host has seen that
+    // (What the short tiles add is a thirteenth of a share each at most.  The host has seen that
     // the line has room for that with a CTA for each SM; with fewer it is seen here.)
-    const float tiles = ((float)before[p.B] / (float)st.tile_rows + (float)st.units) * (float)p.Hkv;
-    if ((float)all * (1.f + tiles / (14.f * (float)ctas)) > 2e9f) ctas = st.sms;
+    if ((float)all * (1.f + (float)n_tiles / (13.f * (float)ctas)) > 2e9f) ctas = st.sms;
+    const int pieces = st.max_items - 2;
+    ctas *= 1 + n_tiles / (ctas * (pieces * 3 / 4));
     int64_t per64 = (all + ctas - 1) / ctas;
     per64 = max(per64, (int64_t)kMinBlocks * kPairCost);
     per64 = max(per64, (int64_t)((most + st.max_states - 3) / (st.max_states - 2)) * kPairCost);
-    const int per = (int)per64;
-    const int least = (per + kSingleCost * (st.max_items - 2) - 1) / (kSingleCost * (st.max_items - 2));
+    int per = (int)per64;
+    const int most_per = per + per / 8;
+    const int least = (most_per + kSingleCost * pieces - 1) / (kSingleCost * pieces);
     carry = 0;
     for (int u0 = 0; u0 < st.units; u0 += N) {
         const int u = u0 + tid;
@@ -205,6 +213,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
         carry += total;
     }
     const int line = (int)carry;
+    per = max(per, min(most_per, (line + ctas - 1) / ctas));
     if (tid == 0) {
         first_of[st.units] = line;
         st.head[0] = per;
