@@ -71,8 +71,9 @@ typedef struct {
  * that read it NaN.
  * Precision: the split kernels are those of atlas_attn_decode (bf16 weights as two bf16 parts,
  * fp32 products for fp32).  The bf16 tensor-core kernels take the weights as two bf16 parts where
- * the tiles have 128 rows (at most 128 to a group and kv head, on average), where the second costs
- * nothing, or where few keys carry a row, and as one elsewhere, as atlas_attn_prefill does.  The
+ * the tiles have 128 rows (at most 128 to a kv head of a group, on average, or of a sequence whose
+ * rows have tiles of their own), where the second costs nothing, or where few keys carry a row, and
+ * as one elsewhere, as atlas_attn_prefill does.  The
  * fp32 one takes three tf32 products for each, within the 1e-5 of the largest value that holds for
  * all fp32 calls; its sums, which the tensor cores cut off and do not round, are about 1e-6 off in
  * the root mean square where fp32 products are 4e-7.

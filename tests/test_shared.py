@@ -181,6 +181,11 @@ CASES = [
     ("bf16", 8, 8, 128, 16, 64, [0, 12], [4500], [64 + 9 * b for b in range(12)], dict(ragged=[64 - 5 * b for b in range(12)])),
     ("bf16", 2, 2, 64, 8, 300, [0, 1, 2], [640, 9], [300, 411], dict(softcap=6.0)),
     ("bf16", 40, 40, 64, 16, 1, list(range(0, 71, 2)), [1 + n % 3 for n in range(35)], [1 + b % 3 for b in range(70)], {}),
+    # own keys of 17 to 32 rows as splits beside the tiles
+    ("bf16", 8, 2, 128, 16, 7, [0, 3, 5], [300, 41], [7, 40, 200, 9, 1000], dict(ragged=[7, 0, 3, 7, 1])),
+    ("bf16", 8, 1, 64, 32, 4, [0, 30], [900], list(range(4, 34)), dict(sinks=True)),
+    # more tiles than the pieces of one wave of CTAs
+    ("bf16", 64, 64, 64, 16, 1, [0, 100, 200], [130, 1], [1 + b % 5 for b in range(200)], {}),
 ]
 
 
