@@ -56,15 +56,18 @@ int64_t own_split(int64_t max_ctx) {
 constexpr float kOwnRate = 70e3f, kOwnRateWide = 50e3f;
 
 // Whether the split kernels take less time: the prefixes once for each CTA's rows, against the
-// plan's launch, a longer start, and the prefixes once.  Fitted to 36 measured sizes: bf16, 32 / 8
-// heads of 128, one prefix, split kernels and tensor cores: 8 sequences behind 1024 keys 22 and 42
-// us, behind 32768 59 and 73; 16 behind 8192 46 and 48; 32 behind 8192 72 and 48; 64 behind 1024 44
-// and 44, behind 32768 315 and 83.  fp32: 8 behind 1024 28 and 48, behind 8192 79 and 56.
-bool split_pays(double prefix_bytes, int64_t tiles, double flops, bool f32) {
+// plan's launch, a longer start, and the prefixes once.  In fp32 the own keys count too: beside
+// prefixes of more than 4 rows they are taken 8 columns wide, where 4 would do.
+// Fitted to 52 measured sizes: bf16, 32 / 8 heads of 128, one prefix, split kernels and tensor cores:
+// 8 sequences behind 1024 keys 22 and 42 us, behind 32768 59 and 73; 16 behind 8192 46 and 48; 32
+// behind 8192 72 and 48; 64 behind 1024 44 and 44, behind 32768 315 and 83.  fp32: 8 behind 1024 22
+// and 36, behind 8192 73 and 43; heads of 64, 32 in 4 groups behind 2000 60 and 38.
+bool split_pays(double prefix_bytes, int64_t tiles, double flops, double own_bytes, bool own_twice, bool f32) {
     // bytes and floating point operations a microsecond
-    const double tc = f32 ? 22.0 + std::max(prefix_bytes / 2.9e6, flops / 1.2e8)
-                          : 18.0 + std::max(prefix_bytes / 5e6, flops / 9e8);
-    return (double)tiles * prefix_bytes / (f32 ? 5e6 : 6e6) <= tc;
+    if (!f32)
+        return (double)tiles * prefix_bytes / 6e6 <= 18.0 + std::max(prefix_bytes / 5e6, flops / 9e8);
+    const double tc = 26.0 + std::max(prefix_bytes / 2.9e6, flops / 1.2e8) + own_bytes / 6e6;
+    return 10.0 + ((double)tiles * prefix_bytes + own_bytes * (own_twice ? 1.3 : 1.0)) / 3.6e6 <= tc;
 }
 
 // Rows and own keys of a sequence up to which the own keys of more than 16 rows are splits of the
@@ -110,13 +113,14 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     const bool few = plan->own.path == Path::SplitBF16 || plan->own.path == Path::SplitF32;
     const int cols = f32 ? (group_rows <= 4 ? 4 : 8) : group_rows <= 8 ? 8 : 16;
     const double bytes = 2.0 * S->n_groups * max_prefix * Hkv * D * (f32 ? 4 : 2);
-    plan->split = few && split_pays(bytes, (group_rows + cols - 1) / cols,
-                                    4.0 * D * rows * Hkv * max_prefix, f32);
+    const int64_t seq_rows = (int64_t)G * L->q_len, max_ctx = (int64_t)L->max_pages_per_seq * P;
+    // (own keys: half of the most there may be)
+    plan->split = few && split_pays(bytes, (group_rows + cols - 1) / cols, 4.0 * D * rows * Hkv * max_prefix,
+                                    (double)L->batch * Hkv * max_ctx * D * (f32 ? 4 : 2),
+                                    cols == 8 && seq_rows <= 4, f32);
     if (few && (L->debug_flags & ATLAS_DEBUG_SHARED_SPLIT)) plan->split = true;
     if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->split = false;
-    const int64_t seq_rows = (int64_t)G * L->q_len;
     plan->stream = !f32 && !plan->split;
-    const int64_t max_ctx = (int64_t)L->max_pages_per_seq * P;
     const bool own_splits = seq_rows <= kOwnSplitRows && max_ctx <= kOwnSplitKeys;
     plan->whole = plan->stream && !few && L->split_tokens == 0 && whole_pays(seq_rows, max_prefix, own_splits);
     if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->whole = false;

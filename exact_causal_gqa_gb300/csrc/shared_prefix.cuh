@@ -110,8 +110,9 @@ __device__ __forceinline__ bool shared_real(const Params &p, int seq0, int rows,
 //
 // Lengths on the line, measured: a block of a 256-row tile (a pair of MMA tiles) 2.0 us, of one
 // whose rows end in its first half 1.1 us, and what a tile takes besides (its queries, the first
-// products, the epilogue) about two blocks.
-constexpr int kPairCost = 7, kSingleCost = 4, kTileBlocks = 2;
+// products, masked blocks, the epilogue) 4 to 6 blocks: 47 prompts of 256 rows with 256 to 1587 own
+// keys behind 355 take 452, 409 and 402 us with 2, 4 and 6.
+constexpr int kPairCost = 7, kSingleCost = 4, kTileBlocks = 5;
 
 // Length of a tile's block.
 __device__ __forceinline__ int block_cost(const SharedStream &st, int tile, int rows) {
