@@ -70,6 +70,13 @@ constexpr int BN = 64;   // keys per block
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when the max grows 256x
 constexpr int kSegBlocks = 4;  // key blocks per O accumulation segment
+// SHARED: the prefixes' outputs are as exact as fp32 sums in some order (8e-7 root mean square behind
+// 4000 keys, where torch's are 8e-7 and the split kernels' 2e-7): segments of two blocks, and hi
+// parts to the nearest, so that lo parts have either sign and lo.lo, which is left out, no mean.
+// Four blocks and hi parts cut off 2.2e-6, two 1.4e-6; 64 x 8 heads of 64 on 8000 keys take 87 us
+// for 79.  (One block is not enough: the softmax could end two segments before the first is folded,
+// which a parity wait cannot tell apart; with two it is at most one ahead.)
+constexpr int kSegBlocksShared = 2;
 
 template <int D>
 struct Cfg {
@@ -145,11 +152,18 @@ __device__ __forceinline__ void umma_tf32_tmem_a(uint32_t d_tmem, uint32_t a_tme
         : "memory");
 }
 
-// x truncated to tf32 (the value the tensor core reads) and the exact remainder.
+// x as tf32, cut off or to the nearest (the value the tensor core reads), and the exact remainder.
+template <bool NEAREST>
 __device__ __forceinline__ float tf32_hi(float x) {
-    return __uint_as_float(__float_as_uint(x) & 0xFFFFE000u);
+    uint32_t b = __float_as_uint(x);
+    if (NEAREST) {
+        const uint32_t up = b + 0x1000u;
+        b = (up & 0x7f800000u) == 0x7f800000u ? b : up;  // (what would leave fp32's range is cut off)
+    }
+    return __uint_as_float(b & 0xffffe000u);
 }
-__device__ __forceinline__ float tf32_lo(float x) { return x - tf32_hi(x); }
+template <bool NEAREST>
+__device__ __forceinline__ float tf32_lo(float x) { return x - tf32_hi<NEAREST>(x); }
 
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, kWaitLimitNs));
@@ -187,6 +201,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                        const __grid_constant__ CUtensorMap tmV, const TcParams p) {
     allow_dependent_launch();  // the merge may start its CTAs (it waits for this grid)
     using C = Cfg<D>;
+    constexpr int kSeg = SHARED ? kSegBlocksShared : kSegBlocks;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -462,9 +477,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 ok = wait_warp(BAR(C::B_PFULL), j & 1, abort_flag) &&
                      wait_warp(BAR(C::B_VT_READY), j & 1, abort_flag);
                 // A new segment overwrites O: the previous one must have been read out.
-                const bool fresh = j % kSegBlocks == 0;
+                const bool fresh = j % kSeg == 0;
                 if (ok && fresh && j > 0)
-                    ok = wait_warp(BAR(C::B_O_DRAINED), (j / kSegBlocks - 1) & 1, abort_flag);
+                    ok = wait_warp(BAR(C::B_O_DRAINED), (j / kSeg - 1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -487,7 +502,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     umma_commit(BAR(C::B_PVDONE));
                     umma_commit(BAR(C::B_VT_FREE));
                     // a segment followed by another one: the converter folds it
-                    if ((j + 1) % kSegBlocks == 0 && j + 1 < nb) umma_commit(BAR(C::B_SEG_DONE));
+                    if ((j + 1) % kSeg == 0 && j + 1 < nb) umma_commit(BAR(C::B_SEG_DONE));
                 }
                 __syncwarp();
             }
@@ -528,8 +543,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             float4 *dst = reinterpret_cast<float4 *>(smem + C::OFF_KLO);
             for (int k = ct; k < C::kBlkBytes / 16; k += 128) {
                 const float4 x = src[k];
-                dst[k] = make_float4(tf32_lo(x.x), tf32_lo(x.y), tf32_lo(x.z), tf32_lo(x.w));
-                src[k] = make_float4(tf32_hi(x.x), tf32_hi(x.y), tf32_hi(x.z), tf32_hi(x.w));
+                dst[k] = make_float4(tf32_lo<SHARED>(x.x), tf32_lo<SHARED>(x.y), tf32_lo<SHARED>(x.z), tf32_lo<SHARED>(x.w));
+                src[k] = make_float4(tf32_hi<SHARED>(x.x), tf32_hi<SHARED>(x.y), tf32_hi<SHARED>(x.z), tf32_hi<SHARED>(x.w));
             }
             fence_proxy_async_smem();
             mbar_arrive(BAR(C::B_KLO_READY));
@@ -572,11 +587,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     // V^T: slab k0/32, row dim, 16-byte chunk (k0 % 32) / 4
                     const uint32_t off = (k0 / 32) * C::kVtSlab + sw128(dim, (k0 % 32) / 4);
                     *reinterpret_cast<float4 *>(smem + C::OFF_VTH + off) =
-                        make_float4(tf32_hi(v[0][e]), tf32_hi(v[1][e]), tf32_hi(v[2][e]),
-                                    tf32_hi(v[3][e]));
+                        make_float4(tf32_hi<SHARED>(v[0][e]), tf32_hi<SHARED>(v[1][e]), tf32_hi<SHARED>(v[2][e]),
+                                    tf32_hi<SHARED>(v[3][e]));
                     *reinterpret_cast<float4 *>(smem + C::OFF_VTL + off) =
-                        make_float4(tf32_lo(v[0][e]), tf32_lo(v[1][e]), tf32_lo(v[2][e]),
-                                    tf32_lo(v[3][e]));
+                        make_float4(tf32_lo<SHARED>(v[0][e]), tf32_lo<SHARED>(v[1][e]), tf32_lo<SHARED>(v[2][e]),
+                                    tf32_lo<SHARED>(v[3][e]));
                 }
             }
             fence_proxy_async_smem();
@@ -597,8 +612,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 ok = false;
                 break;
             }
-            const bool fold = j % kSegBlocks == 0 && j > 0;
-            const int g = j / kSegBlocks - 1;  // the segment folded at block j
+            const bool fold = j % kSeg == 0 && j > 0;
+            const int g = j / kSeg - 1;  // the segment folded at block j
             if (fold) {
                 if (!wait_warp(BAR(C::B_SEG_DONE), g & 1, abort_flag) ||
                     !wait_warp(BAR(C::B_MSEG), g & 1, abort_flag)) {
@@ -645,7 +660,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 break;
             }
         }
-        if (ok && (nb - 1) / kSegBlocks > 0) {
+        if (ok && (nb - 1) / kSeg > 0) {
             m_run_s[r] = m_run;
             mbar_arrive(BAR(C::B_FOLDED));
         }
@@ -692,8 +707,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     const float xs[4] = {x.x * sgn, x.y * sgn, x.z * sgn, x.w * sgn};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        hv[4 * ch + e] = __float_as_uint(tf32_hi(xs[e]));
-                        lv[4 * ch + e] = __float_as_uint(tf32_lo(xs[e]));
+                        hv[4 * ch + e] = __float_as_uint(tf32_hi<SHARED>(xs[e]));
+                        lv[4 * ch + e] = __float_as_uint(tf32_lo<SHARED>(xs[e]));
                     }
                 }
                 tmem_st32(tl + C::QH + 32 * sl, hv);
@@ -783,7 +798,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                         }
                         const float2 e2 = make_float2(ex2(t.x), ex2(t.y));
                         rs2[k & 3] = fadd2(rs2[k & 3], e2);
-                        const float2 hi = make_float2(tf32_hi(e2.x), tf32_hi(e2.y));
+                        const float2 hi = make_float2(tf32_hi<SHARED>(e2.x), tf32_hi<SHARED>(e2.y));
                         const float2 lo = fadd2(e2, make_float2(-hi.x, -hi.y));
                         ph[2 * k] = __float_as_uint(hi.x);
                         ph[2 * k + 1] = __float_as_uint(hi.y);
@@ -803,7 +818,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             // PV(j-1) by the same thread, and its commit tracks every earlier MMA.  At a
             // segment's first block O holds the previous segment, which the converter
             // folds with the max it ended on (below), so nothing is rescaled here.
-            if (j % kSegBlocks != 0 && __any_sync(0xffffffffu, corr != 1.f)) {
+            if (j % kSeg != 0 && __any_sync(0xffffffffu, corr != 1.f)) {
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
@@ -817,16 +832,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(BAR(C::B_PFULL));
-            if ((j + 1) % kSegBlocks == 0 && j + 1 < nb) {
+            if ((j + 1) % kSeg == 0 && j + 1 < nb) {
                 // the max this segment's O is relative to, for the converter's fold
-                reinterpret_cast<float *>(smem + C::OFF_MSEG)[((j / kSegBlocks) & 1) * BM + r] =
+                reinterpret_cast<float *>(smem + C::OFF_MSEG)[((j / kSeg) & 1) * BM + r] =
                     m_used;
                 mbar_arrive(BAR(C::B_MSEG));
             }
         }
         if (ok && !wait_warp(BAR(C::B_PVDONE), (nb - 1) & 1, abort_flag)) ok = false;
         // every segment but the last one is in the running sum
-        const bool folded = (nb - 1) / kSegBlocks > 0;
+        const bool folded = (nb - 1) / kSeg > 0;
         if (ok && folded && !wait_warp(BAR(C::B_FOLDED), 0, abort_flag)) ok = false;
         if (!ok) {
             failed = true;

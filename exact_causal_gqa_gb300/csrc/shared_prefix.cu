@@ -60,13 +60,13 @@ constexpr float kOwnRate = 70e3f, kOwnRateWide = 50e3f;
 // prefixes of more than 4 rows they are taken 8 columns wide, where 4 would do.
 // Fitted to 52 measured sizes: bf16, 32 / 8 heads of 128, one prefix, split kernels and tensor cores:
 // 8 sequences behind 1024 keys 22 and 42 us, behind 32768 59 and 73; 16 behind 8192 46 and 48; 32
-// behind 8192 72 and 48; 64 behind 1024 44 and 44, behind 32768 315 and 83.  fp32: 8 behind 1024 22
-// and 36, behind 8192 73 and 43; heads of 64, 32 in 4 groups behind 2000 60 and 38.
+// behind 8192 72 and 48; 64 behind 1024 44 and 44, behind 32768 315 and 83.  fp32: 8 behind 1024 23
+// and 42, behind 8192 73 and 50; heads of 64, 32 in 4 groups behind 2000 61 and 43.
 bool split_pays(double prefix_bytes, int64_t tiles, double flops, double own_bytes, bool own_twice, bool f32) {
     // bytes and floating point operations a microsecond
     if (!f32)
         return (double)tiles * prefix_bytes / 6e6 <= 18.0 + std::max(prefix_bytes / 5e6, flops / 9e8);
-    const double tc = 26.0 + std::max(prefix_bytes / 2.9e6, flops / 1.2e8) + own_bytes / 6e6;
+    const double tc = 28.0 + std::max(prefix_bytes / 2.7e6, flops / 1.2e8) + own_bytes / 6e6;
     return 10.0 + ((double)tiles * prefix_bytes + own_bytes * (own_twice ? 1.3 : 1.0)) / 3.6e6 <= tc;
 }
 
