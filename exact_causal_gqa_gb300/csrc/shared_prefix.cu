@@ -165,7 +165,7 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
         plan->chunk = 0;
         // (short tiles that count as more blocks make for more CTAs than SMs)
         plan->ctas = sms + units / 10 + 2;
-        const double line = (double)units * kPairCost * (double)(blocks + kTileBlocks);
+        const double line = (double)units * kPairCost * (double)(blocks + kWholeTileBlocks);
         if (line * (1.0 + (double)units / (sms * 13.0)) + 1e6 >= INT32_MAX)
             return ATLAS_ERR_UNSUPPORTED;  // (places in the line have 32 bits)
         const int64_t states = plan->whole ? plan->ctas * 2 * cta_rows : out_rows * plan->n_pre;

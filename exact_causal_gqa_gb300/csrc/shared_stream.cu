@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
     constexpr int N = kPlanThreads;
     __shared__ int s_starts[N + 1], s_pre[N], s_len[N], s_before[N + 1], s_group[N], s_rows[N],
         s_blocks[N], s_weight[N], s_cost[N], s_first[N + 1];
+    __shared__ __align__(16) int s_key[N];  // the sequences' order: length, then place
     const SharedStream &st = p.st;
     const int tid = (int)threadIdx.x;
     const bool small = p.B <= N;  // (and as many groups at most)
@@ -99,6 +100,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
         mine = p.seq_lens[tid];
         if (small) s_len[tid] = mine;
     }
+    static_assert(N == 1 << 9, "the keys' places");
+    s_key[tid] = tid < p.B ? min(max(mine, 0), (1 << 22) - 1) << 9 | (N - 1 - tid) : -1;
     const bool bad = __syncthreads_or(wrong) != 0;
     uint32_t flags = bad ? ATLAS_DEV_BAD_SEQLEN : 0u;
 
@@ -150,6 +153,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
     };
     __shared__ int s_most;
     if (tid == 0) s_most = 0;
+    const int tile_blocks = st.whole ? kWholeTileBlocks : kTileBlocks;
     int64_t all = 0;
     int n_tiles = 0;
     for (int u0 = 0; u0 < st.units; u0 += N) {
@@ -166,7 +170,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
             }
             if (rows_of[u] > 0 && blocks_of[u] > 0) {
                 nb = blocks_of[u];
-                length = (int64_t)head_cost(rows_of[u], nb + kTileBlocks) * p.Hkv;
+                length = (int64_t)head_cost(rows_of[u], nb + tile_blocks) * p.Hkv;
                 tiles = (int64_t)((rows_of[u] + st.tile_rows - 1) / st.tile_rows) * p.Hkv;
             }
         }
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
         int64_t length = 0;
         if (u < st.units) {
             const bool some = rows_of[u] > 0 && blocks_of[u] > 0;
-            const int nb = some ? max(blocks_of[u] + kTileBlocks, least) : 0;
+            const int nb = some ? max(blocks_of[u] + tile_blocks, least) : 0;
             weight_of[u] = nb;
             cost_of[u] = some ? head_cost(rows_of[u], nb) : 1;
             length = some ? (int64_t)cost_of[u] * p.Hkv : 0;
@@ -283,10 +287,13 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
             // The order of the sequences' own splits: the longest first, so that the CTAs left
             // over when the others are done are short ones.
             for (int b = me; b < p.B && !st.whole; b += kInfoThreads) {
-                const int mine = lens[b];
+                const int mine = s_key[b];
                 int rank = 0;
-#pragma unroll 8
-                for (int k = 0; k < p.B; ++k) rank += lens[k] > mine || (lens[k] == mine && k < b);
+#pragma unroll 4
+                for (int k = 0; k < p.B; k += 4) {
+                    const int4 x = *reinterpret_cast<const int4 *>(s_key + k);
+                    rank += (x.x > mine) + (x.y > mine) + (x.z > mine) + (x.w > mine);
+                }
                 st.order[rank] = b;
             }
             for (int b = me; b <= p.B; b += kInfoThreads) st.before[b] = before[b];
