@@ -29,6 +29,15 @@ namespace {
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+struct Range {
+    const void *at;
+    size_t bytes;
+};
+bool meet(const Range &a, const Range &b) {
+    const char *x = static_cast<const char *>(a.at), *y = static_cast<const char *>(b.at);
+    return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+
 struct SharedPlan {
     Plan own;
     bool split;            // the split kernels, in one launch
@@ -447,6 +456,14 @@ extern "C" atlas_status atlas_attn_shared(const void *q, const void *k_pages, co
     atlas_status st = shared_plan(Hq, Hkv, D, P, S, L, &plan);
     if (st != ATLAS_OK) return st;
     if (!L->workspace || L->workspace_bytes < plan.bytes) return ATLAS_ERR_WORKSPACE;
+    // What is written, and what else there is: tiles read their queries while others are done.
+    const size_t rows = (size_t)L->batch * Hq * L->q_len, size = L->kv_dtype == ATLAS_F32 ? 4 : 2;
+    const size_t pool = (size_t)L->num_pages * Hkv * P * D * size;
+    const Range all[] = {{L->out, rows * D * (L->out_dtype == ATLAS_F32 ? 4 : 2)}, {L->lse, rows * 4},
+                         {L->workspace, plan.bytes}, {q, rows * D * size}, {k_pages, pool}, {v_pages, pool}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 6; ++j)
+            if (meet(all[i], all[j])) return ATLAS_ERR_INVALID_ARG;
     cudaStream_t stream = static_cast<cudaStream_t>(L->stream);
     cudaEvent_t ev[3] = {nullptr, nullptr, nullptr};
     if (L->events)

@@ -60,7 +60,8 @@ typedef struct {
  * the bf16 tensor-core kernels, which cut a prefix where the SMs' shares end, it bounds the parts
  * of a prefix instead (max_prefix_pages * page_tokens / split_tokens + 2).  A window is
  * ATLAS_ERR_INVALID_ARG (it would cut the prefix off), a phase other than ATLAS_PHASE_ALL or a
- * chunk_range ATLAS_ERR_UNSUPPORTED.  `out` may not overlap what the call reads.
+ * chunk_range ATLAS_ERR_UNSUPPORTED.  out, lse and the workspace may not overlap one another, q
+ * or the pools (ATLAS_ERR_INVALID_ARG).
  * The same call on the same arrays gives the same bits.  On the split kernels a sequence's bits
  * depend on its own group alone (and on the sizes that the call is planned from); on the bf16
  * tensor-core kernels also on the other groups and lengths of the batch and on sm_count, which

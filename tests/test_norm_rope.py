@@ -144,6 +144,10 @@ CASES = [
     ("f32", 2, 8, 2, 128, 64, 33, [100, 4], 3, 128, True, False, None, dict(weights=False, eps=0.25)),
     ("bf16", 2, 8, 2, 128, 64, 70, [100, 4], 3, 96, True, True, None, dict(eps=1e-5)),
     ("bf16", 2, 4, 2, 128, 16, 3, [5, 16], 1, 64, False, False, None, dict(size=1e-4, eps=0.0)),
+    ("f32", 2, 4, 2, 128, 16, 5, [3, 30], 1, 10, False, True, None, dict(per_head=True, offset=1.0)),
+    ("f32", 1, 2, 1, 128, 16, 3, [3], 1, 70, True, False, None, dict(per_head=True)),
+    ("bf16", 1, 2, 2, 64, 16, 3, [3], 1, 36, False, False, None, {}),   # both halves have a rotated part
+    ("bf16", 1, 2, 2, 64, 16, 3, [3], 1, 34, True, False, None, dict(per_head=True, kind="f32")),
 ]
 
 
@@ -284,15 +288,15 @@ def test_pages_whose_offsets_pass_32_bits(rot):
 @gpu
 @pytest.mark.parametrize("per_head,rot", [(False, 128), (True, 128), (False, 62)])
 def test_many_tokens_are_as_one_by_one(per_head, rot):
-    """Two tokens a CTA, and the last CTA with one: the bits of calls of one token."""
-    B, n = 3, 901
+    """Two or four tokens a CTA, and the last CTA with fewer: the bits of calls of one token."""
+    B, n = 3, 1701
     q, k, v, kp, vp, table, lens, pos = step("bf16", B, 4, 2, 128, 16, n, [5, 16, 30], 1, 8)
     r = np.random.default_rng(4)
     wq, wk = (weights(r, H, 128, per_head, torch.float32) for H in (4, 2))
     kw = dict(q_weight=wq, k_weight=wk, rot_dim=rot)
     pools = kp.clone(), vp.clone()
     out = atlas.kv_append_norm_rope(q, k, v, kp, vp, table, lens, pos, **kw)
-    for i in (0, 1, 450, 899, 900):
+    for i in (0, 1, 450, n - 2, n - 1):
         one = atlas.kv_append_norm_rope(*(t[:, :, i:i + 1] for t in (q, k, v)), *pools, table, lens + i,
                                         pos[:, :, i:i + 1].contiguous(), **kw)
         assert torch.equal(one, out[:, :, i:i + 1])

@@ -452,3 +452,29 @@ def test_one_wrong_option(name, make):
         x(0.1, **{name: make()})
     with pytest.raises(atlas.AtlasError):
         x(0.1, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+
+
+@gpu
+@pytest.mark.parametrize("path", PATHS)
+def test_outputs_over_inputs(path):
+    x = Case("bf16", 8, 2, 64, 16, 2, [0, 2, 4], [100, 70], [50, 41, 60, 77], 8)
+    before = [t.clone() for t in x.args[:3]]
+    space = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    rows = x.q.shape[0] * 8 * 2
+    over = [dict(out=x.args[0]), dict(out=x.args[1].reshape(-1)[:rows * 64].reshape(x.q.shape)),
+            dict(out=x.args[2].reshape(-1)[-rows * 64:].reshape(x.q.shape)), dict(workspace=x.args[0]),
+            dict(workspace=space, out=space[1024:1024 + rows * 128].view(torch.bfloat16).reshape(x.q.shape)),
+            dict(workspace=space, lse=space[4096:4096 + rows * 4].view(torch.float32).reshape(x.q.shape[:3])),
+            dict(out=space[:rows * 128].view(torch.bfloat16).reshape(x.q.shape),
+                 lse=space[16:16 + rows * 4].view(torch.float32).reshape(x.q.shape[:3]))]
+    for kw in over:
+        with pytest.raises(atlas.AtlasError):
+            x(0.1, debug_flags=path, **kw)
+    torch.cuda.synchronize()
+    bits = [[y.view(torch.int16) for y in z] for z in (before, x.args[:3])]       # (they hold NaN)
+    assert all(torch.equal(a, b) for a, b in zip(*bits)) and (space == 0).all()
+    # side by side they are accepted
+    out = space[:rows * 128].view(torch.bfloat16).reshape(x.q.shape)
+    lse = space[rows * 128:rows * 132].view(torch.float32).reshape(x.q.shape[:3])
+    assert torch.equal(x(0.1, debug_flags=path, out=out, lse=lse, workspace=space[rows * 132:]),
+                       x(0.1, debug_flags=path))
