@@ -285,6 +285,23 @@ def test_bad_lengths_groups_and_pages_are_reported(dtype, q_len, path):
 
 
 @gpu
+@pytest.mark.parametrize("path", [0, 4, 8, 24])
+@pytest.mark.parametrize("dtype,q_len", [("bf16", 3), ("bf16", 40), ("f32", 3), ("f32", 24)])
+def test_bad_query_counts_are_reported(dtype, q_len, path):
+    x = Case(dtype, 8, 2, 64, 16, q_len, [0, 2, 4], [100, 70], [50, 41, 60, 77], 8, [q_len, 2, q_len, 1])
+    good = x(0.1, debug_flags=path, out=torch.zeros_like(x.args[0]))
+    for bad in (-1, q_len + 1, 2 ** 31 - 1, -(2 ** 31)):
+        x.q_lens = torch.tensor([q_len, bad, q_len, 1], dtype=torch.int32, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = x(0.1, status=status, debug_flags=path, out=torch.zeros_like(x.args[0]))
+        assert int(status.item()) == atlas.DEV_BAD_SEQLEN
+        assert torch.isnan(out[1]).all()
+        for b in (0, 2, 3):   # (twice the bound, as for bad lengths)
+            tol = 2 * (BF16_ABS + 2.0 ** -8 * 4) if dtype == "bf16" else 2 * F32_REL * 4
+            assert float((out[b].float() - good[b].float()).abs().max()) <= tol
+
+
+@gpu
 @pytest.mark.parametrize("dtype,q_len", [("bf16", 1), ("bf16", 24), ("f32", 1)])
 def test_captured_and_replayed_with_other_groups_and_lengths(dtype, q_len):
     x = Case(dtype, 8, 2, 128, 16, q_len, [0, 2, 4], [500, 100], [40, 41, 60, 77], 9)
