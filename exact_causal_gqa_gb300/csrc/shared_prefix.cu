@@ -29,6 +29,11 @@ namespace {
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// SMs to plan for (a number that no device has is cut to what the plan's sums have room for).
+int planned_sms(const atlas_launch *L) {
+    return std::min(L->sm_count > 0 ? L->sm_count : device_sm_count(), 1 << 14);
+}
+
 struct Range {
     const void *at;
     size_t bytes;
@@ -114,7 +119,7 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     const int64_t max_prefix = (int64_t)S->max_prefix_pages * P;
     if (max_prefix > INT32_MAX / 2) return ATLAS_ERR_INVALID_ARG;
 
-    const int64_t sms = L->sm_count > 0 ? L->sm_count : device_sm_count();
+    const int64_t sms = planned_sms(L);
     const int G = Hq / Hkv;
     const int64_t rows = (int64_t)L->batch * G * L->q_len;  // of one kv head, all groups
     const int64_t group_rows = (rows + S->n_groups - 1) / S->n_groups;
@@ -327,7 +332,7 @@ SharedStream stream_arrays(const SharedPlan &plan, int32_t G, const atlas_shared
     st.tile_rows = 128 * plan.tiles;
     st.max_items = shared_tc_items(plan.tiles);
     st.max_states = plan.n_pre;
-    st.sms = L->sm_count > 0 ? L->sm_count : device_sm_count();
+    st.sms = planned_sms(L);
     int32_t *at = reinterpret_cast<int32_t *>(static_cast<char *>(L->workspace) + plan.plan_at);
     auto take = [&](int64_t n) {
         int32_t *x = at;
@@ -509,7 +514,7 @@ extern "C" atlas_status atlas_attn_shared(const void *q, const void *k_pages, co
     mp.out = L->out;
     mp.out_bf16 = L->out_dtype == ATLAS_BF16;
     mp.lse = L->lse;
-    mp.sms = L->sm_count > 0 ? L->sm_count : device_sm_count();
+    mp.sms = planned_sms(L);
     mp.group_starts = S->group_starts;
     mp.prefix_lens = S->prefix_lens;
     mp.n_groups = S->n_groups;

@@ -79,6 +79,8 @@ def test_workspace_holds_the_states_of_both_parts(lib):
     assert atlas.shared_workspace_size((4, 8, 1, 128), 8, 2, 128, 16, 8, 2, 16, 64, split_tokens=64) == n
     with pytest.raises(atlas.AtlasError):
         atlas.shared_workspace_size((4, 8, 1, 128), 8, 2, 128, 16, 8, 5, 16, 64)
+    # more SMs than any device has change nothing more
+    assert ws(lib, sm_count=2 ** 31 - 1) == ws(lib, sm_count=1 << 20) != SIZE_MAX
 
 
 def test_arguments_are_checked_before_any_launch(lib):
