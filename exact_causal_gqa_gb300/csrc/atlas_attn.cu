@@ -418,6 +418,7 @@ atlas_status run_attention(atlas_kind kind, const void *q, const void *k_pages, 
         tp.out = L->out;
         tp.out_bf16 = L->out_dtype == ATLAS_BF16;
         tp.lse = L->lse;
+        tp.nearest = (L->debug_flags & kNearestProducts) != 0;
         tp.ws_acc = sp.ws_acc;
         tp.ws_ml = sp.ws_ml;
         tp.status = L->status_word;

@@ -70,13 +70,14 @@ constexpr int BN = 64;   // keys per block
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when the max grows 256x
 constexpr int kSegBlocks = 4;  // key blocks per O accumulation segment
-// SHARED: the prefixes' outputs are as exact as fp32 sums in some order (8e-7 root mean square behind
-// 4000 keys, where torch's are 8e-7 and the split kernels' 2e-7): segments of two blocks, and hi
-// parts to the nearest, so that lo parts have either sign and lo.lo, which is left out, no mean.
-// Four blocks and hi parts cut off 2.2e-6, two 1.4e-6; 64 x 8 heads of 64 on 8000 keys take 87 us
-// for 79.  (One block is not enough: the softmax could end two segments before the first is folded,
-// which a parity wait cannot tell apart; with two it is at most one ahead.)
-constexpr int kSegBlocksShared = 2;
+// NEAREST, for calls with shared prefixes (the prefixes and own splits of more than 16 rows): outputs
+// as exact as fp32 sums in some order, 8e-7 root mean square behind 4000 keys, where torch's are 8e-7
+// and the split kernels' 2e-7.  Segments of two blocks, and hi parts to the nearest, so that lo parts
+// have either sign and lo.lo, which is left out, no mean.  Four blocks and hi parts cut off 2.2e-6, two
+// 1.4e-6; 64 x 8 heads of 64 on 8000 keys take 87 us for 79.  (One block is not enough: the softmax
+// could end two segments before the first is folded, which a parity wait cannot tell apart; with two it
+// is at most one ahead.)
+constexpr int kSegBlocksNearest = 2;
 
 template <int D>
 struct Cfg {
@@ -195,13 +196,13 @@ __device__ void empty_row(const TcParams &p, int b, int hkv, int f) {
 }
 
 // SHARED: the splits of prefixes that groups of sequences share (shared_prefix.cuh).
-template <int D, bool SHARED = false>
+template <int D, bool SHARED = false, bool NEAREST = SHARED>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     fmha_tf32x3_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const TcParams p) {
     allow_dependent_launch();  // the merge may start its CTAs (it waits for this grid)
     using C = Cfg<D>;
-    constexpr int kSeg = SHARED ? kSegBlocksShared : kSegBlocks;
+    constexpr int kSeg = NEAREST ? kSegBlocksNearest : kSegBlocks;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -543,8 +544,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             float4 *dst = reinterpret_cast<float4 *>(smem + C::OFF_KLO);
             for (int k = ct; k < C::kBlkBytes / 16; k += 128) {
                 const float4 x = src[k];
-                dst[k] = make_float4(tf32_lo<SHARED>(x.x), tf32_lo<SHARED>(x.y), tf32_lo<SHARED>(x.z), tf32_lo<SHARED>(x.w));
-                src[k] = make_float4(tf32_hi<SHARED>(x.x), tf32_hi<SHARED>(x.y), tf32_hi<SHARED>(x.z), tf32_hi<SHARED>(x.w));
+                dst[k] = make_float4(tf32_lo<NEAREST>(x.x), tf32_lo<NEAREST>(x.y), tf32_lo<NEAREST>(x.z), tf32_lo<NEAREST>(x.w));
+                src[k] = make_float4(tf32_hi<NEAREST>(x.x), tf32_hi<NEAREST>(x.y), tf32_hi<NEAREST>(x.z), tf32_hi<NEAREST>(x.w));
             }
             fence_proxy_async_smem();
             mbar_arrive(BAR(C::B_KLO_READY));
@@ -587,11 +588,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     // V^T: slab k0/32, row dim, 16-byte chunk (k0 % 32) / 4
                     const uint32_t off = (k0 / 32) * C::kVtSlab + sw128(dim, (k0 % 32) / 4);
                     *reinterpret_cast<float4 *>(smem + C::OFF_VTH + off) =
-                        make_float4(tf32_hi<SHARED>(v[0][e]), tf32_hi<SHARED>(v[1][e]), tf32_hi<SHARED>(v[2][e]),
-                                    tf32_hi<SHARED>(v[3][e]));
+                        make_float4(tf32_hi<NEAREST>(v[0][e]), tf32_hi<NEAREST>(v[1][e]), tf32_hi<NEAREST>(v[2][e]),
+                                    tf32_hi<NEAREST>(v[3][e]));
                     *reinterpret_cast<float4 *>(smem + C::OFF_VTL + off) =
-                        make_float4(tf32_lo<SHARED>(v[0][e]), tf32_lo<SHARED>(v[1][e]), tf32_lo<SHARED>(v[2][e]),
-                                    tf32_lo<SHARED>(v[3][e]));
+                        make_float4(tf32_lo<NEAREST>(v[0][e]), tf32_lo<NEAREST>(v[1][e]), tf32_lo<NEAREST>(v[2][e]),
+                                    tf32_lo<NEAREST>(v[3][e]));
                 }
             }
             fence_proxy_async_smem();
@@ -707,8 +708,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     const float xs[4] = {x.x * sgn, x.y * sgn, x.z * sgn, x.w * sgn};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        hv[4 * ch + e] = __float_as_uint(tf32_hi<SHARED>(xs[e]));
-                        lv[4 * ch + e] = __float_as_uint(tf32_lo<SHARED>(xs[e]));
+                        hv[4 * ch + e] = __float_as_uint(tf32_hi<NEAREST>(xs[e]));
+                        lv[4 * ch + e] = __float_as_uint(tf32_lo<NEAREST>(xs[e]));
                     }
                 }
                 tmem_st32(tl + C::QH + 32 * sl, hv);
@@ -798,7 +799,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                         }
                         const float2 e2 = make_float2(ex2(t.x), ex2(t.y));
                         rs2[k & 3] = fadd2(rs2[k & 3], e2);
-                        const float2 hi = make_float2(tf32_hi<SHARED>(e2.x), tf32_hi<SHARED>(e2.y));
+                        const float2 hi = make_float2(tf32_hi<NEAREST>(e2.x), tf32_hi<NEAREST>(e2.y));
                         const float2 lo = fadd2(e2, make_float2(-hi.x, -hi.y));
                         ph[2 * k] = __float_as_uint(hi.x);
                         ph[2 * k + 1] = __float_as_uint(hi.y);
@@ -919,7 +920,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #undef BAR
 }
 
-template <int D>
+template <int D, bool NEAREST>
 cudaError_t launch_instance(const TcParams &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,
                             const CUtensorMap &tmV, cudaStream_t stream) {
     using C = Cfg<D>;
@@ -928,14 +929,14 @@ cudaError_t launch_instance(const TcParams &p, const CUtensorMap &tmQ, const CUt
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < 64 && !configured[dev]) {
-        err = cudaFuncSetAttribute(fmha_tf32x3_kernel<D>,
+        err = cudaFuncSetAttribute(fmha_tf32x3_kernel<D, false, NEAREST>,
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (err != cudaSuccess) return err;
         configured[dev] = 1;
     }
     const int tiles = p.B * p.Hkv * p.tiles_per_unit;
     dim3 grid = p.split ? dim3(p.n_chunks, tiles, 1) : dim3(tiles, 1, 1);
-    fmha_tf32x3_kernel<D><<<grid, C::kThreads, C::kSmem, stream>>>(tmQ, tmK, tmV, p);
+    fmha_tf32x3_kernel<D, false, NEAREST><<<grid, C::kThreads, C::kSmem, stream>>>(tmQ, tmK, tmV, p);
     return cudaGetLastError();
 }
 
@@ -967,8 +968,11 @@ cudaError_t launch_shared_tc_f32(const TcParams &p, int64_t ctas, const CUtensor
 
 cudaError_t launch_fmha_tc_f32(const TcParams &p, const CUtensorMap &tmQ, const CUtensorMap &tmK,
                                const CUtensorMap &tmV, cudaStream_t stream) {
-    return p.D == 64 ? launch_instance<64>(p, tmQ, tmK, tmV, stream)
-                     : launch_instance<128>(p, tmQ, tmK, tmV, stream);
+    if (p.nearest)
+        return p.D == 64 ? launch_instance<64, true>(p, tmQ, tmK, tmV, stream)
+                         : launch_instance<128, true>(p, tmQ, tmK, tmV, stream);
+    return p.D == 64 ? launch_instance<64, false>(p, tmQ, tmK, tmV, stream)
+                     : launch_instance<128, false>(p, tmQ, tmK, tmV, stream);
 }
 
 }  // namespace atlas

@@ -201,6 +201,9 @@ struct SharedMergeParams : MergeParams {
     SharedStream st;
 };
 
+// A bit of atlas_launch.debug_flags for the library's own calls: TcParams::nearest.
+constexpr uint32_t kNearestProducts = 1u << 31;
+
 // Tensor-core (tcgen05 / TMEM) path for many query rows per (sequence, kv head):
 // 128-row query tiles x 128-key blocks (bf16) or 64-key blocks (fp32 as 3 x tf32),
 // head_dim 64 or 128.  Either writes the
@@ -240,6 +243,7 @@ struct TcParams {
     int32_t n_groups;
     const void *q;                // read row by row there (no tensor map)
     SharedStream st;
+    int32_t nearest;              // fp32: the more exact form of the products
 };
 
 // Paged KV append (kv_append.cu).

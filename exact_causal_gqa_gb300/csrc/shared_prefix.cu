@@ -387,7 +387,7 @@ atlas_status launch_tc(const SharedPlan &plan, const void *q, const void *k_page
     }
     atlas_launch own = *L;
     own.phase = ATLAS_PHASE_CHUNKS;
-    own.debug_flags &= ~ATLAS_DEBUG_TC_DIRECT;
+    own.debug_flags = (own.debug_flags & ~ATLAS_DEBUG_TC_DIRECT) | kNearestProducts;
     own.events = nullptr;
     own.workspace_bytes = plan.own.ws_bytes;
     st = run_attention(ATLAS_KIND_SUFFIX, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P,

@@ -76,8 +76,8 @@ typedef struct {
  * rows have tiles of their own), where the second costs nothing, or where few keys carry a row, and
  * as one elsewhere, as atlas_attn_prefill does.  The
  * fp32 one takes three tf32 products for each, within the 1e-5 of the largest value that holds for
- * all fp32 calls: 7e-7 to 1e-6 off in the root mean square, where the split kernels are 2e-7 to 3e-7
- * (own keys of more than 16 rows go as in atlas_attn_suffix, 2e-6).
+ * all fp32 calls: 7e-7 to 1e-6 off in the root mean square (atlas_attn_suffix 2e-6), where the split
+ * kernels are 2e-7 to 3e-7.
  */
 atlas_status atlas_attn_shared(const void *q, const void *k_pages, const void *v_pages,
                                const int32_t *page_table, const int32_t *seq_lens,

@@ -228,12 +228,18 @@ def test_matches_the_plain_form(dtype, Hq, Hkv, D, P, q_len, starts, pre, lens, 
 @pytest.mark.parametrize("B,q_len", [(5, 1), (3, 24)])
 def test_no_prefix_is_a_suffix(dtype, B, q_len):
     """Prefixes of no keys leave the states of the sequences' own splits: with the same split
-    size the merge gives the suffix call's bits."""
+    size the merge gives the suffix call's bits.  fp32 rows of more than 16 take products of the
+    more exact form: both calls are within F32_REL of the largest of the same exact rows, so within
+    twice that of one another."""
     lens = [q_len + 31 * b for b in range(B)]
     x = Case(dtype, 8, 2, 128, 16, q_len, [0, 2, B], [0, 0], lens, 3)
     a = x(0.09, split_tokens=64)
     q, kp, vp, _, _, _, table, own = x.args
-    assert torch.equal(a, atlas.suffix(q, kp, vp, table, own, *x.sizes, 0.09, split_tokens=64))
+    b = atlas.suffix(q, kp, vp, table, own, *x.sizes, 0.09, split_tokens=64)
+    if dtype == "f32" and q_len > 4:
+        assert float((a - b).abs().max()) <= 2 * F32_REL * float(b.abs().max()) * (1 + F32_REL)
+    else:
+        assert torch.equal(a, b)
 
 
 @gpu
