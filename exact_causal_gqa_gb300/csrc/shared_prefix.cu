@@ -95,7 +95,7 @@ constexpr int64_t kOwnSplitRows = 32, kOwnSplitKeys = 1024;
 // end in the first half, against 9.5 for each own tile of 128 rows on the tensor cores, which has a
 // launch, a start and states to itself there, or 2.6 where the own keys are splits.  Fitted to 98
 // sizes of 20 to 264 rows, prefixes of 300 to 16000 keys and 100 or 800 own ones (32 / 8 heads of
-// 128), of which three lose more than 6 %; whole tiles and others: 128 sequences, 1500 keys, 264
+// 128), of which few lose more than 6 %; whole tiles and others: 128 sequences, 1500 keys, 264
 // rows 403 and 510 us, 64 rows 164 and 176, 20 rows 146 and 102; 16, 16000 keys, 264 rows 367 and 291.
 bool whole_pays(int64_t rows, int64_t max_prefix, bool own_splits) {
     const int64_t pairs = rows / 256 + (rows % 256 > 128), single = rows % 256 > 0 && rows % 256 <= 128;
