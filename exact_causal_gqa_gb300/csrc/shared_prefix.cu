@@ -45,6 +45,7 @@ bool meet(const Range &a, const Range &b) {
 
 struct SharedPlan {
     Plan own;
+    bool few;              // at most 16 rows to a sequence and kv head: the decode kernels' calls
     bool split;            // the split kernels, in one launch
     bool whole, stream;    // bf16 on the tensor cores: whole tiles, or the prefixes' (both: stream)
     int tiles;             // tensor cores: query tiles to a CTA; split kernels: columns
@@ -124,7 +125,7 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     const int64_t rows = (int64_t)L->batch * G * L->q_len;  // of one kv head, all groups
     const int64_t group_rows = (rows + S->n_groups - 1) / S->n_groups;
     const bool f32 = L->kv_dtype == ATLAS_F32;
-    const bool few = plan->own.path == Path::SplitBF16 || plan->own.path == Path::SplitF32;
+    const bool few = plan->few = plan->own.path == Path::SplitBF16 || plan->own.path == Path::SplitF32;
     const int cols = f32 ? (group_rows <= 4 ? 4 : 8) : group_rows <= 8 ? 8 : 16;
     const double bytes = 2.0 * S->n_groups * max_prefix * Hkv * D * (f32 ? 4 : 2);
     const int64_t seq_rows = (int64_t)G * L->q_len, max_ctx = (int64_t)L->max_pages_per_seq * P;
@@ -302,7 +303,11 @@ atlas_status tc_params(const SharedPlan &plan, const void *q, const void *k_page
     tp->row_step = 1;
     tp->chunk = plan.chunk;
     tp->n_chunks = plan.n_pre;
-    tp->hilo_below = plan.tiles == 1 ? INT32_MAX : hilo_below(scale, D);
+    // bf16 weights in two parts wherever the call without prefixes, on the split kernels, takes them
+    // so (64 sequences behind 32768 keys 107 -> 110 us, 192 of 4 rows in 7 groups 227 -> 243), and
+    // where the second part costs nothing.  The tiles of more rows are those of atlas_attn_suffix
+    // (16 prompts of 256 rows behind 8192 keys take 357 us, with two parts throughout 424).
+    tp->hilo_below = plan.few || plan.tiles == 1 ? INT32_MAX : hilo_below(scale, D);
     tp->negate_scores = scale < 0.f;
     tp->scale_log2 = fabsf(scale) * kLog2e;
     tp->softcap_log2 = L->softcap > 0.f ? L->softcap * kLog2e : 0.f;
