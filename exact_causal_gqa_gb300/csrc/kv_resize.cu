@@ -201,15 +201,16 @@ __global__ void __launch_bounds__(kThreads) kv_resize_kernel(const ResizeParams 
         s_len[tid] = r.m.len;
         s_fresh[tid] = moves && !r.m.bad ? r.m.fresh : 0;
         __syncthreads();
+        // (places in the lists in 64 bits: a list may have 2^31 - 1, and a step goes past its end)
         const int total = fits ? r.all : 0;
-        for (int e0 = me; e0 < total; e0 += threads * kAtOnce) {
+        for (int64_t e0 = me; e0 < total; e0 += threads * kAtOnce) {
             int32_t *from[kAtOnce], *to[kAtOnce];
             int id[kAtOnce];
             bool back[kAtOnce];
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
-                const int e = e0 + u * threads;
-                if (e >= total) continue;
+                if (e0 + u * threads >= total) continue;
+                const int e = (int)e0 + u * threads;
                 int lo = 0, hi = kThreads - 1;  // the first sequence whose sum is above e
                 while (lo < hi) {
                     const int mid = (lo + hi) / 2;
@@ -239,13 +240,13 @@ __global__ void __launch_bounds__(kThreads) kv_resize_kernel(const ResizeParams 
         // The slots of new tokens: pages that were there from the table, those that are taken
         // now from the ring, so that nothing written in this call is read in it.
         const int slots = p.slots ? min(kThreads, p.B - b0) * p.max_new : 0;
-        for (int e0 = me; e0 < slots; e0 += threads * kAtOnce) {
+        for (int64_t e0 = me; e0 < slots; e0 += threads * kAtOnce) {
             int id[kAtOnce], at[kAtOnce];
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
-                const int e = e0 + u * threads;
                 at[u] = -1;
-                if (e >= slots) continue;
+                if (e0 + u * threads >= slots) continue;
+                const int e = (int)e0 + u * threads;
                 const int s = e / p.max_new, i = e - s * p.max_new;
                 if (i >= s_fresh[s]) continue;
                 at[u] = s_len[s] - s_fresh[s] + i;
@@ -255,14 +256,13 @@ __global__ void __launch_bounds__(kThreads) kv_resize_kernel(const ResizeParams 
             }
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
-                const int e = e0 + u * threads;
-                if (e >= slots) continue;
+                if (e0 + u * threads >= slots) continue;
                 int slot = -1;
                 if (at[u] >= 0) {
                     if (id[u] < 0 || id[u] >= p.num_pages) flags |= ATLAS_DEV_BAD_PAGE;
                     else slot = id[u] * p.P + (at[u] & (p.P - 1));
                 }
-                p.slots[(int64_t)b0 * p.max_new + e] = slot;
+                p.slots[(int64_t)b0 * p.max_new + e0 + u * threads] = slot;
             }
         }
         if (b0 + kThreads < p.B) __syncthreads();  // the round's arrays are rewritten

@@ -237,3 +237,41 @@ def test_tensors_on_the_host():
     with pytest.raises(ValueError, match="page_table must be a CUDA tensor"):
         atlas.kv_resize(torch.zeros((3, 4), **i32), torch.zeros(3, **i32), torch.ones(3, **i32),
                         torch.arange(9, **i32), torch.tensor([0, 9], **i32), 16)
+
+
+@gpu
+def test_the_most_slots_there_may_be():
+    """2^31 - 1 of them: places in the list, a step past its last among them, need more than 31 bits."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    n = 2 ** 31 - 1
+    table, held = torch.full((1, 4), -1, **i32), torch.zeros(1, **i32)
+    ring, state = torch.arange(5, 14, **i32).flip(0).contiguous() - 5, torch.tensor([7, 9], **i32)
+    slots, status = torch.full((1, n), 7, **i32), torch.zeros(1, **i32)
+    for new, first in (([3], 47), (None, 0)):
+        new = None if new is None else torch.tensor(new, **i32)
+        atlas.kv_resize(table, held, torch.tensor([50], **i32), ring, state, 16, n_new=new, slots=slots, status=status)
+        torch.cuda.synchronize()
+        assert table.tolist() == [[1, 0, 8, 7]] and held.tolist() == [4] and state.tolist() == [2, 5]
+        pages = torch.tensor([1, 0, 8, 7], **i32)
+        t = torch.arange(first, 50, **i32)
+        assert torch.equal(slots[0, : 50 - first], pages[(t // 16).long()] * 16 + t % 16)
+        assert bool((slots[0, 50 - first:] == -1).all()) and int(status.item()) == 0
+
+
+@gpu
+def test_the_most_moves_there_may_be():
+    """Two sequences that take 2^31 - 2 pages of one token between them, and give them back."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    width = 2 ** 30 - 1
+    table, held = torch.full((2, width), -1, **i32), torch.zeros(2, **i32)
+    ring, state = torch.arange(2 * width, **i32), torch.tensor([0, 2 * width], **i32)
+    status = torch.zeros(1, **i32)
+    atlas.kv_resize(table, held, torch.tensor([width, width], **i32), ring, state, 1, status=status)
+    torch.cuda.synchronize()
+    assert held.tolist() == [width, width] and state.tolist() == [0, 0] and int(status.item()) == 0
+    assert torch.equal(table.reshape(-1), ring)
+    ring.fill_(-1)
+    atlas.kv_resize(table, held, torch.tensor([0, 0], **i32), ring, state, 1, status=status)
+    torch.cuda.synchronize()
+    assert held.tolist() == [0, 0] and state.tolist() == [0, 2 * width] and int(status.item()) == 0
+    assert bool((table == -1).all()) and torch.equal(ring, torch.arange(2 * width, **i32))
