@@ -551,14 +551,15 @@ def shared(q, k_pages, v_pages, prefix_table, prefix_lens, group_starts, page_ta
 
 def shared_workspace_size(q_shape, n_q_heads, n_kv_heads, head_dim, page_tokens, max_pages_per_seq,
                           n_groups, max_prefix_pages, num_pages, dtype=torch.bfloat16,
-                          out_dtype=None, split_tokens=0, debug_flags=0) -> int:
-    """Workspace bytes a shared() call needs (from shapes and the split size only)."""
+                          out_dtype=None, split_tokens=0, debug_flags=0, sm_count=0) -> int:
+    """Workspace bytes a shared() call needs: from shapes, the split size and the number of SMs that
+    it is planned for (sm_count, as given to the call; 0: those of the current device)."""
     L = _Launch()
     L.batch, L.q_len = q_shape[0], q_shape[2]
     L.max_pages_per_seq, L.num_pages = max_pages_per_seq, num_pages
     L.q_dtype = L.kv_dtype = _DTYPES.get(dtype, -1)
     L.out_dtype = _DTYPES.get(out_dtype or dtype, -1)
-    L.split_tokens, L.debug_flags = split_tokens, debug_flags
+    L.split_tokens, L.debug_flags, L.sm_count = split_tokens, debug_flags, sm_count
     S = _Shared(n_groups=n_groups, max_prefix_pages=max_prefix_pages)
     n = load_library().atlas_attn_shared_workspace_size(n_q_heads, n_kv_heads, head_dim, page_tokens,
                                                         ctypes.byref(S), ctypes.byref(L))

@@ -87,8 +87,8 @@ atlas_status atlas_attn_shared(const void *q, const void *k_pages, const void *v
                                int32_t page_tokens, float scale, const atlas_shared *S,
                                const atlas_launch *L);
 
-/* Bytes of device workspace the call needs; reads the sizes of *S and *L, ignores their
- * pointers.  SIZE_MAX if the arguments are invalid. */
+/* Bytes of device workspace the call needs; reads the sizes of *S and *L (split_tokens, sm_count and
+ * debug_flags among them), ignores their pointers.  SIZE_MAX if the call would be refused. */
 size_t atlas_attn_shared_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                                         int32_t page_tokens, const atlas_shared *S,
                                         const atlas_launch *L);

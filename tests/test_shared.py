@@ -83,6 +83,15 @@ def test_workspace_holds_the_states_of_both_parts(lib):
     assert ws(lib, sm_count=2 ** 31 - 1) == ws(lib, sm_count=1 << 20) != SIZE_MAX
 
 
+@pytest.mark.parametrize("sms", [0, 1, 8, 152, 300])
+def test_the_workspace_is_that_of_the_sms_planned_for(lib, sms):
+    """64 steps behind 32768 keys: more SMs, more states."""
+    S = prefixes(n_groups=1, max_prefix_pages=2048)
+    n = ws(lib, S, Hq=32, Hkv=8, batch=64, max_pages_per_seq=128, sm_count=sms)
+    assert atlas.shared_workspace_size((64, 32, 1, 128), 32, 8, 128, 16, 128, 1, 2048, 64, sm_count=sms) == n
+    assert sms in (0, 152) or n != ws(lib, S, Hq=32, Hkv=8, batch=64, max_pages_per_seq=128, sm_count=152)
+
+
 def test_arguments_are_checked_before_any_launch(lib):
     need = ws(lib)
     good = dict(workspace=0x1000, workspace_bytes=need)
@@ -428,6 +437,23 @@ def test_fewer_sms_and_events(dtype, path):
         torch.cuda.synchronize()
         assert np.abs(widen(out) - ref).max() <= tol
         assert timer.main_ms() > 0 and timer.merge_ms() > 0
+
+
+@gpu
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype,q_len", [("bf16", 1), ("bf16", 40), ("f32", 1), ("f32", 24)])
+def test_a_workspace_of_the_size_given_for_that_many_sms(dtype, q_len, path):
+    x = Case(dtype, 8, 2, 128, 16, q_len, [0, 30, 40], [2000, 300], [q_len + b for b in range(40)], 5)
+    q, kp, _, ptab, _, starts, table, _ = x.args
+    for sms in (1, 7, 152, 300):
+        n = atlas.shared_workspace_size(q.shape, *x.sizes, table.shape[1], len(starts) - 1, ptab.shape[1],
+                                        kp.shape[0], dtype=DT[dtype], debug_flags=path, sm_count=sms)
+        space = torch.full((n + 4096,), 77, dtype=torch.uint8, device="cuda")
+        want = x(0.09, debug_flags=path, sm_count=sms)
+        assert torch.equal(x(0.09, debug_flags=path, sm_count=sms, workspace=space[:n]), want)
+        assert (space[n:] == 77).all()
+        with pytest.raises(atlas.AtlasError):
+            x(0.09, debug_flags=path, sm_count=sms, workspace=space[:n - 1])
 
 
 def test_tensors_on_the_host():
