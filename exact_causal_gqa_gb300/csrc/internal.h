@@ -158,7 +158,7 @@ struct SharedStream {
     int32_t units;       // n_groups or batch
     int32_t tile_rows;   // rows of a CTA's tiles: 128 or 256
     int32_t max_items;   // (tile, key range) pieces of one CTA at most
-    int32_t max_states;  // CTAs that a tile may be cut among at most
+    int32_t max_states;  // CTAs that a tile may be cut among at most (whole 0)
     int32_t sms;
     // by the plan kernel
     int32_t *head;       // [2]: a CTA's length of the line, and all of it

@@ -73,14 +73,15 @@ constexpr float kOwnRate = 70e3f, kOwnRateWide = 50e3f;
 // Whether the split kernels take less time: the prefixes once for each CTA's rows, against the
 // plan's launch, a longer start, and the prefixes once.  In fp32 the own keys count too: beside
 // prefixes of more than 4 rows they are taken 8 columns wide, where 4 would do.
-// Fitted to 52 measured sizes: bf16, 32 / 8 heads of 128, one prefix, split kernels and tensor cores:
-// 8 sequences behind 1024 keys 22 and 42 us, behind 32768 59 and 73; 16 behind 8192 46 and 48; 32
-// behind 8192 72 and 48; 64 behind 1024 44 and 44, behind 32768 315 and 83.  fp32: 8 behind 1024 23
-// and 42, behind 8192 73 and 50; heads of 64, 32 in 4 groups behind 2000 61 and 43.
+// Fitted to 56 measured sizes in bf16 and 20 in fp32: bf16, 32 / 8 heads of 128, one prefix, split
+// kernels and tensor cores: 8 sequences behind 1024 keys 17 and 27 us, behind 32768 53 and 54; 16
+// behind 8192 42 and 33; 32 behind 8192 67 and 35; 64 behind 1024 39 and 33, behind 32768 309 and 82;
+// heads of 64, 64 in 4 groups behind 4096 43 and 33.  fp32: 8 behind 1024 23 and 42, behind 8192 73
+// and 50; heads of 64, 32 in 4 groups behind 2000 61 and 43.
 bool split_pays(double prefix_bytes, int64_t tiles, double flops, double own_bytes, bool own_twice, bool f32) {
     // bytes and floating point operations a microsecond
     if (!f32)
-        return (double)tiles * prefix_bytes / 6e6 <= 18.0 + std::max(prefix_bytes / 5e6, flops / 9e8);
+        return (double)tiles * prefix_bytes / 6e6 <= 13.0 + std::max(prefix_bytes / 5e6, flops / 9e8);
     const double tc = 28.0 + std::max(prefix_bytes / 2.7e6, flops / 1.2e8) + own_bytes / 6e6;
     return 10.0 + ((double)tiles * prefix_bytes + own_bytes * (own_twice ? 1.3 : 1.0)) / 3.6e6 <= tc;
 }

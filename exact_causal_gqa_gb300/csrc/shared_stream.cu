@@ -195,8 +195,11 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
     const int pieces = st.max_items - 2;
     ctas *= 1 + n_tiles / (ctas * (pieces * 3 / 4));
     int64_t per64 = (all + ctas - 1) / ctas;
-    per64 = max(per64, (int64_t)kMinBlocks * kPairCost);
-    per64 = max(per64, (int64_t)((most + st.max_states - 3) / (st.max_states - 2)) * kPairCost);
+    // (A share of n blocks' length, of a tile's longest kind; with st.whole a tile may have any
+    // number of states, two places to a CTA.)
+    const int longest = st.tile_rows == 256 ? kPairCost : kSingleCost;
+    per64 = max(per64, (int64_t)kMinBlocks * longest);
+    if (!st.whole) per64 = max(per64, (int64_t)((most + st.max_states - 3) / (st.max_states - 2)) * longest);
     int per = (int)per64;
     const int most_per = per + per / 8;
     const int least = (most_per + kSingleCost * pieces - 1) / (kSingleCost * pieces);

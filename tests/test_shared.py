@@ -425,6 +425,37 @@ def test_calls_on_two_streams_at_once(dtype, q_len, path):
 
 
 @gpu
+@pytest.mark.parametrize("prefix,B,path,least", [(32768, 32, 8, 137), (8192, 32, 8, 132), (8192, 64, 8, 132),
+                                                 (8192, 1, 24, 137)])
+def test_the_line_is_cut_among_all_sms(prefix, B, path, least):
+    """8 kv heads behind long prefixes with next to no own keys: the shares (in the plan's record of
+    a sequence, or of whole tiles the numbers of pieces) leave a tenth of the SMs without work at most.
+    (Where a tile's 64 blocks have room for 64 / 4 + 3 states, and are cut in 17 at most, a share has 4
+    of the 66 that each of 8 tiles counts for: 132.)"""
+    n, G, Hkv, P, D = (1, 4, 8, 64, 64) if path == 8 else (30, 4, 8, 64, 64)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pages = prefix // P
+    q = torch.randn(B, G * Hkv, n, D, device="cuda").to(torch.bfloat16)
+    kp, vp = (torch.randn(pages + B, Hkv, P, D, device="cuda").to(torch.bfloat16) for _ in range(2))
+    space = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    atlas.shared(q, kp, vp, torch.arange(pages, **i32)[None], torch.tensor([prefix], **i32),
+                 torch.tensor([0, B], **i32), torch.arange(pages, pages + B, **i32)[:, None],
+                 torch.full((B,), n, **i32), G * Hkv, Hkv, D, P, 0.1, workspace=space, debug_flags=path, sm_count=152)
+    words = space.view(torch.int32)
+    if path == 8:
+        # a sequence's record: blocks, rows before it, rows, first place, length of a head, weight, share
+        at = ((words[:-8] == prefix // 128) & (words[1:-7] == 0) & (words[2:-6] == B * G * n) &
+              (words[3:-5] == 0)).nonzero().flatten().tolist()
+        assert len(at) == 1
+        line, share = int(words[at[0] + 4]) * Hkv, int(words[at[0] + 6])
+        ctas = -(-line // share)
+    else:
+        # a CTA's piece of whole tiles: unit, kv head, first row, rows, first block, blocks, state, keys, own keys
+        ctas = int(((words[3:-6] == G * n) & (words[7:-2] == prefix) & (words[8:-1] == n)).sum()) - (Hkv - 1)
+    assert least <= ctas <= 153
+
+
+@gpu
 @pytest.mark.parametrize("path", PATHS)
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_fewer_sms_and_events(dtype, path):
