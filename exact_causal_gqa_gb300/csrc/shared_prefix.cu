@@ -92,16 +92,21 @@ bool split_pays(double prefix_bytes, int64_t tiles, double flops, double own_byt
 // 97 with 120.
 constexpr int64_t kOwnSplitRows = 32, kOwnSplitKeys = 1024;
 
-// Whether tiles over whole keys take less time than the prefixes' tiles, which many sequences'
-// rows fill, beside the own ones: a block of a prefix 2.0 us for 256 rows, and 1.1 where a sequence's
-// end in the first half, against 9.5 for each own tile of 128 rows on the tensor cores, which has a
+// Whether tiles over whole keys take less time than the prefixes' tiles, which the rows of a group's
+// sequences fill, beside the own ones: a block of a prefix 2.0 us for 256 rows, and 1.1 where a
+// sequence's (or a group's) end in the first half, against 9.5 for each own tile of 128 rows on the tensor cores, which has a
 // launch, a start and states to itself there, or 2.6 where the own keys are splits.  Fitted to 98
 // sizes of 20 to 264 rows, prefixes of 300 to 16000 keys and 100 or 800 own ones (32 / 8 heads of
 // 128), of which few lose more than 6 %; whole tiles and others: 128 sequences, 1500 keys, 264
-// rows 403 and 510 us, 64 rows 164 and 176, 20 rows 146 and 102; 16, 16000 keys, 264 rows 367 and 291.
-bool whole_pays(int64_t rows, int64_t max_prefix, bool own_splits) {
-    const int64_t pairs = rows / 256 + (rows % 256 > 128), single = rows % 256 > 0 && rows % 256 <= 128;
-    const double more = 2.0 * (double)pairs + 1.1 * (double)single - (double)rows / 128.0;
+// rows 403 and 510 us, 64 rows 164 and 176, 20 rows 146 and 102; 16, 16000 keys, 264 rows 367 and
+// 291.  Behind 16000 keys with 800 own ones, 80 rows: 2 sequences with a group each 53 and 65 us, 16
+// with a group each 179 and 187, 32 in 4 groups 318 and 207.
+bool whole_pays(int64_t rows, int64_t group_rows, int64_t max_prefix, bool own_splits) {
+    auto block = [](int64_t n) {  // of the tiles of n rows
+        const int64_t pairs = n / 256 + (n % 256 > 128), single = n % 256 > 0 && n % 256 <= 128;
+        return 2.0 * (double)pairs + 1.1 * (double)single;
+    };
+    const double more = block(rows) - block(group_rows) * (double)rows / (double)group_rows;
     return (double)((max_prefix + 127) / 128) * more <=
            (own_splits ? 2.6 : 9.5) * (double)((rows + 127) / 128);
 }
@@ -138,7 +143,7 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->split = false;
     plan->stream = !f32 && !plan->split;
     const bool own_splits = seq_rows <= kOwnSplitRows && max_ctx <= kOwnSplitKeys;
-    plan->whole = plan->stream && !few && L->split_tokens == 0 && whole_pays(seq_rows, max_prefix, own_splits);
+    plan->whole = plan->stream && !few && L->split_tokens == 0 && whole_pays(seq_rows, group_rows, max_prefix, own_splits);
     if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->whole = false;
     if (L->debug_flags & ATLAS_DEBUG_SHARED_WHOLE) plan->whole = plan->stream;
     if (plan->stream && !plan->whole && few && L->split_tokens == 0 &&

@@ -83,6 +83,18 @@ def test_workspace_holds_the_states_of_both_parts(lib):
     assert ws(lib, sm_count=2 ** 31 - 1) == ws(lib, sm_count=1 << 20) != SIZE_MAX
 
 
+@pytest.mark.parametrize("B,groups,q_len,prefix_pages,whole", [
+    (1, 1, 20, 1000, True), (8, 8, 20, 1000, True), (8, 8, 5, 1000, True), (64, 64, 75, 125, True),
+    (32, 4, 20, 1000, False), (64, 1, 5, 1000, False), (64, 1, 64, 1000, True)])
+def test_tiles_of_their_own_where_a_gather_fills_no_more(lib, B, groups, q_len, prefix_pages, whole):
+    """Rows of a sequence alone in its group, or that fill tiles, are not gathered (as the sizes tell)."""
+    def size(flags):
+        return ws(lib, prefixes(n_groups=groups, max_prefix_pages=prefix_pages), Hq=32, Hkv=8, batch=B, q_len=q_len,
+                  max_pages_per_seq=100, debug_flags=flags)
+    own, gathered = size(atlas.DEBUG_SHARED_WHOLE), size(atlas.DEBUG_SHARED_TC)
+    assert own != gathered and size(0) == (own if whole else gathered)
+
+
 @pytest.mark.parametrize("sms", [0, 1, 8, 152, 300])
 def test_the_workspace_is_that_of_the_sms_planned_for(lib, sms):
     """64 steps behind 32768 keys: more SMs, more states."""
