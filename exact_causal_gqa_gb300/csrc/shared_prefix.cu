@@ -116,11 +116,17 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     if (!S || !L) return ATLAS_ERR_INVALID_ARG;
     if (L->window != 0) return ATLAS_ERR_INVALID_ARG;
     if (L->phase != ATLAS_PHASE_ALL || L->chunk_range) return ATLAS_ERR_UNSUPPORTED;
+    if (L->split_tokens < 0 || L->split_tokens % kSplitBlockTokens != 0) return ATLAS_ERR_INVALID_ARG;
+    // The call's checks, and its kernels without prefixes.  (No splits: what those may be too many
+    // for counts only where they are launched.)
     atlas_launch own = *L;
-    own.phase = ATLAS_PHASE_CHUNKS;  // partial states only, whatever the sizes
-    own.debug_flags &= ~ATLAS_DEBUG_TC_DIRECT;
-    const atlas_status st = make_plan(ATLAS_KIND_SUFFIX, Hq, Hkv, D, P, &own, &plan->own);
+    own.split_tokens = 0;
+    own.debug_flags |= ATLAS_DEBUG_TC_DIRECT;
+    atlas_status st = make_plan(ATLAS_KIND_SUFFIX, Hq, Hkv, D, P, &own, &plan->own);
     if (st != ATLAS_OK) return st;
+    own.split_tokens = L->split_tokens;
+    own.debug_flags = L->debug_flags & ~ATLAS_DEBUG_TC_DIRECT;
+    own.phase = ATLAS_PHASE_CHUNKS;  // partial states only, whatever the sizes
     if (S->n_groups < 1 || S->n_groups > L->batch || S->max_prefix_pages < 1)
         return ATLAS_ERR_INVALID_ARG;
     const int64_t max_prefix = (int64_t)S->max_prefix_pages * P;
@@ -147,14 +153,13 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->whole = false;
     if (L->debug_flags & ATLAS_DEBUG_SHARED_WHOLE) plan->whole = plan->stream;
     if (plan->stream && !plan->whole && few && L->split_tokens == 0 &&
-        (int64_t)L->batch * Hkv * plan->own.col_tiles >= 2 * sms) {
+        (int64_t)L->batch * Hkv * plan->own.col_tiles >= 2 * sms)
         // The own splits run beside the tiles, the longest first: where there are enough
         // sequences they are best left whole (up to 4096 keys).
         own.split_tokens = (int32_t)own_split(max_ctx);
-        if (make_plan(ATLAS_KIND_SUFFIX, Hq, Hkv, D, P, &own, &plan->own) != ATLAS_OK)
-            return ATLAS_ERR_UNSUPPORTED;
-    }
-    if (plan->stream && !plan->whole && !few && L->split_tokens == 0 && own_splits) {
+    if (plan->whole) {
+        plan->own.ws_bytes = 0;  // (no states but those of cut tiles)
+    } else if (plan->stream && !few && L->split_tokens == 0 && own_splits) {
         const int64_t out = (int64_t)L->batch * Hq * L->q_len;
         plan->own.path = Path::SplitBF16;
         plan->own.col_tiles = (int)((seq_rows + 15) / 16);
@@ -163,8 +168,12 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
         plan->own.acc_bytes = (size_t)out * plan->own.n_chunks * D * sizeof(float);
         plan->own.ml_offset = (size_t)round_up((int64_t)plan->own.acc_bytes, 256);
         plan->own.ws_bytes = plan->own.ml_offset + (size_t)out * plan->own.n_chunks * 2 * sizeof(float);
+    } else {
+        st = make_plan(ATLAS_KIND_SUFFIX, Hq, Hkv, D, P, &own, &plan->own);
+        if (st != ATLAS_OK) return st;
     }
-    const bool own_cols = plan->own.path == Path::SplitBF16 || plan->own.path == Path::SplitF32;
+    const bool own_cols =
+        !plan->whole && (plan->own.path == Path::SplitBF16 || plan->own.path == Path::SplitF32);
     if (own_cols && (int64_t)plan->own.n_chunks * Hkv * plan->own.col_tiles * L->batch >= INT32_MAX)
         return ATLAS_ERR_UNSUPPORTED;  // (the own splits' CTAs)
     const int64_t tile_of = plan->whole ? seq_rows : group_rows;

@@ -95,6 +95,20 @@ def test_tiles_of_their_own_where_a_gather_fills_no_more(lib, B, groups, q_len, 
     assert own != gathered and size(0) == (own if whole else gathered)
 
 
+def serving(lib, B, q_len, own, prefix, heads=(32, 8), groups=1, dtype=1, P=16, **kw):
+    """Workspace of B sequences of q_len rows, tables of that many own and prefix keys."""
+    return ws(lib, prefixes(n_groups=groups, max_prefix_pages=-(-prefix // P)), Hq=heads[0], Hkv=heads[1], P=P,
+              batch=B, q_len=q_len, max_pages_per_seq=-(-own // P), q_dtype=dtype, kv_dtype=dtype, out_dtype=dtype, **kw)
+
+
+@pytest.mark.parametrize("B,q_len,own,prefix,heads", [
+    (255, 1024, 1024, 1000, (32, 8)), (256, 1024, 1024, 1000, (32, 8)), (300, 1024, 1024, 1000, (32, 8)),
+    (2048, 128, 1024, 1000, (32, 8)), (2049, 128, 1024, 1000, (32, 8)), (128, 1024, 4096, 1000, (64, 8))])
+def test_batches_of_more_tiles_than_a_grid_of_splits_has(lib, B, q_len, own, prefix, heads):
+    """65535 tiles of own keys and more, whose rows have tiles over all their keys."""
+    assert serving(lib, B, q_len, own, prefix, heads) != SIZE_MAX
+
+
 @pytest.mark.parametrize("sms", [0, 1, 8, 152, 300])
 def test_the_workspace_is_that_of_the_sms_planned_for(lib, sms):
     """64 steps behind 32768 keys: more SMs, more states."""

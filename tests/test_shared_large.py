@@ -1,0 +1,96 @@
+"""Attention behind shared prefixes for batches of very many rows or wide tables: some of the
+sequences against fp64 on the GPU.  Tolerances are those of tests/test_shared.py."""
+import math
+
+import pytest
+import torch
+
+import exact_causal_gqa_gb300 as atlas
+from tests.gpu_helpers import BF16_ABS, F32_REL
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+SPLIT, TC, WHOLE = atlas.DEBUG_SHARED_SPLIT, atlas.DEBUG_SHARED_TC, atlas.DEBUG_SHARED_WHOLE | atlas.DEBUG_SHARED_TC
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Batch:
+    """B sequences of own lengths lens, groups from starts on behind prefixes of pre keys; tables as
+    wide as asked, whose entries behind the last page are out of range."""
+
+    def __init__(self, dtype, Hq, Hkv, D, P, q_len, starts, pre, lens, own_width=0, pre_width=0, ragged=None):
+        g = torch.Generator(device="cuda").manual_seed(len(lens) + q_len)
+        lens, pre = torch.tensor(lens), torch.tensor(pre)
+        pages, shared = -(-lens // P), -(-pre // P)
+        n = int(pages.sum() + shared.sum())
+
+        def normal(*shape):
+            return torch.randn(shape, generator=g, device="cuda", dtype=DT[dtype])
+
+        def table(count, first, width):
+            width = max(width, int(count.max()), 1)
+            at = first + torch.cumsum(count, 0)[:, None] - count[:, None] + torch.arange(width)
+            at = torch.where(torch.arange(width) < count[:, None], ids[at.clamp(max=n - 1)], 10 ** 6)
+            return at.int().cuda()
+
+        ids = torch.randperm(n, generator=g, device="cuda").cpu()
+        self.starts, self.pre, self.lens, self.ragged = list(starts), pre.tolist(), lens.tolist(), ragged
+        self.q, self.k, self.v = normal(len(lens), Hq, q_len, D), normal(n, Hkv, P, D), normal(n, Hkv, P, D)
+        self.prefix_table, self.table = table(shared, 0, pre_width), table(pages, int(shared.sum()), own_width)
+        self.sizes = Hq, Hkv, D, P
+        self.scale = D ** -0.5
+
+    def __call__(self, starts=None, pre=None, lens=None, **kw):
+        return atlas.shared(self.q, self.k, self.v, self.prefix_table, ints(pre or self.pre),
+                            ints(starts or self.starts), self.table, ints(lens or self.lens), *self.sizes, self.scale,
+                            q_lens=None if self.ragged is None else ints(self.ragged), **kw)
+
+    def workspace(self, **kw):
+        return atlas.shared_workspace_size(self.q.shape, *self.sizes, self.table.shape[1], len(self.pre),
+                                           self.prefix_table.shape[1], self.k.shape[0], dtype=self.q.dtype, **kw)
+
+    def keys(self, pages, row, length):
+        Hkv, P, D = pages.shape[1:]
+        return pages[row[: -(-length // P)].long()].transpose(0, 1).reshape(Hkv, -1, D)[:, :length].double()
+
+    def exact(self, b):
+        """out, lse of sequence b's rows, in fp64."""
+        Hq, Hkv, D, _ = self.sizes
+        rows, L = self.q.shape[2] if self.ragged is None else self.ragged[b], self.lens[b]
+        parts = [(self.table[b], L)]
+        for n, length in enumerate(self.pre):
+            if self.starts[n] <= b < self.starts[n + 1]:
+                parts.insert(0, (self.prefix_table[n], length))
+        k, v = (torch.cat([self.keys(x, *p) for p in parts], 1).repeat_interleave(Hq // Hkv, 0) for x in (self.k, self.v))
+        T = k.shape[1]
+        seen = torch.arange(T, device="cuda") <= torch.arange(T - rows, T, device="cuda")[:, None]
+        s = (self.q[b, :, :rows].double() @ k.transpose(1, 2) * self.scale).masked_fill(~seen, -math.inf)
+        return torch.softmax(s, -1) @ v, torch.logsumexp(s, -1)
+
+    def check(self, some, **kw):
+        """Rows of the sequences `some`; padding stays as it is, and nothing is written behind the workspace."""
+        f32 = self.q.dtype == torch.float32
+        out = torch.full(self.q.shape, 99.0, device="cuda")
+        lse, status = torch.full(self.q.shape[:3], 99.0, device="cuda"), ints([0])
+        need = self.workspace(**{k: v for k, v in kw.items() if k in ("split_tokens", "debug_flags", "sm_count")})
+        space = torch.full((need + 1024,), 77, dtype=torch.uint8, device="cuda")
+        self(out=out, lse=lse, status=status, workspace=space[:need], **kw)
+        assert int(status.item()) == 0 and bool((space[need:] == 77).all())
+        for b in some:
+            rows = self.q.shape[2] if self.ragged is None else self.ragged[b]
+            want, want_lse = self.exact(b)
+            tol = F32_REL * float(want.abs().max()) if f32 and rows else BF16_ABS
+            assert bool(((out[b, :, :rows].double() - want).abs() <= tol).all()), b
+            assert bool(((lse[b, :, :rows].double() - want_lse).abs() <= (2e-5 if f32 else 1e-4)).all()), b
+            assert bool((out[b, :, rows:] == 99).all()) and bool((lse[b, :, rows:] == 99).all()), b
+        assert bool(torch.isfinite(out).all())
+        return out
+
+
+@pytest.mark.parametrize("B,q_len,prefix", [(2049, 128, 100), (256, 1024, 300)])
+def test_more_tiles_than_a_grid_of_splits_has(B, q_len, prefix):
+    x = Batch("bf16", 32, 8, 64, 16, q_len, [0, B // 2, B], [prefix, 77], [q_len + b % 40 for b in range(B)], own_width=80)
+    x.check([0, 1, B // 2 - 1, B // 2, B - 2, B - 1])
