@@ -195,9 +195,12 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
         plan->chunk = 0;
         // (short tiles that count as more blocks make for more CTAs than SMs)
         plan->ctas = sms + units / 10 + 2;
-        const double line = (double)units * kPairCost * (double)(blocks + kWholeTileBlocks);
-        if (line * (1.0 + (double)units / (sms * 13.0)) + 1e6 >= INT32_MAX)
-            return ATLAS_ERR_UNSUPPORTED;  // (places in the line have 32 bits)
+        // Places in the line have 32 bits.  Short tiles count for more, so that a share has few enough
+        // pieces: with a = blocks + 5 at most to a tile, a share is at most 28 such tiles of 7 a block
+        // (three quarters of a CTA's pieces), and a tile counts for at least 9/8 of a share over 4 * 38
+        // blocks, 1.46 a: no more than that for any tile, and one for rounding.
+        const double line = (double)units * kPairCost * (1.5 * (double)(blocks + kWholeTileBlocks) + 2.0);
+        if (line + 1e6 >= INT32_MAX) return ATLAS_ERR_UNSUPPORTED;
         const int64_t states = plan->whole ? plan->ctas * 2 * cta_rows : out_rows * plan->n_pre;
         plan->ml_at = plan->acc_at + (size_t)round_up(states * D * 4, 256);
         plan->plan_at = plan->ml_at + (size_t)round_up(states * 8, 256);

@@ -189,9 +189,6 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
     // have.  Shares grow by what that adds, up to an eighth: a few CTAs more than SMs would wait for
     // one to end (57 sequences of 256 rows, 256 to 1792 own keys: 708 us, not 451).
     int ctas = st.own_rate > 0.f ? ctas_beside(p, (float)all, (float)own_keys) : st.sms;
-    // (What the short tiles add is a thirteenth of a share each at most.  The host has seen that
-    // the line has room for that with a CTA for each SM; with fewer it is seen here.)
-    if ((float)all * (1.f + (float)n_tiles / (13.f * (float)ctas)) > 2e9f) ctas = st.sms;
     const int pieces = st.max_items - 2;
     ctas *= 1 + n_tiles / (ctas * (pieces * 3 / 4));
     int64_t per64 = (all + ctas - 1) / ctas;

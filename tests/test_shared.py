@@ -110,6 +110,13 @@ def test_batches_of_more_tiles_than_a_grid_of_splits_has(lib, B, q_len, own, pre
 
 
 @pytest.mark.parametrize("sms", [0, 1, 8, 152, 300])
+def test_batches_behind_wide_tables(lib, sms):
+    """A line of many tiles of many blocks, whatever the number of SMs that it is cut among."""
+    assert serving(lib, 256, 512, 131072, 131072, sm_count=sms) != SIZE_MAX
+    assert serving(lib, 64, 1024, 131072, 131072, groups=64, sm_count=sms) != SIZE_MAX
+
+
+@pytest.mark.parametrize("sms", [0, 1, 8, 152, 300])
 def test_the_workspace_is_that_of_the_sms_planned_for(lib, sms):
     """64 steps behind 32768 keys: more SMs, more states."""
     S = prefixes(n_groups=1, max_prefix_pages=2048)

@@ -94,3 +94,10 @@ class Batch:
 def test_more_tiles_than_a_grid_of_splits_has(B, q_len, prefix):
     x = Batch("bf16", 32, 8, 64, 16, q_len, [0, B // 2, B], [prefix, 77], [q_len + b % 40 for b in range(B)], own_width=80)
     x.check([0, 1, B // 2 - 1, B // 2, B - 2, B - 1])
+
+
+@pytest.mark.parametrize("B,q_len,starts,sms", [(256, 512, [0, 100, 256], 0), (40, 256, [0, 39, 40], 3)])
+def test_tables_far_wider_than_the_lengths(B, q_len, starts, sms):
+    x = Batch("bf16", 32, 8, 64, 16, q_len, starts, [300, 5000], [q_len + b % 40 for b in range(B)], own_width=8192,
+              pre_width=8192)
+    x.check([0, starts[1] - 1, starts[1], B - 1], sm_count=sms)
