@@ -260,6 +260,9 @@ cudaError_t launch_fmha_tc(const TcParams &p, const CUtensorMap &tmQ, const CUte
                            const CUtensorMap &tmV, cudaStream_t stream);
 // The tiles of p.st (bf16; with st.whole the call's output, else partial states and a
 // dependent of the launch before), or the splits of shared prefixes, `ctas` of them at most.
+// Borders of n_groups groups of B sequences among the n from b0 on.
+cudaError_t launch_shared_starts(const int32_t *starts, int32_t *mine, int n_groups, int B, int b0, int n,
+                                 cudaStream_t stream);
 // p.st's arrays, one CTA; and the output rows of the tiles that are cut (st.whole).
 cudaError_t launch_shared_plan(const TcParams &p, cudaStream_t stream);
 cudaError_t launch_shared_cut_merge(const TcParams &p, int64_t ctas, cudaStream_t stream);

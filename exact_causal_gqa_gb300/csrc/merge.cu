@@ -92,7 +92,11 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const Params p) {
     const bool bad_len = qn < 0 || qn > p.q_len || L < p.row_step * qn || L > p.max_pages * p.P ||
                          (p.require_full && L != qn) || n_pre < 0;
     if (!bad_len && i >= qn) active = false;  // padding row: not a query, not written
-    if (W == 1 && !active) return;            // (W > 1: every warp reaches the exchange)
+    if (W == 1 && !active) {                  // (W > 1: every warp reaches the exchange)
+        // (a grid of padding rows alone must not end before the splits: another part may follow)
+        if (kShared) wait_for_previous_grid();
+        return;
+    }
     // the split kernel that wrote the partials has completed, its writes visible
     asm volatile("griddepcontrol.wait;" ::: "memory");
 

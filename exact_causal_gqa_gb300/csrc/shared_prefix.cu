@@ -55,7 +55,17 @@ struct SharedPlan {
     size_t acc_at, ml_at;  // the prefixes' states in the workspace (whole: the cut tiles')
     size_t plan_at;        // stream: its arrays
     size_t bytes;
+    // The whole call: neighbouring sequences in parts of so many (the last has what is left), each
+    // with the groups' borders among them in the workspace.
+    int32_t part, parts;
+    bool sparing;          // own keys in no more splits than fill the SMs
+    size_t starts_at;
 };
+
+// States of a call at most, in bytes.  A batch that needs more runs in parts, one after the other, in
+// the same workspace: a part has some 10^5 rows of states and takes milliseconds, its launches, its
+// end and another pass over the prefixes a hundredth of that.
+constexpr size_t kMostBytes = (size_t)512 << 20;
 
 // CTAs of a wave of the split kernels, in hundredths of the SMs, and a CTA's keys at least.
 constexpr int64_t kSplitWave = 200, kSplitWaveF32 = 300, kMinSplit = 128, kMinSplitF32 = 64;
@@ -111,9 +121,10 @@ bool whole_pays(int64_t rows, int64_t group_rows, int64_t max_prefix, bool own_s
            (own_splits ? 2.6 : 9.5) * (double)((rows + 127) / 128);
 }
 
-atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const atlas_shared *S,
-                         const atlas_launch *L, SharedPlan *plan) {
-    if (!S || !L) return ATLAS_ERR_INVALID_ARG;
+// The plan of a part: L is its launch, `groups` the groups that it has, on average.  `sparing`: own
+// keys in no more splits than fill the SMs.
+atlas_status plan_part(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const atlas_shared *S,
+                       const atlas_launch *L, int32_t groups, bool sparing, SharedPlan *plan) {
     if (L->window != 0) return ATLAS_ERR_INVALID_ARG;
     if (L->phase != ATLAS_PHASE_ALL || L->chunk_range) return ATLAS_ERR_UNSUPPORTED;
     if (L->split_tokens < 0 || L->split_tokens % kSplitBlockTokens != 0) return ATLAS_ERR_INVALID_ARG;
@@ -127,19 +138,18 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     own.split_tokens = L->split_tokens;
     own.debug_flags = L->debug_flags & ~ATLAS_DEBUG_TC_DIRECT;
     own.phase = ATLAS_PHASE_CHUNKS;  // partial states only, whatever the sizes
-    if (S->n_groups < 1 || S->n_groups > L->batch || S->max_prefix_pages < 1)
-        return ATLAS_ERR_INVALID_ARG;
+    if (S->max_prefix_pages < 1) return ATLAS_ERR_INVALID_ARG;
     const int64_t max_prefix = (int64_t)S->max_prefix_pages * P;
     if (max_prefix > INT32_MAX / 2) return ATLAS_ERR_INVALID_ARG;
 
     const int64_t sms = planned_sms(L);
     const int G = Hq / Hkv;
     const int64_t rows = (int64_t)L->batch * G * L->q_len;  // of one kv head, all groups
-    const int64_t group_rows = (rows + S->n_groups - 1) / S->n_groups;
+    const int64_t group_rows = (rows + groups - 1) / groups;
     const bool f32 = L->kv_dtype == ATLAS_F32;
     const bool few = plan->few = plan->own.path == Path::SplitBF16 || plan->own.path == Path::SplitF32;
     const int cols = f32 ? (group_rows <= 4 ? 4 : 8) : group_rows <= 8 ? 8 : 16;
-    const double bytes = 2.0 * S->n_groups * max_prefix * Hkv * D * (f32 ? 4 : 2);
+    const double bytes = 2.0 * groups * max_prefix * Hkv * D * (f32 ? 4 : 2);
     const int64_t seq_rows = (int64_t)G * L->q_len, max_ctx = (int64_t)L->max_pages_per_seq * P;
     // (own keys: half of the most there may be)
     plan->split = few && split_pays(bytes, (group_rows + cols - 1) / cols, 4.0 * D * rows * Hkv * max_prefix,
@@ -169,6 +179,11 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
         plan->own.ml_offset = (size_t)round_up((int64_t)plan->own.acc_bytes, 256);
         plan->own.ws_bytes = plan->own.ml_offset + (size_t)out * plan->own.n_chunks * 2 * sizeof(float);
     } else {
+        if (sparing && !few && L->split_tokens == 0) {
+            const int64_t tiles = (int64_t)L->batch * Hkv * ((seq_rows + 127) / 128);
+            const int64_t splits = (6 * sms + tiles - 1) / tiles;
+            own.split_tokens = (int32_t)round_up(std::max<int64_t>((max_ctx + splits - 1) / splits, 1024), 128);
+        }
         st = make_plan(ATLAS_KIND_SUFFIX, Hq, Hkv, D, P, &own, &plan->own);
         if (st != ATLAS_OK) return st;
     }
@@ -181,8 +196,8 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     // CTAs of one split: a group's last may be partly filled
     const int64_t cta_rows = plan->split ? cols : 128 * plan->tiles;
     const int64_t units = (plan->whole ? L->batch * ((seq_rows + cta_rows - 1) / cta_rows)
-                                       : rows / cta_rows + S->n_groups) * Hkv;
-    const int64_t likely = std::max<int64_t>((rows + cta_rows - 1) / cta_rows, S->n_groups) * Hkv;
+                                       : rows / cta_rows + std::min(S->n_groups, L->batch)) * Hkv;
+    const int64_t likely = std::max<int64_t>((rows + cta_rows - 1) / cta_rows, groups) * Hkv;
     const int64_t out_rows = (int64_t)L->batch * Hq * L->q_len;
     plan->acc_at = plan->whole ? 0 : (size_t)round_up((int64_t)plan->own.ws_bytes, 256);
     if (plan->stream) {
@@ -240,6 +255,49 @@ atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const at
     plan->ml_at = plan->acc_at + (size_t)round_up(out_rows * plan->n_pre * D * 4, 256);
     plan->bytes = plan->ml_at + (size_t)out_rows * plan->n_pre * 8;
     return ATLAS_OK;
+}
+
+// Groups of a part of n of B sequences, on average.
+int32_t part_groups(int64_t n_groups, int64_t n, int64_t B) { return (int32_t)((n_groups * n + B - 1) / B); }
+
+// The whole call's plan, that of its first part; `bytes` is what the call needs.
+atlas_status shared_plan(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const atlas_shared *S,
+                         const atlas_launch *L, SharedPlan *plan) {
+    if (!S || !L || L->batch < 1 || S->n_groups < 1 || S->n_groups > L->batch) return ATLAS_ERR_INVALID_ARG;
+    const int64_t B = L->batch;
+    atlas_launch part = *L;
+    for (bool sparing = false;; sparing = true) {
+        // (parts of equal sizes)
+        const int64_t parts = (B + part.batch - 1) / part.batch, last = B - (parts - 1) * part.batch;
+        SharedPlan rest;
+        rest.bytes = 0;
+        atlas_launch behind = part;
+        behind.batch = (int32_t)last;
+        atlas_status st = plan_part(Hq, Hkv, D, P, S, &part, part_groups(S->n_groups, part.batch, B), sparing, plan);
+        if (st == ATLAS_OK && last != part.batch)
+            st = plan_part(Hq, Hkv, D, P, S, &behind, part_groups(S->n_groups, last, B), sparing, &rest);
+        if (st == ATLAS_ERR_INVALID_ARG) return st;
+        if (st == ATLAS_OK) {
+            plan->sparing = sparing;
+            plan->part = part.batch;
+            plan->parts = (int32_t)parts;
+            if (parts > 1) {
+                plan->starts_at = (size_t)round_up((int64_t)std::max(plan->bytes, rest.bytes), 256);
+                plan->bytes = plan->starts_at + 4 * ((size_t)S->n_groups + 1);
+            }
+            if (plan->bytes <= kMostBytes || (part.batch == 1 && sparing)) return ATLAS_OK;
+        } else if (part.batch == 1 && sparing) {
+            return st;
+        }
+        if (!sparing) continue;  // (fewer splits first)
+        int64_t size = part.batch / 2;
+        if (st == ATLAS_OK)
+            size = std::min((int64_t)((double)part.batch * (double)kMostBytes / (double)plan->bytes),
+                            (int64_t)part.batch * 7 / 8);
+        size = std::max<int64_t>(size, 1);
+        const int64_t fewer = (B + size - 1) / size;
+        part.batch = (int32_t)((B + fewer - 1) / fewer);
+    }
 }
 
 // The own splits and the prefixes' in one launch; or (order given) the own ones alone, behind
@@ -410,6 +468,7 @@ atlas_status launch_tc(const SharedPlan &plan, const void *q, const void *k_page
     }
     atlas_launch own = *L;
     own.phase = ATLAS_PHASE_CHUNKS;
+    own.split_tokens = plan.own.chunk;
     own.debug_flags = (own.debug_flags & ~ATLAS_DEBUG_TC_DIRECT) | kNearestProducts;
     own.events = nullptr;
     own.workspace_bytes = plan.own.ws_bytes;
@@ -448,6 +507,60 @@ atlas_status launch_whole(const SharedPlan &plan, const void *q, const void *k_p
         launch_shared_cut_merge(tp, plan.ctas, stream) != cudaSuccess)
         return ATLAS_ERR_CUDA;
     return ATLAS_OK;
+}
+
+// All launches of a part; `between` is recorded before the merge.
+atlas_status launch_part(const SharedPlan &plan, const void *q, const void *k_pages, const void *v_pages,
+                         const int32_t *page_table, const int32_t *seq_lens, int32_t Hq, int32_t Hkv, int32_t D,
+                         int32_t P, float scale, const atlas_shared *S, const atlas_launch *L, cudaEvent_t between) {
+    cudaStream_t stream = static_cast<cudaStream_t>(L->stream);
+    float *pre_acc = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.acc_at);
+    float *pre_ml = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.ml_at);
+    if (plan.whole) {
+        return launch_whole(plan, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P, scale, S, L,
+                            pre_acc, pre_ml, between);
+    }
+    if (plan.split) {
+        if (launch_split(plan, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P, scale, S, L,
+                         pre_acc, pre_ml) != cudaSuccess)
+            return ATLAS_ERR_CUDA;
+    } else {
+        const atlas_status st = launch_tc(plan, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P, scale, S, L,
+                                          pre_acc, pre_ml);
+        if (st != ATLAS_OK) return st;
+    }
+    if (between && cudaEventRecord(between, stream) != cudaSuccess) return ATLAS_ERR_CUDA;
+
+    SharedMergeParams mp{};
+    mp.seq_lens = seq_lens;
+    mp.B = L->batch;
+    mp.Hq = Hq;
+    mp.D = D;
+    mp.q_len = L->q_len;
+    mp.max_pages = L->max_pages_per_seq;
+    mp.P = P;
+    mp.chunk = plan.own.chunk;
+    mp.n_chunks = plan.own.n_chunks;
+    mp.row_step = 1;
+    mp.sinks = L->sinks;
+    mp.q_lens = L->q_lens;
+    mp.ws_acc = static_cast<float *>(L->workspace);
+    mp.ws_ml = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.own.ml_offset);
+    mp.out = L->out;
+    mp.out_bf16 = L->out_dtype == ATLAS_BF16;
+    mp.lse = L->lse;
+    mp.sms = planned_sms(L);
+    mp.group_starts = S->group_starts;
+    mp.prefix_lens = S->prefix_lens;
+    mp.n_groups = S->n_groups;
+    mp.max_prefix = S->max_prefix_pages * P;
+    mp.pre_chunk = plan.chunk;
+    mp.n_pre = plan.n_pre;
+    mp.pre_acc = pre_acc;
+    mp.pre_ml = pre_ml;
+    mp.G = Hq / Hkv;
+    if (plan.stream) mp.st = stream_arrays(plan, mp.G, S, L);
+    return launch_shared_merge(mp, stream) == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 
 }  // namespace
@@ -499,56 +612,31 @@ extern "C" atlas_status atlas_attn_shared(const void *q, const void *k_pages, co
 
     (void)cudaGetLastError();
     if (ev[0] && cudaEventRecord(ev[0], stream) != cudaSuccess) return ATLAS_ERR_CUDA;
-    float *pre_acc = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.acc_at);
-    float *pre_ml = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.ml_at);
-    if (plan.whole) {
-        st = launch_whole(plan, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P, scale, S, L,
-                          pre_acc, pre_ml, ev[1]);
+    if (plan.parts == 1) {
+        st = launch_part(plan, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P, scale, S, L, ev[1]);
         if (st != ATLAS_OK) return st;
-        if (ev[2] && cudaEventRecord(ev[2], stream) != cudaSuccess) return ATLAS_ERR_CUDA;
-        return ATLAS_OK;
     }
-    if (plan.split) {
-        if (launch_split(plan, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P, scale, S, L,
-                         pre_acc, pre_ml) != cudaSuccess)
+    for (int64_t b0 = 0; plan.parts > 1 && b0 < L->batch; b0 += plan.part) {
+        const int32_t n = (int32_t)std::min<int64_t>(plan.part, L->batch - b0);
+        const size_t row0 = (size_t)b0 * Hq * L->q_len;
+        atlas_launch part = *L;
+        part.batch = n;
+        part.out = static_cast<char *>(L->out) + row0 * D * (L->out_dtype == ATLAS_F32 ? 4 : 2);
+        if (L->lse) part.lse = L->lse + row0;
+        if (L->q_lens) part.q_lens = L->q_lens + b0;
+        int32_t *const starts = reinterpret_cast<int32_t *>(static_cast<char *>(L->workspace) + plan.starts_at);
+        atlas_shared groups = *S;
+        groups.group_starts = starts;
+        SharedPlan own;
+        st = plan_part(Hq, Hkv, D, P, S, &part, part_groups(S->n_groups, n, L->batch), plan.sparing, &own);
+        if (st != ATLAS_OK) return st;
+        if (launch_shared_starts(S->group_starts, starts, S->n_groups, L->batch, (int)b0, n, stream) != cudaSuccess)
             return ATLAS_ERR_CUDA;
-    } else {
-        st = launch_tc(plan, q, k_pages, v_pages, page_table, seq_lens, Hq, Hkv, D, P, scale, S, L,
-                       pre_acc, pre_ml);
+        st = launch_part(own, static_cast<const char *>(q) + row0 * D * size, k_pages, v_pages,
+                         page_table + b0 * L->max_pages_per_seq, seq_lens + b0, Hq, Hkv, D, P, scale,
+                         &groups, &part, b0 + n == L->batch ? ev[1] : nullptr);
         if (st != ATLAS_OK) return st;
     }
-    if (ev[1] && cudaEventRecord(ev[1], stream) != cudaSuccess) return ATLAS_ERR_CUDA;
-
-    SharedMergeParams mp{};
-    mp.seq_lens = seq_lens;
-    mp.B = L->batch;
-    mp.Hq = Hq;
-    mp.D = D;
-    mp.q_len = L->q_len;
-    mp.max_pages = L->max_pages_per_seq;
-    mp.P = P;
-    mp.chunk = plan.own.chunk;
-    mp.n_chunks = plan.own.n_chunks;
-    mp.row_step = 1;
-    mp.sinks = L->sinks;
-    mp.q_lens = L->q_lens;
-    mp.ws_acc = static_cast<float *>(L->workspace);
-    mp.ws_ml = reinterpret_cast<float *>(static_cast<char *>(L->workspace) + plan.own.ml_offset);
-    mp.out = L->out;
-    mp.out_bf16 = L->out_dtype == ATLAS_BF16;
-    mp.lse = L->lse;
-    mp.sms = planned_sms(L);
-    mp.group_starts = S->group_starts;
-    mp.prefix_lens = S->prefix_lens;
-    mp.n_groups = S->n_groups;
-    mp.max_prefix = S->max_prefix_pages * P;
-    mp.pre_chunk = plan.chunk;
-    mp.n_pre = plan.n_pre;
-    mp.pre_acc = pre_acc;
-    mp.pre_ml = pre_ml;
-    mp.G = Hq / Hkv;
-    if (plan.stream) mp.st = stream_arrays(plan, mp.G, S, L);
-    if (launch_shared_merge(mp, stream) != cudaSuccess) return ATLAS_ERR_CUDA;
     if (ev[2] && cudaEventRecord(ev[2], stream) != cudaSuccess) return ATLAS_ERR_CUDA;
     return ATLAS_OK;
 }

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
     __shared__ __align__(16) int s_key[N];  // the sequences' order: length, then place
     const SharedStream &st = p.st;
     const int tid = (int)threadIdx.x;
-    const bool small = p.B <= N;  // (and as many groups at most)
+    const bool small = p.B <= N && st.n_groups <= N;
     const int *const starts = small ? s_starts : st.group_starts;
     const int *const pre_lens = small ? s_pre : st.prefix_lens, *const lens = small ? s_len : p.seq_lens;
     int *const before = small ? s_before : st.before, *const group_of = small ? s_group : st.group;
@@ -419,7 +419,24 @@ __global__ void __launch_bounds__(kCutWarps * 32) shared_cut_merge_kernel(const 
     }
 }
 
+// The groups' borders among sequences [b0, b0 + n): out of range wherever those of the batch are.
+__global__ void __launch_bounds__(kPlanThreads) shared_starts_kernel(const int32_t *starts, int32_t *mine,
+                                                                     int n_groups, int B, int b0, int n) {
+    bool wrong = false;
+    for (int i = (int)threadIdx.x; i < n_groups; i += kPlanThreads)
+        wrong |= starts[i] < 0 || starts[i + 1] < starts[i] || starts[i + 1] > B;
+    wrong = __syncthreads_or(wrong) != 0;
+    for (int i = (int)threadIdx.x; i <= n_groups; i += kPlanThreads)
+        mine[i] = wrong ? -1 : min(max(starts[i] - b0, 0), n);
+}
+
 }  // namespace
+
+cudaError_t launch_shared_starts(const int32_t *starts, int32_t *mine, int n_groups, int B, int b0, int n,
+                                 cudaStream_t stream) {
+    shared_starts_kernel<<<1, kPlanThreads, 0, stream>>>(starts, mine, n_groups, B, b0, n);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_shared_plan(const TcParams &p, cudaStream_t stream) {
     shared_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);

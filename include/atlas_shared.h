@@ -62,6 +62,11 @@ typedef struct {
  * ATLAS_ERR_INVALID_ARG (it would cut the prefix off), a phase other than ATLAS_PHASE_ALL or a
  * chunk_range ATLAS_ERR_UNSUPPORTED.  out, lse and the workspace may not overlap one another, q
  * or the pools (ATLAS_ERR_INVALID_ARG).
+ * A call whose partial states would take more than 512 MB runs in parts of neighbouring sequences, one
+ * after the other in the same workspace (event 1: before the last part's merge); a single sequence of
+ * very many rows may need more.  Refused as ATLAS_ERR_UNSUPPORTED, beside what atlas_attn_suffix
+ * refuses: a sequence alone of more than 65535 tiles of 128 rows whose own keys are split, and one (or
+ * its prefix) of more than 2^31 / 11 pairs of a 256-row tile and a 128-key block of its tables.
  * The same call on the same arrays gives the same bits.  On the split kernels a sequence's bits
  * depend on its own group alone (and on the sizes that the call is planned from); on the bf16
  * tensor-core kernels also on the other groups and lengths of the batch and on sm_count, which

@@ -109,6 +109,31 @@ def test_batches_of_more_tiles_than_a_grid_of_splits_has(lib, B, q_len, own, pre
     assert serving(lib, B, q_len, own, prefix, heads) != SIZE_MAX
 
 
+@pytest.mark.parametrize("B,q_len,own,prefix,dtype", [
+    (64, 300, 2048, 32768, 1), (64, 300, 2048, 32768, 0), (512, 300, 32768, 32768, 1), (512, 300, 32768, 32768, 0),
+    (512, 320, 32768, 32768, 1), (256, 256, 131072, 131072, 1), (256, 256, 131072, 131072, 0),
+    (4, 8192, 131072, 131072, 1), (4, 8192, 131072, 131072, 0), (60000, 20, 131072, 131072, 1),
+    (60000, 1, 131072, 131072, 1), (60000, 1, 131072, 131072, 0)])
+def test_the_workspace_has_bounds(lib, B, q_len, own, prefix, dtype):
+    for groups in (1, B):
+        assert serving(lib, B, q_len, own, prefix, groups=groups, dtype=dtype) <= 512 << 20
+        # (splits that are asked for may make one sequence's states more, beside the groups' six words each)
+        alone = serving(lib, 1, q_len, own, prefix, dtype=dtype, split_tokens=2048) + 256 + 24 * (B + 1)
+        assert serving(lib, B, q_len, own, prefix, groups=groups, dtype=dtype, split_tokens=2048) <= max(512 << 20, alone)
+    # a batch that fits is not cut: the bound changes nothing there
+    assert serving(lib, 4, 20, own, prefix, dtype=dtype) < 512 << 20
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("B,q_len,own,prefix,heads", [
+    (256, 1024, 1024, 1000, (32, 8)), (2049, 128, 1024, 1000, (32, 8)), (9000, 40, 4096, 40000, (8, 8)),
+    (70000, 1, 512, 4000, (8, 8)), (70000, 3, 512, 64, (32, 8))])
+def test_batches_of_any_number_of_tiles(lib, B, q_len, own, prefix, heads, dtype):
+    for flags in (0, atlas.DEBUG_SHARED_SPLIT, atlas.DEBUG_SHARED_TC, atlas.DEBUG_SHARED_WHOLE):
+        for groups in (1, 1 + B // 3, B):
+            assert serving(lib, B, q_len, own, prefix, heads, groups, dtype, debug_flags=flags) != SIZE_MAX
+
+
 @pytest.mark.parametrize("sms", [0, 1, 8, 152, 300])
 def test_batches_behind_wide_tables(lib, sms):
     """A line of many tiles of many blocks, whatever the number of SMs that it is cut among."""

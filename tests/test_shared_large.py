@@ -101,3 +101,95 @@ def test_tables_far_wider_than_the_lengths(B, q_len, starts, sms):
     x = Batch("bf16", 32, 8, 64, 16, q_len, starts, [300, 5000], [q_len + b % 40 for b in range(B)], own_width=8192,
               pre_width=8192)
     x.check([0, starts[1] - 1, starts[1], B - 1], sm_count=sms)
+
+
+PARTS = [
+    # dtype, Hq, Hkv, q_len, path, ragged: few rows on each path, and tiles of many
+    ("bf16", 16, 2, 1, SPLIT, False), ("bf16", 16, 2, 1, TC, False), ("bf16", 8, 2, 2, 0, True),
+    ("bf16", 4, 2, 12, TC, True), ("f32", 16, 2, 1, SPLIT, False), ("f32", 16, 2, 1, TC, False),
+    ("f32", 4, 1, 7, 0, True)]
+STARTS, PRE = [0, 5, 30, 31, 31, 60], [700, 40, 0, 9, 129]   # (the last four sequences in no group)
+
+
+def in_parts(dtype, Hq, Hkv, q_len, ragged):
+    """64 sequences whose states of 64 keys each, of tables of 65536 keys, need more than one part."""
+    return Batch(dtype, Hq, Hkv, 64, 128, q_len, STARTS, PRE, [q_len + 5 * b % 300 for b in range(64)], own_width=512,
+                 pre_width=512, ragged=[b % (q_len + 1) for b in range(64)] if ragged else None)
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,q_len,path,ragged", PARTS)
+def test_in_parts(dtype, Hq, Hkv, q_len, path, ragged):
+    """Groups whose sequences are in several parts, none, or in no group at all."""
+    x = in_parts(dtype, Hq, Hkv, q_len, ragged)
+    rows = 64 * Hq * q_len
+    whole = rows * 2 * 1024 * (64 * 4 + 8)   # states of the batch in one part
+    assert x.workspace(split_tokens=64, debug_flags=path) <= 512 << 20 < whole
+    x.check(range(64), split_tokens=64, debug_flags=path)
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,q_len,path,ragged", PARTS)
+def test_in_parts_what_is_out_of_range_is_reported(dtype, Hq, Hkv, q_len, path, ragged):
+    x = in_parts(dtype, Hq, Hkv, q_len, False)
+    kw = dict(split_tokens=64, debug_flags=path, out_dtype=torch.float32)
+    good = x(**kw)
+    lens, pre = list(x.lens), list(x.pre)
+    lens[40] = q_len - 1
+    pre[0] = 512 * 128 + 1
+    for change, nan in ((dict(lens=lens), {40}), (dict(pre=pre), set(range(5))),
+                        (dict(starts=[0, 5, 30, 31, 31, 65]), set(range(64))),
+                        (dict(starts=[0, 5, 4, 31, 31, 60]), set(range(64))),
+                        (dict(starts=[-1, 5, 30, 31, 31, 60]), set(range(64)))):
+        status = ints([0])
+        out = x(status=status, **change, **kw)
+        assert int(status.item()) == atlas.DEV_BAD_SEQLEN
+        for b in range(64):
+            if b in nan:
+                assert bool(torch.isnan(out[b]).all())
+            else:   # (twice the bound: tiles may be cut elsewhere when a sequence drops out)
+                tol = 2 * (BF16_ABS if dtype == "bf16" else F32_REL * 8)
+                assert float(good.abs().max()) <= 8 and float((out[b] - good[b]).abs().max()) <= tol
+
+
+def test_in_parts_rows_of_padding_alone():
+    """Parts in which no sequence has a query, before and behind parts that have."""
+    for ragged in ([0] * 40 + [1] * 24, [1] * 20 + [0] * 44, [0] * 64):
+        for path in (SPLIT, TC):
+            x = in_parts("bf16", 16, 2, 1, False)
+            x.ragged = ragged
+            x.check(range(64), split_tokens=64, debug_flags=path)
+
+
+@pytest.mark.parametrize("dtype,path,B,D", [("bf16", WHOLE, 5200, 128), ("f32", 0, 8200, 64), ("bf16", TC, 8200, 64)])
+def test_many_sequences_in_parts(dtype, path, B, D):
+    """More than 512 MB of cut tiles' places, and more than 65535 tiles of own keys."""
+    x = Batch(dtype, 8, 8, D, 32, 17, [0, 3000, 3001, B - 1], [100, 33, 200], [17 + b % 40 for b in range(B)])
+    some = sorted({*range(0, B, 97), 2999, 3000, 3001, B - 2, B - 1, *range(B // 2 - 3, B // 2 + 3)})
+    x.check(some, debug_flags=path)
+
+
+@pytest.mark.parametrize("dtype,path", [("bf16", SPLIT), ("bf16", TC), ("f32", 0)])
+def test_in_parts_captured_and_replayed(dtype, path):
+    x = in_parts(dtype, 16, 2, 1, False)
+    space = torch.empty(x.workspace(split_tokens=64, debug_flags=path), dtype=torch.uint8, device="cuda")
+    args = [ints(x.pre), ints(x.starts), ints(x.lens)]
+    out = torch.empty(x.q.shape, device="cuda")
+
+    def call():
+        return atlas.shared(x.q, x.k, x.v, x.prefix_table, args[0], args[1], x.table, args[2], *x.sizes, x.scale,
+                            out=out, workspace=space, split_tokens=64, debug_flags=path)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            call()
+    for pre, starts, lens in ((x.pre, x.starts, x.lens), ([3, 40, 0, 9, 100], [1, 1, 40, 50, 50, 64], x.lens[::-1])):
+        lens = [min(a, b) for a, b in zip(lens, x.lens)]
+        torch.cuda.synchronize()
+        for t, v in zip(args, (pre, starts, lens)):
+            t.copy_(torch.tensor(v, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bool(torch.isfinite(out).all())
+        assert torch.equal(out, x(starts, pre, lens, split_tokens=64, debug_flags=path, out_dtype=torch.float32))
