@@ -199,14 +199,18 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
     if (!st.whole) per64 = max(per64, (int64_t)((most + st.max_states - 3) / (st.max_states - 2)) * longest);
     int per = (int)per64;
     const int most_per = per + per / 8;
-    const int least = (most_per + kSingleCost * pieces - 1) / (kSingleCost * pieces);
+    auto least_blocks = [&](int rows) {  // of a unit's tiles, with a short one among them or without
+        const bool pairs = st.tile_rows == 256 && (rows % 256 == 0 || rows % 256 > 128);
+        const int blocks = (pairs ? kPairCost : kSingleCost) * pieces;
+        return (most_per + blocks - 1) / blocks;
+    };
     carry = 0;
     for (int u0 = 0; u0 < st.units; u0 += N) {
         const int u = u0 + tid;
         int64_t length = 0;
         if (u < st.units) {
             const bool some = rows_of[u] > 0 && blocks_of[u] > 0;
-            const int nb = some ? max(blocks_of[u] + tile_blocks, least) : 0;
+            const int nb = some ? max(blocks_of[u] + tile_blocks, least_blocks(rows_of[u])) : 0;
             weight_of[u] = nb;
             cost_of[u] = some ? head_cost(rows_of[u], nb) : 1;
             length = some ? (int64_t)cost_of[u] * p.Hkv : 0;

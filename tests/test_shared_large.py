@@ -103,6 +103,21 @@ def test_tables_far_wider_than_the_lengths(B, q_len, starts, sms):
     x.check([0, starts[1] - 1, starts[1], B - 1], sm_count=sms)
 
 
+def test_whole_tiles_fill_whole_waves():
+    """10240 tiles of 256 rows among three CTAs to an SM, not a few more: 22.5 tiles a share have room
+    among a CTA's 38 pieces, so none counts for more blocks than it has."""
+    B, n, prefix, sms = 256, 320, 300, 152
+    x = Batch("bf16", 32, 8, 64, 16, n, [0, B], [prefix], [n] * B)
+    space = torch.zeros(x.workspace(debug_flags=WHOLE, sm_count=sms), dtype=torch.uint8, device="cuda")
+    x(workspace=space, debug_flags=WHOLE, sm_count=sms)
+    # a CTA has 40 places for its pieces: unit, kv head, first row, rows, first block, blocks, state, keys,
+    # own keys, group
+    words = space[: space.numel() // 4 * 4].view(torch.int32)
+    at = ((words[3:-6] == 4 * n) & (words[7:-2] == prefix) & (words[9:] == 0)).nonzero().flatten()
+    ctas = torch.unique((at - at[0]) // 400).numel()
+    assert 2 * sms < ctas <= 3 * sms
+
+
 PARTS = [
     # dtype, Hq, Hkv, q_len, path, ragged: few rows on each path, and tiles of many
     ("bf16", 16, 2, 1, SPLIT, False), ("bf16", 16, 2, 1, TC, False), ("bf16", 8, 2, 2, 0, True),
