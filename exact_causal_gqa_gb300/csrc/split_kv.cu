@@ -330,6 +330,9 @@ __device__ void write_partials(const Params &p, const SplitCta &at, const float 
                 a += f * cacc[(w * NCOLS + c) * D + d];
                 l += f * cl[w * NCOLS + c];
             }
+        } else {  // no weight at all: 0, or NaN where a score was
+#pragma unroll
+            for (int w = 0; w < W; ++w) l += cl[w * NCOLS + c];
         }
         if (part) {
             part[c * (D + 2) + d] = a;

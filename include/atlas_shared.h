@@ -75,6 +75,10 @@ typedef struct {
  * every row NaN; a prefix length out of range does so for its group, a bad seq_len or q_len
  * for its sequence; a page id outside the pool sets ATLAS_DEV_BAD_PAGE and leaves the rows
  * that read it NaN.
+ * Infinities and NaN in K and V are not scanned for and propagate to the rows that see them: a NaN
+ * score, or one of +inf, makes its row NaN (in fp32 on the tensor cores any infinite key element does,
+ * to all rows of its group and kv head), a score of -inf has no weight, and a value that is NaN or
+ * infinite makes its element NaN or infinite.  A sink that is NaN or +inf makes its head's rows NaN.
  * Precision: the split kernels are those of atlas_attn_decode (bf16 weights as two bf16 parts,
  * fp32 products for fp32).  The bf16 tensor-core kernels take the weights as two bf16 parts for up
  * to 16 rows to a sequence and kv head (decode steps, drafted rows), as atlas_attn_decode and
