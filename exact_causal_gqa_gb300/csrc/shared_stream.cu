@@ -186,8 +186,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
     const int most = s_most;
     // A CTA's share: one CTA for each SM (two, three for very many tiles), few enough states of a
     // tile, and few enough pieces of a CTA, for which short tiles count as more blocks than they
-    // have.  Shares grow by what that adds, up to an eighth: a few CTAs more than SMs would wait for
-    // one to end (57 sequences of 256 rows, 256 to 1792 own keys: 708 us, not 451).
+    // have.  Shares grow by what that adds where an eighth is enough: a few CTAs more than SMs would
+    // wait for one to end (120 prompts of 275 rows, up to 1792 own keys behind 355: 1913 us, not 1161).
+    // Where it is not they stay as they are (210 behind 300: 1461 us, an eighth larger 1616).
     int ctas = st.own_rate > 0.f ? ctas_beside(p, (float)all, (float)own_keys) : st.sms;
     const int pieces = st.max_items - 2;
     ctas *= 1 + n_tiles / (ctas * (pieces * 3 / 4));
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const TcParam
         carry += total;
     }
     const int line = (int)carry;
-    per = max(per, min(most_per, (line + ctas - 1) / ctas));
+    if ((line + ctas - 1) / ctas <= most_per) per = max(per, (line + ctas - 1) / ctas);
     if (tid == 0) {
         first_of[st.units] = line;
         st.head[0] = per;

@@ -118,6 +118,20 @@ def test_whole_tiles_fill_whole_waves():
     assert 2 * sms < ctas <= 3 * sms
 
 
+def test_shares_that_grow_save_a_wave_of_ctas():
+    """Prompts of 275 rows, 4 tiles of 256 and a short one for each of 8 kv heads, of 11 blocks with what a
+    tile takes besides: a head is 32 * 11 long.  167 of them: shares of 1548, in which tiles count as 12 blocks
+    for their pieces, grow to 1688 and stay 304, two for each SM.  210: shares of 1946 and tiles of 15 blocks
+    would have to grow by more than an eighth, and do not: 806400 / 1946 = 415 CTAs."""
+    for B, ctas in ((167, 304), (210, 415)):
+        x = Batch("bf16", 32, 8, 64, 16, 275, [0, B], [300], [275] * B)
+        space = torch.zeros(x.workspace(debug_flags=WHOLE, sm_count=152), dtype=torch.uint8, device="cuda")
+        x(workspace=space, debug_flags=WHOLE, sm_count=152)
+        words = space[: space.numel() // 4 * 4].view(torch.int32)
+        at = ((words[3:-6] == 1100) & (words[7:-2] == 300) & (words[9:] == 0)).nonzero().flatten()
+        assert torch.unique((at - at[0]) // 400).numel() == ctas
+
+
 PARTS = [
     # dtype, Hq, Hkv, q_len, path, ragged: few rows on each path, and tiles of many
     ("bf16", 16, 2, 1, SPLIT, False), ("bf16", 16, 2, 1, TC, False), ("bf16", 8, 2, 2, 0, True),
