@@ -15,6 +15,7 @@
 // bf16 sequences whose rows fill tiles by themselves have little use for a gather (whole_pays).
 // Their tiles walk the prefix's blocks and go on with the sequence's own, in one launch, and write
 // the output; only tiles that a cut between two CTAs goes through are merged.
+// A batch whose states would take too much memory runs in parts (kMostBytes).
 #include "internal.h"
 #include "atlas_shared.h"
 #include "shared_prefix.cuh"
@@ -63,8 +64,9 @@ struct SharedPlan {
 };
 
 // States of a call at most, in bytes.  A batch that needs more runs in parts, one after the other, in
-// the same workspace: a part has some 10^5 rows of states and takes milliseconds, its launches, its
-// end and another pass over the prefixes a hundredth of that.
+// the same workspace.  A part has some 10^5 rows of states and takes a millisecond or more, its
+// launches, its end and another pass over the prefixes some 40 us: 1200 sequences of 4 rows in 40
+// groups behind 4096 keys 928 -> 975 us in two parts, 64 of 300 rows behind 32768 9.0 -> 9.1 ms in five.
 constexpr size_t kMostBytes = (size_t)512 << 20;
 
 // CTAs of a wave of the split kernels, in hundredths of the SMs, and a CTA's keys at least.
@@ -104,13 +106,13 @@ constexpr int64_t kOwnSplitRows = 32, kOwnSplitKeys = 1024;
 
 // Whether tiles over whole keys take less time than the prefixes' tiles, which the rows of a group's
 // sequences fill, beside the own ones: a block of a prefix 2.0 us for 256 rows, and 1.1 where a
-// sequence's (or a group's) end in the first half, against 9.5 for each own tile of 128 rows on the tensor cores, which has a
-// launch, a start and states to itself there, or 2.6 where the own keys are splits.  Fitted to 98
-// sizes of 20 to 264 rows, prefixes of 300 to 16000 keys and 100 or 800 own ones (32 / 8 heads of
-// 128), of which few lose more than 6 %; whole tiles and others: 128 sequences, 1500 keys, 264
-// rows 403 and 510 us, 64 rows 164 and 176, 20 rows 146 and 102; 16, 16000 keys, 264 rows 367 and
-// 291.  Behind 16000 keys with 800 own ones, 80 rows: 2 sequences with a group each 53 and 65 us, 16
-// with a group each 179 and 187, 32 in 4 groups 318 and 207.
+// sequence's (or a group's) end in the first half, against 9.5 for each own tile of 128 rows on the
+// tensor cores, which has a launch, a start and states to itself there, or 2.6 where the own keys are
+// splits.  Fitted to 98 sizes of 20 to 264 rows, prefixes of 300 to 16000 keys and 100 or 800 own ones
+// (32 / 8 heads of 128), of which few lose more than 6 %; whole tiles and others, 100 own keys: 128
+// sequences behind 1500 keys, 264 rows 424 and 536 us, 64 rows 180 and 177, 20 rows 178 and 103; 16
+// behind 16000 keys, 264 rows 368 and 294.  Behind 16000 keys with 800 own ones, 80 rows: 2 sequences
+// with a group each 53 and 65 us, 16 with a group each 179 and 187, 32 in 4 groups 318 and 207.
 bool whole_pays(int64_t rows, int64_t group_rows, int64_t max_prefix, bool own_splits) {
     auto block = [](int64_t n) {  // of the tiles of n rows
         const int64_t pairs = n / 256 + (n % 256 > 128), single = n % 256 > 0 && n % 256 <= 128;

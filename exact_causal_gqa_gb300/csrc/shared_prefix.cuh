@@ -111,8 +111,8 @@ __device__ __forceinline__ bool shared_real(const Params &p, int seq0, int rows,
 // Lengths on the line, measured: a block of a 256-row tile (a pair of MMA tiles) 2.0 us, of one
 // whose rows end in its first half 1.1 us, and what a tile takes besides (its queries, the first
 // products, the epilogue) about two blocks, or with own keys, whose last blocks are masked, five: 47
-// prompts of 256 rows with 256 to 1587 own keys behind 355 take 452, 409, 405 and 402 us with 2, 4, 5
-// and 6, 64 steps behind 32768 102 with 2 and 104 with 5.
+// prompts of 256 rows with 256 to 1587 own keys behind 355 take 407, 380, 378 and 376 us with 2, 4, 5
+// and 6, 64 steps behind 32768 as long with 2 as with 5.
 constexpr int kPairCost = 7, kSingleCost = 4, kTileBlocks = 2, kWholeTileBlocks = 5;
 
 // Length of a tile's block.

@@ -40,8 +40,8 @@ __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t &total) {
 // end on all: the number for which both are done the soonest.  The tiles are bound by their
 // products and the splits by memory, so that neither gains from all SMs: 64 sequences of up to
 // 2048 own keys behind 32768 shared ones take 113 us with 152 CTAs of tiles, 99 with 96, 108 with
-// 64.  Times measured: a pair's block 2.6 us beside the splits and a CTA's start and end 12;
-// memory 6 MB a microsecond at most.
+// 64 (weights in one part).  Times measured: a pair's block 2.6 us beside the splits and a CTA's start
+// and end 12; memory 6 MB a microsecond at most.  (2.6 to 3.2 us lead to the same times within 2 %.)
 __device__ int ctas_beside(const TcParams &p, float line, float own_keys) {
     __shared__ uint64_t best[kPlanThreads / 32];
     const int sms = p.st.sms;
