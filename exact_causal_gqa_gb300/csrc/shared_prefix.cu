@@ -113,7 +113,12 @@ constexpr int64_t kOwnSplitRows = 32, kOwnSplitKeys = 1024;
 // sequences behind 1500 keys, 264 rows 424 and 536 us, 64 rows 180 and 177, 20 rows 178 and 103; 16
 // behind 16000 keys, 264 rows 368 and 294.  Behind 16000 keys with 800 own ones, 80 rows: 2 sequences
 // with a group each 53 and 65 us, 16 with a group each 179 and 187, 32 in 4 groups 318 and 207.
-bool whole_pays(int64_t rows, int64_t group_rows, int64_t max_prefix, bool own_splits) {
+// Of `tiles` in all: where one is cut among more than 16 CTAs, of two blocks each at least, the merge of
+// its states, one after the other, takes longer than is saved: a sequence of 80 rows and one kv head
+// behind 32768 keys 99 us for 31, behind 8192 43 for 29; of 8 kv heads 65 for 72, and 41 for 33.
+bool whole_pays(int64_t rows, int64_t group_rows, int64_t max_prefix, int64_t max_ctx, int64_t tiles, int64_t sms,
+                bool own_splits) {
+    if (std::min(sms / tiles, (max_prefix + max_ctx) / 256) > 16) return false;
     auto block = [](int64_t n) {  // of the tiles of n rows
         const int64_t pairs = n / 256 + (n % 256 > 128), single = n % 256 > 0 && n % 256 <= 128;
         return 2.0 * (double)pairs + 1.1 * (double)single;
@@ -161,7 +166,9 @@ atlas_status plan_part(int32_t Hq, int32_t Hkv, int32_t D, int32_t P, const atla
     if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->split = false;
     plan->stream = !f32 && !plan->split;
     const bool own_splits = seq_rows <= kOwnSplitRows && max_ctx <= kOwnSplitKeys;
-    plan->whole = plan->stream && !few && L->split_tokens == 0 && whole_pays(seq_rows, group_rows, max_prefix, own_splits);
+    plan->whole = plan->stream && !few && L->split_tokens == 0 &&
+                  whole_pays(seq_rows, group_rows, max_prefix, max_ctx, L->batch * Hkv * ((seq_rows + 255) / 256), sms,
+                             own_splits);
     if (L->debug_flags & ATLAS_DEBUG_SHARED_TC) plan->whole = false;
     if (L->debug_flags & ATLAS_DEBUG_SHARED_WHOLE) plan->whole = plan->stream;
     if (plan->stream && !plan->whole && few && L->split_tokens == 0 &&

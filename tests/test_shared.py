@@ -84,13 +84,14 @@ def test_workspace_holds_the_states_of_both_parts(lib):
 
 
 @pytest.mark.parametrize("B,groups,q_len,prefix_pages,whole", [
-    (1, 1, 20, 1000, True), (8, 8, 20, 1000, True), (8, 8, 5, 1000, True), (64, 64, 75, 125, True),
+    (1, 1, 20, 1000, False), (1, 1, 20, 100, True), (2, 2, 20, 1000, True), (8, 8, 20, 1000, True), (8, 8, 5, 1000, True), (64, 64, 75, 125, True),
     (32, 4, 20, 1000, False), (64, 1, 5, 1000, False), (64, 1, 64, 1000, True)])
 def test_tiles_of_their_own_where_a_gather_fills_no_more(lib, B, groups, q_len, prefix_pages, whole):
-    """Rows of a sequence alone in its group, or that fill tiles, are not gathered (as the sizes tell)."""
+    """Rows of a sequence alone in its group, or that fill tiles, are not gathered (as the sizes tell), where
+    8 kv heads leave a tile to 16 of 152 SMs at most, or it has 33 blocks at most."""
     def size(flags):
         return ws(lib, prefixes(n_groups=groups, max_prefix_pages=prefix_pages), Hq=32, Hkv=8, batch=B, q_len=q_len,
-                  max_pages_per_seq=100, debug_flags=flags)
+                  max_pages_per_seq=100, debug_flags=flags, sm_count=152)
     own, gathered = size(atlas.DEBUG_SHARED_WHOLE), size(atlas.DEBUG_SHARED_TC)
     assert own != gathered and size(0) == (own if whole else gathered)
 
