@@ -222,3 +222,29 @@ def test_in_parts_captured_and_replayed(dtype, path):
         torch.cuda.synchronize()
         assert bool(torch.isfinite(out).all())
         assert torch.equal(out, x(starts, pre, lens, split_tokens=64, debug_flags=path, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("dtype,path", [("bf16", SPLIT), ("bf16", TC), ("bf16", WHOLE), ("f32", SPLIT), ("f32", TC)])
+def test_more_groups_than_the_plan_has_threads_in_parts_of_fewer_sequences(dtype, path):
+    """700 sequences with a prefix each, in two parts (of states; whole tiles in one)."""
+    x = Batch(dtype, 8, 2, 64, 128, 1, list(range(701)), [n % 300 for n in range(700)], [1 + b % 90 for b in range(700)],
+              own_width=128, pre_width=128)
+    x.check([*range(0, 700, 23), 349, 350, 351, 699], split_tokens=64, debug_flags=path)
+
+
+@pytest.mark.parametrize("dtype,path", [("bf16", 0), ("bf16", SPLIT), ("bf16", TC), ("bf16", WHOLE), ("f32", SPLIT),
+                                        ("f32", TC)])
+def test_more_sequences_than_a_grid_has_in_z(dtype, path):
+    B = 70000
+    x = Batch(dtype, 2, 1, 64, 8, 1, [0, 30000, 35001, B - 1], [60, 300, 9], [1 + b % 20 for b in range(B)])
+    x.check([*range(0, B, 997), 29999, 30000, 34999, 35000, 35001, B - 2, B - 1], debug_flags=path)
+
+
+@pytest.mark.parametrize("dtype,path", [("bf16", SPLIT), ("bf16", TC), ("f32", 0)])
+def test_in_parts_events_and_fewer_sms(dtype, path):
+    x = in_parts(dtype, 16, 2, 1, False)
+    timer = atlas.EventTimer()
+    for sms in (1, 7, 300):
+        x.check(range(0, 64, 5), split_tokens=64, debug_flags=path, sm_count=sms, events=timer.handles)
+        torch.cuda.synchronize()
+        assert timer.main_ms() > 0 and timer.merge_ms() > 0
