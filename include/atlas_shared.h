@@ -82,8 +82,7 @@ typedef struct {
  * Precision: the split kernels are those of atlas_attn_decode (bf16 weights as two bf16 parts,
  * fp32 products for fp32).  The bf16 tensor-core kernels take the weights as two bf16 parts for up
  * to 16 rows to a sequence and kv head (decode steps, drafted rows), as atlas_attn_decode and
- * atlas_attn_suffix do there: a step's bits do not depend on how many others share its prompt.  For
- * more rows they do so where the tiles have 128 rows (at most 128 to a kv head of a group, on average,
+ * atlas_attn_suffix do there: a step is as exact however many others share its prompt.  For more rows they do so where the tiles have 128 rows (at most 128 to a kv head of a group, on average,
  * or of a sequence whose rows have tiles of their own), where the second part costs nothing, or where
  * few keys carry a row, and take one part elsewhere, as atlas_attn_suffix and atlas_attn_prefill do.
  * The fp32 one takes three tf32 products for each, within the 1e-5 of the largest value that holds for
