@@ -82,12 +82,13 @@ typedef struct {
  * Precision: the split kernels are those of atlas_attn_decode (bf16 weights as two bf16 parts,
  * fp32 products for fp32).  The bf16 tensor-core kernels take the weights as two bf16 parts for up
  * to 16 rows to a sequence and kv head (decode steps, drafted rows), as atlas_attn_decode and
- * atlas_attn_suffix do there: a step is as exact however many others share its prompt.  For more rows they do so where the tiles have 128 rows (at most 128 to a kv head of a group, on average,
- * or of a sequence whose rows have tiles of their own), where the second part costs nothing, or where
+ * atlas_attn_suffix do there: a step is as exact however many others share its prompt.  For more
+ * rows they do so where the tiles have 128 rows (at most 128 to a kv head of a group, on average, or
+ * of a sequence whose rows have tiles of their own), where the second part costs nothing, or where
  * few keys carry a row, and take one part elsewhere, as atlas_attn_suffix and atlas_attn_prefill do.
- * The fp32 one takes three tf32 products for each, within the 1e-5 of the largest value that holds for
- * all fp32 calls: 7e-7 to 1e-6 off in the root mean square (atlas_attn_suffix 2e-6), where the split
- * kernels are 2e-7 to 3e-7.
+ * The fp32 one takes three tf32 products for each, within the 1e-5 of the largest value that holds
+ * for all fp32 calls: 7e-7 to 1e-6 off in the root mean square (atlas_attn_suffix 2e-6), where the
+ * split kernels are 2e-7 to 3e-7.
  */
 atlas_status atlas_attn_shared(const void *q, const void *k_pages, const void *v_pages,
                                const int32_t *page_table, const int32_t *seq_lens,
